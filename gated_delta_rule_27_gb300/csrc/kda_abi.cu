@@ -3,6 +3,8 @@
 // anything is enqueued; the kernels themselves live in the other files.
 #include <limits.h>
 
+#include <initializer_list>
+
 #include "kda_internal.cuh"
 #include "kda_testing.h"
 
@@ -287,6 +289,135 @@ kda_status kda_state_snapshot(const float *S_pool, const int32_t *seq_idx, int32
 kda_status kda_state_restore(const float *S_saved, const int32_t *seq_idx, int32_t n, int32_t num_slots, int32_t H,
                              int32_t d_k, int32_t d_v, float *S_pool, int32_t *status, void *stream) {
     return state_copy(S_saved, S_pool, seq_idx, n, num_slots, H, d_k, d_v, true, status, stream);
+}
+
+// What the tree entry points share: sizes, then the packed layout's pointers (only when there are requests).
+static kda_status tree_check(int32_t num_seqs, int32_t total_nodes, int32_t bound, int32_t num_slots,
+                             kda_dtype in_dtype) {
+    if (num_seqs < 0 || total_nodes < 0 || num_slots < 0 || !valid_dtype(in_dtype)) return KDA_ERR_INVALID_ARG;
+    if (bound < 1) return KDA_ERR_INVALID_ARG;
+    return bound > KDA_TREE_MAX_NODES ? KDA_ERR_UNSUPPORTED : KDA_OK;
+}
+static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+static bool given4(const void *p) { return p && aligned4(p); }
+static bool given16(const void *p) { return p && aligned16(p); }
+
+kda_status kda_tree_step(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                         const int32_t *parent, const int32_t *cu_nodes, const int32_t *seq_idx, int32_t num_seqs,
+                         int32_t total_nodes, int32_t max_nodes, int32_t num_slots, int32_t H, int32_t d_k,
+                         int32_t d_v, kda_dtype in_dtype, const float *S_pool, void *o, float *u, int32_t *status,
+                         void *stream, const kda_fusion_opts *opts) {
+    if (kda_status st = tree_check(num_seqs, total_nodes, max_nodes, num_slots, in_dtype)) return st;
+    if (H <= 0) return KDA_ERR_INVALID_ARG;
+    kda::Fusion fu;
+    if (kda_status st = fusion_from(opts, total_nodes > 0, o, &fu)) return st;
+    if (d_k != d_v || !supported_d(d_k)) return KDA_ERR_UNSUPPORTED;
+    if ((int64_t)total_nodes * H > INT_MAX || (int64_t)num_seqs * H > INT_MAX || (int64_t)num_slots * H > INT_MAX)
+        return KDA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || total_nodes == 0) return KDA_OK;
+    if (!given16(q) || !given16(k) || !given16(v) || !given16(g) || !given4(beta) || !given4(parent) ||
+        !given4(cu_nodes) || !aligned4(seq_idx) || !given16(S_pool) || !given16(o) || !aligned16(u) ||
+        !aligned4(status))
+        return KDA_ERR_INVALID_ARG;
+    for (const void *out : {(const void *)o, (const void *)u})
+        if (out && (out == q || out == k || out == v || out == (const void *)g || out == (const void *)S_pool ||
+                    out == (const void *)beta || out == fu.gate))
+            return KDA_ERR_INVALID_ARG;
+    if (o == (const void *)u) return KDA_ERR_INVALID_ARG;
+    const kda::TreeStepArgs a{q, k, v, g, beta, parent, cu_nodes, seq_idx, num_seqs, total_nodes, max_nodes,
+                              num_slots, H, d_k, S_pool, o, u, status, fu};
+    return kda::launch_tree_step(a, in_dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK
+                                                                                                : KDA_ERR_CUDA;
+}
+
+kda_status kda_tree_commit(const void *k, const float *g, const float *u, const int32_t *cu_nodes,
+                           const int32_t *path, const int32_t *path_len, const int32_t *seq_idx, int32_t num_seqs,
+                           int32_t total_nodes, int32_t path_stride, int32_t num_slots, int32_t H, int32_t d_k,
+                           int32_t d_v, kda_dtype in_dtype, float *S_pool, int32_t *status, void *stream,
+                           const kda_fusion_opts *opts) {
+    if (kda_status st = tree_check(num_seqs, total_nodes, path_stride, num_slots, in_dtype)) return st;
+    if (H <= 0) return KDA_ERR_INVALID_ARG;
+    const bool qk_norm = opts && opts->qk_l2norm;
+    if (qk_norm && !(opts->qk_eps >= 0.f)) return KDA_ERR_INVALID_ARG;
+    if (d_k != d_v || !supported_d(d_k)) return KDA_ERR_UNSUPPORTED;
+    if ((int64_t)total_nodes * H > INT_MAX || (int64_t)num_seqs * H > INT_MAX || (int64_t)num_slots * H > INT_MAX)
+        return KDA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || total_nodes == 0) return KDA_OK;
+    if (!given16(k) || !given16(g) || !given16(u) || !given4(cu_nodes) || !given4(path) || !given4(path_len) ||
+        !aligned4(seq_idx) || !given16(S_pool) || !aligned4(status))
+        return KDA_ERR_INVALID_ARG;
+    const void *out = S_pool;
+    if (out == k || out == (const void *)g || out == (const void *)u) return KDA_ERR_INVALID_ARG;
+    const kda::TreeCommitArgs a{k, g, u, cu_nodes, path, path_len, seq_idx, num_seqs, total_nodes, path_stride,
+                                num_slots, H, d_k, S_pool, status, qk_norm ? 1 : 0, qk_norm ? opts->qk_eps : 0.f};
+    return kda::launch_tree_commit(a, in_dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK
+                                                                                                  : KDA_ERR_CUDA;
+}
+
+static kda_status tree_conv_check(int32_t num_seqs, int32_t total_nodes, int32_t num_slots, int32_t C, int32_t W) {
+    if (C <= 0) return KDA_ERR_INVALID_ARG;
+    if (W < 1 || W > KDA_SHORT_CONV_MAX_W) return KDA_ERR_UNSUPPORTED;
+    // the grid's second dimension is the request
+    if (num_seqs > 65535 || (int64_t)C * W > INT_MAX) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+kda_status kda_tree_conv(const void *x, const float *w, const int32_t *parent, const int32_t *cu_nodes,
+                         const int32_t *seq_idx, int32_t num_seqs, int32_t total_nodes, int32_t max_nodes,
+                         int32_t num_slots, int32_t C, int32_t W, kda_dtype in_dtype, const float *conv_pool, void *y,
+                         int32_t *status, void *stream) {
+    if (kda_status st = tree_check(num_seqs, total_nodes, max_nodes, num_slots, in_dtype)) return st;
+    if (kda_status st = tree_conv_check(num_seqs, total_nodes, num_slots, C, W)) return st;
+    if (num_seqs == 0 || total_nodes == 0) return KDA_OK;
+    const uintptr_t el = in_dtype == KDA_BF16 ? 1u : 3u;
+    if (!x || !y || x == y || (reinterpret_cast<uintptr_t>(x) & el) || (reinterpret_cast<uintptr_t>(y) & el) ||
+        !given4(w) || !given4(parent) || !given4(cu_nodes) || !aligned4(seq_idx) || !aligned4(conv_pool) ||
+        (W > 1 && !conv_pool) || y == (const void *)conv_pool || y == (const void *)w || !aligned4(status))
+        return KDA_ERR_INVALID_ARG;
+    const kda::TreeConvArgs a{x, w, parent, cu_nodes, seq_idx, num_seqs, total_nodes, max_nodes, num_slots, C, W,
+                              conv_pool, y, status};
+    return kda::launch_tree_conv(a, in_dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK
+                                                                                                : KDA_ERR_CUDA;
+}
+
+kda_status kda_tree_conv_commit(const void *x, const int32_t *cu_nodes, const int32_t *path, const int32_t *path_len,
+                                const int32_t *seq_idx, int32_t num_seqs, int32_t total_nodes, int32_t path_stride,
+                                int32_t num_slots, int32_t C, int32_t W, kda_dtype in_dtype, float *conv_pool,
+                                int32_t *status, void *stream) {
+    if (kda_status st = tree_check(num_seqs, total_nodes, path_stride, num_slots, in_dtype)) return st;
+    if (kda_status st = tree_conv_check(num_seqs, total_nodes, num_slots, C, W)) return st;
+    if (num_seqs == 0 || total_nodes == 0 || W == 1) return KDA_OK;  // a width of one carries nothing
+    const uintptr_t el = in_dtype == KDA_BF16 ? 1u : 3u;
+    if (!x || (reinterpret_cast<uintptr_t>(x) & el) || !given4(cu_nodes) || !given4(path) || !given4(path_len) ||
+        !aligned4(seq_idx) || !given4(conv_pool) || x == (const void *)conv_pool || !aligned4(status))
+        return KDA_ERR_INVALID_ARG;
+    const kda::TreeConvCommitArgs a{x, cu_nodes, path, path_len, seq_idx, num_seqs, total_nodes, path_stride,
+                                    num_slots, C, W, conv_pool, status};
+    return kda::launch_tree_conv_commit(a, in_dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? KDA_OK
+               : KDA_ERR_CUDA;
+}
+
+kda_status kda_draft_verify(const void *logits, const float *draft_probs, const int32_t *tokens, const int32_t *parent,
+                            const int32_t *cu_nodes, const float *temperature, const float *u_accept,
+                            const float *u_next, int32_t num_seqs, int32_t total_nodes, int32_t V, kda_dtype in_dtype,
+                            int32_t path_stride, int32_t *path, int32_t *path_len, int32_t *next_token,
+                            int32_t *status, void *stream) {
+    if (kda_status st = tree_check(num_seqs, total_nodes, path_stride, 0, in_dtype)) return st;
+    if (V <= 0) return KDA_ERR_INVALID_ARG;
+    if (V > KDA_VERIFY_MAX_VOCAB) return KDA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return KDA_OK;
+    const uintptr_t el = in_dtype == KDA_BF16 ? 1u : 3u;
+    if (total_nodes > 0 && (!logits || (reinterpret_cast<uintptr_t>(logits) & el) || !aligned4(draft_probs) ||
+                            !given4(tokens) || !given4(parent) || !aligned4(temperature) || !given4(u_accept) ||
+                            !given4(u_next)))
+        return KDA_ERR_INVALID_ARG;
+    if (!given4(cu_nodes) || !given4(path) || !given4(path_len) || !given4(next_token) || !aligned4(status))
+        return KDA_ERR_INVALID_ARG;
+    const kda::DraftVerifyArgs a{logits, draft_probs, tokens, parent, cu_nodes, temperature, u_accept, u_next,
+                                 num_seqs, total_nodes, V, path_stride, path, path_len, next_token, status};
+    return kda::launch_draft_verify(a, in_dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK
+                                                                                                   : KDA_ERR_CUDA;
 }
 
 }  // extern "C"

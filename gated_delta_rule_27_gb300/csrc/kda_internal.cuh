@@ -246,4 +246,58 @@ cudaError_t launch_conv_decode(const void *x, const float *w, int N, int C, int 
 cudaError_t launch_state_copy(const float *src, float *dst, const int32_t *idx, int n, int num_slots, int H, int d,
                               bool scatter, int32_t *status, cudaStream_t st);
 
+// Draft trees (kda_tree.cu): KDA attention of every node over the state pool, the pool's move along the
+// accepted paths, and the short convolution's counterparts; and the verification of the drafted tokens
+// (kda_verify.cu).  Arguments as in kda.h.
+struct TreeStepArgs {
+    const void *q, *k, *v;
+    const float *g, *beta;
+    const int32_t *parent, *cu, *seq_idx;
+    int num_seqs, total_nodes, max_nodes, num_slots, H, d;
+    const float *S_pool;
+    void *o;
+    float *u;
+    int32_t *status;
+    Fusion fu;
+};
+struct TreeCommitArgs {
+    const void *k;
+    const float *g, *u;
+    const int32_t *cu, *path, *path_len, *seq_idx;
+    int num_seqs, total_nodes, path_stride, num_slots, H, d;
+    float *S_pool;
+    int32_t *status;
+    int qk_norm;
+    float qk_eps;
+};
+struct TreeConvArgs {
+    const void *x;
+    const float *w;
+    const int32_t *parent, *cu, *seq_idx;
+    int num_seqs, total_nodes, max_nodes, num_slots, C, W;
+    const float *pool;
+    void *y;
+    int32_t *status;
+};
+struct TreeConvCommitArgs {
+    const void *x;
+    const int32_t *cu, *path, *path_len, *seq_idx;
+    int num_seqs, total_nodes, path_stride, num_slots, C, W;
+    float *pool;
+    int32_t *status;
+};
+struct DraftVerifyArgs {
+    const void *logits;
+    const float *probs;
+    const int32_t *tokens, *parent, *cu;
+    const float *temperature, *u, *u_next;
+    int num_seqs, total_nodes, V, path_stride;
+    int32_t *path, *path_len, *next_token, *status;
+};
+cudaError_t launch_tree_step(const TreeStepArgs &a, kda_dtype dt, cudaStream_t st);
+cudaError_t launch_tree_commit(const TreeCommitArgs &a, kda_dtype dt, cudaStream_t st);
+cudaError_t launch_tree_conv(const TreeConvArgs &a, kda_dtype dt, cudaStream_t st);
+cudaError_t launch_tree_conv_commit(const TreeConvCommitArgs &a, kda_dtype dt, cudaStream_t st);
+cudaError_t launch_draft_verify(const DraftVerifyArgs &a, kda_dtype dt, cudaStream_t st);
+
 }  // namespace kda

@@ -1,0 +1,99 @@
+// kda_tree.cuh -- packed draft trees, as the tree kernels read them.
+//
+// Request n owns rows [cu[n], cu[n + 1]) of every packed tensor; its first row is the tree's root and
+// parent[row] is a local index below the row's own (-1: the root).  A tree is used only after
+// read_tree() has found it inside these rules, so no index taken from it can leave its tensors.
+#pragma once
+
+#include "kda_internal.cuh"
+
+namespace kda {
+
+constexpr int kMaxNodes = KDA_TREE_MAX_NODES;
+
+struct TreeShared {
+    unsigned long long anc[kMaxNodes];  // bit a of anc[i]: node a lies on the path from the root to node i (i included)
+    int parent[kMaxNodes];
+    int bad;
+};
+
+struct Tree {
+    int row0, nodes;
+};
+
+// Rows of request n, or nodes = -1 where cu breaks the rules (any thread; the same answer in all of them).
+__device__ __forceinline__ Tree tree_rows(const int32_t *__restrict__ cu, int n, int total_nodes, int max_nodes) {
+    const int lo = cu[n], hi = cu[n + 1];
+    if (lo < 0 || hi < lo || hi > total_nodes || hi - lo > max_nodes) return Tree{0, -1};
+    return Tree{lo, hi - lo};
+}
+
+// The block's threads read and check request n's tree together (two block barriers).  Returns nodes = -1,
+// with KDA_ERR_INVALID_ARG recorded in *status by one thread of the block, where it breaks the rules.
+// The paths come from pointer doubling: after r rounds a node's mask covers its 2^r nearest ancestors.
+__device__ __forceinline__ Tree read_tree(TreeShared &ts, const int32_t *__restrict__ parent,
+                                          const int32_t *__restrict__ cu, int n, int total_nodes, int max_nodes,
+                                          bool want_paths) {
+    const Tree t = tree_rows(cu, n, total_nodes, max_nodes);
+    const int tid = threadIdx.x;
+    if (tid < 32) {
+        bool bad = t.nodes < 0;
+        for (int i = tid; i < t.nodes; i += 32) {
+            const int p = parent[t.row0 + i];
+            bad |= i == 0 ? p != -1 : (p < 0 || p >= i);
+            ts.parent[i] = p;
+        }
+        bad = __any_sync(0xffffffffu, bad);
+        if (tid == 0) ts.bad = bad;
+        if (want_paths && !bad) {
+            __syncwarp();
+            // two nodes per lane: i = tid, tid + 32
+            unsigned long long m[2];
+            int jump[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int i = tid + 32 * r;
+                m[r] = 1ull << i;
+                jump[r] = i < t.nodes ? ts.parent[i] : -1;
+            }
+            for (int span = 1; span < t.nodes; span <<= 1) {
+                unsigned long long up[2];
+                int next[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int j = jump[r] < 0 ? 0 : jump[r];
+                    const unsigned long long lo = __shfl_sync(0xffffffffu, m[0], j & 31);
+                    const unsigned long long hi = __shfl_sync(0xffffffffu, m[1], j & 31);
+                    const int nlo = __shfl_sync(0xffffffffu, jump[0], j & 31);
+                    const int nhi = __shfl_sync(0xffffffffu, jump[1], j & 31);
+                    up[r] = j < 32 ? lo : hi;
+                    next[r] = j < 32 ? nlo : nhi;
+                }
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    if (jump[r] >= 0) {
+                        m[r] |= up[r];
+                        jump[r] = next[r];
+                    }
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                if (tid + 32 * r < t.nodes) ts.anc[tid + 32 * r] = m[r];
+        }
+    }
+    __syncthreads();
+    return ts.bad ? Tree{0, -1} : t;
+}
+
+__device__ __forceinline__ void report_invalid(int32_t *status) {
+    if (status) atomicCAS(status, 0, (int32_t)KDA_ERR_INVALID_ARG);
+}
+
+// The pool slot of request n, or -1 for one outside the pool.
+__device__ __forceinline__ int slot_of(const int32_t *__restrict__ seq_idx, int n, int num_slots) {
+    const int slot = seq_idx ? seq_idx[n] : n;
+    return slot < 0 || slot >= num_slots ? -1 : slot;
+}
+
+}  // namespace kda

@@ -20,12 +20,14 @@ KDA_F32, KDA_BF16 = 0, 1
 SYMBOLS = ("kda_status_string", "kda_prefill_workspace_size", "kda_prefill_chunked", "kda_prefill_chunked_profiled",
            "kda_prefill_check", "kda_decode_step", "kda_prefill_chunked_noalloc", "kda_prefill_noalloc_check",
            "kda_decode_step_indexed", "kda_state_snapshot", "kda_state_restore", "kda_prefill_chunked_ex",
-           "kda_decode_step_ex", "kda_short_conv_prefill", "kda_short_conv_decode")
+           "kda_decode_step_ex", "kda_short_conv_prefill", "kda_short_conv_decode", "kda_tree_step",
+           "kda_tree_commit", "kda_tree_conv", "kda_tree_conv_commit", "kda_draft_verify")
 # include/kda_testing.h (test hooks)
 TESTING_SYMBOLS = ("kda_testing_set_plan", "kda_testing_set_fault")
 PLAN_AUTO, PLAN_THREE, PLAN_CHAIN, PLAN_PIPE = -1, 0, 2, 3
 FAULT_NONE, FAULT_NO_PUBLISH, FAULT_CHUNK_TABLE = 0, 1, 2
 PREFILL_MAX_KERNELS = 4
+TREE_MAX_NODES = 64
 
 _lib = None
 
@@ -101,6 +103,14 @@ def _declare(lib: ctypes.CDLL) -> ctypes.CDLL:
     for name in ("kda_state_snapshot", "kda_state_restore"):
         getattr(lib, name).restype = ctypes.c_int
         getattr(lib, name).argtypes = [fp, vp, i32, i32, i32, i32, i32, fp, vp, vp]
+    dt, fusion = ctypes.c_int, ctypes.POINTER(FusionOpts)
+    for name, types in (("kda_tree_step", [vp] * 8 + [i32] * 7 + [dt] + [vp] * 5 + [fusion]),
+                        ("kda_tree_commit", [vp] * 7 + [i32] * 7 + [dt] + [vp] * 3 + [fusion]),
+                        ("kda_tree_conv", [vp] * 5 + [i32] * 6 + [dt] + [vp] * 4),
+                        ("kda_tree_conv_commit", [vp] * 5 + [i32] * 6 + [dt] + [vp] * 3),
+                        ("kda_draft_verify", [vp] * 8 + [i32] * 3 + [dt, i32] + [vp] * 5)):
+        getattr(lib, name).restype = ctypes.c_int
+        getattr(lib, name).argtypes = types
     lib.kda_testing_set_plan.restype = ctypes.c_int
     lib.kda_testing_set_plan.argtypes = [i32]
     lib.kda_testing_set_fault.restype = ctypes.c_int
@@ -300,6 +310,128 @@ def kda_state_restore(S_saved, seq_idx, S_pool, status=None, stream=None) -> Non
                                   _ptr(S_pool), _ptr(status), _stream(stream))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_state_restore")
+
+
+def _i32(t, name: str):
+    if t is not None and t.dtype != torch.int32:
+        raise TypeError("libkda takes int32 %s, got %s" % (name, t.dtype))
+    return _ptr(t)
+
+
+def _f32(t, name: str):
+    if t is not None and t.dtype != torch.float32:
+        raise TypeError("libkda takes fp32 %s, got %s" % (name, t.dtype))
+    return _ptr(t)
+
+
+def _shape(t, shape, name: str) -> None:
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+
+
+def _like(t, ref, name: str):
+    if t.dtype != ref.dtype:
+        raise TypeError("%s is %s, expected %s" % (name, t.dtype, ref.dtype))
+    return _ptr(t)
+
+
+def kda_tree_step(q, k, v, g, beta, parent, cu_nodes, seq_idx, S_pool, o, u, max_nodes, status=None, stream=None,
+                  **fusion) -> None:
+    """KDA attention of every draft-tree node over the state pool (kda_tree_step): q, k, v, g [T, H, d] and beta
+    [T, H] packed as include/kda.h says, o and u (or None) written; keywords of fusion_opts."""
+    T, H, d_k = q.shape
+    N = cu_nodes.numel() - 1
+    for t, name in ((k, "k"), (v, "v"), (g, "g"), (o, "o"), (u, "u"), (fusion.get("out_gate"), "out_gate")):
+        _shape(t, (T, H, d_k), name)
+    _shape(beta, (T, H), "beta")
+    _shape(parent, (T,), "parent")
+    _shape(seq_idx, (N,), "seq_idx")
+    _shape(S_pool, (S_pool.shape[0], H, d_k, d_k), "S_pool")
+    opts = fusion_opts(**fusion)
+    rc = load().kda_tree_step(_ptr(q), _like(k, q, "k"), _like(v, q, "v"), _f32(g, "g"), _f32(beta, "beta"),
+                              _i32(parent, "parent"), _i32(cu_nodes, "cu_nodes"), _i32(seq_idx, "seq_idx"), N, T,
+                              max_nodes, S_pool.shape[0], H, d_k, d_k, _dtype_code(q), _f32(S_pool, "S_pool"),
+                              _like(o, q, "o"), _f32(u, "u"), _i32(status, "status"), _stream(stream),
+                              None if opts is None else ctypes.byref(opts))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_tree_step")
+
+
+def kda_tree_commit(k, g, u, cu_nodes, path, path_len, seq_idx, S_pool, status=None, stream=None, qk_l2norm=False,
+                    qk_eps=1e-6) -> None:
+    """Moves the pool's states along the accepted paths (kda_tree_commit), in place."""
+    T, H, d_k = k.shape
+    N = cu_nodes.numel() - 1
+    _shape(g, (T, H, d_k), "g")
+    _shape(u, (T, H, d_k), "u")
+    _shape(path, (N, path.shape[1]), "path")
+    _shape(path_len, (N,), "path_len")
+    _shape(seq_idx, (N,), "seq_idx")
+    _shape(S_pool, (S_pool.shape[0], H, d_k, d_k), "S_pool")
+    opts = fusion_opts(qk_l2norm=qk_l2norm, qk_eps=qk_eps)
+    rc = load().kda_tree_commit(_ptr(k), _f32(g, "g"), _f32(u, "u"), _i32(cu_nodes, "cu_nodes"), _i32(path, "path"),
+                                _i32(path_len, "path_len"), _i32(seq_idx, "seq_idx"), N, T, path.shape[1],
+                                S_pool.shape[0], H, d_k, d_k, _dtype_code(k), _f32(S_pool, "S_pool"),
+                                _i32(status, "status"), _stream(stream), None if opts is None else ctypes.byref(opts))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_tree_commit")
+
+
+def kda_tree_conv(x, w, parent, cu_nodes, seq_idx, conv_pool, y, max_nodes, status=None, stream=None) -> None:
+    """The short convolution along every node's path (kda_tree_conv): x, y [T, C], w [C, W], conv_pool
+    [slots, W - 1, C] (read only)."""
+    T = x.shape[0]
+    C, W = w.shape
+    N = cu_nodes.numel() - 1
+    _shape(x, (T, C), "x")
+    _shape(y, (T, C), "y")
+    _shape(parent, (T,), "parent")
+    _shape(seq_idx, (N,), "seq_idx")
+    _shape(conv_pool, (conv_pool.shape[0], W - 1, C), "conv_pool")
+    rc = load().kda_tree_conv(_ptr(x), _f32(w, "w"), _i32(parent, "parent"), _i32(cu_nodes, "cu_nodes"),
+                              _i32(seq_idx, "seq_idx"), N, T, max_nodes, conv_pool.shape[0], C, W, _dtype_code(x),
+                              _f32(conv_pool, "conv_pool"), _like(y, x, "y"), _i32(status, "status"),
+                              _stream(stream))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_tree_conv")
+
+
+def kda_tree_conv_commit(x, cu_nodes, path, path_len, seq_idx, conv_pool, status=None, stream=None) -> None:
+    """Moves the carried convolution inputs along the accepted paths (kda_tree_conv_commit), in place."""
+    T, C = x.shape
+    N = cu_nodes.numel() - 1
+    _shape(path, (N, path.shape[1]), "path")
+    _shape(path_len, (N,), "path_len")
+    _shape(seq_idx, (N,), "seq_idx")
+    _shape(conv_pool, (conv_pool.shape[0], conv_pool.shape[1], C), "conv_pool")
+    rc = load().kda_tree_conv_commit(_ptr(x), _i32(cu_nodes, "cu_nodes"), _i32(path, "path"),
+                                     _i32(path_len, "path_len"), _i32(seq_idx, "seq_idx"), N, T, path.shape[1],
+                                     conv_pool.shape[0], C, conv_pool.shape[1] + 1, _dtype_code(x),
+                                     _f32(conv_pool, "conv_pool"), _i32(status, "status"), _stream(stream))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_tree_conv_commit")
+
+
+def kda_draft_verify(logits, tokens, parent, cu_nodes, u_accept, u_next, path, path_len, next_token, draft_probs=None,
+                     temperature=None, status=None, stream=None) -> None:
+    """Verifies drafted tokens against the target's logits [T, V] (kda_draft_verify): writes the kept paths
+    [N, max nodes], their lengths and the next tokens."""
+    T, V = logits.shape
+    N = cu_nodes.numel() - 1
+    for t, name in ((tokens, "tokens"), (parent, "parent"), (u_accept, "u_accept")):
+        _shape(t, (T,), name)
+    for t, name in ((u_next, "u_next"), (path_len, "path_len"), (next_token, "next_token"),
+                    (temperature, "temperature")):
+        _shape(t, (N,), name)
+    _shape(draft_probs, (T, V), "draft_probs")
+    _shape(path, (N, path.shape[1]), "path")
+    rc = load().kda_draft_verify(_ptr(logits), _f32(draft_probs, "draft_probs"), _i32(tokens, "tokens"),
+                                 _i32(parent, "parent"), _i32(cu_nodes, "cu_nodes"), _f32(temperature, "temperature"),
+                                 _f32(u_accept, "u_accept"), _f32(u_next, "u_next"), N, T, V, _dtype_code(logits),
+                                 path.shape[1], _i32(path, "path"), _i32(path_len, "path_len"),
+                                 _i32(next_token, "next_token"), _i32(status, "status"), _stream(stream))
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_draft_verify")
 
 
 def new_workspace(T, N, H, d_k, d_v, in_dtype, chunk_size, device) -> torch.Tensor:

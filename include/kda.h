@@ -264,6 +264,127 @@ KDA_API kda_status kda_short_conv_decode(const void *x, const float *w, int32_t 
                                          kda_dtype in_dtype, float *conv_state, void *y, void *stream);
 
 /*
+ * Speculative serving over draft trees (Lecture 11, section 2, "Serving
+ * state" row, and section 3: after any rollback the state must equal that of
+ * a run from scratch).  A round runs the model once over a small tree of
+ * drafted tokens behind each request's last token, keeps one path, and moves
+ * the request's states along it:
+ *     kda_tree_conv, kda_tree_step   every node's output; the pools are only read
+ *     kda_draft_verify               the accepted path and the next token
+ *     kda_tree_commit, kda_tree_conv_commit   the pools moved along the path
+ * Nothing is copied or rolled back: a rejected node has changed no state.
+ *
+ * Packed trees.  Request n owns rows [cu_nodes[n], cu_nodes[n + 1]) of every
+ * [total_nodes, ...] tensor; the first is the tree's root (the request's last
+ * token, not yet in its state).
+ *   parent      [total_nodes] int32, device: -1 for the root, else the LOCAL
+ *               index of the parent, below the row's own
+ *   cu_nodes    [num_seqs + 1] int32, device
+ *   seq_idx     [num_seqs] int32, device: distinct pool slots, or NULL: request
+ *               n uses slot n
+ *   max_nodes   an upper bound of the trees' sizes, 1 to KDA_TREE_MAX_NODES
+ *   status      optional device int32 (NULL to skip): a request whose tree,
+ *               path or slot breaks these rules is skipped (nothing of it is
+ *               written, but by kda_draft_verify an empty path) and sets
+ *               *status to KDA_ERR_INVALID_ARG if it was 0.
+ * A request may have no nodes.  All pointers are device pointers, contiguous,
+ * 16-byte aligned unless said otherwise; index arrays, beta, u_accept, u_next
+ * and temperature 4-byte aligned.
+ */
+#define KDA_TREE_MAX_NODES 64
+
+/*
+ * KDA attention of every tree node over its request's slot of the state pool:
+ * with S' the state after the node's parent (the pool's for the root),
+ *     u = beta (v - (D S')^T k),  S = D S' + k u^T,  o = S^T q.
+ *
+ *   q, k, v, g, beta  as kda_decode_step, [total_nodes, H, ...]
+ *   S_pool   [num_slots, H, d_k, d_v] fp32, read only
+ *   o        [total_nodes, H, d_v] in_dtype
+ *   u        [total_nodes, H, d_v] fp32, what kda_tree_commit needs, or NULL
+ *   opts     the fused normalisations (out_gate [total_nodes, H, d_v]), or NULL
+ * o and u must not alias an input.
+ */
+KDA_API kda_status kda_tree_step(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                                 const int32_t *parent, const int32_t *cu_nodes, const int32_t *seq_idx,
+                                 int32_t num_seqs, int32_t total_nodes, int32_t max_nodes, int32_t num_slots,
+                                 int32_t H, int32_t d_k, int32_t d_v, kda_dtype in_dtype, const float *S_pool,
+                                 void *o, float *u, int32_t *status, void *stream, const kda_fusion_opts *opts);
+
+/*
+ * Moves the slots' states along the accepted paths, in place: the state after
+ * the path's last node, from the k and g that kda_tree_step was given and the
+ * u that it wrote.
+ *
+ *   path      [num_seqs, path_stride] int32, device: local node indices from
+ *             the root on, path_len[n] of them (the rest is not read)
+ *   path_len  [num_seqs] int32, device; 0 leaves the slot as it is
+ *   opts      NULL, or the options of the step (only its q/k normalisation is
+ *             used here)
+ */
+KDA_API kda_status kda_tree_commit(const void *k, const float *g, const float *u, const int32_t *cu_nodes,
+                                   const int32_t *path, const int32_t *path_len, const int32_t *seq_idx,
+                                   int32_t num_seqs, int32_t total_nodes, int32_t path_stride, int32_t num_slots,
+                                   int32_t H, int32_t d_k, int32_t d_v, kda_dtype in_dtype, float *S_pool,
+                                   int32_t *status, void *stream, const kda_fusion_opts *opts);
+
+/*
+ * The short convolution along every node's path: y_i[c] = sum_{j < W} w[c, j]
+ * x_{a_j(i)}[c] with a_j(i) the j-th node above i, then, past the root, the
+ * slot's carried inputs.
+ *
+ *   x, y       [total_nodes, C] in_dtype; y must not alias x; element-aligned
+ *   w          [C, W] fp32, 1 <= W <= KDA_SHORT_CONV_MAX_W
+ *   conv_pool  [num_slots, W - 1, C] fp32, oldest first, read only (NULL if W = 1)
+ * kda_tree_conv_commit replaces a slot's carried inputs by the last W - 1 of
+ * [its carried inputs, the inputs x along the accepted path].
+ */
+KDA_API kda_status kda_tree_conv(const void *x, const float *w, const int32_t *parent, const int32_t *cu_nodes,
+                                 const int32_t *seq_idx, int32_t num_seqs, int32_t total_nodes, int32_t max_nodes,
+                                 int32_t num_slots, int32_t C, int32_t W, kda_dtype in_dtype, const float *conv_pool,
+                                 void *y, int32_t *status, void *stream);
+KDA_API kda_status kda_tree_conv_commit(const void *x, const int32_t *cu_nodes, const int32_t *path,
+                                        const int32_t *path_len, const int32_t *seq_idx, int32_t num_seqs,
+                                        int32_t total_nodes, int32_t path_stride, int32_t num_slots, int32_t C,
+                                        int32_t W, kda_dtype in_dtype, float *conv_pool, int32_t *status,
+                                        void *stream);
+
+/*
+ * Accepts or rejects drafted tokens so that what is kept, and the next token,
+ * follow the target's distribution p = softmax(logits / temperature).
+ * From the root on, a node's children are tried in row order.  Child c, drawn
+ * from the draft distribution q at its parent, is accepted if u_c q_c < p_c;
+ * after a rejection p becomes the normalised excess max(p - q, 0).  Without
+ * draft_probs q is one at the child's token.  The walk ends at the first node
+ * that accepts no child; the next token is the first whose cumulative p is
+ * above u_next.  (Where rounding leaves no excess, the node's own p serves.)
+ *
+ *   logits        [total_nodes, V] in_dtype, element-aligned; NaN and -inf have
+ *                 probability 0; +inf shares all of it
+ *   tokens        [total_nodes] int32 (a root's is not read); one outside
+ *                 [0, V) is never accepted and sets *status
+ *   draft_probs   [total_nodes, V] fp32, row i the q of node i's children, or NULL
+ *   temperature   [num_seqs] fp32, or NULL for 1; <= 0 (or NaN): greedy, all
+ *                 of p at the lowest index of the largest logit
+ *   u_accept      [total_nodes] fp32 in [0, 1) (a root's is not read)
+ *   u_next        [num_seqs] fp32 in [0, 1)
+ *   path          [num_seqs, path_stride] int32: the kept nodes, root first, then
+ *                 -1; path_stride bounds the trees' sizes as max_nodes does
+ *   path_len      [num_seqs] int32: at least 1 (the root) unless the tree is empty
+ *   next_token    [num_seqs] int32; -1 for an empty tree, and where no logit of
+ *                 the last node is above -inf
+ * Sums over the vocabulary are exact in steps of 2^-40 of the largest weight:
+ * the decisions depend on no order of additions.
+ */
+#define KDA_VERIFY_MAX_VOCAB (1 << 22)
+KDA_API kda_status kda_draft_verify(const void *logits, const float *draft_probs, const int32_t *tokens,
+                                    const int32_t *parent, const int32_t *cu_nodes, const float *temperature,
+                                    const float *u_accept, const float *u_next, int32_t num_seqs,
+                                    int32_t total_nodes, int32_t V, kda_dtype in_dtype, int32_t path_stride,
+                                    int32_t *path, int32_t *path_len, int32_t *next_token, int32_t *status,
+                                    void *stream);
+
+/*
  * Chunked prefill that allocates nothing.  The course pages have no
  * counterpart to this entry point; it repackages kda_prefill_chunked for
  * callers that cannot give the library device scratch: code that runs while a
