@@ -408,6 +408,7 @@ cudaError_t launch_conv_commit_t(const TreeConvCommitArgs &a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_tree_step(const TreeStepArgs &a, kda_dtype dt, cudaStream_t st) {
+    if (dt == KDA_BF16 && a.d == 128) return launch_tree_step_tc(a, st);
     return dt == KDA_BF16 ? launch_step_t<__nv_bfloat16>(a, st) : launch_step_t<float>(a, st);
 }
 cudaError_t launch_tree_commit(const TreeCommitArgs &a, kda_dtype dt, cudaStream_t st) {
