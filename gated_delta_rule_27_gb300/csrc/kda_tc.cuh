@@ -315,6 +315,22 @@ __device__ __forceinline__ void tmem_ld16x2(uint32_t taddr0, uint32_t taddr1, fl
     }
 }
 
+// Two runs of 8 consecutive columns of the thread's TMEM lane, `stride` columns apart, waited for in the same
+// statement.
+__device__ __forceinline__ void tmem_ld8x2(uint32_t taddr, uint32_t stride, float (&r)[2][8]) {
+    uint32_t u[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+          "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(taddr), "r"(taddr + stride)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i / 8][i % 8] = __uint_as_float(u[i]);
+}
+
 // Four runs of 8 consecutive columns of the thread's TMEM lane, `stride` columns apart, waited for in the same
 // statement.
 __device__ __forceinline__ void tmem_ld8x4(uint32_t taddr, uint32_t stride, float (&r)[4][8]) {

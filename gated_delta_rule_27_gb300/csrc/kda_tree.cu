@@ -70,7 +70,7 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
     // log-decay along the paths: each channel by its own thread, parents before children
     for (int c = tid; c < D; c += NT)
         for (int i = 0; i < M; ++i)
-            s_b[i * D + c] = g[base + (size_t)i * row_stride + c] + (i ? s_b[ts.parent[i] * D + c] : 0.f);
+            s_b[i * D + c] = log_decay(g[base + (size_t)i * row_stride + c]) + (i ? s_b[ts.parent[i] * D + c] : 0.f);
     __syncthreads();
     // A and P: a warp per (node, ancestor); the exponent b_i - b_a is one of the path's own decays, so no
     // reference point is needed and no factor leaves the range of the decays themselves
@@ -254,7 +254,7 @@ tree_commit_kernel(const Tin *__restrict__ k, const float *__restrict__ g, const
             float b = 0.f;
             for (int r = L - 1; r >= 0; --r) {
                 s_k[r][c] *= expf(b) * (qk_norm ? s_scale[r] : 1.f);
-                b += g[((size_t)s_row[r] * H + h) * D + c];
+                b += log_decay(g[((size_t)s_row[r] * H + h) * D + c]);
             }
             s_dec[c] = expf(b);
         }

@@ -28,15 +28,15 @@ __device__ __forceinline__ Tree tree_rows(const int32_t *__restrict__ cu, int n,
     return Tree{lo, hi - lo};
 }
 
-// The block's threads read and check request n's tree together (two block barriers).  Returns nodes = -1,
-// with KDA_ERR_INVALID_ARG recorded in *status by one thread of the block, where it breaks the rules.
+// One warp reads and checks request n's tree, the block waits for it (one block barrier).  Returns nodes = -1,
+// where it breaks the rules.
 // The paths come from pointer doubling: after r rounds a node's mask covers its 2^r nearest ancestors.
 __device__ __forceinline__ Tree read_tree(TreeShared &ts, const int32_t *__restrict__ parent,
                                           const int32_t *__restrict__ cu, int n, int total_nodes, int max_nodes,
-                                          bool want_paths) {
+                                          bool want_paths, int reader = 0) {
     const Tree t = tree_rows(cu, n, total_nodes, max_nodes);
-    const int tid = threadIdx.x;
-    if (tid < 32) {
+    const int tid = (int)threadIdx.x - 32 * reader;
+    if (tid >= 0 && tid < 32) {
         bool bad = t.nodes < 0;
         for (int i = tid; i < t.nodes; i += 32) {
             const int p = parent[t.row0 + i];
@@ -85,6 +85,10 @@ __device__ __forceinline__ Tree read_tree(TreeShared &ts, const int32_t *__restr
     __syncthreads();
     return ts.bad ? Tree{0, -1} : t;
 }
+
+// A log-decay, cut where its exponential is zero in fp32, so that sums along a path and their differences stay
+// finite for a decay of -inf.
+__device__ __forceinline__ float log_decay(float g) { return g < -110.f ? -110.f : g; }
 
 __device__ __forceinline__ void report_invalid(int32_t *status) {
     if (status) atomicCAS(status, 0, (int32_t)KDA_ERR_INVALID_ARG);

@@ -1,30 +1,35 @@
 // kda_tree_tc.cu -- the draft-tree step on the Blackwell tensor cores (tcgen05): bf16 inputs, d = 128.
 //
 // With b_i the log-decay along the path to node i, K~ = k e^b, Q~ = q e^b and K^ = k e^{-b} (kda_tree.cu has the
-// recurrence), one CTA per (request, head) forms
-//     [A | P]^T-rows:  D1 = [K~ ; Q~] K^T        (nodes x nodes, masked to the paths; A scaled by beta)
-//     state products:  D2 = S^T [K~ ; Q~]^T      (128 state columns x 2 M)
-//     u_i = beta_i v_i - beta_i x_i - sum_a A_ia u_a,   o_i = y_i + sum_a P_ia u_a
-// so the pool's state is read once, whatever the tree's size.  The floor is that read, 64 KB per (request, head).
+// recurrence), one CTA per (request, head) forms, for a tree of at most MP nodes,
+//     D1 = [K~ ; Q~] K^^T      A and P: masked to the paths, A scaled by beta
+//     D2 = S^T [K~ ; Q~]^T     x and y: the pool's state, 128 columns, times every node's decayed key and query
+//     r  = beta (v - x),  T = (I + A)^{-1}
+//     D3 = r^T (T - I)^T       u = r + D3
+//     D4 = u^T P^T             o = y + D4
+// so the state is read once, whatever the tree's size.  The floor is that read, 64 KB per (request, head).
 //
 // u moves the fp32 state, so it is formed to fp32 accuracy: every operand is split into two bf16 parts, hi + lo,
 // and each product takes hi hi + hi lo + lo hi with fp32 accumulators (2^-17 relative to a term; one part alone
-// would leave 2^-9).  The substitution runs in fp32 on the CUDA cores: D2's lanes are state columns, so a thread owns a column and needs
-// no other thread's results.  A factor e^{-b} would overflow where the decays along a path sum to more than
-// kMaxRange; such a request takes its A and P pairwise from the path's own exponents instead.
+// would leave 2^-9); T comes from an fp32 substitution.  All of it but D2 and what follows is done before the
+// state has arrived.  A factor e^{-b} would overflow where the decays along a path sum to more than kMaxRange;
+// such a request takes its A and P pairwise from the path's own exponents instead.
+//
+// D3 and D4 multiply entries off the paths by zero.  Where an operand is not finite that would carry a NaN from
+// one branch into another, so such a request or column takes a substitution that skips them (solve_masked).
 #include "kda_tc.cuh"
 #include "kda_tree.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kD = 128, kThreads = 256;
+constexpr int kD = 128, kWorkers = 256, kThreads = 288;  // eight worker warps; one that reads the tree and issues the MMAs
 constexpr float kMaxRange = 80.f;
 
-// Shared memory for trees of at most MP nodes, in bytes.  Operand images are K-major with the 128-byte swizzle in
-// two panels of 64 channels, but the state's, which is read as the MN-major A operand (two groups of 64 state
-// columns by 128 rows).  MMAs with fewer than 128 valid A rows read past their image, never past the allocation;
-// what they read there only reaches accumulator rows that nobody looks at.
+// Shared memory for trees of at most MP nodes, in bytes.  Operand images are K-major with the 128-byte swizzle, 64
+// elements to a row (keys and queries: two panels of 64 channels), but the state's, which is read as the MN-major
+// A operand (two groups of 64 state columns by 128 rows).  MMAs with fewer than 128 valid A rows read past their
+// image, never past the allocation; what they read there only reaches accumulator rows that nobody looks at.
 template <int MP>
 struct Layout {
     static constexpr uint32_t kq_panel = 4 * MP * 128;   // rows: K~ hi, Q~ hi, K~ lo, Q~ lo
@@ -35,15 +40,21 @@ struct Layout {
     static constexpr uint32_t s_hi = kq + 2 * kq_panel;
     static constexpr uint32_t s_lo = s_hi + 32768;
     static constexpr uint32_t ki = s_lo + 32768;
-    static constexpr uint32_t ki_bytes = 2 * ki_panel > ap_bytes ? 2 * ki_panel : (ap_bytes + 1023) / 1024 * 1024;
-    static constexpr uint32_t b = ki + ki_bytes;         // fp32 [MP][128]
-    static constexpr uint32_t v = b + MP * 512;          // bf16 [MP][128]
-    static constexpr uint32_t total = v + MP * 256;
-    static constexpr uint32_t ap = ki;                   // fp32 A [MP][ap_stride], then P: once D1 has been formed
-    static constexpr uint32_t u = s_hi;                  // fp32 [MP][128], once D2 has been formed
-    static constexpr uint32_t o = s_lo;                  // fp32 [MP][128]
-    static constexpr uint32_t d2_cols = 4 * MP;
-    static constexpr uint32_t tmem_cols = MP == 8 ? 64 : MP == 16 ? 128 : MP == 32 ? 256 : 512;
+    static constexpr uint32_t b = ki + 2 * ki_panel;     // fp32 [MP][128]: g, then (MP > 16) the paths' sums b
+    static constexpr uint32_t b_bytes = MP * 512 > ap_bytes ? MP * 512 : ap_bytes;
+    static constexpr uint32_t v = b + b_bytes;           // bf16 [MP][128]
+    static constexpr uint32_t tb = v + MP * 256;         // fp32 3 x [32][36]: the blocks of T (MP = 64)
+    static constexpr uint32_t total = tb + (MP == 64 ? 3 * 32 * 36 * 4 : 0);
+    // later uses of the same bytes
+    static constexpr uint32_t t_img = ki;                // T - I: rows hi, lo (once D1 is done)
+    static constexpr uint32_t p_img = ki + MP * 256;     // P: rows hi, lo
+    static constexpr uint32_t ap = b;                    // fp32 A [MP][ap_stride], then P (once the images are built)
+    static constexpr uint32_t z = kq;                    // bf16 [MP][128] (once D2 is done)
+    static constexpr uint32_t r_img = s_hi;              // r: 128 rows hi, 128 rows lo (once D2 is done)
+    static constexpr uint32_t u_img = s_lo;              // u, the same way
+    static constexpr uint32_t o = s_hi;                  // fp32 [MP][128] (once D3 is done)
+    static constexpr uint32_t d1 = 4 * MP, d3 = 4 * MP, d4 = 6 * MP;  // accumulator columns; D2 at 0
+    static constexpr uint32_t tmem_cols = 8 * MP;
 };
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -69,10 +80,33 @@ __device__ __forceinline__ void split8(const float (&f)[8], uint4 &hi, uint4 &lo
     hi = make_uint4(h[0], h[1], h[2], h[3]);
     lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
+// Writes eight consecutive values of an image row, hi at `img` and lo `lo_rows` rows further.
+__device__ __forceinline__ void store_split8(uint8_t *img, int row, int col, int lo_rows, const float (&f)[8]) {
+    uint4 hi, lo;
+    split8(f, hi, lo);
+    const uint32_t at = tc::sw128_offset(row, col);
+    *reinterpret_cast<uint4 *>(img + at) = hi;
+    *reinterpret_cast<uint4 *>(img + lo_rows * 128 + at) = lo;
+}
+__device__ __forceinline__ void store_split1(uint8_t *img, int row, int col, int lo_rows, float f) {
+    const __nv_bfloat16 hi = __float2bfloat16_rn(f), lo = __float2bfloat16_rn(f - __bfloat162float(hi));
+    const uint32_t at = tc::sw128_offset(row, col);
+    *reinterpret_cast<__nv_bfloat16 *>(img + at) = hi;
+    *reinterpret_cast<__nv_bfloat16 *>(img + lo_rows * 128 + at) = lo;
+}
 __device__ __forceinline__ void ldg8(const float *p, float (&f)[8]) {
     asm volatile("ld.global.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
                  : "l"(p));
+}
+__device__ __forceinline__ bool is_finite(float x) { return fabsf(x) < INFINITY; }
+__device__ __forceinline__ void add8(float (&f)[8], const float4 &a, const float4 &b) {
+    f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
+    f[4] += b.x; f[5] += b.y; f[6] += b.z; f[7] += b.w;
+}
+
+__device__ __forceinline__ float4 log_decay4(const float4 &g) {
+    return make_float4(log_decay(g.x), log_decay(g.y), log_decay(g.z), log_decay(g.w));
 }
 
 struct Args {
@@ -91,68 +125,74 @@ struct Args {
     float out_eps;
 };
 
-// Forward substitution of one state column (thread) over all nodes, eight at a time: the products with the u of
-// earlier blocks, then the block's own triangle.  Masked: entries off the path are skipped instead of
-// multiplied by zero, which a non-finite u of another branch would turn into NaN.  Returns false if a u is not
-// finite (never in the masked form).
-template <int MP, bool Masked>
-__device__ __forceinline__ bool substitute(uint8_t *sm, const TreeShared &ts, const float *s_beta, uint32_t d2, int M,
-                                           int c) {
+// r of eight nodes for the thread's state column, from the accumulator's hi and lo columns
+template <int MP>
+__device__ __forceinline__ void residual8(const uint8_t *sm, const float *s_beta, const float (&x_hi)[8],
+                                          const float (&x_lo)[8], int i0, int c, float (&r)[8]) {
+    const __nv_bfloat16 *s_v = reinterpret_cast<const __nv_bfloat16 *>(sm + Layout<MP>::v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        r[e] = s_beta[i0 + e] * (__bfloat162float(s_v[(i0 + e) * kD + c]) - (x_hi[e] + x_lo[e]));
+}
+
+// u and o of the thread's state column by forward substitution over the paths' entries only.  u is kept in the
+// thread's own two rows of u's image, which no other thread reads.
+template <int MP>
+__device__ void solve_masked(uint8_t *sm, const TreeShared &ts, const float *s_beta, uint32_t tmem, int M, int c,
+                             float *u_out, size_t row_stride) {
     using L = Layout<MP>;
     const float *sA = reinterpret_cast<const float *>(sm + L::ap), *sP = sA + MP * L::ap_stride;
-    float *s_u = reinterpret_cast<float *>(sm + L::u), *s_o = reinterpret_cast<float *>(sm + L::o);
-    const __nv_bfloat16 *s_v = reinterpret_cast<const __nv_bfloat16 *>(sm + L::v);
-    bool finite = true;
+    auto mine = [&](int a) {
+        return reinterpret_cast<float *>(sm + L::u_img + (a >> 5) * 16384 + c * 128 + (a & 31) * 4);
+    };
+    float *s_o = reinterpret_cast<float *>(sm + L::o);
     for (int i0 = 0; i0 < M; i0 += 8) {
-        float t[4][8], w[8], out[8];
-        tc::tmem_ld8x4(d2 + i0, MP, t);
+        float t[4][8], r[8];
+        tc::tmem_ld8x4(tmem + i0, MP, t);
+        residual8<MP>(sm, s_beta, t[0], t[2], i0, c, r);
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            w[r] = s_beta[i0 + r] * (__bfloat162float(s_v[(i0 + r) * kD + c]) - (t[0][r] + t[2][r]));
-            out[r] = t[1][r] + t[3][r];
-        }
-        for (int a = 0; a < i0; a += 4) {
-            float ua[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) ua[e] = s_u[(a + e) * kD + c];
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const float4 A = *reinterpret_cast<const float4 *>(&sA[(i0 + r) * L::ap_stride + a]);
-                const float4 P = *reinterpret_cast<const float4 *>(&sP[(i0 + r) * L::ap_stride + a]);
-                const float Av[4] = {A.x, A.y, A.z, A.w}, Pv[4] = {P.x, P.y, P.z, P.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (!Masked || (i0 + r < M && ((ts.anc[i0 + r] >> (a + e)) & 1))) {
-                        w[r] = fmaf(-Av[e], ua[e], w[r]);
-                        out[r] = fmaf(Pv[e], ua[e], out[r]);
+        for (int e = 0; e < 8; ++e) {
+            const int i = i0 + e;
+            if (i < M) {
+                float w = r[e], out = t[1][e] + t[3][e];
+                for (int a = 0; a < i; ++a) {
+                    if ((ts.anc[i] >> a) & 1) {
+                        w = fmaf(-sA[i * L::ap_stride + a], *mine(a), w);
+                        out = fmaf(sP[i * L::ap_stride + a], *mine(a), out);
                     }
                 }
+                *mine(i) = w;
+                s_o[i * kD + c] = fmaf(sP[i * L::ap_stride + i], w, out);
+                if (u_out) u_out[(size_t)i * row_stride] = w;
             }
-        }
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            float Av[8], Pv[8];
-#pragma unroll
-            for (int h = 0; h <= r / 4; ++h) {
-                const float4 A = *reinterpret_cast<const float4 *>(&sA[(i0 + r) * L::ap_stride + i0 + 4 * h]);
-                const float4 P = *reinterpret_cast<const float4 *>(&sP[(i0 + r) * L::ap_stride + i0 + 4 * h]);
-                Av[4 * h] = A.x; Av[4 * h + 1] = A.y; Av[4 * h + 2] = A.z; Av[4 * h + 3] = A.w;
-                Pv[4 * h] = P.x; Pv[4 * h + 1] = P.y; Pv[4 * h + 2] = P.z; Pv[4 * h + 3] = P.w;
-            }
-#pragma unroll
-            for (int a = 0; a < r; ++a) {
-                if (!Masked || (i0 + r < M && ((ts.anc[i0 + r] >> (i0 + a)) & 1))) {
-                    w[r] = fmaf(-Av[a], w[a], w[r]);
-                    out[r] = fmaf(Pv[a], w[a], out[r]);
-                }
-            }
-            out[r] = fmaf(Pv[r], w[r], out[r]);
-            finite &= i0 + r >= M || fabsf(w[r]) < INFINITY;
-            s_u[(i0 + r) * kD + c] = w[r];
-            s_o[(i0 + r) * kD + c] = out[r];
         }
     }
-    return Masked || finite;
+}
+
+// T = (I + A)^{-1} of an NB x NB diagonal block of A, one column per lane: T_ij = [i = j] - sum_{a < i} A_ia T_aj.
+template <int NB>
+__device__ __forceinline__ void invert_block(const float *A, int stride, int lane, float (&t)[NB]) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        float acc[2] = {i == lane ? 1.f : 0.f, 0.f};
+#pragma unroll
+        for (int a0 = 0; a0 < i; a0 += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(&A[i * stride + a0]);
+            const float xa[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (a0 + e < i) acc[e & 1] = fmaf(-xa[e], t[a0 + e], acc[e & 1]);
+        }
+        t[i] = acc[0] + acc[1];
+    }
+}
+
+// The MMAs of D (+)= A_hi [B_hi | B_lo]^T + A_lo [B_hi | B_lo]^T over `steps` slices of 16 elements.
+template <uint32_t Id>
+__device__ __forceinline__ void mma_split(uint32_t d, uint32_t a_hi, uint32_t a_lo, uint32_t b, int steps) {
+    constexpr uint64_t kKmaj = tc::smem_desc_base(16, 1024, tc::SW_128B);
+    for (int c = 0; c < steps; ++c) tc::mma_bf16(d, tc::smem_desc(kKmaj, a_hi + c * 32), tc::smem_desc(kKmaj, b + c * 32), Id, c > 0);
+    for (int c = 0; c < steps; ++c) tc::mma_bf16(d, tc::smem_desc(kKmaj, a_lo + c * 32), tc::smem_desc(kKmaj, b + c * 32), Id, true);
 }
 
 template <int MP>
@@ -161,8 +201,9 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
     extern __shared__ uint8_t raw[];
     __shared__ TreeShared ts;
     __shared__ float s_beta[MP], s_scale[2 * MP];
-    __shared__ uint64_t bars[2];
+    __shared__ uint64_t bars[4];
     __shared__ uint32_t s_tmem;
+    __shared__ int s_wild;  // A, P or T holds something that is not finite
     const int n = blockIdx.x / p.H, h = blockIdx.x % p.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Tree t = tree_rows(p.cu, n, p.total_nodes, p.max_nodes);
     const int slot = slot_of(p.seq_idx, n, p.num_slots);
@@ -173,231 +214,391 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
     if (t.nodes == 0) return;
     const int M = t.nodes;
     uint8_t *sm = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
+    const uint32_t sa = tc::smem_u32(sm);
     const size_t base = ((size_t)t.row0 * p.H + h) * kD, row_stride = (size_t)p.H * kD;
 
-    // All of the CTA's reads, issued at once: g and v on their way to shared memory, k, q and the state in registers.
-    for (int i = tid; i < M * 32; i += kThreads)
-        tc::cp_async16(sm + L::b + i * 16, p.g + base + (size_t)(i >> 5) * row_stride + (i & 31) * 4);
-    for (int i = tid; i < M * 16; i += kThreads)
-        tc::cp_async16(sm + L::v + i * 16, p.v + base + (size_t)(i >> 4) * row_stride + (i & 15) * 8);
-    constexpr int kUnits = MP * 16 > kThreads ? MP * 16 / kThreads : 1;  // (node, 8 channels) per thread
+    // The CTA's reads, issued at once: g, v and beta on their way to shared memory, k, q and the state in registers.
+    constexpr int kUnits = MP / 16;  // (node, 8 channels) per worker: node (tid / 16) + 16 e, channels 8 (tid % 16) on
     uint4 kr[kUnits], qr[kUnits];
+    float s[8][8];                   // state row (tid / 16) + 16 j, columns 8 (tid % 16) on
+    if (warp < 8) {
+        for (int i = tid; i < M * 32; i += kWorkers)
+            tc::cp_async16(sm + L::b + i * 16, p.g + base + (size_t)(i >> 5) * row_stride + (i & 31) * 4);
 #pragma unroll
-    for (int e = 0; e < kUnits; ++e) {
-        const int i = (tid + e * kThreads) >> 4, ch = tid & 15;
-        kr[e] = qr[e] = make_uint4(0, 0, 0, 0);
-        if (i < M) {
-            kr[e] = __ldg(reinterpret_cast<const uint4 *>(p.k + base + (size_t)i * row_stride) + ch);
-            qr[e] = __ldg(reinterpret_cast<const uint4 *>(p.q + base + (size_t)i * row_stride) + ch);
+        for (int e = 0; e < kUnits; ++e) {
+            const int i = (tid >> 4) + 16 * e, ch = tid & 15;
+            kr[e] = qr[e] = make_uint4(0, 0, 0, 0);
+            if (i < M) {
+                kr[e] = __ldg(reinterpret_cast<const uint4 *>(p.k + base + (size_t)i * row_stride) + ch);
+                qr[e] = __ldg(reinterpret_cast<const uint4 *>(p.q + base + (size_t)i * row_stride) + ch);
+            }
         }
-    }
-    if (tid < MP) s_beta[tid] = tid < M ? p.beta[(size_t)(t.row0 + tid) * p.H + h] : 0.f;
-    const float *S = p.S_pool + ((size_t)slot * p.H + h) * kD * kD;
-    float s[8][8];  // row (tid / 16) + 16 j, columns 8 (tid % 16) on
+        for (int i = tid; i < M * 16; i += kWorkers)
+            tc::cp_async16(sm + L::v + i * 16, p.v + base + (size_t)(i >> 4) * row_stride + (i & 15) * 8);
+        const float *S = p.S_pool + ((size_t)slot * p.H + h) * kD * kD;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ldg8(S + (size_t)((tid >> 4) + 16 * j) * kD + (tid & 15) * 8, s[j]);
-
-    if (warp == 0) {
+        for (int j = 0; j < 8; ++j) ldg8(S + (size_t)((tid >> 4) + 16 * j) * kD + (tid & 15) * 8, s[j]);
+        tc::cp_async_wait_all();
+    } else {
+        for (int i = lane; i < MP; i += 32) s_beta[i] = i < M ? p.beta[(size_t)(t.row0 + i) * p.H + h] : 0.f;
         tc::tmem_alloc(&s_tmem, L::tmem_cols);
         tc::tmem_relinquish();
+        if (lane == 0) {
+            for (int i = 0; i < 4; ++i) tc::mbar_init(&bars[i], 1);
+            tc::fence_mbar_init();
+            s_wild = 0;
+        }
+        tc::tc_fence_before();
     }
-    if (tid == 0) {
-        tc::mbar_init(&bars[0], 1);
-        tc::mbar_init(&bars[1], 1);
-        tc::fence_mbar_init();
-    }
-    tc::cp_async_wait_all();
-    tc::tc_fence_before();
-    const bool good = read_tree(ts, p.parent, p.cu, n, p.total_nodes, p.max_nodes, true).nodes > 0;  // a block barrier
+    const bool good = read_tree(ts, p.parent, p.cu, n, p.total_nodes, p.max_nodes, true, 8).nodes > 0;  // a block barrier
     tc::tc_fence_after();
-    const uint32_t tmem = s_tmem, d2 = tmem, d1 = tmem + L::d2_cols;
+    const uint32_t tmem = s_tmem;
     if (!good) {
         if (tid == 0) report_invalid(p.status);
-        if (warp == 0) tc::tmem_dealloc(tmem, L::tmem_cols);
+        if (warp == 8) tc::tmem_dealloc(tmem, L::tmem_cols);
         return;
     }
 
-    // log-decays along the paths, each channel by its own thread, parents before children
+    // Operand images of K~, Q~ and K^.  b sums g over the path; above 16 nodes, 16 nodes at a time, from the b of
+    // the nearest ancestor in an earlier group.
     float *s_b = reinterpret_cast<float *>(sm + L::b);
     float range = 0.f;
-    if (tid < kD) {
-        float b = 0.f;
-        for (int i = 0; i < M; ++i) {
-            const int par = ts.parent[i];
-            b = s_b[i * kD + tid] + (par < 0 ? 0.f : par == i - 1 ? b : s_b[par * kD + tid]);
-            s_b[i * kD + tid] = b;
-            range = fmaxf(range, fabsf(b));
-        }
-    }
-    const bool pairwise = __syncthreads_or(!(range <= kMaxRange));
-
-    // operand images of K~, Q~ and K^
 #pragma unroll
     for (int e = 0; e < kUnits; ++e) {
-        const int i = (tid + e * kThreads) >> 4, ch = tid & 15;
-        if (MP * 16 < kThreads && i >= MP) break;  // warp-uniform
-        float kf[8], qf[8], ki[8], b[8];
-        unpack8(kr[e], kf);
-        unpack8(qr[e], qf);
-        if (p.qk_norm) {  // 16 threads hold a row
-            float sk = 0.f, sq = 0.f;
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                sk = fmaf(kf[x], kf[x], sk);
-                sq = fmaf(qf[x], qf[x], sq);
+        const int i = (tid >> 4) + 16 * e, ch = tid & 15;
+        float b[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (warp < 8 && i < M) {
+            const unsigned long long anc = ts.anc[i];
+            uint32_t here = (uint32_t)(anc >> (16 * e)) & 0xffffu;
+            const unsigned long long before = anc & ((1ull << (16 * e)) - 1);
+            if (e > 0 && before) {
+                const float4 *x = reinterpret_cast<const float4 *>(s_b + (63 - __clzll((long long)before)) * kD + ch * 8);
+                add8(b, x[0], x[1]);
             }
-#pragma unroll
-            for (int off = 8; off; off >>= 1) {
-                sk += __shfl_xor_sync(0xffffffffu, sk, off);
-                sq += __shfl_xor_sync(0xffffffffu, sq, off);
-            }
-            sk = rsqrtf(sk + p.qk_eps);
-            sq = rsqrtf(sq + p.qk_eps);
-            if (ch == 0) {
-                s_scale[i] = sk;
-                s_scale[MP + i] = sq;
-            }
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                kf[x] *= sk;
-                qf[x] *= sq;
+            while (here) {
+                const int a = 16 * e + __ffs((int)here) - 1;
+                here &= here - 1;
+                const float4 *x = reinterpret_cast<const float4 *>(s_b + a * kD + ch * 8);
+                add8(b, log_decay4(x[0]), log_decay4(x[1]));
             }
         }
-        if (i < M) {
-            const float4 b0 = *reinterpret_cast<const float4 *>(&s_b[i * kD + ch * 8]);
-            const float4 b1 = *reinterpret_cast<const float4 *>(&s_b[i * kD + ch * 8 + 4]);
-            b[0] = b0.x; b[1] = b0.y; b[2] = b0.z; b[3] = b0.w;
-            b[4] = b1.x; b[5] = b1.y; b[6] = b1.z; b[7] = b1.w;
+        if (MP > 16) {
+            __syncthreads();  // every sum of this group is formed
+            if (warp < 8 && i < M) {
+                float4 *x = reinterpret_cast<float4 *>(s_b + i * kD + ch * 8);
+                x[0] = make_float4(b[0], b[1], b[2], b[3]);
+                x[1] = make_float4(b[4], b[5], b[6], b[7]);
+            }
+            __syncthreads();
         }
+        if (warp < 8) {
+            float kf[8], qf[8], ki[8];
+            unpack8(kr[e], kf);
+            unpack8(qr[e], qf);
+            if (p.qk_norm) {  // 16 threads hold a row
+                float sk = 0.f, sq = 0.f;
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            ki[x] = 0.f;
-            if (i < M) {
-                const float up = expf(b[x]);
-                ki[x] = kf[x] * expf(-b[x]);
+                for (int x = 0; x < 8; ++x) {
+                    sk = fmaf(kf[x], kf[x], sk);
+                    sq = fmaf(qf[x], qf[x], sq);
+                }
+#pragma unroll
+                for (int off = 8; off; off >>= 1) {
+                    sk += __shfl_xor_sync(0xffffffffu, sk, off);
+                    sq += __shfl_xor_sync(0xffffffffu, sq, off);
+                }
+                sk = rsqrtf(sk + p.qk_eps);
+                sq = rsqrtf(sq + p.qk_eps);
+                if (ch == 0) {
+                    s_scale[i] = sk;
+                    s_scale[MP + i] = sq;
+                }
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    kf[x] *= sk;
+                    qf[x] *= sq;
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const float up = expf(b[x]);  // rows past the tree: zero keys, b = 0
+                range = fmaxf(range, fabsf(b[x]));
+                ki[x] = __fdividef(kf[x], up);  // used while up is within e^{+-kMaxRange}
                 kf[x] *= up;
                 qf[x] *= up;
             }
+            uint8_t *kq = sm + L::kq + (ch >> 3) * L::kq_panel;
+            store_split8(kq, i, (ch & 7) * 8, 2 * MP, kf);
+            store_split8(kq, MP + i, (ch & 7) * 8, 2 * MP, qf);
+            store_split8(sm + L::ki + (ch >> 3) * L::ki_panel, i, (ch & 7) * 8, MP, ki);
         }
-        uint4 hi, lo;
-        uint8_t *kq = sm + L::kq + (ch >> 3) * L::kq_panel, *kin = sm + L::ki + (ch >> 3) * L::ki_panel;
-        const uint32_t at = tc::sw128_offset(i, (ch & 7) * 8);  // the row groups below are multiples of eight rows
-        split8(kf, hi, lo);
-        *reinterpret_cast<uint4 *>(kq + at) = hi;
-        *reinterpret_cast<uint4 *>(kq + 2 * MP * 128 + at) = lo;
-        split8(qf, hi, lo);
-        *reinterpret_cast<uint4 *>(kq + MP * 128 + at) = hi;
-        *reinterpret_cast<uint4 *>(kq + 3 * MP * 128 + at) = lo;
-        split8(ki, hi, lo);
-        *reinterpret_cast<uint4 *>(kin + at) = hi;
-        *reinterpret_cast<uint4 *>(kin + MP * 128 + at) = lo;
     }
     tc::fence_async_smem();
-    __syncthreads();
-    constexpr uint64_t kKmaj = tc::smem_desc_base(16, 1024, tc::SW_128B);
-    constexpr uint64_t kSmn = tc::smem_desc_base(16384, 1024, tc::SW_128B);
-    if (tid == 0 && !pairwise) {  // D1: hi x [hi | lo], then lo x [hi | lo]
-        constexpr uint32_t id = tc::idesc_bf16_f32(128, 2 * MP, false, false);
-        for (int part = 0; part < 2; ++part)
-            for (int c = 0; c < 8; ++c) {
-                const uint32_t a = tc::smem_u32(sm) + L::kq + (c >> 2) * L::kq_panel + part * 2 * MP * 128 + (c & 3) * 32;
-                const uint32_t b = tc::smem_u32(sm) + L::ki + (c >> 2) * L::ki_panel + (c & 3) * 32;
-                tc::mma_bf16(d1, tc::smem_desc(kKmaj, a), tc::smem_desc(kKmaj, b), id, part + c > 0);
+    const bool pairwise = __syncthreads_or(!(range <= kMaxRange));
+    float *sA = reinterpret_cast<float *>(sm + L::ap), *sP = sA + MP * L::ap_stride;
+    if (pairwise) {
+        // A warp per (node, ancestor), four channels a lane, into the state images' place first: the results'
+        // own place holds b.
+        float *xA = reinterpret_cast<float *>(sm + L::s_hi), *xP = xA + MP * L::ap_stride;
+        if (MP == 16) {
+            if (tid < kD)
+                for (int i = 0; i < M; ++i)
+                    s_b[i * kD + tid] = log_decay(s_b[i * kD + tid]) + (i ? s_b[ts.parent[i] * kD + tid] : 0.f);
+            __syncthreads();
+        }
+        if (warp < 8)
+            for (int x = warp; x < MP * MP; x += 8) {
+                const int i = x / MP, a = x % MP;
+                float va = 0.f, vp = 0.f;
+                if (i < M && ((ts.anc[i] >> a) & 1)) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int c = lane + 32 * e;
+                        const float ka = __bfloat162float(p.k[base + (size_t)a * row_stride + c]) *
+                                         expf(s_b[i * kD + c] - s_b[a * kD + c]);
+                        va = fmaf(__bfloat162float(p.k[base + (size_t)i * row_stride + c]), ka, va);
+                        vp = fmaf(__bfloat162float(p.q[base + (size_t)i * row_stride + c]), ka, vp);
+                    }
+#pragma unroll
+                    for (int off = 16; off; off >>= 1) {
+                        va += __shfl_xor_sync(0xffffffffu, va, off);
+                        vp += __shfl_xor_sync(0xffffffffu, vp, off);
+                    }
+                    if (p.qk_norm) {
+                        va *= s_scale[i] * s_scale[a];
+                        vp *= s_scale[MP + i] * s_scale[a];
+                    }
+                    va = a == i ? 0.f : s_beta[i] * va;
+                }
+                if (lane == 0) {
+                    xA[i * L::ap_stride + a] = va;
+                    xP[i * L::ap_stride + a] = vp;
+                }
             }
+        __syncthreads();
+        for (int x = tid; x < 2 * MP * L::ap_stride; x += kThreads) sA[x] = xA[x];
+        __syncthreads();
+    } else if (warp == 8 && lane == 0) {  // D1, a panel at a time
+        constexpr uint32_t id = tc::idesc_bf16_f32(128, 2 * MP, false, false);
+        constexpr uint64_t kKmaj = tc::smem_desc_base(16, 1024, tc::SW_128B);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            const uint32_t a = sa + L::kq + (c >> 3) * 2 * MP * 128 + ((c >> 2) & 1) * L::kq_panel + (c & 3) * 32;
+            const uint32_t b = sa + L::ki + ((c >> 2) & 1) * L::ki_panel + (c & 3) * 32;
+            tc::mma_bf16(tmem + L::d1, tc::smem_desc(kKmaj, a), tc::smem_desc(kKmaj, b), id, c > 0);
+        }
         tc::mma_commit(&bars[0]);
     }
-    // the state's images
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int row = (tid >> 4) + 16 * j, col = (tid & 15) * 8;
-        uint4 hi, lo;
-        split8(s[j], hi, lo);
-        const uint32_t at = (col >> 6) * 16384 + tc::sw128_offset(row, col & 63);
-        *reinterpret_cast<uint4 *>(sm + L::s_hi + at) = hi;
-        *reinterpret_cast<uint4 *>(sm + L::s_lo + at) = lo;
-    }
-    tc::fence_async_smem();
-    __syncthreads();
-    if (tid == 0) {  // D2: S hi x [hi | lo], then S lo x hi
-        constexpr uint32_t id4 = tc::idesc_bf16_f32(128, 4 * MP, true, false);
-        constexpr uint32_t id2 = tc::idesc_bf16_f32(128, 2 * MP, true, false);
-        for (int part = 0; part < 2; ++part)
-            for (int c = 0; c < 8; ++c) {
-                const uint32_t a = tc::smem_u32(sm) + (part ? L::s_lo : L::s_hi) + c * 2048;
-                const uint32_t b = tc::smem_u32(sm) + L::kq + (c >> 2) * L::kq_panel + (c & 3) * 32;
-                tc::mma_bf16(d2, tc::smem_desc(kSmn, a), tc::smem_desc(kKmaj, b), part ? id2 : id4, part + c > 0);
-            }
-        tc::mma_commit(&bars[1]);
-    }
     __syncwarp();
-
-    float *sA = reinterpret_cast<float *>(sm + L::ap), *sP = sA + MP * L::ap_stride;
+    if (warp < 8) {  // the state's images
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int row = (tid >> 4) + 16 * j, col = (tid & 15) * 8;
+            uint4 hi, lo;
+            split8(s[j], hi, lo);
+            const uint32_t at = (col >> 6) * 16384 + tc::sw128_offset(row, col & 63);
+            *reinterpret_cast<uint4 *>(sm + L::s_hi + at) = hi;
+            *reinterpret_cast<uint4 *>(sm + L::s_lo + at) = lo;
+        }
+        tc::fence_async_smem();
+    }
+    __syncthreads();
     bool ok = true;
-    if (!pairwise) {
-        if (warp * 32 < 2 * MP && warp < 4) {  // lanes are the rows of [K~ ; Q~]
-            ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[0], 0));
+    if (warp == 8) {
+        if (lane == 0) {  // D2: S hi x [hi | lo], then S lo x hi
+            constexpr uint32_t id4 = tc::idesc_bf16_f32(128, 4 * MP, true, false);
+            constexpr uint32_t id2 = tc::idesc_bf16_f32(128, 2 * MP, true, false);
+            constexpr uint64_t kSmn = tc::smem_desc_base(16384, 1024, tc::SW_128B);
+            constexpr uint64_t kKmaj = tc::smem_desc_base(16, 1024, tc::SW_128B);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                const uint32_t a = sa + (c >> 3 ? L::s_lo : L::s_hi) + (c & 7) * 2048;
+                const uint32_t b = sa + L::kq + ((c >> 2) & 1) * L::kq_panel + (c & 3) * 32;
+                tc::mma_bf16(tmem, tc::smem_desc(kSmn, a), tc::smem_desc(kKmaj, b), c >> 3 ? id2 : id4, c > 0);
+            }
+            tc::mma_commit(&bars[1]);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // A, P, T and the images of T - I and P, while D2 runs.  Lane r of D1 is row r of [K~ ; Q~].
+        const int row = (warp - 4) * 32 + lane;
+        if ((warp - 4) * 32 < 2 * MP) {
+            if (!pairwise) ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[0], 0));
             tc::tc_fence_after();
-            const int r = warp * 32 + lane, i = r % MP;
+            const bool is_a = row < MP;
+            const int i = is_a ? row : row - MP;
             const unsigned long long anc = i < M ? ts.anc[i] : 0ull;
-            const bool is_a = r < MP;
             const float scale = is_a ? s_beta[i] : 1.f;
+            bool wild = false;
             for (int a0 = 0; a0 < MP; a0 += 8) {
-                float x[4][8];  // columns a0 on of the hi part, then of the lo part; the other two runs are not used
-                if (ok) tc::tmem_ld8x4(d1 + ((uint32_t)(warp * 32) << 16) + a0, MP == 8 ? 8 : MP, x);
                 float val[8];
+                float *dst = (is_a ? sA : sP) + i * L::ap_stride + a0;
+                if (!pairwise) {
+                    float x[2][8];
+                    tc::tmem_ld8x2(tmem + L::d1 + ((uint32_t)((warp - 4) * 32) << 16) + a0, MP, x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        val[e] = ((anc >> (a0 + e)) & 1) && !(is_a && a0 + e == i) ? scale * (x[0][e] + x[1][e]) : 0.f;
+                    reinterpret_cast<float4 *>(dst)[0] = make_float4(val[0], val[1], val[2], val[3]);
+                    reinterpret_cast<float4 *>(dst)[1] = make_float4(val[4], val[5], val[6], val[7]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) val[e] = dst[e];
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) wild |= !is_finite(val[e]);
+                if (!is_a) store_split8(sm + L::p_img, i, a0, MP, val);
+            }
+            if (wild) s_wild = 1;
+        }
+        if (MP == 64) tc::named_barrier(1, 128);
+        else __syncwarp();
+        constexpr int NB = MP < 32 ? MP : 32;
+        float *tb = reinterpret_cast<float *>(sm + L::tb);  // MP = 64: T's diagonal blocks and A21 T11, [32][36] each
+        if (warp - 4 < MP / NB) {
+            const int o = (warp - 4) * NB;
+            float tc_[NB];
+            invert_block<NB>(sA + o * L::ap_stride + o, L::ap_stride, lane, tc_);
+            bool wild = false;
+            if (lane < NB) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    wild |= !is_finite(tc_[i]);
+                    store_split1(sm + L::t_img, o + i, o + lane, MP, i == lane ? 0.f : tc_[i]);
+                    if (MP == 64) tb[(warp - 4) * 32 * 36 + i * 36 + lane] = tc_[i];
+                }
+                if (wild) s_wild = 1;
+            }
+        }
+        if (MP == 64) {  // T21 = -T22 (A21 T11); nothing above the diagonal
+            tc::named_barrier(1, 128);
+            const int i = (tid - 128) >> 2, j0 = (tid & 3) * 8;
+            const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            store_split8(sm + L::t_img, i, 32 + j0, MP, zero);
+#pragma unroll
+            for (int step = 0; step < 2; ++step) {
+                const float *left = step ? tb + 32 * 36 + i * 36 : sA + (32 + i) * L::ap_stride;
+                const float *right = step ? tb + 2 * 32 * 36 : tb;
+                float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+                for (int a = 0; a < 32; ++a) {
+                    const float x = left[a];
+                    const float4 *y = reinterpret_cast<const float4 *>(right + a * 36 + j0);
+                    const float4 y0 = y[0], y1 = y[1];
+                    acc[0] = fmaf(x, y0.x, acc[0]); acc[1] = fmaf(x, y0.y, acc[1]);
+                    acc[2] = fmaf(x, y0.z, acc[2]); acc[3] = fmaf(x, y0.w, acc[3]);
+                    acc[4] = fmaf(x, y1.x, acc[4]); acc[5] = fmaf(x, y1.y, acc[5]);
+                    acc[6] = fmaf(x, y1.z, acc[6]); acc[7] = fmaf(x, y1.w, acc[7]);
+                }
+                if (step == 0) {
+                    float4 *dst = reinterpret_cast<float4 *>(tb + 2 * 32 * 36 + i * 36 + j0);
+                    dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                    dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+                    tc::named_barrier(1, 128);
+                } else {
+                    bool wild = false;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        acc[e] = -acc[e];
+                        wild |= !is_finite(acc[e]);
+                    }
+                    store_split8(sm + L::t_img, 32 + i, j0, MP, acc);
+                    if (wild) s_wild = 1;
+                }
+            }
+        }
+        tc::fence_async_smem();
+        // the gate, into the place of D2's operands
+        ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bars[1], 0));
+        if (p.gate)
+            for (int i = tid - 128; i < M * 16; i += 128)
+                tc::cp_async16(sm + L::z + i * 16, p.gate + base + (size_t)(i >> 4) * row_stride + (i & 15) * 8);
+    }
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    bool finite = true;
+    if (warp < 4) {  // r, for D3; a thread is a state column
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[1], 0));
+        tc::tc_fence_after();
+        for (int i0 = 0; i0 < MP; i0 += 8) {
+            float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (i0 < M) {
+                float x[2][8];
+                tc::tmem_ld8x2(lanes + i0, 2 * MP, x);
+                residual8<MP>(sm, s_beta, x[0], x[1], i0, tid, r);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int a = a0 + e;
-                    val[e] = ((anc >> a) & 1) && !(is_a && a == i) ? scale * (x[0][e] + x[1][e]) : 0.f;
-                }
-                if (r < 2 * MP) {
-                    float4 *dst = reinterpret_cast<float4 *>((is_a ? sA : sP) + i * L::ap_stride + a0);
-                    dst[0] = make_float4(val[0], val[1], val[2], val[3]);
-                    dst[1] = make_float4(val[4], val[5], val[6], val[7]);
+                    r[e] = i0 + e < M ? r[e] : 0.f;
+                    finite &= is_finite(r[e]);
                 }
             }
+            store_split8(sm + L::r_img, tid, i0, 128, r);
         }
-    } else {
-        // a warp per (node, ancestor), four channels a lane; K^ is not used, so A and P go over it
-        for (int x = warp; x < M * M; x += kThreads / 32) {
-            const int i = x / M, a = x % M;
-            float sa = 0.f, sp = 0.f;
-            if ((ts.anc[i] >> a) & 1) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int c = lane + 32 * e;
-                    const float ka = __bfloat162float(p.k[base + (size_t)a * row_stride + c]) *
-                                     expf(s_b[i * kD + c] - s_b[a * kD + c]);
-                    sa = fmaf(__bfloat162float(p.k[base + (size_t)i * row_stride + c]), ka, sa);
-                    sp = fmaf(__bfloat162float(p.q[base + (size_t)i * row_stride + c]), ka, sp);
-                }
-#pragma unroll
-                for (int off = 16; off; off >>= 1) {
-                    sa += __shfl_xor_sync(0xffffffffu, sa, off);
-                    sp += __shfl_xor_sync(0xffffffffu, sp, off);
-                }
-                if (p.qk_norm) {
-                    sa *= s_scale[i] * s_scale[a];
-                    sp *= s_scale[MP + i] * s_scale[a];
-                }
-            }
-            if (lane == 0) {
-                sA[i * L::ap_stride + a] = a == i ? 0.f : s_beta[i] * sa;
-                sP[i * L::ap_stride + a] = sp;
-            }
-        }
-    }
-    ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bars[1], 0));
-    tc::tc_fence_after();
-    ok = __syncthreads_and(ok);  // every wait was met, A and P are complete, and the state's images are free
-    if (ok && warp < 4) {
-        const uint32_t lanes = d2 + ((uint32_t)(warp * 32) << 16);
-        if (!__all_sync(0xffffffffu, substitute<MP, false>(sm, ts, s_beta, lanes, M, tid)))
-            substitute<MP, true>(sm, ts, s_beta, lanes, M, tid);
+        tc::fence_async_smem();
         tc::tc_fence_before();
     }
-    __syncthreads();
-    if (warp == 0) {
+    ok = __syncthreads_and(ok);  // every wait so far was met; r, T and P are complete
+    if (ok && warp == 8) {
+        tc::tc_fence_after();
+        if (lane == 0) {
+            mma_split<tc::idesc_bf16_f32(128, 2 * MP, false, false)>(tmem + L::d3, sa + L::r_img, sa + L::r_img + 16384,
+                                                                     sa + L::t_img, MP / 16);
+            tc::mma_commit(&bars[2]);
+        }
+        __syncwarp();
+    }
+    const bool masked = s_wild || !__all_sync(0xffffffffu, finite);  // of a worker warp's columns
+    float *u_out = p.u ? p.u + base + tid : nullptr;
+    if (ok && warp < 4) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[2], 0));
+        tc::tc_fence_after();
+        if (masked) {
+            solve_masked<MP>(sm, ts, s_beta, lanes, M, tid, u_out, row_stride);
+        } else {
+            for (int i0 = 0; i0 < MP; i0 += 8) {
+                float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (i0 < M) {
+                    float x[2][8], d[2][8];
+                    tc::tmem_ld8x2(lanes + i0, 2 * MP, x);
+                    tc::tmem_ld8x2(lanes + L::d3 + i0, MP, d);
+                    residual8<MP>(sm, s_beta, x[0], x[1], i0, tid, u);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        u[e] = i0 + e < M ? u[e] + (d[0][e] + d[1][e]) : 0.f;
+                        if (u_out && i0 + e < M) u_out[(size_t)(i0 + e) * row_stride] = u[e];
+                    }
+                }
+                store_split8(sm + L::u_img, tid, i0, 128, u);
+            }
+        }
+        tc::fence_async_smem();
+        tc::tc_fence_before();
+    }
+    ok = __syncthreads_and(ok);
+    if (ok && warp == 8) {
+        tc::tc_fence_after();
+        if (lane == 0) {
+            mma_split<tc::idesc_bf16_f32(128, 2 * MP, false, false)>(tmem + L::d4, sa + L::u_img, sa + L::u_img + 16384,
+                                                                     sa + L::p_img, MP / 16);
+            tc::mma_commit(&bars[3]);
+        }
+        __syncwarp();
+    }
+    if (ok && warp < 4) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[3], 0));
+        tc::tc_fence_after();
+        float *s_o = reinterpret_cast<float *>(sm + L::o);
+        for (int i0 = 0; i0 < M && !masked; i0 += 8) {
+            float y[2][8], d[2][8];
+            tc::tmem_ld8x2(lanes + MP + i0, 2 * MP, y);
+            tc::tmem_ld8x2(lanes + L::d4 + i0, MP, d);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s_o[(i0 + e) * kD + tid] = (y[0][e] + y[1][e]) + (d[0][e] + d[1][e]);
+        }
+        tc::tc_fence_before();
+    }
+    tc::cp_async_wait_all();
+    ok = __syncthreads_and(ok);
+    if (warp == 8) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem, L::tmem_cols);
     }
@@ -405,13 +606,11 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
         if (tid == 0 && p.status) atomicCAS(p.status, 0, (int32_t)KDA_ERR_TIMEOUT);
         return;
     }
-    for (int i = warp; i < M; i += kThreads / 32) {
+    for (int i = warp; i < M && warp < 8; i += 8) {
         const size_t at = base + (size_t)i * row_stride + lane * 4;
-        if (p.u)
-            *reinterpret_cast<float4 *>(p.u + at) = *reinterpret_cast<const float4 *>(sm + L::u + i * 512 + lane * 16);
         float4 x = *reinterpret_cast<const float4 *>(sm + L::o + i * 512 + lane * 16);
         if (p.gate) {
-            const uint2 z = __ldg(reinterpret_cast<const uint2 *>(p.gate + at));
+            const uint2 z = *reinterpret_cast<const uint2 *>(sm + L::z + i * 256 + lane * 8);
             float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
             if (p.weight) w = __ldg(reinterpret_cast<const float4 *>(p.weight) + lane);
             float ss = fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, x.w * x.w)));
@@ -445,7 +644,6 @@ cudaError_t launch_tree_step_tc(const TreeStepArgs &a, cudaStream_t st) {
                  (__nv_bfloat16 *)a.o, a.u, a.status, a.fu.qk_norm, a.fu.qk_eps, (const __nv_bfloat16 *)a.fu.gate,
                  a.fu.weight, a.fu.out_eps};
     const int ctas = a.num_seqs * a.H;
-    if (a.max_nodes <= 8) return launch_mp<8>(p, ctas, st);
     if (a.max_nodes <= 16) return launch_mp<16>(p, ctas, st);
     if (a.max_nodes <= 32) return launch_mp<32>(p, ctas, st);
     return launch_mp<64>(p, ctas, st);

@@ -115,6 +115,46 @@ def test_extreme_gates(d, dtype, back):
     assert rel(o, o_ref) <= TOL[dtype] and rel(u, u_ref) <= 1e-4
 
 
+@pytest.mark.parametrize("d,dtype", [(16, F32), (128, F32), (128, BF)])
+def test_a_decay_of_minus_infinity_forgets(d, dtype):
+    """A log-decay of -inf clears its channels: what is above it on the path is gone, nothing becomes NaN."""
+    x = step_inputs([20, 40], 1, d, dtype, seed=3)
+    x["g"][torch.rand(x["g"].shape, generator=torch.Generator().manual_seed(1)) < 0.1] = -float("inf")
+    o, u, pool = run_step(x, 64)
+    o_ref, u_ref, states = tree.tree_step(*(f64(x[n]) for n in ("q", "k", "v", "g", "beta")), x["parent"], x["cu"], x["slots"], f64(x["pool"]))
+    assert rel(o, o_ref) <= TOL[dtype] and rel(u, u_ref) <= 1e-4
+    path, want = [[0] + [i for i in range(1, 20) if _above(x["parent"], i, 19)] + [-1] * 19, [-1] * 20], f64(x["pool"]).copy()
+    taken = sum(i >= 0 for i in path[0])
+    want[x["slots"][0]] = states[19]
+    libkda.kda_tree_commit(x["k"].cuda(), x["g"].cuda(), u, i32(x["cu"]), i32([path[0][:20], path[1]]), i32([taken, 0]), i32(x["slots"]), pool)
+    assert rel(pool, want) <= 1e-4
+
+
+def _above(parent, i, leaf):
+    while leaf > i:
+        leaf = parent[leaf]
+    return leaf == i
+
+
+@pytest.mark.parametrize("d,dtype", [(64, F32), (128, F32), (128, BF)])
+@pytest.mark.parametrize("M", [12, 30, 60])
+def test_a_bad_node_only_reaches_its_descendants(M, d, dtype):
+    """NaN or infinite values of one node leave every node that is not below it untouched."""
+    clean = step_inputs([M], 2, d, dtype, seed=M)
+    # a node with some of the later ones below it, and some not
+    bad = next(b for b in range(1, M) if 1 < sum(_above(clean["parent"], b, i) for i in range(M)) < M - b)
+    below = [_above(clean["parent"], bad, i) for i in range(M)]
+    want = run_step(clean, M)[:2]
+    for name, value in (("v", float("nan")), ("v", float("inf")), ("k", float("nan")), ("q", float("nan")), ("g", float("nan")), ("beta", float("inf"))):
+        x = dict(clean, **{name: clean[name].clone()})
+        x[name][bad, 1] = value
+        for got, ref in zip(run_step(x, M)[:2], want):
+            keep = [i for i in range(M) if not below[i]]
+            assert torch.equal(got[:, 0], ref[:, 0])
+            assert rel(got[keep], f64(ref[keep])) <= TOL[got.dtype]
+    assert not torch.isfinite(run_step(dict(clean, v=torch.where(torch.arange(M)[:, None, None] == bad, float("nan"), clean["v"].float()).to(dtype)), M)[0][bad]).any()
+
+
 @pytest.mark.parametrize("d,dtype", [(64, F32), (128, BF)])
 def test_step_is_independent_of_the_batch_and_of_u(d, dtype):
     """A request alone, without u and under a larger bound gives the bits it gives in a batch."""
