@@ -405,7 +405,7 @@ kda_status kda_draft_verify(const void *logits, const float *draft_probs, const 
                             int32_t *status, void *stream) {
     if (kda_status st = tree_check(num_seqs, total_nodes, path_stride, 0, in_dtype)) return st;
     if (V <= 0) return KDA_ERR_INVALID_ARG;
-    if (V > KDA_VERIFY_MAX_VOCAB) return KDA_ERR_UNSUPPORTED;
+    if (V > KDA_VERIFY_MAX_VOCAB || num_seqs > INT_MAX / 8) return KDA_ERR_UNSUPPORTED;  // up to 8 CTAs a request
     if (num_seqs == 0) return KDA_OK;
     const uintptr_t el = in_dtype == KDA_BF16 ? 1u : 3u;
     if (total_nodes > 0 && (!logits || (reinterpret_cast<uintptr_t>(logits) & el) || !aligned4(draft_probs) ||

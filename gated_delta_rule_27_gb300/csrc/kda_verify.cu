@@ -11,28 +11,87 @@
 //
 // Sums over the vocabulary are exact: every term is cut to a multiple of 2^-40 and added as an integer, so
 // neither the split of the row nor the order of the additions can change a decision.
+//
+// Only the rows that the walk visits are read.  One cluster of CTAs serves a request; each CTA keeps its part of
+// the visited row in shared memory, so that the maximum, the sum, the excess after a rejection and the search
+// for the next token all work on one read of the row.
+#include <cooperative_groups.h>
+
+#include "kda_tc.cuh"
 #include "kda_tree.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace kda {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kVec = 4;
+constexpr int kThreads = 256, kWarps = kThreads / 32, kMaxCluster = 8;
+constexpr uint32_t kMaxPart = 65536;  // bytes of a row that a CTA keeps; a longer part is read again by every pass
 constexpr float kFixed = 1099511627776.f;  // 2^40
 
 __device__ __forceinline__ unsigned long long fixed40(float x) { return __float2ull_rz(x * kFixed); }
 
-// What a row's weights are computed from.
-struct RowStats {
-    float top, scale;
-    int best;   // the lowest index of the largest logit; -1: no logit above -inf
-    int onehot; // all the weight at `best` (temperature 0)
+// A sum of values in [0, 1] cut to multiples of 2^-40, without 64-bit conversions: adding 1 with rounding towards
+// zero leaves the first 23 bits of the value in the sum's mantissa, adding 2^-17 to the rest the next 17; the bit
+// patterns add up as integers.  At most kFlush values between two flushes.
+constexpr int kFlush = 256;
+struct FixedSum {
+    uint32_t hi = 0, lo = 0;
+    __device__ __forceinline__ void add(float x) {
+        const float a = __fadd_rz(x, 1.f);
+        const float b = __fadd_rz(__fsub_rn(x, __fsub_rn(a, 1.f)), 0x1p-17f);
+        hi += __float_as_uint(a);
+        lo += __float_as_uint(b);
+    }
+    __device__ __forceinline__ unsigned long long take(uint32_t count) {
+        const uint32_t h = hi - count * 0x3f800000u, l = lo - count * 0x37000000u;
+        hi = lo = 0;
+        return ((unsigned long long)h << 17) + l;
+    }
 };
-// w_t.  NaN logits weigh nothing; logits of +inf share the weight.
-__device__ __forceinline__ float weight_of(const RowStats &r, float l, int t) {
-    if (r.onehot) return t == r.best ? 1.f : 0.f;
-    if (l == r.top) return 1.f;  // also where both are +inf
-    return fmaxf(exp2f(__fmul_rn(__fsub_rn(l, r.top), r.scale)), 0.f);
+
+// What a row's weights are computed from.
+struct Row {
+    float top, scale;
+    int best;    // the lowest index of the largest logit; -1: no logit above -inf
+    bool onehot; // all the weight at `best` (temperature 0)
+    bool flat;   // top is +inf: the weight is one at +inf and zero elsewhere
+};
+// 2^x; below 2^-126, far below the sums' resolution, it is zero
+__device__ __forceinline__ float exp2_of(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
+// w_t of a row with a spread-out weight; a NaN logit weighs nothing
+__device__ __forceinline__ float weight_of(const Row &r, float l) {
+    if (r.flat) return l == r.top ? 1.f : 0.f;
+    return fmaxf(exp2_of(__fmul_rn(__fsub_rn(l, r.top), r.scale)), 0.f);
+}
+__device__ __forceinline__ float excess_of(float w, float C, float q) { return fmaxf(__fsub_rn(w, __fmul_rn(C, q)), 0.f); }
+
+struct Found {  // a maximum and its lowest index
+    float top;
+    int best;
+};
+__device__ __forceinline__ Found better(Found a, Found b) {
+    return b.top > a.top || (b.top == a.top && (uint32_t)b.best < (uint32_t)a.best) ? b : a;
+}
+
+struct Shared {
+    TreeShared tree;
+    unsigned long long child[kMaxNodes];            // children of each node
+    int token[kMaxNodes];                           // of the visited node's children, in order
+    float u[kMaxNodes], logit[kMaxNodes], q[kMaxNodes];
+    int removed[kMaxNodes];                         // tokens rejected at the visited node, when there is no q
+    unsigned long long removed_w[kMaxNodes];
+    unsigned long long part[64];
+    unsigned long long warp_sum[kWarps];
+    Found warp_max[kWarps];
+    Found cta_max[2][kMaxCluster];                  // exchanged: two places, taken in turn
+    unsigned long long cta_sum[2][kMaxCluster];
+    unsigned long long sum_w[kMaxCluster], sum_r[kMaxCluster];
+};
 
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long x) {
 #pragma unroll
@@ -40,182 +99,401 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long x) {
     return x;
 }
 
-struct Shared {
-    TreeShared tree;
-    unsigned long long sum[kWarps];
-    float top[kWarps];
-    int best[kWarps];
-    int removed[kMaxNodes];
-    int found;
-};
-
-__device__ __forceinline__ unsigned long long block_sum(Shared &sh, unsigned long long x) {
+// Every thread gets the CTAs' sums of x in sums[] (shared memory) and their total.
+__device__ __forceinline__ unsigned long long cluster_sum(Shared &sh, cg::cluster_group &cluster, int &turn, int size,
+                                                          unsigned long long x, unsigned long long *sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     x = warp_sum(x);
+    if (lane == 0) sh.warp_sum[warp] = x;
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh.sum[threadIdx.x >> 5] = x;
-    __syncthreads();
+    turn ^= 1;
+    if (threadIdx.x < size) {
+        unsigned long long total = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) total += sh.warp_sum[w];
+        cluster.map_shared_rank(&sh, threadIdx.x)->cta_sum[turn][cluster.block_rank()] = total;
+    }
+    cluster.sync();
     unsigned long long total = 0;
-    for (int w = 0; w < kWarps; ++w) total += sh.sum[w];
+    for (int r = 0; r < size; ++r) total += sh.cta_sum[turn][r];
+    if (threadIdx.x < size) sums[threadIdx.x] = sh.cta_sum[turn][threadIdx.x];
     return total;
 }
 
-// r_t of the row after its rejections
-template <typename Tin>
-__device__ __forceinline__ float rest_of(const Shared &sh, const RowStats &st, const Tin *row, const float *q, float C,
-                                         int removed, int t) {
-    const float w = weight_of(st, to_f32(row[t]), t);
-    if (q) return C > 0.f ? fmaxf(__fsub_rn(w, __fmul_rn(C, q[t])), 0.f) : w;
-    for (int i = 0; i < removed; ++i)
-        if (sh.removed[i] == t) return 0.f;
-    return w;
+__device__ __forceinline__ Found cluster_max(Shared &sh, cg::cluster_group &cluster, int &turn, int size, Found f) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int off = 16; off; off >>= 1)
+        f = better(f, Found{__shfl_xor_sync(0xffffffffu, f.top, off), __shfl_xor_sync(0xffffffffu, f.best, off)});
+    if (lane == 0) sh.warp_max[warp] = f;
+    __syncthreads();
+    turn ^= 1;
+    if (threadIdx.x < size) {
+        Found a = sh.warp_max[0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) a = better(a, sh.warp_max[w]);
+        cluster.map_shared_rank(&sh, threadIdx.x)->cta_max[turn][cluster.block_rank()] = a;
+    }
+    cluster.sync();
+    Found a = sh.cta_max[turn][0];
+    for (int r = 1; r < size; ++r) a = better(a, sh.cta_max[turn][r]);
+    return a;
 }
 
+// A CTA's part of one row.  The row is cut at 16-byte boundaries of memory into vectors of `kVec` logits, of which
+// the first and last may be partial; `lead` is the number of places before the row's first logit in vector 0.
 template <typename Tin>
-__global__ void __launch_bounds__(kThreads)
-draft_verify_kernel(const Tin *__restrict__ logits, const float *__restrict__ probs, const int32_t *__restrict__ tokens,
-                    const int32_t *__restrict__ parent, const int32_t *__restrict__ cu,
-                    const float *__restrict__ temperature, const float *__restrict__ u,
-                    const float *__restrict__ u_next, int total_nodes, int V, int path_stride,
-                    int32_t *__restrict__ path, int32_t *__restrict__ path_len, int32_t *__restrict__ next_token,
-                    int32_t *__restrict__ status) {
+struct Part {
+    static constexpr int kVec = 16 / sizeof(Tin);
+    const Tin *row;
+    uint4 *kept;  // the part in shared memory, or null
+    int lead, V, v0, v1;
+
+    __device__ __forceinline__ uint4 load(int v) const {
+        const int i0 = v * kVec - lead;
+        if (i0 >= 0 && i0 + kVec <= V) return __ldg(reinterpret_cast<const uint4 *>(row + i0));
+        union {
+            uint4 vec;
+            Tin x[kVec];
+        } out;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) out.x[e] = i0 + e >= 0 && i0 + e < V ? row[i0 + e] : from_f32<Tin>(-INFINITY);
+        return out.vec;
+    }
+    // Starts the copy of the part to shared memory (complete after cp_async_wait_all and a block barrier).
+    __device__ __forceinline__ void fetch() const {
+        if (!kept) return;
+        for (int v = v0 + threadIdx.x; v < v1; v += kThreads) {
+            const int i0 = v * kVec - lead;
+            if (i0 >= 0 && i0 + kVec <= V) tc::cp_async16(kept + (v - v0), row + i0);
+            else kept[v - v0] = load(v);
+        }
+    }
+    __device__ __forceinline__ void get(int v, float (&l)[kVec]) const {
+        const uint4 x = kept ? kept[v - v0] : load(v);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (sizeof(Tin) == 4) {
+                l[e] = __uint_as_float(w[e]);
+            } else {
+                l[2 * e] = __uint_as_float(w[e] << 16);
+                l[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+            }
+        }
+    }
+    __device__ __forceinline__ void get_q(const float *q, int v, float (&x)[kVec]) const {
+        const int i0 = v * kVec - lead;
+        const float *at = q + i0;
+        if (i0 >= 0 && i0 + kVec <= V && (reinterpret_cast<uintptr_t>(at) & 15u) == 0) {
+#pragma unroll
+            for (int e = 0; e < kVec / 4; ++e) {
+                const float4 y = __ldg(reinterpret_cast<const float4 *>(at) + e);
+                x[4 * e] = y.x; x[4 * e + 1] = y.y; x[4 * e + 2] = y.z; x[4 * e + 3] = y.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) x[e] = i0 + e >= 0 && i0 + e < V ? __ldg(at + e) : 0.f;
+        }
+    }
+};
+
+struct Args {
+    const void *logits;
+    const float *probs;
+    const int32_t *tokens, *parent, *cu;
+    const float *temperature, *u, *u_next;
+    int total_nodes, V, path_stride;
+    uint32_t part_bytes;  // of dynamic shared memory: 0 where a part would not fit
+    int32_t *path, *path_len, *next_token, *status;
+};
+
+template <typename Tin>
+__global__ void __launch_bounds__(kThreads) draft_verify_kernel(const Args p) {
+    using P = Part<Tin>;
+    extern __shared__ uint4 kept[];
     __shared__ Shared sh;
-    const int n = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const Tree t = read_tree(sh.tree, parent, cu, n, total_nodes, min(path_stride, kMaxNodes), false);
-    if (t.nodes < 0 && tid == 0) report_invalid(status);
-    int len = 0, next = -1;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int size = cluster.num_blocks(), rank = cluster.block_rank();
+    const int n = blockIdx.x / size, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Tree t = read_tree(sh.tree, p.parent, p.cu, n, p.total_nodes, min(p.path_stride, kMaxNodes), false);
+    const bool writer = rank == 0 && tid == 0;
+    if (t.nodes < 0 && writer) report_invalid(p.status);
+    if (tid < t.nodes) {
+        unsigned long long mask = 0;
+        for (int j = tid + 1; j < t.nodes; ++j) mask |= (unsigned long long)(sh.tree.parent[j] == tid) << j;
+        sh.child[tid] = mask;
+    }
+    __syncthreads();
+    int len = 0, next = -1, turn = 0;
+    int owner = -1;  // the CTA that finds the next token in its part of the row; none: `next` is it
+    Row r{};
+    P part{};
+    const float *q = nullptr;
+    float C = 0.f;
+    int removed = 0;
+    unsigned long long at = 0;
     if (t.nodes > 0) {
-        const float temp = temperature ? temperature[n] : 1.f;
+        const float temp = p.temperature ? p.temperature[n] : 1.f;
+        r.onehot = !(temp > 0.f);
+        r.scale = r.onehot ? 0.f : 1.4426950408889634f / fmaxf(temp, 1e-30f);
         int node = 0;
         for (;;) {
-            if (tid == 0) path[(size_t)n * path_stride + len] = node;
+            if (writer) p.path[(size_t)n * p.path_stride + len] = node;
             ++len;
-            const Tin *row = logits + (size_t)(t.row0 + node) * V;
-            const float *q = probs ? probs + (size_t)(t.row0 + node) * V : nullptr;
-            // the largest logit and its lowest index
-            RowStats st;
-            st.top = -INFINITY;
-            st.best = -1;
-            for (int i = tid; i < V; i += kThreads) {
-                const float l = to_f32(row[i]);
-                if (l > st.top) { st.top = l; st.best = i; }
-            }
+            part.row = reinterpret_cast<const Tin *>(p.logits) + (size_t)(t.row0 + node) * p.V;
+            part.lead = (int)((reinterpret_cast<uintptr_t>(part.row) & 15u) / sizeof(Tin));
+            part.V = p.V;
+            part.kept = p.part_bytes ? kept : nullptr;
+            const int vectors = (part.lead + p.V + P::kVec - 1) / P::kVec, each = (vectors + size - 1) / size;
+            part.v0 = min(vectors, rank * each);
+            part.v1 = min(vectors, part.v0 + each);
+            q = p.probs ? p.probs + (size_t)(t.row0 + node) * p.V : nullptr;
+            C = 0.f;
+            removed = 0;
+            part.fetch();
+            const unsigned long long children = sh.child[node];
+            if (warp == 0)  // what the children's trials need
+                for (int j = lane; j < kMaxNodes; j += 32)
+                    if ((children >> j) & 1) {
+                        const int token = p.tokens[t.row0 + j], c = __popcll(children & ((1ull << j) - 1));
+                        const bool in = token >= 0 && token < p.V;
+                        sh.token[c] = in ? token : -1;
+                        sh.u[c] = p.u[t.row0 + j];
+                        sh.logit[c] = in ? to_f32(part.row[token]) : 0.f;
+                        sh.q[c] = q && in ? q[token] : 1.f;
+                    }
+            tc::cp_async_wait_all();
+            __syncthreads();
+            Found f{-INFINITY, -1};
+            for (int v = part.v0 + tid; v < part.v1; v += kThreads) {
+                float l[P::kVec];
+                part.get(v, l);
+                if (r.onehot) {
 #pragma unroll
-            for (int off = 16; off; off >>= 1) {
-                const float l = __shfl_xor_sync(0xffffffffu, st.top, off);
-                const int b = __shfl_xor_sync(0xffffffffu, st.best, off);
-                if (l > st.top || (l == st.top && b < st.best)) { st.top = l; st.best = b; }
-            }
-            __syncthreads();
-            if (lane == 0) { sh.top[warp] = st.top; sh.best[warp] = st.best; }
-            __syncthreads();
-            st.top = -INFINITY;
-            st.best = -1;
-            for (int w = 0; w < kWarps; ++w)
-                if (sh.top[w] > st.top || (sh.top[w] == st.top && sh.best[w] < st.best)) {
-                    st.top = sh.top[w];
-                    st.best = sh.best[w];
+                    for (int e = 0; e < P::kVec; ++e)
+                        if (l[e] > f.top) f = Found{l[e], v * P::kVec - part.lead + e};
+                } else {
+#pragma unroll
+                    for (int e = 0; e < P::kVec; ++e) f.top = fmaxf(f.top, l[e]);  // of NaN and a number, the number
                 }
-            st.onehot = !(temp > 0.f);
-            st.scale = st.onehot ? 0.f : 1.4426950408889634f / temp;
-            if (st.best < 0) break;  // no weight anywhere
-            unsigned long long part = 0;
-            for (int i = tid; i < V; i += kThreads) part += fixed40(weight_of(st, to_f32(row[i]), i));
-            const unsigned long long Z = block_sum(sh, part);
-            unsigned long long s = Z;
-            float C = 0.f;
-            int removed = 0, accepted = -1;
-            for (int j = node + 1; j < t.nodes && accepted < 0; ++j) {
-                if (sh.tree.parent[j] != node) continue;
-                const int token = tokens[t.row0 + j];
-                if (token < 0 || token >= V) {
-                    if (tid == 0) report_invalid(status);
+            }
+            if (!r.onehot && f.top > -INFINITY) f.best = 0;  // only `onehot` uses the place
+            f = cluster_max(sh, cluster, turn, size, f);
+            r.top = f.top;
+            r.best = f.best;
+            r.flat = f.top == INFINITY;
+            if (r.best < 0) break;  // no weight anywhere
+            unsigned long long Z = 1ull << 40;
+            if (!r.onehot) {
+                unsigned long long mine = 0;
+                for (int v = part.v0 + tid; v < part.v1;) {
+                    FixedSum sum;
+                    int count = 0;
+                    for (; v < part.v1 && count < kFlush; v += kThreads, count += P::kVec) {
+                        float l[P::kVec];
+                        part.get(v, l);
+#pragma unroll
+                        for (int e = 0; e < P::kVec; ++e) sum.add(weight_of(r, l[e]));
+                    }
+                    mine += sum.take(count);
+                }
+                Z = cluster_sum(sh, cluster, turn, size, mine, sh.sum_w);
+            }
+            unsigned long long s = Z, *sums = sh.sum_w;
+            const int trials = __popcll(children);
+            int accepted = -1;
+            for (int c = 0; c < trials && accepted < 0; ++c) {
+                const int token = sh.token[c];
+                if (token < 0) {
+                    if (writer) report_invalid(p.status);
                     continue;
                 }
-                const float r = rest_of(sh, st, row, q, C, removed, token);
-                const float sf = __ull2float_rn(s) * (1.f / kFixed), qc = q ? q[token] : 1.f;
-                if (__fmul_rn(__fmul_rn(u[t.row0 + j], qc), sf) < r) {
-                    accepted = j;
-                } else if (q) {
-                    C = __fadd_rn(C, sf);
-                    part = 0;
-                    for (int i = tid; i < V; i += kThreads) part += fixed40(rest_of(sh, st, row, q, C, 0, i));
-                    s = block_sum(sh, part);
-                } else {
-                    s -= fixed40(r);
+                const float w = r.onehot ? (token == r.best ? 1.f : 0.f)
+                                : r.flat ? weight_of(r, sh.logit[c])
+                                         : fmaxf(exp2f(__fmul_rn(__fsub_rn(sh.logit[c], r.top), r.scale)), 0.f);
+                const float sf = __ull2float_rn(s) * (1.f / kFixed), qc = sh.q[c];
+                float rest = w;
+                if (q && C > 0.f) rest = excess_of(w, C, qc);
+                for (int i = 0; i < removed; ++i) rest = sh.removed[i] == token ? 0.f : rest;
+                if (__fmul_rn(__fmul_rn(sh.u[c], qc), sf) < rest) {
+                    unsigned long long m = children;
+                    for (int i = 0; i < c; ++i) m &= m - 1;
+                    accepted = __ffsll((long long)m) - 1;
+                } else if (!q) {
+                    const unsigned long long cut = fixed40(rest);
+                    s -= cut;
                     __syncthreads();
-                    if (tid == 0) sh.removed[removed] = token;
+                    if (tid == 0) {
+                        sh.removed[removed] = token;
+                        sh.removed_w[removed] = cut;
+                    }
                     ++removed;
                     __syncthreads();
+                } else {
+                    C = __fadd_rn(C, sf);
+                    if (r.onehot) {
+                        s = fixed40(excess_of(1.f, C, q[r.best]));
+                    } else {
+                        unsigned long long mine = 0;
+                        for (int v = part.v0 + tid; v < part.v1;) {
+                            FixedSum sum;
+                            int count = 0;
+                            for (; v < part.v1 && count < kFlush; v += kThreads, count += P::kVec) {
+                                float l[P::kVec], x[P::kVec];
+                                part.get_q(q, v, x);
+                                part.get(v, l);
+#pragma unroll
+                                for (int e = 0; e < P::kVec; ++e) sum.add(excess_of(weight_of(r, l[e]), C, x[e]));
+                            }
+                            mine += sum.take(count);
+                        }
+                        s = cluster_sum(sh, cluster, turn, size, mine, sh.sum_r);
+                        sums = sh.sum_r;
+                    }
                 }
             }
             if (accepted >= 0) {
                 node = accepted;
+                __syncthreads();  // the row's part and the children's values are free
                 continue;
             }
             if (s == 0) {  // nothing is left of the target: its own distribution
                 s = Z;
                 C = 0.f;
                 removed = 0;
-                q = nullptr;
+                sums = sh.sum_w;
+            }
+            if (r.onehot) {  // all that is left is at one place, unless that was removed
+                next = r.best;
+                break;
             }
             // the next token: the first one whose cumulative sum is above u s
-            const double un = (double)u_next[n];
-            unsigned long long at = un > 0.0 ? (unsigned long long)(un * (double)s) : 0ull;
+            const double un = (double)p.u_next[n];
+            at = un > 0.0 ? (unsigned long long)(un * (double)s) : 0ull;
             if (at >= s) at = s - 1;
-            unsigned long long before = 0;
-            for (int i0 = 0; i0 < V && next < 0; i0 += kThreads * kVec) {
-                unsigned long long f[kVec], mine = 0;
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    const int i = i0 + tid * kVec + e;
-                    f[e] = i < V ? fixed40(rest_of(sh, st, row, q, C, removed, i)) : 0ull;
-                    mine += f[e];
-                }
-                unsigned long long upto = mine;
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const unsigned long long x = __shfl_up_sync(0xffffffffu, upto, off);
-                    if (lane >= off) upto += x;
-                }
-                __syncthreads();
-                if (lane == 31) sh.sum[warp] = upto;
-                if (tid == 0) sh.found = -1;
-                __syncthreads();
-                unsigned long long base = before + upto - mine;
-                for (int w = 0; w < kWarps; ++w) {
-                    if (w < warp) base += sh.sum[w];
-                    before += sh.sum[w];
-                }
-                if (base <= at && at < base + mine) {
-                    int e = 0;
-                    while (base + f[e] <= at) base += f[e++];
-                    sh.found = i0 + tid * kVec + e;
-                }
-                __syncthreads();
-                next = sh.found;
+            __syncthreads();  // sums[] is written
+            for (owner = 0; owner < size - 1; ++owner) {
+                unsigned long long here = sums[owner];
+                const int first = owner * each * P::kVec - part.lead, end = first + each * P::kVec;
+                for (int i = 0; i < removed; ++i)
+                    if (sh.removed[i] >= first && sh.removed[i] < end) here -= sh.removed_w[i];
+                if (at < here) break;
+                at -= here;
             }
             break;
         }
     }
-    for (int i = len + tid; i < path_stride; i += kThreads) path[(size_t)n * path_stride + i] = -1;
-    if (tid == 0) {
-        path_len[n] = len;
-        next_token[n] = next;
+    if (owner == rank) {
+        // 64 runs of 32 vectors at a time: their sums, then the run, the vector and the logit that pass `at`
+        auto rest = [&](int v, float (&x)[P::kVec]) {
+            float l[P::kVec];
+            part.get(v, l);
+            if (q && C > 0.f) {
+                float y[P::kVec];
+                part.get_q(q, v, y);
+#pragma unroll
+                for (int e = 0; e < P::kVec; ++e) x[e] = excess_of(weight_of(r, l[e]), C, y[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < P::kVec; ++e) {
+                    x[e] = weight_of(r, l[e]);
+                    for (int i = 0; i < removed; ++i)
+                        if (sh.removed[i] == v * P::kVec - part.lead + e) x[e] = 0.f;
+                }
+            }
+        };
+        bool search = true;
+        for (int v0 = part.v0; v0 < part.v1 && search; v0 += 64 * 32) {
+            for (int run = warp; run < 64; run += kWarps) {
+                const int v = v0 + run * 32 + lane;
+                FixedSum sum;
+                if (v < part.v1) {
+                    float x[P::kVec];
+                    rest(v, x);
+#pragma unroll
+                    for (int e = 0; e < P::kVec; ++e) sum.add(x[e]);
+                }
+                const unsigned long long total = warp_sum(v < part.v1 ? sum.take(P::kVec) : 0ull);
+                if (lane == 0) sh.part[run] = total;
+            }
+            __syncthreads();
+            int run = 0;
+            for (; run < 64 && at >= sh.part[run]; ++run) at -= sh.part[run];
+            if (run < 64) {
+                search = false;
+                if (warp == 0) {
+                    const int v = v0 + run * 32 + lane;
+                    float x[P::kVec];
+                    unsigned long long mine = 0;
+                    if (v < part.v1) {
+                        rest(v, x);
+                        FixedSum sum;
+#pragma unroll
+                        for (int e = 0; e < P::kVec; ++e) sum.add(x[e]);
+                        mine = sum.take(P::kVec);
+                    }
+                    unsigned long long upto = mine;
+#pragma unroll
+                    for (int off = 1; off < 32; off <<= 1) {
+                        const unsigned long long y = __shfl_up_sync(0xffffffffu, upto, off);
+                        if (lane >= off) upto += y;
+                    }
+                    if (upto - mine <= at && at < upto) {
+                        unsigned long long left = at - (upto - mine);
+                        int found = 0;
+#pragma unroll
+                        for (int e = P::kVec - 1; e >= 0; --e) {  // the last logit that starts at or below `left`
+                            unsigned long long start = 0;
+#pragma unroll
+                            for (int d = 0; d < P::kVec; ++d) start += d < e ? fixed40(x[d]) : 0ull;
+                            if (start <= left && left < start + fixed40(x[e])) found = e;
+                        }
+                        p.next_token[n] = v * P::kVec - part.lead + found;
+                    }
+                }
+            }
+            __syncthreads();
+        }
+    } else if (writer && owner < 0) {
+        p.next_token[n] = next;
     }
+    for (int i = len + tid; i < p.path_stride && rank == 0; i += kThreads) p.path[(size_t)n * p.path_stride + i] = -1;
+    if (writer) p.path_len[n] = len;
+    cluster.sync();  // no CTA leaves while another may still write to its shared memory
+}
+
+template <typename Tin>
+cudaError_t launch_t(Args p, int num_seqs, cudaStream_t st) {
+    constexpr int kVec = 16 / sizeof(Tin);
+    // CTAs per request: a row is split as long as a part has two vectors per thread; large batches fill the GPU
+    // with fewer.
+    int size = 1;
+    while (size < kMaxCluster && p.V >= 2 * size * kThreads * kVec) size *= 2;
+    const int vectors = (p.V + 2 * (kVec - 1)) / kVec, each = (vectors + size - 1) / size;
+    p.part_bytes = (uint32_t)each * 16 <= kMaxPart ? (uint32_t)each * 16 : 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)num_seqs * size);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = p.part_bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaFuncSetAttribute(draft_verify_kernel<Tin>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxPart);
+    if (e != cudaSuccess) return e;
+    return cudaLaunchKernelEx(&cfg, draft_verify_kernel<Tin>, (const Args)p);
 }
 
 }  // namespace
 
 cudaError_t launch_draft_verify(const DraftVerifyArgs &a, kda_dtype dt, cudaStream_t st) {
-    if (dt == KDA_BF16)
-        draft_verify_kernel<__nv_bfloat16><<<a.num_seqs, kThreads, 0, st>>>(
-            (const __nv_bfloat16 *)a.logits, a.probs, a.tokens, a.parent, a.cu, a.temperature, a.u, a.u_next,
-            a.total_nodes, a.V, a.path_stride, a.path, a.path_len, a.next_token, a.status);
-    else
-        draft_verify_kernel<float><<<a.num_seqs, kThreads, 0, st>>>(
-            (const float *)a.logits, a.probs, a.tokens, a.parent, a.cu, a.temperature, a.u, a.u_next, a.total_nodes,
-            a.V, a.path_stride, a.path, a.path_len, a.next_token, a.status);
-    return cudaGetLastError();
+    const Args p{a.logits, a.probs, a.tokens, a.parent, a.cu, a.temperature, a.u, a.u_next, a.total_nodes, a.V,
+                 a.path_stride, 0, a.path, a.path_len, a.next_token, a.status};
+    return dt == KDA_BF16 ? launch_t<__nv_bfloat16>(p, a.num_seqs, st) : launch_t<float>(p, a.num_seqs, st);
 }
 
 }  // namespace kda
