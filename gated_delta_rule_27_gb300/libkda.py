@@ -312,47 +312,49 @@ def kda_state_restore(S_saved, seq_idx, S_pool, status=None, stream=None) -> Non
         raise KdaError(rc, "kda_state_restore")
 
 
-def _i32(t, name: str):
-    if t is not None and t.dtype != torch.int32:
-        raise TypeError("libkda takes int32 %s, got %s" % (name, t.dtype))
-    return _ptr(t)
+def _arg(t, dtype, shape, name: str):
+    """The address of a contiguous device tensor of this dtype and shape (None passes as null)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError("%s is %s, libkda takes %s here" % (name, t.dtype, dtype))
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
+    if not t.is_cuda:
+        raise ValueError("libkda takes device tensors; %s is on %s" % (name, t.device))
+    if not t.is_contiguous():
+        raise ValueError("libkda takes contiguous tensors; %s is not" % name)
+    return t.data_ptr()
 
 
-def _f32(t, name: str):
-    if t is not None and t.dtype != torch.float32:
-        raise TypeError("libkda takes fp32 %s, got %s" % (name, t.dtype))
-    return _ptr(t)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _shape(t, shape, name: str) -> None:
-    if t is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-
-
-def _like(t, ref, name: str):
-    if t.dtype != ref.dtype:
-        raise TypeError("%s is %s, expected %s" % (name, t.dtype, ref.dtype))
-    return _ptr(t)
+def _stream_of(stream, t):
+    """The given stream, or the current one of the tensor's device, as an address."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(t.get_device()) if _raw_stream else torch.cuda.current_stream(t.device).cuda_stream
 
 
 def kda_tree_step(q, k, v, g, beta, parent, cu_nodes, seq_idx, S_pool, o, u, max_nodes, status=None, stream=None,
                   **fusion) -> None:
     """KDA attention of every draft-tree node over the state pool (kda_tree_step): q, k, v, g [T, H, d] and beta
     [T, H] packed as include/kda.h says, o and u (or None) written; keywords of fusion_opts."""
-    T, H, d_k = q.shape
-    N = cu_nodes.numel() - 1
-    for t, name in ((k, "k"), (v, "v"), (g, "g"), (o, "o"), (u, "u"), (fusion.get("out_gate"), "out_gate")):
-        _shape(t, (T, H, d_k), name)
-    _shape(beta, (T, H), "beta")
-    _shape(parent, (T,), "parent")
-    _shape(seq_idx, (N,), "seq_idx")
-    _shape(S_pool, (S_pool.shape[0], H, d_k, d_k), "S_pool")
-    opts = fusion_opts(**fusion)
-    rc = load().kda_tree_step(_ptr(q), _like(k, q, "k"), _like(v, q, "v"), _f32(g, "g"), _f32(beta, "beta"),
-                              _i32(parent, "parent"), _i32(cu_nodes, "cu_nodes"), _i32(seq_idx, "seq_idx"), N, T,
-                              max_nodes, S_pool.shape[0], H, d_k, d_k, _dtype_code(q), _f32(S_pool, "S_pool"),
-                              _like(o, q, "o"), _f32(u, "u"), _i32(status, "status"), _stream(stream),
-                              None if opts is None else ctypes.byref(opts))
+    dt, rows, i32, f32 = q.dtype, q.shape, torch.int32, torch.float32
+    T, H, d = rows
+    N, slots = cu_nodes.shape[0] - 1, S_pool.shape[0]
+    opts = None
+    if fusion:
+        _arg(fusion.get("out_gate"), dt, rows, "out_gate")
+        _arg(fusion.get("out_weight"), f32, (d,), "out_weight")
+        opts = fusion_opts(**fusion)
+    rc = load().kda_tree_step(_arg(q, dt, rows, "q"), _arg(k, dt, rows, "k"), _arg(v, dt, rows, "v"),
+                              _arg(g, f32, rows, "g"), _arg(beta, f32, (T, H), "beta"),
+                              _arg(parent, i32, (T,), "parent"), _arg(cu_nodes, i32, (N + 1,), "cu_nodes"),
+                              _arg(seq_idx, i32, (N,), "seq_idx"), N, T, max_nodes, slots, H, d, d, _dtype_code(q),
+                              _arg(S_pool, f32, (slots, H, d, d), "S_pool"), _arg(o, dt, rows, "o"),
+                              _arg(u, f32, rows, "u"), _arg(status, i32, (1,), "status"), _stream_of(stream, q), opts)
     if rc != KDA_OK:
         raise KdaError(rc, "kda_tree_step")
 
@@ -360,19 +362,15 @@ def kda_tree_step(q, k, v, g, beta, parent, cu_nodes, seq_idx, S_pool, o, u, max
 def kda_tree_commit(k, g, u, cu_nodes, path, path_len, seq_idx, S_pool, status=None, stream=None, qk_l2norm=False,
                     qk_eps=1e-6) -> None:
     """Moves the pool's states along the accepted paths (kda_tree_commit), in place."""
-    T, H, d_k = k.shape
-    N = cu_nodes.numel() - 1
-    _shape(g, (T, H, d_k), "g")
-    _shape(u, (T, H, d_k), "u")
-    _shape(path, (N, path.shape[1]), "path")
-    _shape(path_len, (N,), "path_len")
-    _shape(seq_idx, (N,), "seq_idx")
-    _shape(S_pool, (S_pool.shape[0], H, d_k, d_k), "S_pool")
-    opts = fusion_opts(qk_l2norm=qk_l2norm, qk_eps=qk_eps)
-    rc = load().kda_tree_commit(_ptr(k), _f32(g, "g"), _f32(u, "u"), _i32(cu_nodes, "cu_nodes"), _i32(path, "path"),
-                                _i32(path_len, "path_len"), _i32(seq_idx, "seq_idx"), N, T, path.shape[1],
-                                S_pool.shape[0], H, d_k, d_k, _dtype_code(k), _f32(S_pool, "S_pool"),
-                                _i32(status, "status"), _stream(stream), None if opts is None else ctypes.byref(opts))
+    rows, i32, f32 = k.shape, torch.int32, torch.float32
+    T, H, d = rows
+    N, slots, width = cu_nodes.shape[0] - 1, S_pool.shape[0], path.shape[1]
+    opts = fusion_opts(qk_l2norm=True, qk_eps=qk_eps) if qk_l2norm else None
+    rc = load().kda_tree_commit(_arg(k, k.dtype, rows, "k"), _arg(g, f32, rows, "g"), _arg(u, f32, rows, "u"),
+                                _arg(cu_nodes, i32, (N + 1,), "cu_nodes"), _arg(path, i32, (N, width), "path"),
+                                _arg(path_len, i32, (N,), "path_len"), _arg(seq_idx, i32, (N,), "seq_idx"), N, T,
+                                width, slots, H, d, d, _dtype_code(k), _arg(S_pool, f32, (slots, H, d, d), "S_pool"),
+                                _arg(status, i32, (1,), "status"), _stream_of(stream, k), opts)
     if rc != KDA_OK:
         raise KdaError(rc, "kda_tree_commit")
 
@@ -380,34 +378,29 @@ def kda_tree_commit(k, g, u, cu_nodes, path, path_len, seq_idx, S_pool, status=N
 def kda_tree_conv(x, w, parent, cu_nodes, seq_idx, conv_pool, y, max_nodes, status=None, stream=None) -> None:
     """The short convolution along every node's path (kda_tree_conv): x, y [T, C], w [C, W], conv_pool
     [slots, W - 1, C] (read only)."""
-    T = x.shape[0]
-    C, W = w.shape
-    N = cu_nodes.numel() - 1
-    _shape(x, (T, C), "x")
-    _shape(y, (T, C), "y")
-    _shape(parent, (T,), "parent")
-    _shape(seq_idx, (N,), "seq_idx")
-    _shape(conv_pool, (conv_pool.shape[0], W - 1, C), "conv_pool")
-    rc = load().kda_tree_conv(_ptr(x), _f32(w, "w"), _i32(parent, "parent"), _i32(cu_nodes, "cu_nodes"),
-                              _i32(seq_idx, "seq_idx"), N, T, max_nodes, conv_pool.shape[0], C, W, _dtype_code(x),
-                              _f32(conv_pool, "conv_pool"), _like(y, x, "y"), _i32(status, "status"),
-                              _stream(stream))
+    dt, rows, i32, f32 = x.dtype, x.shape, torch.int32, torch.float32
+    T, C = rows
+    N, slots, W = cu_nodes.shape[0] - 1, conv_pool.shape[0], w.shape[1]
+    rc = load().kda_tree_conv(_arg(x, dt, rows, "x"), _arg(w, f32, (C, W), "w"), _arg(parent, i32, (T,), "parent"),
+                              _arg(cu_nodes, i32, (N + 1,), "cu_nodes"), _arg(seq_idx, i32, (N,), "seq_idx"), N, T,
+                              max_nodes, slots, C, W, _dtype_code(x),
+                              _arg(conv_pool, f32, (slots, W - 1, C), "conv_pool"), _arg(y, dt, rows, "y"),
+                              _arg(status, i32, (1,), "status"), _stream_of(stream, x))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_tree_conv")
 
 
 def kda_tree_conv_commit(x, cu_nodes, path, path_len, seq_idx, conv_pool, status=None, stream=None) -> None:
     """Moves the carried convolution inputs along the accepted paths (kda_tree_conv_commit), in place."""
+    i32 = torch.int32
     T, C = x.shape
-    N = cu_nodes.numel() - 1
-    _shape(path, (N, path.shape[1]), "path")
-    _shape(path_len, (N,), "path_len")
-    _shape(seq_idx, (N,), "seq_idx")
-    _shape(conv_pool, (conv_pool.shape[0], conv_pool.shape[1], C), "conv_pool")
-    rc = load().kda_tree_conv_commit(_ptr(x), _i32(cu_nodes, "cu_nodes"), _i32(path, "path"),
-                                     _i32(path_len, "path_len"), _i32(seq_idx, "seq_idx"), N, T, path.shape[1],
-                                     conv_pool.shape[0], C, conv_pool.shape[1] + 1, _dtype_code(x),
-                                     _f32(conv_pool, "conv_pool"), _i32(status, "status"), _stream(stream))
+    N, width = cu_nodes.shape[0] - 1, path.shape[1]
+    slots, carried, _ = conv_pool.shape
+    rc = load().kda_tree_conv_commit(_arg(x, x.dtype, (T, C), "x"), _arg(cu_nodes, i32, (N + 1,), "cu_nodes"),
+                                     _arg(path, i32, (N, width), "path"), _arg(path_len, i32, (N,), "path_len"),
+                                     _arg(seq_idx, i32, (N,), "seq_idx"), N, T, width, slots, C, carried + 1,
+                                     _dtype_code(x), _arg(conv_pool, torch.float32, (slots, carried, C), "conv_pool"),
+                                     _arg(status, i32, (1,), "status"), _stream_of(stream, x))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_tree_conv_commit")
 
@@ -416,20 +409,16 @@ def kda_draft_verify(logits, tokens, parent, cu_nodes, u_accept, u_next, path, p
                      temperature=None, status=None, stream=None) -> None:
     """Verifies drafted tokens against the target's logits [T, V] (kda_draft_verify): writes the kept paths
     [N, max nodes], their lengths and the next tokens."""
-    T, V = logits.shape
-    N = cu_nodes.numel() - 1
-    for t, name in ((tokens, "tokens"), (parent, "parent"), (u_accept, "u_accept")):
-        _shape(t, (T,), name)
-    for t, name in ((u_next, "u_next"), (path_len, "path_len"), (next_token, "next_token"),
-                    (temperature, "temperature")):
-        _shape(t, (N,), name)
-    _shape(draft_probs, (T, V), "draft_probs")
-    _shape(path, (N, path.shape[1]), "path")
-    rc = load().kda_draft_verify(_ptr(logits), _f32(draft_probs, "draft_probs"), _i32(tokens, "tokens"),
-                                 _i32(parent, "parent"), _i32(cu_nodes, "cu_nodes"), _f32(temperature, "temperature"),
-                                 _f32(u_accept, "u_accept"), _f32(u_next, "u_next"), N, T, V, _dtype_code(logits),
-                                 path.shape[1], _i32(path, "path"), _i32(path_len, "path_len"),
-                                 _i32(next_token, "next_token"), _i32(status, "status"), _stream(stream))
+    rows, i32, f32 = logits.shape, torch.int32, torch.float32
+    T, V = rows
+    N, width = cu_nodes.shape[0] - 1, path.shape[1]
+    rc = load().kda_draft_verify(_arg(logits, logits.dtype, rows, "logits"), _arg(draft_probs, f32, rows, "draft_probs"),
+                                 _arg(tokens, i32, (T,), "tokens"), _arg(parent, i32, (T,), "parent"),
+                                 _arg(cu_nodes, i32, (N + 1,), "cu_nodes"), _arg(temperature, f32, (N,), "temperature"),
+                                 _arg(u_accept, f32, (T,), "u_accept"), _arg(u_next, f32, (N,), "u_next"), N, T, V,
+                                 _dtype_code(logits), width, _arg(path, i32, (N, width), "path"),
+                                 _arg(path_len, i32, (N,), "path_len"), _arg(next_token, i32, (N,), "next_token"),
+                                 _arg(status, i32, (1,), "status"), _stream_of(stream, logits))
     if rc != KDA_OK:
         raise KdaError(rc, "kda_draft_verify")
 
