@@ -12,6 +12,7 @@
 //
 // and the state after the path that ends in node l is  e^{b_l} S + sum_a (k_a e^{b_l - b_a}) u_a^T, so the
 // commit needs the stored u and no second recurrence: it is one pass over the state.
+#include "kda_tc.cuh"
 #include "kda_tree.cuh"
 
 namespace kda {
@@ -188,33 +189,30 @@ cudaError_t launch_step_t(const TreeStepArgs &a, cudaStream_t st) {
 // Commit
 // ---------------------------------------------------------------------------
 // One CTA per (request, head), laid out like the decode step: each thread holds 16 rows by four columns of the
-// state in registers, loaded before anything else.  The path is taken kChunk nodes at a time: with the decay
-// to the chunk's end folded into its keys, a chunk is  S <- e^{b} S + sum_a (k_a e^{b - b_a}) u_a^T.
+// state in registers.  The state's loads are issued before anything else that takes time, and the path's rows of
+// k, g and u follow as asynchronous copies, so one wait covers both.  The path is taken kChunk nodes at a time:
+// with the decay to the chunk's end folded into its keys, a chunk is  S <- e^{b} S + sum_a (k_a e^{b - b_a}) u_a^T.
+// Bound by HBM: the state once each way.
 constexpr int kRows = 16, kChunk = 8;
 
 template <typename Tin, int D>
-__global__ void __launch_bounds__((D / 4) * (D / kRows))
+__global__ void __launch_bounds__((D / 4) * (D / kRows), D == 128 ? 3 : 1)
 tree_commit_kernel(const Tin *__restrict__ k, const float *__restrict__ g, const float *__restrict__ u,
                    const int32_t *__restrict__ cu, const int32_t *__restrict__ path,
                    const int32_t *__restrict__ path_len, const int32_t *__restrict__ seq_idx, int H, int total_nodes,
                    int path_stride, int num_slots, float *__restrict__ S_pool, int32_t *__restrict__ status,
                    int qk_norm, float qk_eps) {
     constexpr int CG = D / 4, NT = CG * (D / kRows);
-    __shared__ float s_k[kChunk][D], s_dec[D];
-    __shared__ __align__(16) float s_u[kChunk][D];
+    constexpr int KV = D * (int)sizeof(Tin) / 16, FV = D / 4;  // 16-byte vectors of a row of k; of g or u
+    __shared__ __align__(16) float s_k[kChunk][D], s_u[kChunk][D], s_g[kChunk][D];
+    __shared__ __align__(16) float s_dec[D];
+    __shared__ __align__(16) Tin s_raw[kChunk][D];
     __shared__ float s_scale[kChunk];
-    __shared__ int s_row[kChunk];
     const int n = blockIdx.x / H, h = blockIdx.x % H, tid = threadIdx.x;
-    const int len = path_len[n];
-    if (len == 0) return;
+    const int len = path_len[n], slot = slot_of(seq_idx, n, num_slots);
     const Tree t = tree_rows(cu, n, total_nodes, kMaxNodes);
-    const int slot = slot_of(seq_idx, n, num_slots);
-    int bad = t.nodes < 0 || slot < 0 || len < 0 || len > path_stride || len > t.nodes;
-    for (int i = tid; i < len && !bad; i += NT) {
-        const int node = path[(size_t)n * path_stride + i];
-        bad = node < 0 || node >= t.nodes;
-    }
-    if (__syncthreads_or(bad)) {
+    if (len == 0) return;
+    if (t.nodes < 0 || slot < 0 || len < 0 || len > path_stride || len > t.nodes) {
         if (tid == 0) report_invalid(status);
         return;
     }
@@ -224,25 +222,36 @@ tree_commit_kernel(const Tin *__restrict__ k, const float *__restrict__ g, const
 #pragma unroll
     for (int j = 0; j < kRows; ++j) s[j] = __ldcs(&Sv[(size_t)(rg * kRows + j) * CG + cg]);
 
+    const int32_t *nodes = path + (size_t)n * path_stride;
     for (int l0 = 0; l0 < len; l0 += kChunk) {
         const int L = min(kChunk, len - l0);
-        __syncthreads();
-        for (int i = tid; i < L; i += NT)  // (d = 16 runs four threads, fewer than a chunk has nodes)
-            s_row[i] = t.row0 + path[(size_t)n * path_stride + l0 + i];
-        __syncthreads();
-        for (int i = tid; i < L * D; i += NT) {
-            const size_t at = ((size_t)s_row[i / D] * H + h) * D + i % D;
-            s_k[i / D][i % D] = to_f32(k[at]);
-            s_u[i / D][i % D] = u[at];
+        int bad = 0;
+        for (int i = tid; i < L * (KV + 2 * FV); i += NT) {
+            const int r = i / (KV + 2 * FV), e = i % (KV + 2 * FV);
+            const int node = nodes[l0 + r];
+            if (node < 0 || node >= t.nodes) {
+                bad = 1;
+                continue;
+            }
+            const size_t at = ((size_t)(t.row0 + node) * H + h) * D;
+            if (e < KV) tc::cp_async16(reinterpret_cast<char *>(s_raw[r]) + e * 16, reinterpret_cast<const char *>(k + at) + e * 16);
+            else if (e < KV + FV) tc::cp_async16(&s_g[r][(e - KV) * 4], g + at + (e - KV) * 4);
+            else tc::cp_async16(&s_u[r][(e - KV - FV) * 4], u + at + (e - KV - FV) * 4);
         }
-        __syncthreads();
+        if (l0 == 0)  // the whole path is checked before anything is written
+            for (int i = kChunk + tid; i < len; i += NT) bad |= nodes[i] < 0 || nodes[i] >= t.nodes;
+        tc::cp_async_wait_all();
+        if (__syncthreads_or(bad)) {
+            if (tid == 0) report_invalid(status);
+            return;
+        }
         if (qk_norm) {  // a group of min(NT, 32) threads per row
             constexpr int G = NT < 32 ? NT : 32;
             const int lane = tid % G;
             for (int r = tid / G; r < kChunk; r += NT / G) {
                 float ss = 0.f;
                 if (r < L)
-                    for (int c = lane; c < D; c += G) ss = fmaf(s_k[r][c], s_k[r][c], ss);
+                    for (int c = lane; c < D; c += G) ss = fmaf(to_f32(s_raw[r][c]), to_f32(s_raw[r][c]), ss);
 #pragma unroll
                 for (int off = G / 2; off; off >>= 1)
                     ss += __shfl_xor_sync(G == 32 ? 0xffffffffu : (1u << G) - 1u, ss, off);
@@ -253,26 +262,36 @@ tree_commit_kernel(const Tin *__restrict__ k, const float *__restrict__ g, const
         for (int c = tid; c < D; c += NT) {  // decays to the chunk's end, per channel
             float b = 0.f;
             for (int r = L - 1; r >= 0; --r) {
-                s_k[r][c] *= expf(b) * (qk_norm ? s_scale[r] : 1.f);
-                b += log_decay(g[((size_t)s_row[r] * H + h) * D + c]);
+                s_k[r][c] = to_f32(s_raw[r][c]) * (expf(b) * (qk_norm ? s_scale[r] : 1.f));
+                b += log_decay(s_g[r][c]);
             }
             s_dec[c] = expf(b);
         }
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kRows; ++j) {
-            const float d = s_dec[rg * kRows + j];
-            s[j].x *= d; s[j].y *= d; s[j].z *= d; s[j].w *= d;
+        for (int j0 = 0; j0 < kRows; j0 += 4) {
+            const float4 d4 = *reinterpret_cast<const float4 *>(&s_dec[rg * kRows + j0]);
+            const float d[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[j0 + e].x *= d[e]; s[j0 + e].y *= d[e]; s[j0 + e].z *= d[e]; s[j0 + e].w *= d[e];
+            }
         }
         for (int r = 0; r < L; ++r) {
             const float4 w = *reinterpret_cast<const float4 *>(&s_u[r][cg * 4]);
 #pragma unroll
-            for (int j = 0; j < kRows; ++j) {
-                const float kr = s_k[r][rg * kRows + j];
-                s[j].x = fmaf(kr, w.x, s[j].x); s[j].y = fmaf(kr, w.y, s[j].y);
-                s[j].z = fmaf(kr, w.z, s[j].z); s[j].w = fmaf(kr, w.w, s[j].w);
+            for (int j0 = 0; j0 < kRows; j0 += 4) {
+                const float4 k4 = *reinterpret_cast<const float4 *>(&s_k[r][rg * kRows + j0]);
+                const float kr[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float4 &x = s[j0 + e];
+                    x.x = fmaf(kr[e], w.x, x.x); x.y = fmaf(kr[e], w.y, x.y);
+                    x.z = fmaf(kr[e], w.z, x.z); x.w = fmaf(kr[e], w.w, x.w);
+                }
             }
         }
+        if (l0 + kChunk < len) __syncthreads();  // the chunk's rows are free
     }
 #pragma unroll
     for (int j = 0; j < kRows; ++j) __stcs(&Sv[(size_t)(rg * kRows + j) * CG + cg], s[j]);
@@ -300,68 +319,139 @@ cudaError_t launch_commit_t(const TreeCommitArgs &a, cudaStream_t st) {
 // Short convolution along the paths
 // ---------------------------------------------------------------------------
 // y_i[c] = sum_j w[c, j] x_{j-th ancestor of i}[c]; past the root the request's carried inputs follow, newest
-// first.  One CTA per (request, 128 channels).
-constexpr int kConvThreads = 128;
+// first.  One CTA per (request, channel block); a thread owns VEC neighbouring channels, whose rows it reads as
+// 16 bytes (VEC = 8 of bf16, 4 of fp32; VEC = 1 where C or an address does not allow that).  A row is read once
+// from HBM and again, for the nodes below it, from L1.
+constexpr int kConvThreads = 64;
 
-template <typename Tin, int W>
+template <typename Tin, int VEC>
+__device__ __forceinline__ void load_row(const Tin *p, float (&f)[VEC]) {
+    if constexpr (VEC == 1) {
+        f[0] = to_f32(*p);
+    } else {
+        union {
+            uint4 v;
+            Tin x[VEC];
+        } r;
+        r.v = __ldg(reinterpret_cast<const uint4 *>(p));
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f[e] = to_f32(r.x[e]);
+    }
+}
+template <typename Tin, int VEC>
+__device__ __forceinline__ void store_row(Tin *p, const float (&f)[VEC]) {
+    if constexpr (VEC == 1) {
+        *p = from_f32<Tin>(f[0]);
+    } else {
+        union {
+            uint4 v;
+            Tin x[VEC];
+        } r;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) r.x[e] = from_f32<Tin>(f[e]);
+        *reinterpret_cast<uint4 *>(p) = r.v;
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void load_f32(const float *p, float (&f)[VEC]) {
+    if constexpr (VEC == 1) {
+        f[0] = *p;
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(p + e);
+            f[e] = v.x; f[e + 1] = v.y; f[e + 2] = v.z; f[e + 3] = v.w;
+        }
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void store_f32(float *p, const float (&f)[VEC]) {
+    if constexpr (VEC == 1) {
+        *p = f[0];
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4)
+            *reinterpret_cast<float4 *>(p + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+    }
+}
+
+template <typename Tin, int W, int VEC>
 __global__ void __launch_bounds__(kConvThreads)
 tree_conv_kernel(const Tin *__restrict__ x, const float *__restrict__ w, const int32_t *__restrict__ parent,
                  const int32_t *__restrict__ cu, const int32_t *__restrict__ seq_idx, int total_nodes, int max_nodes,
                  int num_slots, int C, const float *__restrict__ pool, Tin *__restrict__ y,
                  int32_t *__restrict__ status) {
     __shared__ TreeShared ts;
-    const int n = blockIdx.y, c = blockIdx.x * kConvThreads + threadIdx.x;
-    const Tree t = read_tree(ts, parent, cu, n, total_nodes, max_nodes, false);
+    __shared__ int s_tap[kMaxNodes][W];  // the j-th input before node i: a node, or -1 - m for the m-th carried one
+    const int n = blockIdx.y, tid = threadIdx.x, c = (blockIdx.x * kConvThreads + tid) * VEC;
     const int slot = slot_of(seq_idx, n, num_slots);
+    float wt[W][VEC];
+    if (c < C) {
+        float all[W * VEC];
+        if constexpr (VEC == 1) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) all[j] = w[(size_t)c * W + j];
+        } else {
+            load_f32<W * VEC>(w + (size_t)c * W, all);
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) wt[j][e] = all[e * W + j];
+    }
+    const Tree t = read_tree(ts, parent, cu, n, total_nodes, max_nodes, false);
     if (t.nodes < 0 || slot < 0) {
-        if (threadIdx.x == 0) report_invalid(status);
+        if (tid == 0) report_invalid(status);
         return;
     }
-    if (c >= C) return;
-    float wt[W], past[W];  // past[j]: the j-th input before the root
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-        wt[j] = w[(size_t)c * W + j];
-        past[j] = j < W - 1 ? pool[((size_t)slot * (W - 1) + (W - 2 - j)) * C + c] : 0.f;
-    }
-    for (int i = 0; i < t.nodes; ++i) {
-        float acc = 0.f;
-        int at = i, carried = 0;
+    for (int i = tid; i < t.nodes; i += kConvThreads) {
+        int at = i, m = 0;
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-            float xv = 0.f;
-            if (at >= 0) {
-                xv = to_f32(x[(size_t)(t.row0 + at) * C + c]);
-                at = ts.parent[at];
-            } else {
-#pragma unroll
-                for (int m = 0; m < W; ++m) xv = m == carried ? past[m] : xv;
-                ++carried;
-            }
-            acc = fmaf(wt[j], xv, acc);
+            s_tap[i][j] = at >= 0 ? at : -1 - m++;
+            at = at >= 0 ? ts.parent[at] : -1;
         }
-        y[(size_t)(t.row0 + i) * C + c] = from_f32<Tin>(acc);
+    }
+    __syncthreads();
+    if (c >= C) return;
+    const Tin *xs = x + (size_t)t.row0 * C + c;
+    const float *past = pool + ((ptrdiff_t)slot * (W - 1) + (W - 2)) * C + c;  // the newest carried input (W > 1)
+#pragma unroll 4
+    for (int i = 0; i < t.nodes; ++i) {
+        float acc[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            const int tap = s_tap[i][j];
+            float v[VEC];
+            if (tap >= 0) load_row<Tin, VEC>(xs + (size_t)tap * C, v);
+            else load_f32<VEC>(past - (ptrdiff_t)(-1 - tap) * C, v);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) acc[e] = fmaf(wt[j][e], v[e], acc[e]);
+        }
+        store_row<Tin, VEC>(y + (size_t)(t.row0 + i) * C + c, acc);
     }
 }
 
 // The carried inputs after a path: the last W - 1 of [carried inputs, the path's inputs].
-template <typename Tin>
+template <typename Tin, int VEC>
 __global__ void __launch_bounds__(kConvThreads)
 tree_conv_commit_kernel(const Tin *__restrict__ x, const int32_t *__restrict__ cu, const int32_t *__restrict__ path,
                         const int32_t *__restrict__ path_len, const int32_t *__restrict__ seq_idx, int total_nodes,
                         int path_stride, int num_slots, int C, int W, float *__restrict__ pool,
                         int32_t *__restrict__ status) {
-    const int n = blockIdx.y, c = blockIdx.x * kConvThreads + threadIdx.x;
-    const int len = path_len[n];
-    if (len == 0) return;
+    const int n = blockIdx.y, c = (blockIdx.x * kConvThreads + threadIdx.x) * VEC;
+    const int len = path_len[n], slot = slot_of(seq_idx, n, num_slots);
     const Tree t = tree_rows(cu, n, total_nodes, kMaxNodes);
-    const int slot = slot_of(seq_idx, n, num_slots);
+    if (len == 0) return;
     bool bad = t.nodes < 0 || slot < 0 || len < 0 || len > path_stride || len > t.nodes;
     int node[KDA_SHORT_CONV_MAX_W - 1];  // node of the new carried input j, or -1 for an old one
-    for (int j = 0; j < W - 1 && !bad; ++j) {
+#pragma unroll
+    for (int j = 0; j < KDA_SHORT_CONV_MAX_W - 1; ++j) {
         const int l = len - (W - 1) + j;
         node[j] = -1;
-        if (l >= 0) {
+        if (j < W - 1 && l >= 0 && !bad) {
             node[j] = path[(size_t)n * path_stride + l];
             bad = node[j] < 0 || node[j] >= t.nodes;
         }
@@ -371,21 +461,36 @@ tree_conv_commit_kernel(const Tin *__restrict__ x, const int32_t *__restrict__ c
         return;
     }
     if (c >= C) return;
-    float next[KDA_SHORT_CONV_MAX_W - 1];
-    for (int j = 0; j < W - 1; ++j)
-        next[j] = node[j] >= 0 ? to_f32(x[(size_t)(t.row0 + node[j]) * C + c])
-                               : pool[((size_t)slot * (W - 1) + j + len) * C + c];
-    for (int j = 0; j < W - 1; ++j) pool[((size_t)slot * (W - 1) + j) * C + c] = next[j];
+    float next[KDA_SHORT_CONV_MAX_W - 1][VEC];
+    float *mine = pool + (size_t)slot * (W - 1) * C + c;
+#pragma unroll
+    for (int j = 0; j < KDA_SHORT_CONV_MAX_W - 1; ++j) {
+        if (j < W - 1) {
+            if (node[j] >= 0) load_row<Tin, VEC>(x + (size_t)(t.row0 + node[j]) * C + c, next[j]);
+            else load_f32<VEC>(mine + (size_t)(j + len) * C, next[j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < KDA_SHORT_CONV_MAX_W - 1; ++j)
+        if (j < W - 1) store_f32<VEC>(mine + (size_t)j * C, next[j]);
 }
 
+// Whether rows of C elements and their fp32 counterparts can be taken 16 bytes at a time.
 template <typename Tin>
-cudaError_t launch_conv_t(const TreeConvArgs &a, cudaStream_t st) {
-    const dim3 grid((a.C + kConvThreads - 1) / kConvThreads, a.num_seqs);
+bool rows_of_vectors(int C, const void *a, const void *b, const void *c, const void *d) {
+    const uintptr_t any = (uintptr_t)a | (uintptr_t)b | (uintptr_t)c | (uintptr_t)d;
+    return C % (16 / (int)sizeof(Tin)) == 0 && (any & 15u) == 0;
+}
+
+template <typename Tin, int VEC>
+cudaError_t launch_conv_v(const TreeConvArgs &a, cudaStream_t st) {
+    const dim3 grid((a.C + kConvThreads * VEC - 1) / (kConvThreads * VEC), a.num_seqs);
 #define KDA_TREE_CONV(WW)                                                                                          \
     case WW:                                                                                                       \
-        tree_conv_kernel<Tin, WW><<<grid, kConvThreads, 0, st>>>((const Tin *)a.x, a.w, a.parent, a.cu, a.seq_idx, \
-                                                                 a.total_nodes, a.max_nodes, a.num_slots, a.C,     \
-                                                                 a.pool, (Tin *)a.y, a.status);                    \
+        tree_conv_kernel<Tin, WW, VEC><<<grid, kConvThreads, 0, st>>>((const Tin *)a.x, a.w, a.parent, a.cu,       \
+                                                                      a.seq_idx, a.total_nodes, a.max_nodes,       \
+                                                                      a.num_slots, a.C, a.pool, (Tin *)a.y,        \
+                                                                      a.status);                                   \
         break;
     switch (a.W) {
         KDA_TREE_CONV(1) KDA_TREE_CONV(2) KDA_TREE_CONV(3) KDA_TREE_CONV(4)
@@ -396,13 +501,25 @@ cudaError_t launch_conv_t(const TreeConvArgs &a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
+template <typename Tin, int VEC>
+cudaError_t launch_conv_commit_v(const TreeConvCommitArgs &a, cudaStream_t st) {
+    const dim3 grid((a.C + kConvThreads * VEC - 1) / (kConvThreads * VEC), a.num_seqs);
+    tree_conv_commit_kernel<Tin, VEC><<<grid, kConvThreads, 0, st>>>((const Tin *)a.x, a.cu, a.path, a.path_len,
+                                                                     a.seq_idx, a.total_nodes, a.path_stride,
+                                                                     a.num_slots, a.C, a.W, a.pool, a.status);
+    return cudaGetLastError();
+}
+
+template <typename Tin>
+cudaError_t launch_conv_t(const TreeConvArgs &a, cudaStream_t st) {
+    constexpr int VEC = 16 / (int)sizeof(Tin);
+    return rows_of_vectors<Tin>(a.C, a.x, a.y, a.pool, a.w) ? launch_conv_v<Tin, VEC>(a, st) : launch_conv_v<Tin, 1>(a, st);
+}
 template <typename Tin>
 cudaError_t launch_conv_commit_t(const TreeConvCommitArgs &a, cudaStream_t st) {
-    const dim3 grid((a.C + kConvThreads - 1) / kConvThreads, a.num_seqs);
-    tree_conv_commit_kernel<Tin><<<grid, kConvThreads, 0, st>>>((const Tin *)a.x, a.cu, a.path, a.path_len, a.seq_idx,
-                                                                a.total_nodes, a.path_stride, a.num_slots, a.C, a.W,
-                                                                a.pool, a.status);
-    return cudaGetLastError();
+    constexpr int VEC = 16 / (int)sizeof(Tin);
+    return rows_of_vectors<Tin>(a.C, a.x, a.pool, nullptr, nullptr) ? launch_conv_commit_v<Tin, VEC>(a, st)
+                                                                    : launch_conv_commit_v<Tin, 1>(a, st);
 }
 
 }  // namespace
