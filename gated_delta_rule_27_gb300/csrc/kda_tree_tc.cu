@@ -4,31 +4,36 @@
 // recurrence), one CTA per (request, head) forms, for a tree of at most MP nodes,
 //     D1 = [K~ ; Q~] K^^T      A and P: masked to the paths, A scaled by beta
 //     D2 = S^T [K~ ; Q~]^T     x and y: the pool's state, 128 columns, times every node's decayed key and query
-//     r  = beta (v - x),  T = (I + A)^{-1}
-//     D3 = r^T (T - I)^T       u = r + D3
-//     D4 = u^T P^T             o = y + D4
+//     r  = beta (v - x),  T = (I + A)^{-1},  G = P T
+//     D3 = r^T [T - I ; G]^T   u = r + D3,  o = y + D3     (MP = 64: u first, then o = y + u^T P^T as D4)
 // so the state is read once, whatever the tree's size.  The floor is that read, 64 KB per (request, head).
 //
 // u moves the fp32 state, so it is formed to fp32 accuracy: every operand is split into two bf16 parts, hi + lo,
 // and each product takes hi hi + hi lo + lo hi with fp32 accumulators (2^-17 relative to a term; one part alone
-// would leave 2^-9); T comes from an fp32 substitution.  All of it but D2 and what follows is done before the
-// state has arrived.  A factor e^{-b} would overflow where the decays along a path sum to more than kMaxRange;
-// such a request takes its A and P pairwise from the path's own exponents instead.
+// would leave 2^-9); T comes from an fp32 substitution.  A, P and T are done while the state arrives.  A factor
+// e^{-b} would overflow where the decays along a path sum to more than kMaxRange; such a request takes its A and P
+// pairwise from the path's own exponents instead.
 //
 // D3 and D4 multiply entries off the paths by zero.  Where an operand is not finite that would carry a NaN from
 // one branch into another, so such a request or column takes a substitution that skips them (solve_masked).
+//
+// What bounds it is the length of one CTA's dependent steps, so the CTAs are kept small enough for several to share
+// an SM (the state passes through shared memory in two halves of 64 rows, half 1 loading while half 0 is
+// multiplied), each state row group goes to the tensor core as soon as it is converted, and a CTA pulls the inputs
+// of the one that will take its place into L2.
 #include "kda_tc.cuh"
 #include "kda_tree.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kD = 128, kWorkers = 256, kThreads = 288;  // eight worker warps; one that reads the tree and issues the MMAs
-constexpr float kMaxRange = 80.f;
+// Eight worker warps; warp 8 reads the tree and, for MP = 16, forms T and G; warp 9 issues the MMAs.
+constexpr int kD = 128, kWorkers = 256, kThreads = 320;
+constexpr float kMaxRange = 115.f;  // in powers of two
 
 // Shared memory for trees of at most MP nodes, in bytes.  Operand images are K-major with the 128-byte swizzle, 64
 // elements to a row (keys and queries: two panels of 64 channels), but the state's, which is read as the MN-major
-// A operand (two groups of 64 state columns by 128 rows).  MMAs with fewer than 128 valid A rows read past their
+// A operand (two groups of 64 state columns by 64 rows, a half of the state).  MMAs with fewer than 128 valid A rows read past their
 // image, never past the allocation; what they read there only reaches accumulator rows that nobody looks at.
 template <int MP>
 struct Layout {
@@ -38,22 +43,27 @@ struct Layout {
     static constexpr uint32_t ap_bytes = 2 * MP * ap_stride * 4;
     static constexpr uint32_t kq = 0;
     static constexpr uint32_t s_hi = kq + 2 * kq_panel;
-    static constexpr uint32_t s_lo = s_hi + 32768;
-    static constexpr uint32_t ki = s_lo + 32768;
+    static constexpr uint32_t s_lo = s_hi + 16384;
+    static constexpr uint32_t ki = s_lo + 16384;
     static constexpr uint32_t b = ki + 2 * ki_panel;     // fp32 [MP][128]: g, then (MP > 16) the paths' sums b
-    static constexpr uint32_t b_bytes = MP * 512 > ap_bytes ? MP * 512 : ap_bytes;
+    static constexpr uint32_t ap_tg = MP == 64 ? ap_bytes : 2 * ap_bytes;
+    static constexpr uint32_t b_bytes = MP * 512 > ap_tg ? MP * 512 : (ap_tg + 1023) / 1024 * 1024;
     static constexpr uint32_t v = b + b_bytes;           // bf16 [MP][128]
-    static constexpr uint32_t tb = v + MP * 256;         // fp32 3 x [32][36]: the blocks of T (MP = 64)
-    static constexpr uint32_t total = tb + (MP == 64 ? 3 * 32 * 36 * 4 : 0);
+    static constexpr uint32_t w = v + MP * 256;          // fp32 [128]: the output weight
+    static constexpr uint32_t tb = w + 512;              // fp32 3 x [32][36]: the blocks of T (MP = 64)
+    static constexpr bool early_z = MP == 16;            // the gate has a place of its own, else D2's operands'
+    static constexpr uint32_t z = early_z ? tb : kq;     // bf16 [MP][128]: the gate
+    static constexpr uint32_t total = MP == 64 ? tb + 3 * 32 * 36 * 4 : early_z ? tb + MP * 256 : tb;
     // later uses of the same bytes
-    static constexpr uint32_t t_img = ki;                // T - I: rows hi, lo (once D1 is done)
-    static constexpr uint32_t p_img = ki + MP * 256;     // P: rows hi, lo
+    static constexpr uint32_t t_img = ki;                // rows T - I hi, G hi, T - I lo, G lo (MP = 64: T - I hi, lo)
+    static constexpr uint32_t p_img = ki + MP * 256;     // MP = 64: P hi, lo   (both once D1 is done)
     static constexpr uint32_t ap = b;                    // fp32 A [MP][ap_stride], then P (once the images are built)
-    static constexpr uint32_t z = kq;                    // bf16 [MP][128] (once D2 is done)
+    static constexpr uint32_t tg = MP < 64 ? ap + ap_bytes : tb;  // fp32 T - I [MP][ap_stride], then G (MP = 64: tb)
     static constexpr uint32_t r_img = s_hi;              // r: 128 rows hi, 128 rows lo (once D2 is done)
-    static constexpr uint32_t u_img = s_lo;              // u, the same way
-    static constexpr uint32_t o = s_hi;                  // fp32 [MP][128] (once D3 is done)
-    static constexpr uint32_t d1 = 4 * MP, d3 = 4 * MP, d4 = 6 * MP;  // accumulator columns; D2 at 0
+    static constexpr uint32_t u_img = s_hi;              // MP = 64: u, the same way (once D3 is done)
+    static constexpr uint32_t o = kq + (early_z ? 0 : MP * 256);  // fp32 [MP][128] (once D2 is done)
+    // accumulator columns: D2 at 0; D1 and, once it has been read, D3 (then D4) behind it
+    static constexpr uint32_t d1 = 4 * MP, d3 = 4 * MP, d4 = 6 * MP;
     static constexpr uint32_t tmem_cols = 8 * MP;
 };
 
@@ -105,15 +115,25 @@ __device__ __forceinline__ void add8(float (&f)[8], const float4 &a, const float
     f[4] += b.x; f[5] += b.y; f[6] += b.z; f[7] += b.w;
 }
 
-__device__ __forceinline__ float4 log_decay4(const float4 &g) {
-    return make_float4(log_decay(g.x), log_decay(g.y), log_decay(g.z), log_decay(g.w));
+// The decays' exponents are kept in base 2, the hardware's exponential.
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float4 log2_decay4(const float4 &g) {
+    return make_float4(log_decay(g.x) * kLog2e, log_decay(g.y) * kLog2e, log_decay(g.z) * kLog2e,
+                       log_decay(g.w) * kLog2e);
 }
+__device__ __forceinline__ float exp2_of(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// The logistic function to about 2^-21, for a bf16 result.
+__device__ __forceinline__ float gate_of(float z) { return __fdividef(1.f, 1.f + exp2_of(-kLog2e * z)); }
 
 struct Args {
     const __nv_bfloat16 *q, *k, *v;
     const float *g, *beta;
     const int32_t *parent, *cu, *seq_idx;
-    int H, total_nodes, max_nodes, num_slots;
+    int H, total_nodes, max_nodes, num_slots, ahead;
     const float *S_pool;
     __nv_bfloat16 *o;
     float *u;
@@ -136,14 +156,14 @@ __device__ __forceinline__ void residual8(const uint8_t *sm, const float *s_beta
 }
 
 // u and o of the thread's state column by forward substitution over the paths' entries only.  u is kept in the
-// thread's own two rows of u's image, which no other thread reads.
+// thread's own two rows of the image of r (or u), whose products are then not used.
 template <int MP>
 __device__ void solve_masked(uint8_t *sm, const TreeShared &ts, const float *s_beta, uint32_t tmem, int M, int c,
                              float *u_out, size_t row_stride) {
     using L = Layout<MP>;
     const float *sA = reinterpret_cast<const float *>(sm + L::ap), *sP = sA + MP * L::ap_stride;
     auto mine = [&](int a) {
-        return reinterpret_cast<float *>(sm + L::u_img + (a >> 5) * 16384 + c * 128 + (a & 31) * 4);
+        return reinterpret_cast<float *>(sm + L::r_img + (a >> 5) * 16384 + c * 128 + (a & 31) * 4);
     };
     float *s_o = reinterpret_cast<float *>(sm + L::o);
     for (int i0 = 0; i0 < M; i0 += 8) {
@@ -187,23 +207,61 @@ __device__ __forceinline__ void invert_block(const float *A, int stride, int lan
     }
 }
 
-// The MMAs of D (+)= A_hi [B_hi | B_lo]^T + A_lo [B_hi | B_lo]^T over `steps` slices of 16 elements.
-template <uint32_t Id>
-__device__ __forceinline__ void mma_split(uint32_t d, uint32_t a_hi, uint32_t a_lo, uint32_t b, int steps) {
+// The MMAs of D = A_hi B^T + A_lo B'^T over MP / 16 slices of 16 elements; B' is the first part of B's rows.
+template <int MP, uint32_t IdHi, uint32_t IdLo>
+__device__ __forceinline__ void mma_split(uint32_t d, uint32_t a_hi, uint32_t a_lo, uint32_t b, bool elected) {
     constexpr uint64_t kKmaj = tc::smem_desc_base(16, 1024, tc::SW_128B);
-    for (int c = 0; c < steps; ++c) tc::mma_bf16(d, tc::smem_desc(kKmaj, a_hi + c * 32), tc::smem_desc(kKmaj, b + c * 32), Id, c > 0);
-    for (int c = 0; c < steps; ++c) tc::mma_bf16(d, tc::smem_desc(kKmaj, a_lo + c * 32), tc::smem_desc(kKmaj, b + c * 32), Id, true);
+#pragma unroll
+    for (int c = 0; c < MP / 16; ++c)
+        tc::mma_bf16_warp(d, tc::smem_desc(kKmaj, a_hi + c * 32), tc::smem_desc(kKmaj, b + c * 32), IdHi, c > 0, elected);
+#pragma unroll
+    for (int c = 0; c < MP / 16; ++c)
+        tc::mma_bf16_warp(d, tc::smem_desc(kKmaj, a_lo + c * 32), tc::smem_desc(kKmaj, b + c * 32), IdLo, true, elected);
+}
+
+// Reads the rows of D1 that belong to this warp's lanes (row r of [K~ ; Q~]), masks and scales them into A and P.
+template <int MP>
+__device__ __forceinline__ void read_paths(uint8_t *sm, const TreeShared &ts, const float *s_beta, uint32_t tmem, int M,
+                                           int row, bool pairwise, int *s_wild) {
+    using L = Layout<MP>;
+    const bool is_a = row < MP;
+    const int i = is_a ? row : row - MP;
+    const unsigned long long anc = i < M ? ts.anc[i] : 0ull;
+    const float scale = is_a ? s_beta[i] : 1.f;
+    float *dst = reinterpret_cast<float *>(sm + L::ap) + ((is_a ? 0 : MP) + i) * L::ap_stride;
+    bool wild = false;
+#pragma unroll 2
+    for (int a0 = 0; a0 < MP; a0 += 8) {
+        float val[8];
+        if (!pairwise) {
+            float x[2][8];
+            tc::tmem_ld8x2(tmem + L::d1 + ((uint32_t)(row & ~31) << 16) + a0, MP, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                val[e] = ((anc >> (a0 + e)) & 1) && !(is_a && a0 + e == i) ? scale * (x[0][e] + x[1][e]) : 0.f;
+            reinterpret_cast<float4 *>(dst + a0)[0] = make_float4(val[0], val[1], val[2], val[3]);
+            reinterpret_cast<float4 *>(dst + a0)[1] = make_float4(val[4], val[5], val[6], val[7]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) val[e] = dst[a0 + e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) wild |= !is_finite(val[e]);
+        if (MP == 64 && !is_a) store_split8(sm + L::p_img, i, a0, MP, val);
+    }
+    if (wild) *s_wild = 1;
 }
 
 template <int MP>
-__global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tree_step_tc_kernel(const Args p) {
     using L = Layout<MP>;
     extern __shared__ uint8_t raw[];
     __shared__ TreeShared ts;
     __shared__ float s_beta[MP], s_scale[2 * MP];
-    __shared__ uint64_t bars[4];
+    __shared__ uint64_t bar_d1, bar_d3, bar_d4, bar_half[2], bar_rows[8];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_wild;  // A, P or T holds something that is not finite
+    __shared__ int s_wild;    // A, P, T or G holds something that is not finite
+    __shared__ int s_bad[4];  // r does, in the columns of one quarter of the lanes
     const int n = blockIdx.x / p.H, h = blockIdx.x % p.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Tree t = tree_rows(p.cu, n, p.total_nodes, p.max_nodes);
     const int slot = slot_of(p.seq_idx, n, p.num_slots);
@@ -217,10 +275,12 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
     const uint32_t sa = tc::smem_u32(sm);
     const size_t base = ((size_t)t.row0 * p.H + h) * kD, row_stride = (size_t)p.H * kD;
 
-    // The CTA's reads, issued at once: g, v and beta on their way to shared memory, k, q and the state in registers.
+    // The CTA's reads, issued at once: g, v, the gate and its weight on their way to shared memory, k, q and half of
+    // the state in registers.
     constexpr int kUnits = MP / 16;  // (node, 8 channels) per worker: node (tid / 16) + 16 e, channels 8 (tid % 16) on
     uint4 kr[kUnits], qr[kUnits];
-    float s[8][8];                   // state row (tid / 16) + 16 j, columns 8 (tid % 16) on
+    float s[4][8];                   // state row (tid / 16) + 16 j of the half, columns 8 (tid % 16) on
+    const float *S = p.S_pool + ((size_t)slot * p.H + h) * kD * kD + (size_t)(tid >> 4) * kD + (tid & 15) * 8;
     if (warp < 8) {
         for (int i = tid; i < M * 32; i += kWorkers)
             tc::cp_async16(sm + L::b + i * 16, p.g + base + (size_t)(i >> 5) * row_stride + (i & 31) * 4);
@@ -235,19 +295,38 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
         }
         for (int i = tid; i < M * 16; i += kWorkers)
             tc::cp_async16(sm + L::v + i * 16, p.v + base + (size_t)(i >> 4) * row_stride + (i & 15) * 8);
-        const float *S = p.S_pool + ((size_t)slot * p.H + h) * kD * kD;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ldg8(S + (size_t)((tid >> 4) + 16 * j) * kD + (tid & 15) * 8, s[j]);
+        for (int j = 0; j < 4; ++j) ldg8(S + (size_t)(16 * j) * kD, s[j]);
+        if (p.gate) {
+            if (L::early_z)
+                for (int i = tid; i < M * 16; i += kWorkers)
+                    tc::cp_async16(sm + L::z + i * 16, p.gate + base + (size_t)(i >> 4) * row_stride + (i & 15) * 8);
+            if (warp == 0) {
+                if (p.weight) tc::cp_async16(sm + L::w + lane * 16, p.weight + lane * 4);
+                else *reinterpret_cast<float4 *>(sm + L::w + lane * 16) = make_float4(1.f, 1.f, 1.f, 1.f);
+            }
+        }
         tc::cp_async_wait_all();
-    } else {
-        for (int i = lane; i < MP; i += 32) s_beta[i] = i < M ? p.beta[(size_t)(t.row0 + i) * p.H + h] : 0.f;
+        for (int i = tid; i < M * 32; i += kWorkers) {  // the vectors that this thread copied
+            float4 *x = reinterpret_cast<float4 *>(sm + L::b + i * 16);
+            *x = log2_decay4(*x);
+        }
+    } else if (warp == 9) {
+        if (lane == 0) tc::bulk_prefetch_l2(p.S_pool + (((size_t)slot * p.H + h) * kD + 64) * kD, 32768);
         tc::tmem_alloc(&s_tmem, L::tmem_cols);
         tc::tmem_relinquish();
         if (lane == 0) {
-            for (int i = 0; i < 4; ++i) tc::mbar_init(&bars[i], 1);
+            tc::mbar_init(&bar_d1, 1);
+            tc::mbar_init(&bar_d3, 1);
+            tc::mbar_init(&bar_d4, 1);
+            tc::mbar_init(&bar_half[0], 1);
+            tc::mbar_init(&bar_half[1], 1);
+            for (int i = 0; i < 8; ++i) tc::mbar_init(&bar_rows[i], 8);
             tc::fence_mbar_init();
             s_wild = 0;
+            for (int i = 0; i < 4; ++i) s_bad[i] = 0;
         }
+        for (int i = lane; i < MP; i += 32) s_beta[i] = i < M ? p.beta[(size_t)(t.row0 + i) * p.H + h] : 0.f;
         tc::tc_fence_before();
     }
     const bool good = read_tree(ts, p.parent, p.cu, n, p.total_nodes, p.max_nodes, true, 8).nodes > 0;  // a block barrier
@@ -255,10 +334,9 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
     const uint32_t tmem = s_tmem;
     if (!good) {
         if (tid == 0) report_invalid(p.status);
-        if (warp == 8) tc::tmem_dealloc(tmem, L::tmem_cols);
+        if (warp == 9) tc::tmem_dealloc(tmem, L::tmem_cols);
         return;
     }
-
     // Operand images of K~, Q~ and K^.  b sums g over the path; above 16 nodes, 16 nodes at a time, from the b of
     // the nearest ancestor in an earlier group.
     float *s_b = reinterpret_cast<float *>(sm + L::b);
@@ -279,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
                 const int a = 16 * e + __ffs((int)here) - 1;
                 here &= here - 1;
                 const float4 *x = reinterpret_cast<const float4 *>(s_b + a * kD + ch * 8);
-                add8(b, log_decay4(x[0]), log_decay4(x[1]));
+                add8(b, x[0], x[1]);
             }
         }
         if (MP > 16) {
@@ -291,12 +369,13 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
             }
             __syncthreads();
         }
-        if (warp < 8) {
+        if (warp < 8 && (warp << 1) + 16 * e < M) {  // what the images hold past the tree is never looked at
             float kf[8], qf[8], ki[8];
             unpack8(kr[e], kf);
             unpack8(qr[e], qf);
+            float sk = 1.f, sq = 1.f;
             if (p.qk_norm) {  // 16 threads hold a row
-                float sk = 0.f, sq = 0.f;
+                sk = sq = 0.f;
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
                     sk = fmaf(kf[x], kf[x], sk);
@@ -313,19 +392,15 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
                     s_scale[i] = sk;
                     s_scale[MP + i] = sq;
                 }
-#pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    kf[x] *= sk;
-                    qf[x] *= sq;
-                }
             }
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
-                const float up = expf(b[x]);  // rows past the tree: zero keys, b = 0
+                const float up = exp2_of(b[x]);
                 range = fmaxf(range, fabsf(b[x]));
-                ki[x] = __fdividef(kf[x], up);  // used while up is within e^{+-kMaxRange}
+                kf[x] *= sk;
+                qf[x] *= sq * up;
+                ki[x] = kf[x] * exp2_of(-b[x]);  // used while b is within +-kMaxRange
                 kf[x] *= up;
-                qf[x] *= up;
             }
             uint8_t *kq = sm + L::kq + (ch >> 3) * L::kq_panel;
             store_split8(kq, i, (ch & 7) * 8, 2 * MP, kf);
@@ -337,13 +412,13 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
     const bool pairwise = __syncthreads_or(!(range <= kMaxRange));
     float *sA = reinterpret_cast<float *>(sm + L::ap), *sP = sA + MP * L::ap_stride;
     if (pairwise) {
-        // A warp per (node, ancestor), four channels a lane, into the state images' place first: the results'
-        // own place holds b.
-        float *xA = reinterpret_cast<float *>(sm + L::s_hi), *xP = xA + MP * L::ap_stride;
+        // A warp per (node, ancestor), four channels a lane.  The results' own place holds b, so they pass through
+        // the place of K^, which is not used, and (for the larger half of MP = 64) of the state's first rows.
+        float *xA = reinterpret_cast<float *>(sm + (MP == 64 ? L::s_hi : L::ki)), *xP = xA + MP * L::ap_stride;
+        static_assert(MP == 64 ? L::ap_bytes <= 32768 + 2 * L::ki_panel : L::ap_bytes <= 2 * L::ki_panel, "");
         if (MP == 16) {
             if (tid < kD)
-                for (int i = 0; i < M; ++i)
-                    s_b[i * kD + tid] = log_decay(s_b[i * kD + tid]) + (i ? s_b[ts.parent[i] * kD + tid] : 0.f);
+                for (int i = 1; i < M; ++i) s_b[i * kD + tid] += s_b[ts.parent[i] * kD + tid];
             __syncthreads();
         }
         if (warp < 8)
@@ -355,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
                     for (int e = 0; e < 4; ++e) {
                         const int c = lane + 32 * e;
                         const float ka = __bfloat162float(p.k[base + (size_t)a * row_stride + c]) *
-                                         expf(s_b[i * kD + c] - s_b[a * kD + c]);
+                                         exp2_of(s_b[i * kD + c] - s_b[a * kD + c]);
                         va = fmaf(__bfloat162float(p.k[base + (size_t)i * row_stride + c]), ka, va);
                         vp = fmaf(__bfloat162float(p.q[base + (size_t)i * row_stride + c]), ka, vp);
                     }
@@ -378,99 +453,136 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
         __syncthreads();
         for (int x = tid; x < 2 * MP * L::ap_stride; x += kThreads) sA[x] = xA[x];
         __syncthreads();
-    } else if (warp == 8 && lane == 0) {  // D1, a panel at a time
-        constexpr uint32_t id = tc::idesc_bf16_f32(128, 2 * MP, false, false);
-        constexpr uint64_t kKmaj = tc::smem_desc_base(16, 1024, tc::SW_128B);
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-            const uint32_t a = sa + L::kq + (c >> 3) * 2 * MP * 128 + ((c >> 2) & 1) * L::kq_panel + (c & 3) * 32;
-            const uint32_t b = sa + L::ki + ((c >> 2) & 1) * L::ki_panel + (c & 3) * 32;
-            tc::mma_bf16(tmem + L::d1, tc::smem_desc(kKmaj, a), tc::smem_desc(kKmaj, b), id, c > 0);
-        }
-        tc::mma_commit(&bars[0]);
     }
-    __syncwarp();
-    if (warp < 8) {  // the state's images
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int row = (tid >> 4) + 16 * j, col = (tid & 15) * 8;
-            uint4 hi, lo;
-            split8(s[j], hi, lo);
-            const uint32_t at = (col >> 6) * 16384 + tc::sw128_offset(row, col & 63);
-            *reinterpret_cast<uint4 *>(sm + L::s_hi + at) = hi;
-            *reinterpret_cast<uint4 *>(sm + L::s_lo + at) = lo;
+
+    if (warp == 8 && blockIdx.x + p.ahead < gridDim.x) {  // the inputs of the CTA that starts about when this one ends
+        const int next = blockIdx.x + p.ahead, nn = next / p.H, nh = next % p.H;
+        const Tree nt = tree_rows(p.cu, nn, p.total_nodes, p.max_nodes);
+        const int ns = slot_of(p.seq_idx, nn, p.num_slots);
+        if (nt.nodes > 0 && ns >= 0) {
+            if (lane < 2)
+                tc::bulk_prefetch_l2(p.S_pool + (((size_t)ns * p.H + nh) * kD + 64 * lane) * kD, 32768);
+            for (int i = lane; i < nt.nodes; i += 32) {
+                const size_t at = ((size_t)(nt.row0 + i) * p.H + nh) * kD;
+                tc::bulk_prefetch_l2(p.g + at, 512);
+                tc::bulk_prefetch_l2(p.k + at, 256);
+                tc::bulk_prefetch_l2(p.q + at, 256);
+                tc::bulk_prefetch_l2(p.v + at, 256);
+                if (p.gate) tc::bulk_prefetch_l2(p.gate + at, 256);
+            }
         }
-        tc::fence_async_smem();
     }
-    __syncthreads();
+
     bool ok = true;
-    if (warp == 8) {
-        if (lane == 0) {  // D2: S hi x [hi | lo], then S lo x hi
-            constexpr uint32_t id4 = tc::idesc_bf16_f32(128, 4 * MP, true, false);
-            constexpr uint32_t id2 = tc::idesc_bf16_f32(128, 2 * MP, true, false);
-            constexpr uint64_t kSmn = tc::smem_desc_base(16384, 1024, tc::SW_128B);
-            constexpr uint64_t kKmaj = tc::smem_desc_base(16, 1024, tc::SW_128B);
+    constexpr int kPath = MP == 16 ? 8 : 4;  // the first of the warps that form T
+    if (warp == 9) {
+        constexpr uint64_t kKmaj = tc::smem_desc_base(16, 1024, tc::SW_128B);
+        constexpr uint64_t kSmn = tc::smem_desc_base(8192, 1024, tc::SW_128B);
+        constexpr uint32_t id1 = tc::idesc_bf16_f32(128, 2 * MP, false, false);
+        constexpr uint32_t id4 = tc::idesc_bf16_f32(128, 4 * MP, true, false);
+        constexpr uint32_t id2 = tc::idesc_bf16_f32(128, 2 * MP, true, false);
+        const bool elected = tc::elect_one();
+        if (!pairwise) {  // D1: hi x [hi | lo], then lo x [hi | lo]
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-                const uint32_t a = sa + (c >> 3 ? L::s_lo : L::s_hi) + (c & 7) * 2048;
-                const uint32_t b = sa + L::kq + ((c >> 2) & 1) * L::kq_panel + (c & 3) * 32;
-                tc::mma_bf16(tmem, tc::smem_desc(kSmn, a), tc::smem_desc(kKmaj, b), c >> 3 ? id2 : id4, c > 0);
+                const uint32_t a = sa + L::kq + (c >> 3) * 2 * MP * 128 + ((c >> 2) & 1) * L::kq_panel + (c & 3) * 32;
+                const uint32_t b = sa + L::ki + ((c >> 2) & 1) * L::ki_panel + (c & 3) * 32;
+                tc::mma_bf16_warp(tmem + L::d1, tc::smem_desc(kKmaj, a), tc::smem_desc(kKmaj, b), id1, c > 0, elected);
             }
-            tc::mma_commit(&bars[1]);
+            if (elected) tc::mma_commit(&bar_d1);
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {  // D2, 16 state rows at a time: S hi x [hi | lo] + S lo x hi
+            ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bar_rows[c], 0));
+            tc::tc_fence_after();
+            const uint32_t a = (c & 3) * 2048, b = sa + L::kq + (c >> 2) * L::kq_panel + (c & 3) * 32;
+            tc::mma_bf16_warp(tmem, tc::smem_desc(kSmn, sa + L::s_hi + a), tc::smem_desc(kKmaj, b), id4, c > 0, elected);
+            tc::mma_bf16_warp(tmem, tc::smem_desc(kSmn, sa + L::s_lo + a), tc::smem_desc(kKmaj, b), id2, true, elected);
+            if ((c & 3) == 3 && elected) tc::mma_commit(&bar_half[c >> 2]);
         }
         __syncwarp();
-    } else if (warp >= 4) {
-        // A, P, T and the images of T - I and P, while D2 runs.  Lane r of D1 is row r of [K~ ; Q~].
-        const int row = (warp - 4) * 32 + lane;
-        if ((warp - 4) * 32 < 2 * MP) {
-            if (!pairwise) ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[0], 0));
-            tc::tc_fence_after();
-            const bool is_a = row < MP;
-            const int i = is_a ? row : row - MP;
-            const unsigned long long anc = i < M ? ts.anc[i] : 0ull;
-            const float scale = is_a ? s_beta[i] : 1.f;
-            bool wild = false;
-            for (int a0 = 0; a0 < MP; a0 += 8) {
-                float val[8];
-                float *dst = (is_a ? sA : sP) + i * L::ap_stride + a0;
-                if (!pairwise) {
-                    float x[2][8];
-                    tc::tmem_ld8x2(tmem + L::d1 + ((uint32_t)((warp - 4) * 32) << 16) + a0, MP, x);
+    } else if (warp < 8) {  // the state's images, half by half
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        val[e] = ((anc >> (a0 + e)) & 1) && !(is_a && a0 + e == i) ? scale * (x[0][e] + x[1][e]) : 0.f;
-                    reinterpret_cast<float4 *>(dst)[0] = make_float4(val[0], val[1], val[2], val[3]);
-                    reinterpret_cast<float4 *>(dst)[1] = make_float4(val[4], val[5], val[6], val[7]);
+        for (int half = 0; half < 2; ++half) {
+            if (half) ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bar_half[0], 0));  // the place is free
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = (tid >> 4) + 16 * j, col = (tid & 15) * 8;
+                uint4 hi, lo;
+                split8(s[j], hi, lo);
+                const uint32_t at = (col >> 6) * 8192 + tc::sw128_offset(row, col & 63);
+                *reinterpret_cast<uint4 *>(sm + L::s_hi + at) = hi;
+                *reinterpret_cast<uint4 *>(sm + L::s_lo + at) = lo;
+                tc::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bar_rows[4 * half + j]);
+            }
+            if (!half) {  // only now: a fence waits for the loads before it
+#pragma unroll
+                for (int j = 0; j < 4; ++j) ldg8(S + (size_t)(64 + 16 * j) * kD, s[j]);
+            }
+        }
+    }
+    if (warp >= kPath && warp < kPath + (MP == 16 ? 1 : 4)) {
+        // A, P, T and the images that u and o are formed with
+        const int w = warp - kPath;
+        float *tb = reinterpret_cast<float *>(sm + L::tg);  // T - I and G; or T's diagonal blocks and A21 T11, [32][36] each
+        if (!pairwise) ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bar_d1, 0));
+        tc::tc_fence_after();
+        if (w * 32 < 2 * MP) read_paths<MP>(sm, ts, s_beta, tmem, M, w * 32 + lane, pairwise, &s_wild);
+        bool wild = false;
+        if constexpr (MP < 64) {
+            // one warp (MP = 16: its lower half) writes T - I, the other (half) forms G = P T from the same T
+            if (MP == 32) tc::named_barrier(1, 128);
+            else __syncwarp();
+            const int j = MP == 16 ? lane & 15 : lane;
+            const bool is_t = MP == 16 ? lane < 16 : w == 0;
+            if (MP == 16 || w < 2) {
+                float tc_[MP];
+                invert_block<MP>(sA, L::ap_stride, j, tc_);
+                if (is_t) {
+#pragma unroll
+                    for (int i = 0; i < MP; ++i) tb[i * L::ap_stride + j] = i == j ? 0.f : tc_[i];
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) val[e] = dst[e];
+                    for (int i = 0; i < MP; ++i) {
+                        float acc[2] = {0.f, 0.f};
+#pragma unroll
+                        for (int a0 = 0; a0 <= i; a0 += 4) {
+                            const float4 y = *reinterpret_cast<const float4 *>(&sP[i * L::ap_stride + a0]);
+                            const float ya[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (a0 + e <= i) acc[e & 1] = fmaf(ya[e], tc_[a0 + e], acc[e & 1]);
+                        }
+                        tb[(MP + i) * L::ap_stride + j] = acc[0] + acc[1];
+                    }
                 }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) wild |= !is_finite(val[e]);
-                if (!is_a) store_split8(sm + L::p_img, i, a0, MP, val);
             }
-            if (wild) s_wild = 1;
-        }
-        if (MP == 64) tc::named_barrier(1, 128);
-        else __syncwarp();
-        constexpr int NB = MP < 32 ? MP : 32;
-        float *tb = reinterpret_cast<float *>(sm + L::tb);  // MP = 64: T's diagonal blocks and A21 T11, [32][36] each
-        if (warp - 4 < MP / NB) {
-            const int o = (warp - 4) * NB;
-            float tc_[NB];
-            invert_block<NB>(sA + o * L::ap_stride + o, L::ap_stride, lane, tc_);
-            bool wild = false;
-            if (lane < NB) {
+            if (MP == 32) tc::named_barrier(1, 128);
+            else __syncwarp();
+            for (int x = w * 32 + lane; x < 2 * MP * (MP / 8); x += MP == 16 ? 32 : 128) {
+                const int row = x / (MP / 8), c0 = x % (MP / 8) * 8;
+                const float4 *from = reinterpret_cast<const float4 *>(tb + row * L::ap_stride + c0);
+                const float4 f0 = from[0], f1 = from[1];
+                const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
-                for (int i = 0; i < NB; ++i) {
+                for (int e = 0; e < 8; ++e) wild |= !is_finite(f[e]);
+                store_split8(sm + L::t_img, row, c0, 2 * MP, f);
+            }
+        } else {
+            tc::named_barrier(1, 128);
+            if (w < 2) {
+                float tc_[32];
+                invert_block<32>(sA + w * 32 * (L::ap_stride + 1), L::ap_stride, lane, tc_);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
                     wild |= !is_finite(tc_[i]);
-                    store_split1(sm + L::t_img, o + i, o + lane, MP, i == lane ? 0.f : tc_[i]);
-                    if (MP == 64) tb[(warp - 4) * 32 * 36 + i * 36 + lane] = tc_[i];
+                    store_split1(sm + L::t_img, w * 32 + i, w * 32 + lane, MP, i == lane ? 0.f : tc_[i]);
+                    tb[w * 32 * 36 + i * 36 + lane] = tc_[i];
                 }
-                if (wild) s_wild = 1;
             }
-        }
-        if (MP == 64) {  // T21 = -T22 (A21 T11); nothing above the diagonal
+            // T21 = -T22 (A21 T11); nothing above the diagonal
             tc::named_barrier(1, 128);
             const int i = (tid - 128) >> 2, j0 = (tid & 3) * 8;
             const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -480,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
                 const float *left = step ? tb + 32 * 36 + i * 36 : sA + (32 + i) * L::ap_stride;
                 const float *right = step ? tb + 2 * 32 * 36 : tb;
                 float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 8
                 for (int a = 0; a < 32; ++a) {
                     const float x = left[a];
                     const float4 *y = reinterpret_cast<const float4 *>(right + a * 36 + j0);
@@ -496,109 +608,129 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
                     dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
                     tc::named_barrier(1, 128);
                 } else {
-                    bool wild = false;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         acc[e] = -acc[e];
                         wild |= !is_finite(acc[e]);
                     }
                     store_split8(sm + L::t_img, 32 + i, j0, MP, acc);
-                    if (wild) s_wild = 1;
                 }
             }
         }
+        if (wild) s_wild = 1;
         tc::fence_async_smem();
-        // the gate, into the place of D2's operands
-        ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bars[1], 0));
-        if (p.gate)
+        if (!L::early_z && p.gate) {  // the gate, into the place of D2's operands
+            ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bar_half[1], 0));
             for (int i = tid - 128; i < M * 16; i += 128)
                 tc::cp_async16(sm + L::z + i * 16, p.gate + base + (size_t)(i >> 4) * row_stride + (i & 15) * 8);
+        }
     }
+    // A thread is a state column from here on; two warps share a quarter of TMEM's lanes and take half of the nodes
+    // each (for r only where no warp is busy with T).
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    bool finite = true;
-    if (warp < 4) {  // r, for D3; a thread is a state column
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[1], 0));
+    const int col = tid & (kD - 1), side = warp >> 2;
+    constexpr int kHalf = MP / 2, kSides = MP == 16 ? 2 : 1;
+    if (warp < 4 * kSides) {  // r, for D3
+        ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bar_half[1], 0));
         tc::tc_fence_after();
-        for (int i0 = 0; i0 < MP; i0 += 8) {
+        bool finite = true;
+        for (int i0 = side * (MP / kSides); i0 < (side + 1) * (MP / kSides); i0 += 8) {
             float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (i0 < M) {
                 float x[2][8];
                 tc::tmem_ld8x2(lanes + i0, 2 * MP, x);
-                residual8<MP>(sm, s_beta, x[0], x[1], i0, tid, r);
+                residual8<MP>(sm, s_beta, x[0], x[1], i0, col, r);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     r[e] = i0 + e < M ? r[e] : 0.f;
                     finite &= is_finite(r[e]);
                 }
             }
-            store_split8(sm + L::r_img, tid, i0, 128, r);
+            store_split8(sm + L::r_img, col, i0, 128, r);
         }
+        if (!finite) s_bad[warp & 3] = 1;
         tc::fence_async_smem();
         tc::tc_fence_before();
     }
-    ok = __syncthreads_and(ok);  // every wait so far was met; r, T and P are complete
-    if (ok && warp == 8) {
+    ok = __syncthreads_and(ok);  // every wait so far was met; r, T, G and P are complete
+    constexpr uint32_t id_2mp = tc::idesc_bf16_f32(128, 2 * MP, false, false);
+    if (ok && warp == 9) {
         tc::tc_fence_after();
-        if (lane == 0) {
-            mma_split<tc::idesc_bf16_f32(128, 2 * MP, false, false)>(tmem + L::d3, sa + L::r_img, sa + L::r_img + 16384,
-                                                                     sa + L::t_img, MP / 16);
-            tc::mma_commit(&bars[2]);
-        }
+        // MP = 64: columns u hi, u lo; else u hi, o hi, u lo, o lo
+        constexpr uint32_t id_hi = MP == 64 ? id_2mp : tc::idesc_bf16_f32(128, 4 * MP, false, false);
+        const bool elected = tc::elect_one();
+        mma_split<MP, id_hi, id_2mp>(tmem + L::d3, sa + L::r_img, sa + L::r_img + 16384, sa + L::t_img, elected);
+        if (elected) tc::mma_commit(&bar_d3);
         __syncwarp();
     }
-    const bool masked = s_wild || !__all_sync(0xffffffffu, finite);  // of a worker warp's columns
-    float *u_out = p.u ? p.u + base + tid : nullptr;
-    if (ok && warp < 4) {
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[2], 0));
+    const bool masked = s_wild || s_bad[warp & 3];
+    float *u_out = p.u ? p.u + base + col : nullptr;
+    float *s_o = reinterpret_cast<float *>(sm + L::o);
+    if (ok && warp < 8) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&bar_d3, 0));
         tc::tc_fence_after();
         if (masked) {
-            solve_masked<MP>(sm, ts, s_beta, lanes, M, tid, u_out, row_stride);
+            if (side == 0) solve_masked<MP>(sm, ts, s_beta, lanes, M, col, u_out, row_stride);
         } else {
-            for (int i0 = 0; i0 < MP; i0 += 8) {
+            for (int i0 = side * kHalf; i0 < (side + 1) * kHalf; i0 += 8) {
                 float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
                 if (i0 < M) {
-                    float x[2][8], d[2][8];
-                    tc::tmem_ld8x2(lanes + i0, 2 * MP, x);
-                    tc::tmem_ld8x2(lanes + L::d3 + i0, MP, d);
-                    residual8<MP>(sm, s_beta, x[0], x[1], i0, tid, u);
+                    if constexpr (MP == 64) {
+                        float x[2][8], d[2][8];
+                        tc::tmem_ld8x2(lanes + i0, 2 * MP, x);
+                        tc::tmem_ld8x2(lanes + L::d3 + i0, MP, d);
+                        residual8<MP>(sm, s_beta, x[0], x[1], i0, col, u);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        u[e] = i0 + e < M ? u[e] + (d[0][e] + d[1][e]) : 0.f;
-                        if (u_out && i0 + e < M) u_out[(size_t)(i0 + e) * row_stride] = u[e];
+                        for (int e = 0; e < 8; ++e) u[e] = i0 + e < M ? u[e] + (d[0][e] + d[1][e]) : 0.f;
+                    } else {
+                        float x[4][8], d[4][8];
+                        tc::tmem_ld8x4(lanes + i0, MP, x);
+                        tc::tmem_ld8x4(lanes + L::d3 + i0, MP, d);
+                        residual8<MP>(sm, s_beta, x[0], x[2], i0, col, u);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            u[e] += d[0][e] + d[2][e];
+                            s_o[(i0 + e) * kD + col] = (x[1][e] + x[3][e]) + (d[1][e] + d[3][e]);
+                        }
+                    }
+                    if (u_out) {
+                        float *out = u_out + (size_t)i0 * row_stride;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e, out += row_stride)
+                            if (i0 + e < M) *out = u[e];
                     }
                 }
-                store_split8(sm + L::u_img, tid, i0, 128, u);
+                if (MP == 64) store_split8(sm + L::u_img, col, i0, 128, u);
             }
         }
-        tc::fence_async_smem();
+        if (MP == 64) tc::fence_async_smem();
         tc::tc_fence_before();
     }
-    ok = __syncthreads_and(ok);
-    if (ok && warp == 8) {
-        tc::tc_fence_after();
-        if (lane == 0) {
-            mma_split<tc::idesc_bf16_f32(128, 2 * MP, false, false)>(tmem + L::d4, sa + L::u_img, sa + L::u_img + 16384,
-                                                                     sa + L::p_img, MP / 16);
-            tc::mma_commit(&bars[3]);
+    if (MP == 64) {
+        ok = __syncthreads_and(ok);
+        if (ok && warp == 9) {
+            tc::tc_fence_after();
+            const bool elected = tc::elect_one();
+            mma_split<MP, id_2mp, id_2mp>(tmem + L::d4, sa + L::u_img, sa + L::u_img + 16384, sa + L::p_img, elected);
+            if (elected) tc::mma_commit(&bar_d4);
+            __syncwarp();
         }
-        __syncwarp();
-    }
-    if (ok && warp < 4) {
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars[3], 0));
-        tc::tc_fence_after();
-        float *s_o = reinterpret_cast<float *>(sm + L::o);
-        for (int i0 = 0; i0 < M && !masked; i0 += 8) {
-            float y[2][8], d[2][8];
-            tc::tmem_ld8x2(lanes + MP + i0, 2 * MP, y);
-            tc::tmem_ld8x2(lanes + L::d4 + i0, MP, d);
+        if (ok && warp < 8) {
+            ok = __all_sync(0xffffffffu, tc::mbar_wait(&bar_d4, 0));
+            tc::tc_fence_after();
+            for (int i0 = side * kHalf; i0 < min(M, (side + 1) * kHalf) && !masked; i0 += 8) {
+                float y[2][8], d[2][8];
+                tc::tmem_ld8x2(lanes + MP + i0, 2 * MP, y);
+                tc::tmem_ld8x2(lanes + L::d4 + i0, MP, d);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s_o[(i0 + e) * kD + tid] = (y[0][e] + y[1][e]) + (d[0][e] + d[1][e]);
+                for (int e = 0; e < 8; ++e) s_o[(i0 + e) * kD + col] = (y[0][e] + y[1][e]) + (d[0][e] + d[1][e]);
+            }
+            tc::tc_fence_before();
         }
-        tc::tc_fence_before();
     }
-    tc::cp_async_wait_all();
+    if (!L::early_z) tc::cp_async_wait_all();
     ok = __syncthreads_and(ok);
-    if (warp == 8) {
+    if (warp == 9) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem, L::tmem_cols);
     }
@@ -606,32 +738,38 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
         if (tid == 0 && p.status) atomicCAS(p.status, 0, (int32_t)KDA_ERR_TIMEOUT);
         return;
     }
-    for (int i = warp; i < M && warp < 8; i += 8) {
-        const size_t at = base + (size_t)i * row_stride + lane * 4;
-        float4 x = *reinterpret_cast<const float4 *>(sm + L::o + i * 512 + lane * 16);
-        if (p.gate) {
-            const uint2 z = *reinterpret_cast<const uint2 *>(sm + L::z + i * 256 + lane * 8);
-            float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
-            if (p.weight) w = __ldg(reinterpret_cast<const float4 *>(p.weight) + lane);
-            float ss = fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, x.w * x.w)));
+    if (warp < 8) {
+        const float4 w = *reinterpret_cast<const float4 *>(sm + L::w + lane * 16);
+        __nv_bfloat16 *out = p.o + base + (size_t)warp * row_stride + lane * 4;
+#pragma unroll 2
+        for (int i = warp; i < M; i += 8, out += 8 * row_stride) {
+            float4 x = *reinterpret_cast<const float4 *>(sm + L::o + i * 512 + lane * 16);
+            if (p.gate) {
+                const uint2 z = *reinterpret_cast<const uint2 *>(sm + L::z + i * 256 + lane * 8);
+                float ss = fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, x.w * x.w)));
 #pragma unroll
-            for (int off = 16; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-            const float inv = rsqrtf(ss / (float)kD + p.out_eps);
-            x.x *= inv * w.x * sigmoidf(__uint_as_float(z.x << 16));
-            x.y *= inv * w.y * sigmoidf(__uint_as_float(z.x & 0xffff0000u));
-            x.z *= inv * w.z * sigmoidf(__uint_as_float(z.y << 16));
-            x.w *= inv * w.w * sigmoidf(__uint_as_float(z.y & 0xffff0000u));
+                for (int off = 16; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+                const float inv = rsqrtf(ss * (1.f / kD) + p.out_eps);
+                x.x *= inv * w.x * gate_of(__uint_as_float(z.x << 16));
+                x.y *= inv * w.y * gate_of(__uint_as_float(z.x & 0xffff0000u));
+                x.z *= inv * w.z * gate_of(__uint_as_float(z.y << 16));
+                x.w *= inv * w.w * gate_of(__uint_as_float(z.y & 0xffff0000u));
+            }
+            *reinterpret_cast<uint2 *>(out) = make_uint2(pack2(x.x, x.y), pack2(x.z, x.w));
         }
-        *reinterpret_cast<uint2 *>(p.o + at) = make_uint2(pack2(x.x, x.y), pack2(x.z, x.w));
     }
 }
 
 template <int MP>
-cudaError_t launch_mp(const Args &p, int ctas, cudaStream_t st) {
+cudaError_t launch_mp(Args p, int ctas, cudaStream_t st) {
     constexpr int smem = Layout<MP>::total + 1024;
     cudaError_t e =
         cudaFuncSetAttribute(tree_step_tc_kernel<MP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    int device = 0, sms = 0;
+    if ((e = cudaGetDevice(&device)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device)) != cudaSuccess) return e;
+    p.ahead = sms * (MP == 64 ? 1 : MP == 32 ? 2 : 3);  // the CTAs that run at once
     tree_step_tc_kernel<MP><<<ctas, kThreads, smem, st>>>(p);
     return cudaGetLastError();
 }
@@ -640,7 +778,7 @@ cudaError_t launch_mp(const Args &p, int ctas, cudaStream_t st) {
 
 cudaError_t launch_tree_step_tc(const TreeStepArgs &a, cudaStream_t st) {
     const Args p{(const __nv_bfloat16 *)a.q, (const __nv_bfloat16 *)a.k, (const __nv_bfloat16 *)a.v, a.g, a.beta,
-                 a.parent, a.cu, a.seq_idx, a.H, a.total_nodes, a.max_nodes, a.num_slots, a.S_pool,
+                 a.parent, a.cu, a.seq_idx, a.H, a.total_nodes, a.max_nodes, a.num_slots, 0, a.S_pool,
                  (__nv_bfloat16 *)a.o, a.u, a.status, a.fu.qk_norm, a.fu.qk_eps, (const __nv_bfloat16 *)a.fu.gate,
                  a.fu.weight, a.fu.out_eps};
     const int ctas = a.num_seqs * a.H;
