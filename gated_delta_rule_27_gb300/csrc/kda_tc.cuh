@@ -205,6 +205,9 @@ __device__ __forceinline__ void tma_prefetch_3d(const void *tmap, int x, int y, 
                  : "memory");
 }
 
+// Prefetches the line of global memory that holds p into L2.
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // Prefetches `bytes` (a multiple of 16, 16-byte aligned) of global memory into L2.
 __device__ __forceinline__ void bulk_prefetch_l2(const void *src, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");

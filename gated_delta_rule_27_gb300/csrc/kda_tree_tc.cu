@@ -19,8 +19,7 @@
 //
 // What bounds it is the length of one CTA's dependent steps, so the CTAs are kept small enough for several to share
 // an SM (the state passes through shared memory in two halves of 64 rows, half 1 loading while half 0 is
-// multiplied), each state row group goes to the tensor core as soon as it is converted, and a CTA pulls the inputs
-// of the one that will take its place into L2.
+// multiplied), and a CTA pulls the inputs of the one that will take its place into L2.
 #include "kda_tc.cuh"
 #include "kda_tree.cuh"
 
@@ -109,7 +108,6 @@ __device__ __forceinline__ void ldg8(const float *p, float (&f)[8]) {
                  : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
                  : "l"(p));
 }
-__device__ __forceinline__ bool is_finite(float x) { return fabsf(x) < INFINITY; }
 __device__ __forceinline__ void add8(float (&f)[8], const float4 &a, const float4 &b) {
     f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
     f[4] += b.x; f[5] += b.y; f[6] += b.z; f[7] += b.w;
@@ -189,21 +187,54 @@ __device__ void solve_masked(uint8_t *sm, const TreeShared &ts, const float *s_b
     }
 }
 
-// T = (I + A)^{-1} of an NB x NB diagonal block of A, one column per lane: T_ij = [i = j] - sum_{a < i} A_ia T_aj.
-template <int NB>
+// Two multiply-adds in one instruction, and the sum of a pair.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n"
+        ".reg .b64 x, y, z, w;\n"
+        "mov.b64 x, {%2, %3};\n"
+        "mov.b64 y, {%4, %5};\n"
+        "mov.b64 z, {%6, %7};\n"
+        "fma.rn.f32x2 w, x, y, z;\n"
+        "mov.b64 {%0, %1}, w;\n"
+        "}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+// sum_{a < n} x_a t_a, x a 16-byte aligned row in shared memory whose entries at and behind n are zero (up to the
+// next multiple of four)
+template <int n>
+__device__ __forceinline__ float row_dot(const float *x, const float *t) {
+    float2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+    for (int a = 0; a < n; a += 4) {
+        const float4 y = *reinterpret_cast<const float4 *>(x + a);
+        acc[0] = fma2(make_float2(y.x, y.y), make_float2(t[a], t[a + 1]), acc[0]);
+        if (a + 2 < n) acc[1] = fma2(make_float2(y.z, y.w), make_float2(t[a + 2], t[a + 3]), acc[1]);
+    }
+    return (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+}
+
+// T = (I + A)^{-1} of an NB x NB diagonal block of A (zero on and above its diagonal), one column per lane:
+// T_ij = [i = j] - sum_{a < i} A_ia T_aj.
+template <int NB, int I = 0>
 __device__ __forceinline__ void invert_block(const float *A, int stride, int lane, float (&t)[NB]) {
+    if constexpr (I == 0) {
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-        float acc[2] = {i == lane ? 1.f : 0.f, 0.f};
-#pragma unroll
-        for (int a0 = 0; a0 < i; a0 += 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(&A[i * stride + a0]);
-            const float xa[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (a0 + e < i) acc[e & 1] = fmaf(-xa[e], t[a0 + e], acc[e & 1]);
-        }
-        t[i] = acc[0] + acc[1];
+        for (int i = 0; i < NB; ++i) t[i] = 0.f;  // what a row's last vector reaches past its entries
+    }
+    if constexpr (I < NB) {
+        t[I] = (I == lane ? 1.f : 0.f) - row_dot<I>(A + I * stride, t);
+        invert_block<NB, I + 1>(A, stride, lane, t);
+    }
+}
+// One column of G = P T (P zero above its diagonal) to g[i * stride].
+template <int NB, int I = 0>
+__device__ __forceinline__ void multiply_block(const float *P, int stride, const float (&t)[NB], float *g) {
+    if constexpr (I < NB) {
+        g[I * stride] = row_dot<I + 1>(P + I * stride, t);
+        multiply_block<NB, I + 1>(P, stride, t, g);
     }
 }
 
@@ -229,7 +260,7 @@ __device__ __forceinline__ void read_paths(uint8_t *sm, const TreeShared &ts, co
     const unsigned long long anc = i < M ? ts.anc[i] : 0ull;
     const float scale = is_a ? s_beta[i] : 1.f;
     float *dst = reinterpret_cast<float *>(sm + L::ap) + ((is_a ? 0 : MP) + i) * L::ap_stride;
-    bool wild = false;
+    float zero = 0.f;  // NaN once it has met something that is not finite
 #pragma unroll 2
     for (int a0 = 0; a0 < MP; a0 += 8) {
         float val[8];
@@ -246,10 +277,10 @@ __device__ __forceinline__ void read_paths(uint8_t *sm, const TreeShared &ts, co
             for (int e = 0; e < 8; ++e) val[e] = dst[a0 + e];
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) wild |= !is_finite(val[e]);
+        for (int e = 0; e < 8; ++e) zero = fmaf(val[e], 0.f, zero);
         if (MP == 64 && !is_a) store_split8(sm + L::p_img, i, a0, MP, val);
     }
-    if (wild) *s_wild = 1;
+    if (zero != 0.f) *s_wild = 1;
 }
 
 template <int MP>
@@ -258,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
     extern __shared__ uint8_t raw[];
     __shared__ TreeShared ts;
     __shared__ float s_beta[MP], s_scale[2 * MP];
-    __shared__ uint64_t bar_d1, bar_d3, bar_d4, bar_half[2], bar_rows[8];
+    __shared__ uint64_t bar_d1, bar_d3, bar_d4, bar_half[2], bar_rows[2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_wild;    // A, P, T or G holds something that is not finite
     __shared__ int s_bad[4];  // r does, in the columns of one quarter of the lanes
@@ -321,13 +352,22 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
             tc::mbar_init(&bar_d4, 1);
             tc::mbar_init(&bar_half[0], 1);
             tc::mbar_init(&bar_half[1], 1);
-            for (int i = 0; i < 8; ++i) tc::mbar_init(&bar_rows[i], 8);
+            for (int i = 0; i < 2; ++i) tc::mbar_init(&bar_rows[i], 8);
             tc::fence_mbar_init();
             s_wild = 0;
             for (int i = 0; i < 4; ++i) s_bad[i] = 0;
         }
         for (int i = lane; i < MP; i += 32) s_beta[i] = i < M ? p.beta[(size_t)(t.row0 + i) * p.H + h] : 0.f;
         tc::tc_fence_before();
+    }
+    // Warp 8 looks up the CTA that starts about when this one ends, and asks for its inputs once they will not be in
+    // the way of this one's.
+    const int later = blockIdx.x + p.ahead;
+    Tree lt{0, 0};
+    int lslot = -1;
+    if (warp == 8 && later < gridDim.x) {
+        lt = tree_rows(p.cu, later / p.H, p.total_nodes, p.max_nodes);
+        lslot = slot_of(p.seq_idx, later / p.H, p.num_slots);
     }
     const bool good = read_tree(ts, p.parent, p.cu, n, p.total_nodes, p.max_nodes, true, 8).nodes > 0;  // a block barrier
     tc::tc_fence_after();
@@ -455,21 +495,18 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
         __syncthreads();
     }
 
-    if (warp == 8 && blockIdx.x + p.ahead < gridDim.x) {  // the inputs of the CTA that starts about when this one ends
-        const int next = blockIdx.x + p.ahead, nn = next / p.H, nh = next % p.H;
-        const Tree nt = tree_rows(p.cu, nn, p.total_nodes, p.max_nodes);
-        const int ns = slot_of(p.seq_idx, nn, p.num_slots);
-        if (nt.nodes > 0 && ns >= 0) {
-            if (lane < 2)
-                tc::bulk_prefetch_l2(p.S_pool + (((size_t)ns * p.H + nh) * kD + 64 * lane) * kD, 32768);
-            for (int i = lane; i < nt.nodes; i += 32) {
-                const size_t at = ((size_t)(nt.row0 + i) * p.H + nh) * kD;
-                tc::bulk_prefetch_l2(p.g + at, 512);
-                tc::bulk_prefetch_l2(p.k + at, 256);
-                tc::bulk_prefetch_l2(p.q + at, 256);
-                tc::bulk_prefetch_l2(p.v + at, 256);
-                if (p.gate) tc::bulk_prefetch_l2(p.gate + at, 256);
-            }
+    if (warp == 8 && lslot >= 0 && lt.nodes > 0) {
+        const int lh = later % p.H;
+        if (lane < 2)
+            tc::bulk_prefetch_l2(p.S_pool + (((size_t)lslot * p.H + lh) * kD + 64 * lane) * kD, 32768);
+        // the nodes' rows by 128-byte lines: four of g, two each of k, q, v and the gate (one bulk request per row
+        // held the warp for 60 clocks each)
+        for (int i = lane; i < lt.nodes * 4; i += 32) {
+            const size_t at = ((size_t)(lt.row0 + (i >> 2)) * p.H + lh) * kD;
+            tc::prefetch_l2(p.g + at + (i & 3) * 32);
+            const __nv_bfloat16 *x = i & 2 ? p.k : p.q, *y = i & 2 ? p.v : p.gate;
+            tc::prefetch_l2(x + at + (i & 1) * 64);
+            if (y) tc::prefetch_l2(y + at + (i & 1) * 64);
         }
     }
 
@@ -492,9 +529,11 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
             if (elected) tc::mma_commit(&bar_d1);
         }
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {  // D2, 16 state rows at a time: S hi x [hi | lo] + S lo x hi
-            ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bar_rows[c], 0));
-            tc::tc_fence_after();
+        for (int c = 0; c < 8; ++c) {  // D2, half by half, 16 state rows at a time: S hi x [hi | lo] + S lo x hi
+            if ((c & 3) == 0) {
+                ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bar_rows[c >> 2], 0));
+                tc::tc_fence_after();
+            }
             const uint32_t a = (c & 3) * 2048, b = sa + L::kq + (c >> 2) * L::kq_panel + (c & 3) * 32;
             tc::mma_bf16_warp(tmem, tc::smem_desc(kSmn, sa + L::s_hi + a), tc::smem_desc(kKmaj, b), id4, c > 0, elected);
             tc::mma_bf16_warp(tmem, tc::smem_desc(kSmn, sa + L::s_lo + a), tc::smem_desc(kKmaj, b), id2, true, elected);
@@ -513,10 +552,10 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
                 const uint32_t at = (col >> 6) * 8192 + tc::sw128_offset(row, col & 63);
                 *reinterpret_cast<uint4 *>(sm + L::s_hi + at) = hi;
                 *reinterpret_cast<uint4 *>(sm + L::s_lo + at) = lo;
-                tc::fence_async_smem();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bar_rows[4 * half + j]);
             }
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bar_rows[half]);
             if (!half) {  // only now: a fence waits for the loads before it
 #pragma unroll
                 for (int j = 0; j < 4; ++j) ldg8(S + (size_t)(64 + 16 * j) * kD, s[j]);
@@ -530,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
         if (!pairwise) ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bar_d1, 0));
         tc::tc_fence_after();
         if (w * 32 < 2 * MP) read_paths<MP>(sm, ts, s_beta, tmem, M, w * 32 + lane, pairwise, &s_wild);
-        bool wild = false;
+        float zero = 0.f;
         if constexpr (MP < 64) {
             // one warp (MP = 16: its lower half) writes T - I, the other (half) forms G = P T from the same T
             if (MP == 32) tc::named_barrier(1, 128);
@@ -544,19 +583,7 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
 #pragma unroll
                     for (int i = 0; i < MP; ++i) tb[i * L::ap_stride + j] = i == j ? 0.f : tc_[i];
                 } else {
-#pragma unroll
-                    for (int i = 0; i < MP; ++i) {
-                        float acc[2] = {0.f, 0.f};
-#pragma unroll
-                        for (int a0 = 0; a0 <= i; a0 += 4) {
-                            const float4 y = *reinterpret_cast<const float4 *>(&sP[i * L::ap_stride + a0]);
-                            const float ya[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (a0 + e <= i) acc[e & 1] = fmaf(ya[e], tc_[a0 + e], acc[e & 1]);
-                        }
-                        tb[(MP + i) * L::ap_stride + j] = acc[0] + acc[1];
-                    }
+                    multiply_block<MP>(sP, L::ap_stride, tc_, tb + MP * L::ap_stride + j);
                 }
             }
             if (MP == 32) tc::named_barrier(1, 128);
@@ -567,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
                 const float4 f0 = from[0], f1 = from[1];
                 const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
-                for (int e = 0; e < 8; ++e) wild |= !is_finite(f[e]);
+                for (int e = 0; e < 8; ++e) zero = fmaf(f[e], 0.f, zero);
                 store_split8(sm + L::t_img, row, c0, 2 * MP, f);
             }
         } else {
@@ -577,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
                 invert_block<32>(sA + w * 32 * (L::ap_stride + 1), L::ap_stride, lane, tc_);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                    wild |= !is_finite(tc_[i]);
+                    zero = fmaf(tc_[i], 0.f, zero);
                     store_split1(sm + L::t_img, w * 32 + i, w * 32 + lane, MP, i == lane ? 0.f : tc_[i]);
                     tb[w * 32 * 36 + i * 36 + lane] = tc_[i];
                 }
@@ -585,8 +612,8 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
             // T21 = -T22 (A21 T11); nothing above the diagonal
             tc::named_barrier(1, 128);
             const int i = (tid - 128) >> 2, j0 = (tid & 3) * 8;
-            const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            store_split8(sm + L::t_img, i, 32 + j0, MP, zero);
+            const float none[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            store_split8(sm + L::t_img, i, 32 + j0, MP, none);
 #pragma unroll
             for (int step = 0; step < 2; ++step) {
                 const float *left = step ? tb + 32 * 36 + i * 36 : sA + (32 + i) * L::ap_stride;
@@ -611,13 +638,13 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         acc[e] = -acc[e];
-                        wild |= !is_finite(acc[e]);
+                        zero = fmaf(acc[e], 0.f, zero);
                     }
                     store_split8(sm + L::t_img, 32 + i, j0, MP, acc);
                 }
             }
         }
-        if (wild) s_wild = 1;
+        if (zero != 0.f) s_wild = 1;
         tc::fence_async_smem();
         if (!L::early_z && p.gate) {  // the gate, into the place of D2's operands
             ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bar_half[1], 0));
@@ -633,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
     if (warp < 4 * kSides) {  // r, for D3
         ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bar_half[1], 0));
         tc::tc_fence_after();
-        bool finite = true;
+        float zero = 0.f;
         for (int i0 = side * (MP / kSides); i0 < (side + 1) * (MP / kSides); i0 += 8) {
             float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (i0 < M) {
@@ -643,12 +670,12 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     r[e] = i0 + e < M ? r[e] : 0.f;
-                    finite &= is_finite(r[e]);
+                    zero = fmaf(r[e], 0.f, zero);
                 }
             }
             store_split8(sm + L::r_img, col, i0, 128, r);
         }
-        if (!finite) s_bad[warp & 3] = 1;
+        if (zero != 0.f) s_bad[warp & 3] = 1;
         tc::fence_async_smem();
         tc::tc_fence_before();
     }
