@@ -15,6 +15,11 @@
 // Only the rows that the walk visits are read.  One cluster of CTAs serves a request; each CTA keeps its part of
 // the visited row in shared memory, so that the maximum, the sum, the excess after a rejection and the search
 // for the next token all work on one read of the row.
+//
+// What bounds it is the walk's length: visited nodes, one after the other, each with an exchange between the
+// cluster's CTAs.  So a node's first trial is decided from an fp32 sum that comes with the maximum in one exchange,
+// wherever that decides it (kMargin covers the sum's error a hundred times over); the exact sums are formed only
+// where a trial is closer than that, or lost.  Meanwhile the first child's row is on its way to L2.
 #include <cooperative_groups.h>
 
 #include "kda_tc.cuh"
@@ -27,26 +32,26 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32, kMaxCluster = 8;
 constexpr uint32_t kMaxPart = 65536;  // bytes of a row that a CTA keeps; a longer part is read again by every pass
+constexpr int kRuns = kMaxPart / 16 / 32;  // a run: the 32 vectors of 16 bytes that a warp takes at once
 constexpr float kFixed = 1099511627776.f;  // 2^40
+constexpr float kMargin = 1e-4f;
 
 __device__ __forceinline__ unsigned long long fixed40(float x) { return __float2ull_rz(x * kFixed); }
 
-// A sum of values in [0, 1] cut to multiples of 2^-40, without 64-bit conversions: adding 1 with rounding towards
-// zero leaves the first 23 bits of the value in the sum's mantissa, adding 2^-17 to the rest the next 17; the bit
-// patterns add up as integers.  At most kFlush values between two flushes.
-constexpr int kFlush = 256;
+// A sum of at most 8 values in [0, 1] cut to multiples of 2^-40, without 64-bit conversions: adding 1 with rounding
+// towards zero leaves the first 23 bits of the value in the sum's mantissa, adding 2^-17 to the rest the next 17;
+// the bit patterns add up as integers, and so do 32 lanes' (8 x 32 x 2^23 fits 32 bits).
 struct FixedSum {
     uint32_t hi = 0, lo = 0;
     __device__ __forceinline__ void add(float x) {
         const float a = __fadd_rz(x, 1.f);
         const float b = __fadd_rz(__fsub_rn(x, __fsub_rn(a, 1.f)), 0x1p-17f);
-        hi += __float_as_uint(a);
-        lo += __float_as_uint(b);
+        hi += __float_as_uint(a) - 0x3f800000u;
+        lo += __float_as_uint(b) - 0x37000000u;
     }
-    __device__ __forceinline__ unsigned long long take(uint32_t count) {
-        const uint32_t h = hi - count * 0x3f800000u, l = lo - count * 0x37000000u;
-        hi = lo = 0;
-        return ((unsigned long long)h << 17) + l;
+    __device__ __forceinline__ unsigned long long mine() const { return ((unsigned long long)hi << 17) + lo; }
+    __device__ __forceinline__ unsigned long long of_warp() const {
+        return ((unsigned long long)__reduce_add_sync(0xffffffffu, hi) << 17) + __reduce_add_sync(0xffffffffu, lo);
     }
 };
 
@@ -70,22 +75,30 @@ __device__ __forceinline__ float weight_of(const Row &r, float l) {
 }
 __device__ __forceinline__ float excess_of(float w, float C, float q) { return fmaxf(__fsub_rn(w, __fmul_rn(C, q)), 0.f); }
 
-struct Found {  // a maximum and its lowest index
+struct Found {  // a maximum, its lowest index, and (to fp32) the sum of the weights relative to it
     float top;
     int best;
+    float sum;
 };
 __device__ __forceinline__ Found better(Found a, Found b) {
     return b.top > a.top || (b.top == a.top && (uint32_t)b.best < (uint32_t)a.best) ? b : a;
+}
+// The same with the sums, which are NaN where a logit is NaN or +inf.
+__device__ __forceinline__ Found merged(Found a, Found b, float scale) {
+    Found f = better(a, b);
+    const float lower = fminf(a.top, b.top), part = b.top > a.top ? a.sum : b.sum, rest = b.top > a.top ? b.sum : a.sum;
+    f.sum = lower > -INFINITY ? fmaf(part, exp2_of((lower - f.top) * scale), rest) : rest;
+    return f;
 }
 
 struct Shared {
     TreeShared tree;
     unsigned long long child[kMaxNodes];            // children of each node
-    int token[kMaxNodes];                           // of the visited node's children, in order
-    float u[kMaxNodes], logit[kMaxNodes], q[kMaxNodes];
+    int token[kMaxNodes];                           // each node's token, or -1 for one outside the vocabulary
+    float u[kMaxNodes], logit[kMaxNodes], q[kMaxNodes];  // its number, and its parent's logit and q for its token
     int removed[kMaxNodes];                         // tokens rejected at the visited node, when there is no q
     unsigned long long removed_w[kMaxNodes];
-    unsigned long long part[64];
+    unsigned long long part[kRuns];                 // the exact sums of the CTA's runs (of a part that is kept)
     unsigned long long warp_sum[kWarps];
     Found warp_max[kWarps];
     Found cta_max[2][kMaxCluster];                  // exchanged: two places, taken in turn
@@ -93,17 +106,10 @@ struct Shared {
     unsigned long long sum_w[kMaxCluster], sum_r[kMaxCluster];
 };
 
-__device__ __forceinline__ unsigned long long warp_sum(unsigned long long x) {
-#pragma unroll
-    for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    return x;
-}
-
-// Every thread gets the CTAs' sums of x in sums[] (shared memory) and their total.
+// Every thread gets the CTAs' sums in sums[] (shared memory) and their total; x is the warp's sum (in lane 0).
 __device__ __forceinline__ unsigned long long cluster_sum(Shared &sh, cg::cluster_group &cluster, int &turn, int size,
                                                           unsigned long long x, unsigned long long *sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    x = warp_sum(x);
     if (lane == 0) sh.warp_sum[warp] = x;
     __syncthreads();
     turn ^= 1;
@@ -120,23 +126,28 @@ __device__ __forceinline__ unsigned long long cluster_sum(Shared &sh, cg::cluste
     return total;
 }
 
-__device__ __forceinline__ Found cluster_max(Shared &sh, cg::cluster_group &cluster, int &turn, int size, Found f) {
+// f.top and f.best are the thread's, f.sum the thread's relative to its warp's maximum (which f.top has become).
+__device__ __forceinline__ Found cluster_max(Shared &sh, cg::cluster_group &cluster, int &turn, int size, float scale,
+                                             Found f) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int off = 16; off; off >>= 1)
-        f = better(f, Found{__shfl_xor_sync(0xffffffffu, f.top, off), __shfl_xor_sync(0xffffffffu, f.best, off)});
+    for (int off = 16; off; off >>= 1) {
+        const float other = __shfl_xor_sync(0xffffffffu, f.sum, off);
+        f = better(f, Found{__shfl_xor_sync(0xffffffffu, f.top, off), __shfl_xor_sync(0xffffffffu, f.best, off), f.sum});
+        f.sum += other;
+    }
     if (lane == 0) sh.warp_max[warp] = f;
     __syncthreads();
     turn ^= 1;
     if (threadIdx.x < size) {
         Found a = sh.warp_max[0];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) a = better(a, sh.warp_max[w]);
+        for (int w = 1; w < kWarps; ++w) a = merged(a, sh.warp_max[w], scale);
         cluster.map_shared_rank(&sh, threadIdx.x)->cta_max[turn][cluster.block_rank()] = a;
     }
     cluster.sync();
     Found a = sh.cta_max[turn][0];
-    for (int r = 1; r < size; ++r) a = better(a, sh.cta_max[turn][r]);
+    for (int r = 1; r < size; ++r) a = merged(a, sh.cta_max[turn][r], scale);
     return a;
 }
 
@@ -169,6 +180,16 @@ struct Part {
             else kept[v - v0] = load(v);
         }
     }
+    // Asks L2 for the part of another row (its 128-byte lines).
+    __device__ __forceinline__ void ask(const Tin *other) const {
+        const char *first = reinterpret_cast<const char *>(other) + (size_t)max(0, v0 * kVec - lead) * sizeof(Tin);
+        const char *end = reinterpret_cast<const char *>(other) + (size_t)min(V, v1 * kVec - lead) * sizeof(Tin);
+        for (const char *at = first + threadIdx.x * 128; at < end; at += kThreads * 128) tc::prefetch_l2(at);
+    }
+    __device__ __forceinline__ void ask_q(const float *q) const {
+        for (int i = max(0, v0 * kVec - lead) + threadIdx.x * 32; i < min(V, v1 * kVec - lead); i += kThreads * 32)
+            tc::prefetch_l2(q + i);
+    }
     __device__ __forceinline__ void get(int v, float (&l)[kVec]) const {
         const uint4 x = kept ? kept[v - v0] : load(v);
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -180,6 +201,17 @@ struct Part {
                 l[2 * e] = __uint_as_float(w[e] << 16);
                 l[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
             }
+        }
+    }
+    // The largest of a vector's logits (of NaN and a number, the number).
+    __device__ __forceinline__ float top(int v) const {
+        const uint4 x = kept ? kept[v - v0] : load(v);
+        if constexpr (sizeof(Tin) == 4) {
+            return fmaxf(fmaxf(__uint_as_float(x.x), __uint_as_float(x.y)), fmaxf(__uint_as_float(x.z), __uint_as_float(x.w)));
+        } else {
+            const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&x);
+            const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+            return fmaxf(__bfloat162float(m.x), __bfloat162float(m.y));
         }
     }
     __device__ __forceinline__ void get_q(const float *q, int v, float (&x)[kVec]) const {
@@ -198,6 +230,17 @@ struct Part {
     }
 };
 
+// The sum of the lanes up to this one.
+__device__ __forceinline__ unsigned long long scan(unsigned long long x) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+    }
+    return x;
+}
+
 struct Args {
     const void *logits;
     const float *probs;
@@ -209,30 +252,64 @@ struct Args {
 };
 
 template <typename Tin>
-__global__ void __launch_bounds__(kThreads) draft_verify_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p) {
     using P = Part<Tin>;
+    constexpr int kBatch = 16 / P::kVec;
     extern __shared__ uint4 kept[];
     __shared__ Shared sh;
     cg::cluster_group cluster = cg::this_cluster();
     const int size = cluster.num_blocks(), rank = cluster.block_rank();
     const int n = blockIdx.x / size, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const Tree t = read_tree(sh.tree, p.parent, p.cu, n, p.total_nodes, min(p.path_stride, kMaxNodes), false);
     const bool writer = rank == 0 && tid == 0;
+    Row r{};
+    P part{};
+    part.V = p.V;
+    part.kept = p.part_bytes ? kept : nullptr;
+    int each = 0;
+    auto place = [&](int row) {  // this CTA's part of a row
+        part.row = reinterpret_cast<const Tin *>(p.logits) + (size_t)row * p.V;
+        part.lead = (int)((reinterpret_cast<uintptr_t>(part.row) & 15u) / sizeof(Tin));
+        const int vectors = (part.lead + p.V + P::kVec - 1) / P::kVec;
+        each = (vectors + size - 1) / size;
+        part.v0 = min(vectors, rank * each);
+        part.v1 = min(vectors, part.v0 + each);
+    };
+    const Tree root = tree_rows(p.cu, n, p.total_nodes, min(p.path_stride, kMaxNodes));
+    if (root.nodes > 0) {  // its row is on its way before the tree has been read
+        place(root.row0);
+        part.fetch();
+    }
+    cluster.barrier_arrive();  // (awaited before the first write to another CTA)
+    // the nodes' tokens and numbers, a thread each
+    const int mine = tid - (kThreads - kMaxNodes);
+    int token = -1;
+    float number = 0.f;
+    if (mine > 0 && mine < root.nodes) {
+        token = p.tokens[root.row0 + mine];
+        number = p.u[root.row0 + mine];
+    }
+    const Tree t = read_tree(sh.tree, p.parent, p.cu, n, p.total_nodes, min(p.path_stride, kMaxNodes), false);
     if (t.nodes < 0 && writer) report_invalid(p.status);
     if (tid < t.nodes) {
         unsigned long long mask = 0;
         for (int j = tid + 1; j < t.nodes; ++j) mask |= (unsigned long long)(sh.tree.parent[j] == tid) << j;
         sh.child[tid] = mask;
+    } else if (mine > 0 && mine < t.nodes) {
+        const size_t at = (size_t)(t.row0 + sh.tree.parent[mine]) * p.V + token;
+        const bool in = token >= 0 && token < p.V;
+        sh.token[mine] = in ? token : -1;
+        sh.u[mine] = number;
+        sh.logit[mine] = in ? to_f32(reinterpret_cast<const Tin *>(p.logits)[at]) : 0.f;
+        sh.q[mine] = p.probs && in ? p.probs[at] : 1.f;
     }
-    __syncthreads();
+    cluster.barrier_wait();
     int len = 0, next = -1, turn = 0;
     int owner = -1;  // the CTA that finds the next token in its part of the row; none: `next` is it
-    Row r{};
-    P part{};
     const float *q = nullptr;
     float C = 0.f;
     int removed = 0;
     unsigned long long at = 0;
+    bool runs_known = false;  // sh.part holds the sums of the runs of r
     if (t.nodes > 0) {
         const float temp = p.temperature ? p.temperature[n] : 1.f;
         r.onehot = !(temp > 0.f);
@@ -241,69 +318,101 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const Args p) {
         for (;;) {
             if (writer) p.path[(size_t)n * p.path_stride + len] = node;
             ++len;
-            part.row = reinterpret_cast<const Tin *>(p.logits) + (size_t)(t.row0 + node) * p.V;
-            part.lead = (int)((reinterpret_cast<uintptr_t>(part.row) & 15u) / sizeof(Tin));
-            part.V = p.V;
-            part.kept = p.part_bytes ? kept : nullptr;
-            const int vectors = (part.lead + p.V + P::kVec - 1) / P::kVec, each = (vectors + size - 1) / size;
-            part.v0 = min(vectors, rank * each);
-            part.v1 = min(vectors, part.v0 + each);
+            if (node > 0) {
+                place(t.row0 + node);
+                part.fetch();
+            }
             q = p.probs ? p.probs + (size_t)(t.row0 + node) * p.V : nullptr;
             C = 0.f;
             removed = 0;
-            part.fetch();
-            const unsigned long long children = sh.child[node];
-            if (warp == 0)  // what the children's trials need
-                for (int j = lane; j < kMaxNodes; j += 32)
-                    if ((children >> j) & 1) {
-                        const int token = p.tokens[t.row0 + j], c = __popcll(children & ((1ull << j) - 1));
-                        const bool in = token >= 0 && token < p.V;
-                        sh.token[c] = in ? token : -1;
-                        sh.u[c] = p.u[t.row0 + j];
-                        sh.logit[c] = in ? to_f32(part.row[token]) : 0.f;
-                        sh.q[c] = q && in ? q[token] : 1.f;
-                    }
             tc::cp_async_wait_all();
             __syncthreads();
-            Found f{-INFINITY, -1};
+            const unsigned long long children = sh.child[node];
+            const int trials = __popcll(children), first = __ffsll((long long)children) - 1;
+            if (trials) part.ask(part.row + (ptrdiff_t)(first - node) * p.V);
+            Found f{-INFINITY, -1, 0.f};
             for (int v = part.v0 + tid; v < part.v1; v += kThreads) {
-                float l[P::kVec];
-                part.get(v, l);
                 if (r.onehot) {
+                    float l[P::kVec];
+                    part.get(v, l);
 #pragma unroll
                     for (int e = 0; e < P::kVec; ++e)
-                        if (l[e] > f.top) f = Found{l[e], v * P::kVec - part.lead + e};
+                        if (l[e] > f.top) f = Found{l[e], v * P::kVec - part.lead + e, 0.f};
                 } else {
-#pragma unroll
-                    for (int e = 0; e < P::kVec; ++e) f.top = fmaxf(f.top, l[e]);  // of NaN and a number, the number
+                    f.top = fmaxf(f.top, part.top(v));
                 }
             }
-            if (!r.onehot && f.top > -INFINITY) f.best = 0;  // only `onehot` uses the place
-            f = cluster_max(sh, cluster, turn, size, f);
+            if (!r.onehot) {
+                if (f.top > -INFINITY) f.best = 0;  // only `onehot` uses the place
+#pragma unroll
+                for (int off = 16; off; off >>= 1) f.top = fmaxf(f.top, __shfl_xor_sync(0xffffffffu, f.top, off));
+                if (trials && f.top > -INFINITY) {
+                    for (int v = part.v0 + tid; v < part.v1; v += kThreads) {
+                        float l[P::kVec];
+                        part.get(v, l);
+#pragma unroll
+                        for (int e = 0; e < P::kVec; ++e) f.sum += exp2_of((l[e] - f.top) * r.scale);
+                    }
+                }
+            }
+            f = cluster_max(sh, cluster, turn, size, r.scale, f);
             r.top = f.top;
             r.best = f.best;
             r.flat = f.top == INFINITY;
             if (r.best < 0) break;  // no weight anywhere
+            if (trials && !r.onehot && sh.token[first] >= 0) {
+                const float w = exp2f(__fmul_rn(__fsub_rn(sh.logit[first], r.top), r.scale));
+                if (sh.u[first] * sh.q[first] * f.sum < w * (1.f - kMargin)) {  // never where the sum is NaN
+                    node = first;
+                    __syncthreads();  // the row's part is free
+                    continue;
+                }
+            }
+            // The exact sum of r over the CTA's part, its runs' sums kept in sh.part; batches of kBatch vectors, so
+            // that as many reads of q are under way at once.
+            auto exact = [&](bool with_q) {
+                unsigned long long sum = 0;
+                for (int v = part.v0 + warp * 32; v < part.v1; v += kBatch * kThreads) {
+                    float x[kBatch][P::kVec];
+                    if (with_q) {
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i)
+                            if (v + i * kThreads + lane < part.v1) part.get_q(q, v + i * kThreads + lane, x[i]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int at = v + i * kThreads;
+                        FixedSum f;
+                        if (at + lane < part.v1) {
+                            float l[P::kVec];
+                            part.get(at + lane, l);
+#pragma unroll
+                            for (int e = 0; e < P::kVec; ++e) {
+                                const float w = weight_of(r, l[e]);
+                                f.add(with_q ? excess_of(w, C, x[i][e]) : w);
+                            }
+                        }
+                        if (at < part.v1) {
+                            const unsigned long long run = f.of_warp();
+                            sum += run;
+                            if (lane == 0 && part.kept) sh.part[(at - part.v0) >> 5] = run;
+                        }
+                    }
+                }
+                return sum;
+            };
             unsigned long long Z = 1ull << 40;
             if (!r.onehot) {
-                unsigned long long mine = 0;
-                for (int v = part.v0 + tid; v < part.v1;) {
-                    FixedSum sum;
-                    int count = 0;
-                    for (; v < part.v1 && count < kFlush; v += kThreads, count += P::kVec) {
-                        float l[P::kVec];
-                        part.get(v, l);
-#pragma unroll
-                        for (int e = 0; e < P::kVec; ++e) sum.add(weight_of(r, l[e]));
-                    }
-                    mine += sum.take(count);
-                }
-                Z = cluster_sum(sh, cluster, turn, size, mine, sh.sum_w);
+                if (q && trials) part.ask_q(q);
+                Z = cluster_sum(sh, cluster, turn, size, exact(false), sh.sum_w);
             }
             unsigned long long s = Z, *sums = sh.sum_w;
-            const int trials = __popcll(children);
+            runs_known = part.kept != nullptr;
             int accepted = -1;
-            for (int c = 0; c < trials && accepted < 0; ++c) {
+            unsigned long long untried = children;
+            while (untried && accepted < 0) {
+                const int c = __ffsll((long long)untried) - 1;
+                untried &= untried - 1;
                 const int token = sh.token[c];
                 if (token < 0) {
                     if (writer) report_invalid(p.status);
@@ -317,9 +426,7 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const Args p) {
                 if (q && C > 0.f) rest = excess_of(w, C, qc);
                 for (int i = 0; i < removed; ++i) rest = sh.removed[i] == token ? 0.f : rest;
                 if (__fmul_rn(__fmul_rn(sh.u[c], qc), sf) < rest) {
-                    unsigned long long m = children;
-                    for (int i = 0; i < c; ++i) m &= m - 1;
-                    accepted = __ffsll((long long)m) - 1;
+                    accepted = c;
                 } else if (!q) {
                     const unsigned long long cut = fixed40(rest);
                     s -= cut;
@@ -335,33 +442,21 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const Args p) {
                     if (r.onehot) {
                         s = fixed40(excess_of(1.f, C, q[r.best]));
                     } else {
-                        unsigned long long mine = 0;
-                        for (int v = part.v0 + tid; v < part.v1;) {
-                            FixedSum sum;
-                            int count = 0;
-                            for (; v < part.v1 && count < kFlush; v += kThreads, count += P::kVec) {
-                                float l[P::kVec], x[P::kVec];
-                                part.get_q(q, v, x);
-                                part.get(v, l);
-#pragma unroll
-                                for (int e = 0; e < P::kVec; ++e) sum.add(excess_of(weight_of(r, l[e]), C, x[e]));
-                            }
-                            mine += sum.take(count);
-                        }
-                        s = cluster_sum(sh, cluster, turn, size, mine, sh.sum_r);
+                        s = cluster_sum(sh, cluster, turn, size, exact(true), sh.sum_r);
                         sums = sh.sum_r;
                     }
                 }
             }
             if (accepted >= 0) {
                 node = accepted;
-                __syncthreads();  // the row's part and the children's values are free
+                __syncthreads();  // the row's part is free
                 continue;
             }
             if (s == 0) {  // nothing is left of the target: its own distribution
                 s = Z;
                 C = 0.f;
                 removed = 0;
+                runs_known &= sums == sh.sum_w;
                 sums = sh.sum_w;
             }
             if (r.onehot) {  // all that is left is at one place, unless that was removed
@@ -385,7 +480,6 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const Args p) {
         }
     }
     if (owner == rank) {
-        // 64 runs of 32 vectors at a time: their sums, then the run, the vector and the logit that pass `at`
         auto rest = [&](int v, float (&x)[P::kVec]) {
             float l[P::kVec];
             part.get(v, l);
@@ -403,64 +497,92 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const Args p) {
                 }
             }
         };
-        bool search = true;
-        for (int v0 = part.v0; v0 < part.v1 && search; v0 += 64 * 32) {
-            for (int run = warp; run < 64; run += kWarps) {
-                const int v = v0 + run * 32 + lane;
-                FixedSum sum;
-                if (v < part.v1) {
-                    float x[P::kVec];
-                    rest(v, x);
-#pragma unroll
-                    for (int e = 0; e < P::kVec; ++e) sum.add(x[e]);
-                }
-                const unsigned long long total = warp_sum(v < part.v1 ? sum.take(P::kVec) : 0ull);
-                if (lane == 0) sh.part[run] = total;
-            }
-            __syncthreads();
-            int run = 0;
-            for (; run < 64 && at >= sh.part[run]; ++run) at -= sh.part[run];
-            if (run < 64) {
-                search = false;
-                if (warp == 0) {
+        // The run, the vector and the logit that pass `at`.  A part that is not kept is searched kRuns runs at a time.
+        for (int v0 = part.v0; v0 < part.v1; v0 += kRuns * 32) {
+            if (!runs_known) {
+                __syncthreads();
+                for (int run = warp; run < kRuns; run += kWarps) {
                     const int v = v0 + run * 32 + lane;
-                    float x[P::kVec];
-                    unsigned long long mine = 0;
+                    FixedSum sum;
                     if (v < part.v1) {
+                        float x[P::kVec];
                         rest(v, x);
-                        FixedSum sum;
 #pragma unroll
                         for (int e = 0; e < P::kVec; ++e) sum.add(x[e]);
-                        mine = sum.take(P::kVec);
                     }
-                    unsigned long long upto = mine;
-#pragma unroll
-                    for (int off = 1; off < 32; off <<= 1) {
-                        const unsigned long long y = __shfl_up_sync(0xffffffffu, upto, off);
-                        if (lane >= off) upto += y;
+                    const unsigned long long total = sum.of_warp();
+                    if (lane == 0) sh.part[run] = total;
+                }
+                __syncthreads();
+            } else if (removed) {
+                if (tid == 0)
+                    for (int i = 0; i < removed; ++i) {
+                        const int v = (sh.removed[i] + part.lead) / P::kVec;
+                        if (v >= part.v0 && v < part.v1) sh.part[(v - part.v0) >> 5] -= sh.removed_w[i];
                     }
-                    if (upto - mine <= at && at < upto) {
-                        unsigned long long left = at - (upto - mine);
-                        int found = 0;
+                __syncthreads();
+            }
+            // every warp finds the run (kRuns / 32 entries a lane), the first goes on to the logit
+            constexpr int kEach = kRuns / 32;
+            unsigned long long own[kEach], sum = 0;
 #pragma unroll
-                        for (int e = P::kVec - 1; e >= 0; --e) {  // the last logit that starts at or below `left`
-                            unsigned long long start = 0;
+            for (int i = 0; i < kEach; ++i) {
+                const int run = lane * kEach + i;
+                own[i] = v0 + run * 32 < part.v1 ? sh.part[run] : 0ull;
+                sum += own[i];
+            }
+            unsigned long long upto = scan(sum);
+            const uint32_t here = __ballot_sync(0xffffffffu, at < upto);
+            if (!here) {
+                at -= __shfl_sync(0xffffffffu, upto, 31);
+                continue;
+            }
+            const int who = __ffs((int)here) - 1;
+            int run = lane * kEach;
+            unsigned long long left = at - (upto - sum);
 #pragma unroll
-                            for (int d = 0; d < P::kVec; ++d) start += d < e ? fixed40(x[d]) : 0ull;
-                            if (start <= left && left < start + fixed40(x[e])) found = e;
+            for (int i = 0; i < kEach - 1; ++i)
+                if (run == lane * kEach + i && left >= own[i]) {
+                    left -= own[i];
+                    ++run;
+                }
+            run = __shfl_sync(0xffffffffu, run, who);
+            left = __shfl_sync(0xffffffffu, left, who);
+            if (warp == 0) {
+                const int v = v0 + run * 32 + lane;
+                float x[P::kVec];
+                FixedSum f;
+                if (v < part.v1) {
+                    rest(v, x);
+#pragma unroll
+                    for (int e = 0; e < P::kVec; ++e) f.add(x[e]);
+                }
+                upto = scan(f.mine());
+                if (left < upto && left >= upto - f.mine()) {
+                    left -= upto - f.mine();
+                    int found = 0;
+                    bool passed = false;
+#pragma unroll
+                    for (int e = 0; e < P::kVec; ++e) {
+                        const unsigned long long w = fixed40(x[e]);
+                        if (!passed && left < w) {
+                            passed = true;
+                            found = e;
                         }
-                        p.next_token[n] = v * P::kVec - part.lead + found;
+                        left -= passed ? 0ull : w;
                     }
+                    p.next_token[n] = v * P::kVec - part.lead + found;
                 }
             }
-            __syncthreads();
+            break;
         }
     } else if (writer && owner < 0) {
         p.next_token[n] = next;
     }
+    tc::cp_async_wait_all();  // (a root's row that was fetched for a tree that is not one)
     for (int i = len + tid; i < p.path_stride && rank == 0; i += kThreads) p.path[(size_t)n * p.path_stride + i] = -1;
     if (writer) p.path_len[n] = len;
-    cluster.sync();  // no CTA leaves while another may still write to its shared memory
+    // (the last exchange is behind every CTA: none writes to another's shared memory any more)
 }
 
 template <typename Tin>
