@@ -38,16 +38,24 @@ constexpr float kMargin = 1e-4f;
 
 __device__ __forceinline__ unsigned long long fixed40(float x) { return __float2ull_rz(x * kFixed); }
 
+// Arithmetic on pairs, one instruction each.
+#define KDA_PAIR_OP(name, instr)                                                                                __device__ __forceinline__ float2 name(float2 a, float2 b) {                                                    float2 d;                                                                                                   asm("{\n.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\n" instr " z, x, y;\n"              "mov.b64 {%0, %1}, z;\n}\n"                                                                               : "=f"(d.x), "=f"(d.y)                                                                                      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));                                                              return d;                                                                                               }
+KDA_PAIR_OP(add2, "add.rn.f32x2")
+KDA_PAIR_OP(add_rz2, "add.rz.f32x2")
+KDA_PAIR_OP(sub2, "sub.rn.f32x2")
+KDA_PAIR_OP(mul2, "mul.rn.f32x2")
+#undef KDA_PAIR_OP
+
 // A sum of at most 8 values in [0, 1] cut to multiples of 2^-40, without 64-bit conversions: adding 1 with rounding
 // towards zero leaves the first 23 bits of the value in the sum's mantissa, adding 2^-17 to the rest the next 17;
 // the bit patterns add up as integers, and so do 32 lanes' (8 x 32 x 2^23 fits 32 bits).
 struct FixedSum {
     uint32_t hi = 0, lo = 0;
-    __device__ __forceinline__ void add(float x) {
-        const float a = __fadd_rz(x, 1.f);
-        const float b = __fadd_rz(__fsub_rn(x, __fsub_rn(a, 1.f)), 0x1p-17f);
-        hi += __float_as_uint(a) - 0x3f800000u;
-        lo += __float_as_uint(b) - 0x37000000u;
+    __device__ __forceinline__ void add2(float2 x) {
+        const float2 a = add_rz2(x, make_float2(1.f, 1.f));
+        const float2 b = add_rz2(sub2(x, sub2(a, make_float2(1.f, 1.f))), make_float2(0x1p-17f, 0x1p-17f));
+        hi += __float_as_uint(a.x) + __float_as_uint(a.y) - 2 * 0x3f800000u;
+        lo += __float_as_uint(b.x) + __float_as_uint(b.y) - 2 * 0x37000000u;
     }
     __device__ __forceinline__ unsigned long long mine() const { return ((unsigned long long)hi << 17) + lo; }
     __device__ __forceinline__ unsigned long long of_warp() const {
@@ -74,21 +82,35 @@ __device__ __forceinline__ float weight_of(const Row &r, float l) {
     return fmaxf(exp2_of(__fmul_rn(__fsub_rn(l, r.top), r.scale)), 0.f);
 }
 __device__ __forceinline__ float excess_of(float w, float C, float q) { return fmaxf(__fsub_rn(w, __fmul_rn(C, q)), 0.f); }
+// Pairs of the same.  `plain`: the row has neither a NaN nor a +inf logit.
+__device__ __forceinline__ float2 weights_of(const Row &r, bool plain, float2 l) {
+    if (!plain) return make_float2(weight_of(r, l.x), weight_of(r, l.y));
+    const float2 x = mul2(sub2(l, make_float2(r.top, r.top)), make_float2(r.scale, r.scale));
+    return make_float2(exp2_of(x.x), exp2_of(x.y));
+}
+__device__ __forceinline__ float2 excesses_of(float2 w, float C, float2 q) {
+    const float2 x = sub2(w, mul2(make_float2(C, C), q));
+    return make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f));
+}
 
-struct Found {  // a maximum, its lowest index, and (to fp32) the sum of the weights relative to it
+struct __align__(16) Found {  // a maximum, its lowest index, and (to fp32) the sum of the weights relative to it
     float top;
     int best;
     float sum;
+    float unused;
 };
 __device__ __forceinline__ Found better(Found a, Found b) {
     return b.top > a.top || (b.top == a.top && (uint32_t)b.best < (uint32_t)a.best) ? b : a;
 }
-// The same with the sums, which are NaN where a logit is NaN or +inf.
-__device__ __forceinline__ Found merged(Found a, Found b, float scale) {
-    Found f = better(a, b);
-    const float lower = fminf(a.top, b.top), part = b.top > a.top ? a.sum : b.sum, rest = b.top > a.top ? b.sum : a.sum;
-    f.sum = lower > -INFINITY ? fmaf(part, exp2_of((lower - f.top) * scale), rest) : rest;
-    return f;
+// The same over the entries of the first `n` lanes (n a power of two, the answer in those lanes), with the sums,
+// which become NaN where a logit is NaN or +inf.
+__device__ __forceinline__ Found merged(Found f, int n, float scale) {
+    Found a = f;
+    for (int off = n >> 1; off; off >>= 1)
+        a = better(a, Found{__shfl_xor_sync(0xffffffffu, a.top, off), __shfl_xor_sync(0xffffffffu, a.best, off), 0.f, 0.f});
+    a.sum = f.top > -INFINITY ? f.sum * exp2_of((f.top - a.top) * scale) : 0.f;
+    for (int off = n >> 1; off; off >>= 1) a.sum += __shfl_xor_sync(0xffffffffu, a.sum, off);
+    return a;
 }
 
 struct Shared {
@@ -96,59 +118,75 @@ struct Shared {
     unsigned long long child[kMaxNodes];            // children of each node
     int token[kMaxNodes];                           // each node's token, or -1 for one outside the vocabulary
     float u[kMaxNodes], logit[kMaxNodes], q[kMaxNodes];  // its number, and its parent's logit and q for its token
+    int path[kMaxNodes];                            // the nodes visited
     int removed[kMaxNodes];                         // tokens rejected at the visited node, when there is no q
     unsigned long long removed_w[kMaxNodes];
     unsigned long long part[kRuns];                 // the exact sums of the CTA's runs (of a part that is kept)
     unsigned long long warp_sum[kWarps];
     Found warp_max[kWarps];
-    Found cta_max[2][kMaxCluster];                  // exchanged: two places, taken in turn
+    Found cta_max[2][kMaxCluster];                  // exchanged: two places, taken in turn, each with its barrier
     unsigned long long cta_sum[2][kMaxCluster];
+    uint64_t bar[2];
     unsigned long long sum_w[kMaxCluster], sum_r[kMaxCluster];
 };
 
+// An exchange between the cluster's CTAs: each sends its value to every other's place for it, and goes on once its
+// own places are filled.  Two sets of places are enough: a CTA sends for exchange e + 2 only with all values of
+// e + 1 in hand, whose senders had read theirs of e.
+struct Exchange {
+    int count = 0, size = 1, rank = 0;
+    bool ok = true;  // every wait so far was met (the same in all threads of the CTA)
+    __device__ __forceinline__ int turn() const { return count & 1; }
+    __device__ __forceinline__ void expect(Shared &sh, uint32_t bytes) const {
+        if (threadIdx.x == 0) tc::mbar_arrive_expect_tx(&sh.bar[turn()], bytes * size);
+    }
+    __device__ __forceinline__ void wait(Shared &sh) {
+        ok = __syncthreads_and(ok && tc::mbar_wait(&sh.bar[turn()], (count >> 1) & 1));
+        ++count;
+    }
+};
+
 // Every thread gets the CTAs' sums in sums[] (shared memory) and their total; x is the warp's sum (in lane 0).
-__device__ __forceinline__ unsigned long long cluster_sum(Shared &sh, cg::cluster_group &cluster, int &turn, int size,
-                                                          unsigned long long x, unsigned long long *sums) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ unsigned long long cluster_sum(Shared &sh, Exchange &ex, unsigned long long x,
+                                                          unsigned long long *sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, turn = ex.turn();
     if (lane == 0) sh.warp_sum[warp] = x;
+    ex.expect(sh, 8);
     __syncthreads();
-    turn ^= 1;
-    if (threadIdx.x < size) {
+    if (threadIdx.x < ex.size) {
         unsigned long long total = 0;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) total += sh.warp_sum[w];
-        cluster.map_shared_rank(&sh, threadIdx.x)->cta_sum[turn][cluster.block_rank()] = total;
+        tc::st_async_b64(tc::map_to_cta(&sh.cta_sum[turn][ex.rank], threadIdx.x), total,
+                         tc::map_to_cta(&sh.bar[turn], threadIdx.x));
     }
-    cluster.sync();
+    ex.wait(sh);
     unsigned long long total = 0;
-    for (int r = 0; r < size; ++r) total += sh.cta_sum[turn][r];
-    if (threadIdx.x < size) sums[threadIdx.x] = sh.cta_sum[turn][threadIdx.x];
+    for (int r = 0; r < ex.size; ++r) total += sh.cta_sum[turn][r];
+    if (threadIdx.x < ex.size) sums[threadIdx.x] = sh.cta_sum[turn][threadIdx.x];
     return total;
 }
 
 // f.top and f.best are the thread's, f.sum the thread's relative to its warp's maximum (which f.top has become).
-__device__ __forceinline__ Found cluster_max(Shared &sh, cg::cluster_group &cluster, int &turn, int size, float scale,
-                                             Found f) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ Found cluster_max(Shared &sh, Exchange &ex, float scale, Found f) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, turn = ex.turn();
 #pragma unroll
     for (int off = 16; off; off >>= 1) {
         const float other = __shfl_xor_sync(0xffffffffu, f.sum, off);
-        f = better(f, Found{__shfl_xor_sync(0xffffffffu, f.top, off), __shfl_xor_sync(0xffffffffu, f.best, off), f.sum});
+        f = better(f, Found{__shfl_xor_sync(0xffffffffu, f.top, off), __shfl_xor_sync(0xffffffffu, f.best, off), f.sum, 0.f});
         f.sum += other;
     }
     if (lane == 0) sh.warp_max[warp] = f;
+    ex.expect(sh, 16);
     __syncthreads();
-    turn ^= 1;
-    if (threadIdx.x < size) {
-        Found a = sh.warp_max[0];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) a = merged(a, sh.warp_max[w], scale);
-        cluster.map_shared_rank(&sh, threadIdx.x)->cta_max[turn][cluster.block_rank()] = a;
+    if (warp == 0) {
+        const Found a = merged(sh.warp_max[lane % kWarps], kWarps, scale);
+        if (lane < ex.size)
+            tc::st_async_b32x4(tc::map_to_cta(&sh.cta_max[turn][ex.rank], lane), __float_as_uint(a.top), (uint32_t)a.best,
+                               __float_as_uint(a.sum), 0u, tc::map_to_cta(&sh.bar[turn], lane));
     }
-    cluster.sync();
-    Found a = sh.cta_max[turn][0];
-    for (int r = 1; r < size; ++r) a = merged(a, sh.cta_max[turn][r], scale);
-    return a;
+    ex.wait(sh);
+    return merged(sh.cta_max[turn][lane & (ex.size - 1)], ex.size, scale);
 }
 
 // A CTA's part of one row.  The row is cut at 16-byte boundaries of memory into vectors of `kVec` logits, of which
@@ -279,6 +317,11 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
         place(root.row0);
         part.fetch();
     }
+    if (tid == 0) {
+        tc::mbar_init(&sh.bar[0], 1);
+        tc::mbar_init(&sh.bar[1], 1);
+        tc::fence_mbar_init();
+    }
     cluster.barrier_arrive();  // (awaited before the first write to another CTA)
     // the nodes' tokens and numbers, a thread each
     const int mine = tid - (kThreads - kMaxNodes);
@@ -303,12 +346,16 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
         sh.q[mine] = p.probs && in ? p.probs[at] : 1.f;
     }
     cluster.barrier_wait();
-    int len = 0, next = -1, turn = 0;
+    int len = 0, next = -1;
+    Exchange ex;
+    ex.size = size;
+    ex.rank = rank;
     int owner = -1;  // the CTA that finds the next token in its part of the row; none: `next` is it
     const float *q = nullptr;
     float C = 0.f;
     int removed = 0;
     unsigned long long at = 0;
+    bool plain = false;       // the row has neither NaN nor +inf
     bool runs_known = false;  // sh.part holds the sums of the runs of r
     if (t.nodes > 0) {
         const float temp = p.temperature ? p.temperature[n] : 1.f;
@@ -316,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
         r.scale = r.onehot ? 0.f : 1.4426950408889634f / fmaxf(temp, 1e-30f);
         int node = 0;
         for (;;) {
-            if (writer) p.path[(size_t)n * p.path_stride + len] = node;
+            if (tid == 0) sh.path[len] = node;  // (written out at the end: an exchange would wait for the store)
             ++len;
             if (node > 0) {
                 place(t.row0 + node);
@@ -330,14 +377,14 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
             const unsigned long long children = sh.child[node];
             const int trials = __popcll(children), first = __ffsll((long long)children) - 1;
             if (trials) part.ask(part.row + (ptrdiff_t)(first - node) * p.V);
-            Found f{-INFINITY, -1, 0.f};
+            Found f{-INFINITY, -1, 0.f, 0.f};
             for (int v = part.v0 + tid; v < part.v1; v += kThreads) {
                 if (r.onehot) {
                     float l[P::kVec];
                     part.get(v, l);
 #pragma unroll
                     for (int e = 0; e < P::kVec; ++e)
-                        if (l[e] > f.top) f = Found{l[e], v * P::kVec - part.lead + e, 0.f};
+                        if (l[e] > f.top) f = Found{l[e], v * P::kVec - part.lead + e, 0.f, 0.f};
                 } else {
                     f.top = fmaxf(f.top, part.top(v));
                 }
@@ -347,19 +394,25 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
 #pragma unroll
                 for (int off = 16; off; off >>= 1) f.top = fmaxf(f.top, __shfl_xor_sync(0xffffffffu, f.top, off));
                 if (trials && f.top > -INFINITY) {
+                    float2 sum = make_float2(0.f, 0.f);
+                    const Row warps{f.top, r.scale, 0, false, false};
+#pragma unroll 2
                     for (int v = part.v0 + tid; v < part.v1; v += kThreads) {
                         float l[P::kVec];
                         part.get(v, l);
 #pragma unroll
-                        for (int e = 0; e < P::kVec; ++e) f.sum += exp2_of((l[e] - f.top) * r.scale);
+                        for (int e = 0; e < P::kVec; e += 2)
+                            sum = add2(sum, weights_of(warps, true, make_float2(l[e], l[e + 1])));
                     }
+                    f.sum = sum.x + sum.y;
                 }
             }
-            f = cluster_max(sh, cluster, turn, size, r.scale, f);
+            f = cluster_max(sh, ex, r.scale, f);
             r.top = f.top;
             r.best = f.best;
             r.flat = f.top == INFINITY;
-            if (r.best < 0) break;  // no weight anywhere
+            plain = trials && f.sum < INFINITY;
+            if (r.best < 0 || !ex.ok) break;  // no weight anywhere
             if (trials && !r.onehot && sh.token[first] >= 0) {
                 const float w = exp2f(__fmul_rn(__fsub_rn(sh.logit[first], r.top), r.scale));
                 if (sh.u[first] * sh.q[first] * f.sum < w * (1.f - kMargin)) {  // never where the sum is NaN
@@ -387,9 +440,10 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
                             float l[P::kVec];
                             part.get(at + lane, l);
 #pragma unroll
-                            for (int e = 0; e < P::kVec; ++e) {
-                                const float w = weight_of(r, l[e]);
-                                f.add(with_q ? excess_of(w, C, x[i][e]) : w);
+                            for (int e = 0; e < P::kVec; e += 2) {
+                                float2 w = weights_of(r, plain, make_float2(l[e], l[e + 1]));
+                                if (with_q) w = excesses_of(w, C, make_float2(x[i][e], x[i][e + 1]));
+                                f.add2(w);
                             }
                         }
                         if (at < part.v1) {
@@ -404,8 +458,9 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
             unsigned long long Z = 1ull << 40;
             if (!r.onehot) {
                 if (q && trials) part.ask_q(q);
-                Z = cluster_sum(sh, cluster, turn, size, exact(false), sh.sum_w);
+                Z = cluster_sum(sh, ex, exact(false), sh.sum_w);
             }
+            if (!ex.ok) break;
             unsigned long long s = Z, *sums = sh.sum_w;
             runs_known = part.kept != nullptr;
             int accepted = -1;
@@ -442,11 +497,13 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
                     if (r.onehot) {
                         s = fixed40(excess_of(1.f, C, q[r.best]));
                     } else {
-                        s = cluster_sum(sh, cluster, turn, size, exact(true), sh.sum_r);
+                        s = cluster_sum(sh, ex, exact(true), sh.sum_r);
                         sums = sh.sum_r;
+                        if (!ex.ok) break;
                     }
                 }
             }
+            if (!ex.ok) break;
             if (accepted >= 0) {
                 node = accepted;
                 __syncthreads();  // the row's part is free
@@ -508,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
                         float x[P::kVec];
                         rest(v, x);
 #pragma unroll
-                        for (int e = 0; e < P::kVec; ++e) sum.add(x[e]);
+                        for (int e = 0; e < P::kVec; e += 2) sum.add2(make_float2(x[e], x[e + 1]));
                     }
                     const unsigned long long total = sum.of_warp();
                     if (lane == 0) sh.part[run] = total;
@@ -555,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
                 if (v < part.v1) {
                     rest(v, x);
 #pragma unroll
-                    for (int e = 0; e < P::kVec; ++e) f.add(x[e]);
+                    for (int e = 0; e < P::kVec; e += 2) f.add2(make_float2(x[e], x[e + 1]));
                 }
                 upto = scan(f.mine());
                 if (left < upto && left >= upto - f.mine()) {
@@ -579,10 +636,16 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
     } else if (writer && owner < 0) {
         p.next_token[n] = next;
     }
+    if (!ex.ok) {  // an exchange that never came: an empty path
+        len = 0;
+        if (writer && p.status) atomicCAS(p.status, 0, (int32_t)KDA_ERR_TIMEOUT);
+    }
     tc::cp_async_wait_all();  // (a root's row that was fetched for a tree that is not one)
-    for (int i = len + tid; i < p.path_stride && rank == 0; i += kThreads) p.path[(size_t)n * p.path_stride + i] = -1;
+    __syncthreads();
+    for (int i = tid; i < p.path_stride && rank == 0; i += kThreads)
+        p.path[(size_t)n * p.path_stride + i] = i < len ? sh.path[i] : -1;
     if (writer) p.path_len[n] = len;
-    // (the last exchange is behind every CTA: none writes to another's shared memory any more)
+    // (every CTA has all values of the last exchange: none writes to another's shared memory any more)
 }
 
 template <typename Tin>
