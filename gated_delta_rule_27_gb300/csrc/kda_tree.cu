@@ -320,8 +320,8 @@ cudaError_t launch_commit_t(const TreeCommitArgs &a, cudaStream_t st) {
 // ---------------------------------------------------------------------------
 // y_i[c] = sum_j w[c, j] x_{j-th ancestor of i}[c]; past the root the request's carried inputs follow, newest
 // first.  One CTA per (request, channel block); a thread owns VEC neighbouring channels, whose rows it reads as
-// 16 bytes (VEC = 8 of bf16, 4 of fp32; VEC = 1 where C or an address does not allow that).  A row is read once
-// from HBM and again, for the nodes below it, from L1.
+// 16 bytes (VEC = 8 of bf16, 4 of fp32; VEC = 1 where C or an address does not allow that).  All of the block's
+// rows are on their way to shared memory at once, each read once; a thread copies what it will use itself.
 constexpr int kConvThreads = 64;
 
 template <typename Tin, int VEC>
@@ -333,7 +333,7 @@ __device__ __forceinline__ void load_row(const Tin *p, float (&f)[VEC]) {
             uint4 v;
             Tin x[VEC];
         } r;
-        r.v = __ldg(reinterpret_cast<const uint4 *>(p));
+        r.v = *reinterpret_cast<const uint4 *>(p);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) f[e] = to_f32(r.x[e]);
     }
@@ -375,6 +375,19 @@ __device__ __forceinline__ void store_f32(float *p, const float (&f)[VEC]) {
     }
 }
 
+// One CTA's rows in shared memory: max_nodes of x, then the W - 1 carried ones (fp32).
+template <typename Tin, int VEC>
+constexpr size_t conv_row_bytes() { return (size_t)kConvThreads * VEC * sizeof(Tin); }
+
+template <typename Tin, int VEC>
+__device__ __forceinline__ void fetch_row(Tin *to, const Tin *from) {
+    if constexpr (VEC == 1) *to = *from;
+    else
+#pragma unroll
+        for (int e = 0; e < VEC * (int)sizeof(Tin); e += 16)
+            tc::cp_async16(reinterpret_cast<char *>(to) + e, reinterpret_cast<const char *>(from) + e);
+}
+
 template <typename Tin, int W, int VEC>
 __global__ void __launch_bounds__(kConvThreads)
 tree_conv_kernel(const Tin *__restrict__ x, const float *__restrict__ w, const int32_t *__restrict__ parent,
@@ -383,10 +396,19 @@ tree_conv_kernel(const Tin *__restrict__ x, const float *__restrict__ w, const i
                  int32_t *__restrict__ status) {
     __shared__ TreeShared ts;
     __shared__ int s_tap[kMaxNodes][W];  // the j-th input before node i: a node, or -1 - m for the m-th carried one
+    extern __shared__ uint4 rows[];
+    Tin *s_x = reinterpret_cast<Tin *>(rows) + threadIdx.x * VEC;
+    float *s_past = reinterpret_cast<float *>(reinterpret_cast<char *>(rows) + max_nodes * conv_row_bytes<Tin, VEC>()) + threadIdx.x * VEC;
+    constexpr int kStride = kConvThreads * VEC;
     const int n = blockIdx.y, tid = threadIdx.x, c = (blockIdx.x * kConvThreads + tid) * VEC;
     const int slot = slot_of(seq_idx, n, num_slots);
+    const Tree own = tree_rows(cu, n, total_nodes, max_nodes);
     float wt[W][VEC];
-    if (c < C) {
+    if (c < C && own.nodes > 0 && slot >= 0) {
+        for (int i = 0; i < own.nodes; ++i)
+            fetch_row<Tin, VEC>(s_x + i * kStride, x + (size_t)(own.row0 + i) * C + c);
+        for (int m = 0; m < W - 1; ++m)  // the newest first
+            fetch_row<float, VEC>(s_past + m * kStride, pool + ((size_t)slot * (W - 1) + (W - 2 - m)) * C + c);
         float all[W * VEC];
         if constexpr (VEC == 1) {
 #pragma unroll
@@ -402,6 +424,7 @@ tree_conv_kernel(const Tin *__restrict__ x, const float *__restrict__ w, const i
     const Tree t = read_tree(ts, parent, cu, n, total_nodes, max_nodes, false);
     if (t.nodes < 0 || slot < 0) {
         if (tid == 0) report_invalid(status);
+        tc::cp_async_wait_all();
         return;
     }
     for (int i = tid; i < t.nodes; i += kConvThreads) {
@@ -412,11 +435,10 @@ tree_conv_kernel(const Tin *__restrict__ x, const float *__restrict__ w, const i
             at = at >= 0 ? ts.parent[at] : -1;
         }
     }
+    tc::cp_async_wait_all();
     __syncthreads();
     if (c >= C) return;
-    const Tin *xs = x + (size_t)t.row0 * C + c;
-    const float *past = pool + ((ptrdiff_t)slot * (W - 1) + (W - 2)) * C + c;  // the newest carried input (W > 1)
-#pragma unroll 4
+#pragma unroll 2
     for (int i = 0; i < t.nodes; ++i) {
         float acc[VEC];
 #pragma unroll
@@ -425,8 +447,8 @@ tree_conv_kernel(const Tin *__restrict__ x, const float *__restrict__ w, const i
         for (int j = 0; j < W; ++j) {
             const int tap = s_tap[i][j];
             float v[VEC];
-            if (tap >= 0) load_row<Tin, VEC>(xs + (size_t)tap * C, v);
-            else load_f32<VEC>(past - (ptrdiff_t)(-1 - tap) * C, v);
+            if (tap >= 0) load_row<Tin, VEC>(s_x + tap * kStride, v);
+            else load_f32<VEC>(s_past + (-1 - tap) * kStride, v);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) acc[e] = fmaf(wt[j][e], v[e], acc[e]);
         }
@@ -485,12 +507,17 @@ bool rows_of_vectors(int C, const void *a, const void *b, const void *c, const v
 template <typename Tin, int VEC>
 cudaError_t launch_conv_v(const TreeConvArgs &a, cudaStream_t st) {
     const dim3 grid((a.C + kConvThreads * VEC - 1) / (kConvThreads * VEC), a.num_seqs);
+    const size_t smem = a.max_nodes * conv_row_bytes<Tin, VEC>() + (size_t)(a.W - 1) * conv_row_bytes<float, VEC>();
+    cudaError_t e = cudaSuccess;
 #define KDA_TREE_CONV(WW)                                                                                          \
     case WW:                                                                                                       \
-        tree_conv_kernel<Tin, WW, VEC><<<grid, kConvThreads, 0, st>>>((const Tin *)a.x, a.w, a.parent, a.cu,       \
-                                                                      a.seq_idx, a.total_nodes, a.max_nodes,       \
-                                                                      a.num_slots, a.C, a.pool, (Tin *)a.y,        \
-                                                                      a.status);                                   \
+        e = cudaFuncSetAttribute(tree_conv_kernel<Tin, WW, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,      \
+                                 (int)smem);                                                                       \
+        if (e != cudaSuccess) return e;                                                                            \
+        tree_conv_kernel<Tin, WW, VEC><<<grid, kConvThreads, smem, st>>>((const Tin *)a.x, a.w, a.parent, a.cu,    \
+                                                                         a.seq_idx, a.total_nodes, a.max_nodes,    \
+                                                                         a.num_slots, a.C, a.pool, (Tin *)a.y,     \
+                                                                         a.status);                                \
         break;
     switch (a.W) {
         KDA_TREE_CONV(1) KDA_TREE_CONV(2) KDA_TREE_CONV(3) KDA_TREE_CONV(4)

@@ -99,15 +99,21 @@ struct __align__(16) Found {  // a maximum, its lowest index, and (to fp32) the 
     float sum;
     float unused;
 };
-__device__ __forceinline__ Found better(Found a, Found b) {
-    return b.top > a.top || (b.top == a.top && (uint32_t)b.best < (uint32_t)a.best) ? b : a;
+// The largest of the warp's values, and the lowest index that goes with it.
+__device__ __forceinline__ Found best_of_warp(float top, int best) {
+    const uint32_t bits = __float_as_uint(top + 0.f);  // (-0 becomes 0)
+    const uint32_t key = bits & 0x80000000u ? ~bits : bits | 0x80000000u;  // ordered as the values are
+    const uint32_t most = __reduce_max_sync(0xffffffffu, key);
+    Found f;
+    f.top = __uint_as_float(most & 0x80000000u ? most & 0x7fffffffu : ~most);
+    f.best = (int)__reduce_min_sync(0xffffffffu, key == most ? (uint32_t)best : 0xffffffffu);
+    f.sum = f.unused = 0.f;
+    return f;
 }
-// The same over the entries of the first `n` lanes (n a power of two, the answer in those lanes), with the sums,
-// which become NaN where a logit is NaN or +inf.
+// The same over the entries that the lanes hold, lane l the entry l mod n (n a power of two), with the sums, which
+// become NaN where a logit is NaN or +inf.
 __device__ __forceinline__ Found merged(Found f, int n, float scale) {
-    Found a = f;
-    for (int off = n >> 1; off; off >>= 1)
-        a = better(a, Found{__shfl_xor_sync(0xffffffffu, a.top, off), __shfl_xor_sync(0xffffffffu, a.best, off), 0.f, 0.f});
+    Found a = best_of_warp(f.top, f.best);
     a.sum = f.top > -INFINITY ? f.sum * exp2_of((f.top - a.top) * scale) : 0.f;
     for (int off = n >> 1; off; off >>= 1) a.sum += __shfl_xor_sync(0xffffffffu, a.sum, off);
     return a;
@@ -170,12 +176,11 @@ __device__ __forceinline__ unsigned long long cluster_sum(Shared &sh, Exchange &
 // f.top and f.best are the thread's, f.sum the thread's relative to its warp's maximum (which f.top has become).
 __device__ __forceinline__ Found cluster_max(Shared &sh, Exchange &ex, float scale, Found f) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, turn = ex.turn();
+    float sum = f.sum;
 #pragma unroll
-    for (int off = 16; off; off >>= 1) {
-        const float other = __shfl_xor_sync(0xffffffffu, f.sum, off);
-        f = better(f, Found{__shfl_xor_sync(0xffffffffu, f.top, off), __shfl_xor_sync(0xffffffffu, f.best, off), f.sum, 0.f});
-        f.sum += other;
-    }
+    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    f = best_of_warp(f.top, f.best);
+    f.sum = sum;
     if (lane == 0) sh.warp_max[warp] = f;
     ex.expect(sh, 16);
     __syncthreads();
@@ -337,13 +342,15 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
         unsigned long long mask = 0;
         for (int j = tid + 1; j < t.nodes; ++j) mask |= (unsigned long long)(sh.tree.parent[j] == tid) << j;
         sh.child[tid] = mask;
-    } else if (mine > 0 && mine < t.nodes) {
-        const size_t at = (size_t)(t.row0 + sh.tree.parent[mine]) * p.V + token;
-        const bool in = token >= 0 && token < p.V;
-        sh.token[mine] = in ? token : -1;
-        sh.u[mine] = number;
-        sh.logit[mine] = in ? to_f32(reinterpret_cast<const Tin *>(p.logits)[at]) : 0.f;
-        sh.q[mine] = p.probs && in ? p.probs[at] : 1.f;
+    }
+    float logit = 0.f, qt = 1.f;
+    if (mine > 0 && mine < t.nodes) {
+        if (token < 0 || token >= p.V) token = -1;
+        if (token >= 0) {
+            const size_t from = (size_t)(t.row0 + sh.tree.parent[mine]) * p.V + token;
+            logit = to_f32(reinterpret_cast<const Tin *>(p.logits)[from]);
+            if (p.probs) qt = p.probs[from];
+        }
     }
     cluster.barrier_wait();
     int len = 0, next = -1;
@@ -373,6 +380,12 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
             C = 0.f;
             removed = 0;
             tc::cp_async_wait_all();
+            if (len == 1 && mine > 0 && mine < t.nodes) {  // the gathered values have come with the first row
+                sh.token[mine] = token;
+                sh.u[mine] = number;
+                sh.logit[mine] = logit;
+                sh.q[mine] = qt;
+            }
             __syncthreads();
             const unsigned long long children = sh.child[node];
             const int trials = __popcll(children), first = __ffsll((long long)children) - 1;
@@ -391,8 +404,7 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
             }
             if (!r.onehot) {
                 if (f.top > -INFINITY) f.best = 0;  // only `onehot` uses the place
-#pragma unroll
-                for (int off = 16; off; off >>= 1) f.top = fmaxf(f.top, __shfl_xor_sync(0xffffffffu, f.top, off));
+                f.top = best_of_warp(f.top, 0).top;
                 if (trials && f.top > -INFINITY) {
                     float2 sum = make_float2(0.f, 0.f);
                     const Row warps{f.top, r.scale, 0, false, false};
@@ -651,11 +663,18 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
 template <typename Tin>
 cudaError_t launch_t(Args p, int num_seqs, cudaStream_t st) {
     constexpr int kVec = 16 / sizeof(Tin);
-    // CTAs per request: a row is split as long as a part has two vectors per thread; large batches fill the GPU
-    // with fewer.
+    // CTAs per request: a row is split as long as a part has two vectors per thread (64 requests over 131072 tokens:
+    // 189, 109, 48 and 59 us with 2, 4, 8 and 16); half as many once each SM has a request, where they would only
+    // queue (256 requests over 100003 tokens: 127, 61, 69 and 115 us), if a part can then still be kept.
+    int device = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+    if (e != cudaSuccess) return e;
     int size = 1;
     while (size < kMaxCluster && p.V >= 2 * size * kThreads * kVec) size *= 2;
-    const int vectors = (p.V + 2 * (kVec - 1)) / kVec, each = (vectors + size - 1) / size;
+    const int vectors = (p.V + 2 * (kVec - 1)) / kVec;
+    if (size == kMaxCluster && num_seqs >= sms && (uint32_t)(vectors + size / 2 - 1) / (size / 2) * 16 <= kMaxPart) size /= 2;
+    const int each = (vectors + size - 1) / size;
     p.part_bytes = (uint32_t)each * 16 <= kMaxPart ? (uint32_t)each * 16 : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)num_seqs * size);
@@ -668,7 +687,7 @@ cudaError_t launch_t(Args p, int num_seqs, cudaStream_t st) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaFuncSetAttribute(draft_verify_kernel<Tin>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxPart);
+    e = cudaFuncSetAttribute(draft_verify_kernel<Tin>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxPart);
     if (e != cudaSuccess) return e;
     return cudaLaunchKernelEx(&cfg, draft_verify_kernel<Tin>, (const Args)p);
 }
