@@ -108,6 +108,22 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
     }
 }
 
+// Two multiply-adds in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n"
+        ".reg .b64 x, y, z, w;\n"
+        "mov.b64 x, {%2, %3};\n"
+        "mov.b64 y, {%4, %5};\n"
+        "mov.b64 z, {%6, %7};\n"
+        "fma.rn.f32x2 w, x, y, z;\n"
+        "mov.b64 {%0, %1}, w;\n"
+        "}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
 // 16-byte asynchronous copy global -> shared of the issuing thread, and the wait for all of its copies.
 __device__ __forceinline__ void cp_async16(void *dst_smem, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst_smem)), "l"(src) : "memory");

@@ -334,8 +334,17 @@ __device__ __forceinline__ void load_row(const Tin *p, float (&f)[VEC]) {
             Tin x[VEC];
         } r;
         r.v = *reinterpret_cast<const uint4 *>(p);
+        if constexpr (sizeof(Tin) == 2) {
+            const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) f[e] = to_f32(r.x[e]);
+            for (int e = 0; e < 4; ++e) {
+                f[2 * e] = __uint_as_float(w[e] << 16);
+                f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) f[e] = to_f32(r.x[e]);
+        }
     }
 }
 template <typename Tin, int VEC>
@@ -395,7 +404,8 @@ tree_conv_kernel(const Tin *__restrict__ x, const float *__restrict__ w, const i
                  int num_slots, int C, const float *__restrict__ pool, Tin *__restrict__ y,
                  int32_t *__restrict__ status) {
     __shared__ TreeShared ts;
-    __shared__ int s_tap[kMaxNodes][W];  // the j-th input before node i: a node, or -1 - m for the m-th carried one
+    // where the j-th input before node i lies: its row's offset in bytes, or -1 - the offset of a carried row
+    __shared__ __align__(16) int s_tap[kMaxNodes][W];
     extern __shared__ uint4 rows[];
     Tin *s_x = reinterpret_cast<Tin *>(rows) + threadIdx.x * VEC;
     float *s_past = reinterpret_cast<float *>(reinterpret_cast<char *>(rows) + max_nodes * conv_row_bytes<Tin, VEC>()) + threadIdx.x * VEC;
@@ -431,28 +441,46 @@ tree_conv_kernel(const Tin *__restrict__ x, const float *__restrict__ w, const i
         int at = i, m = 0;
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-            s_tap[i][j] = at >= 0 ? at : -1 - m++;
+            s_tap[i][j] = at >= 0 ? at * (int)conv_row_bytes<Tin, VEC>() : -1 - m++ * (int)conv_row_bytes<float, VEC>();
             at = at >= 0 ? ts.parent[at] : -1;
         }
     }
     tc::cp_async_wait_all();
     __syncthreads();
     if (c >= C) return;
+    Tin *out = y + (size_t)t.row0 * C + c;
+    const char *xs = reinterpret_cast<const char *>(s_x), *ps = reinterpret_cast<const char *>(s_past);
 #pragma unroll 2
-    for (int i = 0; i < t.nodes; ++i) {
+    for (int i = 0; i < t.nodes; ++i, out += C) {
+        int tap[W];
+        if constexpr (W % 4 == 0) {
+#pragma unroll
+            for (int j = 0; j < W; j += 4) *reinterpret_cast<int4 *>(&tap[j]) = *reinterpret_cast<const int4 *>(&s_tap[i][j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < W; ++j) tap[j] = s_tap[i][j];
+        }
         float acc[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-            const int tap = s_tap[i][j];
             float v[VEC];
-            if (tap >= 0) load_row<Tin, VEC>(s_x + tap * kStride, v);
-            else load_f32<VEC>(s_past + (-1 - tap) * kStride, v);
+            if (tap[j] >= 0) load_row<Tin, VEC>(reinterpret_cast<const Tin *>(xs + tap[j]), v);
+            else load_f32<VEC>(reinterpret_cast<const float *>(ps + (-1 - tap[j])), v);
+            if constexpr (VEC == 1) {
+                acc[0] = fmaf(wt[j][0], v[0], acc[0]);
+            } else {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) acc[e] = fmaf(wt[j][e], v[e], acc[e]);
+                for (int e = 0; e < VEC; e += 2) {  // two multiply-adds an instruction
+                    const float2 r = tc::fma2(make_float2(wt[j][e], wt[j][e + 1]), make_float2(v[e], v[e + 1]),
+                                              make_float2(acc[e], acc[e + 1]));
+                    acc[e] = r.x;
+                    acc[e + 1] = r.y;
+                }
+            }
         }
-        store_row<Tin, VEC>(y + (size_t)(t.row0 + i) * C + c, acc);
+        store_row<Tin, VEC>(out, acc);
     }
 }
 

@@ -187,21 +187,6 @@ __device__ void solve_masked(uint8_t *sm, const TreeShared &ts, const float *s_b
     }
 }
 
-// Two multiply-adds in one instruction, and the sum of a pair.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n"
-        ".reg .b64 x, y, z, w;\n"
-        "mov.b64 x, {%2, %3};\n"
-        "mov.b64 y, {%4, %5};\n"
-        "mov.b64 z, {%6, %7};\n"
-        "fma.rn.f32x2 w, x, y, z;\n"
-        "mov.b64 {%0, %1}, w;\n"
-        "}\n"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
 // sum_{a < n} x_a t_a, x a 16-byte aligned row in shared memory whose entries at and behind n are zero (up to the
 // next multiple of four)
 template <int n>
@@ -210,8 +195,8 @@ __device__ __forceinline__ float row_dot(const float *x, const float *t) {
 #pragma unroll
     for (int a = 0; a < n; a += 4) {
         const float4 y = *reinterpret_cast<const float4 *>(x + a);
-        acc[0] = fma2(make_float2(y.x, y.y), make_float2(t[a], t[a + 1]), acc[0]);
-        if (a + 2 < n) acc[1] = fma2(make_float2(y.z, y.w), make_float2(t[a + 2], t[a + 3]), acc[1]);
+        acc[0] = tc::fma2(make_float2(y.x, y.y), make_float2(t[a], t[a + 1]), acc[0]);
+        if (a + 2 < n) acc[1] = tc::fma2(make_float2(y.z, y.w), make_float2(t[a + 2], t[a + 3]), acc[1]);
     }
     return (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
 }
