@@ -21,142 +21,320 @@ namespace {
 // ---------------------------------------------------------------------------
 // Step, fp32 on the CUDA cores: any supported d and type
 // ---------------------------------------------------------------------------
-// One CTA per (request, head), one thread per state column.  Nodes go in blocks of kNB: a block's products
-// with the state are accumulated in registers over one sweep of the state's rows, then its u follow by
-// forward substitution in node order (a node's ancestors all have lower indices).
-constexpr int kNB = 8;
+// One CTA of 128 threads per (request, head).  With K~ = k e^b, Q~ = q e^b, K^ = k e^{-b} in shared memory, A and P
+// are one dot product per (node, ancestor) and thread; the products with the state go in register tiles of TN nodes
+// by four columns, which read a vector of shared memory for every eight multiply-adds or more; the substitution has
+// a thread per column, eight nodes at a time.  Where the decays along a path sum to more than kMaxRange, so that
+// e^{-b} would overflow, A and P take the path's own exponents instead.
+// Bound by the multiply-adds with the state, 4 d^2 for each node, and their operands' way from shared memory.
+constexpr int kStepThreads = 128, kStepWarps = kStepThreads / 32;
+constexpr float kMaxRange = 80.f;
+
+template <int D>
+struct StepLayout {  // offsets in floats; R: rows, max_nodes rounded up to eight
+    static constexpr int kPitch = D + 4;  // rows of K~, Q~, K^ start on distinct banks
+    int R, ap_stride, ke, qe, ki, gb, A, P, beta, scale, S, total;
+    __host__ __device__ explicit StepLayout(int max_nodes) {
+        R = (max_nodes + 7) & ~7;
+        ap_stride = R + 4;
+        ke = 0;
+        qe = ke + R * kPitch;
+        ki = qe + R * kPitch;   // K^, then x and u [R][D]
+        gb = ki + R * kPitch;   // g, then b, then y and o [R][D]
+        A = gb + R * D;
+        P = A + R * ap_stride;
+        beta = P + R * ap_stride;
+        scale = beta + R;
+        S = scale + 2 * R;
+        total = S + D * D;
+    }
+    // the state is read through L1 where it would not fit beside the rest
+    __host__ __device__ bool keeps_state() const { return total * 4 <= 225 * 1024; }
+    __host__ __device__ int bytes() const { return (keeps_state() ? total : S) * 4; }
+};
+
+// CPL neighbouring values of a row as fp32.
+template <int CPL, typename Tin>
+__device__ __forceinline__ void load_some(const Tin *p, float (&f)[CPL]) {
+#pragma unroll
+    for (int e = 0; e < CPL; ++e) f[e] = to_f32(p[e]);
+}
+
+// Forward substitution of one state column over all nodes, eight at a time: the products with the u of earlier
+// blocks, then the block's own triangle.  Masked: entries off the path are skipped instead of multiplied by zero,
+// which a non-finite u of another branch would turn into NaN.  Returns false if a u is not finite.
+template <typename Tin, int D, bool Masked>
+__device__ __forceinline__ bool substitute(float *sm, const StepLayout<D> &L, const TreeShared &ts, const Tin *v,
+                                           size_t row_stride, int M, int c) {
+    const float *sA = sm + L.A, *sP = sm + L.P;
+    float *s_x = sm + L.ki, *s_y = sm + L.gb, *s_u = sm + L.ke, *s_o = sm + L.qe;
+    bool finite = true;
+    for (int i0 = 0; i0 < M; i0 += 8) {
+        float w[8], out[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const int i = min(i0 + r, M - 1);
+            w[r] = sm[L.beta + i] * (to_f32(v[(size_t)i * row_stride]) - s_x[i * D + c]);
+            out[r] = s_y[i * D + c];
+        }
+        for (int a = 0; a < i0; a += 4) {
+            float ua[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ua[e] = s_u[(a + e) * D + c];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const float4 A = *reinterpret_cast<const float4 *>(&sA[(i0 + r) * L.ap_stride + a]);
+                const float4 P = *reinterpret_cast<const float4 *>(&sP[(i0 + r) * L.ap_stride + a]);
+                const float Av[4] = {A.x, A.y, A.z, A.w}, Pv[4] = {P.x, P.y, P.z, P.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (!Masked || (i0 + r < M && ((ts.anc[i0 + r] >> (a + e)) & 1))) {
+                        w[r] = fmaf(-Av[e], ua[e], w[r]);
+                        out[r] = fmaf(Pv[e], ua[e], out[r]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const float *rowA = &sA[(i0 + r) * L.ap_stride + i0], *rowP = &sP[(i0 + r) * L.ap_stride + i0];
+#pragma unroll
+            for (int a = 0; a < r; ++a) {
+                if (!Masked || (i0 + r < M && ((ts.anc[i0 + r] >> (i0 + a)) & 1))) {
+                    w[r] = fmaf(-rowA[a], w[a], w[r]);
+                    out[r] = fmaf(rowP[a], w[a], out[r]);
+                }
+            }
+            out[r] = fmaf(rowP[r], w[r], out[r]);
+            if (i0 + r < M) {
+                finite &= fabsf(w[r]) < INFINITY;
+                s_u[(i0 + r) * D + c] = w[r];
+                s_o[(i0 + r) * D + c] = out[r];
+            }
+        }
+    }
+    return finite;
+}
 
 template <typename Tin, int D>
-__global__ void __launch_bounds__(D < 32 ? 32 : D)
+__global__ void __launch_bounds__(kStepThreads)
 tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin *__restrict__ v,
                  const float *__restrict__ g, const float *__restrict__ beta, const int32_t *__restrict__ parent,
                  const int32_t *__restrict__ cu, const int32_t *__restrict__ seq_idx, int H, int total_nodes,
                  int max_nodes, int num_slots, const float *__restrict__ S_pool, Tin *__restrict__ o,
                  float *__restrict__ u, int32_t *__restrict__ status, int qk_norm, float qk_eps,
                  const Tin *__restrict__ gate, const float *__restrict__ weight, float out_eps) {
-    constexpr int NT = D < 32 ? 32 : D;
-    extern __shared__ float sm[];
+    constexpr int CG = D / 4, NG = kStepThreads / CG, TN = D == 128 ? 4 : 2;  // products: column groups, node groups
+    constexpr int CPL = D < 32 ? 1 : D / 32, LANES = D / CPL;                 // rows: channels per lane
+    constexpr int kPitch = StepLayout<D>::kPitch;
+    extern __shared__ __align__(16) float sm[];
     __shared__ TreeShared ts;
+    const StepLayout<D> L(max_nodes);
     const int n = blockIdx.x / H, h = blockIdx.x % H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const Tree t = read_tree(ts, parent, cu, n, total_nodes, max_nodes, true);
+    const Tree t = tree_rows(cu, n, total_nodes, max_nodes);
     const int slot = slot_of(seq_idx, n, num_slots);
     if (t.nodes < 0 || slot < 0) {
         if (tid == 0) report_invalid(status);
         return;
     }
+    if (t.nodes == 0) return;
     const int M = t.nodes;
-    float *s_k = sm, *s_q = s_k + max_nodes * D, *s_b = s_q + max_nodes * D, *s_u = s_b + max_nodes * D;
-    float *s_A = s_u + max_nodes * D, *s_P = s_A + max_nodes * max_nodes, *s_beta = s_P + max_nodes * max_nodes;
-    const size_t row_stride = (size_t)H * D;
-    const size_t base = ((size_t)t.row0 * H + h) * D;
-
-    for (int i = tid; i < M; i += NT) s_beta[i] = beta[(size_t)(t.row0 + i) * H + h];
-    for (int i = tid; i < M * D; i += NT) {
-        const size_t at = base + (size_t)(i / D) * row_stride + i % D;
-        s_k[i] = to_f32(k[at]);
-        s_q[i] = to_f32(q[at]);
-    }
-    __syncthreads();
-    if (qk_norm) {  // q, k L2-normalised in fp32: a warp per row
-        for (int r = warp; r < 2 * M; r += NT / 32) {
-            float *x = r < M ? s_k + r * D : s_q + (r - M) * D;
-            float ss = 0.f;
-            for (int c = lane; c < D; c += 32) ss = fmaf(x[c], x[c], ss);
-#pragma unroll
-            for (int off = 16; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-            const float inv = rsqrtf(ss + qk_eps);
-            for (int c = lane; c < D; c += 32) x[c] *= inv;
-        }
-    }
-    // log-decay along the paths: each channel by its own thread, parents before children
-    for (int c = tid; c < D; c += NT)
-        for (int i = 0; i < M; ++i)
-            s_b[i * D + c] = log_decay(g[base + (size_t)i * row_stride + c]) + (i ? s_b[ts.parent[i] * D + c] : 0.f);
-    __syncthreads();
-    // A and P: a warp per (node, ancestor); the exponent b_i - b_a is one of the path's own decays, so no
-    // reference point is needed and no factor leaves the range of the decays themselves
-    for (int p = warp; p < M * M; p += NT / 32) {
-        const int i = p / M, a = p % M;
-        if (!((ts.anc[i] >> a) & 1)) continue;
-        float sa = 0.f, sp = 0.f;
-        for (int c = lane; c < D; c += 32) {
-            const float kd = s_k[a * D + c] * expf(s_b[i * D + c] - s_b[a * D + c]);
-            sa = fmaf(s_k[i * D + c], kd, sa);
-            sp = fmaf(s_q[i * D + c], kd, sp);
-        }
-#pragma unroll
-        for (int off = 16; off; off >>= 1) {
-            sa += __shfl_xor_sync(0xffffffffu, sa, off);
-            sp += __shfl_xor_sync(0xffffffffu, sp, off);
-        }
-        if (lane == 0) {
-            s_A[i * M + a] = s_beta[i] * sa;
-            s_P[i * M + a] = sp;
-        }
-    }
-    __syncthreads();
-    for (int i = tid; i < M * D; i += NT) {
-        const float e = expf(s_b[i]);
-        s_k[i] *= e;
-        s_q[i] *= e;
-    }
-    __syncthreads();
-
+    const size_t row_stride = (size_t)H * D, base = ((size_t)t.row0 * H + h) * D;
     const float *S = S_pool + ((size_t)slot * H + h) * D * D;
-    const int col = tid;
-    for (int i0 = 0; i0 < M; i0 += kNB) {
-        float x[kNB], y[kNB];
+    for (int i = tid; i < M * CG; i += kStepThreads)
+        tc::cp_async16(sm + L.gb + i * 4, g + base + (size_t)(i / CG) * row_stride + i % CG * 4);
+    tc::cp_async_commit();
+    if (L.keeps_state()) {
+        for (int i = tid; i < D * CG; i += kStepThreads) tc::cp_async16(sm + L.S + i * 4, S + i * 4);
+        S = sm + L.S;
+    }
+    tc::cp_async_commit();
+    for (int i = tid; i < M; i += kStepThreads) sm[L.beta + i] = beta[(size_t)(t.row0 + i) * H + h];
+    tc::cp_async_wait_all_but_one();
+    if (read_tree(ts, parent, cu, n, total_nodes, max_nodes, true).nodes < 0) {  // a block barrier
+        tc::cp_async_wait_all();
+        if (tid == 0) report_invalid(status);
+        return;
+    }
+
+    // K~, Q~, K^, a warp per node.  b sums g over the path, 16 nodes at a time, from the b of the nearest ancestor
+    // in an earlier group.
+    float range = 0.f;
+    const int c0 = lane * CPL;
+    for (int first = 0; first < M; first += 16) {
+        float b[16 / kStepWarps][CPL];
 #pragma unroll
-        for (int r = 0; r < kNB; ++r) x[r] = y[r] = 0.f;
-        if (col < D) {
-#pragma unroll 4
-            for (int c = 0; c < D; ++c) {
-                const float s = S[(size_t)c * D + col];
+        for (int e = 0; e < 16 / kStepWarps; ++e) {
+            const int i = first + warp + e * kStepWarps;
 #pragma unroll
-                for (int r = 0; r < kNB; ++r) {
-                    if (i0 + r < M) {
-                        x[r] = fmaf(s_k[(i0 + r) * D + c], s, x[r]);
-                        y[r] = fmaf(s_q[(i0 + r) * D + c], s, y[r]);
-                    }
+            for (int x = 0; x < CPL; ++x) b[e][x] = 0.f;
+            if (i < M && lane < LANES) {
+                const unsigned long long anc = ts.anc[i], before = anc & ((1ull << first) - 1);
+                uint32_t here = (uint32_t)(anc >> first) & 0xffffu;
+                if (before) {
+                    const float *from = sm + L.gb + (63 - __clzll((long long)before)) * D + c0;
+#pragma unroll
+                    for (int x = 0; x < CPL; ++x) b[e][x] = from[x];
+                }
+                while (here) {
+                    const float *from = sm + L.gb + (first + __ffs((int)here) - 1) * D + c0;
+                    here &= here - 1;
+#pragma unroll
+                    for (int x = 0; x < CPL; ++x) b[e][x] += log_decay(from[x]);
                 }
             }
         }
-        __syncthreads();  // the block's rows of s_q are read: they take its outputs below
-        if (col < D) {
+        __syncthreads();  // every sum of this group is formed
 #pragma unroll
-            for (int r = 0; r < kNB; ++r) {
-                const int i = i0 + r;
-                if (i < M) {
-                    const size_t at = base + (size_t)i * row_stride + col;
-                    const unsigned long long anc = ts.anc[i];
-                    float w = s_beta[i] * (to_f32(v[at]) - x[r]), out = y[r];
-                    for (int a = 0; a < i; ++a) {
-                        if ((anc >> a) & 1) {
-                            w = fmaf(-s_A[i * M + a], s_u[a * D + col], w);
-                            out = fmaf(s_P[i * M + a], s_u[a * D + col], out);
-                        }
-                    }
-                    s_u[i * D + col] = w;
-                    out = fmaf(s_P[i * M + i], w, out);
-                    if (u) u[at] = w;
-                    if (gate) s_q[i * D + col] = out;
-                    else o[at] = from_f32<Tin>(out);
+        for (int e = 0; e < 16 / kStepWarps; ++e) {
+            const int i = first + warp + e * kStepWarps;
+            if (i >= M) break;
+            float kf[CPL], qf[CPL];
+#pragma unroll
+            for (int x = 0; x < CPL; ++x) kf[x] = qf[x] = 0.f;
+            if (lane < LANES) {
+                load_some<CPL>(k + base + (size_t)i * row_stride + c0, kf);
+                load_some<CPL>(q + base + (size_t)i * row_stride + c0, qf);
+            }
+            float sk = 1.f, sq = 1.f;
+            if (qk_norm) {
+                sk = sq = 0.f;
+#pragma unroll
+                for (int x = 0; x < CPL; ++x) {
+                    sk = fmaf(kf[x], kf[x], sk);
+                    sq = fmaf(qf[x], qf[x], sq);
                 }
+#pragma unroll
+                for (int off = 16; off; off >>= 1) {
+                    sk += __shfl_xor_sync(0xffffffffu, sk, off);
+                    sq += __shfl_xor_sync(0xffffffffu, sq, off);
+                }
+                sk = rsqrtf(sk + qk_eps);
+                sq = rsqrtf(sq + qk_eps);
+                if (lane == 0) {
+                    sm[L.scale + i] = sk;
+                    sm[L.scale + L.R + i] = sq;
+                }
+            }
+            if (lane < LANES) {
+#pragma unroll
+                for (int x = 0; x < CPL; ++x) {
+                    const float up = expf(b[e][x]), key = kf[x] * sk;
+                    range = fmaxf(range, fabsf(b[e][x]));
+                    sm[L.gb + i * D + c0 + x] = b[e][x];
+                    sm[L.ke + i * kPitch + c0 + x] = key * up;
+                    sm[L.qe + i * kPitch + c0 + x] = qf[x] * sq * up;
+                    sm[L.ki + i * kPitch + c0 + x] = key * expf(-b[e][x]);
+                }
+            }
+        }
+        if (first + 16 < M) __syncthreads();
+    }
+    tc::cp_async_wait_all();
+    const bool pairwise = __syncthreads_or(!(range <= kMaxRange));
+
+    // A and P: a thread per (node, ancestor)
+    for (int p = tid; p < M * M; p += kStepThreads) {
+        const int i = p / M, a = p % M;
+        float sa = 0.f, sp = 0.f;
+        if ((ts.anc[i] >> a) & 1) {
+            if (!pairwise) {
+                const float *x = sm + L.ke + i * kPitch, *y = sm + L.qe + i * kPitch, *z = sm + L.ki + a * kPitch;
+#pragma unroll 4
+                for (int c = 0; c < D; c += 4) {
+                    const float4 x4 = *reinterpret_cast<const float4 *>(x + c), y4 = *reinterpret_cast<const float4 *>(y + c),
+                                 z4 = *reinterpret_cast<const float4 *>(z + c);
+                    sa = fmaf(x4.x, z4.x, sa); sa = fmaf(x4.y, z4.y, sa); sa = fmaf(x4.z, z4.z, sa); sa = fmaf(x4.w, z4.w, sa);
+                    sp = fmaf(y4.x, z4.x, sp); sp = fmaf(y4.y, z4.y, sp); sp = fmaf(y4.z, z4.z, sp); sp = fmaf(y4.w, z4.w, sp);
+                }
+            } else {
+                const Tin *ka = k + base + (size_t)a * row_stride, *ki = k + base + (size_t)i * row_stride,
+                          *qi = q + base + (size_t)i * row_stride;
+                for (int c = 0; c < D; ++c) {
+                    const float kd = to_f32(ka[c]) * expf(sm[L.gb + i * D + c] - sm[L.gb + a * D + c]);
+                    sa = fmaf(to_f32(ki[c]), kd, sa);
+                    sp = fmaf(to_f32(qi[c]), kd, sp);
+                }
+                if (qk_norm) {
+                    sa *= sm[L.scale + i] * sm[L.scale + a];
+                    sp *= sm[L.scale + L.R + i] * sm[L.scale + a];
+                }
+            }
+            sa = a == i ? 0.f : sa * sm[L.beta + i];
+        }
+        sm[L.A + i * L.ap_stride + a] = sa;
+        sm[L.P + i * L.ap_stride + a] = sp;
+    }
+    __syncthreads();  // K^ and b are no longer needed
+
+    // x and y
+    const int cg = tid % CG, ng = tid / CG;
+    for (int i0 = ng * TN; i0 < M; i0 += NG * TN) {
+        float x[TN][4], y[TN][4];
+#pragma unroll
+        for (int r = 0; r < TN; ++r)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[r][e] = y[r][e] = 0.f;
+        const float *ke[TN], *qe[TN];
+#pragma unroll
+        for (int r = 0; r < TN; ++r) {
+            ke[r] = sm + L.ke + min(i0 + r, M - 1) * kPitch;
+            qe[r] = sm + L.qe + min(i0 + r, M - 1) * kPitch;
+        }
+#pragma unroll 2
+        for (int c = 0; c < D; c += 4) {
+            float4 s[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j] = *reinterpret_cast<const float4 *>(S + (size_t)(c + j) * D + cg * 4);
+#pragma unroll
+            for (int r = 0; r < TN; ++r) {
+                const float4 kk = *reinterpret_cast<const float4 *>(ke[r] + c), qq = *reinterpret_cast<const float4 *>(qe[r] + c);
+                const float kv[4] = {kk.x, kk.y, kk.z, kk.w}, qv[4] = {qq.x, qq.y, qq.z, qq.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[r][0] = fmaf(kv[j], s[j].x, x[r][0]); x[r][1] = fmaf(kv[j], s[j].y, x[r][1]);
+                    x[r][2] = fmaf(kv[j], s[j].z, x[r][2]); x[r][3] = fmaf(kv[j], s[j].w, x[r][3]);
+                    y[r][0] = fmaf(qv[j], s[j].x, y[r][0]); y[r][1] = fmaf(qv[j], s[j].y, y[r][1]);
+                    y[r][2] = fmaf(qv[j], s[j].z, y[r][2]); y[r][3] = fmaf(qv[j], s[j].w, y[r][3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < TN; ++r) {
+            if (i0 + r < M) {
+                *reinterpret_cast<float4 *>(sm + L.ki + (i0 + r) * D + cg * 4) = make_float4(x[r][0], x[r][1], x[r][2], x[r][3]);
+                *reinterpret_cast<float4 *>(sm + L.gb + (i0 + r) * D + cg * 4) = make_float4(y[r][0], y[r][1], y[r][2], y[r][3]);
             }
         }
     }
-    if (gate) {  // gated output normalisation: a warp per row
-        __syncthreads();
-        for (int i = warp; i < M; i += NT / 32) {
-            const float *x = s_q + i * D;
+    __syncthreads();  // K~ and Q~ are no longer needed: u and o take their place
+    for (int c = tid; c < D; c += kStepThreads) {
+        const Tin *vc = v + base + c;
+        if (!substitute<Tin, D, false>(sm, L, ts, vc, row_stride, M, c)) substitute<Tin, D, true>(sm, L, ts, vc, row_stride, M, c);
+    }
+    __syncthreads();
+    for (int i = warp; i < M; i += kStepWarps) {  // a warp per row
+        const size_t at = base + (size_t)i * row_stride + c0;
+        float x[CPL];
+        float inv = 1.f;
+        if (gate) {
             float ss = 0.f;
-            for (int c = lane; c < D; c += 32) ss = fmaf(x[c], x[c], ss);
+            if (lane < LANES)
+#pragma unroll
+                for (int e = 0; e < CPL; ++e) ss = fmaf(sm[L.qe + i * D + c0 + e], sm[L.qe + i * D + c0 + e], ss);
 #pragma unroll
             for (int off = 16; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-            const float inv = rsqrtf(ss / (float)D + out_eps);
-            for (int c = lane; c < D; c += 32) {
-                const size_t at = base + (size_t)i * row_stride + c;
-                o[at] = from_f32<Tin>(x[c] * inv * (weight ? weight[c] : 1.f) * sigmoidf(to_f32(gate[at])));
+            inv = rsqrtf(ss / (float)D + out_eps);
+        }
+        if (lane < LANES) {
+            float z[CPL];
+            if (gate) load_some<CPL>(gate + at, z);
+#pragma unroll
+            for (int e = 0; e < CPL; ++e) {
+                x[e] = sm[L.qe + i * D + c0 + e];
+                if (gate) x[e] *= inv * (weight ? weight[c0 + e] : 1.f) * sigmoidf(z[e]);
+                o[at + e] = from_f32<Tin>(x[e]);
+                if (u) u[at + e] = sm[L.ke + i * D + c0 + e];
             }
         }
     }
@@ -164,11 +342,11 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
 
 template <typename Tin, int D>
 cudaError_t launch_step_d(const TreeStepArgs &a, cudaStream_t st) {
-    const size_t smem = ((size_t)4 * a.max_nodes * D + 2 * (size_t)a.max_nodes * a.max_nodes + a.max_nodes) * 4;
+    const int smem = StepLayout<D>(a.max_nodes).bytes();
     auto *kernel = tree_step_kernel<Tin, D>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<a.num_seqs * a.H, D < 32 ? 32 : D, smem, st>>>(
+    kernel<<<a.num_seqs * a.H, kStepThreads, smem, st>>>(
         (const Tin *)a.q, (const Tin *)a.k, (const Tin *)a.v, a.g, a.beta, a.parent, a.cu, a.seq_idx, a.H,
         a.total_nodes, a.max_nodes, a.num_slots, a.S_pool, (Tin *)a.o, a.u, a.status, a.fu.qk_norm, a.fu.qk_eps,
         (const Tin *)a.fu.gate, a.fu.weight, a.fu.out_eps);
@@ -180,7 +358,9 @@ cudaError_t launch_step_t(const TreeStepArgs &a, cudaStream_t st) {
     switch (a.d) {
         case 16: return launch_step_d<Tin, 16>(a, st);
         case 64: return launch_step_d<Tin, 64>(a, st);
-        case 128: return launch_step_d<Tin, 128>(a, st);
+        case 128:
+            if constexpr (sizeof(Tin) == 4) return launch_step_d<Tin, 128>(a, st);
+            else return launch_tree_step_tc(a, st);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -580,7 +760,6 @@ cudaError_t launch_conv_commit_t(const TreeConvCommitArgs &a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_tree_step(const TreeStepArgs &a, kda_dtype dt, cudaStream_t st) {
-    if (dt == KDA_BF16 && a.d == 128) return launch_tree_step_tc(a, st);
     return dt == KDA_BF16 ? launch_step_t<__nv_bfloat16>(a, st) : launch_step_t<float>(a, st);
 }
 cudaError_t launch_tree_commit(const TreeCommitArgs &a, kda_dtype dt, cudaStream_t st) {
