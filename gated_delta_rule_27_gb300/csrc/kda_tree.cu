@@ -343,10 +343,9 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
 template <typename Tin, int D>
 cudaError_t launch_step_d(const TreeStepArgs &a, cudaStream_t st) {
     const int smem = StepLayout<D>(a.max_nodes).bytes();
-    auto *kernel = tree_step_kernel<Tin, D>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_smem<tree_step_kernel<Tin, D>>(smem);
     if (e != cudaSuccess) return e;
-    kernel<<<a.num_seqs * a.H, kStepThreads, smem, st>>>(
+    tree_step_kernel<Tin, D><<<a.num_seqs * a.H, kStepThreads, smem, st>>>(
         (const Tin *)a.q, (const Tin *)a.k, (const Tin *)a.v, a.g, a.beta, a.parent, a.cu, a.seq_idx, a.H,
         a.total_nodes, a.max_nodes, a.num_slots, a.S_pool, (Tin *)a.o, a.u, a.status, a.fu.qk_norm, a.fu.qk_eps,
         (const Tin *)a.fu.gate, a.fu.weight, a.fu.out_eps);
@@ -719,8 +718,7 @@ cudaError_t launch_conv_v(const TreeConvArgs &a, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
 #define KDA_TREE_CONV(WW)                                                                                          \
     case WW:                                                                                                       \
-        e = cudaFuncSetAttribute(tree_conv_kernel<Tin, WW, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,      \
-                                 (int)smem);                                                                       \
+        e = allow_smem<tree_conv_kernel<Tin, WW, VEC>>((int)smem);                                                 \
         if (e != cudaSuccess) return e;                                                                            \
         tree_conv_kernel<Tin, WW, VEC><<<grid, kConvThreads, smem, st>>>((const Tin *)a.x, a.w, a.parent, a.cu,    \
                                                                          a.seq_idx, a.total_nodes, a.max_nodes,    \

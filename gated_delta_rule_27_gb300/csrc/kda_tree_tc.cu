@@ -775,12 +775,10 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
 template <int MP>
 cudaError_t launch_mp(Args p, int ctas, cudaStream_t st) {
     constexpr int smem = Layout<MP>::total + 1024;
-    cudaError_t e =
-        cudaFuncSetAttribute(tree_step_tc_kernel<MP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    int sms = 0;
+    cudaError_t e = allow_smem<tree_step_tc_kernel<MP>>(smem);
+    if (e == cudaSuccess) e = sm_count(&sms);
     if (e != cudaSuccess) return e;
-    int device = 0, sms = 0;
-    if ((e = cudaGetDevice(&device)) != cudaSuccess) return e;
-    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device)) != cudaSuccess) return e;
     p.ahead = sms * (MP == 64 ? 1 : MP == 32 ? 2 : 3);  // the CTAs that run at once
     tree_step_tc_kernel<MP><<<ctas, kThreads, smem, st>>>(p);
     return cudaGetLastError();

@@ -666,9 +666,8 @@ cudaError_t launch_t(Args p, int num_seqs, cudaStream_t st) {
     // CTAs per request: a row is split as long as a part has two vectors per thread (64 requests over 131072 tokens:
     // 189, 109, 48 and 59 us with 2, 4, 8 and 16); half as many once each SM has a request, where they would only
     // queue (256 requests over 100003 tokens: 127, 61, 69 and 115 us), if a part can then still be kept.
-    int device = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&device);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
     int size = 1;
     while (size < kMaxCluster && p.V >= 2 * size * kThreads * kVec) size *= 2;
@@ -687,7 +686,7 @@ cudaError_t launch_t(Args p, int num_seqs, cudaStream_t st) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaFuncSetAttribute(draft_verify_kernel<Tin>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxPart);
+    e = allow_smem<draft_verify_kernel<Tin>>(kMaxPart);
     if (e != cudaSuccess) return e;
     return cudaLaunchKernelEx(&cfg, draft_verify_kernel<Tin>, (const Args)p);
 }

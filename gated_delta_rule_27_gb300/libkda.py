@@ -316,15 +316,15 @@ def _arg(t, dtype, shape, name: str):
     """The address of a contiguous device tensor of this dtype and shape (None passes as null)."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError("%s is %s, libkda takes %s here" % (name, t.dtype, dtype))
     if t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if not t.is_cuda:
         raise ValueError("libkda takes device tensors; %s is on %s" % (name, t.device))
-    if not t.is_contiguous():
-        raise ValueError("libkda takes contiguous tensors; %s is not" % name)
-    return t.data_ptr()
+    raise ValueError("libkda takes contiguous tensors; %s is not" % name)
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -338,17 +338,16 @@ def _stream_of(stream, t):
 
 
 def kda_tree_step(q, k, v, g, beta, parent, cu_nodes, seq_idx, S_pool, o, u, max_nodes, status=None, stream=None,
-                  **fusion) -> None:
+                  qk_l2norm=False, qk_eps=1e-6, out_gate=None, out_weight=None, out_eps=1e-6) -> None:
     """KDA attention of every draft-tree node over the state pool (kda_tree_step): q, k, v, g [T, H, d] and beta
-    [T, H] packed as include/kda.h says, o and u (or None) written; keywords of fusion_opts."""
+    [T, H] packed as include/kda.h says, o and u (or None) written; the fused normalisations as for fusion_opts."""
     dt, rows, i32, f32 = q.dtype, q.shape, torch.int32, torch.float32
     T, H, d = rows
     N, slots = cu_nodes.shape[0] - 1, S_pool.shape[0]
     opts = None
-    if fusion:
-        _arg(fusion.get("out_gate"), dt, rows, "out_gate")
-        _arg(fusion.get("out_weight"), f32, (d,), "out_weight")
-        opts = fusion_opts(**fusion)
+    if qk_l2norm or out_gate is not None:
+        opts = FusionOpts(1 if qk_l2norm else 0, qk_eps, _arg(out_gate, dt, rows, "out_gate"),
+                          _arg(out_weight, f32, (d,), "out_weight"), out_eps)
     rc = load().kda_tree_step(_arg(q, dt, rows, "q"), _arg(k, dt, rows, "k"), _arg(v, dt, rows, "v"),
                               _arg(g, f32, rows, "g"), _arg(beta, f32, (T, H), "beta"),
                               _arg(parent, i32, (T,), "parent"), _arg(cu_nodes, i32, (N + 1,), "cu_nodes"),
@@ -365,7 +364,7 @@ def kda_tree_commit(k, g, u, cu_nodes, path, path_len, seq_idx, S_pool, status=N
     rows, i32, f32 = k.shape, torch.int32, torch.float32
     T, H, d = rows
     N, slots, width = cu_nodes.shape[0] - 1, S_pool.shape[0], path.shape[1]
-    opts = fusion_opts(qk_l2norm=True, qk_eps=qk_eps) if qk_l2norm else None
+    opts = FusionOpts(1, qk_eps, None, None, 0.0) if qk_l2norm else None
     rc = load().kda_tree_commit(_arg(k, k.dtype, rows, "k"), _arg(g, f32, rows, "g"), _arg(u, f32, rows, "u"),
                                 _arg(cu_nodes, i32, (N + 1,), "cu_nodes"), _arg(path, i32, (N, width), "path"),
                                 _arg(path_len, i32, (N,), "path_len"), _arg(seq_idx, i32, (N,), "seq_idx"), N, T,
