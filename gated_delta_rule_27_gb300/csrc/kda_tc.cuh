@@ -108,7 +108,21 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
     }
 }
 
-// Two multiply-adds in one instruction.
+// Arithmetic on pairs, one instruction each.
+#define KDA_PAIR_OP(name, instr)                                                                            \
+    __device__ __forceinline__ float2 name(float2 a, float2 b) {                                            \
+        float2 d;                                                                                           \
+        asm("{\n.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\n" instr " z, x, y;\n"  \
+            "mov.b64 {%0, %1}, z;\n}\n"                                                                   \
+            : "=f"(d.x), "=f"(d.y)                                                                          \
+            : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));                                                      \
+        return d;                                                                                           \
+    }
+KDA_PAIR_OP(add2, "add.rn.f32x2")
+KDA_PAIR_OP(add_rz2, "add.rz.f32x2")
+KDA_PAIR_OP(sub2, "sub.rn.f32x2")
+KDA_PAIR_OP(mul2, "mul.rn.f32x2")
+#undef KDA_PAIR_OP
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
     asm("{\n"

@@ -84,7 +84,9 @@ __device__ __forceinline__ void split8(const float (&f)[8], uint4 &hi, uint4 &lo
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         h[i] = pack2(f[2 * i], f[2 * i + 1]);
-        l[i] = pack2(f[2 * i] - __uint_as_float(h[i] << 16), f[2 * i + 1] - __uint_as_float(h[i] & 0xffff0000u));
+        const float2 rest = tc::sub2(make_float2(f[2 * i], f[2 * i + 1]),
+                                     make_float2(__uint_as_float(h[i] << 16), __uint_as_float(h[i] & 0xffff0000u)));
+        l[i] = pack2(rest.x, rest.y);
     }
     hi = make_uint4(h[0], h[1], h[2], h[3]);
     lo = make_uint4(l[0], l[1], l[2], l[3]);
@@ -108,9 +110,35 @@ __device__ __forceinline__ void ldg8(const float *p, float (&f)[8]) {
                  : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
                  : "l"(p));
 }
-__device__ __forceinline__ void add8(float (&f)[8], const float4 &a, const float4 &b) {
-    f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
-    f[4] += b.x; f[5] += b.y; f[6] += b.z; f[7] += b.w;
+// Eight values as four pairs.
+template <typename Op>
+__device__ __forceinline__ void pairs8(float (&f)[8], const float (&a)[8], const float (&b)[8], Op op) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        const float2 r = op(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]));
+        f[e] = r.x;
+        f[e + 1] = r.y;
+    }
+}
+__device__ __forceinline__ void add8(float (&f)[8], const float (&a)[8], const float (&b)[8]) {
+    pairs8(f, a, b, [](float2 x, float2 y) { return tc::add2(x, y); });
+}
+__device__ __forceinline__ void mul8(float (&f)[8], const float (&a)[8], const float (&b)[8]) {
+    pairs8(f, a, b, [](float2 x, float2 y) { return tc::mul2(x, y); });
+}
+__device__ __forceinline__ void scale8(float (&f)[8], const float (&a)[8], float b) {
+    pairs8(f, a, a, [b](float2 x, float2) { return tc::mul2(x, make_float2(b, b)); });
+}
+__device__ __forceinline__ float sum_squares8(const float (&f)[8]) {
+    float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) ss = tc::fma2(make_float2(f[e], f[e + 1]), make_float2(f[e], f[e + 1]), ss);
+    return ss.x + ss.y;
+}
+__device__ __forceinline__ void read8(const float *p, float (&f)[8]) {
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
 // The decays' exponents are kept in base 2, the hardware's exponential.
@@ -148,9 +176,13 @@ template <int MP>
 __device__ __forceinline__ void residual8(const uint8_t *sm, const float *s_beta, const float (&x_hi)[8],
                                           const float (&x_lo)[8], int i0, int c, float (&r)[8]) {
     const __nv_bfloat16 *s_v = reinterpret_cast<const __nv_bfloat16 *>(sm + Layout<MP>::v);
+    float x[8], v[8], beta[8];
+    add8(x, x_hi, x_lo);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        r[e] = s_beta[i0 + e] * (__bfloat162float(s_v[(i0 + e) * kD + c]) - (x_hi[e] + x_lo[e]));
+    for (int e = 0; e < 8; ++e) v[e] = __bfloat162float(s_v[(i0 + e) * kD + c]);
+    read8(s_beta + i0, beta);
+    pairs8(r, v, x, [](float2 a, float2 b) { return tc::sub2(a, b); });
+    mul8(r, r, beta);
 }
 
 // u and o of the thread's state column by forward substitution over the paths' entries only.  u is kept in the
@@ -273,8 +305,9 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
     using L = Layout<MP>;
     extern __shared__ uint8_t raw[];
     __shared__ TreeShared ts;
-    __shared__ float s_beta[MP], s_scale[2 * MP];
-    __shared__ uint64_t bar_d1, bar_d3, bar_d4, bar_half[2], bar_rows[2];
+    __shared__ __align__(16) float s_beta[MP];
+    __shared__ float s_scale[2 * MP];
+    __shared__ uint64_t bar_d1, bar_d3, bar_d4, bar_half[2], bar_rows;
     __shared__ uint32_t s_tmem;
     __shared__ int s_wild;    // A, P, T or G holds something that is not finite
     __shared__ int s_bad[4];  // r does, in the columns of one quarter of the lanes
@@ -337,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
             tc::mbar_init(&bar_d4, 1);
             tc::mbar_init(&bar_half[0], 1);
             tc::mbar_init(&bar_half[1], 1);
-            for (int i = 0; i < 2; ++i) tc::mbar_init(&bar_rows[i], 8);
+            tc::mbar_init(&bar_rows, 8);
             tc::fence_mbar_init();
             s_wild = 0;
             for (int i = 0; i < 4; ++i) s_bad[i] = 0;
@@ -375,14 +408,14 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
             uint32_t here = (uint32_t)(anc >> (16 * e)) & 0xffffu;
             const unsigned long long before = anc & ((1ull << (16 * e)) - 1);
             if (e > 0 && before) {
-                const float4 *x = reinterpret_cast<const float4 *>(s_b + (63 - __clzll((long long)before)) * kD + ch * 8);
-                add8(b, x[0], x[1]);
+                read8(s_b + (63 - __clzll((long long)before)) * kD + ch * 8, b);
             }
             while (here) {
                 const int a = 16 * e + __ffs((int)here) - 1;
                 here &= here - 1;
-                const float4 *x = reinterpret_cast<const float4 *>(s_b + a * kD + ch * 8);
-                add8(b, x[0], x[1]);
+                float g[8];
+                read8(s_b + a * kD + ch * 8, g);
+                add8(b, b, g);
             }
         }
         if (MP > 16) {
@@ -400,12 +433,8 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
             unpack8(qr[e], qf);
             float sk = 1.f, sq = 1.f;
             if (p.qk_norm) {  // 16 threads hold a row
-                sk = sq = 0.f;
-#pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    sk = fmaf(kf[x], kf[x], sk);
-                    sq = fmaf(qf[x], qf[x], sq);
-                }
+                sk = sum_squares8(kf);
+                sq = sum_squares8(qf);
 #pragma unroll
                 for (int off = 8; off; off >>= 1) {
                     sk += __shfl_xor_sync(0xffffffffu, sk, off);
@@ -418,29 +447,50 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
                     s_scale[MP + i] = sq;
                 }
             }
+            float up[8], down[8];
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
-                const float up = exp2_of(b[x]);
+                up[x] = exp2_of(b[x]);
+                down[x] = exp2_of(-b[x]);  // used while b is within +-kMaxRange
                 range = fmaxf(range, fabsf(b[x]));
-                kf[x] *= sk;
-                qf[x] *= sq * up;
-                ki[x] = kf[x] * exp2_of(-b[x]);  // used while b is within +-kMaxRange
-                kf[x] *= up;
             }
+            scale8(kf, kf, sk);
+            scale8(qf, qf, sq);
+            mul8(ki, kf, down);
+            mul8(kf, kf, up);
+            mul8(qf, qf, up);
             uint8_t *kq = sm + L::kq + (ch >> 3) * L::kq_panel;
             store_split8(kq, i, (ch & 7) * 8, 2 * MP, kf);
             store_split8(kq, MP + i, (ch & 7) * 8, 2 * MP, qf);
             store_split8(sm + L::ki + (ch >> 3) * L::ki_panel, i, (ch & 7) * 8, MP, ki);
         }
     }
-    tc::fence_async_smem();
+    // The state's images, half by half; half 1 is asked for once half 0 is out of the registers (and behind the fence,
+    // which waits for the loads before it).
+    auto state_images = [&] {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int row = (tid >> 4) + 16 * j, col = (tid & 15) * 8;
+            uint4 hi, lo;
+            split8(s[j], hi, lo);
+            const uint32_t at = (col >> 6) * 8192 + tc::sw128_offset(row, col & 63);
+            *reinterpret_cast<uint4 *>(sm + L::s_hi + at) = hi;
+            *reinterpret_cast<uint4 *>(sm + L::s_lo + at) = lo;
+        }
+        tc::fence_async_smem();
+    };
+    if (warp < 8) {
+        state_images();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ldg8(S + (size_t)(64 + 16 * j) * kD, s[j]);
+    }
     const bool pairwise = __syncthreads_or(!(range <= kMaxRange));
     float *sA = reinterpret_cast<float *>(sm + L::ap), *sP = sA + MP * L::ap_stride;
     if (pairwise) {
         // A warp per (node, ancestor), four channels a lane.  The results' own place holds b, so they pass through
-        // the place of K^, which is not used, and (for the larger half of MP = 64) of the state's first rows.
-        float *xA = reinterpret_cast<float *>(sm + (MP == 64 ? L::s_hi : L::ki)), *xP = xA + MP * L::ap_stride;
-        static_assert(MP == 64 ? L::ap_bytes <= 32768 + 2 * L::ki_panel : L::ap_bytes <= 2 * L::ki_panel, "");
+        // the place of K^, which is not used.
+        float *xA = reinterpret_cast<float *>(sm + L::ki), *xP = xA + MP * MP;
+        static_assert(2 * MP * MP * 4 <= 2 * L::ki_panel, "A and P pass through the place of K^");
         if (MP == 16) {
             if (tid < kD)
                 for (int i = 1; i < M; ++i) s_b[i * kD + tid] += s_b[ts.parent[i] * kD + tid];
@@ -471,12 +521,12 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
                     va = a == i ? 0.f : s_beta[i] * va;
                 }
                 if (lane == 0) {
-                    xA[i * L::ap_stride + a] = va;
-                    xP[i * L::ap_stride + a] = vp;
+                    xA[x] = va;
+                    xP[x] = vp;
                 }
             }
         __syncthreads();
-        for (int x = tid; x < 2 * MP * L::ap_stride; x += kThreads) sA[x] = xA[x];
+        for (int x = tid; x < 2 * MP * MP; x += kThreads) sA[x / MP * L::ap_stride + x % MP] = xA[x];
         __syncthreads();
     }
 
@@ -504,19 +554,21 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
         constexpr uint32_t id4 = tc::idesc_bf16_f32(128, 4 * MP, true, false);
         constexpr uint32_t id2 = tc::idesc_bf16_f32(128, 2 * MP, true, false);
         const bool elected = tc::elect_one();
-        if (!pairwise) {  // D1: hi x [hi | lo], then lo x [hi | lo]
+        // D2, half by half, 16 state rows at a time: S hi x [hi | lo] + S lo x hi; D1 between the halves, so that
+        // half 0's place is free early
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const uint32_t a = sa + L::kq + (c >> 3) * 2 * MP * 128 + ((c >> 2) & 1) * L::kq_panel + (c & 3) * 32;
-                const uint32_t b = sa + L::ki + ((c >> 2) & 1) * L::ki_panel + (c & 3) * 32;
-                tc::mma_bf16_warp(tmem + L::d1, tc::smem_desc(kKmaj, a), tc::smem_desc(kKmaj, b), id1, c > 0, elected);
-            }
-            if (elected) tc::mma_commit(&bar_d1);
-        }
+        for (int c = 0; c < 8; ++c) {
+            if (c == 4) {
+                if (!pairwise) {  // D1: hi x [hi | lo], then lo x [hi | lo]
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {  // D2, half by half, 16 state rows at a time: S hi x [hi | lo] + S lo x hi
-            if ((c & 3) == 0) {
-                ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bar_rows[c >> 2], 0));
+                    for (int e = 0; e < 16; ++e) {
+                        const uint32_t a = sa + L::kq + (e >> 3) * 2 * MP * 128 + ((e >> 2) & 1) * L::kq_panel + (e & 3) * 32;
+                        const uint32_t b = sa + L::ki + ((e >> 2) & 1) * L::ki_panel + (e & 3) * 32;
+                        tc::mma_bf16_warp(tmem + L::d1, tc::smem_desc(kKmaj, a), tc::smem_desc(kKmaj, b), id1, e > 0, elected);
+                    }
+                    if (elected) tc::mma_commit(&bar_d1);
+                }
+                ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bar_rows, 0));
                 tc::tc_fence_after();
             }
             const uint32_t a = (c & 3) * 2048, b = sa + L::kq + (c >> 2) * L::kq_panel + (c & 3) * 32;
@@ -525,27 +577,11 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
             if ((c & 3) == 3 && elected) tc::mma_commit(&bar_half[c >> 2]);
         }
         __syncwarp();
-    } else if (warp < 8) {  // the state's images, half by half
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (half) ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bar_half[0], 0));  // the place is free
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int row = (tid >> 4) + 16 * j, col = (tid & 15) * 8;
-                uint4 hi, lo;
-                split8(s[j], hi, lo);
-                const uint32_t at = (col >> 6) * 8192 + tc::sw128_offset(row, col & 63);
-                *reinterpret_cast<uint4 *>(sm + L::s_hi + at) = hi;
-                *reinterpret_cast<uint4 *>(sm + L::s_lo + at) = lo;
-            }
-            tc::fence_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bar_rows[half]);
-            if (!half) {  // only now: a fence waits for the loads before it
-#pragma unroll
-                for (int j = 0; j < 4; ++j) ldg8(S + (size_t)(64 + 16 * j) * kD, s[j]);
-            }
-        }
+    } else if (warp < 8) {
+        ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bar_half[0], 0));  // the images' place is free
+        state_images();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bar_rows);
     }
     if (warp >= kPath && warp < kPath + (MP == 16 ? 1 : 4)) {
         // A, P, T and the images that u and o are formed with
@@ -699,11 +735,14 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
                         tc::tmem_ld8x4(lanes + i0, MP, x);
                         tc::tmem_ld8x4(lanes + L::d3 + i0, MP, d);
                         residual8<MP>(sm, s_beta, x[0], x[2], i0, col, u);
+                        float y[8], out[8];
+                        add8(out, d[0], d[2]);
+                        add8(u, u, out);
+                        add8(y, x[1], x[3]);
+                        add8(out, d[1], d[3]);
+                        add8(out, out, y);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            u[e] += d[0][e] + d[2][e];
-                            s_o[(i0 + e) * kD + col] = (x[1][e] + x[3][e]) + (d[1][e] + d[3][e]);
-                        }
+                        for (int e = 0; e < 8; ++e) s_o[(i0 + e) * kD + col] = out[e];
                     }
                     if (u_out) {
                         float *out = u_out + (size_t)i0 * row_stride;

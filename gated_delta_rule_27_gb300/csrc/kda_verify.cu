@@ -38,22 +38,14 @@ constexpr float kMargin = 1e-4f;
 
 __device__ __forceinline__ unsigned long long fixed40(float x) { return __float2ull_rz(x * kFixed); }
 
-// Arithmetic on pairs, one instruction each.
-#define KDA_PAIR_OP(name, instr)                                                                                __device__ __forceinline__ float2 name(float2 a, float2 b) {                                                    float2 d;                                                                                                   asm("{\n.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\n" instr " z, x, y;\n"              "mov.b64 {%0, %1}, z;\n}\n"                                                                               : "=f"(d.x), "=f"(d.y)                                                                                      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));                                                              return d;                                                                                               }
-KDA_PAIR_OP(add2, "add.rn.f32x2")
-KDA_PAIR_OP(add_rz2, "add.rz.f32x2")
-KDA_PAIR_OP(sub2, "sub.rn.f32x2")
-KDA_PAIR_OP(mul2, "mul.rn.f32x2")
-#undef KDA_PAIR_OP
-
 // A sum of at most 8 values in [0, 1] cut to multiples of 2^-40, without 64-bit conversions: adding 1 with rounding
 // towards zero leaves the first 23 bits of the value in the sum's mantissa, adding 2^-17 to the rest the next 17;
 // the bit patterns add up as integers, and so do 32 lanes' (8 x 32 x 2^23 fits 32 bits).
 struct FixedSum {
     uint32_t hi = 0, lo = 0;
     __device__ __forceinline__ void add2(float2 x) {
-        const float2 a = add_rz2(x, make_float2(1.f, 1.f));
-        const float2 b = add_rz2(sub2(x, sub2(a, make_float2(1.f, 1.f))), make_float2(0x1p-17f, 0x1p-17f));
+        const float2 a = tc::add_rz2(x, make_float2(1.f, 1.f));
+        const float2 b = tc::add_rz2(tc::sub2(x, tc::sub2(a, make_float2(1.f, 1.f))), make_float2(0x1p-17f, 0x1p-17f));
         hi += __float_as_uint(a.x) + __float_as_uint(a.y) - 2 * 0x3f800000u;
         lo += __float_as_uint(b.x) + __float_as_uint(b.y) - 2 * 0x37000000u;
     }
@@ -85,11 +77,11 @@ __device__ __forceinline__ float excess_of(float w, float C, float q) { return f
 // Pairs of the same.  `plain`: the row has neither a NaN nor a +inf logit.
 __device__ __forceinline__ float2 weights_of(const Row &r, bool plain, float2 l) {
     if (!plain) return make_float2(weight_of(r, l.x), weight_of(r, l.y));
-    const float2 x = mul2(sub2(l, make_float2(r.top, r.top)), make_float2(r.scale, r.scale));
+    const float2 x = tc::mul2(tc::sub2(l, make_float2(r.top, r.top)), make_float2(r.scale, r.scale));
     return make_float2(exp2_of(x.x), exp2_of(x.y));
 }
 __device__ __forceinline__ float2 excesses_of(float2 w, float C, float2 q) {
-    const float2 x = sub2(w, mul2(make_float2(C, C), q));
+    const float2 x = tc::sub2(w, tc::mul2(make_float2(C, C), q));
     return make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f));
 }
 
@@ -414,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
                         part.get(v, l);
 #pragma unroll
                         for (int e = 0; e < P::kVec; e += 2)
-                            sum = add2(sum, weights_of(warps, true, make_float2(l[e], l[e + 1])));
+                            sum = tc::add2(sum, weights_of(warps, true, make_float2(l[e], l[e + 1])));
                     }
                     f.sum = sum.x + sum.y;
                 }
