@@ -554,20 +554,18 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
         constexpr uint32_t id4 = tc::idesc_bf16_f32(128, 4 * MP, true, false);
         constexpr uint32_t id2 = tc::idesc_bf16_f32(128, 2 * MP, true, false);
         const bool elected = tc::elect_one();
-        // D2, half by half, 16 state rows at a time: S hi x [hi | lo] + S lo x hi; D1 between the halves, so that
-        // half 0's place is free early
+        if (!pairwise) {  // D1: hi x [hi | lo], then lo x [hi | lo]
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+            for (int c = 0; c < 16; ++c) {
+                const uint32_t a = sa + L::kq + (c >> 3) * 2 * MP * 128 + ((c >> 2) & 1) * L::kq_panel + (c & 3) * 32;
+                const uint32_t b = sa + L::ki + ((c >> 2) & 1) * L::ki_panel + (c & 3) * 32;
+                tc::mma_bf16_warp(tmem + L::d1, tc::smem_desc(kKmaj, a), tc::smem_desc(kKmaj, b), id1, c > 0, elected);
+            }
+            if (elected) tc::mma_commit(&bar_d1);
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {  // D2, half by half, 16 state rows at a time: S hi x [hi | lo] + S lo x hi
             if (c == 4) {
-                if (!pairwise) {  // D1: hi x [hi | lo], then lo x [hi | lo]
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const uint32_t a = sa + L::kq + (e >> 3) * 2 * MP * 128 + ((e >> 2) & 1) * L::kq_panel + (e & 3) * 32;
-                        const uint32_t b = sa + L::ki + ((e >> 2) & 1) * L::ki_panel + (e & 3) * 32;
-                        tc::mma_bf16_warp(tmem + L::d1, tc::smem_desc(kKmaj, a), tc::smem_desc(kKmaj, b), id1, e > 0, elected);
-                    }
-                    if (elected) tc::mma_commit(&bar_d1);
-                }
                 ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bar_rows, 0));
                 tc::tc_fence_after();
             }
@@ -592,28 +590,32 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
         if (w * 32 < 2 * MP) read_paths<MP>(sm, ts, s_beta, tmem, M, w * 32 + lane, pairwise, &s_wild);
         float zero = 0.f;
         if constexpr (MP < 64) {
-            // one warp (MP = 16: its lower half) writes T - I, the other (half) forms G = P T from the same T
+            // MP = 32: one warp writes T - I, another forms G = P T from the same T.  MP = 16: T - I only, G is left to
+            // the warps below.
             if (MP == 32) tc::named_barrier(1, 128);
             else __syncwarp();
-            const int j = MP == 16 ? lane & 15 : lane;
-            const bool is_t = MP == 16 ? lane < 16 : w == 0;
             if (MP == 16 || w < 2) {
                 float tc_[MP];
-                invert_block<MP>(sA, L::ap_stride, j, tc_);
-                if (is_t) {
+                invert_block<MP>(sA, L::ap_stride, lane, tc_);
+                if (w == 0) {
+                    if (lane < MP)
 #pragma unroll
-                    for (int i = 0; i < MP; ++i) tb[i * L::ap_stride + j] = i == j ? 0.f : tc_[i];
+                        for (int i = 0; i < MP; ++i) tb[i * L::ap_stride + lane] = i == lane ? 0.f : tc_[i];
                 } else {
-                    multiply_block<MP>(sP, L::ap_stride, tc_, tb + MP * L::ap_stride + j);
+                    multiply_block<MP>(sP, L::ap_stride, tc_, tb + MP * L::ap_stride + lane);
                 }
             }
-            if (MP == 32) tc::named_barrier(1, 128);
-            else __syncwarp();
-            for (int x = w * 32 + lane; x < 2 * MP * (MP / 8); x += MP == 16 ? 32 : 128) {
+            if (MP == 32) {
+                tc::named_barrier(1, 128);
+            } else {
+                __syncwarp();
+                tc::named_barrier_arrive(2, 160);
+            }
+            constexpr int kRows = MP == 16 ? MP : 2 * MP;
+            for (int x = w * 32 + lane; x < kRows * (MP / 8); x += MP == 16 ? 32 : 128) {
                 const int row = x / (MP / 8), c0 = x % (MP / 8) * 8;
-                const float4 *from = reinterpret_cast<const float4 *>(tb + row * L::ap_stride + c0);
-                const float4 f0 = from[0], f1 = from[1];
-                const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+                float f[8];
+                read8(tb + row * L::ap_stride + c0, f);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) zero = fmaf(f[e], 0.f, zero);
                 store_split8(sm + L::t_img, row, c0, 2 * MP, f);
@@ -673,16 +675,34 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
                 tc::cp_async16(sm + L::z + i * 16, p.gate + base + (size_t)(i >> 4) * row_stride + (i & 15) * 8);
         }
     }
-    // A thread is a state column from here on; two warps share a quarter of TMEM's lanes and take half of the nodes
-    // each (for r only where no warp is busy with T).
+    if (MP == 16 && warp >= 4 && warp < 8) {
+        // G = P T, four rows a warp, two a lane (column lane mod 16).  Warp 8's T - I and P are awaited.
+        const float *sT = reinterpret_cast<const float *>(sm + L::tg);
+        tc::named_barrier(2, 160);
+        const int j = lane & 15;
+        float t16[16], zero = 0.f;
+#pragma unroll
+        for (int a = 0; a < 16; ++a) t16[a] = sT[a * L::ap_stride + j] + (a == j ? 1.f : 0.f);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = 4 * (warp - 4) + 2 * (lane >> 4) + e;
+            const float x = row_dot<16>(sP + i * L::ap_stride, t16);
+            zero = fmaf(x, 0.f, zero);
+            store_split1(sm + L::t_img, MP + i, j, 2 * MP, x);
+        }
+        if (zero != 0.f) s_wild = 1;
+        tc::fence_async_smem();
+    }
+    // A thread is a state column from here on.  Four warps form r; for u and o two warps share a quarter of TMEM's
+    // lanes and take half of the nodes each.
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const int col = tid & (kD - 1), side = warp >> 2;
-    constexpr int kHalf = MP / 2, kSides = MP == 16 ? 2 : 1;
-    if (warp < 4 * kSides) {  // r, for D3
+    constexpr int kHalf = MP / 2;
+    if (warp < 4) {  // r, for D3
         ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bar_half[1], 0));
         tc::tc_fence_after();
         float zero = 0.f;
-        for (int i0 = side * (MP / kSides); i0 < (side + 1) * (MP / kSides); i0 += 8) {
+        for (int i0 = 0; i0 < MP; i0 += 8) {
             float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (i0 < M) {
                 float x[2][8];
