@@ -1,0 +1,562 @@
+// kda_tree_mma.cu -- the draft-tree step with the state in registers: bf16 inputs, d = 128, trees of up to 32 nodes.
+//
+// The mathematics is that of kda_tree_tc.cu: with K~ = k e^b, Q~ = q e^b, K^ = k e^{-b},
+//     A, P = [K~ ; Q~] K^^T (masked to the paths),   X^T, Y^T = S^T [K~ ; Q~]^T,
+//     R = beta (V - X),   U^T = R^T + R^T (T - I)^T with T = (I + A)^{-1},   O^T = Y^T + U^T P^T.
+// Small trees leave each state element a few multiply-adds; what bounds the step is the state's way to the tensor
+// core.  Here a warp owns 32 state columns and loads them as the MMA's A fragments: a lane's float4 of four
+// neighbouring columns is four rows of two 16-column tiles, and state rows 2t, 2t + 1 pair up as bf16.  The state
+// never passes through shared memory, X and Y come out as fragments that are R's and U's A operands as they are,
+// and from the state's load to the stores of u and o a warp waits for no other but for T and the norm of o.
+// (The legacy MMA is the right one here: 16 nodes take 1728 clocks of it per head, below the 4000 in which the
+// SM's share of HBM delivers the head's state; through tcgen05 the operand's conversion and staging took longer
+// than the products.)
+//
+// u is formed to fp32 accuracy as there: every operand in two bf16 parts, hi hi + hi lo + lo hi in fp32.
+#include "kda_tree_bf16.cuh"
+
+namespace kda {
+namespace {
+using namespace tree16;
+
+constexpr int kD = 128, kThreads = 128, kWarps = 4;
+
+// Shared memory for trees of at most MP nodes, in bytes.  A fragment tile holds eight nodes (rows of K~, then Q~,
+// then K^) by 16 channels: for lane l the bf16 pairs of node l / 4, channels 2 (l % 4) on and 8 further, hi parts
+// then lo parts.  It is a B operand, and two of them, for 16 nodes, an A operand.
+template <int MP>
+struct Layout {
+    static constexpr int tiles = MP / 8;
+    static constexpr uint32_t frag_bytes = 528;          // 32 lanes x 16 bytes, and 16 against bank conflicts
+    static constexpr int ap_stride = MP + 4;
+    static constexpr uint32_t ap_bytes = 2 * MP * ap_stride * 4;
+    static constexpr uint32_t frag = 0;
+    static constexpr uint32_t inv = frag + 2 * tiles * 8 * frag_bytes;  // K^'s tiles
+    static constexpr uint32_t b = inv + tiles * 8 * frag_bytes;         // fp32 [MP][128]: g, then (MP > 16) b
+    static constexpr uint32_t b_bytes = MP * 512 > ap_bytes ? MP * 512 : ap_bytes;
+    static constexpr uint32_t row = 320;                 // bytes between rows of v and the gate (bank conflicts)
+    static constexpr uint32_t v = b + b_bytes;
+    static constexpr uint32_t z = v + MP * row;
+    static constexpr uint32_t w = z + MP * row;
+    static constexpr uint32_t total = w + 512;
+    // later uses of the same bytes
+    static constexpr uint32_t ap = b;                    // fp32 A [MP][ap_stride], then P (once the tiles are built)
+    static constexpr uint32_t t = inv;                   // fp32 T - I [MP][ap_stride] (once A and P are formed)
+    static constexpr uint32_t x = frag;                  // the masked solve's r, then y: fp32 [MP][128] each
+};
+
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// c += hi hi + lo hi + hi lo; b: {hi, hi, lo, lo}
+__device__ __forceinline__ void mma_split(float (&c)[4], const uint32_t (&hi)[4], const uint32_t (&lo)[4], const uint4 &b) {
+    mma(c, hi, b.x, b.y);
+    mma(c, lo, b.x, b.y);
+    mma(c, hi, b.z, b.w);
+}
+// A pair of values as bf16 pairs, hi and lo.
+__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
+    hi = pack2(x, y);
+    const float2 rest = tc::sub2(make_float2(x, y), make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)));
+    lo = pack2(rest.x, rest.y);
+}
+__device__ __forceinline__ float4 ldg4(const float *p) {
+    float4 f;
+    asm volatile("ld.global.L1::no_allocate.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "l"(p));
+    return f;
+}
+__device__ __forceinline__ float4 read4(const uint8_t *p) {  // four bf16
+    const uint2 x = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
+                       __uint_as_float(x.y & 0xffff0000u));
+}
+
+// Writes eight channels (chunk ch of 16) of node i to its fragment tile.
+template <int MP>
+__device__ __forceinline__ void store_frag(uint8_t *tiles, int i, int ch, const float (&f)[8]) {
+    uint8_t *at = tiles + ((i >> 3) * 8 + (ch >> 1)) * Layout<MP>::frag_bytes + (i & 7) * 64 + (ch & 1) * 4;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        uint32_t hi, lo;
+        split2(f[2 * t], f[2 * t + 1], hi, lo);
+        *reinterpret_cast<uint32_t *>(at + t * 16) = hi;
+        *reinterpret_cast<uint32_t *>(at + t * 16 + 8) = lo;
+    }
+}
+template <int MP>
+__device__ __forceinline__ uint4 load_frag(const uint8_t *tiles, int tile, int step) {
+    return *reinterpret_cast<const uint4 *>(tiles + (tile * 8 + step) * Layout<MP>::frag_bytes + (threadIdx.x & 31) * 16);
+}
+
+// The fragments c of a product over nodes, as the A operand of the next: node tiles 2 s and 2 s + 1.
+template <int NT>
+__device__ __forceinline__ void as_operand(const float (&c)[NT][4], int s, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+    split2(c[2 * s][0], c[2 * s][1], hi[0], lo[0]);
+    split2(c[2 * s][2], c[2 * s][3], hi[1], lo[1]);
+    if (2 * s + 1 < NT) {
+        split2(c[(2 * s + 1) % NT][0], c[(2 * s + 1) % NT][1], hi[2], lo[2]);
+        split2(c[(2 * s + 1) % NT][2], c[(2 * s + 1) % NT][3], hi[3], lo[3]);
+    } else {
+        hi[2] = hi[3] = lo[2] = lo[3] = 0u;
+    }
+}
+// c[m][n] += A[m] M^T over the nodes, M a lower triangular fp32 matrix in shared memory.
+template <int NT>
+__device__ __forceinline__ void times_transposed(float (&c)[2][NT][4], const float (&a)[2][NT][4], const float *M, int stride) {
+    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+#pragma unroll
+    for (int s = 0; s < (NT + 1) / 2; ++s) {
+        uint32_t hi[2][4], lo[2][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) as_operand<NT>(a[m], s, hi[m], lo[m]);
+#pragma unroll
+        for (int n = 2 * s; n < NT; ++n) {
+            const float *at = M + (n * 8 + g) * stride + 16 * s + 2 * t;
+            const float2 x = *reinterpret_cast<const float2 *>(at);
+            uint4 b;
+            split2(x.x, x.y, b.x, b.z);
+            b.y = b.w = 0u;
+            if (2 * s + 1 < NT) {
+                const float2 y = *reinterpret_cast<const float2 *>(at + 8);
+                split2(y.x, y.y, b.y, b.w);
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m) mma_split(c[m][n], hi[m], lo[m], b);
+        }
+    }
+}
+
+// u and o of one state column by forward substitution over the paths' entries only (r and y in shared memory; u
+// goes back to r's place, o to y's).
+template <int MP>
+__device__ void solve_masked(uint8_t *sm, const TreeShared &ts, int M, int c) {
+    using L = Layout<MP>;
+    const float *sA = reinterpret_cast<const float *>(sm + L::ap), *sP = sA + MP * L::ap_stride;
+    float *r = reinterpret_cast<float *>(sm + L::x), *y = r + MP * kD;
+    for (int i = 0; i < M; ++i) {
+        float w = r[i * kD + c], out = y[i * kD + c];
+        for (int a = 0; a < i; ++a) {
+            if ((ts.anc[i] >> a) & 1) {
+                w = fmaf(-sA[i * L::ap_stride + a], r[a * kD + c], w);
+                out = fmaf(sP[i * L::ap_stride + a], r[a * kD + c], out);
+            }
+        }
+        r[i * kD + c] = w;
+        y[i * kD + c] = fmaf(sP[i * L::ap_stride + i], w, out);
+    }
+}
+
+template <int MP>
+__global__ void __launch_bounds__(kThreads, MP == 32 ? 2 : 4) tree_step_mma_kernel(const Args p) {
+    using L = Layout<MP>;
+    constexpr int NT = MP / 8;
+    extern __shared__ __align__(16) uint8_t sm[];
+    __shared__ TreeShared ts;
+    __shared__ __align__(16) float s_beta[MP];
+    __shared__ float s_scale[2 * MP], s_square[kWarps][MP];
+    __shared__ int s_wild;  // A, P or T holds something that is not finite
+    const int n = blockIdx.x / p.H, h = blockIdx.x % p.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t4 = lane & 3;
+    const Tree t = tree_rows(p.cu, n, p.total_nodes, p.max_nodes);
+    const int slot = slot_of(p.seq_idx, n, p.num_slots);
+    if (t.nodes < 0 || slot < 0) {
+        if (tid == 0) report_invalid(p.status);
+        return;
+    }
+    if (t.nodes == 0) return;
+    const int M = t.nodes;
+    const size_t base = ((size_t)t.row0 * p.H + h) * kD, row_stride = (size_t)p.H * kD;
+
+    // The CTA's reads, issued at once: g, v, the gate and its weight on their way to shared memory; k, q and the
+    // first half of the warp's state columns to registers.
+    constexpr int kUnits = MP / 8;  // (node, 8 channels) per thread: node (tid / 16) + 8 e, channels 8 (tid % 16) on
+    uint4 kr[kUnits], qr[kUnits];
+    for (int i = tid; i < M * 32; i += kThreads)
+        tc::cp_async16(sm + L::b + i * 16, p.g + base + (size_t)(i >> 5) * row_stride + (i & 31) * 4);
+#pragma unroll
+    for (int e = 0; e < kUnits; ++e) {
+        const int i = (tid >> 4) + 8 * e;
+        kr[e] = qr[e] = make_uint4(0, 0, 0, 0);
+        if (i < M) {
+            kr[e] = __ldg(reinterpret_cast<const uint4 *>(p.k + base + (size_t)i * row_stride) + (tid & 15));
+            qr[e] = __ldg(reinterpret_cast<const uint4 *>(p.q + base + (size_t)i * row_stride) + (tid & 15));
+        }
+    }
+    for (int i = tid; i < M * 16; i += kThreads) {
+        tc::cp_async16(sm + L::v + (i >> 4) * L::row + (i & 15) * 16, p.v + base + (size_t)(i >> 4) * row_stride + (i & 15) * 8);
+        if (p.gate)
+            tc::cp_async16(sm + L::z + (i >> 4) * L::row + (i & 15) * 16, p.gate + base + (size_t)(i >> 4) * row_stride + (i & 15) * 8);
+    }
+    if (warp == 1) {
+        if (p.gate && p.weight) tc::cp_async16(sm + L::w + lane * 16, p.weight + lane * 4);
+        else *reinterpret_cast<float4 *>(sm + L::w + lane * 16) = make_float4(1.f, 1.f, 1.f, 1.f);
+    }
+    // step ks of 16 state rows: the lane's rows 2 t, 2 t + 1 and 8 further, columns 4 g on of the warp's 32
+    const float *S = p.S_pool + ((size_t)slot * p.H + h) * kD * kD + (size_t)(2 * t4) * kD + warp * 32 + g * 4;
+    float4 s[4][4];
+    auto load_state = [&](int ks) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[ks & 3][j] = ldg4(S + (size_t)(16 * ks + (j & 1) + 8 * (j >> 1)) * kD);
+    };
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) load_state(ks);
+    if (warp == 2) {
+        for (int i = lane; i < MP; i += 32) s_beta[i] = i < M ? p.beta[(size_t)(t.row0 + i) * p.H + h] : 0.f;
+        if (lane == 0) s_wild = 0;
+    }
+    tc::cp_async_wait_all();
+    for (int i = tid; i < M * 32; i += kThreads) {  // the vectors that this thread copied
+        float4 *x = reinterpret_cast<float4 *>(sm + L::b + i * 16);
+        *x = log2_decay4(*x);
+    }
+    // The last warp looks up the CTA that starts about when this one ends, and asks for its inputs further down.
+    const int later = blockIdx.x + p.ahead;
+    Tree lt{0, 0};
+    int lslot = -1;
+    if (warp == 3 && later < gridDim.x) {
+        lt = tree_rows(p.cu, later / p.H, p.total_nodes, p.max_nodes);
+        lslot = slot_of(p.seq_idx, later / p.H, p.num_slots);
+    }
+    if (read_tree(ts, p.parent, p.cu, n, p.total_nodes, p.max_nodes, true, 0).nodes < 0) {  // a block barrier
+        if (tid == 0) report_invalid(p.status);
+        return;
+    }
+
+    // Fragment tiles of K~, Q~ and K^.  b sums g over the path; above 16 nodes, 16 nodes at a time, from the b of
+    // the nearest ancestor in an earlier group.
+    float *s_b = reinterpret_cast<float *>(sm + L::b);
+    float range = 0.f;
+#pragma unroll
+    for (int first = 0; first < MP; first += 16) {
+        constexpr int kGroup = MP < 16 ? 1 : 2;  // units of this thread in a group of 16 nodes
+        float b[kGroup][8];
+#pragma unroll
+        for (int e = 0; e < kGroup; ++e) {
+            const int i = first + (tid >> 4) + 8 * e, ch = tid & 15;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) b[e][x] = 0.f;
+            if (i < M) {
+                const unsigned long long anc = ts.anc[i], before = anc & ((1ull << first) - 1);
+                uint32_t here = (uint32_t)(anc >> first) & 0xffffu;
+                if (first > 0 && before) read8(s_b + (63 - __clzll((long long)before)) * kD + ch * 8, b[e]);
+                while (here) {
+                    float x[8];
+                    read8(s_b + (first + __ffs((int)here) - 1) * kD + ch * 8, x);
+                    here &= here - 1;
+                    add8(b[e], b[e], x);
+                }
+            }
+        }
+        if (MP > 16) {
+            __syncthreads();  // every sum of this group is formed
+#pragma unroll
+            for (int e = 0; e < kGroup; ++e) {
+                const int i = first + (tid >> 4) + 8 * e, ch = tid & 15;
+                if (i < M) {
+                    float4 *x = reinterpret_cast<float4 *>(s_b + i * kD + ch * 8);
+                    x[0] = make_float4(b[e][0], b[e][1], b[e][2], b[e][3]);
+                    x[1] = make_float4(b[e][4], b[e][5], b[e][6], b[e][7]);
+                }
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int e = 0; e < kGroup; ++e) {
+            const int u = first / 8 + e, i = first + (tid >> 4) + 8 * e, ch = tid & 15;
+            if (first + (warp << 1) + 8 * e >= M) break;  // (of the warp's two nodes; what the tiles hold past the tree is not looked at)
+            float kf[8], qf[8], ki[8], up[8], down[8];
+            unpack8(kr[u], kf);
+            unpack8(qr[u], qf);
+            float sk = 1.f, sq = 1.f;
+            if (p.qk_norm) {  // 16 threads hold a row
+                sk = sum_squares8(kf);
+                sq = sum_squares8(qf);
+#pragma unroll
+                for (int off = 8; off; off >>= 1) {
+                    sk += __shfl_xor_sync(0xffffffffu, sk, off);
+                    sq += __shfl_xor_sync(0xffffffffu, sq, off);
+                }
+                sk = rsqrtf(sk + p.qk_eps);
+                sq = rsqrtf(sq + p.qk_eps);
+                if (ch == 0) {
+                    s_scale[i] = sk;
+                    s_scale[MP + i] = sq;
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                up[x] = exp2_of(b[e][x]);
+                down[x] = exp2_of(-b[e][x]);  // used while b is within +-kMaxRange
+                range = fmaxf(range, fabsf(b[e][x]));
+            }
+            scale8(kf, kf, sk);
+            scale8(qf, qf, sq);
+            mul8(ki, kf, down);
+            mul8(kf, kf, up);
+            mul8(qf, qf, up);
+            store_frag<MP>(sm + L::frag, i, ch, kf);
+            store_frag<MP>(sm + L::frag + NT * 8 * L::frag_bytes, i, ch, qf);
+            store_frag<MP>(sm + L::inv, i, ch, ki);
+        }
+    }
+    const bool pairwise = __syncthreads_or(!(range <= kMaxRange));
+
+    float *sA = reinterpret_cast<float *>(sm + L::ap), *sP = sA + MP * L::ap_stride;
+    if (pairwise) {
+        // A warp per (node, ancestor), four channels a lane.  The results' own place holds b, so they pass through
+        // the place of K^, which is not used.
+        float *xA = reinterpret_cast<float *>(sm + L::inv), *xP = xA + MP * MP;
+        static_assert(2 * MP * MP * 4 <= NT * 8 * L::frag_bytes, "A and P pass through the place of K^");
+        if (MP <= 16) {
+            for (int i = 1; i < M; ++i) s_b[i * kD + tid] += s_b[ts.parent[i] * kD + tid];
+            __syncthreads();
+        }
+        for (int x = warp; x < MP * MP; x += kWarps) {
+            const int i = x / MP, a = x % MP;
+            float va = 0.f, vp = 0.f;
+            if (i < M && ((ts.anc[i] >> a) & 1)) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = lane + 32 * e;
+                    const float ka = __bfloat162float(p.k[base + (size_t)a * row_stride + c]) * exp2_of(s_b[i * kD + c] - s_b[a * kD + c]);
+                    va = fmaf(__bfloat162float(p.k[base + (size_t)i * row_stride + c]), ka, va);
+                    vp = fmaf(__bfloat162float(p.q[base + (size_t)i * row_stride + c]), ka, vp);
+                }
+#pragma unroll
+                for (int off = 16; off; off >>= 1) {
+                    va += __shfl_xor_sync(0xffffffffu, va, off);
+                    vp += __shfl_xor_sync(0xffffffffu, vp, off);
+                }
+                if (p.qk_norm) {
+                    va *= s_scale[i] * s_scale[a];
+                    vp *= s_scale[MP + i] * s_scale[a];
+                }
+                va = a == i ? 0.f : s_beta[i] * va;
+            }
+            if (lane == 0) {
+                xA[x] = va;
+                xP[x] = vp;
+                if (fmaf(va, 0.f, vp * 0.f) != 0.f) s_wild = 1;
+            }
+        }
+        __syncthreads();
+        for (int x = tid; x < 2 * MP * MP; x += kThreads) sA[x / MP * L::ap_stride + x % MP] = xA[x];
+    } else {
+        // 16 rows of [K~ ; Q~] by eight nodes a warp and turn (MP = 8: the rows of K~ and Q~ in one)
+        constexpr int kRowTiles = MP == 8 ? 1 : 2 * NT / 2;
+        float zero = 0.f;
+        for (int task = warp; task < kRowTiles * NT; task += kWarps) {
+            const int m = task / NT, nt = task % NT;  // rows 16 m on of [K~ ; Q~], ancestors 8 nt on
+            if (MP > 16 && 8 * nt > (16 * m) % MP + 15) continue;
+            float c[3][4] = {};
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+                const uint4 lo_rows = load_frag<MP>(sm + L::frag, 2 * m, ks), hi_rows = load_frag<MP>(sm + L::frag, 2 * m + 1, ks);
+                const uint4 b = load_frag<MP>(sm + L::inv, nt, ks);
+                const uint32_t hi[4] = {lo_rows.x, hi_rows.x, lo_rows.y, hi_rows.y}, lo[4] = {lo_rows.z, hi_rows.z, lo_rows.w, hi_rows.w};
+                mma(c[0], hi, b.x, b.y);
+                mma(c[1], lo, b.x, b.y);
+                mma(c[2], hi, b.z, b.w);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = 16 * m + g + 8 * e, i = row % MP, a = 8 * nt + 2 * t4;
+                const bool is_a = row < MP;
+                const unsigned long long anc = i < M ? ts.anc[i] : 0ull;
+                const float scale = is_a ? s_beta[i] : 1.f;
+                float2 val;
+                val.x = (anc >> a) & 1 && !(is_a && a == i) ? scale * (c[0][2 * e] + c[1][2 * e] + c[2][2 * e]) : 0.f;
+                val.y = (anc >> (a + 1)) & 1 && !(is_a && a + 1 == i) ? scale * (c[0][2 * e + 1] + c[1][2 * e + 1] + c[2][2 * e + 1]) : 0.f;
+                zero = fmaf(val.x, 0.f, fmaf(val.y, 0.f, zero));
+                *reinterpret_cast<float2 *>((is_a ? sA : sP) + i * L::ap_stride + a) = val;
+            }
+        }
+        if (zero != 0.f) s_wild = 1;
+    }
+    __syncthreads();  // A and P are complete, and K^ is no longer needed
+    if (warp == 0) {  // T - I, a column a lane
+        float *sT = reinterpret_cast<float *>(sm + L::t);
+        float tc_[MP], zero = 0.f;
+        invert_block<MP>(sA, L::ap_stride, lane, tc_);
+        if (lane < MP) {
+#pragma unroll
+            for (int i = 0; i < MP; ++i) {
+                zero = fmaf(tc_[i], 0.f, zero);
+                sT[i * L::ap_stride + lane] = i == lane ? 0.f : tc_[i];
+            }
+            if (zero != 0.f) s_wild = 1;
+        }
+    } else if (warp == 3 && lslot >= 0 && lt.nodes > 0) {
+        const int lh = later % p.H;
+        if (lane < 2)
+            tc::bulk_prefetch_l2(p.S_pool + (((size_t)lslot * p.H + lh) * kD + 64 * lane) * kD, 32768);
+        // the nodes' rows by 128-byte lines: four of g, two each of k, q, v and the gate
+        for (int i = lane; i < lt.nodes * 4; i += 32) {
+            const size_t at = ((size_t)(lt.row0 + (i >> 2)) * p.H + lh) * kD;
+            tc::prefetch_l2(p.g + at + (i & 3) * 32);
+            const __nv_bfloat16 *x = i & 2 ? p.k : p.q, *y = i & 2 ? p.v : p.gate;
+            tc::prefetch_l2(x + at + (i & 1) * 64);
+            if (y) tc::prefetch_l2(y + at + (i & 1) * 64);
+        }
+    }
+
+    // X^T and Y^T of the warp's 32 columns, 16 state rows at a time
+    float x[2][NT][4], y[2][NT][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[m][j][e] = y[m][j][e] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+        // tile m holds the lane's columns 2 m (rows g of the tile) and 2 m + 1 (rows g + 8)
+        uint32_t hi[2][4], lo[2][4];
+        const float4 *r = s[ks & 3];
+#pragma unroll
+        for (int k8 = 0; k8 < 2; ++k8) {
+            split2(r[2 * k8].x, r[2 * k8 + 1].x, hi[0][2 * k8], lo[0][2 * k8]);
+            split2(r[2 * k8].y, r[2 * k8 + 1].y, hi[0][2 * k8 + 1], lo[0][2 * k8 + 1]);
+            split2(r[2 * k8].z, r[2 * k8 + 1].z, hi[1][2 * k8], lo[1][2 * k8]);
+            split2(r[2 * k8].w, r[2 * k8 + 1].w, hi[1][2 * k8 + 1], lo[1][2 * k8 + 1]);
+        }
+        if (ks + 4 < 8) load_state(ks + 4);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            if (MP > 8 && 8 * j >= M) break;
+            const uint4 bk = load_frag<MP>(sm + L::frag, j, ks), bq = load_frag<MP>(sm + L::frag, NT + j, ks);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                mma_split(x[m][j], hi[m], lo[m], bk);
+                mma_split(y[m][j], hi[m], lo[m], bq);
+            }
+        }
+    }
+    // R.  Of tile j the lane holds nodes 8 j + 2 t4 + {0, 1}, four neighbouring columns of each.
+    const int col = warp * 32 + g * 4;
+    float zero = 0.f;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = 8 * j + 2 * t4 + e;
+            const float4 v = read4(sm + L::v + i * L::row + col * 2);
+            const float beta = s_beta[i];
+            const bool in = i < M;
+            x[0][j][e] = in ? beta * (v.x - x[0][j][e]) : 0.f;
+            x[0][j][2 + e] = in ? beta * (v.y - x[0][j][2 + e]) : 0.f;
+            x[1][j][e] = in ? beta * (v.z - x[1][j][e]) : 0.f;
+            x[1][j][2 + e] = in ? beta * (v.w - x[1][j][2 + e]) : 0.f;
+            zero = fmaf(x[0][j][e], 0.f, fmaf(x[0][j][2 + e], 0.f, zero));
+            zero = fmaf(x[1][j][e], 0.f, fmaf(x[1][j][2 + e], 0.f, zero));
+        }
+    if (zero != 0.f) s_wild = 1;
+    __syncthreads();  // T is complete
+    if (!s_wild) {
+        float u[2][NT][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) u[m][j][e] = x[m][j][e];
+        times_transposed<NT>(u, x, reinterpret_cast<const float *>(sm + L::t), L::ap_stride);
+        if (p.u) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int i = 8 * j + 2 * t4 + e;
+                    if (i < M)
+                        *reinterpret_cast<float4 *>(p.u + base + (size_t)i * row_stride + col) =
+                            make_float4(u[0][j][e], u[0][j][2 + e], u[1][j][e], u[1][j][2 + e]);
+                }
+        }
+        times_transposed<NT>(y, u, sP, L::ap_stride);
+    } else {
+        float *sr = reinterpret_cast<float *>(sm + L::x), *sy = sr + MP * kD;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 8 * j + 2 * t4 + e;
+                *reinterpret_cast<float4 *>(sr + i * kD + col) = make_float4(x[0][j][e], x[0][j][2 + e], x[1][j][e], x[1][j][2 + e]);
+                *reinterpret_cast<float4 *>(sy + i * kD + col) = make_float4(y[0][j][e], y[0][j][2 + e], y[1][j][e], y[1][j][2 + e]);
+            }
+        __syncthreads();
+        solve_masked<MP>(sm, ts, M, tid);
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 8 * j + 2 * t4 + e;
+                const float4 o = *reinterpret_cast<const float4 *>(sy + i * kD + col);
+                y[0][j][e] = o.x; y[0][j][2 + e] = o.y; y[1][j][e] = o.z; y[1][j][2 + e] = o.w;
+                if (p.u && i < M)
+                    *reinterpret_cast<float4 *>(p.u + base + (size_t)i * row_stride + col) = *reinterpret_cast<const float4 *>(sr + i * kD + col);
+            }
+    }
+    if (p.gate) {  // the rows' squares: this lane's columns, the warp's, all
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float ss = fmaf(y[0][j][e], y[0][j][e], fmaf(y[0][j][2 + e], y[0][j][2 + e],
+                                                             fmaf(y[1][j][e], y[1][j][e], y[1][j][2 + e] * y[1][j][2 + e])));
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+                if (g == 0) s_square[warp][8 * j + 2 * t4 + e] = ss;
+            }
+        __syncthreads();
+    }
+    const float4 w = *reinterpret_cast<const float4 *>(sm + L::w + col * 4);
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = 8 * j + 2 * t4 + e;
+            if (i >= M) continue;
+            float4 o = make_float4(y[0][j][e], y[0][j][2 + e], y[1][j][e], y[1][j][2 + e]);
+            if (p.gate) {
+                const float4 z = read4(sm + L::z + i * L::row + col * 2);
+                const float ss = (s_square[0][i] + s_square[1][i]) + (s_square[2][i] + s_square[3][i]);
+                const float inv = rsqrtf(ss * (1.f / kD) + p.out_eps);
+                o.x *= inv * w.x * gate_of(z.x);
+                o.y *= inv * w.y * gate_of(z.y);
+                o.z *= inv * w.z * gate_of(z.z);
+                o.w *= inv * w.w * gate_of(z.w);
+            }
+            *reinterpret_cast<uint2 *>(p.o + base + (size_t)i * row_stride + col) = make_uint2(pack2(o.x, o.y), pack2(o.z, o.w));
+        }
+}
+
+template <int MP>
+cudaError_t launch_mp(Args p, int ctas, cudaStream_t st) {
+    constexpr int smem = Layout<MP>::total;
+    int sms = 0;
+    cudaError_t e = allow_smem<tree_step_mma_kernel<MP>>(smem);
+    if (e == cudaSuccess) e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    p.ahead = sms * (MP == 32 ? 2 : 4);  // the CTAs that run at once
+    tree_step_mma_kernel<MP><<<ctas, kThreads, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_tree_step_mma(const TreeStepArgs &a, cudaStream_t st) {
+    const Args p{(const __nv_bfloat16 *)a.q, (const __nv_bfloat16 *)a.k, (const __nv_bfloat16 *)a.v, a.g, a.beta,
+                 a.parent, a.cu, a.seq_idx, a.H, a.total_nodes, a.max_nodes, a.num_slots, 0, a.S_pool,
+                 (__nv_bfloat16 *)a.o, a.u, a.status, a.fu.qk_norm, a.fu.qk_eps, (const __nv_bfloat16 *)a.fu.gate,
+                 a.fu.weight, a.fu.out_eps};
+    const int ctas = a.num_seqs * a.H;
+    if (a.max_nodes <= 8) return launch_mp<8>(p, ctas, st);
+    if (a.max_nodes <= 16) return launch_mp<16>(p, ctas, st);
+    return launch_mp<32>(p, ctas, st);
+}
+
+}  // namespace kda
