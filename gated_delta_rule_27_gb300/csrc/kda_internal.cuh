@@ -321,8 +321,9 @@ struct DraftVerifyArgs {
     int32_t *path, *path_len, *next_token, *status;
 };
 cudaError_t launch_tree_step(const TreeStepArgs &a, kda_dtype dt, cudaStream_t st);
-cudaError_t launch_tree_step_tc(const TreeStepArgs &a, cudaStream_t st);   // bf16, d = 128 (kda_tree_tc.cu)
-cudaError_t launch_tree_step_mma(const TreeStepArgs &a, cudaStream_t st);  // the same for up to 32 nodes (kda_tree_mma.cu)
+// bf16, d = 128: trees of up to 16 nodes (kda_tree_mma.cu), and of more (kda_tree_tc.cu)
+cudaError_t launch_tree_step_mma(const TreeStepArgs &a, cudaStream_t st);
+cudaError_t launch_tree_step_tc(const TreeStepArgs &a, cudaStream_t st);
 cudaError_t launch_tree_commit(const TreeCommitArgs &a, kda_dtype dt, cudaStream_t st);
 cudaError_t launch_tree_conv(const TreeConvArgs &a, kda_dtype dt, cudaStream_t st);
 cudaError_t launch_tree_conv_commit(const TreeConvCommitArgs &a, kda_dtype dt, cudaStream_t st);

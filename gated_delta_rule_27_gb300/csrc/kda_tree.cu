@@ -150,7 +150,7 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
     }
     tc::cp_async_commit();
     for (int i = tid; i < M; i += kStepThreads) sm[L.beta + i] = beta[(size_t)(t.row0 + i) * H + h];
-    tc::cp_async_wait_all_but_one();
+    tc::cp_async_wait<1>();
     if (read_tree(ts, parent, cu, n, total_nodes, max_nodes, true).nodes < 0) {  // a block barrier
         tc::cp_async_wait_all();
         if (tid == 0) report_invalid(status);
@@ -359,7 +359,9 @@ cudaError_t launch_step_t(const TreeStepArgs &a, cudaStream_t st) {
         case 64: return launch_step_d<Tin, 64>(a, st);
         case 128:
             if constexpr (sizeof(Tin) == 4) return launch_step_d<Tin, 128>(a, st);
-            else return launch_tree_step_tc(a, st);
+            // (256 requests x 32 heads: 3-6 nodes 102 us with the state in registers, 176 with tcgen05; 9-16 nodes 171
+            // and 207; 64 requests of 20-32 nodes 138 and 98)
+            else return a.max_nodes <= 16 ? launch_tree_step_mma(a, st) : launch_tree_step_tc(a, st);
         default: return cudaErrorInvalidValue;
     }
 }

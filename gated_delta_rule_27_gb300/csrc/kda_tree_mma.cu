@@ -1,16 +1,17 @@
-// kda_tree_mma.cu -- the draft-tree step with the state in registers: bf16 inputs, d = 128, trees of up to 32 nodes.
+// kda_tree_mma.cu -- the draft-tree step with the state in registers: bf16 inputs, d = 128, trees of up to 16 nodes.
 //
 // The mathematics is that of kda_tree_tc.cu: with K~ = k e^b, Q~ = q e^b, K^ = k e^{-b},
 //     A, P = [K~ ; Q~] K^^T (masked to the paths),   X^T, Y^T = S^T [K~ ; Q~]^T,
 //     R = beta (V - X),   U^T = R^T + R^T (T - I)^T with T = (I + A)^{-1},   O^T = Y^T + U^T P^T.
 // Small trees leave each state element a few multiply-adds; what bounds the step is the state's way to the tensor
 // core.  Here a warp owns 32 state columns and loads them as the MMA's A fragments: a lane's float4 of four
-// neighbouring columns is four rows of two 16-column tiles, and state rows 2t, 2t + 1 pair up as bf16.  The state
-// never passes through shared memory, X and Y come out as fragments that are R's and U's A operands as they are,
+// neighbouring columns is four rows of two 16-column tiles, and state rows 2t, 2t + 1 pair up as bf16.  X and Y come out as fragments that are R's and U's A operands as they are,
 // and from the state's load to the stores of u and o a warp waits for no other but for T and the norm of o.
 // (The legacy MMA is the right one here: 16 nodes take 1728 clocks of it per head, below the 4000 in which the
 // SM's share of HBM delivers the head's state; through tcgen05 the operand's conversion and staging took longer
-// than the products.)
+// than the products.)  Each warp's rows come through a ring of its own in shared memory: loaded straight to
+// registers, the lanes of a fragment read four rows that lie on the same banks of L1, 16 data cycles a load for 4,
+// and the L1 data pipe was what bounded the step.
 //
 // u is formed to fp32 accuracy as there: every operand in two bf16 parts, hi hi + hi lo + lo hi in fp32.
 #include "kda_tree_bf16.cuh"
@@ -32,13 +33,12 @@ struct Layout {
     static constexpr uint32_t ap_bytes = 2 * MP * ap_stride * 4;
     static constexpr uint32_t frag = 0;
     static constexpr uint32_t inv = frag + 2 * tiles * 8 * frag_bytes;  // K^'s tiles
-    static constexpr uint32_t b = inv + tiles * 8 * frag_bytes;         // fp32 [MP][128]: g, then (MP > 16) b
-    static constexpr uint32_t b_bytes = MP * 512 > ap_bytes ? MP * 512 : ap_bytes;
-    static constexpr uint32_t row = 320;                 // bytes between rows of v and the gate (bank conflicts)
-    static constexpr uint32_t v = b + b_bytes;
-    static constexpr uint32_t z = v + MP * row;
-    static constexpr uint32_t w = z + MP * row;
-    static constexpr uint32_t total = w + 512;
+    static constexpr uint32_t b = inv + tiles * 8 * frag_bytes;         // fp32 [MP][128]: g
+    static constexpr uint32_t b_bytes = MP * 512;
+    static_assert(ap_bytes <= b_bytes, "A and P take the place of g");
+    static constexpr int stages = MP == 8 ? 3 : 2;       // (six CTAs fit an SM; MP = 16: four)
+    static constexpr uint32_t ring = b + b_bytes;        // per warp `stages` x 16 rows of its 32 columns
+    static constexpr uint32_t total = ring + kWarps * stages * 2048;
     // later uses of the same bytes
     static constexpr uint32_t ap = b;                    // fp32 A [MP][ap_stride], then P (once the tiles are built)
     static constexpr uint32_t t = inv;                   // fp32 T - I [MP][ap_stride] (once A and P are formed)
@@ -63,15 +63,19 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     const float2 rest = tc::sub2(make_float2(x, y), make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)));
     lo = pack2(rest.x, rest.y);
 }
-__device__ __forceinline__ float4 ldg4(const float *p) {
-    float4 f;
-    asm volatile("ld.global.L1::no_allocate.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "l"(p));
-    return f;
-}
-__device__ __forceinline__ float4 read4(const uint8_t *p) {  // four bf16
-    const uint2 x = *reinterpret_cast<const uint2 *>(p);
+__device__ __forceinline__ float4 four(uint2 x) {  // of bf16
     return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
                        __uint_as_float(x.y & 0xffff0000u));
+}
+
+// Place of the 16-byte vector u of a row of g or b: a thread's two vectors (eight channels) lie half a row apart, so
+// that 16 threads read a row without bank conflicts.
+__device__ __forceinline__ int spread(int u) { return (u & 1) * 16 + (u >> 1); }
+__device__ __forceinline__ int spread_channel(int c) { return spread(c >> 2) * 4 + (c & 3); }
+__device__ __forceinline__ void read_row8(const float *row, int ch, float (&f)[8]) {
+    const float4 a = reinterpret_cast<const float4 *>(row)[ch], b = reinterpret_cast<const float4 *>(row)[16 + ch];
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
 // Writes eight channels (chunk ch of 16) of node i to its fragment tile.
@@ -150,9 +154,9 @@ __device__ void solve_masked(uint8_t *sm, const TreeShared &ts, int M, int c) {
 }
 
 template <int MP>
-__global__ void __launch_bounds__(kThreads, MP == 32 ? 2 : 4) tree_step_mma_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, MP == 8 ? 6 : 4) tree_step_mma_kernel(const Args p) {
     using L = Layout<MP>;
-    constexpr int NT = MP / 8;
+    constexpr int NT = MP / 8, kStages = L::stages;
     extern __shared__ __align__(16) uint8_t sm[];
     __shared__ TreeShared ts;
     __shared__ __align__(16) float s_beta[MP];
@@ -170,12 +174,12 @@ __global__ void __launch_bounds__(kThreads, MP == 32 ? 2 : 4) tree_step_mma_kern
     const int M = t.nodes;
     const size_t base = ((size_t)t.row0 * p.H + h) * kD, row_stride = (size_t)p.H * kD;
 
-    // The CTA's reads, issued at once: g, v, the gate and its weight on their way to shared memory; k, q and the
-    // first half of the warp's state columns to registers.
+    // The CTA's first reads, issued at once: g on its way to shared memory, k and q to registers, the first rows of
+    // the warp's state columns to its ring.
     constexpr int kUnits = MP / 8;  // (node, 8 channels) per thread: node (tid / 16) + 8 e, channels 8 (tid % 16) on
     uint4 kr[kUnits], qr[kUnits];
     for (int i = tid; i < M * 32; i += kThreads)
-        tc::cp_async16(sm + L::b + i * 16, p.g + base + (size_t)(i >> 5) * row_stride + (i & 31) * 4);
+        tc::cp_async16(sm + L::b + ((i & ~31) + spread(i & 31)) * 16, p.g + base + (size_t)(i >> 5) * row_stride + (i & 31) * 4);
 #pragma unroll
     for (int e = 0; e < kUnits; ++e) {
         const int i = (tid >> 4) + 8 * e;
@@ -185,122 +189,82 @@ __global__ void __launch_bounds__(kThreads, MP == 32 ? 2 : 4) tree_step_mma_kern
             qr[e] = __ldg(reinterpret_cast<const uint4 *>(p.q + base + (size_t)i * row_stride) + (tid & 15));
         }
     }
-    for (int i = tid; i < M * 16; i += kThreads) {
-        tc::cp_async16(sm + L::v + (i >> 4) * L::row + (i & 15) * 16, p.v + base + (size_t)(i >> 4) * row_stride + (i & 15) * 8);
-        if (p.gate)
-            tc::cp_async16(sm + L::z + (i >> 4) * L::row + (i & 15) * 16, p.gate + base + (size_t)(i >> 4) * row_stride + (i & 15) * 8);
-    }
-    if (warp == 1) {
-        if (p.gate && p.weight) tc::cp_async16(sm + L::w + lane * 16, p.weight + lane * 4);
-        else *reinterpret_cast<float4 *>(sm + L::w + lane * 16) = make_float4(1.f, 1.f, 1.f, 1.f);
-    }
-    // step ks of 16 state rows: the lane's rows 2 t, 2 t + 1 and 8 further, columns 4 g on of the warp's 32
-    const float *S = p.S_pool + ((size_t)slot * p.H + h) * kD * kD + (size_t)(2 * t4) * kD + warp * 32 + g * 4;
-    float4 s[4][4];
+    tc::cp_async_commit();
+    // Step ks of 16 state rows: eight lanes copy a row's 128 bytes (16-byte vectors XORed with the row's number), four
+    // rows at once.
+    const float *S = p.S_pool + ((size_t)slot * p.H + h) * kD * kD + (size_t)(lane >> 3) * kD + warp * 32 + (lane & 7) * 4;
+    uint8_t *ring = sm + L::ring + warp * kStages * 2048;
     auto load_state = [&](int ks) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[ks & 3][j] = ldg4(S + (size_t)(16 * ks + (j & 1) + 8 * (j >> 1)) * kD);
+        for (int j = 0; j < 4; ++j) {
+            const int row = 4 * j + (lane >> 3);
+            tc::cp_async16(ring + (ks % kStages) * 2048 + row * 128 + (((lane & 7) ^ row) & 7) * 16, S + (size_t)(16 * ks + 4 * j) * kD);
+        }
+        tc::cp_async_commit();
     };
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) load_state(ks);
+    for (int ks = 0; ks < kStages; ++ks) load_state(ks);
     if (warp == 2) {
         for (int i = lane; i < MP; i += 32) s_beta[i] = i < M ? p.beta[(size_t)(t.row0 + i) * p.H + h] : 0.f;
         if (lane == 0) s_wild = 0;
     }
-    tc::cp_async_wait_all();
+    tc::cp_async_wait<kStages>();
     for (int i = tid; i < M * 32; i += kThreads) {  // the vectors that this thread copied
-        float4 *x = reinterpret_cast<float4 *>(sm + L::b + i * 16);
+        float4 *x = reinterpret_cast<float4 *>(sm + L::b + ((i & ~31) + spread(i & 31)) * 16);
         *x = log2_decay4(*x);
     }
-    // The last warp looks up the CTA that starts about when this one ends, and asks for its inputs further down.
-    const int later = blockIdx.x + p.ahead;
-    Tree lt{0, 0};
-    int lslot = -1;
-    if (warp == 3 && later < gridDim.x) {
-        lt = tree_rows(p.cu, later / p.H, p.total_nodes, p.max_nodes);
-        lslot = slot_of(p.seq_idx, later / p.H, p.num_slots);
-    }
     if (read_tree(ts, p.parent, p.cu, n, p.total_nodes, p.max_nodes, true, 0).nodes < 0) {  // a block barrier
+        tc::cp_async_wait_all();
         if (tid == 0) report_invalid(p.status);
         return;
     }
 
-    // Fragment tiles of K~, Q~ and K^.  b sums g over the path; above 16 nodes, 16 nodes at a time, from the b of
-    // the nearest ancestor in an earlier group.
+    // Fragment tiles of K~, Q~ and K^; b sums g over the path.
     float *s_b = reinterpret_cast<float *>(sm + L::b);
     float range = 0.f;
 #pragma unroll
-    for (int first = 0; first < MP; first += 16) {
-        constexpr int kGroup = MP < 16 ? 1 : 2;  // units of this thread in a group of 16 nodes
-        float b[kGroup][8];
+    for (int e = 0; e < kUnits; ++e) {
+        const int i = (tid >> 4) + 8 * e, ch = tid & 15;
+        if ((warp << 1) + 8 * e >= M) break;  // (of the warp's two nodes; what the tiles hold past the tree is not looked at)
+        float b[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (uint32_t here = i < M ? (uint32_t)ts.anc[i] : 0u; here; here &= here - 1) {
+            float x[8];
+            read_row8(s_b + (__ffs((int)here) - 1) * kD, ch, x);
+            add8(b, b, x);
+        }
+        float kf[8], qf[8], ki[8], up[8], down[8];
+        unpack8(kr[e], kf);
+        unpack8(qr[e], qf);
+        float sk = 1.f, sq = 1.f;
+        if (p.qk_norm) {  // 16 threads hold a row
+            sk = sum_squares8(kf);
+            sq = sum_squares8(qf);
 #pragma unroll
-        for (int e = 0; e < kGroup; ++e) {
-            const int i = first + (tid >> 4) + 8 * e, ch = tid & 15;
-#pragma unroll
-            for (int x = 0; x < 8; ++x) b[e][x] = 0.f;
-            if (i < M) {
-                const unsigned long long anc = ts.anc[i], before = anc & ((1ull << first) - 1);
-                uint32_t here = (uint32_t)(anc >> first) & 0xffffu;
-                if (first > 0 && before) read8(s_b + (63 - __clzll((long long)before)) * kD + ch * 8, b[e]);
-                while (here) {
-                    float x[8];
-                    read8(s_b + (first + __ffs((int)here) - 1) * kD + ch * 8, x);
-                    here &= here - 1;
-                    add8(b[e], b[e], x);
-                }
+            for (int off = 8; off; off >>= 1) {
+                sk += __shfl_xor_sync(0xffffffffu, sk, off);
+                sq += __shfl_xor_sync(0xffffffffu, sq, off);
+            }
+            sk = rsqrtf(sk + p.qk_eps);
+            sq = rsqrtf(sq + p.qk_eps);
+            if (ch == 0) {
+                s_scale[i] = sk;
+                s_scale[MP + i] = sq;
             }
         }
-        if (MP > 16) {
-            __syncthreads();  // every sum of this group is formed
 #pragma unroll
-            for (int e = 0; e < kGroup; ++e) {
-                const int i = first + (tid >> 4) + 8 * e, ch = tid & 15;
-                if (i < M) {
-                    float4 *x = reinterpret_cast<float4 *>(s_b + i * kD + ch * 8);
-                    x[0] = make_float4(b[e][0], b[e][1], b[e][2], b[e][3]);
-                    x[1] = make_float4(b[e][4], b[e][5], b[e][6], b[e][7]);
-                }
-            }
-            __syncthreads();
+        for (int x = 0; x < 8; ++x) {
+            up[x] = exp2_of(b[x]);
+            down[x] = exp2_of(-b[x]);  // used while b is within +-kMaxRange
+            range = fmaxf(range, fabsf(b[x]));
         }
-#pragma unroll
-        for (int e = 0; e < kGroup; ++e) {
-            const int u = first / 8 + e, i = first + (tid >> 4) + 8 * e, ch = tid & 15;
-            if (first + (warp << 1) + 8 * e >= M) break;  // (of the warp's two nodes; what the tiles hold past the tree is not looked at)
-            float kf[8], qf[8], ki[8], up[8], down[8];
-            unpack8(kr[u], kf);
-            unpack8(qr[u], qf);
-            float sk = 1.f, sq = 1.f;
-            if (p.qk_norm) {  // 16 threads hold a row
-                sk = sum_squares8(kf);
-                sq = sum_squares8(qf);
-#pragma unroll
-                for (int off = 8; off; off >>= 1) {
-                    sk += __shfl_xor_sync(0xffffffffu, sk, off);
-                    sq += __shfl_xor_sync(0xffffffffu, sq, off);
-                }
-                sk = rsqrtf(sk + p.qk_eps);
-                sq = rsqrtf(sq + p.qk_eps);
-                if (ch == 0) {
-                    s_scale[i] = sk;
-                    s_scale[MP + i] = sq;
-                }
-            }
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                up[x] = exp2_of(b[e][x]);
-                down[x] = exp2_of(-b[e][x]);  // used while b is within +-kMaxRange
-                range = fmaxf(range, fabsf(b[e][x]));
-            }
-            scale8(kf, kf, sk);
-            scale8(qf, qf, sq);
-            mul8(ki, kf, down);
-            mul8(kf, kf, up);
-            mul8(qf, qf, up);
-            store_frag<MP>(sm + L::frag, i, ch, kf);
-            store_frag<MP>(sm + L::frag + NT * 8 * L::frag_bytes, i, ch, qf);
-            store_frag<MP>(sm + L::inv, i, ch, ki);
-        }
+        scale8(kf, kf, sk);
+        scale8(qf, qf, sq);
+        mul8(ki, kf, down);
+        mul8(kf, kf, up);
+        mul8(qf, qf, up);
+        store_frag<MP>(sm + L::frag, i, ch, kf);
+        store_frag<MP>(sm + L::frag + NT * 8 * L::frag_bytes, i, ch, qf);
+        store_frag<MP>(sm + L::inv, i, ch, ki);
     }
     const bool pairwise = __syncthreads_or(!(range <= kMaxRange));
 
@@ -310,10 +274,8 @@ __global__ void __launch_bounds__(kThreads, MP == 32 ? 2 : 4) tree_step_mma_kern
         // the place of K^, which is not used.
         float *xA = reinterpret_cast<float *>(sm + L::inv), *xP = xA + MP * MP;
         static_assert(2 * MP * MP * 4 <= NT * 8 * L::frag_bytes, "A and P pass through the place of K^");
-        if (MP <= 16) {
-            for (int i = 1; i < M; ++i) s_b[i * kD + tid] += s_b[ts.parent[i] * kD + tid];
-            __syncthreads();
-        }
+        for (int i = 1; i < M; ++i) s_b[i * kD + tid] += s_b[ts.parent[i] * kD + tid];
+        __syncthreads();
         for (int x = warp; x < MP * MP; x += kWarps) {
             const int i = x / MP, a = x % MP;
             float va = 0.f, vp = 0.f;
@@ -321,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, MP == 32 ? 2 : 4) tree_step_mma_kern
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int c = lane + 32 * e;
-                    const float ka = __bfloat162float(p.k[base + (size_t)a * row_stride + c]) * exp2_of(s_b[i * kD + c] - s_b[a * kD + c]);
+                    const float ka = __bfloat162float(p.k[base + (size_t)a * row_stride + c]) * exp2_of(s_b[i * kD + spread_channel(c)] - s_b[a * kD + spread_channel(c)]);
                     va = fmaf(__bfloat162float(p.k[base + (size_t)i * row_stride + c]), ka, va);
                     vp = fmaf(__bfloat162float(p.q[base + (size_t)i * row_stride + c]), ka, vp);
                 }
@@ -350,7 +312,6 @@ __global__ void __launch_bounds__(kThreads, MP == 32 ? 2 : 4) tree_step_mma_kern
         float zero = 0.f;
         for (int task = warp; task < kRowTiles * NT; task += kWarps) {
             const int m = task / NT, nt = task % NT;  // rows 16 m on of [K~ ; Q~], ancestors 8 nt on
-            if (MP > 16 && 8 * nt > (16 * m) % MP + 15) continue;
             float c[3][4] = {};
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
@@ -389,21 +350,26 @@ __global__ void __launch_bounds__(kThreads, MP == 32 ? 2 : 4) tree_step_mma_kern
             }
             if (zero != 0.f) s_wild = 1;
         }
-    } else if (warp == 3 && lslot >= 0 && lt.nodes > 0) {
-        const int lh = later % p.H;
-        if (lane < 2)
-            tc::bulk_prefetch_l2(p.S_pool + (((size_t)lslot * p.H + lh) * kD + 64 * lane) * kD, 32768);
-        // the nodes' rows by 128-byte lines: four of g, two each of k, q, v and the gate
-        for (int i = lane; i < lt.nodes * 4; i += 32) {
-            const size_t at = ((size_t)(lt.row0 + (i >> 2)) * p.H + lh) * kD;
-            tc::prefetch_l2(p.g + at + (i & 3) * 32);
-            const __nv_bfloat16 *x = i & 2 ? p.k : p.q, *y = i & 2 ? p.v : p.gate;
-            tc::prefetch_l2(x + at + (i & 1) * 64);
-            if (y) tc::prefetch_l2(y + at + (i & 1) * 64);
-        }
     }
 
-    // X^T and Y^T of the warp's 32 columns, 16 state rows at a time
+    // X^T and Y^T of the warp's 32 columns, 16 state rows at a time.  Of node tile j a lane holds nodes
+    // 8 j + 2 t4 + {0, 1}, four neighbouring columns of each; their v and gate are asked for now
+    // (at their use they cost 12% of the step).
+    const int col = warp * 32 + g * 4;
+    uint2 vr[NT][2], zr[NT][2];
+    float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
+    if (p.gate && p.weight) w = __ldg(reinterpret_cast<const float4 *>(p.weight + col));
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = 8 * j + 2 * t4 + e;
+            vr[j][e] = zr[j][e] = make_uint2(0u, 0u);
+            if (i < M) {
+                vr[j][e] = __ldg(reinterpret_cast<const uint2 *>(p.v + base + (size_t)i * row_stride + col));
+                if (p.gate) zr[j][e] = __ldg(reinterpret_cast<const uint2 *>(p.gate + base + (size_t)i * row_stride + col));
+            }
+        }
     float x[2][NT][4], y[2][NT][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -415,7 +381,18 @@ __global__ void __launch_bounds__(kThreads, MP == 32 ? 2 : 4) tree_step_mma_kern
     for (int ks = 0; ks < 8; ++ks) {
         // tile m holds the lane's columns 2 m (rows g of the tile) and 2 m + 1 (rows g + 8)
         uint32_t hi[2][4], lo[2][4];
-        const float4 *r = s[ks & 3];
+        // the lane's rows 2 t, 2 t + 1 and 8 further, columns 4 g on of the warp's 32
+        if (ks + kStages <= 8) tc::cp_async_wait<kStages - 1>();
+        else if (ks == 8 - kStages + 1) tc::cp_async_wait_all();
+        __syncwarp();
+        float4 r[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int row = 2 * t4 + (j & 1) + 8 * (j >> 1);
+            r[j] = *reinterpret_cast<const float4 *>(ring + (ks % kStages) * 2048 + row * 128 + ((g ^ row) & 7) * 16);
+        }
+        __syncwarp();
+        if (ks + kStages < 8) load_state(ks + kStages);
 #pragma unroll
         for (int k8 = 0; k8 < 2; ++k8) {
             split2(r[2 * k8].x, r[2 * k8 + 1].x, hi[0][2 * k8], lo[0][2 * k8]);
@@ -423,7 +400,6 @@ __global__ void __launch_bounds__(kThreads, MP == 32 ? 2 : 4) tree_step_mma_kern
             split2(r[2 * k8].z, r[2 * k8 + 1].z, hi[1][2 * k8], lo[1][2 * k8]);
             split2(r[2 * k8].w, r[2 * k8 + 1].w, hi[1][2 * k8 + 1], lo[1][2 * k8 + 1]);
         }
-        if (ks + 4 < 8) load_state(ks + 4);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             if (MP > 8 && 8 * j >= M) break;
@@ -435,15 +411,14 @@ __global__ void __launch_bounds__(kThreads, MP == 32 ? 2 : 4) tree_step_mma_kern
             }
         }
     }
-    // R.  Of tile j the lane holds nodes 8 j + 2 t4 + {0, 1}, four neighbouring columns of each.
-    const int col = warp * 32 + g * 4;
+    // R
     float zero = 0.f;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int i = 8 * j + 2 * t4 + e;
-            const float4 v = read4(sm + L::v + i * L::row + col * 2);
+            const float4 v = four(vr[j][e]);
             const float beta = s_beta[i];
             const bool in = i < M;
             x[0][j][e] = in ? beta * (v.x - x[0][j][e]) : 0.f;
@@ -513,7 +488,6 @@ __global__ void __launch_bounds__(kThreads, MP == 32 ? 2 : 4) tree_step_mma_kern
             }
         __syncthreads();
     }
-    const float4 w = *reinterpret_cast<const float4 *>(sm + L::w + col * 4);
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -522,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, MP == 32 ? 2 : 4) tree_step_mma_kern
             if (i >= M) continue;
             float4 o = make_float4(y[0][j][e], y[0][j][2 + e], y[1][j][e], y[1][j][2 + e]);
             if (p.gate) {
-                const float4 z = read4(sm + L::z + i * L::row + col * 2);
+                const float4 z = four(zr[j][e]);
                 const float ss = (s_square[0][i] + s_square[1][i]) + (s_square[2][i] + s_square[3][i]);
                 const float inv = rsqrtf(ss * (1.f / kD) + p.out_eps);
                 o.x *= inv * w.x * gate_of(z.x);
@@ -535,13 +509,10 @@ __global__ void __launch_bounds__(kThreads, MP == 32 ? 2 : 4) tree_step_mma_kern
 }
 
 template <int MP>
-cudaError_t launch_mp(Args p, int ctas, cudaStream_t st) {
+cudaError_t launch_mp(const Args &p, int ctas, cudaStream_t st) {
     constexpr int smem = Layout<MP>::total;
-    int sms = 0;
-    cudaError_t e = allow_smem<tree_step_mma_kernel<MP>>(smem);
-    if (e == cudaSuccess) e = sm_count(&sms);
+    const cudaError_t e = allow_smem<tree_step_mma_kernel<MP>>(smem);
     if (e != cudaSuccess) return e;
-    p.ahead = sms * (MP == 32 ? 2 : 4);  // the CTAs that run at once
     tree_step_mma_kernel<MP><<<ctas, kThreads, smem, st>>>(p);
     return cudaGetLastError();
 }
@@ -554,9 +525,7 @@ cudaError_t launch_tree_step_mma(const TreeStepArgs &a, cudaStream_t st) {
                  (__nv_bfloat16 *)a.o, a.u, a.status, a.fu.qk_norm, a.fu.qk_eps, (const __nv_bfloat16 *)a.fu.gate,
                  a.fu.weight, a.fu.out_eps};
     const int ctas = a.num_seqs * a.H;
-    if (a.max_nodes <= 8) return launch_mp<8>(p, ctas, st);
-    if (a.max_nodes <= 16) return launch_mp<16>(p, ctas, st);
-    return launch_mp<32>(p, ctas, st);
+    return a.max_nodes <= 8 ? launch_mp<8>(p, ctas, st) : launch_mp<16>(p, ctas, st);
 }
 
 }  // namespace kda

@@ -1,11 +1,12 @@
-// kda_tree_tc.cu -- the draft-tree step on the Blackwell tensor cores (tcgen05): bf16 inputs, d = 128.
+// kda_tree_tc.cu -- the draft-tree step on the Blackwell tensor cores (tcgen05): bf16 inputs, d = 128, trees of 17 to
+// 64 nodes.
 //
 // With b_i the log-decay along the path to node i, K~ = k e^b, Q~ = q e^b and K^ = k e^{-b} (kda_tree.cu has the
 // recurrence), one CTA per (request, head) forms, for a tree of at most MP nodes,
 //     D1 = [K~ ; Q~] K^^T      A and P: masked to the paths, A scaled by beta
 //     D2 = S^T [K~ ; Q~]^T     x and y: the pool's state, 128 columns, times every node's decayed key and query
-//     r  = beta (v - x),  T = (I + A)^{-1},  G = P T
-//     D3 = r^T [T - I ; G]^T   u = r + D3,  o = y + D3     (MP = 64: u first, then o = y + u^T P^T as D4)
+//     r  = beta (v - x),  T = (I + A)^{-1}
+//     D3 = r^T [T - I ; P T]^T   u = r + D3,  o = y + D3     (MP = 64: u first, then o = y + u^T P^T as D4)
 // so the state is read once, whatever the tree's size.  The floor is that read, 64 KB per (request, head).
 //
 // u moves the fp32 state, so it is formed to fp32 accuracy: every operand is split into two bf16 parts, hi + lo,
@@ -20,14 +21,13 @@
 // What bounds it is the length of one CTA's dependent steps, so the CTAs are kept small enough for several to share
 // an SM (the state passes through shared memory in two halves of 64 rows, half 1 loading while half 0 is
 // multiplied), and a CTA pulls the inputs of the one that will take its place into L2.
-#include <stdlib.h>
 #include "kda_tree_bf16.cuh"
 
 namespace kda {
 namespace {
 using namespace tree16;
 
-// Eight worker warps; warp 8 reads the tree and, for MP = 16, forms T and G; warp 9 issues the MMAs.
+// Eight worker warps; warp 8 reads the tree and asks for a later CTA's inputs; warp 9 issues the MMAs.
 constexpr int kD = 128, kWorkers = 256, kThreads = 320;
 
 // Shared memory for trees of at most MP nodes, in bytes.  Operand images are K-major with the 128-byte swizzle, 64
@@ -44,23 +44,22 @@ struct Layout {
     static constexpr uint32_t s_hi = kq + 2 * kq_panel;
     static constexpr uint32_t s_lo = s_hi + 16384;
     static constexpr uint32_t ki = s_lo + 16384;
-    static constexpr uint32_t b = ki + 2 * ki_panel;     // fp32 [MP][128]: g, then (MP > 16) the paths' sums b
+    static constexpr uint32_t b = ki + 2 * ki_panel;     // fp32 [MP][128]: g, then the paths' sums b
     static constexpr uint32_t ap_tg = MP == 64 ? ap_bytes : 2 * ap_bytes;
     static constexpr uint32_t b_bytes = MP * 512 > ap_tg ? MP * 512 : (ap_tg + 1023) / 1024 * 1024;
     static constexpr uint32_t v = b + b_bytes;           // bf16 [MP][128]
     static constexpr uint32_t w = v + MP * 256;          // fp32 [128]: the output weight
     static constexpr uint32_t tb = w + 512;              // fp32 3 x [32][36]: the blocks of T (MP = 64)
-    static constexpr bool early_z = MP == 16;            // the gate has a place of its own, else D2's operands'
-    static constexpr uint32_t z = early_z ? tb : kq;     // bf16 [MP][128]: the gate
-    static constexpr uint32_t total = MP == 64 ? tb + 3 * 32 * 36 * 4 : early_z ? tb + MP * 256 : tb;
+    static constexpr uint32_t total = MP == 64 ? tb + 3 * 32 * 36 * 4 : tb;
     // later uses of the same bytes
-    static constexpr uint32_t t_img = ki;                // rows T - I hi, G hi, T - I lo, G lo (MP = 64: T - I hi, lo)
+    static constexpr uint32_t t_img = ki;                // rows T - I hi, P T hi, T - I lo, P T lo (MP = 64: T - I hi, lo)
     static constexpr uint32_t p_img = ki + MP * 256;     // MP = 64: P hi, lo   (both once D1 is done)
     static constexpr uint32_t ap = b;                    // fp32 A [MP][ap_stride], then P (once the images are built)
-    static constexpr uint32_t tg = MP < 64 ? ap + ap_bytes : tb;  // fp32 T - I [MP][ap_stride], then G (MP = 64: tb)
+    static constexpr uint32_t tg = MP < 64 ? ap + ap_bytes : tb;  // fp32 T - I [MP][ap_stride], then P T (MP = 64: tb)
     static constexpr uint32_t r_img = s_hi;              // r: 128 rows hi, 128 rows lo (once D2 is done)
     static constexpr uint32_t u_img = s_hi;              // MP = 64: u, the same way (once D3 is done)
-    static constexpr uint32_t o = kq + (early_z ? 0 : MP * 256);  // fp32 [MP][128] (once D2 is done)
+    static constexpr uint32_t z = kq;                    // bf16 [MP][128]: the gate (once D2 is done)
+    static constexpr uint32_t o = kq + MP * 256;         // fp32 [MP][128] (once D2 is done)
     // accumulator columns: D2 at 0; D1 and, once it has been read, D3 (then D4) behind it
     static constexpr uint32_t d1 = 4 * MP, d3 = 4 * MP, d4 = 6 * MP;
     static constexpr uint32_t tmem_cols = 8 * MP;
@@ -133,7 +132,7 @@ __device__ void solve_masked(uint8_t *sm, const TreeShared &ts, const float *s_b
     }
 }
 
-// One column of G = P T (P zero above its diagonal) to g[i * stride].
+// One column of P T (P zero above its diagonal) to g[i * stride].
 template <int NB, int I = 0>
 __device__ __forceinline__ void multiply_block(const float *P, int stride, const float (&t)[NB], float *g) {
     if constexpr (I < NB) {
@@ -188,7 +187,7 @@ __device__ __forceinline__ void read_paths(uint8_t *sm, const TreeShared &ts, co
 }
 
 template <int MP>
-__global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tree_step_tc_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kernel(const Args p) {
     using L = Layout<MP>;
     extern __shared__ uint8_t raw[];
     __shared__ TreeShared ts;
@@ -233,14 +232,9 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
             tc::cp_async16(sm + L::v + i * 16, p.v + base + (size_t)(i >> 4) * row_stride + (i & 15) * 8);
 #pragma unroll
         for (int j = 0; j < 4; ++j) ldg8(S + (size_t)(16 * j) * kD, s[j]);
-        if (p.gate) {
-            if (L::early_z)
-                for (int i = tid; i < M * 16; i += kWorkers)
-                    tc::cp_async16(sm + L::z + i * 16, p.gate + base + (size_t)(i >> 4) * row_stride + (i & 15) * 8);
-            if (warp == 0) {
-                if (p.weight) tc::cp_async16(sm + L::w + lane * 16, p.weight + lane * 4);
-                else *reinterpret_cast<float4 *>(sm + L::w + lane * 16) = make_float4(1.f, 1.f, 1.f, 1.f);
-            }
+        if (p.gate && warp == 0) {
+            if (p.weight) tc::cp_async16(sm + L::w + lane * 16, p.weight + lane * 4);
+            else *reinterpret_cast<float4 *>(sm + L::w + lane * 16) = make_float4(1.f, 1.f, 1.f, 1.f);
         }
         tc::cp_async_wait_all();
         for (int i = tid; i < M * 32; i += kWorkers) {  // the vectors that this thread copied
@@ -282,8 +276,8 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
         if (warp == 9) tc::tmem_dealloc(tmem, L::tmem_cols);
         return;
     }
-    // Operand images of K~, Q~ and K^.  b sums g over the path; above 16 nodes, 16 nodes at a time, from the b of
-    // the nearest ancestor in an earlier group.
+    // Operand images of K~, Q~ and K^.  b sums g over the path, 16 nodes at a time, from the b of the nearest ancestor
+    // in an earlier group.
     float *s_b = reinterpret_cast<float *>(sm + L::b);
     float range = 0.f;
 #pragma unroll
@@ -305,15 +299,13 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
                 add8(b, b, g);
             }
         }
-        if (MP > 16) {
-            __syncthreads();  // every sum of this group is formed
-            if (warp < 8 && i < M) {
-                float4 *x = reinterpret_cast<float4 *>(s_b + i * kD + ch * 8);
-                x[0] = make_float4(b[0], b[1], b[2], b[3]);
-                x[1] = make_float4(b[4], b[5], b[6], b[7]);
-            }
-            __syncthreads();
+        __syncthreads();  // every sum of this group is formed
+        if (warp < 8 && i < M) {
+            float4 *x = reinterpret_cast<float4 *>(s_b + i * kD + ch * 8);
+            x[0] = make_float4(b[0], b[1], b[2], b[3]);
+            x[1] = make_float4(b[4], b[5], b[6], b[7]);
         }
+        __syncthreads();
         if (warp < 8 && (warp << 1) + 16 * e < M) {  // what the images hold past the tree is never looked at
             float kf[8], qf[8], ki[8];
             unpack8(kr[e], kf);
@@ -378,11 +370,6 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
         // the place of K^, which is not used.
         float *xA = reinterpret_cast<float *>(sm + L::ki), *xP = xA + MP * MP;
         static_assert(2 * MP * MP * 4 <= 2 * L::ki_panel, "A and P pass through the place of K^");
-        if (MP == 16) {
-            if (tid < kD)
-                for (int i = 1; i < M; ++i) s_b[i * kD + tid] += s_b[ts.parent[i] * kD + tid];
-            __syncthreads();
-        }
         if (warp < 8)
             for (int x = warp; x < MP * MP; x += 8) {
                 const int i = x / MP, a = x % MP;
@@ -433,7 +420,6 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
     }
 
     bool ok = true;
-    constexpr int kPath = MP == 16 ? 8 : 4;  // the first of the warps that form T
     if (warp == 9) {
         constexpr uint64_t kKmaj = tc::smem_desc_base(16, 1024, tc::SW_128B);
         constexpr uint64_t kSmn = tc::smem_desc_base(8192, 1024, tc::SW_128B);
@@ -468,38 +454,29 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bar_rows);
     }
-    if (warp >= kPath && warp < kPath + (MP == 16 ? 1 : 4)) {
+    if (warp >= 4 && warp < 8) {
         // A, P, T and the images that u and o are formed with
-        const int w = warp - kPath;
-        float *tb = reinterpret_cast<float *>(sm + L::tg);  // T - I and G; or T's diagonal blocks and A21 T11, [32][36] each
+        const int w = warp - 4;
+        float *tb = reinterpret_cast<float *>(sm + L::tg);  // T - I and P T; or T's diagonal blocks and A21 T11, [32][36] each
         if (!pairwise) ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bar_d1, 0));
         tc::tc_fence_after();
         if (w * 32 < 2 * MP) read_paths<MP>(sm, ts, s_beta, tmem, M, w * 32 + lane, pairwise, &s_wild);
         float zero = 0.f;
         if constexpr (MP < 64) {
-            // MP = 32: one warp writes T - I, another forms G = P T from the same T.  MP = 16: T - I only, G is left to
-            // the warps below.
-            if (MP == 32) tc::named_barrier(1, 128);
-            else __syncwarp();
-            if (MP == 16 || w < 2) {
+            // one warp writes T - I, another forms P T from the same T, a column a lane
+            tc::named_barrier(1, 128);
+            if (w < 2) {
                 float tc_[MP];
                 invert_block<MP>(sA, L::ap_stride, lane, tc_);
                 if (w == 0) {
-                    if (lane < MP)
 #pragma unroll
-                        for (int i = 0; i < MP; ++i) tb[i * L::ap_stride + lane] = i == lane ? 0.f : tc_[i];
+                    for (int i = 0; i < MP; ++i) tb[i * L::ap_stride + lane] = i == lane ? 0.f : tc_[i];
                 } else {
                     multiply_block<MP>(sP, L::ap_stride, tc_, tb + MP * L::ap_stride + lane);
                 }
             }
-            if (MP == 32) {
-                tc::named_barrier(1, 128);
-            } else {
-                __syncwarp();
-                tc::named_barrier_arrive(2, 160);
-            }
-            constexpr int kRows = MP == 16 ? MP : 2 * MP;
-            for (int x = w * 32 + lane; x < kRows * (MP / 8); x += MP == 16 ? 32 : 128) {
+            tc::named_barrier(1, 128);
+            for (int x = tid - 128; x < 2 * MP * (MP / 8); x += 128) {
                 const int row = x / (MP / 8), c0 = x % (MP / 8) * 8;
                 float f[8];
                 read8(tb + row * L::ap_stride + c0, f);
@@ -556,29 +533,11 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
         }
         if (zero != 0.f) s_wild = 1;
         tc::fence_async_smem();
-        if (!L::early_z && p.gate) {  // the gate, into the place of D2's operands
+        if (p.gate) {  // the gate, into the place of D2's operands
             ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bar_half[1], 0));
             for (int i = tid - 128; i < M * 16; i += 128)
                 tc::cp_async16(sm + L::z + i * 16, p.gate + base + (size_t)(i >> 4) * row_stride + (i & 15) * 8);
         }
-    }
-    if (MP == 16 && warp >= 4 && warp < 8) {
-        // G = P T, four rows a warp, two a lane (column lane mod 16).  Warp 8's T - I and P are awaited.
-        const float *sT = reinterpret_cast<const float *>(sm + L::tg);
-        tc::named_barrier(2, 160);
-        const int j = lane & 15;
-        float t16[16], zero = 0.f;
-#pragma unroll
-        for (int a = 0; a < 16; ++a) t16[a] = sT[a * L::ap_stride + j] + (a == j ? 1.f : 0.f);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int i = 4 * (warp - 4) + 2 * (lane >> 4) + e;
-            const float x = row_dot<16>(sP + i * L::ap_stride, t16);
-            zero = fmaf(x, 0.f, zero);
-            store_split1(sm + L::t_img, MP + i, j, 2 * MP, x);
-        }
-        if (zero != 0.f) s_wild = 1;
-        tc::fence_async_smem();
     }
     // A thread is a state column from here on.  Four warps form r; for u and o two warps share a quarter of TMEM's
     // lanes and take half of the nodes each.
@@ -686,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : MP == 32 ? 2 : 3) tre
             tc::tc_fence_before();
         }
     }
-    if (!L::early_z) tc::cp_async_wait_all();
+    tc::cp_async_wait_all();
     ok = __syncthreads_and(ok);
     if (warp == 9) {
         tc::tc_fence_after();
@@ -725,7 +684,7 @@ cudaError_t launch_mp(Args p, int ctas, cudaStream_t st) {
     cudaError_t e = allow_smem<tree_step_tc_kernel<MP>>(smem);
     if (e == cudaSuccess) e = sm_count(&sms);
     if (e != cudaSuccess) return e;
-    p.ahead = sms * (MP == 64 ? 1 : MP == 32 ? 2 : 3);  // the CTAs that run at once
+    p.ahead = sms * (MP == 64 ? 1 : 2);  // the CTAs that run at once
     tree_step_tc_kernel<MP><<<ctas, kThreads, smem, st>>>(p);
     return cudaGetLastError();
 }
@@ -738,10 +697,7 @@ cudaError_t launch_tree_step_tc(const TreeStepArgs &a, cudaStream_t st) {
                  (__nv_bfloat16 *)a.o, a.u, a.status, a.fu.qk_norm, a.fu.qk_eps, (const __nv_bfloat16 *)a.fu.gate,
                  a.fu.weight, a.fu.out_eps};
     const int ctas = a.num_seqs * a.H;
-    if (a.max_nodes <= 32 && !getenv("KDA_TC")) return launch_tree_step_mma(a, st);
-    if (a.max_nodes <= 16) return launch_mp<16>(p, ctas, st);
-    if (a.max_nodes <= 32) return launch_mp<32>(p, ctas, st);
-    return launch_mp<64>(p, ctas, st);
+    return a.max_nodes <= 32 ? launch_mp<32>(p, ctas, st) : launch_mp<64>(p, ctas, st);
 }
 
 }  // namespace kda
