@@ -60,60 +60,73 @@ __device__ __forceinline__ void load_some(const Tin *p, float (&f)[CPL]) {
     for (int e = 0; e < CPL; ++e) f[e] = to_f32(p[e]);
 }
 
-// Forward substitution of one state column over all nodes, eight at a time: the products with the u of earlier
-// blocks, then the block's own triangle.  Masked: entries off the path are skipped instead of multiplied by zero,
-// which a non-finite u of another branch would turn into NaN.  Returns false if a u is not finite.
-template <typename Tin, int D, bool Masked>
-__device__ __forceinline__ bool substitute(float *sm, const StepLayout<D> &L, const TreeShared &ts, const Tin *v,
-                                           size_t row_stride, int M, int c) {
-    const float *sA = sm + L.A, *sP = sm + L.P;
-    float *s_x = sm + L.ki, *s_y = sm + L.gb, *s_u = sm + L.ke, *s_o = sm + L.qe;
-    bool finite = true;
-    for (int i0 = 0; i0 < M; i0 += 8) {
-        float w[8], out[8];
+// Adds up[r] * M[row + r][a] * u[a][c] over a < end (a multiple of four) for ROWS rows; M's rows and u lie in shared
+// memory.  Masked: entries off the path are skipped instead of multiplied by zero, which a non-finite u of another
+// branch would turn into NaN.
+template <int D, int ROWS, bool Masked>
+__device__ __forceinline__ void add_rows(float (&acc)[ROWS], float sign, const float *M, int stride, const float *u, int end,
+                                         const unsigned long long *anc, int row, int nodes) {
+    for (int a = 0; a < end; a += 4) {
+        float ua[4];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            const int i = min(i0 + r, M - 1);
-            w[r] = sm[L.beta + i] * (to_f32(v[(size_t)i * row_stride]) - s_x[i * D + c]);
-            out[r] = s_y[i * D + c];
-        }
-        for (int a = 0; a < i0; a += 4) {
-            float ua[4];
+        for (int e = 0; e < 4; ++e) ua[e] = sign * u[(a + e) * D];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) ua[e] = s_u[(a + e) * D + c];
+        for (int r = 0; r < ROWS; ++r) {
+            const float4 m = *reinterpret_cast<const float4 *>(&M[(row + r) * stride + a]);
+            const float mv[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const float4 A = *reinterpret_cast<const float4 *>(&sA[(i0 + r) * L.ap_stride + a]);
-                const float4 P = *reinterpret_cast<const float4 *>(&sP[(i0 + r) * L.ap_stride + a]);
-                const float Av[4] = {A.x, A.y, A.z, A.w}, Pv[4] = {P.x, P.y, P.z, P.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (!Masked || (i0 + r < M && ((ts.anc[i0 + r] >> (a + e)) & 1))) {
-                        w[r] = fmaf(-Av[e], ua[e], w[r]);
-                        out[r] = fmaf(Pv[e], ua[e], out[r]);
-                    }
-                }
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            const float *rowA = &sA[(i0 + r) * L.ap_stride + i0], *rowP = &sP[(i0 + r) * L.ap_stride + i0];
-#pragma unroll
-            for (int a = 0; a < r; ++a) {
-                if (!Masked || (i0 + r < M && ((ts.anc[i0 + r] >> (i0 + a)) & 1))) {
-                    w[r] = fmaf(-rowA[a], w[a], w[r]);
-                    out[r] = fmaf(rowP[a], w[a], out[r]);
-                }
-            }
-            out[r] = fmaf(rowP[r], w[r], out[r]);
-            if (i0 + r < M) {
-                finite &= fabsf(w[r]) < INFINITY;
-                s_u[(i0 + r) * D + c] = w[r];
-                s_o[(i0 + r) * D + c] = out[r];
-            }
+            for (int e = 0; e < 4; ++e)
+                if (!Masked || (row + r < nodes && ((anc[row + r] >> (a + e)) & 1))) acc[r] = fmaf(mv[e], ua[e], acc[r]);
         }
     }
-    return finite;
+}
+
+// u and o from x and y (all threads).  Forward substitution over blocks of eight nodes: the products with the u of
+// earlier blocks are shared out, D threads by 128 / D groups of rows, then a thread per column solves the block's own
+// triangle.  o follows from all of u at once.  Returns false if a u is not finite (to every thread).
+template <typename Tin, int D, bool Masked>
+__device__ __forceinline__ bool substitute(float *sm, const StepLayout<D> &L, const TreeShared &ts, const Tin *v,
+                                           size_t row_stride, int M) {
+    constexpr int RG = kStepThreads / D, ROWS = 8 / RG;
+    const float *sA = sm + L.A, *sP = sm + L.P;
+    const int c = threadIdx.x % D, first = threadIdx.x / D * ROWS;
+    float *s_x = sm + L.ki + c, *s_y = sm + L.gb + c, *s_u = sm + L.ke + c, *s_o = sm + L.qe + c;
+    bool finite = true;
+    for (int i0 = 0; i0 < M; i0 += 8) {
+        float w[ROWS];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            const int i = i0 + first + r;
+            w[r] = i < M ? sm[L.beta + i] * (to_f32(v[(size_t)i * row_stride + c]) - s_x[i * D]) : 0.f;
+        }
+        add_rows<D, ROWS, Masked>(w, -1.f, sA, L.ap_stride, s_u, i0, ts.anc, i0 + first, M);
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) s_u[(i0 + first + r) * D] = w[r];
+        if (RG > 1) __syncthreads();
+        if (first == 0) {
+            float t[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                t[r] = s_u[(i0 + r) * D];
+#pragma unroll
+                for (int a = 0; a < r; ++a)
+                    if (!Masked || (i0 + r < M && ((ts.anc[i0 + r] >> (i0 + a)) & 1)))
+                        t[r] = fmaf(-sA[(i0 + r) * L.ap_stride + i0 + a], t[a], t[r]);
+                finite &= i0 + r >= M || fabsf(t[r]) < INFINITY;
+                s_u[(i0 + r) * D] = t[r];
+            }
+        }
+        if (RG > 1) __syncthreads();
+    }
+    for (int i0 = 0; i0 < M; i0 += 8) {
+        float out[ROWS];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) out[r] = i0 + first + r < M ? s_y[(i0 + first + r) * D] : 0.f;
+        add_rows<D, ROWS, Masked>(out, 1.f, sP, L.ap_stride, s_u, i0 + 8, ts.anc, i0 + first, M);
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) s_o[(i0 + first + r) * D] = out[r];
+    }
+    return __syncthreads_and(finite);
 }
 
 template <typename Tin, int D>
@@ -233,11 +246,12 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
     tc::cp_async_wait_all();
     const bool pairwise = __syncthreads_or(!(range <= kMaxRange));
 
-    // A and P: a thread per (node, ancestor)
-    for (int p = tid; p < M * M; p += kStepThreads) {
-        const int i = p / M, a = p % M;
+    // A and P: a thread per (node, ancestor), with zeros up to a multiple of eight
+    const int M8 = (M + 7) & ~7;
+    for (int p = tid; p < M8 * M8; p += kStepThreads) {
+        const int i = p / M8, a = p % M8;
         float sa = 0.f, sp = 0.f;
-        if ((ts.anc[i] >> a) & 1) {
+        if (i < M && ((ts.anc[i] >> a) & 1)) {
             if (!pairwise) {
                 const float *x = sm + L.ke + i * kPitch, *y = sm + L.qe + i * kPitch, *z = sm + L.ki + a * kPitch;
 #pragma unroll 4
@@ -308,11 +322,7 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
         }
     }
     __syncthreads();  // K~ and Q~ are no longer needed: u and o take their place
-    for (int c = tid; c < D; c += kStepThreads) {
-        const Tin *vc = v + base + c;
-        if (!substitute<Tin, D, false>(sm, L, ts, vc, row_stride, M, c)) substitute<Tin, D, true>(sm, L, ts, vc, row_stride, M, c);
-    }
-    __syncthreads();
+    if (!substitute<Tin, D, false>(sm, L, ts, v + base, row_stride, M)) substitute<Tin, D, true>(sm, L, ts, v + base, row_stride, M);
     for (int i = warp; i < M; i += kStepWarps) {  // a warp per row
         const size_t at = base + (size_t)i * row_stride + c0;
         float x[CPL];
@@ -371,12 +381,13 @@ cudaError_t launch_step_t(const TreeStepArgs &a, cudaStream_t st) {
 // ---------------------------------------------------------------------------
 // One CTA per (request, head), laid out like the decode step: each thread holds 16 rows by four columns of the
 // state in registers.  The state's loads are issued before anything else that takes time, and the path's rows of
-// k, g and u follow as asynchronous copies, so one wait covers both.  The path is taken kChunk nodes at a time:
+// k, g and u follow as asynchronous copies, so one wait covers both.  The path is taken CHUNK nodes at a time (8, or 16
+// where paths may be longer than 8, which would otherwise wait for their rows twice):
 // with the decay to the chunk's end folded into its keys, a chunk is  S <- e^{b} S + sum_a (k_a e^{b - b_a}) u_a^T.
 // Bound by HBM: the state once each way.
-constexpr int kRows = 16, kChunk = 8;
+constexpr int kRows = 16;
 
-template <typename Tin, int D>
+template <typename Tin, int D, int CHUNK>
 __global__ void __launch_bounds__((D / 4) * (D / kRows), D == 128 ? 3 : 1)
 tree_commit_kernel(const Tin *__restrict__ k, const float *__restrict__ g, const float *__restrict__ u,
                    const int32_t *__restrict__ cu, const int32_t *__restrict__ path,
@@ -385,10 +396,10 @@ tree_commit_kernel(const Tin *__restrict__ k, const float *__restrict__ g, const
                    int qk_norm, float qk_eps) {
     constexpr int CG = D / 4, NT = CG * (D / kRows);
     constexpr int KV = D * (int)sizeof(Tin) / 16, FV = D / 4;  // 16-byte vectors of a row of k; of g or u
-    __shared__ __align__(16) float s_k[kChunk][D], s_u[kChunk][D], s_g[kChunk][D];
+    __shared__ __align__(16) float s_k[CHUNK][D], s_u[CHUNK][D], s_g[CHUNK][D];
     __shared__ __align__(16) float s_dec[D];
-    __shared__ __align__(16) Tin s_raw[kChunk][D];
-    __shared__ float s_scale[kChunk];
+    __shared__ __align__(16) Tin s_raw[CHUNK][D];
+    __shared__ float s_scale[CHUNK];
     const int n = blockIdx.x / H, h = blockIdx.x % H, tid = threadIdx.x;
     const int len = path_len[n], slot = slot_of(seq_idx, n, num_slots);
     const Tree t = tree_rows(cu, n, total_nodes, kMaxNodes);
@@ -404,8 +415,8 @@ tree_commit_kernel(const Tin *__restrict__ k, const float *__restrict__ g, const
     for (int j = 0; j < kRows; ++j) s[j] = __ldcs(&Sv[(size_t)(rg * kRows + j) * CG + cg]);
 
     const int32_t *nodes = path + (size_t)n * path_stride;
-    for (int l0 = 0; l0 < len; l0 += kChunk) {
-        const int L = min(kChunk, len - l0);
+    for (int l0 = 0; l0 < len; l0 += CHUNK) {
+        const int L = min(CHUNK, len - l0);
         int bad = 0;
         for (int i = tid; i < L * (KV + 2 * FV); i += NT) {
             const int r = i / (KV + 2 * FV), e = i % (KV + 2 * FV);
@@ -420,7 +431,7 @@ tree_commit_kernel(const Tin *__restrict__ k, const float *__restrict__ g, const
             else tc::cp_async16(&s_u[r][(e - KV - FV) * 4], u + at + (e - KV - FV) * 4);
         }
         if (l0 == 0)  // the whole path is checked before anything is written
-            for (int i = kChunk + tid; i < len; i += NT) bad |= nodes[i] < 0 || nodes[i] >= t.nodes;
+            for (int i = CHUNK + tid; i < len; i += NT) bad |= nodes[i] < 0 || nodes[i] >= t.nodes;
         tc::cp_async_wait_all();
         if (__syncthreads_or(bad)) {
             if (tid == 0) report_invalid(status);
@@ -429,7 +440,7 @@ tree_commit_kernel(const Tin *__restrict__ k, const float *__restrict__ g, const
         if (qk_norm) {  // a group of min(NT, 32) threads per row
             constexpr int G = NT < 32 ? NT : 32;
             const int lane = tid % G;
-            for (int r = tid / G; r < kChunk; r += NT / G) {
+            for (int r = tid / G; r < CHUNK; r += NT / G) {
                 float ss = 0.f;
                 if (r < L)
                     for (int c = lane; c < D; c += G) ss = fmaf(to_f32(s_raw[r][c]), to_f32(s_raw[r][c]), ss);
@@ -472,18 +483,22 @@ tree_commit_kernel(const Tin *__restrict__ k, const float *__restrict__ g, const
                 }
             }
         }
-        if (l0 + kChunk < len) __syncthreads();  // the chunk's rows are free
+        if (l0 + CHUNK < len) __syncthreads();  // the chunk's rows are free
     }
 #pragma unroll
     for (int j = 0; j < kRows; ++j) __stcs(&Sv[(size_t)(rg * kRows + j) * CG + cg], s[j]);
 }
 
-template <typename Tin, int D>
-cudaError_t launch_commit_d(const TreeCommitArgs &a, cudaStream_t st) {
-    tree_commit_kernel<Tin, D><<<a.num_seqs * a.H, (D / 4) * (D / kRows), 0, st>>>(
+template <typename Tin, int D, int CHUNK>
+cudaError_t launch_commit_c(const TreeCommitArgs &a, cudaStream_t st) {
+    tree_commit_kernel<Tin, D, CHUNK><<<a.num_seqs * a.H, (D / 4) * (D / kRows), 0, st>>>(
         (const Tin *)a.k, a.g, a.u, a.cu, a.path, a.path_len, a.seq_idx, a.H, a.total_nodes, a.path_stride,
         a.num_slots, a.S_pool, a.status, a.qk_norm, a.qk_eps);
     return cudaGetLastError();
+}
+template <typename Tin, int D>
+cudaError_t launch_commit_d(const TreeCommitArgs &a, cudaStream_t st) {
+    return a.path_stride > 8 ? launch_commit_c<Tin, D, 16>(a, st) : launch_commit_c<Tin, D, 8>(a, st);
 }
 
 template <typename Tin>
