@@ -2,15 +2,19 @@
 
 Each .cu file under csrc/ is compiled to an object in parallel, then linked
 into ``gated_delta_rule_27_gb300/lib/libkda.so``.  A rebuild happens only when a
-source or header is newer than the library.
+source or header is newer than the library.  The Python marshalling of the
+draft-tree calls (csrc/kda_tree_py.cpp, host code that reads torch tensors) is
+compiled next to it into ``lib/_kda_tree.so``; libkda.so itself knows no torch.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "lib", "libkda.so")
+TREE_PY_SRC = os.path.join(CSRC, "kda_tree_py.cpp")
+TREE_PY = os.path.join(PKG, "lib", "_kda_tree.so")
 # the bounds-checking variant (every checked index is tested before its access; see csrc/kda_check.cuh)
 DEBUG_BUILD_DIR = os.path.join(PKG, "_build_debug")
 DEBUG_LIB = os.path.join(PKG, "lib", "libkda_debug.so")
@@ -85,6 +91,26 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
     return lib
 
 
+def build_tree_py() -> str:
+    """Builds _kda_tree.so, the Python marshalling of the draft-tree calls, against the installed torch."""
+    newer = [TREE_PY_SRC, os.path.join(INCLUDE, "kda.h"), os.path.abspath(__file__)]
+    if os.path.exists(TREE_PY) and all(os.path.getmtime(p) <= os.path.getmtime(TREE_PY) for p in newer):
+        return TREE_PY
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    lib, inc = os.path.join(torch_dir, "lib"), os.path.join(torch_dir, "include")
+    cuda_inc = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    includes = [INCLUDE, inc, os.path.join(inc, "torch", "csrc", "api", "include"), sysconfig.get_path("include"), cuda_inc]
+    os.makedirs(os.path.dirname(TREE_PY), exist_ok=True)
+    tmp = TREE_PY + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", *("-I" + p for p in includes), TREE_PY_SRC,
+           "-o", tmp, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath," + lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on %s:\n%s%s" % (TREE_PY_SRC, r.stdout, r.stderr))
+    os.replace(tmp, TREE_PY)
+    return TREE_PY
+
+
 def _demangle(name: str) -> str:
     """The kernel's name and template arguments, without namespaces and parameter types."""
     try:
@@ -132,3 +158,4 @@ if __name__ == "__main__":
         print(resource_report())
     else:
         print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+        print(build_tree_py())

@@ -8,6 +8,7 @@ device, the call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -312,48 +313,31 @@ def kda_state_restore(S_saved, seq_idx, S_pool, status=None, stream=None) -> Non
         raise KdaError(rc, "kda_state_restore")
 
 
-def _arg(t, dtype, shape, name: str):
-    """The address of a contiguous device tensor of this dtype and shape (None passes as null)."""
-    if t is None:
-        return None
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
-    if t.dtype is not dtype:
-        raise TypeError("%s is %s, libkda takes %s here" % (name, t.dtype, dtype))
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if not t.is_cuda:
-        raise ValueError("libkda takes device tensors; %s is on %s" % (name, t.device))
-    raise ValueError("libkda takes contiguous tensors; %s is not" % name)
+# the draft-tree calls: marshalled and checked by csrc/kda_tree_py.cpp, which calls libkda.so's entry points
+_tree_calls = None
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream_of(stream, t):
-    """The given stream, or the current one of the tensor's device, as an address."""
-    if stream is not None:
-        return stream.cuda_stream
-    return _raw_stream(t.get_device()) if _raw_stream else torch.cuda.current_stream(t.device).cuda_stream
+def _tree():
+    """The marshalling module, built and loaded on first use and given the addresses of the loaded library."""
+    global _tree_calls
+    if _tree_calls is None:
+        lib = load()
+        spec = importlib.util.spec_from_file_location("_kda_tree", _build.build_tree_py())
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.init(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                      for name in ("kda_tree_step", "kda_tree_commit", "kda_tree_conv", "kda_tree_conv_commit",
+                                   "kda_draft_verify")))
+        _tree_calls = module
+    return _tree_calls
 
 
 def kda_tree_step(q, k, v, g, beta, parent, cu_nodes, seq_idx, S_pool, o, u, max_nodes, status=None, stream=None,
                   qk_l2norm=False, qk_eps=1e-6, out_gate=None, out_weight=None, out_eps=1e-6) -> None:
     """KDA attention of every draft-tree node over the state pool (kda_tree_step): q, k, v, g [T, H, d] and beta
     [T, H] packed as include/kda.h says, o and u (or None) written; the fused normalisations as for fusion_opts."""
-    dt, rows, i32, f32 = q.dtype, q.shape, torch.int32, torch.float32
-    T, H, d = rows
-    N, slots = cu_nodes.shape[0] - 1, S_pool.shape[0]
-    opts = None
-    if qk_l2norm or out_gate is not None:
-        opts = FusionOpts(1 if qk_l2norm else 0, qk_eps, _arg(out_gate, dt, rows, "out_gate"),
-                          _arg(out_weight, f32, (d,), "out_weight"), out_eps)
-    rc = load().kda_tree_step(_arg(q, dt, rows, "q"), _arg(k, dt, rows, "k"), _arg(v, dt, rows, "v"),
-                              _arg(g, f32, rows, "g"), _arg(beta, f32, (T, H), "beta"),
-                              _arg(parent, i32, (T,), "parent"), _arg(cu_nodes, i32, (N + 1,), "cu_nodes"),
-                              _arg(seq_idx, i32, (N,), "seq_idx"), N, T, max_nodes, slots, H, d, d, _dtype_code(q),
-                              _arg(S_pool, f32, (slots, H, d, d), "S_pool"), _arg(o, dt, rows, "o"),
-                              _arg(u, f32, rows, "u"), _arg(status, i32, (1,), "status"), _stream_of(stream, q), opts)
+    rc = (_tree_calls or _tree()).tree_step(q, k, v, g, beta, parent, cu_nodes, seq_idx, S_pool, o, u, max_nodes, status,
+                                            stream, qk_l2norm, qk_eps, out_gate, out_weight, out_eps)
     if rc != KDA_OK:
         raise KdaError(rc, "kda_tree_step")
 
@@ -361,15 +345,8 @@ def kda_tree_step(q, k, v, g, beta, parent, cu_nodes, seq_idx, S_pool, o, u, max
 def kda_tree_commit(k, g, u, cu_nodes, path, path_len, seq_idx, S_pool, status=None, stream=None, qk_l2norm=False,
                     qk_eps=1e-6) -> None:
     """Moves the pool's states along the accepted paths (kda_tree_commit), in place."""
-    rows, i32, f32 = k.shape, torch.int32, torch.float32
-    T, H, d = rows
-    N, slots, width = cu_nodes.shape[0] - 1, S_pool.shape[0], path.shape[1]
-    opts = FusionOpts(1, qk_eps, None, None, 0.0) if qk_l2norm else None
-    rc = load().kda_tree_commit(_arg(k, k.dtype, rows, "k"), _arg(g, f32, rows, "g"), _arg(u, f32, rows, "u"),
-                                _arg(cu_nodes, i32, (N + 1,), "cu_nodes"), _arg(path, i32, (N, width), "path"),
-                                _arg(path_len, i32, (N,), "path_len"), _arg(seq_idx, i32, (N,), "seq_idx"), N, T,
-                                width, slots, H, d, d, _dtype_code(k), _arg(S_pool, f32, (slots, H, d, d), "S_pool"),
-                                _arg(status, i32, (1,), "status"), _stream_of(stream, k), opts)
+    rc = (_tree_calls or _tree()).tree_commit(k, g, u, cu_nodes, path, path_len, seq_idx, S_pool, status, stream, qk_l2norm,
+                                              qk_eps)
     if rc != KDA_OK:
         raise KdaError(rc, "kda_tree_commit")
 
@@ -377,29 +354,14 @@ def kda_tree_commit(k, g, u, cu_nodes, path, path_len, seq_idx, S_pool, status=N
 def kda_tree_conv(x, w, parent, cu_nodes, seq_idx, conv_pool, y, max_nodes, status=None, stream=None) -> None:
     """The short convolution along every node's path (kda_tree_conv): x, y [T, C], w [C, W], conv_pool
     [slots, W - 1, C] (read only)."""
-    dt, rows, i32, f32 = x.dtype, x.shape, torch.int32, torch.float32
-    T, C = rows
-    N, slots, W = cu_nodes.shape[0] - 1, conv_pool.shape[0], w.shape[1]
-    rc = load().kda_tree_conv(_arg(x, dt, rows, "x"), _arg(w, f32, (C, W), "w"), _arg(parent, i32, (T,), "parent"),
-                              _arg(cu_nodes, i32, (N + 1,), "cu_nodes"), _arg(seq_idx, i32, (N,), "seq_idx"), N, T,
-                              max_nodes, slots, C, W, _dtype_code(x),
-                              _arg(conv_pool, f32, (slots, W - 1, C), "conv_pool"), _arg(y, dt, rows, "y"),
-                              _arg(status, i32, (1,), "status"), _stream_of(stream, x))
+    rc = (_tree_calls or _tree()).tree_conv(x, w, parent, cu_nodes, seq_idx, conv_pool, y, max_nodes, status, stream)
     if rc != KDA_OK:
         raise KdaError(rc, "kda_tree_conv")
 
 
 def kda_tree_conv_commit(x, cu_nodes, path, path_len, seq_idx, conv_pool, status=None, stream=None) -> None:
     """Moves the carried convolution inputs along the accepted paths (kda_tree_conv_commit), in place."""
-    i32 = torch.int32
-    T, C = x.shape
-    N, width = cu_nodes.shape[0] - 1, path.shape[1]
-    slots, carried, _ = conv_pool.shape
-    rc = load().kda_tree_conv_commit(_arg(x, x.dtype, (T, C), "x"), _arg(cu_nodes, i32, (N + 1,), "cu_nodes"),
-                                     _arg(path, i32, (N, width), "path"), _arg(path_len, i32, (N,), "path_len"),
-                                     _arg(seq_idx, i32, (N,), "seq_idx"), N, T, width, slots, C, carried + 1,
-                                     _dtype_code(x), _arg(conv_pool, torch.float32, (slots, carried, C), "conv_pool"),
-                                     _arg(status, i32, (1,), "status"), _stream_of(stream, x))
+    rc = (_tree_calls or _tree()).tree_conv_commit(x, cu_nodes, path, path_len, seq_idx, conv_pool, status, stream)
     if rc != KDA_OK:
         raise KdaError(rc, "kda_tree_conv_commit")
 
@@ -408,16 +370,8 @@ def kda_draft_verify(logits, tokens, parent, cu_nodes, u_accept, u_next, path, p
                      temperature=None, status=None, stream=None) -> None:
     """Verifies drafted tokens against the target's logits [T, V] (kda_draft_verify): writes the kept paths
     [N, max nodes], their lengths and the next tokens."""
-    rows, i32, f32 = logits.shape, torch.int32, torch.float32
-    T, V = rows
-    N, width = cu_nodes.shape[0] - 1, path.shape[1]
-    rc = load().kda_draft_verify(_arg(logits, logits.dtype, rows, "logits"), _arg(draft_probs, f32, rows, "draft_probs"),
-                                 _arg(tokens, i32, (T,), "tokens"), _arg(parent, i32, (T,), "parent"),
-                                 _arg(cu_nodes, i32, (N + 1,), "cu_nodes"), _arg(temperature, f32, (N,), "temperature"),
-                                 _arg(u_accept, f32, (T,), "u_accept"), _arg(u_next, f32, (N,), "u_next"), N, T, V,
-                                 _dtype_code(logits), width, _arg(path, i32, (N, width), "path"),
-                                 _arg(path_len, i32, (N,), "path_len"), _arg(next_token, i32, (N,), "next_token"),
-                                 _arg(status, i32, (1,), "status"), _stream_of(stream, logits))
+    rc = (_tree_calls or _tree()).draft_verify(logits, tokens, parent, cu_nodes, u_accept, u_next, path, path_len, next_token,
+                                               draft_probs, temperature, status, stream)
     if rc != KDA_OK:
         raise KdaError(rc, "kda_draft_verify")
 
