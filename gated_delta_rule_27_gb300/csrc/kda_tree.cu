@@ -26,7 +26,9 @@ namespace {
 // by four columns, which read a vector of shared memory for every eight multiply-adds or more; the substitution has
 // a thread per column, eight nodes at a time.  Where the decays along a path sum to more than kMaxRange, so that
 // e^{-b} would overflow, A and P take the path's own exponents instead.
-// Bound by the multiply-adds with the state, 4 d^2 for each node, and their operands' way from shared memory.
+// Bound by the multiply-adds with the state, 4 d^2 for each node, and their operands' way from shared memory; with few
+// requests by the latency of its dependent steps (17 requests of up to 13 nodes, 5 heads of d = 64, fp32: 10 us, of
+// which the states' way from HBM is 0.2).
 constexpr int kStepThreads = 128, kStepWarps = kStepThreads / 32;
 constexpr float kMaxRange = 80.f;
 
@@ -384,7 +386,8 @@ cudaError_t launch_step_t(const TreeStepArgs &a, cudaStream_t st) {
 // k, g and u follow as asynchronous copies, so one wait covers both.  The path is taken CHUNK nodes at a time (8, or 16
 // where paths may be longer than 8, which would otherwise wait for their rows twice):
 // with the decay to the chunk's end folded into its keys, a chunk is  S <- e^{b} S + sum_a (k_a e^{b - b_a}) u_a^T.
-// Bound by HBM: the state once each way.
+// Bound by HBM: the state once each way.  Measured, 256 requests x 32 heads of d = 128, bf16, paths of 0 to 6 nodes:
+// 150 us, DRAM busy 78% of the time; 24 warps an SM wait for loads in flight most of theirs.
 constexpr int kRows = 16;
 
 template <typename Tin, int D, int CHUNK>
@@ -518,6 +521,8 @@ cudaError_t launch_commit_t(const TreeCommitArgs &a, cudaStream_t st) {
 // first.  One CTA per (request, channel block); a thread owns VEC neighbouring channels, whose rows it reads as
 // 16 bytes (VEC = 8 of bf16, 4 of fp32; VEC = 1 where C or an address does not allow that).  All of the block's
 // rows are on their way to shared memory at once, each read once; a thread copies what it will use itself.
+// Bound by latency: one CTA's loads, then its sums, with 9 CTAs an SM.  Measured, 256 requests x 9 to 16 nodes x 4096
+// channels, bf16: 21 us, for 53 MB of x and y and 12.6 MB of carried inputs.
 constexpr int kConvThreads = 64;
 
 template <typename Tin, int VEC>

@@ -18,9 +18,13 @@
 // D3 and D4 multiply entries off the paths by zero.  Where an operand is not finite that would carry a NaN from
 // one branch into another, so such a request or column takes a substitution that skips them (solve_masked).
 //
-// What bounds it is the length of one CTA's dependent steps, so the CTAs are kept small enough for several to share
-// an SM (the state passes through shared memory in two halves of 64 rows, half 1 loading while half 0 is
-// multiplied), and a CTA pulls the inputs of the one that will take its place into L2.
+// What bounds it is the length of one CTA's dependent steps, so CTAs of up to 32 nodes are kept small enough for two to
+// share an SM (the state passes through shared memory in two halves of 64 rows, half 1 loading while half 0 is
+// multiplied), and a CTA pulls the inputs of the one that will take its place into L2 (without that 233 us for 207, 256
+// requests of 9 to 16 nodes, 32 heads).  Above 32 nodes the operands' two bf16 parts take a whole SM's shared memory.
+//
+// Measured (32 heads): 64 requests of 20 to 32 nodes 98 us; 16 requests of 33 to 64 nodes 68 us, four turns of one CTA
+// an SM, a third of each spent on A, P and T.
 #include "kda_tree_bf16.cuh"
 
 namespace kda {
@@ -32,8 +36,8 @@ constexpr int kD = 128, kWorkers = 256, kThreads = 320;
 
 // Shared memory for trees of at most MP nodes, in bytes.  Operand images are K-major with the 128-byte swizzle, 64
 // elements to a row (keys and queries: two panels of 64 channels), but the state's, which is read as the MN-major
-// A operand (two groups of 64 state columns by 64 rows, a half of the state).  MMAs with fewer than 128 valid A rows read past their
-// image, never past the allocation; what they read there only reaches accumulator rows that nobody looks at.
+// A operand (two groups of 64 state columns by 64 rows, a half of the state).  MMAs with fewer than 128 valid A rows
+// read past their image, never past the allocation; what they read there only reaches accumulator rows that nobody looks at.
 template <int MP>
 struct Layout {
     static constexpr uint32_t kq_panel = 4 * MP * 128;   // rows: K~ hi, Q~ hi, K~ lo, Q~ lo
@@ -195,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
     __shared__ float s_scale[2 * MP];
     __shared__ uint64_t bar_d1, bar_d3, bar_d4, bar_half[2], bar_rows;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_wild;    // A, P, T or G holds something that is not finite
+    __shared__ int s_wild;    // A, P, T or P T holds something that is not finite
     __shared__ int s_bad[4];  // r does, in the columns of one quarter of the lanes
     const int n = blockIdx.x / p.H, h = blockIdx.x % p.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Tree t = tree_rows(p.cu, n, p.total_nodes, p.max_nodes);
@@ -566,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
         tc::fence_async_smem();
         tc::tc_fence_before();
     }
-    ok = __syncthreads_and(ok);  // every wait so far was met; r, T, G and P are complete
+    ok = __syncthreads_and(ok);  // every wait so far was met; r, T, P T and P are complete
     constexpr uint32_t id_2mp = tc::idesc_bf16_f32(128, 2 * MP, false, false);
     if (ok && warp == 9) {
         tc::tc_fence_after();

@@ -1,7 +1,8 @@
 """Python binding of libkda's C ABI (include/kda.h).
 
-Argument marshalling only: every step of the recurrence runs in libkda's
-CUDA kernels.  torch supplies device memory and streams.  There is no CPU or
+Argument marshalling only (ctypes; csrc/kda_tree_py.cpp for the draft-tree
+calls): every step of the recurrence runs in libkda's CUDA kernels.  torch
+supplies device memory and streams.  There is no CPU or
 PyTorch fallback: if libkda.so cannot be loaded, or a tensor is not on a CUDA
 device, the call raises.
 """
