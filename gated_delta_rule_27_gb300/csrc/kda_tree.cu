@@ -27,7 +27,7 @@ namespace {
 // a thread per column, eight nodes at a time.  Where the decays along a path sum to more than kMaxRange, so that
 // e^{-b} would overflow, A and P take the path's own exponents instead.
 // Bound by the multiply-adds with the state, 4 d^2 for each node, and their operands' way from shared memory; with few
-// requests by the latency of its dependent steps (17 requests of up to 13 nodes, 5 heads of d = 64, fp32: 10 us, of
+// requests by the latency of its dependent steps (17 requests of up to 13 nodes, 5 heads of d = 64, fp32: 8.6 us, of
 // which the states' way from HBM is 0.2).
 constexpr int kStepThreads = 128, kStepWarps = kStepThreads / 32;
 constexpr float kMaxRange = 80.f;
@@ -144,6 +144,8 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
     constexpr int kPitch = StepLayout<D>::kPitch;
     extern __shared__ __align__(16) float sm[];
     __shared__ TreeShared ts;
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
     const StepLayout<D> L(max_nodes);
     const int n = blockIdx.x / H, h = blockIdx.x % H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Tree t = tree_rows(cu, n, total_nodes, max_nodes);
@@ -357,11 +359,10 @@ cudaError_t launch_step_d(const TreeStepArgs &a, cudaStream_t st) {
     const int smem = StepLayout<D>(a.max_nodes).bytes();
     const cudaError_t e = allow_smem<tree_step_kernel<Tin, D>>(smem);
     if (e != cudaSuccess) return e;
-    tree_step_kernel<Tin, D><<<a.num_seqs * a.H, kStepThreads, smem, st>>>(
-        (const Tin *)a.q, (const Tin *)a.k, (const Tin *)a.v, a.g, a.beta, a.parent, a.cu, a.seq_idx, a.H,
-        a.total_nodes, a.max_nodes, a.num_slots, a.S_pool, (Tin *)a.o, a.u, a.status, a.fu.qk_norm, a.fu.qk_eps,
-        (const Tin *)a.fu.gate, a.fu.weight, a.fu.out_eps);
-    return cudaGetLastError();
+    return launch_dependent(tree_step_kernel<Tin, D>, a.num_seqs * a.H, kStepThreads, smem, st, (const Tin *)a.q,
+                            (const Tin *)a.k, (const Tin *)a.v, a.g, a.beta, a.parent, a.cu, a.seq_idx, a.H,
+                            a.total_nodes, a.max_nodes, a.num_slots, a.S_pool, (Tin *)a.o, a.u, a.status, a.fu.qk_norm,
+                            a.fu.qk_eps, (const Tin *)a.fu.gate, a.fu.weight, a.fu.out_eps);
 }
 
 template <typename Tin>
@@ -387,7 +388,7 @@ cudaError_t launch_step_t(const TreeStepArgs &a, cudaStream_t st) {
 // where paths may be longer than 8, which would otherwise wait for their rows twice):
 // with the decay to the chunk's end folded into its keys, a chunk is  S <- e^{b} S + sum_a (k_a e^{b - b_a}) u_a^T.
 // Bound by HBM: the state once each way.  Measured, 256 requests x 32 heads of d = 128, bf16, paths of 0 to 6 nodes:
-// 150 us, DRAM busy 78% of the time; 24 warps an SM wait for loads in flight most of theirs.
+// 148 us, DRAM busy 78% of the time; 24 warps an SM wait for loads in flight most of theirs.
 constexpr int kRows = 16;
 
 template <typename Tin, int D, int CHUNK>
@@ -403,6 +404,8 @@ tree_commit_kernel(const Tin *__restrict__ k, const float *__restrict__ g, const
     __shared__ __align__(16) float s_dec[D];
     __shared__ __align__(16) Tin s_raw[CHUNK][D];
     __shared__ float s_scale[CHUNK];
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
     const int n = blockIdx.x / H, h = blockIdx.x % H, tid = threadIdx.x;
     const int len = path_len[n], slot = slot_of(seq_idx, n, num_slots);
     const Tree t = tree_rows(cu, n, total_nodes, kMaxNodes);
@@ -494,10 +497,9 @@ tree_commit_kernel(const Tin *__restrict__ k, const float *__restrict__ g, const
 
 template <typename Tin, int D, int CHUNK>
 cudaError_t launch_commit_c(const TreeCommitArgs &a, cudaStream_t st) {
-    tree_commit_kernel<Tin, D, CHUNK><<<a.num_seqs * a.H, (D / 4) * (D / kRows), 0, st>>>(
-        (const Tin *)a.k, a.g, a.u, a.cu, a.path, a.path_len, a.seq_idx, a.H, a.total_nodes, a.path_stride,
-        a.num_slots, a.S_pool, a.status, a.qk_norm, a.qk_eps);
-    return cudaGetLastError();
+    return launch_dependent(tree_commit_kernel<Tin, D, CHUNK>, a.num_seqs * a.H, (D / 4) * (D / kRows), 0, st,
+                            (const Tin *)a.k, a.g, a.u, a.cu, a.path, a.path_len, a.seq_idx, a.H, a.total_nodes,
+                            a.path_stride, a.num_slots, a.S_pool, a.status, a.qk_norm, a.qk_eps);
 }
 template <typename Tin, int D>
 cudaError_t launch_commit_d(const TreeCommitArgs &a, cudaStream_t st) {
@@ -610,6 +612,8 @@ tree_conv_kernel(const Tin *__restrict__ x, const float *__restrict__ w, const i
     extern __shared__ uint4 rows[];
     Tin *s_x = reinterpret_cast<Tin *>(rows) + threadIdx.x * VEC;
     float *s_past = reinterpret_cast<float *>(reinterpret_cast<char *>(rows) + max_nodes * conv_row_bytes<Tin, VEC>()) + threadIdx.x * VEC;
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
     constexpr int kStride = kConvThreads * VEC;
     const int n = blockIdx.y, tid = threadIdx.x, c = (blockIdx.x * kConvThreads + tid) * VEC;
     const int slot = slot_of(seq_idx, n, num_slots);
@@ -692,6 +696,8 @@ tree_conv_commit_kernel(const Tin *__restrict__ x, const int32_t *__restrict__ c
                         const int32_t *__restrict__ path_len, const int32_t *__restrict__ seq_idx, int total_nodes,
                         int path_stride, int num_slots, int C, int W, float *__restrict__ pool,
                         int32_t *__restrict__ status) {
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
     const int n = blockIdx.y, c = (blockIdx.x * kConvThreads + threadIdx.x) * VEC;
     const int len = path_len[n], slot = slot_of(seq_idx, n, num_slots);
     const Tree t = tree_rows(cu, n, total_nodes, kMaxNodes);
@@ -742,27 +748,23 @@ cudaError_t launch_conv_v(const TreeConvArgs &a, cudaStream_t st) {
     case WW:                                                                                                       \
         e = allow_smem<tree_conv_kernel<Tin, WW, VEC>>((int)smem);                                                 \
         if (e != cudaSuccess) return e;                                                                            \
-        tree_conv_kernel<Tin, WW, VEC><<<grid, kConvThreads, smem, st>>>((const Tin *)a.x, a.w, a.parent, a.cu,    \
-                                                                         a.seq_idx, a.total_nodes, a.max_nodes,    \
-                                                                         a.num_slots, a.C, a.pool, (Tin *)a.y,     \
-                                                                         a.status);                                \
-        break;
+        return launch_dependent(tree_conv_kernel<Tin, WW, VEC>, grid, kConvThreads, smem, st, (const Tin *)a.x,    \
+                                a.w, a.parent, a.cu, a.seq_idx, a.total_nodes, a.max_nodes, a.num_slots, a.C,      \
+                                a.pool, (Tin *)a.y, a.status);
     switch (a.W) {
         KDA_TREE_CONV(1) KDA_TREE_CONV(2) KDA_TREE_CONV(3) KDA_TREE_CONV(4)
         KDA_TREE_CONV(5) KDA_TREE_CONV(6) KDA_TREE_CONV(7) KDA_TREE_CONV(8)
         default: return cudaErrorInvalidValue;
     }
 #undef KDA_TREE_CONV
-    return cudaGetLastError();
 }
 
 template <typename Tin, int VEC>
 cudaError_t launch_conv_commit_v(const TreeConvCommitArgs &a, cudaStream_t st) {
     const dim3 grid((a.C + kConvThreads * VEC - 1) / (kConvThreads * VEC), a.num_seqs);
-    tree_conv_commit_kernel<Tin, VEC><<<grid, kConvThreads, 0, st>>>((const Tin *)a.x, a.cu, a.path, a.path_len,
-                                                                     a.seq_idx, a.total_nodes, a.path_stride,
-                                                                     a.num_slots, a.C, a.W, a.pool, a.status);
-    return cudaGetLastError();
+    return launch_dependent(tree_conv_commit_kernel<Tin, VEC>, grid, kConvThreads, 0, st, (const Tin *)a.x, a.cu,
+                            a.path, a.path_len, a.seq_idx, a.total_nodes, a.path_stride, a.num_slots, a.C, a.W, a.pool,
+                            a.status);
 }
 
 template <typename Tin>

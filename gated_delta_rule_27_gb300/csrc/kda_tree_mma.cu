@@ -16,7 +16,7 @@
 //
 // u is formed to fp32 accuracy as there: every operand in two bf16 parts, hi hi + hi lo + lo hi in fp32.
 //
-// Measured (32 heads, 9 to 16 nodes): 64 requests 51 us, 256 requests 170 us where the bytes' way takes 114.  Issue slots
+// Measured (32 heads, 9 to 16 nodes): 64 requests 49 us, 256 requests 168 us where the bytes' way takes 114.  Issue slots
 // are 47% busy, the tensor pipe 31%, DRAM 57%: with four CTAs an SM the phases that load (the state) and those that only
 // compute (the decays, A, P, T, the stores) overlap in part.
 #include "kda_tree_bf16.cuh"
@@ -167,6 +167,8 @@ __global__ void __launch_bounds__(kThreads, MP == 8 ? 6 : 4) tree_step_mma_kerne
     __shared__ __align__(16) float s_beta[MP];
     __shared__ float s_scale[2 * MP], s_square[kWarps][MP];
     __shared__ int s_wild;  // A, P or T holds something that is not finite
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
     const int n = blockIdx.x / p.H, h = blockIdx.x % p.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
     const Tree t = tree_rows(p.cu, n, p.total_nodes, p.max_nodes);
@@ -518,8 +520,7 @@ cudaError_t launch_mp(const Args &p, int ctas, cudaStream_t st) {
     constexpr int smem = Layout<MP>::total;
     const cudaError_t e = allow_smem<tree_step_mma_kernel<MP>>(smem);
     if (e != cudaSuccess) return e;
-    tree_step_mma_kernel<MP><<<ctas, kThreads, smem, st>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(tree_step_mma_kernel<MP>, ctas, kThreads, smem, st, p);
 }
 
 }  // namespace

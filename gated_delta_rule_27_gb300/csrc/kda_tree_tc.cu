@@ -23,7 +23,7 @@
 // multiplied), and a CTA pulls the inputs of the one that will take its place into L2 (without that 233 us for 207, 256
 // requests of 9 to 16 nodes, 32 heads).  Above 32 nodes the operands' two bf16 parts take a whole SM's shared memory.
 //
-// Measured (32 heads): 64 requests of 20 to 32 nodes 98 us; 16 requests of 33 to 64 nodes 68 us, four turns of one CTA
+// Measured (32 heads): 64 requests of 20 to 32 nodes 98 us; 16 requests of 33 to 64 nodes 66 us, four turns of one CTA
 // an SM, a third of each spent on A, P and T.
 #include "kda_tree_bf16.cuh"
 
@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
     __shared__ uint32_t s_tmem;
     __shared__ int s_wild;    // A, P, T or P T holds something that is not finite
     __shared__ int s_bad[4];  // r does, in the columns of one quarter of the lanes
+    tc::grid_dep_wait();
     const int n = blockIdx.x / p.H, h = blockIdx.x % p.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Tree t = tree_rows(p.cu, n, p.total_nodes, p.max_nodes);
     const int slot = slot_of(p.seq_idx, n, p.num_slots);
@@ -274,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
     }
     const bool good = read_tree(ts, p.parent, p.cu, n, p.total_nodes, p.max_nodes, true, 8).nodes > 0;  // a block barrier
     tc::tc_fence_after();
+    tc::grid_dep_launch();  // not before this CTA has its tensor memory
     const uint32_t tmem = s_tmem;
     if (!good) {
         if (tid == 0) report_invalid(p.status);
@@ -689,8 +691,7 @@ cudaError_t launch_mp(Args p, int ctas, cudaStream_t st) {
     if (e == cudaSuccess) e = sm_count(&sms);
     if (e != cudaSuccess) return e;
     p.ahead = sms * (MP == 64 ? 1 : 2);  // the CTAs that run at once
-    tree_step_tc_kernel<MP><<<ctas, kThreads, smem, st>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(tree_step_tc_kernel<MP>, ctas, kThreads, smem, st, p);
 }
 
 }  // namespace

@@ -20,8 +20,8 @@
 // cluster's CTAs.  So a node's first trial is decided from an fp32 sum that comes with the maximum in one exchange,
 // wherever that decides it (kMargin covers the sum's error a hundred times over); the exact sums are formed only
 // where a trial is closer than that, or lost.  Meanwhile the first child's row is on its way to L2.
-// Measured: one request, a chain of 5 drafted from given distributions, 32768 fp32 logits a row: 16 us; 64 requests with
-// trees of 9 to 16 nodes over 131072 bf16 logits 49 us; 256 chains of 4 to 8 without distributions over 100003 59 us.
+// Measured: one request, a chain of 5 drafted from given distributions, 32768 fp32 logits a row: 9 to 15 us with the walk's length; 64 requests with
+// trees of 9 to 16 nodes over 131072 bf16 logits 45 to 53 us; 256 chains of 4 to 8 without distributions over 100003 56 to 60 us.
 // The others wait for the longest walk of the batch, several rejections among its trials at about 5 us each: DRAM is
 // 17% busy.
 #include <cooperative_groups.h>
@@ -296,6 +296,7 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
     constexpr int kBatch = 16 / P::kVec;
     extern __shared__ uint4 kept[];
     __shared__ Shared sh;
+    tc::grid_dep_wait();
     cg::cluster_group cluster = cg::this_cluster();
     const int size = cluster.num_blocks(), rank = cluster.block_rank();
     const int n = blockIdx.x / size, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -644,6 +645,9 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
     } else if (writer && owner < 0) {
         p.next_token[n] = next;
     }
+    // (Let in at the start, the next kernel's clusters would take the places of the first walks to end and lie uneven
+    // over the SMs: 64 requests over 131072 tokens 48.4, 56.5 and 45.5 us on three draws, here 48.0, 52.7 and 44.8.)
+    tc::grid_dep_launch();
     if (!ex.ok) {  // an exchange that never came: an empty path
         len = 0;
         if (writer && p.status) atomicCAS(p.status, 0, (int32_t)KDA_ERR_TIMEOUT);
@@ -676,12 +680,14 @@ cudaError_t launch_t(Args p, int num_seqs, cudaStream_t st) {
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = p.part_bytes;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = size;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 2;
     e = allow_smem<draft_verify_kernel<Tin>>(kMaxPart);
     if (e != cudaSuccess) return e;
     return cudaLaunchKernelEx(&cfg, draft_verify_kernel<Tin>, (const Args)p);
