@@ -155,6 +155,7 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
         return;
     }
     if (t.nodes == 0) return;
+    const Links links = load_links(parent, t);
     const int M = t.nodes;
     const size_t row_stride = (size_t)H * D, base = ((size_t)t.row0 * H + h) * D;
     const float *S = S_pool + ((size_t)slot * H + h) * D * D;
@@ -168,7 +169,7 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
     tc::cp_async_commit();
     for (int i = tid; i < M; i += kStepThreads) sm[L.beta + i] = beta[(size_t)(t.row0 + i) * H + h];
     tc::cp_async_wait<1>();
-    if (read_tree(ts, parent, cu, n, total_nodes, max_nodes, true).nodes < 0) {  // a block barrier
+    if (!read_tree(ts, t, links, true)) {  // a block barrier
         tc::cp_async_wait_all();
         if (tid == 0) report_invalid(status);
         return;
@@ -617,11 +618,12 @@ tree_conv_kernel(const Tin *__restrict__ x, const float *__restrict__ w, const i
     constexpr int kStride = kConvThreads * VEC;
     const int n = blockIdx.y, tid = threadIdx.x, c = (blockIdx.x * kConvThreads + tid) * VEC;
     const int slot = slot_of(seq_idx, n, num_slots);
-    const Tree own = tree_rows(cu, n, total_nodes, max_nodes);
+    const Tree t = tree_rows(cu, n, total_nodes, max_nodes);
+    const Links links = load_links(parent, t);
     float wt[W][VEC];
-    if (c < C && own.nodes > 0 && slot >= 0) {
-        for (int i = 0; i < own.nodes; ++i)
-            fetch_row<Tin, VEC>(s_x + i * kStride, x + (size_t)(own.row0 + i) * C + c);
+    if (c < C && t.nodes > 0 && slot >= 0) {
+        for (int i = 0; i < t.nodes; ++i)
+            fetch_row<Tin, VEC>(s_x + i * kStride, x + (size_t)(t.row0 + i) * C + c);
         for (int m = 0; m < W - 1; ++m)  // the newest first
             fetch_row<float, VEC>(s_past + m * kStride, pool + ((size_t)slot * (W - 1) + (W - 2 - m)) * C + c);
         float all[W * VEC];
@@ -636,8 +638,7 @@ tree_conv_kernel(const Tin *__restrict__ x, const float *__restrict__ w, const i
 #pragma unroll
             for (int e = 0; e < VEC; ++e) wt[j][e] = all[e * W + j];
     }
-    const Tree t = read_tree(ts, parent, cu, n, total_nodes, max_nodes, false);
-    if (t.nodes < 0 || slot < 0) {
+    if (!read_tree(ts, t, links, false) || slot < 0) {
         if (tid == 0) report_invalid(status);
         tc::cp_async_wait_all();
         return;

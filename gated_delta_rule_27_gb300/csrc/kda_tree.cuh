@@ -28,62 +28,77 @@ __device__ __forceinline__ Tree tree_rows(const int32_t *__restrict__ cu, int n,
     return Tree{lo, hi - lo};
 }
 
-// One warp reads and checks request n's tree, the block waits for it (one block barrier).  Returns nodes = -1,
-// where it breaks the rules.
-// The paths come from pointer doubling: after r rounds a node's mask covers its 2^r nearest ancestors.
-__device__ __forceinline__ Tree read_tree(TreeShared &ts, const int32_t *__restrict__ parent,
-                                          const int32_t *__restrict__ cu, int n, int total_nodes, int max_nodes,
-                                          bool want_paths, int reader = 0) {
-    const Tree t = tree_rows(cu, n, total_nodes, max_nodes);
-    const int tid = (int)threadIdx.x - 32 * reader;
-    if (tid >= 0 && tid < 32) {
+// The parents of the nodes that a lane of warp `reader` checks (i = lane, lane + 32), asked for as early as the rows are
+// known: read_tree() would wait for them alone.
+struct Links {
+    int p[2];
+};
+__device__ __forceinline__ Links load_links(const int32_t *__restrict__ parent, const Tree &t, int reader = 0) {
+    const int lane = (int)threadIdx.x - 32 * reader;
+    Links l{{-1, -1}};
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+        if (lane >= 0 && lane < 32 && lane + 32 * r < t.nodes) l.p[r] = parent[t.row0 + lane + 32 * r];
+    return l;
+}
+
+// Warp `reader` checks request n's tree, the block waits for it (one block barrier).  Returns false where it breaks
+// the rules.  The paths (where they are wanted) come from pointer doubling: after r rounds a node's mask covers its 2^r
+// nearest ancestors.  Trees of up to 16 nodes have mask and link in one word, so that a round is one exchange.
+__device__ __forceinline__ bool read_tree(TreeShared &ts, const Tree &t, const Links &links, bool want_paths, int reader = 0) {
+    const int lane = (int)threadIdx.x - 32 * reader;
+    if (lane >= 0 && lane < 32) {
         bool bad = t.nodes < 0;
-        for (int i = tid; i < t.nodes; i += 32) {
-            const int p = parent[t.row0 + i];
-            bad |= i == 0 ? p != -1 : (p < 0 || p >= i);
-            ts.parent[i] = p;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int i = lane + 32 * r, p = links.p[r];
+            if (i < t.nodes) {
+                bad |= i == 0 ? p != -1 : (p < 0 || p >= i);
+                ts.parent[i] = p;
+            }
         }
         bad = __any_sync(0xffffffffu, bad);
-        if (tid == 0) ts.bad = bad;
+        if (lane == 0) ts.bad = bad;
         if (want_paths && !bad) {
-            __syncwarp();
-            // two nodes per lane: i = tid, tid + 32
-            unsigned long long m[2];
-            int jump[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int i = tid + 32 * r;
-                m[r] = 1ull << i;
-                jump[r] = i < t.nodes ? ts.parent[i] : -1;
-            }
-            for (int span = 1; span < t.nodes; span <<= 1) {
-                unsigned long long up[2];
-                int next[2];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int j = jump[r] < 0 ? 0 : jump[r];
-                    const unsigned long long lo = __shfl_sync(0xffffffffu, m[0], j & 31);
-                    const unsigned long long hi = __shfl_sync(0xffffffffu, m[1], j & 31);
-                    const int nlo = __shfl_sync(0xffffffffu, jump[0], j & 31);
-                    const int nhi = __shfl_sync(0xffffffffu, jump[1], j & 31);
-                    up[r] = j < 32 ? lo : hi;
-                    next[r] = j < 32 ? nlo : nhi;
+            if (t.nodes <= 16) {
+                uint32_t w = lane < t.nodes ? 1u << lane | (uint32_t)(links.p[0] + 1) << 16 : 0u;
+                for (int span = 1; span < t.nodes; span <<= 1) {
+                    const uint32_t up = __shfl_sync(0xffffffffu, w, (int)(w >> 16) - 1);
+                    if (w >> 16) w = ((w | up) & 0xffffu) | (up & 0xffff0000u);
                 }
+                if (lane < t.nodes) ts.anc[lane] = w & 0xffffu;
+            } else {
+                unsigned long long m[2] = {1ull << lane, 1ull << (lane + 32)};
+                int jump[2] = {links.p[0], links.p[1]};
+                for (int span = 1; span < t.nodes; span <<= 1) {
+                    unsigned long long up[2];
+                    int next[2];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    if (jump[r] >= 0) {
-                        m[r] |= up[r];
-                        jump[r] = next[r];
+                    for (int r = 0; r < 2; ++r) {
+                        const int j = jump[r] < 0 ? 0 : jump[r];
+                        const unsigned long long lo = __shfl_sync(0xffffffffu, m[0], j & 31);
+                        const unsigned long long hi = __shfl_sync(0xffffffffu, m[1], j & 31);
+                        const int nlo = __shfl_sync(0xffffffffu, jump[0], j & 31);
+                        const int nhi = __shfl_sync(0xffffffffu, jump[1], j & 31);
+                        up[r] = j < 32 ? lo : hi;
+                        next[r] = j < 32 ? nlo : nhi;
+                    }
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        if (jump[r] >= 0) {
+                            m[r] |= up[r];
+                            jump[r] = next[r];
+                        }
                     }
                 }
-            }
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-                if (tid + 32 * r < t.nodes) ts.anc[tid + 32 * r] = m[r];
+                for (int r = 0; r < 2; ++r)
+                    if (lane + 32 * r < t.nodes) ts.anc[lane + 32 * r] = m[r];
+            }
         }
     }
     __syncthreads();
-    return ts.bad ? Tree{0, -1} : t;
+    return !ts.bad;
 }
 
 // A log-decay, cut where its exponential is zero in fp32, so that sums along a path and their differences stay

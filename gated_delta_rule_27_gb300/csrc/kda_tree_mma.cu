@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, MP == 8 ? 6 : 4) tree_step_mma_kerne
         return;
     }
     if (t.nodes == 0) return;
+    const Links links = load_links(p.parent, t);
     const int M = t.nodes;
     const size_t base = ((size_t)t.row0 * p.H + h) * kD, row_stride = (size_t)p.H * kD;
 
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, MP == 8 ? 6 : 4) tree_step_mma_kerne
         float4 *x = reinterpret_cast<float4 *>(sm + L::b + ((i & ~31) + spread(i & 31)) * 16);
         *x = log2_decay4(*x);
     }
-    if (read_tree(ts, p.parent, p.cu, n, p.total_nodes, p.max_nodes, true, 0).nodes < 0) {  // a block barrier
+    if (!read_tree(ts, t, links, true)) {  // a block barrier
         tc::cp_async_wait_all();
         if (tid == 0) report_invalid(p.status);
         return;

@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
         return;
     }
     if (t.nodes == 0) return;
+    const Links links = load_links(p.parent, t, 8);
     const int M = t.nodes;
     uint8_t *sm = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
     const uint32_t sa = tc::smem_u32(sm);
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
         lt = tree_rows(p.cu, later / p.H, p.total_nodes, p.max_nodes);
         lslot = slot_of(p.seq_idx, later / p.H, p.num_slots);
     }
-    const bool good = read_tree(ts, p.parent, p.cu, n, p.total_nodes, p.max_nodes, true, 8).nodes > 0;  // a block barrier
+    const bool good = read_tree(ts, t, links, true, 8);  // a block barrier
     tc::tc_fence_after();
     tc::grid_dep_launch();  // not before this CTA has its tensor memory
     const uint32_t tmem = s_tmem;

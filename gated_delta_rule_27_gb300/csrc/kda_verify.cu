@@ -333,7 +333,8 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
         token = p.tokens[root.row0 + mine];
         number = p.u[root.row0 + mine];
     }
-    const Tree t = read_tree(sh.tree, p.parent, p.cu, n, p.total_nodes, min(p.path_stride, kMaxNodes), false);
+    const Links links = load_links(p.parent, root);
+    const Tree t = read_tree(sh.tree, root, links, false) ? root : Tree{0, -1};
     if (t.nodes < 0 && writer) report_invalid(p.status);
     if (tid < t.nodes) {
         unsigned long long mask = 0;
