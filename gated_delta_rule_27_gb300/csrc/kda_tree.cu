@@ -373,8 +373,8 @@ cudaError_t launch_step_t(const TreeStepArgs &a, cudaStream_t st) {
         case 64: return launch_step_d<Tin, 64>(a, st);
         case 128:
             if constexpr (sizeof(Tin) == 4) return launch_step_d<Tin, 128>(a, st);
-            // (256 requests x 32 heads: 3-6 nodes 102 us with the state in registers, 176 with tcgen05; 9-16 nodes 171
-            // and 207; 64 requests of 20-32 nodes 138 and 98)
+            // (256 requests x 32 heads: 3-6 nodes 99 us with the state in registers, 241 with tcgen05; 9-16 nodes 163
+            // and 273; with a variant of the former for 32 nodes, 64 requests of 20-32 took 138 and 98)
             else return a.max_nodes <= 16 ? launch_tree_step_mma(a, st) : launch_tree_step_tc(a, st);
         default: return cudaErrorInvalidValue;
     }

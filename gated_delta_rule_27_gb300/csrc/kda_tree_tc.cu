@@ -11,7 +11,8 @@
 //
 // u moves the fp32 state, so it is formed to fp32 accuracy: every operand is split into two bf16 parts, hi + lo,
 // and each product takes hi hi + hi lo + lo hi with fp32 accumulators (2^-17 relative to a term; one part alone
-// would leave 2^-9); T comes from an fp32 substitution.  A, P and T are done while the state arrives.  A factor
+// would leave 2^-9); T comes from fp32 substitutions in blocks of 16 nodes and products of the blocks in the same
+// two parts.  A, P and T are done while the state arrives.  A factor
 // e^{-b} would overflow where the decays along a path sum to more than kMaxRange; such a request takes its A and P
 // pairwise from the path's own exponents instead.
 //
@@ -20,11 +21,12 @@
 //
 // What bounds it is the length of one CTA's dependent steps, so CTAs of up to 32 nodes are kept small enough for two to
 // share an SM (the state passes through shared memory in two halves of 64 rows, half 1 loading while half 0 is
-// multiplied), and a CTA pulls the inputs of the one that will take its place into L2 (without that 233 us for 207, 256
-// requests of 9 to 16 nodes, 32 heads).  Above 32 nodes the operands' two bf16 parts take a whole SM's shared memory.
+// multiplied), and a CTA pulls the inputs of the one that will take its place into L2 (without that 233 us for 207 when
+// a variant for 16 nodes took 256 requests of 9 to 16, 32 heads).  Above 32 nodes the operands' two bf16 parts take a whole SM's shared memory.
 //
-// Measured (32 heads): 64 requests of 20 to 32 nodes 98 us; 16 requests of 33 to 64 nodes 66 us, four turns of one CTA
-// an SM, a third of each spent on A, P and T.
+// Measured (32 heads): 64 requests of 20 to 32 nodes 88 us, 16 requests of 33 to 64 nodes 62 us, four turns of one CTA
+// an SM.  A CTA's time goes in about equal parts to its first reads and the images of K~, Q~ and K^, to the state's
+// images with A, P and T (all eight warps; four of them form r meanwhile), and to u, o and their stores.
 #include "kda_tree_bf16.cuh"
 
 namespace kda {
@@ -53,13 +55,13 @@ struct Layout {
     static constexpr uint32_t b_bytes = MP * 512 > ap_tg ? MP * 512 : (ap_tg + 1023) / 1024 * 1024;
     static constexpr uint32_t v = b + b_bytes;           // bf16 [MP][128]
     static constexpr uint32_t w = v + MP * 256;          // fp32 [128]: the output weight
-    static constexpr uint32_t tb = w + 512;              // fp32 3 x [32][36]: the blocks of T (MP = 64)
-    static constexpr uint32_t total = MP == 64 ? tb + 3 * 32 * 36 * 4 : tb;
+    static constexpr uint32_t tb = w + 512;              // MP = 64: T and the place of a product, below
+    static constexpr uint32_t total = MP == 64 ? tb + (64 * ap_stride + 32 * 36) * 4 : tb;
     // later uses of the same bytes
     static constexpr uint32_t t_img = ki;                // rows T - I hi, P T hi, T - I lo, P T lo (MP = 64: T - I hi, lo)
     static constexpr uint32_t p_img = ki + MP * 256;     // MP = 64: P hi, lo   (both once D1 is done)
     static constexpr uint32_t ap = b;                    // fp32 A [MP][ap_stride], then P (once the images are built)
-    static constexpr uint32_t tg = MP < 64 ? ap + ap_bytes : tb;  // fp32 T - I [MP][ap_stride], then P T (MP = 64: tb)
+    static constexpr uint32_t tg = MP < 64 ? ap + ap_bytes : tb;  // fp32 T [MP][ap_stride], then P T (MP = 64: a product)
     static constexpr uint32_t r_img = s_hi;              // r: 128 rows hi, 128 rows lo (once D2 is done)
     static constexpr uint32_t u_img = s_hi;              // MP = 64: u, the same way (once D3 is done)
     static constexpr uint32_t z = kq;                    // bf16 [MP][128]: the gate (once D2 is done)
@@ -76,12 +78,6 @@ __device__ __forceinline__ void store_split8(uint8_t *img, int row, int col, int
     const uint32_t at = tc::sw128_offset(row, col);
     *reinterpret_cast<uint4 *>(img + at) = hi;
     *reinterpret_cast<uint4 *>(img + lo_rows * 128 + at) = lo;
-}
-__device__ __forceinline__ void store_split1(uint8_t *img, int row, int col, int lo_rows, float f) {
-    const __nv_bfloat16 hi = __float2bfloat16_rn(f), lo = __float2bfloat16_rn(f - __bfloat162float(hi));
-    const uint32_t at = tc::sw128_offset(row, col);
-    *reinterpret_cast<__nv_bfloat16 *>(img + at) = hi;
-    *reinterpret_cast<__nv_bfloat16 *>(img + lo_rows * 128 + at) = lo;
 }
 __device__ __forceinline__ void ldg8(const float *p, float (&f)[8]) {
     asm volatile("ld.global.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -136,13 +132,64 @@ __device__ void solve_masked(uint8_t *sm, const TreeShared &ts, const float *s_b
     }
 }
 
-// One column of P T (P zero above its diagonal) to g[i * stride].
-template <int NB, int I = 0>
-__device__ __forceinline__ void multiply_block(const float *P, int stride, const float (&t)[NB], float *g) {
-    if constexpr (I < NB) {
-        g[I * stride] = row_dot<I + 1>(P + I * stride, t);
-        multiply_block<NB, I + 1>(P, stride, t, g);
+__device__ __forceinline__ void warp_mma(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
+    hi = pack2(x, y);
+    lo = pack2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+}
+// The 16 x 8 tile  sum_{a < K} left[.][a] right[a][.]  of two fp32 matrices in shared memory, in two bf16 parts, as
+// T's image will hold it (on the CUDA cores in fp32 the joins took 3 of 65 us, 16 requests of 33 to 64 nodes).
+template <int K>
+__device__ __forceinline__ void tile_product(const float *left, int ls, const float *right, int rs, float (&c)[4]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = (lane & 3) * 2;
+    float d[3][4] = {};
+#pragma unroll
+    for (int k = 0; k < K; k += 16) {
+        uint32_t ahi[4], alo[4], bhi[2], blo[2];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const float2 x = *reinterpret_cast<const float2 *>(left + (g + 8 * (r & 1)) * ls + k + t + 8 * (r >> 1));
+            split2(x.x, x.y, ahi[r], alo[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float *y = right + (k + t + 8 * r) * rs + g;
+            split2(y[0], y[rs], bhi[r], blo[r]);
+        }
+        warp_mma(d[0], ahi, bhi);
+        warp_mma(d[1], alo, bhi);
+        warp_mma(d[2], ahi, blo);
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = d[0][e] + d[1][e] + d[2][e];
+}
+// The blocks below the diagonal of T = (I + A)^{-1}, from those on it:  T21 = -T22 (A21 T11), for each pair of NB x NB
+// blocks, a 16 x 8 tile a warp; `tmp` holds the product in brackets, [32][36].
+template <int MP, int NB>
+__device__ __forceinline__ void join_blocks(const float *A, float *T, float *tmp, int tid) {
+    constexpr int kStride = Layout<MP>::ap_stride, kTiles = NB * NB / 128;
+    const int warp = tid >> 5, pair = warp / kTiles, i = warp % kTiles / (NB / 8) * 16, j = warp % (NB / 8) * 8;
+    const int r = i + ((tid & 31) >> 2), cc = j + (tid & 3) * 2;
+    const bool in = pair < MP / (2 * NB);
+    const int at = (2 * pair * NB) * (kStride + 1);  // of the pair's first block
+    float x[4];
+    if (in) {
+        tile_product<NB>(A + at + (NB + i) * kStride, kStride, T + at + j, kStride, x);
+        float *w = tmp + (pair * NB + r) * 36 + cc;
+        w[0] = x[0]; w[1] = x[1]; w[8 * 36] = x[2]; w[8 * 36 + 1] = x[3];
+    }
+    tc::named_barrier(1, kWorkers);
+    if (in) {
+        tile_product<NB>(T + at + (NB + i) * kStride + NB, kStride, tmp + pair * NB * 36 + j, 36, x);
+        float *w = T + at + (NB + r) * kStride + cc;
+        w[0] = -x[0]; w[1] = -x[1]; w[8 * kStride] = -x[2]; w[8 * kStride + 1] = -x[3];
+    }
+    tc::named_barrier(1, kWorkers);
 }
 
 // The MMAs of D = A_hi B^T + A_lo B'^T over MP / 16 slices of 16 elements; B' is the first part of B's rows.
@@ -157,10 +204,11 @@ __device__ __forceinline__ void mma_split(uint32_t d, uint32_t a_hi, uint32_t a_
         tc::mma_bf16_warp(d, tc::smem_desc(kKmaj, a_lo + c * 32), tc::smem_desc(kKmaj, b + c * 32), IdLo, true, elected);
 }
 
-// Reads the rows of D1 that belong to this warp's lanes (row r of [K~ ; Q~]), masks and scales them into A and P.
+// Reads one half of the columns of the rows of D1 that belong to this warp's lanes (row r of [K~ ; Q~]), masks and
+// scales them into A and P.
 template <int MP>
 __device__ __forceinline__ void read_paths(uint8_t *sm, const TreeShared &ts, const float *s_beta, uint32_t tmem, int M,
-                                           int row, bool pairwise, int *s_wild) {
+                                           int row, int half, bool pairwise, int *s_wild) {
     using L = Layout<MP>;
     const bool is_a = row < MP;
     const int i = is_a ? row : row - MP;
@@ -169,7 +217,7 @@ __device__ __forceinline__ void read_paths(uint8_t *sm, const TreeShared &ts, co
     float *dst = reinterpret_cast<float *>(sm + L::ap) + ((is_a ? 0 : MP) + i) * L::ap_stride;
     float zero = 0.f;  // NaN once it has met something that is not finite
 #pragma unroll 2
-    for (int a0 = 0; a0 < MP; a0 += 8) {
+    for (int a0 = half * (MP / 2); a0 < (half + 1) * (MP / 2); a0 += 8) {
         float val[8];
         if (!pairwise) {
             float x[2][8];
@@ -461,85 +509,24 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bar_rows);
     }
-    if (warp >= 4 && warp < 8) {
-        // A, P, T and the images that u and o are formed with
-        const int w = warp - 4;
-        float *tb = reinterpret_cast<float *>(sm + L::tg);  // T - I and P T; or T's diagonal blocks and A21 T11, [32][36] each
+    float *sT = reinterpret_cast<float *>(sm + L::tg), *tmp = sT + MP * L::ap_stride;
+    if (warp < 8) {  // A and P
         if (!pairwise) ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bar_d1, 0));
         tc::tc_fence_after();
-        if (w * 32 < 2 * MP) read_paths<MP>(sm, ts, s_beta, tmem, M, w * 32 + lane, pairwise, &s_wild);
-        float zero = 0.f;
-        if constexpr (MP < 64) {
-            // one warp writes T - I, another forms P T from the same T, a column a lane
-            tc::named_barrier(1, 128);
-            if (w < 2) {
-                float tc_[MP];
-                invert_block<MP>(sA, L::ap_stride, lane, tc_);
-                if (w == 0) {
+        if ((warp & 3) * 32 < 2 * MP) read_paths<MP>(sm, ts, s_beta, tmem, M, (warp & 3) * 32 + lane, warp >> 2, pairwise, &s_wild);
+        tc::named_barrier(1, kWorkers);
+    }
+    if (warp >= 4 && warp < 8) {
+        // T's blocks of 16 on the diagonal, one a warp, while the other warps form r
+        const int b0 = (warp - 4) * 16;
+        if (b0 < MP) {
+            float t[16];
+            invert_block<16>(sA + b0 * (L::ap_stride + 1), L::ap_stride, lane, t);
+            if (lane < 16 || (b0 & 16) == 0) {  // (the zeros beside an upper block are read with it)
 #pragma unroll
-                    for (int i = 0; i < MP; ++i) tb[i * L::ap_stride + lane] = i == lane ? 0.f : tc_[i];
-                } else {
-                    multiply_block<MP>(sP, L::ap_stride, tc_, tb + MP * L::ap_stride + lane);
-                }
-            }
-            tc::named_barrier(1, 128);
-            for (int x = tid - 128; x < 2 * MP * (MP / 8); x += 128) {
-                const int row = x / (MP / 8), c0 = x % (MP / 8) * 8;
-                float f[8];
-                read8(tb + row * L::ap_stride + c0, f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) zero = fmaf(f[e], 0.f, zero);
-                store_split8(sm + L::t_img, row, c0, 2 * MP, f);
-            }
-        } else {
-            tc::named_barrier(1, 128);
-            if (w < 2) {
-                float tc_[32];
-                invert_block<32>(sA + w * 32 * (L::ap_stride + 1), L::ap_stride, lane, tc_);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    zero = fmaf(tc_[i], 0.f, zero);
-                    store_split1(sm + L::t_img, w * 32 + i, w * 32 + lane, MP, i == lane ? 0.f : tc_[i]);
-                    tb[w * 32 * 36 + i * 36 + lane] = tc_[i];
-                }
-            }
-            // T21 = -T22 (A21 T11); nothing above the diagonal
-            tc::named_barrier(1, 128);
-            const int i = (tid - 128) >> 2, j0 = (tid & 3) * 8;
-            const float none[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            store_split8(sm + L::t_img, i, 32 + j0, MP, none);
-#pragma unroll
-            for (int step = 0; step < 2; ++step) {
-                const float *left = step ? tb + 32 * 36 + i * 36 : sA + (32 + i) * L::ap_stride;
-                const float *right = step ? tb + 2 * 32 * 36 : tb;
-                float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-                for (int a = 0; a < 32; ++a) {
-                    const float x = left[a];
-                    const float4 *y = reinterpret_cast<const float4 *>(right + a * 36 + j0);
-                    const float4 y0 = y[0], y1 = y[1];
-                    acc[0] = fmaf(x, y0.x, acc[0]); acc[1] = fmaf(x, y0.y, acc[1]);
-                    acc[2] = fmaf(x, y0.z, acc[2]); acc[3] = fmaf(x, y0.w, acc[3]);
-                    acc[4] = fmaf(x, y1.x, acc[4]); acc[5] = fmaf(x, y1.y, acc[5]);
-                    acc[6] = fmaf(x, y1.z, acc[6]); acc[7] = fmaf(x, y1.w, acc[7]);
-                }
-                if (step == 0) {
-                    float4 *dst = reinterpret_cast<float4 *>(tb + 2 * 32 * 36 + i * 36 + j0);
-                    dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-                    dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-                    tc::named_barrier(1, 128);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        acc[e] = -acc[e];
-                        zero = fmaf(acc[e], 0.f, zero);
-                    }
-                    store_split8(sm + L::t_img, 32 + i, j0, MP, acc);
-                }
+                for (int i = 0; i < 16; ++i) sT[(b0 + i) * L::ap_stride + b0 + lane] = t[i];
             }
         }
-        if (zero != 0.f) s_wild = 1;
-        tc::fence_async_smem();
         if (p.gate) {  // the gate, into the place of D2's operands
             ok &= __all_sync(0xffffffffu, tc::mbar_wait(&bar_half[1], 0));
             for (int i = tid - 128; i < M * 16; i += 128)
@@ -570,6 +557,35 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
             store_split8(sm + L::r_img, col, i0, 128, r);
         }
         if (zero != 0.f) s_bad[warp & 3] = 1;
+    }
+    if (warp < 8) {  // the rest of T, and the images that u and o are formed with
+        tc::named_barrier(1, kWorkers);
+        join_blocks<MP, 16>(sA, sT, tmp, tid);
+        if constexpr (MP == 64) {
+            join_blocks<MP, 32>(sA, sT, tmp, tid);
+        } else {  // P T
+            float x[4];
+            const int i = (warp >> 2) * 16, j = (warp & 3) * 8;
+            tile_product<32>(sP + i * L::ap_stride, L::ap_stride, sT + j, L::ap_stride, x);
+            float *to = tmp + (i + (lane >> 2)) * L::ap_stride + j + (lane & 3) * 2;
+            to[0] = x[0]; to[1] = x[1]; to[8 * L::ap_stride] = x[2]; to[8 * L::ap_stride + 1] = x[3];
+            tc::named_barrier(1, kWorkers);
+        }
+        float zero = 0.f;
+        constexpr int kRows = MP == 64 ? MP : 2 * MP;  // T - I (and P T behind it)
+#pragma unroll
+        for (int x = tid; x < kRows * (MP / 8); x += kWorkers) {
+            const int row = x / (MP / 8), c0 = x % (MP / 8) * 8;
+            float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (row >= MP || c0 <= row) read8(sT + row * L::ap_stride + c0, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (c0 + e == row) f[e] = 0.f;
+                zero = fmaf(f[e], 0.f, zero);
+            }
+            store_split8(sm + L::t_img, row, c0, kRows, f);
+        }
+        if (zero != 0.f) s_wild = 1;
         tc::fence_async_smem();
         tc::tc_fence_before();
     }
