@@ -16,7 +16,7 @@
 //
 // u is formed to fp32 accuracy as there: every operand in two bf16 parts, hi hi + hi lo + lo hi in fp32.
 //
-// Measured (32 heads, 9 to 16 nodes): 64 requests 49 us, 256 requests 168 us where the bytes' way takes 114.  Issue slots
+// Measured (32 heads, 9 to 16 nodes): 64 requests 46 us, 256 requests 162 us where the bytes' way takes 114.  Issue slots
 // are 47% busy, the tensor pipe 31%, DRAM 57%: with four CTAs an SM the phases that load (the state) and those that only
 // compute (the decays, A, P, T, the stores) overlap in part.
 #include "kda_tree_bf16.cuh"
@@ -346,18 +346,44 @@ __global__ void __launch_bounds__(kThreads, MP == 8 ? 6 : 4) tree_step_mma_kerne
         if (zero != 0.f) s_wild = 1;
     }
     __syncthreads();  // A and P are complete, and K^ is no longer needed
-    if (warp == 0) {  // T - I, a column a lane
+    if (warp == 0) {  // T - I
+        // the blocks of eight on the diagonal, a column a lane, then (MP = 16) the one below it, T21 = -T22 (A21 T11)
+        constexpr int kS = L::ap_stride;
         float *sT = reinterpret_cast<float *>(sm + L::t);
-        float tc_[MP], zero = 0.f;
-        invert_block<MP>(sA, L::ap_stride, lane, tc_);
+        const int block = MP == 8 ? 0 : lane & 8, c = lane & 7;
+        float t[8], zero = 0.f;
+        invert_block<8>(sA + block * (kS + 1), kS, c, t);
         if (lane < MP) {
 #pragma unroll
-            for (int i = 0; i < MP; ++i) {
-                zero = fmaf(tc_[i], 0.f, zero);
-                sT[i * L::ap_stride + lane] = i == lane ? 0.f : tc_[i];
+            for (int i = 0; i < 8; ++i) {
+                zero = fmaf(t[i], 0.f, zero);
+                sT[(block + i) * kS + block + c] = MP == 8 && i == c ? 0.f : t[i];
             }
-            if (zero != 0.f) s_wild = 1;
+        } else if (MP == 16 && block == 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sT[i * kS + 8 + c] = 0.f;
         }
+        if constexpr (MP == 16) {
+            const int r = 8 + g, j = 2 * t4;  // two entries of T21 a lane
+            float2 *w = reinterpret_cast<float2 *>(sT + r * kS + j);
+            auto row_times = [&](const float *left, const float *right) {
+                float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int a = 0; a < 8; ++a)
+                    acc = tc::fma2(make_float2(left[a], left[a]), *reinterpret_cast<const float2 *>(right + a * kS), acc);
+                return acc;
+            };
+            __syncwarp();
+            const float2 x = row_times(sA + r * kS, sT + j);
+            *w = x;
+            __syncwarp();
+            const float2 y = row_times(sT + r * kS + 8, sT + 8 * kS + j);
+            __syncwarp();
+            *w = make_float2(-y.x, -y.y);
+            if (lane < MP) sT[lane * (kS + 1)] = 0.f;
+            zero = fmaf(y.x, 0.f, fmaf(y.y, 0.f, zero));
+        }
+        if (zero != 0.f) s_wild = 1;
     }
 
     // X^T and Y^T of the warp's 32 columns, 16 state rows at a time.  Of node tile j a lane holds nodes
