@@ -12,6 +12,8 @@
 //
 // and the state after the path that ends in node l is  e^{b_l} S + sum_a (k_a e^{b_l - b_a}) u_a^T, so the
 // commit needs the stored u and no second recurrence: it is one pass over the state.
+#include <type_traits>
+
 #include "kda_tc.cuh"
 #include "kda_tree.cuh"
 
@@ -27,7 +29,7 @@ namespace {
 // a thread per column, eight nodes at a time.  Where the decays along a path sum to more than kMaxRange, so that
 // e^{-b} would overflow, A and P take the path's own exponents instead.
 // Bound by the multiply-adds with the state, 4 d^2 for each node, and their operands' way from shared memory; with few
-// requests by the latency of its dependent steps (17 requests of up to 13 nodes, 5 heads of d = 64, fp32: 8.6 us, of
+// requests by the latency of its dependent steps (17 requests of up to 13 nodes, 5 heads of d = 64, fp32: 8.7 us, of
 // which the states' way from HBM is 0.2).
 constexpr int kStepThreads = 128, kStepWarps = kStepThreads / 32;
 constexpr float kMaxRange = 80.f;
@@ -41,8 +43,8 @@ struct StepLayout {  // offsets in floats; R: rows, max_nodes rounded up to eigh
         ap_stride = R + 4;
         ke = 0;
         qe = ke + R * kPitch;
-        ki = qe + R * kPitch;   // K^, then x and u [R][D]
-        gb = ki + R * kPitch;   // g, then b, then y and o [R][D]
+        ki = qe + R * kPitch;   // K^, then r [R][D]
+        gb = ki + R * kPitch;   // g, then b, then y [R][D]
         A = gb + R * D;
         P = A + R * ap_stride;
         beta = P + R * ap_stride;
@@ -55,11 +57,21 @@ struct StepLayout {  // offsets in floats; R: rows, max_nodes rounded up to eigh
     __host__ __device__ int bytes() const { return (keeps_state() ? total : S) * 4; }
 };
 
-// CPL neighbouring values of a row as fp32.
-template <int CPL, typename Tin>
-__device__ __forceinline__ void load_some(const Tin *p, float (&f)[CPL]) {
+// N neighbouring values of a row, read and written at once.
+template <typename T, int N>
+struct __align__(N * sizeof(T)) Some {
+    T v[N];
+};
+template <int N, typename T>
+__device__ __forceinline__ Some<T, N> load_some(const T *p, bool in) {
+    Some<T, N> x;
+    if (in) {
+        x = *reinterpret_cast<const Some<T, N> *>(p);
+    } else {
 #pragma unroll
-    for (int e = 0; e < CPL; ++e) f[e] = to_f32(p[e]);
+        for (int e = 0; e < N; ++e) x.v[e] = from_f32<T>(0.f);
+    }
+    return x;
 }
 
 // Adds up[r] * M[row + r][a] * u[a][c] over a < end (a multiple of four) for ROWS rows; M's rows and u lie in shared
@@ -83,23 +95,23 @@ __device__ __forceinline__ void add_rows(float (&acc)[ROWS], float sign, const f
     }
 }
 
-// u and o from x and y (all threads).  Forward substitution over blocks of eight nodes: the products with the u of
+// u and o from r and y (all threads).  Forward substitution over blocks of eight nodes: the products with the u of
 // earlier blocks are shared out, D threads by 128 / D groups of rows, then a thread per column solves the block's own
 // triangle.  o follows from all of u at once.  Returns false if a u is not finite (to every thread).
-template <typename Tin, int D, bool Masked>
-__device__ __forceinline__ bool substitute(float *sm, const StepLayout<D> &L, const TreeShared &ts, const Tin *v,
-                                           size_t row_stride, int M) {
+template <int D, bool Masked>
+__device__ __forceinline__ bool substitute(float *sm, const StepLayout<D> &L, const TreeShared &ts, int M) {
     constexpr int RG = kStepThreads / D, ROWS = 8 / RG;
     const float *sA = sm + L.A, *sP = sm + L.P;
     const int c = threadIdx.x % D, first = threadIdx.x / D * ROWS;
-    float *s_x = sm + L.ki + c, *s_y = sm + L.gb + c, *s_u = sm + L.ke + c, *s_o = sm + L.qe + c;
+    const float *s_r = sm + L.ki + c, *s_y = sm + L.gb + c;
+    float *s_u = sm + L.ke + c, *s_o = sm + L.qe + c;
     bool finite = true;
     for (int i0 = 0; i0 < M; i0 += 8) {
         float w[ROWS];
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
             const int i = i0 + first + r;
-            w[r] = i < M ? sm[L.beta + i] * (to_f32(v[(size_t)i * row_stride + c]) - s_x[i * D]) : 0.f;
+            w[r] = i < M ? s_r[i * D] : 0.f;
         }
         add_rows<D, ROWS, Masked>(w, -1.f, sA, L.ap_stride, s_u, i0, ts.anc, i0 + first, M);
 #pragma unroll
@@ -139,7 +151,7 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
                  int max_nodes, int num_slots, const float *__restrict__ S_pool, Tin *__restrict__ o,
                  float *__restrict__ u, int32_t *__restrict__ status, int qk_norm, float qk_eps,
                  const Tin *__restrict__ gate, const float *__restrict__ weight, float out_eps) {
-    constexpr int CG = D / 4, NG = kStepThreads / CG, TN = D == 128 ? 4 : 2;  // products: column groups, node groups
+    constexpr int CG = D / 4, NG = kStepThreads / CG, kTile = D == 128 ? 4 : 2;  // products: column groups, node groups
     constexpr int CPL = D < 32 ? 1 : D / 32, LANES = D / CPL;                 // rows: channels per lane
     constexpr int kPitch = StepLayout<D>::kPitch;
     extern __shared__ __align__(16) float sm[];
@@ -167,6 +179,20 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
         S = sm + L.S;
     }
     tc::cp_async_commit();
+    // a thread's rows of k and q for the first 16 nodes
+    constexpr int kPer = 16 / kStepWarps;
+    const int c0 = lane * CPL;
+    Some<Tin, CPL> kr[kPer], qr[kPer];
+    auto fetch = [&](int first) {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const int i = first + warp + e * kStepWarps;
+            const size_t at = base + (size_t)i * row_stride + c0;
+            kr[e] = load_some<CPL>(k + at, i < M && lane < LANES);
+            qr[e] = load_some<CPL>(q + at, i < M && lane < LANES);
+        }
+    };
+    fetch(0);
     for (int i = tid; i < M; i += kStepThreads) sm[L.beta + i] = beta[(size_t)(t.row0 + i) * H + h];
     tc::cp_async_wait<1>();
     if (!read_tree(ts, t, links, true)) {  // a block barrier
@@ -178,11 +204,10 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
     // K~, Q~, K^, a warp per node.  b sums g over the path, 16 nodes at a time, from the b of the nearest ancestor
     // in an earlier group.
     float range = 0.f;
-    const int c0 = lane * CPL;
     for (int first = 0; first < M; first += 16) {
-        float b[16 / kStepWarps][CPL];
+        float b[kPer][CPL];
 #pragma unroll
-        for (int e = 0; e < 16 / kStepWarps; ++e) {
+        for (int e = 0; e < kPer; ++e) {
             const int i = first + warp + e * kStepWarps;
 #pragma unroll
             for (int x = 0; x < CPL; ++x) b[e][x] = 0.f;
@@ -204,15 +229,14 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
         }
         __syncthreads();  // every sum of this group is formed
 #pragma unroll
-        for (int e = 0; e < 16 / kStepWarps; ++e) {
+        for (int e = 0; e < kPer; ++e) {
             const int i = first + warp + e * kStepWarps;
             if (i >= M) break;
             float kf[CPL], qf[CPL];
 #pragma unroll
-            for (int x = 0; x < CPL; ++x) kf[x] = qf[x] = 0.f;
-            if (lane < LANES) {
-                load_some<CPL>(k + base + (size_t)i * row_stride + c0, kf);
-                load_some<CPL>(q + base + (size_t)i * row_stride + c0, qf);
+            for (int x = 0; x < CPL; ++x) {
+                kf[x] = to_f32(kr[e].v[x]);
+                qf[x] = to_f32(qr[e].v[x]);
             }
             float sk = 1.f, sq = 1.f;
             if (qk_norm) {
@@ -246,7 +270,10 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
                 }
             }
         }
-        if (first + 16 < M) __syncthreads();
+        if (first + 16 < M) {
+            fetch(first + 16);
+            __syncthreads();
+        }
     }
     tc::cp_async_wait_all();
     const bool pairwise = __syncthreads_or(!(range <= kMaxRange));
@@ -286,71 +313,107 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
     }
     __syncthreads();  // K^ and b are no longer needed
 
-    // x and y
+    // r and y, TN nodes by four columns a thread; v is asked for before the sums
     const int cg = tid % CG, ng = tid / CG;
-    for (int i0 = ng * TN; i0 < M; i0 += NG * TN) {
-        float x[TN][4], y[TN][4];
+    auto products = [&](auto tile) {
+        constexpr int TN = decltype(tile)::value;
+        for (int i0 = ng * TN; i0 < M; i0 += NG * TN) {
+            Some<Tin, 4> vr[TN];
 #pragma unroll
-        for (int r = 0; r < TN; ++r)
+            for (int r = 0; r < TN; ++r) vr[r] = load_some<4>(v + base + (size_t)(i0 + r) * row_stride + cg * 4, i0 + r < M);
+            float x[TN][4], y[TN][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[r][e] = y[r][e] = 0.f;
-        const float *ke[TN], *qe[TN];
+            for (int r = 0; r < TN; ++r)
 #pragma unroll
-        for (int r = 0; r < TN; ++r) {
-            ke[r] = sm + L.ke + min(i0 + r, M - 1) * kPitch;
-            qe[r] = sm + L.qe + min(i0 + r, M - 1) * kPitch;
-        }
-#pragma unroll 2
-        for (int c = 0; c < D; c += 4) {
-            float4 s[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[j] = *reinterpret_cast<const float4 *>(S + (size_t)(c + j) * D + cg * 4);
+                for (int e = 0; e < 4; ++e) x[r][e] = y[r][e] = 0.f;
+            const float *ke[TN], *qe[TN];
 #pragma unroll
             for (int r = 0; r < TN; ++r) {
-                const float4 kk = *reinterpret_cast<const float4 *>(ke[r] + c), qq = *reinterpret_cast<const float4 *>(qe[r] + c);
-                const float kv[4] = {kk.x, kk.y, kk.z, kk.w}, qv[4] = {qq.x, qq.y, qq.z, qq.w};
+                ke[r] = sm + L.ke + min(i0 + r, M - 1) * kPitch;
+                qe[r] = sm + L.qe + min(i0 + r, M - 1) * kPitch;
+            }
+#pragma unroll 2
+            for (int c = 0; c < D; c += 4) {
+                float4 s[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[r][0] = fmaf(kv[j], s[j].x, x[r][0]); x[r][1] = fmaf(kv[j], s[j].y, x[r][1]);
-                    x[r][2] = fmaf(kv[j], s[j].z, x[r][2]); x[r][3] = fmaf(kv[j], s[j].w, x[r][3]);
-                    y[r][0] = fmaf(qv[j], s[j].x, y[r][0]); y[r][1] = fmaf(qv[j], s[j].y, y[r][1]);
-                    y[r][2] = fmaf(qv[j], s[j].z, y[r][2]); y[r][3] = fmaf(qv[j], s[j].w, y[r][3]);
+                for (int j = 0; j < 4; ++j) s[j] = *reinterpret_cast<const float4 *>(S + (size_t)(c + j) * D + cg * 4);
+#pragma unroll
+                for (int r = 0; r < TN; ++r) {
+                    const float4 kk = *reinterpret_cast<const float4 *>(ke[r] + c), qq = *reinterpret_cast<const float4 *>(qe[r] + c);
+                    const float kv[4] = {kk.x, kk.y, kk.z, kk.w}, qv[4] = {qq.x, qq.y, qq.z, qq.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        x[r][0] = fmaf(kv[j], s[j].x, x[r][0]); x[r][1] = fmaf(kv[j], s[j].y, x[r][1]);
+                        x[r][2] = fmaf(kv[j], s[j].z, x[r][2]); x[r][3] = fmaf(kv[j], s[j].w, x[r][3]);
+                        y[r][0] = fmaf(qv[j], s[j].x, y[r][0]); y[r][1] = fmaf(qv[j], s[j].y, y[r][1]);
+                        y[r][2] = fmaf(qv[j], s[j].z, y[r][2]); y[r][3] = fmaf(qv[j], s[j].w, y[r][3]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < TN; ++r) {
+                if (i0 + r < M) {
+                    const float w = sm[L.beta + i0 + r];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[r][e] = w * (to_f32(vr[r].v[e]) - x[r][e]);
+                    *reinterpret_cast<float4 *>(sm + L.ki + (i0 + r) * D + cg * 4) = make_float4(x[r][0], x[r][1], x[r][2], x[r][3]);
+                    *reinterpret_cast<float4 *>(sm + L.gb + (i0 + r) * D + cg * 4) = make_float4(y[r][0], y[r][1], y[r][2], y[r][3]);
                 }
             }
         }
+    };
+    // few nodes: every thread group gets some (256 requests x 32 heads of d = 128, fp32, 3-6 nodes: 284 us for 328)
+    if (M <= NG * kTile / 2) products(std::integral_constant<int, kTile / 2>{});
+    else products(std::integral_constant<int, kTile>{});
+    // the gate's rows for the first 16 nodes and its weight, asked for ahead
+    Some<Tin, CPL> zr[kPer];
+    float wt[CPL];
+    auto fetch_gate = [&](int first) {
 #pragma unroll
-        for (int r = 0; r < TN; ++r) {
-            if (i0 + r < M) {
-                *reinterpret_cast<float4 *>(sm + L.ki + (i0 + r) * D + cg * 4) = make_float4(x[r][0], x[r][1], x[r][2], x[r][3]);
-                *reinterpret_cast<float4 *>(sm + L.gb + (i0 + r) * D + cg * 4) = make_float4(y[r][0], y[r][1], y[r][2], y[r][3]);
-            }
+        for (int e = 0; e < kPer; ++e) {
+            const int i = first + warp + e * kStepWarps;
+            zr[e] = load_some<CPL>(gate + base + (size_t)i * row_stride + c0, gate && i < M && lane < LANES);
         }
-    }
+    };
+    fetch_gate(0);
+#pragma unroll
+    for (int a = 0; a < CPL; ++a) wt[a] = gate && weight && lane < LANES ? weight[c0 + a] : 1.f;
     __syncthreads();  // K~ and Q~ are no longer needed: u and o take their place
-    if (!substitute<Tin, D, false>(sm, L, ts, v + base, row_stride, M)) substitute<Tin, D, true>(sm, L, ts, v + base, row_stride, M);
-    for (int i = warp; i < M; i += kStepWarps) {  // a warp per row
-        const size_t at = base + (size_t)i * row_stride + c0;
-        float x[CPL];
-        float inv = 1.f;
-        if (gate) {
-            float ss = 0.f;
-            if (lane < LANES)
+    if (!substitute<D, false>(sm, L, ts, M)) substitute<D, true>(sm, L, ts, M);
+    for (int first = 0; first < M; first += 16) {  // a warp per row
+        float x[kPer][CPL], inv[kPer];
+        if (first > 0) fetch_gate(first);
 #pragma unroll
-                for (int e = 0; e < CPL; ++e) ss = fmaf(sm[L.qe + i * D + c0 + e], sm[L.qe + i * D + c0 + e], ss);
+        for (int e = 0; e < kPer; ++e) {
+            const int i = first + warp + e * kStepWarps;
+            inv[e] = 0.f;
 #pragma unroll
-            for (int off = 16; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-            inv = rsqrtf(ss / (float)D + out_eps);
-        }
-        if (lane < LANES) {
-            float z[CPL];
-            if (gate) load_some<CPL>(gate + at, z);
-#pragma unroll
-            for (int e = 0; e < CPL; ++e) {
-                x[e] = sm[L.qe + i * D + c0 + e];
-                if (gate) x[e] *= inv * (weight ? weight[c0 + e] : 1.f) * sigmoidf(z[e]);
-                o[at + e] = from_f32<Tin>(x[e]);
-                if (u) u[at + e] = sm[L.ke + i * D + c0 + e];
+            for (int a = 0; a < CPL; ++a) {
+                x[e][a] = i < M && lane < LANES ? sm[L.qe + i * D + c0 + a] : 0.f;
+                inv[e] = fmaf(x[e][a], x[e][a], inv[e]);
             }
+        }
+        if (gate) {
+#pragma unroll
+            for (int off = 16; off; off >>= 1)
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) inv[e] += __shfl_xor_sync(0xffffffffu, inv[e], off);
+        }
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const int i = first + warp + e * kStepWarps;
+            if (i >= M || lane >= LANES) continue;
+            const size_t at = base + (size_t)i * row_stride + c0;
+            const float scale = rsqrtf(inv[e] / (float)D + out_eps);
+            Some<Tin, CPL> out;
+            Some<float, CPL> ui;
+#pragma unroll
+            for (int a = 0; a < CPL; ++a) {
+                out.v[a] = from_f32<Tin>(gate ? x[e][a] * scale * wt[a] * sigmoidf(to_f32(zr[e].v[a])) : x[e][a]);
+                ui.v[a] = sm[L.ke + i * D + c0 + a];
+            }
+            *reinterpret_cast<Some<Tin, CPL> *>(o + at) = out;
+            if (u) *reinterpret_cast<Some<float, CPL> *>(u + at) = ui;
         }
     }
 }
