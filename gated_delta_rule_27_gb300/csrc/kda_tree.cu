@@ -23,15 +23,14 @@ namespace {
 // ---------------------------------------------------------------------------
 // Step, fp32 on the CUDA cores: any supported d and type
 // ---------------------------------------------------------------------------
-// One CTA of 128 threads per (request, head).  With K~ = k e^b, Q~ = q e^b, K^ = k e^{-b} in shared memory, A and P
+// One CTA of NT threads per (request, head).  With K~ = k e^b, Q~ = q e^b, K^ = k e^{-b} in shared memory, A and P
 // are one dot product per (node, ancestor) and thread; the products with the state go in register tiles of TN nodes
 // by four columns, which read a vector of shared memory for every eight multiply-adds or more; the substitution has
 // a thread per column, eight nodes at a time.  Where the decays along a path sum to more than kMaxRange, so that
 // e^{-b} would overflow, A and P take the path's own exponents instead.
 // Bound by the multiply-adds with the state, 4 d^2 for each node, and their operands' way from shared memory; with few
-// requests by the latency of its dependent steps (17 requests of up to 13 nodes, 5 heads of d = 64, fp32: 8.7 us, of
+// requests by the latency of its dependent steps (17 requests of up to 13 nodes, 5 heads of d = 64, fp32: 6.8 us, of
 // which the states' way from HBM is 0.2).
-constexpr int kStepThreads = 128, kStepWarps = kStepThreads / 32;
 constexpr float kMaxRange = 80.f;
 
 template <int D>
@@ -96,11 +95,11 @@ __device__ __forceinline__ void add_rows(float (&acc)[ROWS], float sign, const f
 }
 
 // u and o from r and y (all threads).  Forward substitution over blocks of eight nodes: the products with the u of
-// earlier blocks are shared out, D threads by 128 / D groups of rows, then a thread per column solves the block's own
+// earlier blocks are shared out, D threads by NT / D groups of rows, then a thread per column solves the block's own
 // triangle.  o follows from all of u at once.  Returns false if a u is not finite (to every thread).
-template <int D, bool Masked>
+template <int D, int NT, bool Masked>
 __device__ __forceinline__ bool substitute(float *sm, const StepLayout<D> &L, const TreeShared &ts, int M) {
-    constexpr int RG = kStepThreads / D, ROWS = 8 / RG;
+    constexpr int RG = NT / D, ROWS = 8 / RG;
     const float *sA = sm + L.A, *sP = sm + L.P;
     const int c = threadIdx.x % D, first = threadIdx.x / D * ROWS;
     const float *s_r = sm + L.ki + c, *s_y = sm + L.gb + c;
@@ -143,15 +142,15 @@ __device__ __forceinline__ bool substitute(float *sm, const StepLayout<D> &L, co
     return __syncthreads_and(finite);
 }
 
-template <typename Tin, int D>
-__global__ void __launch_bounds__(kStepThreads)
+template <typename Tin, int D, int NT>
+__global__ void __launch_bounds__(NT)
 tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin *__restrict__ v,
                  const float *__restrict__ g, const float *__restrict__ beta, const int32_t *__restrict__ parent,
                  const int32_t *__restrict__ cu, const int32_t *__restrict__ seq_idx, int H, int total_nodes,
                  int max_nodes, int num_slots, const float *__restrict__ S_pool, Tin *__restrict__ o,
                  float *__restrict__ u, int32_t *__restrict__ status, int qk_norm, float qk_eps,
                  const Tin *__restrict__ gate, const float *__restrict__ weight, float out_eps) {
-    constexpr int CG = D / 4, NG = kStepThreads / CG, kTile = D == 128 ? 4 : 2;  // products: column groups, node groups
+    constexpr int kWarps = NT / 32, CG = D / 4, NG = NT / CG, kTile = D == 128 ? 4 : 2;  // products: column groups, node groups
     constexpr int CPL = D < 32 ? 1 : D / 32, LANES = D / CPL;                 // rows: channels per lane
     constexpr int kPitch = StepLayout<D>::kPitch;
     extern __shared__ __align__(16) float sm[];
@@ -171,29 +170,29 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
     const int M = t.nodes;
     const size_t row_stride = (size_t)H * D, base = ((size_t)t.row0 * H + h) * D;
     const float *S = S_pool + ((size_t)slot * H + h) * D * D;
-    for (int i = tid; i < M * CG; i += kStepThreads)
+    for (int i = tid; i < M * CG; i += NT)
         tc::cp_async16(sm + L.gb + i * 4, g + base + (size_t)(i / CG) * row_stride + i % CG * 4);
     tc::cp_async_commit();
     if (L.keeps_state()) {
-        for (int i = tid; i < D * CG; i += kStepThreads) tc::cp_async16(sm + L.S + i * 4, S + i * 4);
+        for (int i = tid; i < D * CG; i += NT) tc::cp_async16(sm + L.S + i * 4, S + i * 4);
         S = sm + L.S;
     }
     tc::cp_async_commit();
     // a thread's rows of k and q for the first 16 nodes
-    constexpr int kPer = 16 / kStepWarps;
+    constexpr int kPer = 16 / kWarps;
     const int c0 = lane * CPL;
     Some<Tin, CPL> kr[kPer], qr[kPer];
     auto fetch = [&](int first) {
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
-            const int i = first + warp + e * kStepWarps;
+            const int i = first + warp + e * kWarps;
             const size_t at = base + (size_t)i * row_stride + c0;
             kr[e] = load_some<CPL>(k + at, i < M && lane < LANES);
             qr[e] = load_some<CPL>(q + at, i < M && lane < LANES);
         }
     };
     fetch(0);
-    for (int i = tid; i < M; i += kStepThreads) sm[L.beta + i] = beta[(size_t)(t.row0 + i) * H + h];
+    for (int i = tid; i < M; i += NT) sm[L.beta + i] = beta[(size_t)(t.row0 + i) * H + h];
     tc::cp_async_wait<1>();
     if (!read_tree(ts, t, links, true)) {  // a block barrier
         tc::cp_async_wait_all();
@@ -208,7 +207,7 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
         float b[kPer][CPL];
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
-            const int i = first + warp + e * kStepWarps;
+            const int i = first + warp + e * kWarps;
 #pragma unroll
             for (int x = 0; x < CPL; ++x) b[e][x] = 0.f;
             if (i < M && lane < LANES) {
@@ -230,7 +229,7 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
         __syncthreads();  // every sum of this group is formed
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
-            const int i = first + warp + e * kStepWarps;
+            const int i = first + warp + e * kWarps;
             if (i >= M) break;
             float kf[CPL], qf[CPL];
 #pragma unroll
@@ -280,7 +279,7 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
 
     // A and P: a thread per (node, ancestor), with zeros up to a multiple of eight
     const int M8 = (M + 7) & ~7;
-    for (int p = tid; p < M8 * M8; p += kStepThreads) {
+    for (int p = tid; p < M8 * M8; p += NT) {
         const int i = p / M8, a = p % M8;
         float sa = 0.f, sp = 0.f;
         if (i < M && ((ts.anc[i] >> a) & 1)) {
@@ -371,7 +370,7 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
     auto fetch_gate = [&](int first) {
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
-            const int i = first + warp + e * kStepWarps;
+            const int i = first + warp + e * kWarps;
             zr[e] = load_some<CPL>(gate + base + (size_t)i * row_stride + c0, gate && i < M && lane < LANES);
         }
     };
@@ -379,13 +378,13 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
 #pragma unroll
     for (int a = 0; a < CPL; ++a) wt[a] = gate && weight && lane < LANES ? weight[c0 + a] : 1.f;
     __syncthreads();  // K~ and Q~ are no longer needed: u and o take their place
-    if (!substitute<D, false>(sm, L, ts, M)) substitute<D, true>(sm, L, ts, M);
+    if (!substitute<D, NT, false>(sm, L, ts, M)) substitute<D, NT, true>(sm, L, ts, M);
     for (int first = 0; first < M; first += 16) {  // a warp per row
         float x[kPer][CPL], inv[kPer];
         if (first > 0) fetch_gate(first);
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
-            const int i = first + warp + e * kStepWarps;
+            const int i = first + warp + e * kWarps;
             inv[e] = 0.f;
 #pragma unroll
             for (int a = 0; a < CPL; ++a) {
@@ -401,7 +400,7 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
         }
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
-            const int i = first + warp + e * kStepWarps;
+            const int i = first + warp + e * kWarps;
             if (i >= M || lane >= LANES) continue;
             const size_t at = base + (size_t)i * row_stride + c0;
             const float scale = rsqrtf(inv[e] / (float)D + out_eps);
@@ -418,15 +417,34 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
     }
 }
 
-template <typename Tin, int D>
-cudaError_t launch_step_d(const TreeStepArgs &a, cudaStream_t st) {
+template <typename Tin, int D, int NT>
+cudaError_t launch_step_n(const TreeStepArgs &a, cudaStream_t st) {
     const int smem = StepLayout<D>(a.max_nodes).bytes();
-    const cudaError_t e = allow_smem<tree_step_kernel<Tin, D>>(smem);
+    const cudaError_t e = allow_smem<tree_step_kernel<Tin, D, NT>>(smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(tree_step_kernel<Tin, D>, a.num_seqs * a.H, kStepThreads, smem, st, (const Tin *)a.q,
+    return launch_dependent(tree_step_kernel<Tin, D, NT>, a.num_seqs * a.H, NT, smem, st, (const Tin *)a.q,
                             (const Tin *)a.k, (const Tin *)a.v, a.g, a.beta, a.parent, a.cu, a.seq_idx, a.H,
                             a.total_nodes, a.max_nodes, a.num_slots, a.S_pool, (Tin *)a.o, a.u, a.status, a.fu.qk_norm,
                             a.fu.qk_eps, (const Tin *)a.fu.gate, a.fu.weight, a.fu.out_eps);
+}
+
+// 256 threads where shared memory leaves room for few CTAs on an SM (d = 128: 137 us with 128 and 123 with 256, 64
+// requests x 9-16 nodes x 32 heads, fp32; d = 64, bf16: 124 and 91, 16 requests x 33-64 nodes), or where there are few
+// CTAs (8, of 8 nodes: 6.5 and 5.6); else 128, whose barriers stop fewer warps (256 requests x 9-16 nodes, d = 64: 150 and
+// 169).
+template <typename Tin, int D>
+cudaError_t launch_step_d(const TreeStepArgs &a, cudaStream_t st) {
+    if constexpr (D == 128) {
+        return launch_step_n<Tin, D, 256>(a, st);
+    } else if constexpr (D == 64) {
+        int sms = 0;
+        const cudaError_t e = sm_count(&sms);
+        if (e != cudaSuccess) return e;
+        return a.max_nodes > 16 || a.num_seqs * a.H <= 2 * sms ? launch_step_n<Tin, D, 256>(a, st)
+                                                               : launch_step_n<Tin, D, 128>(a, st);
+    } else {
+        return launch_step_n<Tin, D, 128>(a, st);
+    }
 }
 
 template <typename Tin>
