@@ -17,7 +17,7 @@
 // u is formed to fp32 accuracy as there: every operand in two bf16 parts, hi hi + hi lo + lo hi in fp32.
 //
 // Measured (32 heads, 9 to 16 nodes): 64 requests 46 us, 256 requests 162 us where the bytes' way takes 114.  Issue slots
-// are 47% busy, the tensor pipe 31%, DRAM 57%: with four CTAs an SM the phases that load (the state) and those that only
+// are 48% busy, the tensor pipe 33%, DRAM 59%: with four CTAs an SM the phases that load (the state) and those that only
 // compute (the decays, A, P, T, the stores) overlap in part.
 #include "kda_tree_bf16.cuh"
 
