@@ -79,10 +79,19 @@ __device__ __forceinline__ void store_split8(uint8_t *img, int row, int col, int
     *reinterpret_cast<uint4 *>(img + at) = hi;
     *reinterpret_cast<uint4 *>(img + lo_rows * 128 + at) = lo;
 }
-__device__ __forceinline__ void ldg8(const float *p, float (&f)[8]) {
-    asm volatile("ld.global.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
-                 : "l"(p));
+// Eight floats of the state: one 32-byte load where the pool is aligned to that, else two of 16 bytes (all that a pool's
+// address promises).
+__device__ __forceinline__ void ldg8(const float *p, bool aligned32, float (&f)[8]) {
+    if (aligned32) {
+        asm volatile("ld.global.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+                     : "l"(p));
+    } else {
+        asm volatile("ld.global.L1::no_allocate.v4.f32 {%0,%1,%2,%3}, [%8];\n"
+                     "ld.global.L1::no_allocate.v4.f32 {%4,%5,%6,%7}, [%8 + 16];"
+                     : "=&f"(f[0]), "=&f"(f[1]), "=&f"(f[2]), "=&f"(f[3]), "=&f"(f[4]), "=&f"(f[5]), "=&f"(f[6]), "=&f"(f[7])
+                     : "l"(p));
+    }
 }
 // r of eight nodes for the thread's state column, from the accumulator's hi and lo columns
 template <int MP>
@@ -270,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
     uint4 kr[kUnits], qr[kUnits];
     float s[4][8];                   // state row (tid / 16) + 16 j of the half, columns 8 (tid % 16) on
     const float *S = p.S_pool + ((size_t)slot * p.H + h) * kD * kD + (size_t)(tid >> 4) * kD + (tid & 15) * 8;
+    const bool aligned32 = (reinterpret_cast<uintptr_t>(p.S_pool) & 31u) == 0;
     if (warp < 8) {
         for (int i = tid; i < M * 32; i += kWorkers)
             tc::cp_async16(sm + L::b + i * 16, p.g + base + (size_t)(i >> 5) * row_stride + (i & 31) * 4);
@@ -285,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
         for (int i = tid; i < M * 16; i += kWorkers)
             tc::cp_async16(sm + L::v + i * 16, p.v + base + (size_t)(i >> 4) * row_stride + (i & 15) * 8);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) ldg8(S + (size_t)(16 * j) * kD, s[j]);
+        for (int j = 0; j < 4; ++j) ldg8(S + (size_t)(16 * j) * kD, aligned32, s[j]);
         if (p.gate && warp == 0) {
             if (p.weight) tc::cp_async16(sm + L::w + lane * 16, p.weight + lane * 4);
             else *reinterpret_cast<float4 *>(sm + L::w + lane * 16) = make_float4(1.f, 1.f, 1.f, 1.f);
@@ -416,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
     if (warp < 8) {
         state_images();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) ldg8(S + (size_t)(64 + 16 * j) * kD, s[j]);
+        for (int j = 0; j < 4; ++j) ldg8(S + (size_t)(64 + 16 * j) * kD, aligned32, s[j]);
     }
     const bool pairwise = __syncthreads_or(!(range <= kMaxRange));
     float *sA = reinterpret_cast<float *>(sm + L::ap), *sP = sA + MP * L::ap_stride;

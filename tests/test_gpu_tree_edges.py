@@ -1,0 +1,38 @@
+"""The draft-tree operators where they can go wrong: addresses, masked logits, long decays, bounds of a batch.
+
+Tolerances (fixed before measuring), max|x - ref| / max|ref|: 1e-4 for fp32 values, 2e-2 for bf16 outputs, as for the
+operators' other tests, unless a test says and derives its own.
+"""
+import pytest
+import torch
+
+from gated_delta_rule_27_gb300 import libkda
+from tests.test_gpu_tree import BF, F32, i32, run_step, step_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+def shifted(t, floats=4):
+    """The same values, contiguous, 16 bytes behind a 256-byte boundary."""
+    room = torch.empty(t.numel() + floats, dtype=t.dtype, device="cuda")
+    view = room[floats:].view(t.shape)
+    view.copy_(t)
+    assert view.data_ptr() % 32 == 16 and view.is_contiguous()
+    return view
+
+
+@pytest.mark.parametrize("d,dtype", [(16, F32), (64, BF), (128, F32), (128, BF)])
+@pytest.mark.parametrize("M", [5, 12, 30, 60])
+def test_a_pool_at_any_16_byte_boundary(M, d, dtype):
+    """A pool's address need not be a multiple of 32 bytes: step and commit give the bits that they give on one that is."""
+    x = step_inputs([M, M // 2], 2, d, dtype, seed=M + d)
+    o, u, pool = run_step(x, M)
+    q, k, v, g, beta = (x[n].cuda() for n in ("q", "k", "v", "g", "beta"))
+    at16 = shifted(x["pool"])
+    o16, u16, status = torch.zeros_like(q), shifted(torch.zeros_like(u)), i32([0])
+    libkda.kda_tree_step(q, k, v, shifted(g), beta, i32(x["parent"]), i32(x["cu"]), i32(x["slots"]), at16, o16, u16, M, status=status)
+    assert int(status) == 0 and torch.equal(o16, o) and torch.equal(u16, u)
+    path, taken = i32([[0, 1, -1], [0, -1, -1]]), i32([2, 1])
+    for S in (pool, at16):
+        libkda.kda_tree_commit(k, g, u, i32(x["cu"]), path, taken, i32(x["slots"]), S, status=status)
+    assert int(status) == 0 and torch.equal(at16, pool)
