@@ -110,7 +110,7 @@ __device__ __forceinline__ Found best_of_warp(float top, int best) {
 // become NaN where a logit is NaN or +inf.
 __device__ __forceinline__ Found merged(Found f, int n, float scale) {
     Found a = best_of_warp(f.top, f.best);
-    a.sum = f.top > -INFINITY ? f.sum * exp2_of((f.top - a.top) * scale) : 0.f;
+    a.sum = f.top > -INFINITY ? f.sum * exp2_of((f.top - a.top) * scale) : f.sum;  // (there: zero or NaN)
     for (int off = n >> 1; off; off >>= 1) a.sum += __shfl_xor_sync(0xffffffffu, a.sum, off);
     return a;
 }
@@ -403,7 +403,16 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
             if (!r.onehot) {
                 if (f.top > -INFINITY) f.best = 0;  // only `onehot` uses the place
                 f.top = best_of_warp(f.top, 0).top;
-                if (trials && f.top > -INFINITY) {
+                if (trials && f.top == -INFINITY) {
+                    // nothing to add up, but a NaN among these logits has to show in the row's sum
+                    for (int v = part.v0 + tid; v < part.v1; v += kThreads) {
+                        float l[P::kVec];
+                        part.get(v, l);
+#pragma unroll
+                        for (int e = 0; e < P::kVec; ++e)
+                            if (l[e] != l[e]) f.sum = l[e];
+                    }
+                } else if (trials) {
                     float2 sum = make_float2(0.f, 0.f);
                     const Row warps{f.top, r.scale, 0, false, false};
 #pragma unroll 2

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from gated_delta_rule_27_gb300 import libkda
-from tests.test_gpu_tree import BF, F32, i32, run_step, step_inputs
+from tests.test_gpu_tree import BF, F32, check_verify, i32, run_step, step_inputs, verify_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +36,23 @@ def test_a_pool_at_any_16_byte_boundary(M, d, dtype):
     for S in (pool, at16):
         libkda.kda_tree_commit(k, g, u, i32(x["cu"]), path, taken, i32(x["slots"]), S, status=status)
     assert int(status) == 0 and torch.equal(at16, pool)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("probs", [True, False])
+@pytest.mark.parametrize("V", [1000, 5000, 50001])
+def test_verify_a_nan_among_masked_logits(V, probs, dtype):
+    """Rows that are -inf but for 64 tokens and a few NaN, far from those: a NaN weighs nothing, also where a child is
+    rejected and the rest of the row is summed and searched."""
+    x = verify_inputs([4, 8, 5, 7], V, dtype, V + probs, probs)
+    x["logits"][:, 64:] = -float("inf")
+    x["logits"][:, [300, 611, V - 1]] = float("nan")
+    x["tokens"] = [t % 64 for t in x["tokens"]]
+    if probs:  # a draft that is all too sure of one token
+        x["tokens"] = [5] * len(x["tokens"])
+        x["probs"][:] = 0.0
+        x["probs"][:, :64] = 0.1 / 63
+        x["probs"][:, 5] = 0.9
+    x["u"][:] = 0.9999  # most trials are lost
+    paths = check_verify(x, 8)
+    assert min(len(p) for p in paths) == 1
