@@ -6,10 +6,9 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include <atomic>
-
 #include "kda.h"
 #include "kda_check.cuh"
+#include "kda_smem.cuh"
 
 namespace kda {
 
@@ -194,23 +193,6 @@ cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, si
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
-}
-
-// Lets a kernel use `bytes` of dynamic shared memory on the current device; the runtime is asked only when that is
-// more than before.  (A device number past the table asks every time.)
-template <auto Kernel>
-cudaError_t allow_smem(int bytes) {
-    constexpr int kDevices = 64;
-    static std::atomic<int> allowed[kDevices];
-    int device = 0;
-    cudaError_t e = cudaGetDevice(&device);
-    if (e != cudaSuccess || (device < kDevices && allowed[device].load(std::memory_order_relaxed) >= bytes)) return e;
-    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && device < kDevices) {
-        int seen = allowed[device].load(std::memory_order_relaxed);
-        while (seen < bytes && !allowed[device].compare_exchange_weak(seen, bytes, std::memory_order_relaxed)) {}
-    }
-    return e;
 }
 
 // Multiprocessors of the current device.
