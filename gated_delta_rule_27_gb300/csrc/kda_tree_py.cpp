@@ -7,10 +7,12 @@
 // libkda.so serves both bindings.
 #include <Python.h>
 
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <initializer_list>
+#include <optional>
 #include <string>
 
 #include "kda.h"
@@ -102,11 +104,26 @@ void *stream_of(PyObject *stream, const at::Tensor &t) {
     return p;
 }
 
-// Runs a call's body; errors of any kind become Python's.
+// The device of a call's tensors: a launch goes to the current device, so they have to share one and it has to be made
+// current.  (Tensors on the host are refused where they are read.)
+std::optional<c10::Device> device_of(PyObject *const *a, Py_ssize_t n) {
+    std::optional<c10::Device> device;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        if (!THPVariable_Check(a[i])) continue;
+        const c10::Device here = THPVariable_Unpack(a[i]).device();
+        if (!here.is_cuda()) continue;
+        if (device && *device != here) fail(PyExc_ValueError, "libkda takes tensors of one device; got " + device->str() + " and " + here.str());
+        device = here;
+    }
+    return device;
+}
+
+// Runs a call's body on its tensors' device; errors of any kind become Python's.
 template <typename F>
-PyObject *guarded(Py_ssize_t got, Py_ssize_t want, F body) {
+PyObject *guarded(PyObject *const *a, Py_ssize_t got, Py_ssize_t want, F body) {
     try {
         if (got != want) fail(PyExc_TypeError, "wrong number of arguments");
+        const c10::cuda::OptionalCUDAGuard guard(device_of(a, got));
         return PyLong_FromLong(body());
     } catch (const Failed &) {
     } catch (const std::exception &e) {
@@ -118,7 +135,7 @@ PyObject *guarded(Py_ssize_t got, Py_ssize_t want, F body) {
 // q, k, v, g, beta, parent, cu_nodes, seq_idx, S_pool, o, u, max_nodes, status, stream, qk_l2norm, qk_eps, out_gate,
 // out_weight, out_eps
 PyObject *tree_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 19, [&] {
+    return guarded(a, n, 19, [&] {
         const at::Tensor &q = lead(a[0], 3, "q"), &cu = lead(a[6], 1, "cu_nodes"), &pool = lead(a[8], 4, "S_pool");
         const kda_dtype dt = dtype(q);
         const auto type = q.scalar_type();
@@ -136,7 +153,7 @@ PyObject *tree_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 // k, g, u, cu_nodes, path, path_len, seq_idx, S_pool, status, stream, qk_l2norm, qk_eps
 PyObject *tree_commit(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 12, [&] {
+    return guarded(a, n, 12, [&] {
         const at::Tensor &k = lead(a[0], 3, "k"), &cu = lead(a[3], 1, "cu_nodes"), &path = lead(a[4], 2, "path"), &pool = lead(a[7], 4, "S_pool");
         const kda_dtype dt = dtype(k);
         const int64_t T = k.size(0), H = k.size(1), d = k.size(2), N = cu.size(0) - 1, slots = pool.size(0), width = path.size(1);
@@ -152,7 +169,7 @@ PyObject *tree_commit(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 // x, w, parent, cu_nodes, seq_idx, conv_pool, y, max_nodes, status, stream
 PyObject *tree_conv(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 10, [&] {
+    return guarded(a, n, 10, [&] {
         const at::Tensor &x = lead(a[0], 2, "x"), &w = lead(a[1], 2, "w"), &cu = lead(a[3], 1, "cu_nodes"), &pool = lead(a[5], 3, "conv_pool");
         const kda_dtype dt = dtype(x);
         const int64_t T = x.size(0), C = x.size(1), W = w.size(1), N = cu.size(0) - 1, slots = pool.size(0);
@@ -166,7 +183,7 @@ PyObject *tree_conv(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 // x, cu_nodes, path, path_len, seq_idx, conv_pool, status, stream
 PyObject *tree_conv_commit(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 8, [&] {
+    return guarded(a, n, 8, [&] {
         const at::Tensor &x = lead(a[0], 2, "x"), &cu = lead(a[1], 1, "cu_nodes"), &path = lead(a[2], 2, "path"), &pool = lead(a[5], 3, "conv_pool");
         const kda_dtype dt = dtype(x);
         const int64_t T = x.size(0), C = x.size(1), N = cu.size(0) - 1, slots = pool.size(0), carried = pool.size(1), width = path.size(1);
@@ -181,7 +198,7 @@ PyObject *tree_conv_commit(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 // logits, tokens, parent, cu_nodes, u_accept, u_next, path, path_len, next_token, draft_probs, temperature, status, stream
 PyObject *draft_verify(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 13, [&] {
+    return guarded(a, n, 13, [&] {
         const at::Tensor &l = lead(a[0], 2, "logits"), &cu = lead(a[3], 1, "cu_nodes"), &path = lead(a[6], 2, "path");
         const kda_dtype dt = dtype(l);
         const int64_t T = l.size(0), V = l.size(1), N = cu.size(0) - 1, width = path.size(1);

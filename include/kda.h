@@ -287,9 +287,9 @@ KDA_API kda_status kda_short_conv_decode(const void *x, const float *w, int32_t 
  *               path or slot breaks these rules is skipped (nothing of it is
  *               written, but by kda_draft_verify an empty path) and sets
  *               *status to KDA_ERR_INVALID_ARG if it was 0.
- * A request may have no nodes.  All pointers are device pointers, contiguous,
- * 16-byte aligned unless said otherwise; index arrays, beta, u_accept, u_next
- * and temperature 4-byte aligned.
+ * A request may have no nodes.  All pointers are device pointers of the calling
+ * thread's current device, contiguous, 16-byte aligned unless said otherwise;
+ * index arrays, beta, u_accept, u_next and temperature 4-byte aligned.
  */
 #define KDA_TREE_MAX_NODES 64
 
