@@ -223,6 +223,8 @@ bool pipe_self_indexed(TcPlan plan, int num_seqs);
 void testing_set_plan(int plan);
 void testing_set_fault(int fault, long long wait_ns);
 int testing_fault();
+long long testing_wait_ns();
+constexpr int kFaultNoPublish = 1;   // test-only: state images, or a verification's exchanges, are not published
 constexpr int kFaultChunkTable = 2;  // test hook of the bounds-checking build (KDA_TESTING_FAULT_CHUNK_TABLE)
 
 cudaError_t launch_prefill_simt(const void *q, const void *k, const void *v, const float *g, const float *beta,

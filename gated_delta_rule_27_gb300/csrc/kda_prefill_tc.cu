@@ -54,7 +54,6 @@ namespace {
 constexpr int kD = 128, kL = 64, kTile = 32, kNTile = kD / kTile;
 constexpr float kMaxHalfRange = 80.f;  // |b_r - b_m| bound of the tensor-core A/P path
 constexpr uint64_t kFlagWaitNs = 2000000000ull;  // default bound of a wait on another CTA's publication flag
-constexpr int kFaultNoPublish = 1;  // test-only: the chain plan publishes no state image
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -2312,6 +2311,7 @@ void testing_set_fault(int fault, long long wait_ns) {
     g_test_wait_ns.store(wait_ns);
 }
 int testing_fault() { return g_test_fault.load(); }
+long long testing_wait_ns() { return g_test_wait_ns.load(); }
 
 bool pipe_self_indexed(TcPlan plan, int num_seqs) {
 #ifdef KDA_DEBUG_BOUNDS

@@ -39,6 +39,7 @@ constexpr uint32_t kMaxPart = 65536;  // bytes of a row that a CTA keeps; a long
 constexpr int kRuns = kMaxPart / 16 / 32;  // a run: the 32 vectors of 16 bytes that a warp takes at once
 constexpr float kFixed = 1099511627776.f;  // 2^40
 constexpr float kMargin = 1e-4f;
+constexpr uint64_t kWaitNs = 1000000000ull;  // for an exchange
 
 __device__ __forceinline__ unsigned long long fixed40(float x) { return __float2ull_rz(x * kFixed); }
 
@@ -142,14 +143,14 @@ struct Exchange {
     __device__ __forceinline__ void expect(Shared &sh, uint32_t bytes) const {
         if (threadIdx.x == 0) tc::mbar_arrive_expect_tx(&sh.bar[turn()], bytes * size);
     }
-    __device__ __forceinline__ void wait(Shared &sh) {
-        ok = __syncthreads_and(ok && tc::mbar_wait(&sh.bar[turn()], (count >> 1) & 1));
+    __device__ __forceinline__ void wait(Shared &sh, uint64_t wait_ns) {
+        ok = __syncthreads_and(ok && tc::mbar_wait(&sh.bar[turn()], (count >> 1) & 1, wait_ns));
         ++count;
     }
 };
 
 // Every thread gets the CTAs' sums in sums[] (shared memory) and their total; x is the warp's sum (in lane 0).
-__device__ __forceinline__ unsigned long long cluster_sum(Shared &sh, Exchange &ex, unsigned long long x,
+__device__ __forceinline__ unsigned long long cluster_sum(Shared &sh, Exchange &ex, uint64_t wait_ns, unsigned long long x,
                                                           unsigned long long *sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, turn = ex.turn();
     if (lane == 0) sh.warp_sum[warp] = x;
@@ -162,7 +163,7 @@ __device__ __forceinline__ unsigned long long cluster_sum(Shared &sh, Exchange &
         tc::st_async_b64(tc::map_to_cta(&sh.cta_sum[turn][ex.rank], threadIdx.x), total,
                          tc::map_to_cta(&sh.bar[turn], threadIdx.x));
     }
-    ex.wait(sh);
+    ex.wait(sh, wait_ns);
     unsigned long long total = 0;
     for (int r = 0; r < ex.size; ++r) total += sh.cta_sum[turn][r];
     if (threadIdx.x < ex.size) sums[threadIdx.x] = sh.cta_sum[turn][threadIdx.x];
@@ -170,7 +171,7 @@ __device__ __forceinline__ unsigned long long cluster_sum(Shared &sh, Exchange &
 }
 
 // f.top and f.best are the thread's, f.sum the thread's relative to its warp's maximum (which f.top has become).
-__device__ __forceinline__ Found cluster_max(Shared &sh, Exchange &ex, float scale, Found f) {
+__device__ __forceinline__ Found cluster_max(Shared &sh, Exchange &ex, uint64_t wait_ns, float scale, Found f) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, turn = ex.turn();
     float sum = f.sum;
 #pragma unroll
@@ -186,7 +187,7 @@ __device__ __forceinline__ Found cluster_max(Shared &sh, Exchange &ex, float sca
             tc::st_async_b32x4(tc::map_to_cta(&sh.cta_max[turn][ex.rank], lane), __float_as_uint(a.top), (uint32_t)a.best,
                                __float_as_uint(a.sum), 0u, tc::map_to_cta(&sh.bar[turn], lane));
     }
-    ex.wait(sh);
+    ex.wait(sh, wait_ns);
     return merged(sh.cta_max[turn][lane & (ex.size - 1)], ex.size, scale);
 }
 
@@ -287,6 +288,8 @@ struct Args {
     const float *temperature, *u, *u_next;
     int total_nodes, V, path_stride;
     uint32_t part_bytes;  // of dynamic shared memory: 0 where a part would not fit
+    uint64_t wait_ns;     // how long an exchange is waited for
+    bool silent;          // tests of the failure path: each request's last CTA leaves its exchanges unsent
     int32_t *path, *path_len, *next_token, *status;
 };
 
@@ -368,6 +371,10 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
         r.scale = r.onehot ? 0.f : 1.4426950408889634f / fmaxf(temp, 1e-30f);
         int node = 0;
         for (;;) {
+            if (p.silent && rank == size - 1) {
+                ex.ok = false;
+                break;
+            }
             if (tid == 0) sh.path[len] = node;  // (written out at the end: an exchange would wait for the store)
             ++len;
             if (node > 0) {
@@ -426,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
                     f.sum = sum.x + sum.y;
                 }
             }
-            f = cluster_max(sh, ex, r.scale, f);
+            f = cluster_max(sh, ex, p.wait_ns, r.scale, f);
             r.top = f.top;
             r.best = f.best;
             r.flat = f.top == INFINITY;
@@ -477,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
             unsigned long long Z = 1ull << 40;
             if (!r.onehot) {
                 if (q && trials) part.ask_q(q);
-                Z = cluster_sum(sh, ex, exact(false), sh.sum_w);
+                Z = cluster_sum(sh, ex, p.wait_ns, exact(false), sh.sum_w);
             }
             if (!ex.ok) break;
             unsigned long long s = Z, *sums = sh.sum_w;
@@ -516,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
                     if (r.onehot) {
                         s = fixed40(excess_of(1.f, C, q[r.best]));
                     } else {
-                        s = cluster_sum(sh, ex, exact(true), sh.sum_r);
+                        s = cluster_sum(sh, ex, p.wait_ns, exact(true), sh.sum_r);
                         sums = sh.sum_r;
                         if (!ex.ok) break;
                     }
@@ -660,14 +667,20 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const Args p)
     tc::grid_dep_launch();
     if (!ex.ok) {  // an exchange that never came: an empty path
         len = 0;
-        if (writer && p.status) atomicCAS(p.status, 0, (int32_t)KDA_ERR_TIMEOUT);
+        if (tid == 0 && p.status) atomicCAS(p.status, 0, (int32_t)KDA_ERR_TIMEOUT);
     }
     tc::cp_async_wait_all();  // (a root's row that was fetched for a tree that is not one)
     __syncthreads();
+    if (!ex.ok) {
+        // A CTA that was only late may still send to this one, whose shared memory has to be there: it stays until the
+        // others have left or come here too.  (Each of their waits has its limit.)
+        cluster.barrier_arrive();
+        cluster.barrier_wait();
+    }
     for (int i = tid; i < p.path_stride && rank == 0; i += kThreads)
         p.path[(size_t)n * p.path_stride + i] = i < len ? sh.path[i] : -1;
     if (writer) p.path_len[n] = len;
-    // (every CTA has all values of the last exchange: none writes to another's shared memory any more)
+    // (else every CTA has all values of the last exchange: none writes to another's shared memory any more)
 }
 
 template <typename Tin>
@@ -706,8 +719,10 @@ cudaError_t launch_t(Args p, int num_seqs, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_draft_verify(const DraftVerifyArgs &a, kda_dtype dt, cudaStream_t st) {
+    const long long wait_ns = testing_wait_ns();
     const Args p{a.logits, a.probs, a.tokens, a.parent, a.cu, a.temperature, a.u, a.u_next, a.total_nodes, a.V,
-                 a.path_stride, 0, a.path, a.path_len, a.next_token, a.status};
+                 a.path_stride, 0, wait_ns > 0 ? (uint64_t)wait_ns : kWaitNs, testing_fault() == kFaultNoPublish, a.path,
+                 a.path_len, a.next_token, a.status};
     return dt == KDA_BF16 ? launch_t<__nv_bfloat16>(p, a.num_seqs, st) : launch_t<float>(p, a.num_seqs, st);
 }
 

@@ -286,7 +286,9 @@ KDA_API kda_status kda_short_conv_decode(const void *x, const float *w, int32_t 
  *   status      optional device int32 (NULL to skip): a request whose tree,
  *               path or slot breaks these rules is skipped (nothing of it is
  *               written, but by kda_draft_verify an empty path) and sets
- *               *status to KDA_ERR_INVALID_ARG if it was 0.
+ *               *status to KDA_ERR_INVALID_ARG if it was 0.  KDA_ERR_TIMEOUT
+ *               there: a device-side wait ran out, and what a request's
+ *               outputs hold is not to be used.
  * A request may have no nodes.  All pointers are device pointers of the calling
  * thread's current device, contiguous, 16-byte aligned unless said otherwise;
  * index arrays, beta, u_accept, u_next and temperature 4-byte aligned.

@@ -5,11 +5,13 @@
  * the library's own tests can (a) run the tensor-core prefill under each of
  * its launch plans, which must give bit-identical results, and (b) drive a
  * bounded device-side wait to expiry and check that the failure is reported
- * as KDA_ERR_TIMEOUT by kda_prefill_check while the context stays usable.
+ * as KDA_ERR_TIMEOUT (by kda_prefill_check, or in kda_draft_verify's status)
+ * while the context stays usable.
  *
- * Both hooks set process-wide state that every later kda_prefill_chunked
- * call on any thread reads at launch time; a test must restore the defaults
- * (plan -1, fault KDA_TESTING_FAULT_NONE with wait limit 0) when it is done.
+ * Both hooks set process-wide state that every later kda_prefill_chunked (the
+ * fault: or kda_draft_verify) call on any thread reads at launch time; a test
+ * must restore the defaults (plan -1, fault KDA_TESTING_FAULT_NONE with wait
+ * limit 0) when it is done.
  */
 #ifndef KDA_TESTING_H_
 #define KDA_TESTING_H_
@@ -36,7 +38,9 @@ KDA_API kda_status kda_testing_set_plan(int32_t plan);
 /* Faults for tests of the failure path. */
 #define KDA_TESTING_FAULT_NONE 0        /* the default */
 #define KDA_TESTING_FAULT_NO_PUBLISH 1  /* chain and pipe plans: the state chains publish none of their state
-                                           images, so the output units' bounded waits on them run out */
+                                           images, so the output units' bounded waits on them run out;
+                                           draft verification: the last CTA of each request that has several
+                                           sends nothing to the others, whose waits for it run out */
 #define KDA_TESTING_FAULT_CHUNK_TABLE 2 /* bounds-checking build (libkda_debug.so) only: the chunk table claims
                                            1000 chunks more than exist, which the kernels' bounds checks must
                                            catch (KDA_ERR_BOUNDS); the release build ignores this fault */
@@ -44,7 +48,7 @@ KDA_API kda_status kda_testing_set_plan(int32_t plan);
 /*
  * Injects `fault` into later calls and bounds the device-side waits on
  * another CTA's publication flag by `wait_limit_ns` nanoseconds (0 keeps the
- * default of two seconds).  KDA_ERR_INVALID_ARG for an unknown fault or a
+ * default of two seconds, in the draft verification one).  KDA_ERR_INVALID_ARG for an unknown fault or a
  * negative limit.
  */
 KDA_API kda_status kda_testing_set_fault(int32_t fault, int64_t wait_limit_ns);
