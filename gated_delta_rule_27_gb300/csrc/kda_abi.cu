@@ -357,8 +357,9 @@ kda_status kda_tree_commit(const void *k, const float *g, const float *u, const 
 static kda_status tree_conv_check(int32_t num_seqs, int32_t total_nodes, int32_t num_slots, int32_t C, int32_t W) {
     if (C <= 0) return KDA_ERR_INVALID_ARG;
     if (W < 1 || W > KDA_SHORT_CONV_MAX_W) return KDA_ERR_UNSUPPORTED;
-    // the grid's second dimension is the request
-    if (num_seqs > 65535 || (int64_t)C * W > INT_MAX) return KDA_ERR_UNSUPPORTED;
+    // the grid's second dimension is the request; the last block's channel numbers, past C by less than a block's 512,
+    // have to fit an int
+    if (num_seqs > 65535 || (int64_t)C * W > INT_MAX || C > INT_MAX - 512) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 

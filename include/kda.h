@@ -336,7 +336,9 @@ KDA_API kda_status kda_tree_commit(const void *k, const float *g, const float *u
  * slot's carried inputs.
  *
  *   x, y       [total_nodes, C] in_dtype; y must not alias x; element-aligned
- *   w          [C, W] fp32, 1 <= W <= KDA_SHORT_CONV_MAX_W
+ *   w          [C, W] fp32, 1 <= W <= KDA_SHORT_CONV_MAX_W; C * W and C + 512
+ *              at most INT32_MAX
+ *   num_seqs   at most 65535
  *   conv_pool  [num_slots, W - 1, C] fp32, oldest first, read only (NULL if W = 1)
  * kda_tree_conv_commit replaces a slot's carried inputs by the last W - 1 of
  * [its carried inputs, the inputs x along the accepted path].
