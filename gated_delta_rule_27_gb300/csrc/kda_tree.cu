@@ -795,7 +795,13 @@ tree_conv_commit_kernel(const Tin *__restrict__ x, const int32_t *__restrict__ c
             bad = node[j] < 0 || node[j] >= t.nodes;
         }
     }
-    if (bad) {
+    // the nodes before those count too: a path is refused here where the state's commit refuses it
+    static_assert(kConvThreads >= kMaxNodes, "a thread per node of the path");
+    if (!bad && (int)threadIdx.x < len) {
+        const int at = path[(size_t)n * path_stride + threadIdx.x];
+        bad = at < 0 || at >= t.nodes;
+    }
+    if (__syncthreads_or(bad)) {
         if (threadIdx.x == 0) report_invalid(status);
         return;
     }

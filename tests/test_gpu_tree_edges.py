@@ -56,3 +56,23 @@ def test_verify_a_nan_among_masked_logits(V, probs, dtype):
     x["u"][:] = 0.9999  # most trials are lost
     paths = check_verify(x, 8)
     assert min(len(p) for p in paths) == 1
+
+
+@pytest.mark.parametrize("W", [2, 4])
+@pytest.mark.parametrize("C", [130, 2048])
+def test_both_commits_refuse_the_same_paths(C, W):
+    """A path with a node outside its tree moves neither the state nor the carried inputs, wherever in the path it is."""
+    M, N = 9, 4
+    path = torch.arange(M, dtype=torch.int32).repeat(N, 1)
+    path[1, 0], path[2, 3], path[3, M - 1] = -1, M, -1
+    cu, taken, slots = i32([M * n for n in range(N + 1)]), i32([M] * N), i32(list(range(N)))
+    g = torch.Generator(device="cuda").manual_seed(C + W)
+    conv = torch.randn((N, W - 1, C), generator=g, device="cuda")
+    S = torch.randn((N, 1, 64, 64), generator=g, device="cuda")
+    x, k = (torch.randn(s, generator=g, device="cuda") for s in ((N * M, C), (N * M, 1, 64)))
+    status, before = [i32([0]), i32([0])], (conv.clone(), S.clone())
+    libkda.kda_tree_conv_commit(x, cu, path.cuda(), taken, slots, conv, status=status[0])
+    libkda.kda_tree_commit(k, -k.abs(), k, cu, path.cuda(), taken, slots, S, status=status[1])
+    assert [int(s) for s in status] == [libkda.KDA_ERR_INVALID_ARG] * 2
+    assert torch.equal(conv[0], x[M - (W - 1):M]) and torch.equal(conv[1:], before[0][1:])
+    assert not torch.equal(S[0], before[1][0]) and torch.equal(S[1:], before[1][1:])
