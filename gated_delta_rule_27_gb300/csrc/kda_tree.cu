@@ -73,6 +73,13 @@ __device__ __forceinline__ Some<T, N> load_some(const T *p, bool in) {
     return x;
 }
 
+template <int N, typename T>
+__device__ __forceinline__ void load_floats(const T *p, bool in, float (&f)[N]) {
+    const Some<T, N> x = load_some<N>(p, in);
+#pragma unroll
+    for (int e = 0; e < N; ++e) f[e] = to_f32(x.v[e]);
+}
+
 // Adds up[r] * M[row + r][a] * u[a][c] over a < end (a multiple of four) for ROWS rows; M's rows and u lie in shared
 // memory.  Masked: entries off the path are skipped instead of multiplied by zero, which a non-finite u of another
 // branch would turn into NaN.
@@ -282,33 +289,42 @@ tree_step_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const Tin
     for (int p = tid; p < M8 * M8; p += NT) {
         const int i = p / M8, a = p % M8;
         float sa = 0.f, sp = 0.f;
-        if (i < M && ((ts.anc[i] >> a) & 1)) {
-            if (!pairwise) {
-                const float *x = sm + L.ke + i * kPitch, *y = sm + L.qe + i * kPitch, *z = sm + L.ki + a * kPitch;
+        if (!pairwise && i < M && ((ts.anc[i] >> a) & 1)) {
+            const float *x = sm + L.ke + i * kPitch, *y = sm + L.qe + i * kPitch, *z = sm + L.ki + a * kPitch;
 #pragma unroll 4
-                for (int c = 0; c < D; c += 4) {
-                    const float4 x4 = *reinterpret_cast<const float4 *>(x + c), y4 = *reinterpret_cast<const float4 *>(y + c),
-                                 z4 = *reinterpret_cast<const float4 *>(z + c);
-                    sa = fmaf(x4.x, z4.x, sa); sa = fmaf(x4.y, z4.y, sa); sa = fmaf(x4.z, z4.z, sa); sa = fmaf(x4.w, z4.w, sa);
-                    sp = fmaf(y4.x, z4.x, sp); sp = fmaf(y4.y, z4.y, sp); sp = fmaf(y4.z, z4.z, sp); sp = fmaf(y4.w, z4.w, sp);
-                }
-            } else {
-                const Tin *ka = k + base + (size_t)a * row_stride, *ki = k + base + (size_t)i * row_stride,
-                          *qi = q + base + (size_t)i * row_stride;
-                for (int c = 0; c < D; ++c) {
-                    const float kd = to_f32(ka[c]) * expf(sm[L.gb + i * D + c] - sm[L.gb + a * D + c]);
-                    sa = fmaf(to_f32(ki[c]), kd, sa);
-                    sp = fmaf(to_f32(qi[c]), kd, sp);
-                }
-                if (qk_norm) {
-                    sa *= sm[L.scale + i] * sm[L.scale + a];
-                    sp *= sm[L.scale + L.R + i] * sm[L.scale + a];
-                }
+            for (int c = 0; c < D; c += 4) {
+                const float4 x4 = *reinterpret_cast<const float4 *>(x + c), y4 = *reinterpret_cast<const float4 *>(y + c),
+                             z4 = *reinterpret_cast<const float4 *>(z + c);
+                sa = fmaf(x4.x, z4.x, sa); sa = fmaf(x4.y, z4.y, sa); sa = fmaf(x4.z, z4.z, sa); sa = fmaf(x4.w, z4.w, sa);
+                sp = fmaf(y4.x, z4.x, sp); sp = fmaf(y4.y, z4.y, sp); sp = fmaf(y4.z, z4.z, sp); sp = fmaf(y4.w, z4.w, sp);
             }
             sa = a == i ? 0.f : sa * sm[L.beta + i];
         }
         sm[L.A + i * L.ap_stride + a] = sa;
         sm[L.P + i * L.ap_stride + a] = sp;
+    }
+    if (pairwise) {  // a warp per node
+        __syncthreads();  // the zeros lie
+        for (int i = warp; i < M; i += kWarps) {
+            const size_t own = base + (size_t)i * row_stride + c0;
+            float ki[CPL], qi[CPL];
+            load_floats(k + own, lane < LANES, ki);
+            load_floats(q + own, lane < LANES, qi);
+            pairs_of_node<4>(ts, i, ki, qi,
+                             [&](int a, float (&ka)[CPL], float (&ga)[CPL]) {
+                                 const size_t at = base + (size_t)a * row_stride + c0;
+                                 load_floats(k + at, lane < LANES, ka);
+                                 load_floats(g + at, lane < LANES, ga);
+   #pragma unroll
+                                 for (int e = 0; e < CPL; ++e) ga[e] = log_decay(ga[e]);
+                             },
+                             [](float x) { return expf(x); },
+                             [&](int a, float x, bool is_p) {
+                                 if (qk_norm) x *= sm[L.scale + (is_p ? L.R : 0) + i] * sm[L.scale + a];
+                                 if (!is_p) x = a == i ? 0.f : x * sm[L.beta + i];
+                                 sm[(is_p ? L.P : L.A) + i * L.ap_stride + a] = x;
+                             });
+        }
     }
     __syncthreads();  // K^ and b are no longer needed
 

@@ -105,6 +105,65 @@ __device__ __forceinline__ bool read_tree(TreeShared &ts, const Tree &t, const L
 // finite for a decay of -inf.
 __device__ __forceinline__ float log_decay(float g) { return g < -110.f ? -110.f : g; }
 
+// Row i of A (without beta) and of P by one warp, from the exponents of the path itself: going up from node i the decays
+// between the two nodes are summed anew, so that the sum is no larger than what it says, however much the path as a whole
+// decays (differences of sums from the root are off by 2^-24 of those sums: 1.4e-4 in o below 32 tokens of -200).  Some
+// ancestors at a time, whose rows come with one wait and whose sums over the lanes share their exchanges (nine for four).
+//   rows(a, k, g)  the lane's channels of a node's key (before its norm) and log-decay
+//   factor(b)      the exponential of a log-decay
+//   put(a, x, is_p)  takes the entry of ancestor a (node i itself among them), called by one lane for each
+template <int Some, int C, typename Rows, typename Factor, typename Put>
+__device__ __forceinline__ void pairs_of_node(const TreeShared &ts, int i, const float (&ki)[C], const float (&qi)[C], Rows rows,
+                                              Factor factor, Put put) {
+    static_assert(Some == 2 || Some == 4, "one of these many ancestors at a time");
+    const int lane = threadIdx.x & 31;
+    float b[C];
+#pragma unroll
+    for (int x = 0; x < C; ++x) b[x] = 0.f;
+    for (int top = i; top >= 0;) {
+        int at[Some];
+        float k[Some][C], g[Some][C], v[2 * Some];
+#pragma unroll
+        for (int j = 0; j < Some; ++j) {
+            at[j] = top;
+#pragma unroll
+            for (int x = 0; x < C; ++x) k[j][x] = g[j][x] = 0.f;
+            if (top >= 0) {
+                rows(top, k[j], g[j]);
+                top = ts.parent[top];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < Some; ++j) {
+            v[j] = v[Some + j] = 0.f;
+#pragma unroll
+            for (int x = 0; x < C; ++x) {
+                const float e = k[j][x] * factor(b[x]);
+                v[j] = fmaf(ki[x], e, v[j]);
+                v[Some + j] = fmaf(qi[x], e, v[Some + j]);
+                b[x] += g[j][x];
+            }
+        }
+        // each exchange halves what a lane still sums: of 2 Some groups of lanes, group j ends up with v[j]
+        constexpr int kLanes = 32 / (2 * Some);
+#pragma unroll
+        for (int half = Some; half; half >>= 1) {
+            const bool upper = lane & (half * kLanes);
+#pragma unroll
+            for (int j = 0; j < half; ++j) {
+                const float mine = upper ? v[j + half] : v[j], other = upper ? v[j] : v[j + half];
+                v[j] = mine + __shfl_xor_sync(0xffffffffu, other, half * kLanes);
+            }
+        }
+#pragma unroll
+        for (int off = kLanes / 2; off; off >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+        const int j = lane / kLanes & (Some - 1);
+        int a = j & 1 ? at[1] : at[0];
+        if constexpr (Some == 4) a = j & 2 ? (j & 1 ? at[3] : at[2]) : a;
+        if (lane % kLanes == 0 && a >= 0) put(a, v[0], lane >= 16);
+    }
+}
+
 __device__ __forceinline__ void report_invalid(int32_t *status) {
     if (status) atomicCAS(status, 0, (int32_t)KDA_ERR_INVALID_ARG);
 }

@@ -76,7 +76,6 @@ __device__ __forceinline__ float4 four(uint2 x) {  // of bf16
 // Place of the 16-byte vector u of a row of g or b: a thread's two vectors (eight channels) lie half a row apart, so
 // that 16 threads read a row without bank conflicts.
 __device__ __forceinline__ int spread(int u) { return (u & 1) * 16 + (u >> 1); }
-__device__ __forceinline__ int spread_channel(int c) { return spread(c >> 2) * 4 + (c & 3); }
 __device__ __forceinline__ void read_row8(const float *row, int ch, float (&f)[8]) {
     const float4 a = reinterpret_cast<const float4 *>(row)[ch], b = reinterpret_cast<const float4 *>(row)[16 + ch];
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
@@ -278,39 +277,33 @@ __global__ void __launch_bounds__(kThreads, MP == 8 ? 6 : 4) tree_step_mma_kerne
 
     float *sA = reinterpret_cast<float *>(sm + L::ap), *sP = sA + MP * L::ap_stride;
     if (pairwise) {
-        // A warp per (node, ancestor), four channels a lane.  The results' own place holds b, so they pass through
-        // the place of K^, which is not used.
-        float *xA = reinterpret_cast<float *>(sm + L::inv), *xP = xA + MP * MP;
+        // A warp per node, four neighbouring channels a lane.  The results' own place holds g, so they pass through the
+        // place of K^, which is not used.
+        float *xA = reinterpret_cast<float *>(sm + L::inv);
         static_assert(2 * MP * MP * 4 <= NT * 8 * L::frag_bytes, "A and P pass through the place of K^");
-        for (int i = 1; i < M; ++i) s_b[i * kD + tid] += s_b[ts.parent[i] * kD + tid];
+        for (int x = tid; x < 2 * MP * MP; x += kThreads) xA[x] = 0.f;
         __syncthreads();
-        for (int x = warp; x < MP * MP; x += kWarps) {
-            const int i = x / MP, a = x % MP;
-            float va = 0.f, vp = 0.f;
-            if (i < M && ((ts.anc[i] >> a) & 1)) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int c = lane + 32 * e;
-                    const float ka = __bfloat162float(p.k[base + (size_t)a * row_stride + c]) * exp2_of(s_b[i * kD + spread_channel(c)] - s_b[a * kD + spread_channel(c)]);
-                    va = fmaf(__bfloat162float(p.k[base + (size_t)i * row_stride + c]), ka, va);
-                    vp = fmaf(__bfloat162float(p.q[base + (size_t)i * row_stride + c]), ka, vp);
-                }
-#pragma unroll
-                for (int off = 16; off; off >>= 1) {
-                    va += __shfl_xor_sync(0xffffffffu, va, off);
-                    vp += __shfl_xor_sync(0xffffffffu, vp, off);
-                }
-                if (p.qk_norm) {
-                    va *= s_scale[i] * s_scale[a];
-                    vp *= s_scale[MP + i] * s_scale[a];
-                }
-                va = a == i ? 0.f : s_beta[i] * va;
-            }
-            if (lane == 0) {
-                xA[x] = va;
-                xP[x] = vp;
-                if (fmaf(va, 0.f, vp * 0.f) != 0.f) s_wild = 1;
-            }
+        for (int i = warp; i < M; i += kWarps) {
+            auto row4 = [&](const __nv_bfloat16 *x, int a, float (&f)[4]) {
+                const float4 y = four(__ldg(reinterpret_cast<const uint2 *>(x + base + (size_t)a * row_stride) + lane));
+                f[0] = y.x; f[1] = y.y; f[2] = y.z; f[3] = y.w;
+            };
+            float ki[4], qi[4];
+            row4(p.k, i, ki);
+            row4(p.q, i, qi);
+            pairs_of_node<4>(ts, i, ki, qi,
+                             [&](int a, float (&ka)[4], float (&ga)[4]) {
+                                 row4(p.k, a, ka);
+                                 const float4 y = reinterpret_cast<const float4 *>(s_b + a * kD)[spread(lane)];
+                                 ga[0] = y.x; ga[1] = y.y; ga[2] = y.z; ga[3] = y.w;
+                             },
+                             [](float x) { return exp2_of(x); },
+                             [&](int a, float x, bool is_p) {
+                                 if (p.qk_norm) x *= s_scale[is_p ? MP + i : i] * s_scale[a];
+                                 if (!is_p) x = a == i ? 0.f : s_beta[i] * x;
+                                 xA[(is_p ? MP * MP : 0) + i * MP + a] = x;
+                                 if (x * 0.f != 0.f) s_wild = 1;
+                             });
         }
         __syncthreads();
         for (int x = tid; x < 2 * MP * MP; x += kThreads) sA[x / MP * L::ap_stride + x % MP] = xA[x];

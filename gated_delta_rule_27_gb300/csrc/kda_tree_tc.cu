@@ -431,41 +431,34 @@ __global__ void __launch_bounds__(kThreads, MP == 64 ? 1 : 2) tree_step_tc_kerne
     const bool pairwise = __syncthreads_or(!(range <= kMaxRange));
     float *sA = reinterpret_cast<float *>(sm + L::ap), *sP = sA + MP * L::ap_stride;
     if (pairwise) {
-        // A warp per (node, ancestor), four channels a lane.  The results' own place holds b, so they pass through
-        // the place of K^, which is not used.
-        float *xA = reinterpret_cast<float *>(sm + L::ki), *xP = xA + MP * MP;
-        static_assert(2 * MP * MP * 4 <= 2 * L::ki_panel, "A and P pass through the place of K^");
-        if (warp < 8)
-            for (int x = warp; x < MP * MP; x += 8) {
-                const int i = x / MP, a = x % MP;
-                float va = 0.f, vp = 0.f;
-                if (i < M && ((ts.anc[i] >> a) & 1)) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int c = lane + 32 * e;
-                        const float ka = __bfloat162float(p.k[base + (size_t)a * row_stride + c]) *
-                                         exp2_of(s_b[i * kD + c] - s_b[a * kD + c]);
-                        va = fmaf(__bfloat162float(p.k[base + (size_t)i * row_stride + c]), ka, va);
-                        vp = fmaf(__bfloat162float(p.q[base + (size_t)i * row_stride + c]), ka, vp);
-                    }
-#pragma unroll
-                    for (int off = 16; off; off >>= 1) {
-                        va += __shfl_xor_sync(0xffffffffu, va, off);
-                        vp += __shfl_xor_sync(0xffffffffu, vp, off);
-                    }
-                    if (p.qk_norm) {
-                        va *= s_scale[i] * s_scale[a];
-                        vp *= s_scale[MP + i] * s_scale[a];
-                    }
-                    va = a == i ? 0.f : s_beta[i] * va;
-                }
-                if (lane == 0) {
-                    xA[x] = va;
-                    xP[x] = vp;
-                }
+        // A warp per node, four neighbouring channels a lane; the results take b's place.  (MP = 32: four ancestors at a
+        // time would spill registers of the ordinary case: 92.9 us for 89.4 where 64 requests have 20 to 32 nodes.)
+        if (warp < 8) {
+            for (int x = tid; x < 2 * MP * L::ap_stride; x += kWorkers) sA[x] = 0.f;
+            tc::named_barrier(1, kWorkers);
+            for (int i = warp; i < M; i += 8) {
+                auto row4 = [&](const __nv_bfloat16 *x, int a, float (&f)[4]) {
+                    const uint2 y = __ldg(reinterpret_cast<const uint2 *>(x + base + (size_t)a * row_stride) + lane);
+                    f[0] = __uint_as_float(y.x << 16); f[1] = __uint_as_float(y.x & 0xffff0000u);
+                    f[2] = __uint_as_float(y.y << 16); f[3] = __uint_as_float(y.y & 0xffff0000u);
+                };
+                float ki[4], qi[4];
+                row4(p.k, i, ki);
+                row4(p.q, i, qi);
+                pairs_of_node<MP == 64 ? 4 : 2>(ts, i, ki, qi,
+                                                [&](int a, float (&ka)[4], float (&ga)[4]) {
+                                                    row4(p.k, a, ka);
+                                                    const float4 y = log2_decay4(__ldg(reinterpret_cast<const float4 *>(p.g + base + (size_t)a * row_stride) + lane));
+                                                    ga[0] = y.x; ga[1] = y.y; ga[2] = y.z; ga[3] = y.w;
+                                                },
+                                                [](float x) { return exp2_of(x); },
+                                                [&](int a, float x, bool is_p) {
+                                                    if (p.qk_norm) x *= s_scale[is_p ? MP + i : i] * s_scale[a];
+                                                    if (!is_p) x = a == i ? 0.f : s_beta[i] * x;
+                                                    (is_p ? sP : sA)[i * L::ap_stride + a] = x;
+                                                });
             }
-        __syncthreads();
-        for (int x = tid; x < 2 * MP * MP; x += kThreads) sA[x / MP * L::ap_stride + x % MP] = xA[x];
+        }
         __syncthreads();
     }
 

@@ -7,6 +7,8 @@ import pytest
 import torch
 
 from gated_delta_rule_27_gb300 import libkda
+from oracle import tree
+from tests.gpu_helpers import f64, rel
 from tests.test_gpu_tree import BF, F32, check_verify, i32, run_step, step_inputs, verify_inputs
 
 pytestmark = pytest.mark.gpu
@@ -76,3 +78,23 @@ def test_both_commits_refuse_the_same_paths(C, W):
     assert [int(s) for s in status] == [libkda.KDA_ERR_INVALID_ARG] * 2
     assert torch.equal(conv[0], x[M - (W - 1):M]) and torch.equal(conv[1:], before[0][1:])
     assert not torch.equal(S[0], before[1][0]) and torch.equal(S[1:], before[1][1:])
+
+
+@pytest.mark.parametrize("d,dtype", [(16, F32), (64, F32), (64, BF), (128, F32), (128, BF)])
+@pytest.mark.parametrize("back", [1, 3])
+@pytest.mark.parametrize("M", [16, 31, 64])
+def test_a_steep_start_costs_no_accuracy_below_it(M, back, d, dtype):
+    """Half of the channels are cleared by every node of the upper half, and the lower half forgets little: what it adds up
+    has small exponents, however far the sums from the root have fallen.
+
+    Tolerance 2e-5.  An exponent whose factor counts (above e^-20) is a sum of up to 64 decays with an error of at most
+    64 x 2^-25 of 20, so a factor is off by 4e-5 at e^-20 and 2e-6 at e^-1; the products of two bf16 parts leave 3 x 2^-18 a
+    term, 1.1e-5 where all have one sign.
+    """
+    x = step_inputs([M], 2, d, dtype, seed=M + d, back=back)
+    x["g"][: M // 2, :, : d // 2] = -200.0
+    x["g"][M // 2:] *= 0.01
+    o, u, _ = run_step(x, M)
+    o_ref, u_ref, _ = tree.tree_step(*(f64(x[n]) for n in ("q", "k", "v", "g", "beta")), x["parent"], x["cu"], x["slots"], f64(x["pool"]))
+    assert rel(u, u_ref) <= 2e-5
+    assert rel(o, o_ref) <= (2e-5 if dtype == F32 else 2e-2)
