@@ -8,8 +8,10 @@
 namespace kda {
 namespace tree16 {
 
-// Largest |b| (powers of two) for which A and P are formed from the factors e^b and e^{-b}.
-constexpr float kMaxRange = 115.f;
+// Largest |b| (powers of two) for which A and P are formed from the factors e^b and e^{-b}.  The second bf16 part of q e^b
+// ends 17 bits below the value and bf16 at 2^-133, so a query keeps all its bits down to 2^-20 at the range's end (with
+// 2^-115 one of 1e-5 kept four: o off by 8%).
+constexpr float kMaxRange = 96.f;
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);

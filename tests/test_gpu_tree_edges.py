@@ -98,3 +98,21 @@ def test_a_steep_start_costs_no_accuracy_below_it(M, back, d, dtype):
     o_ref, u_ref, _ = tree.tree_step(*(f64(x[n]) for n in ("q", "k", "v", "g", "beta")), x["parent"], x["cu"], x["slots"], f64(x["pool"]))
     assert rel(u, u_ref) <= 2e-5
     assert rel(o, o_ref) <= (2e-5 if dtype == F32 else 2e-2)
+
+
+@pytest.mark.parametrize("scale", [1.0, 1e-2, 1e-4])
+@pytest.mark.parametrize("nats", [50.0, 78.0, 90.0])
+@pytest.mark.parametrize("M", [8, 16, 24, 40])
+def test_small_queries_below_a_long_decay(M, nats, scale):
+    """The output is linear in q: far down a path, too, where the factors e^b are small, a small q loses no bits.
+
+    Tolerance 2^-8 of a row's largest entry: the output's own rounding is half of that, what the parts of q leave out a
+    hundredth.
+    """
+    x = step_inputs([M], 2, 128, BF, seed=M, back=1)
+    x["q"] = (scale * x["q"].float()).to(BF)
+    x["g"][:] = -nats / M
+    o, _, _ = run_step(x, M)
+    o_ref, _, _ = tree.tree_step(*(f64(x[n]) for n in ("q", "k", "v", "g", "beta")), x["parent"], x["cu"], x["slots"], f64(x["pool"]))
+    off = abs(f64(o) - o_ref).max(-1) / abs(o_ref).max(-1)
+    assert off.max() <= 2.0 ** -8
