@@ -25,6 +25,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "lib", "libkda.so")
 TREE_PY_SRC = os.path.join(CSRC, "kda_tree_py.cpp")
 TREE_PY = os.path.join(PKG, "lib", "_kda_tree.so")
+TREE_PY_FOR = os.path.join(PKG, "lib", "_kda_tree.txt")  # the torch and the Python that it was built for
 # the bounds-checking variant (every checked index is tested before its access; see csrc/kda_check.cuh)
 DEBUG_BUILD_DIR = os.path.join(PKG, "_build_debug")
 DEBUG_LIB = os.path.join(PKG, "lib", "libkda_debug.so")
@@ -91,12 +92,25 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
     return lib
 
 
+def _text(path: str):
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
+
+
 def build_tree_py() -> str:
-    """Builds _kda_tree.so, the Python marshalling of the draft-tree calls, against the installed torch."""
-    newer = [TREE_PY_SRC, os.path.join(INCLUDE, "kda.h"), os.path.abspath(__file__)]
-    if os.path.exists(TREE_PY) and all(os.path.getmtime(p) <= os.path.getmtime(TREE_PY) for p in newer):
-        return TREE_PY
+    """Builds _kda_tree.so, the Python marshalling of the draft-tree calls, against the installed torch.
+
+    It links torch's C++ ABI, so the torch and the Python that it was built for are kept beside it, and others than
+    those make it stale as a newer source does.
+    """
     torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        built_for = "%s\n%s\n%s" % (torch_dir, sys.version, f.read())
+    newer = [TREE_PY_SRC, os.path.join(INCLUDE, "kda.h"), os.path.abspath(__file__)]
+    if os.path.exists(TREE_PY) and all(os.path.getmtime(p) <= os.path.getmtime(TREE_PY) for p in newer) and _text(TREE_PY_FOR) == built_for:
+        return TREE_PY
     lib, inc = os.path.join(torch_dir, "lib"), os.path.join(torch_dir, "include")
     cuda_inc = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     includes = [INCLUDE, inc, os.path.join(inc, "torch", "csrc", "api", "include"), sysconfig.get_path("include"), cuda_inc]
@@ -108,6 +122,9 @@ def build_tree_py() -> str:
     if r.returncode != 0:
         raise RuntimeError("g++ failed on %s:\n%s%s" % (TREE_PY_SRC, r.stdout, r.stderr))
     os.replace(tmp, TREE_PY)
+    with open(TREE_PY_FOR + ".tmp%d" % os.getpid(), "w") as f:
+        f.write(built_for)
+    os.replace(f.name, TREE_PY_FOR)
     return TREE_PY
 
 
