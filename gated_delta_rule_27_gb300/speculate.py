@@ -131,6 +131,9 @@ def generate(model: Model, last, slots, pools: Pools, rounds: int, shape=(-1, 0,
                                 status=bufs.status)
         tree_commit(trees, path, path_len, pools, H, d, bufs)
         kept, lengths, drawn = path.tolist(), path_len.tolist(), next_token.tolist()
+        for n, token in enumerate(drawn):
+            if token < 0:  # and a round on top of it would embed row -1
+                raise ValueError("request %d: no token to go on with; its last node has no logit above -inf" % n)
         for n, row in enumerate(tokens.tolist()):
             new[n] += [row[i] for i in kept[n][1:lengths[n]]] + [drawn[n]]
     if int(bufs.status):
