@@ -118,7 +118,7 @@ def generate(model: Model, last, slots, pools: Pools, rounds: int, shape=(-1, 0,
     i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=device)
     trees = Trees(i32(list(shape) * N), i32([n * M for n in range(N + 1)]), slots, M)
     bufs = TreeBuffers(N * M, H, d, device)
-    path, path_len, next_token = i32([[0] * M] * N), i32([0] * N), last.clone()
+    path, path_len, next_token = i32([[0] * M] * N).view(N, M), i32([0] * N), last.clone()
     heat = torch.full((N,), float(temperature), device=device)
     new = [[] for _ in range(N)]
     for _ in range(rounds):
@@ -127,7 +127,7 @@ def generate(model: Model, last, slots, pools: Pools, rounds: int, shape=(-1, 0,
         y = tree_forward(model.embed[flat.long()], trees, pools, model.weights, H, d, bufs)
         libkda.kda_draft_verify(model.target_logits(flat, y), flat, trees.parent, trees.cu_nodes,
                                 torch.rand(N * M, generator=gen, device=device), torch.rand(N, generator=gen, device=device),
-                                path, path_len, next_token, draft_probs=probs.view(N * M, -1), temperature=heat,
+                                path, path_len, next_token, draft_probs=probs.flatten(0, 1), temperature=heat,
                                 status=bufs.status)
         tree_commit(trees, path, path_len, pools, H, d, bufs)
         kept, lengths, drawn = path.tolist(), path_len.tolist(), next_token.tolist()
@@ -138,7 +138,7 @@ def generate(model: Model, last, slots, pools: Pools, rounds: int, shape=(-1, 0,
             new[n] += [row[i] for i in kept[n][1:lengths[n]]] + [drawn[n]]
     if int(bufs.status):
         raise libkda.KdaError(int(bufs.status), "a speculative round")
-    return new, sum(map(len, new)) / (N * rounds)
+    return new, sum(map(len, new)) / max(1, N * rounds)
 
 
 if __name__ == "__main__":
