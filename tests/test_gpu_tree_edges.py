@@ -116,3 +116,32 @@ def test_small_queries_below_a_long_decay(M, nats, scale):
     o_ref, _, _ = tree.tree_step(*(f64(x[n]) for n in ("q", "k", "v", "g", "beta")), x["parent"], x["cu"], x["slots"], f64(x["pool"]))
     off = abs(f64(o) - o_ref).max(-1) / abs(o_ref).max(-1)
     assert off.max() <= 2.0 ** -8
+
+
+def alone(x, n):
+    """Request n of a batch by itself."""
+    rows = slice(x["cu"][n], x["cu"][n + 1])
+    return dict(x, cu=[0, rows.stop - rows.start], slots=[x["slots"][n]], parent=x["parent"][rows], **{t: x[t][rows] for t in ("q", "k", "v", "g", "beta")})
+
+
+@pytest.mark.parametrize("d,dtype,bound,others", [(128, BF, 8, (5, 6)), (128, BF, 16, (9, 12)), (128, BF, 32, (17, 25)), (128, BF, 64, (33, 50)),
+                                                  (128, F32, 64, (12, 16, 33)), (64, F32, 64, (12, 16, 33)), (64, BF, 64, (12, 16, 33)), (16, F32, 64, (12, 16, 33))])
+def test_bits_do_not_depend_on_the_batch(bound, others, d, dtype):
+    """A request gives the bits of o and u alone that it gives among others, and under every bound of its kernel."""
+    lengths = [others[0], others[0] - 3, 2]
+    x = step_inputs(lengths, 3, d, dtype, seed=bound + d)
+    o, u, _ = run_step(x, bound)
+    for n in range(3):
+        rows = slice(x["cu"][n], x["cu"][n + 1])
+        for M in others + (bound,):
+            got = run_step(alone(x, n), M)
+            assert torch.equal(got[0], o[rows]) and torch.equal(got[1], u[rows])
+
+
+@pytest.mark.parametrize("low,high", [(8, 9), (16, 17), (32, 33), (8, 64)])
+def test_bounds_of_two_kernels_agree(low, high):
+    """bf16 at d = 128: the bound picks the kernel.  Each one's products of two bf16 parts are off by at most 3 x 2^-18 a
+    term, so two differ by at most twice that in u (2.3e-5 of the largest), and by one rounding (2^-8) more in o."""
+    x = step_inputs([low, low - 5, 1], 2, 128, BF, seed=low)
+    (o, u, _), (o2, u2, _) = run_step(x, low), run_step(x, high)
+    assert rel(u2, f64(u)) <= 2.3e-5 and rel(o2, f64(o)) <= 2.0 ** -8 + 2.3e-5
