@@ -101,8 +101,7 @@ __device__ __forceinline__ bool read_tree(TreeShared &ts, const Tree &t, const L
     return !ts.bad;
 }
 
-// A log-decay, cut where its exponential is zero in fp32, so that sums along a path and their differences stay
-// finite for a decay of -inf.
+// A log-decay, cut where its exponential is zero in fp32, so that sums along a path stay finite for a decay of -inf.
 __device__ __forceinline__ float log_decay(float g) { return g < -110.f ? -110.f : g; }
 
 // Row i of A (without beta) and of P by one warp, from the exponents of the path itself: going up from node i the decays

@@ -2,8 +2,8 @@
 //
 // A speculative round makes one call of these per layer and operator, on tensors of a few rows.  Marshalled through
 // ctypes, a call cost more time on the host than its kernel takes on the GPU: 11.5 us for a step, 9 for a commit,
-// 7.5 for a convolution, 10 for a verification, of which a launch is 3.  The same checks on the tensors' own fields
-// leave 3.6, 2.8, 2.5 and 3.0 us.  The entry points are called through the addresses that init() is given, so one
+// 7.5 for a convolution, 10 for a verification, of which a launch is 3.  The same checks on the tensors' own fields, and
+// that they share a device, leave 4.0, 3.3, 2.7 and 3.3 us.  The entry points are called through the addresses that init() is given, so one
 // libkda.so serves both bindings.
 #include <Python.h>
 

@@ -9,12 +9,15 @@
 //     D3 = r^T [T - I ; P T]^T   u = r + D3,  o = y + D3     (MP = 64: u first, then o = y + u^T P^T as D4)
 // so the state is read once, whatever the tree's size.  The floor is that read, 64 KB per (request, head).
 //
-// u moves the fp32 state, so it is formed to fp32 accuracy: every operand is split into two bf16 parts, hi + lo,
-// and each product takes hi hi + hi lo + lo hi with fp32 accumulators (2^-17 relative to a term; one part alone
-// would leave 2^-9); T comes from fp32 substitutions in blocks of 16 nodes and products of the blocks in the same
-// two parts.  A, P and T are done while the state arrives.  A factor
-// e^{-b} would overflow where the decays along a path sum to more than kMaxRange; such a request takes its A and P
-// pairwise from the path's own exponents instead.
+// u moves the fp32 state, so one bf16 part (2^-9 of a term) is not enough for it: every operand is split into two, hi +
+// lo, 16 bits of the 24, and each product takes hi hi + hi lo + lo hi with fp32 accumulators.  That leaves 3 x 2^-18 of a
+// term at most; u is off by 2.4e-7 of its size where fp32 products leave 0.6e-7 (2-norm; states of 0.1.  States of 1 and a
+// twentieth of the decay: 3e-6 and 1.5e-7).  A third part
+// would close that gap, but its images (32 to 48 KB at MP = 64) do not fit a CTA's shared memory, nor two such CTAs at
+// MP = 32.  T comes from fp32 substitutions in blocks of 16 nodes and products of the blocks in the same
+// two parts.  A, P and T are done while the state arrives.  Where the decays along a path sum to more than kMaxRange, the
+// factors e^b and e^{-b} would leave their range; such a request takes its A and P node by node from the path's own
+// exponents instead (16 requests of 33 to 64 nodes: 124 us for 61).
 //
 // D3 and D4 multiply entries off the paths by zero.  Where an operand is not finite that would carry a NaN from
 // one branch into another, so such a request or column takes a substitution that skips them (solve_masked).
@@ -80,7 +83,7 @@ __device__ __forceinline__ void store_split8(uint8_t *img, int row, int col, int
     *reinterpret_cast<uint4 *>(img + lo_rows * 128 + at) = lo;
 }
 // Eight floats of the state: one 32-byte load where the pool is aligned to that, else two of 16 bytes (all that a pool's
-// address promises).
+// address promises; 61.1 and 63.9 us for 16 requests of 33 to 64 nodes, 88.7 and 99.0 for 64 of 20 to 32).
 __device__ __forceinline__ void ldg8(const float *p, bool aligned32, float (&f)[8]) {
     if (aligned32) {
         asm volatile("ld.global.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"

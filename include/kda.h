@@ -310,8 +310,9 @@ KDA_API kda_status kda_short_conv_decode(const void *x, const float *w, int32_t 
  * Accuracy.  With fp32 inputs, and with bf16 ones at d_k < 128, all arithmetic
  * is fp32.  With bf16 inputs at d_k = 128 every operand of a product, the
  * state among them, is taken as two bf16 parts (16 bits of the 24) with fp32
- * sums: u is then off by 2 to 6e-7 of its size (2-norm) where fp32 leaves
- * 0.5 to 1.5e-7, and more where u is much smaller than v and S^T k.
+ * sums: u is then off by 2 to 3e-7 of its size (2-norm) where S^T k is small
+ * beside v, and by up to 4e-6 where it is as large or larger; fp32 leaves 0.5
+ * to 2e-7.  o is rounded to bf16 and no worse for it.
  * A request's bits do not depend on the other requests.  With bf16 inputs at
  * d_k = 128 they depend on max_nodes, which picks the kernel (up to 8, 16, 32
  * and 64 nodes): results under two bounds agree as stated above.
