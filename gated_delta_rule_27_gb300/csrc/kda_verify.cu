@@ -23,7 +23,7 @@
 // worst, and the cuts to 2^-40 take 4e-6; at 131072 logits it is below 5e-6 in all.)  Meanwhile the first child's row is
 // on its way to L2.
 // Measured: one request, a chain of 5 drafted from given distributions, 32768 fp32 logits a row: 9 to 15 us with the walk's length; 64 requests with
-// trees of 9 to 16 nodes over 131072 bf16 logits 45 to 53 us; 256 chains of 4 to 8 without distributions over 100003 56 to 60 us.
+// trees of 9 to 16 nodes over 131072 bf16 logits 45 to 55 us; 256 chains of 4 to 8 without distributions over 100003 56 to 60 us.
 // The others wait for the longest walk of the batch, several rejections among its trials at about 5 us each: DRAM is
 // 17% busy.
 #include <cooperative_groups.h>
