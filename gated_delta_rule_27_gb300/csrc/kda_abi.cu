@@ -6,6 +6,7 @@
 #include <initializer_list>
 
 #include "kda_internal.cuh"
+#include "kda_linear.cuh"
 #include "kda_testing.h"
 
 namespace {
@@ -419,6 +420,103 @@ kda_status kda_draft_verify(const void *logits, const float *draft_probs, const 
                                  num_seqs, total_nodes, V, path_stride, path, path_len, next_token, status};
     return kda::launch_draft_verify(a, in_dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK
                                                                                                    : KDA_ERR_CUDA;
+}
+
+// Sizes that the linear-attention entry points share.
+static kda_status linear_check(int32_t rows, int32_t H, int32_t H_qk, int32_t d_k, int32_t d_v, kda_dtype in_dtype) {
+    if (rows < 0 || H <= 0 || H > 65535 || H_qk <= 0 || H % H_qk || !valid_dtype(in_dtype)) return KDA_ERR_INVALID_ARG;
+    if (d_k != d_v || !supported_d(d_k)) return KDA_ERR_UNSUPPORTED;
+    return (int64_t)rows * H > INT_MAX ? KDA_ERR_UNSUPPORTED : KDA_OK;
+}
+
+// Segments of a prefill call and where its workspace holds them.
+static kda_status linear_plan(int32_t total_tokens, int32_t num_seqs, int32_t H, int32_t d, int32_t *seg, int32_t *slots,
+                              kda::linear::Layout *lay) {
+    if (num_seqs < 0) return KDA_ERR_INVALID_ARG;
+    *seg = kda::linear::plan_segment(total_tokens, H);
+    const int64_t n = total_tokens / *seg + (int64_t)num_seqs;
+    if (n * H > INT_MAX) return KDA_ERR_UNSUPPORTED;
+    *slots = (int32_t)n;
+    *lay = kda::linear::layout(n, H, d, total_tokens > *seg);
+    return KDA_OK;
+}
+
+size_t kda_linear_workspace_size(int32_t total_tokens, int32_t num_seqs, int32_t H, int32_t d_k, int32_t d_v, kda_dtype in_dtype) {
+    int32_t seg, slots;
+    kda::linear::Layout lay;
+    if (linear_check(total_tokens, H, H, d_k, d_v, in_dtype) || linear_plan(total_tokens, num_seqs, H, d_k, &seg, &slots, &lay)) return 0;
+    return lay.total;
+}
+
+kda_status kda_linear_prefill(const void *q, const void *k, const void *v, const float *g, int32_t g_per_token,
+                              const int32_t *cu_seqlens, int32_t num_seqs, int32_t total_tokens, int32_t H, int32_t H_qk,
+                              int32_t d_k, int32_t d_v, kda_dtype in_dtype, const float *S0, void *o, float *S_final,
+                              void *workspace, size_t workspace_bytes, void *stream, const kda_fusion_opts *opts) {
+    if (kda_status st = linear_check(total_tokens, H, H_qk, d_k, d_v, in_dtype)) return st;
+    int32_t seg, slots;
+    kda::linear::Layout lay;
+    if (kda_status st = linear_plan(total_tokens, num_seqs, H, d_k, &seg, &slots, &lay)) return st;
+    kda::Fusion fu;
+    if (kda_status st = fusion_from(opts, total_tokens > 0, o, &fu)) return st;
+    if (num_seqs == 0) return total_tokens == 0 ? KDA_OK : KDA_ERR_INVALID_ARG;
+    if (!given4(cu_seqlens)) return KDA_ERR_INVALID_ARG;
+    if (total_tokens > 0) {
+        if (!given16(q) || !given16(k) || !given16(v) || !given4(g) || !given16(o)) return KDA_ERR_INVALID_ARG;
+        if (o == q || o == k || o == v || o == (const void *)g) return KDA_ERR_INVALID_ARG;
+    }
+    if (!aligned16(S0) || !aligned16(S_final)) return KDA_ERR_INVALID_ARG;
+    if (S_final && (S_final == q || S_final == k || S_final == v || S_final == o || S_final == (const void *)g)) return KDA_ERR_INVALID_ARG;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < lay.total) return KDA_ERR_INVALID_ARG;
+    char *ws = static_cast<char *>(workspace);
+    kda::linear::Args a{};
+    a.q = q, a.k = k, a.v = v, a.g = g, a.per_token = g_per_token != 0, a.cu = cu_seqlens;
+    a.num_seqs = num_seqs, a.total = total_tokens, a.H = H, a.Hqk = H_qk, a.seg = seg, a.slots = slots;
+    a.S0 = S0, a.o = o, a.S_final = S_final, a.aliased = S0 && S0 == S_final;
+    a.seg_decay = reinterpret_cast<float *>(ws + lay.decay_off);
+    a.seg_state = reinterpret_cast<float *>(ws + lay.state_off);
+    a.status = reinterpret_cast<int32_t *>(ws), a.fu = fu;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = in_dtype == KDA_BF16 && d_k == 128 ? kda::launch_linear_tc(a, s) : kda::launch_linear_simt(a, d_k, in_dtype, s);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_linear_decode_step(const void *q, const void *k, const void *v, const float *g, int32_t g_per_token,
+                                  const int32_t *seq_idx, int32_t num_active, int32_t num_slots, int32_t H, int32_t H_qk,
+                                  int32_t d_k, int32_t d_v, kda_dtype in_dtype, float *S_pool, void *o, int32_t *status,
+                                  void *stream, const kda_fusion_opts *opts) {
+    if (kda_status st = linear_check(num_active, H, H_qk, d_k, d_v, in_dtype)) return st;
+    if (num_slots < 0) return KDA_ERR_INVALID_ARG;
+    if ((int64_t)num_slots * H > INT_MAX) return KDA_ERR_UNSUPPORTED;
+    kda::Fusion fu;
+    if (kda_status st = fusion_from(opts, num_active > 0, o, &fu)) return st;
+    if (num_active == 0) return KDA_OK;
+    if (!given16(q) || !given16(k) || !given16(v) || !given4(g) || !aligned4(seq_idx) || !given16(S_pool) || !given16(o) || !aligned4(status))
+        return KDA_ERR_INVALID_ARG;
+    if (o == q || o == k || o == v || o == (const void *)g || o == (const void *)S_pool) return KDA_ERR_INVALID_ARG;
+    const void *pool = S_pool;
+    if (pool == q || pool == k || pool == v || pool == (const void *)g || pool == fu.gate) return KDA_ERR_INVALID_ARG;
+    const kda::LinearDecodeArgs a{q, k, v, g, g_per_token != 0, seq_idx, num_active, num_slots, H, H_qk, d_k, S_pool, o, status, fu};
+    return kda::launch_linear_decode(a, in_dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_rope(const void *q, const void *k, const int32_t *positions, const uint64_t *steps, int32_t total_tokens,
+                    int32_t H_q, int32_t H_k, int32_t d, int32_t rot, int32_t interleaved, float scale, kda_dtype in_dtype,
+                    void *q_out, void *k_out, void *stream) {
+    if (total_tokens < 0 || H_q < 0 || H_k < 0 || H_q > 65535 || H_k > 65535 || H_q + H_k == 0 || d <= 0 || rot < 2 || rot > d || rot % 2 ||
+        !valid_dtype(in_dtype))
+        return KDA_ERR_INVALID_ARG;
+    if ((int64_t)total_tokens * (H_q + H_k) > INT_MAX || d > KDA_ROPE_MAX_D) return KDA_ERR_UNSUPPORTED;
+    if (total_tokens == 0) return KDA_OK;
+    const uintptr_t el = in_dtype == KDA_BF16 ? 1u : 3u;
+    const auto given = [el](const void *p, int32_t heads) { return heads == 0 || (p && (reinterpret_cast<uintptr_t>(p) & el) == 0); };
+    if (!given4(positions) || !steps || (reinterpret_cast<uintptr_t>(steps) & 7u) || !given(q, H_q) || !given(q_out, H_q) ||
+        !given(k, H_k) || !given(k_out, H_k))
+        return KDA_ERR_INVALID_ARG;
+    // in place or apart, but not one in the other's place
+    if (H_q && H_k && (q == k || q_out == k_out || q_out == k || k_out == q)) return KDA_ERR_INVALID_ARG;
+    const kda::RopeArgs a{q, k, positions, reinterpret_cast<const unsigned long long *>(steps), total_tokens, H_q, H_k, d, rot,
+                          interleaved != 0, scale, q_out, k_out};
+    return kda::launch_rope(a, in_dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -1,0 +1,154 @@
+// kda_linear.cuh -- linear attention with one decay per head: what its kernels share.
+//
+// Per (document, head), with g one log-decay of a token (or of the head):
+//     S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t.
+// A run of tokens 1..n behind a state S is, with b_i = g_1 + ... + g_i,
+//     o_i = exp(b_i) S^T q_i + sum_{j <= i} exp(b_i - b_j) (q_i . k_j) v_j,
+//     S_n = exp(b_n) S + sum_j exp(b_n - b_j) k_j v_j^T,
+// all exponents at most 0 where no log-decay is positive, so nothing overflows on the way.
+//
+// A document of more than `seg` tokens is split into segments that run side by side: a first kernel forms what each
+// adds to the state by its end, a second chains those into the state before each segment, and the last forms the
+// outputs.  Segments are numbered without a table: document n owns slots cu[n] / seg + n and on, one for each of its
+// segments (an empty document one): cu[n + 1] / seg + n + 1 is never below the end of that run, and the last slot is
+// below total / seg + num_seqs.  The document of a slot is the last one whose first slot is not above it.
+#pragma once
+
+#include "kda_internal.cuh"
+
+namespace kda {
+namespace linear {
+
+constexpr float kLog2e = 1.4426950408889634f;
+// Log2-decays are taken as at least this: 2^-160 is 0 in fp32 (down to its smallest subnormal), as a decay of minus
+// infinity is, and differences of their sums stay numbers.
+constexpr float kMinLog2 = -160.f;
+
+// A token's log-decay in base 2 (NaN stays NaN).
+__device__ __forceinline__ float log2_decay(float g) {
+    const float x = g * kLog2e;
+    return x < kMinLog2 ? kMinLog2 : x;
+}
+
+// Whether cu_seqlens describes num_seqs documents of total tokens in all; every thread of the block calls it and gets
+// the answer.
+__device__ __forceinline__ bool valid_table(const int32_t *__restrict__ cu, int num_seqs, int total) {
+    bool ok = true;
+    for (int n = threadIdx.x; n <= num_seqs; n += blockDim.x) {
+        const int here = cu[n];
+        ok = ok && here >= 0 && here <= total;
+        if (n == 0) ok = ok && here == 0;
+        ok = ok && (n == num_seqs ? here == total : here <= cu[n + 1]);
+    }
+    return __syncthreads_and(ok);
+}
+
+struct Segment {
+    int doc, t0, len;   // document, first token, tokens (0 for an empty document)
+    int count;          // segments of its document
+    bool first, last;   // of them
+};
+
+// The segment of a slot; false if the slot has none.  Called by a whole warp: 32 documents are looked at at once.
+__device__ __forceinline__ bool find_segment(const int32_t *__restrict__ cu, int num_seqs, int seg, int slot, Segment *s) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = num_seqs;  // the document is in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 31) / 32, at = lo + lane * step;
+        const bool below = lane * step < n && cu[at] / seg + at <= slot;
+        const int hit = __popc(__ballot_sync(0xffffffffu, below)) - 1;  // the first is always below
+        lo += hit * step;
+        n = min(step, n - hit * step);
+    }
+    const int begin = cu[lo], len = cu[lo + 1] - begin, i = slot - (begin / seg + lo), count = len > seg ? (len + seg - 1) / seg : 1;
+    if (i >= count) return false;
+    s->doc = lo;
+    s->t0 = begin + i * seg;
+    s->len = min(seg, len - i * seg);
+    s->count = count;
+    s->first = i == 0;
+    s->last = i == count - 1;
+    return true;
+}
+
+// Where a segment's state begins: its document's incoming state (null: zeros), or what the chain left in the slot
+// before it.  With S_final in S0's place the last segment's end could overtake the first one's start, so the chain
+// leaves a copy of S0 in the document's last slot, which has no other use.
+struct Args;
+__device__ __forceinline__ const float *segment_start(const Args &a, const Segment &s, int slot, int h, size_t state);
+
+// Tokens of a segment: as many segments of the whole batch as give each SM one of some head, as long as that leaves
+// them at least 256 tokens.
+inline int plan_segment(int64_t total, int64_t H) {
+    constexpr int64_t kSms = 152;
+    const int64_t parts = H < kSms ? kSms / H : 1, seg = ((total + parts - 1) / parts + 63) / 64 * 64;
+    return (int)(seg < 256 ? 256 : seg);
+}
+
+struct Args {
+    const void *q, *k, *v;
+    const float *g;       // [total, H], or [H] where !per_token
+    int per_token;
+    const int32_t *cu;
+    int num_seqs, total, H, Hqk;  // head h of v reads head h / (H / Hqk) of q and k
+    int seg, slots;       // tokens of a segment (a multiple of 64), slots of segments
+    const float *S0;      // [num_seqs, H, d, d] or null
+    void *o;
+    float *S_final;       // or null
+    float *seg_state;     // [slots, H, d, d]: first what a segment adds, then the state behind it
+    float *seg_decay;     // [slots, H]: the product of its decays
+    int32_t *status;
+    int aliased;          // S_final is S0: a document of several segments starts from a copy of it
+    int first;            // whether the kernel is its call's first, which sets the status word
+    Fusion fu;
+};
+
+__device__ __forceinline__ const float *segment_start(const Args &a, const Segment &s, int slot, int h, size_t state) {
+    if (s.first && !(a.aliased && s.count > 1)) return a.S0 ? a.S0 + ((size_t)s.doc * a.H + h) * state : nullptr;
+    return a.seg_state + ((size_t)(s.first ? slot + s.count - 1 : slot - 1) * a.H + h) * state;
+}
+
+// Workspace: the status word (256 bytes), then the segments' decays and states.
+struct Layout {
+    size_t decay_off, state_off, total;
+};
+inline Layout layout(int64_t slots, int64_t H, int d, bool split) {
+    Layout l;
+    l.decay_off = 256;
+    l.state_off = l.decay_off + (split ? align256((size_t)slots * H * 4) : 0);
+    l.total = l.state_off + (split ? (size_t)slots * H * d * d * 4 : 0);
+    return l;
+}
+
+}  // namespace linear
+
+// Chunked linear attention (kda_linear_tc.cu: bf16, d = 128; kda_linear_simt.cu: the rest), and the chaining of the
+// segments' states between its two passes.
+cudaError_t launch_linear_tc(const linear::Args &a, cudaStream_t st);
+cudaError_t launch_linear_simt(const linear::Args &a, int d, kda_dtype dt, cudaStream_t st);
+cudaError_t launch_linear_chain(const linear::Args &a, int d, cudaStream_t st);
+// One token of each listed slot of a pool (kda_linear_decode.cu).
+struct LinearDecodeArgs {
+    const void *q, *k, *v;
+    const float *g;
+    int per_token;
+    const int32_t *idx;  // or null: sequence i is slot i
+    int num_active, num_slots, H, Hqk, d;
+    float *S;
+    void *o;
+    int32_t *status;
+    Fusion fu;
+};
+cudaError_t launch_linear_decode(const LinearDecodeArgs &a, kda_dtype dt, cudaStream_t st);
+// Rotary positions (kda_rope.cu).
+struct RopeArgs {
+    const void *q, *k;
+    const int32_t *positions;
+    const unsigned long long *steps;
+    int total, Hq, Hk, d, rot, interleaved;
+    float scale;
+    void *q_out, *k_out;
+};
+cudaError_t launch_rope(const RopeArgs &a, kda_dtype dt, cudaStream_t st);
+
+}  // namespace kda

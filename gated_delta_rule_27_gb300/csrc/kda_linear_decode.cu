@@ -1,0 +1,136 @@
+// kda_linear_decode.cu -- linear attention with one decay per head, one new token for each listed slot of a pool:
+//     S <- exp(g) S + k v^T,   o = S^T q.
+//
+// Bound by HBM: the fp32 state is read and written once (128 KB a sequence and head at d = 128), everything else is
+// small.  One CTA owns one state; a thread holds 16 rows of four adjacent columns, all loaded before any arithmetic.
+// The new state needs no sum over rows, so it is stored at once; o's sums over rows end in shared memory, in a fixed
+// order.
+#include "kda_linear.cuh"
+#include "kda_tc.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kRows = 16;
+
+template <typename Tin, int D>
+__global__ void __launch_bounds__((D / 4) * (D / kRows))
+linear_decode_kernel(const LinearDecodeArgs a) {
+    constexpr int CG = D / 4, RG = D / kRows, NT = CG * RG;
+    __shared__ float s_q[D], s_k[D], s_part[RG][D], s_o[D], s_scale[3];
+    const int tid = threadIdx.x, cg = tid % CG, rg = tid / CG;
+    const int n = blockIdx.x / a.H, h = blockIdx.x - n * a.H;
+    tc::grid_dep_launch();
+    tc::grid_dep_wait();
+    const int slot = a.idx ? a.idx[n] : n;
+    if (slot < 0 || slot >= a.num_slots) {
+        if (a.status && tid == 0) atomicCAS(a.status, 0, (int32_t)KDA_ERR_INVALID_ARG);
+        return;
+    }
+    float4 *S = reinterpret_cast<float4 *>(a.S + ((size_t)slot * a.H + h) * D * D);
+    float4 s[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) s[j] = __ldcs(&S[(size_t)(rg * kRows + j) * CG + cg]);
+    const size_t qk = ((size_t)n * a.Hqk + h / (a.H / a.Hqk)) * D, vo = ((size_t)n * a.H + h) * D;
+    const Tin *q = static_cast<const Tin *>(a.q), *k = static_cast<const Tin *>(a.k), *v = static_cast<const Tin *>(a.v);
+    for (int i = tid; i < D; i += NT) {
+        s_q[i] = to_f32(q[qk + i]);
+        s_k[i] = to_f32(k[qk + i]);
+    }
+    const float decay = expf(a.per_token ? a.g[(size_t)n * a.H + h] : a.g[h]);
+    float4 vv;
+    vv.x = to_f32(v[vo + cg * 4]);
+    vv.y = to_f32(v[vo + cg * 4 + 1]);
+    vv.z = to_f32(v[vo + cg * 4 + 2]);
+    vv.w = to_f32(v[vo + cg * 4 + 3]);
+    __syncthreads();
+    float rk = 1.f, rq = 1.f;
+    if (a.fu.qk_norm) {
+        if (tid < 2 * 16) {  // q by the first 16 threads, k by the next
+            const float *x = tid < 16 ? s_q : s_k;
+            float ss = 0.f;
+            for (int i = tid & 15; i < D; i += 16) ss = fmaf(x[i], x[i], ss);
+            const unsigned mask = NT >= 32 ? 0xffffffffu : (1u << NT) - 1u;
+            if (NT >= 32) {
+#pragma unroll
+                for (int off = 8; off; off >>= 1) ss += __shfl_xor_sync(mask, ss, off);
+                if ((tid & 15) == 0) s_scale[tid >> 4] = rsqrtf(ss + a.fu.qk_eps);
+            }
+        }
+        if (NT < 32 && tid < 2) {
+            const float *x = tid ? s_k : s_q;
+            float ss = 0.f;
+            for (int i = 0; i < D; ++i) ss = fmaf(x[i], x[i], ss);
+            s_scale[tid] = rsqrtf(ss + a.fu.qk_eps);
+        }
+        __syncthreads();
+        rq = s_scale[0];
+        rk = s_scale[1];
+    }
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+        const int r = rg * kRows + j;
+        const float kr = s_k[r] * rk, qr = s_q[r];
+        s[j].x = fmaf(kr, vv.x, decay * s[j].x);
+        s[j].y = fmaf(kr, vv.y, decay * s[j].y);
+        s[j].z = fmaf(kr, vv.z, decay * s[j].z);
+        s[j].w = fmaf(kr, vv.w, decay * s[j].w);
+        __stcs(&S[(size_t)r * CG + cg], s[j]);
+        acc.x = fmaf(qr, s[j].x, acc.x);
+        acc.y = fmaf(qr, s[j].y, acc.y);
+        acc.z = fmaf(qr, s[j].z, acc.z);
+        acc.w = fmaf(qr, s[j].w, acc.w);
+    }
+    *reinterpret_cast<float4 *>(&s_part[rg][cg * 4]) = acc;
+    __syncthreads();
+    Tin *o = static_cast<Tin *>(a.o) + vo;
+    const Tin *z = static_cast<const Tin *>(a.fu.gate);
+    for (int c = tid; c < D; c += NT) {
+        float x = 0.f;
+#pragma unroll
+        for (int r = 0; r < RG; ++r) x += s_part[r][c];
+        x *= rq;
+        if (z) s_o[c] = x;
+        else o[c] = from_f32<Tin>(x);
+    }
+    if (z) {
+        __syncthreads();
+        if (NT >= 32 && tid < 32) {
+            float ss = 0.f;
+            for (int i = tid; i < D; i += 32) ss = fmaf(s_o[i], s_o[i], ss);
+#pragma unroll
+            for (int off = 16; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+            if (tid == 0) s_scale[2] = rsqrtf(ss / (float)D + a.fu.out_eps);
+        } else if (NT < 32 && tid == 0) {
+            float ss = 0.f;
+            for (int i = 0; i < D; ++i) ss = fmaf(s_o[i], s_o[i], ss);
+            s_scale[2] = rsqrtf(ss / (float)D + a.fu.out_eps);
+        }
+        __syncthreads();
+        for (int c = tid; c < D; c += NT)
+            o[c] = from_f32<Tin>(s_o[c] * s_scale[2] * (a.fu.weight ? a.fu.weight[c] : 1.f) * sigmoidf(to_f32(z[vo + c])));
+    }
+}
+
+template <typename Tin, int D>
+cudaError_t launch_d(const LinearDecodeArgs &a, cudaStream_t st) {
+    return launch_dependent(linear_decode_kernel<Tin, D>, dim3((unsigned)(a.num_active * a.H)), dim3((D / 4) * (D / kRows)), 0, st, a);
+}
+template <typename Tin>
+cudaError_t launch_t(const LinearDecodeArgs &a, cudaStream_t st) {
+    switch (a.d) {
+        case 16: return launch_d<Tin, 16>(a, st);
+        case 64: return launch_d<Tin, 64>(a, st);
+        case 128: return launch_d<Tin, 128>(a, st);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_linear_decode(const LinearDecodeArgs &a, kda_dtype dt, cudaStream_t st) {
+    return dt == KDA_BF16 ? launch_t<__nv_bfloat16>(a, st) : launch_t<float>(a, st);
+}
+
+}  // namespace kda

@@ -1,4 +1,4 @@
-// kda_tree_py.cpp -- Python marshalling of the draft-tree entry points.
+// kda_tree_py.cpp -- Python marshalling of the draft-tree, linear-attention and rotary entry points.
 //
 // A speculative round makes one call of these per layer and operator, on tensors of a few rows.  Marshalled through
 // ctypes, a call cost more time on the host than its kernel takes on the GPU: 11.5 us for a step, 9 for a commit,
@@ -31,6 +31,9 @@ decltype(&kda_tree_commit) p_tree_commit;
 decltype(&kda_tree_conv) p_tree_conv;
 decltype(&kda_tree_conv_commit) p_tree_conv_commit;
 decltype(&kda_draft_verify) p_draft_verify;
+decltype(&kda_linear_prefill) p_linear_prefill;
+decltype(&kda_linear_decode_step) p_linear_decode_step;
+decltype(&kda_rope) p_rope;
 
 using Shape = std::initializer_list<int64_t>;
 
@@ -212,14 +215,80 @@ PyObject *draft_verify(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// The addresses of the five entry points, in the order of the functions above.
+// A linear-attention call's sizes, from its q [rows, H_qk, d] and v [rows, H, d].
+struct LinearSizes {
+    const at::Tensor &q, &v;
+    int64_t rows, H, Hqk, d;
+    c10::ScalarType type;
+    bool per_token;
+};
+LinearSizes linear_sizes(PyObject *oq, PyObject *ov, PyObject *og) {
+    const at::Tensor &q = lead(oq, 3, "q"), &v = lead(ov, 3, "v"), &g = tensor(og, "g");
+    dtype(q);
+    if (g.dim() != 1 && g.dim() != 2) fail(PyExc_ValueError, "g has shape " + text(g.sizes()) + ", expected one log-decay a token and head, or one a head");
+    return {q, v, v.size(0), v.size(1), q.size(1), v.size(2), q.scalar_type(), g.dim() == 2};
+}
+float *decays(PyObject *o, const LinearSizes &s) {
+    return s.per_token ? arg<float>(o, {s.rows, s.H}, "g") : arg<float>(o, {s.H}, "g");
+}
+
+// q, k, v, g, cu_seqlens, o, S0, S_final, workspace, stream, qk_l2norm, qk_eps, out_gate, out_weight, out_eps
+PyObject *linear_prefill(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(a, n, 15, [&] {
+        const LinearSizes s = linear_sizes(a[0], a[2], a[3]);
+        const at::Tensor &cu = lead(a[4], 1, "cu_seqlens"), &ws = lead(a[8], 1, "workspace");
+        const int64_t N = cu.size(0) - 1;
+        kda_fusion_opts opts{truth(a[10]), real(a[11]), arg(a[12], s.type, {s.rows, s.H, s.d}, "out_gate"), arg<float>(a[13], {s.d}, "out_weight"), real(a[14])};
+        return (long)p_linear_prefill(arg(a[0], s.type, {s.rows, s.Hqk, s.d}, "q"), arg(a[1], s.type, {s.rows, s.Hqk, s.d}, "k"),
+                                      arg(a[2], s.type, {s.rows, s.H, s.d}, "v"), decays(a[3], s), s.per_token,
+                                      arg<int32_t>(a[4], {N + 1}, "cu_seqlens"), small(N, "the batch"), small(s.rows, "the number of tokens"),
+                                      small(s.H, "H"), small(s.Hqk, "H_qk"), small(s.d, "d"), small(s.d, "d"), dtype(s.q),
+                                      arg<float>(a[6], {N, s.H, s.d, s.d}, "S0"), arg(a[5], s.type, {s.rows, s.H, s.d}, "o"),
+                                      arg<float>(a[7], {N, s.H, s.d, s.d}, "S_final"), arg(a[8], c10::ScalarType::Byte, {ws.size(0)}, "workspace"),
+                                      (size_t)ws.size(0), stream_of(a[9], s.q), opts.qk_l2norm || opts.out_gate ? &opts : nullptr);
+    });
+}
+
+// q, k, v, g, S_pool, o, seq_idx, status, stream, qk_l2norm, qk_eps, out_gate, out_weight, out_eps
+PyObject *linear_decode_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(a, n, 14, [&] {
+        const LinearSizes s = linear_sizes(a[0], a[2], a[3]);
+        const at::Tensor &pool = lead(a[4], 4, "S_pool");
+        const int64_t slots = pool.size(0);
+        if (a[6] == Py_None && slots < s.rows) fail(PyExc_ValueError, "S_pool has fewer slots than there are sequences");
+        kda_fusion_opts opts{truth(a[9]), real(a[10]), arg(a[11], s.type, {s.rows, s.H, s.d}, "out_gate"), arg<float>(a[12], {s.d}, "out_weight"), real(a[13])};
+        return (long)p_linear_decode_step(arg(a[0], s.type, {s.rows, s.Hqk, s.d}, "q"), arg(a[1], s.type, {s.rows, s.Hqk, s.d}, "k"),
+                                          arg(a[2], s.type, {s.rows, s.H, s.d}, "v"), decays(a[3], s), s.per_token,
+                                          arg<int32_t>(a[6], {s.rows}, "seq_idx"), small(s.rows, "the batch"), small(slots, "the pool"),
+                                          small(s.H, "H"), small(s.Hqk, "H_qk"), small(s.d, "d"), small(s.d, "d"), dtype(s.q),
+                                          arg<float>(a[4], {slots, s.H, s.d, s.d}, "S_pool"), arg(a[5], s.type, {s.rows, s.H, s.d}, "o"),
+                                          arg<int32_t>(a[7], {1}, "status"), stream_of(a[8], s.q), opts.qk_l2norm || opts.out_gate ? &opts : nullptr);
+    });
+}
+
+// q, k, positions, steps, q_out, k_out, interleaved, scale, stream
+PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(a, n, 9, [&] {
+        const at::Tensor &q = lead(a[0], 3, "q"), &steps = lead(a[3], 1, "steps");
+        const kda_dtype dt = dtype(q);
+        const auto type = q.scalar_type();
+        const int64_t T = q.size(0), Hq = q.size(1), d = q.size(2), Hk = a[1] == Py_None ? 0 : lead(a[1], 3, "k").size(1);
+        if (Hk == 0 && a[5] != Py_None && a[1] == Py_None) fail(PyExc_ValueError, "k_out without k");
+        return (long)p_rope(arg(a[0], type, {T, Hq, d}, "q"), arg(a[1], type, {T, Hk, d}, "k"), arg<int32_t>(a[2], {T}, "positions"),
+                            static_cast<const uint64_t *>(arg(a[3], c10::ScalarType::Long, {steps.size(0)}, "steps")), small(T, "the number of tokens"),
+                            small(Hq, "H_q"), small(Hk, "H_k"), small(d, "d"), small(2 * steps.size(0), "rot"), truth(a[6]), real(a[7]), dt,
+                            arg(a[4], type, {T, Hq, d}, "q_out"), arg(a[5], type, {T, Hk, d}, "k_out"), stream_of(a[8], q));
+    });
+}
+
+// The addresses of the entry points, in the order of the functions above.
 PyObject *init(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    void *p[5];
-    if (n != 5) {
-        PyErr_SetString(PyExc_TypeError, "init takes five addresses");
+    void *p[8];
+    if (n != 8) {
+        PyErr_SetString(PyExc_TypeError, "init takes eight addresses");
         return nullptr;
     }
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < 8; ++i) {
         p[i] = PyLong_AsVoidPtr(a[i]);
         if (!p[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a null address");
@@ -231,12 +300,16 @@ PyObject *init(PyObject *, PyObject *const *a, Py_ssize_t n) {
     p_tree_conv = reinterpret_cast<decltype(p_tree_conv)>(p[2]);
     p_tree_conv_commit = reinterpret_cast<decltype(p_tree_conv_commit)>(p[3]);
     p_draft_verify = reinterpret_cast<decltype(p_draft_verify)>(p[4]);
+    p_linear_prefill = reinterpret_cast<decltype(p_linear_prefill)>(p[5]);
+    p_linear_decode_step = reinterpret_cast<decltype(p_linear_decode_step)>(p[6]);
+    p_rope = reinterpret_cast<decltype(p_rope)>(p[7]);
     Py_RETURN_NONE;
 }
 
 #define KDA_FUNCTION(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef functions[] = {KDA_FUNCTION(init),             KDA_FUNCTION(tree_step),    KDA_FUNCTION(tree_commit), KDA_FUNCTION(tree_conv),
-                           KDA_FUNCTION(tree_conv_commit), KDA_FUNCTION(draft_verify), {nullptr, nullptr, 0, nullptr}};
+                           KDA_FUNCTION(tree_conv_commit), KDA_FUNCTION(draft_verify),
+                           KDA_FUNCTION(linear_prefill),   KDA_FUNCTION(linear_decode_step), KDA_FUNCTION(rope), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_tree", nullptr, -1, functions, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

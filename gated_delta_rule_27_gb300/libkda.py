@@ -1,7 +1,7 @@
 """Python binding of libkda's C ABI (include/kda.h).
 
-Argument marshalling only (ctypes; csrc/kda_tree_py.cpp for the draft-tree
-calls): every step of the recurrence runs in libkda's CUDA kernels.  torch
+Argument marshalling only (ctypes; csrc/kda_tree_py.cpp for the draft-tree,
+linear-attention and rotary calls): every step of the recurrence runs in libkda's CUDA kernels.  torch
 supplies device memory and streams.  There is no CPU or
 PyTorch fallback: if libkda.so cannot be loaded, or a tensor is not on a CUDA
 device, the call raises.
@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
+import math
 import os
 
 import torch
@@ -23,13 +24,15 @@ SYMBOLS = ("kda_status_string", "kda_prefill_workspace_size", "kda_prefill_chunk
            "kda_prefill_check", "kda_decode_step", "kda_prefill_chunked_noalloc", "kda_prefill_noalloc_check",
            "kda_decode_step_indexed", "kda_state_snapshot", "kda_state_restore", "kda_prefill_chunked_ex",
            "kda_decode_step_ex", "kda_short_conv_prefill", "kda_short_conv_decode", "kda_tree_step",
-           "kda_tree_commit", "kda_tree_conv", "kda_tree_conv_commit", "kda_draft_verify")
+           "kda_tree_commit", "kda_tree_conv", "kda_tree_conv_commit", "kda_draft_verify", "kda_linear_workspace_size",
+           "kda_linear_prefill", "kda_linear_decode_step", "kda_rope")
 # include/kda_testing.h (test hooks)
 TESTING_SYMBOLS = ("kda_testing_set_plan", "kda_testing_set_fault")
 PLAN_AUTO, PLAN_THREE, PLAN_CHAIN, PLAN_PIPE = -1, 0, 2, 3
 FAULT_NONE, FAULT_NO_PUBLISH, FAULT_CHUNK_TABLE = 0, 1, 2
 PREFILL_MAX_KERNELS = 4
 TREE_MAX_NODES = 64
+ROPE_MAX_D = 1024
 
 _lib = None
 
@@ -110,9 +113,14 @@ def _declare(lib: ctypes.CDLL) -> ctypes.CDLL:
                         ("kda_tree_commit", [vp] * 7 + [i32] * 7 + [dt] + [vp] * 3 + [fusion]),
                         ("kda_tree_conv", [vp] * 5 + [i32] * 6 + [dt] + [vp] * 4),
                         ("kda_tree_conv_commit", [vp] * 5 + [i32] * 6 + [dt] + [vp] * 3),
-                        ("kda_draft_verify", [vp] * 8 + [i32] * 3 + [dt, i32] + [vp] * 5)):
+                        ("kda_draft_verify", [vp] * 8 + [i32] * 3 + [dt, i32] + [vp] * 5),
+                        ("kda_linear_prefill", [vp] * 4 + [i32, vp] + [i32] * 6 + [dt] + [vp] * 4 + [ctypes.c_size_t, vp, fusion]),
+                        ("kda_linear_decode_step", [vp] * 4 + [i32, vp] + [i32] * 6 + [dt] + [vp] * 4 + [fusion]),
+                        ("kda_rope", [vp] * 4 + [i32] * 6 + [ctypes.c_float, dt] + [vp] * 3)):
         getattr(lib, name).restype = ctypes.c_int
         getattr(lib, name).argtypes = types
+    lib.kda_linear_workspace_size.restype = ctypes.c_size_t
+    lib.kda_linear_workspace_size.argtypes = [i32, i32, i32, i32, i32, dt]
     lib.kda_testing_set_plan.restype = ctypes.c_int
     lib.kda_testing_set_plan.argtypes = [i32]
     lib.kda_testing_set_fault.restype = ctypes.c_int
@@ -314,7 +322,8 @@ def kda_state_restore(S_saved, seq_idx, S_pool, status=None, stream=None) -> Non
         raise KdaError(rc, "kda_state_restore")
 
 
-# the draft-tree calls: marshalled and checked by csrc/kda_tree_py.cpp, which calls libkda.so's entry points
+# the draft-tree, linear-attention and rotary calls: marshalled and checked by csrc/kda_tree_py.cpp, which calls
+# libkda.so's entry points
 _tree_calls = None
 
 
@@ -328,7 +337,7 @@ def _tree():
         spec.loader.exec_module(module)
         module.init(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
                       for name in ("kda_tree_step", "kda_tree_commit", "kda_tree_conv", "kda_tree_conv_commit",
-                                   "kda_draft_verify")))
+                                   "kda_draft_verify", "kda_linear_prefill", "kda_linear_decode_step", "kda_rope")))
         _tree_calls = module
     return _tree_calls
 
@@ -375,6 +384,94 @@ def kda_draft_verify(logits, tokens, parent, cu_nodes, u_accept, u_next, path, p
                                                draft_probs, temperature, status, stream)
     if rc != KDA_OK:
         raise KdaError(rc, "kda_draft_verify")
+
+
+def kda_linear_workspace_size(total_tokens: int, num_seqs: int, H: int, d_k: int, d_v: int, in_dtype: int) -> int:
+    return int(load().kda_linear_workspace_size(total_tokens, num_seqs, H, d_k, d_v, in_dtype))
+
+
+def new_linear_workspace(q, v, cu_seqlens) -> torch.Tensor:
+    """The device scratch of kda_linear_prefill for tensors of these shapes."""
+    T, H, d = v.shape
+    n = kda_linear_workspace_size(T, cu_seqlens.numel() - 1, H, d, d, _dtype_code(q))
+    if n == 0:
+        raise KdaError(KDA_ERR_UNSUPPORTED, "kda_linear_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def kda_linear_prefill(q, k, v, g, cu_seqlens, o, S0=None, S_final=None, workspace=None, stream=None, qk_l2norm=False,
+                       qk_eps=1e-6, out_gate=None, out_weight=None, out_eps=1e-6) -> None:
+    """Linear attention with one decay per head over packed documents (kda_linear_prefill): q, k [T, H_qk, d], v, o
+    [T, H, d], g [T, H] or [H]; the fused normalisations as for fusion_opts."""
+    if workspace is None and torch.is_tensor(q) and torch.is_tensor(v) and v.dim() == 3 and torch.is_tensor(cu_seqlens):
+        workspace = new_linear_workspace(q, v, cu_seqlens)
+    rc = (_tree_calls or _tree()).linear_prefill(q, k, v, g, cu_seqlens, o, S0, S_final, workspace, stream, qk_l2norm, qk_eps,
+                                                 out_gate, out_weight, out_eps)
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_linear_prefill")
+
+
+def kda_linear_decode_step(q, k, v, g, S_pool, o, seq_idx=None, status=None, stream=None, qk_l2norm=False, qk_eps=1e-6,
+                           out_gate=None, out_weight=None, out_eps=1e-6) -> None:
+    """One token for each listed slot of a pool of linear-attention states (kda_linear_decode_step): q, k [N, H_qk, d],
+    v, o [N, H, d], g [N, H] or [H], S_pool [slots, H, d, d] updated in place."""
+    rc = (_tree_calls or _tree()).linear_decode_step(q, k, v, g, S_pool, o, seq_idx, status, stream, qk_l2norm, qk_eps,
+                                                     out_gate, out_weight, out_eps)
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_linear_decode_step")
+
+
+def kda_rope(q, k, positions, steps, q_out, k_out, interleaved=False, scale=1.0, stream=None) -> None:
+    """Rotary positions of q [T, H_q, d] and k [T, H_k, d] (or None) (kda_rope): positions [T] int32, steps from
+    rope_steps; q_out and k_out may be q and k."""
+    rc = (_tree_calls or _tree()).rope(q, k, positions, steps, q_out, k_out, interleaved, scale, stream)
+    if rc != KDA_OK:
+        raise KdaError(rc, "kda_rope")
+
+
+def rope_steps(inv_freq) -> torch.Tensor:
+    """kda_rope's table for frequencies in radians a position (fp64, [rot / 2]): int64 with the bits of the part of a
+    turn that a position adds, in steps of 2^-64 turn.  Negative frequencies turn back."""
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+        raise TypeError("rope_steps takes a one-dimensional tensor of float64")
+    turn = torch.remainder(inv_freq / (2 * math.pi), 1.0) * 2.0 ** 32
+    upper = torch.floor(turn)
+    lower = torch.floor((turn - upper) * 2.0 ** 32)
+    return (upper.to(torch.int64) << 32) + lower.to(torch.int64)
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling=None):
+    """(inv_freq [rot / 2] fp64, scale) of rotary positions, pair i turning base^(-2i / rot) radians a position.
+
+    scaling stretches them for contexts longer than the original one:
+      {"type": "linear", "factor": s}  every pair s times slower
+      {"type": "ntk", "factor": s}     the base grown so that the slowest pair is s times slower and the fastest kept
+      {"type": "yarn", "factor": s, "original_max_position": n, "beta_fast": 32, "beta_slow": 1}
+          pairs that turn more than beta_fast times in n positions kept, those that turn less than beta_slow times s
+          times slower, a linear blend between; scale is 0.1 ln s + 1
+    """
+    if rot < 2 or rot % 2:
+        raise ValueError("rot is even and at least 2, got %r" % (rot,))
+    pair = torch.arange(rot // 2, dtype=torch.float64)
+    kind = None if scaling is None else scaling["type"]
+    factor = 1.0 if scaling is None else float(scaling["factor"])
+    if factor < 1.0:
+        raise ValueError("a scaling's factor is at least 1, got %r" % (factor,))
+    if kind == "ntk":
+        base = base * factor ** (rot / (rot - 2)) if rot > 2 else base
+    plain = base ** (-2.0 * pair / rot)
+    if kind in (None, "ntk"):
+        return plain, 1.0
+    if kind == "linear":
+        return plain / factor, 1.0
+    if kind != "yarn":
+        raise ValueError("unknown scaling %r" % (kind,))
+    original = scaling["original_max_position"]
+    at = lambda turns: rot * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))  # noqa: E731
+    lo = max(0.0, math.floor(at(scaling.get("beta_fast", 32.0))))
+    hi = min(rot - 1.0, math.ceil(at(scaling.get("beta_slow", 1.0))))
+    slow = ((pair - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+    return plain * (1 - slow) + plain / factor * slow, 0.1 * math.log(factor) + 1.0
 
 
 def new_workspace(T, N, H, d_k, d_v, in_dtype, chunk_size, device) -> torch.Tensor:

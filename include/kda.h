@@ -399,6 +399,86 @@ KDA_API kda_status kda_draft_verify(const void *logits, const float *draft_probs
                                     void *stream);
 
 /*
+ * Linear attention with one decay per head: the recurrence without the delta
+ * rule,
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t
+ * per (sequence, head), g one log-decay of a token and head, or of the head.
+ * The course pages have no counterpart; it serves layers of that kind with
+ * the states, packing and fused normalisations of the calls above.
+ *
+ * kda_linear_prefill: the chunked form over packed documents.
+ *   q, k       [total_tokens, H_qk, d_k] in_dtype; head h of v reads head
+ *              h / (H / H_qk) of q and k (H a multiple of H_qk)
+ *   v, o       [total_tokens, H, d_v] in_dtype; o must not alias an input
+ *   g          fp32 natural-log decays, [total_tokens, H], or [H] if
+ *              g_per_token is 0; -inf (forget everything) is allowed
+ *   cu_seqlens as kda_prefill_chunked, whose rule for invalid tables holds
+ *   S0, S_final  [num_seqs, H, d_k, d_v] fp32, each may be NULL; S_final may be
+ *              S0 itself (no other overlap)
+ *   workspace  device scratch of kda_linear_workspace_size(...) bytes, 256-byte
+ *              aligned; kda_prefill_check reads how the call ended
+ *   opts       the fused normalisations (out_gate [total_tokens, H, d_v]), or NULL
+ * d_k == d_v in {16, 64, 128}.  A document's bits do not depend on the other
+ * documents' values, but on the batch's number of tokens and on H, which choose
+ * how documents are split: results of two packings agree as stated below.
+ *
+ * Accuracy.  bf16 at d = 128: sums are fp32; the products' operands that are
+ * not inputs are bf16 -- the scores and the state where they form o (each adds
+ * an error of the size of o's own rounding), and k v^T's decayed v in two parts
+ * (16 bits of the 24: S is off by 2 to 4e-6 of its size, 2-norm).  Elsewhere
+ * all arithmetic is fp32.  A NaN or infinity in a token's q, k or v can reach
+ * the earlier outputs of its document in the same 64 tokens, but no other
+ * document.
+ *
+ * kda_linear_decode_step: one token for each of num_active sequences.
+ *   q, k, v, g, o, opts  as above with num_active rows
+ *   seq_idx    [num_active] int32, device: distinct slots of the pool (listing a
+ *              slot twice makes the two updates race), or NULL: sequence i
+ *              steps slot i
+ *   S_pool     [num_slots, H, d_k, d_v] fp32, the listed slots read and
+ *              overwritten with S_t, the others left alone
+ *   status     optional device int32 (NULL to skip): a slot outside
+ *              [0, num_slots) is skipped and sets *status to
+ *              KDA_ERR_INVALID_ARG if it was 0
+ */
+KDA_API size_t kda_linear_workspace_size(int32_t total_tokens, int32_t num_seqs, int32_t H, int32_t d_k, int32_t d_v,
+                                         kda_dtype in_dtype);
+KDA_API kda_status kda_linear_prefill(const void *q, const void *k, const void *v, const float *g, int32_t g_per_token,
+                                      const int32_t *cu_seqlens, int32_t num_seqs, int32_t total_tokens, int32_t H,
+                                      int32_t H_qk, int32_t d_k, int32_t d_v, kda_dtype in_dtype, const float *S0,
+                                      void *o, float *S_final, void *workspace, size_t workspace_bytes, void *stream,
+                                      const kda_fusion_opts *opts);
+KDA_API kda_status kda_linear_decode_step(const void *q, const void *k, const void *v, const float *g,
+                                          int32_t g_per_token, const int32_t *seq_idx, int32_t num_active,
+                                          int32_t num_slots, int32_t H, int32_t H_qk, int32_t d_k, int32_t d_v,
+                                          kda_dtype in_dtype, float *S_pool, void *o, int32_t *status, void *stream,
+                                          const kda_fusion_opts *opts);
+
+/*
+ * Rotary positions of q and k: with angle = positions[t] * frequency_i, pair
+ * (x, y) of every head of token t becomes
+ *     scale (x cos - y sin, y cos + x sin).
+ *   q, q_out   [total_tokens, H_q, d] in_dtype     k, k_out [total_tokens, H_k, d]
+ *              each output may be its own input, no other overlap; H_q or H_k may
+ *              be 0 (its pointers NULL)
+ *   positions  [total_tokens] int32, device; any sign
+ *   steps      [rot / 2] uint64, device: frequency_i as a part of a turn, in steps
+ *              of 2^-64 turn (a negative frequency as its two's complement, which
+ *              turns back).  Angles are formed in whole numbers, exact for every
+ *              position.
+ *   rot        how many of a head's first elements turn, even, 2 to d; the others
+ *              are copied.  Pairs are (2i, 2i + 1) if `interleaved`, else
+ *              (i, i + rot / 2).
+ * d is 2 to KDA_ROPE_MAX_D.  Pointers to q and k are element-aligned, steps 8-byte,
+ * positions 4-byte aligned.
+ */
+#define KDA_ROPE_MAX_D 1024
+KDA_API kda_status kda_rope(const void *q, const void *k, const int32_t *positions, const uint64_t *steps,
+                            int32_t total_tokens, int32_t H_q, int32_t H_k, int32_t d, int32_t rot,
+                            int32_t interleaved, float scale, kda_dtype in_dtype, void *q_out, void *k_out,
+                            void *stream);
+
+/*
  * Chunked prefill that allocates nothing.  The course pages have no
  * counterpart to this entry point; it repackages kda_prefill_chunked for
  * callers that cannot give the library device scratch: code that runs while a
