@@ -21,13 +21,13 @@ namespace linear {
 
 constexpr float kLog2e = 1.4426950408889634f;
 // Log2-decays are taken as at least this: 2^-160 is 0 in fp32 (down to its smallest subnormal), as a decay of minus
-// infinity is, and differences of their sums stay numbers.
+// infinity is, and differences of their sums stay numbers.  (At most its opposite, which is infinite in fp32.)
 constexpr float kMinLog2 = -160.f;
 
 // A token's log-decay in base 2 (NaN stays NaN).
 __device__ __forceinline__ float log2_decay(float g) {
     const float x = g * kLog2e;
-    return x < kMinLog2 ? kMinLog2 : x;
+    return x < kMinLog2 ? kMinLog2 : x > -kMinLog2 ? -kMinLog2 : x;
 }
 
 // Whether cu_seqlens describes num_seqs documents of total tokens in all; every thread of the block calls it and gets

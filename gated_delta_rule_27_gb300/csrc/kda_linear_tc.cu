@@ -4,17 +4,18 @@
 //     P_ij = 2^(b_i - b_j) (q_i . k_j)        (j <= i, else 0)
 //     O^T  = 2^(b_i) S^T Q^T + V^T P^T
 //     S^T <- 2^(b_64) S^T + V'^T K,           V'_j = 2^(b_64 - b_j) v_j
-// so each product has 128 rows (the value dimension) or the chunk's 64 tokens, and S^T stays in tensor memory for a
-// whole segment.  q, k, v are read once, o is written once: 1 KB a token and head against 98 kFLOP, so HBM bounds
+// so each product has 128 rows (the value dimension) or the chunk's 64 tokens.  S^T stays in the registers of one warpgroup
+// for a whole segment: the tensor core cuts its sums off instead of rounding them, which a sum over thousands of tokens
+// would show (8e-6 of S after 4096 tokens), so it forms each chunk's V'^T K by itself and the sum over chunks is rounded.
+// q, k, v are read once, o is written once: 1 KB a token and head against 98 kFLOP, so HBM bounds
 // it and the work per chunk only has to hide behind the copies (a CTA with its SM's share of HBM takes 1.45 us a
 // chunk).  What a CTA does is spread over warps that each do one thing, chunk after chunk, across segments:
 //     warps 0-1    P: Q K^T from tensor memory, times the decays, to shared memory in bf16
-//     warp 2       copies of q, k, v (and of the output gate) by TMA, three chunks ahead
+//     warp 2       copies of q, k, v (and of the output gate) by TMA, three chunks ahead, and the decays' sums
 //     warp 3       issues all MMAs
-//     warps 4-7    V': v times its decay, in two bf16 parts, to tensor memory (the A operand of the state's product)
-//     warps 8-11   S: the state's decay in place, and its bf16 copy (the A operand of S^T Q^T)
+//     warps 4-7    the norms of q and k (fused normalisation only); V': v times its decay, in two bf16 parts, to tensor memory (the A operand of the state's product)
+//     warps 8-11   S: the state, decayed and added to, and its bf16 copy (the A operand of S^T Q^T)
 //     warps 12-15  O: the two parts of o added, normalised, to shared memory and out by TMA
-//     warp 16      the decays' sums; warps 17-18 the norms of q and k (fused normalisation only)
 //
 // Roundings to bf16: P and the copy of S, which only reach o, itself rounded to bf16 (each adds an error of the size
 // of that rounding in its part of o).  V' reaches the state, which is fp32: it is taken in two parts (16 bits of 24).
@@ -38,22 +39,20 @@ constexpr int kTile = kC * kDim * 2;
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kRing = 4;  // chunks whose decays are kept
 
-// A wait that ran out ends the whole CTA: everyone polls `dead`.
-__device__ __forceinline__ bool wait_or_dead(uint64_t *bar, uint32_t parity, volatile int *dead) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = tc::globaltimer_ns();
-    for (;;) {
-        for (int i = 0; i < 32; ++i)
-            if (tc::mbar_try_wait(bar, parity)) return true;
-        if (*dead) return false;
-        if (tc::globaltimer_ns() - t0 > kWaitNs) {
-            *dead = 1;
-            return false;
-        }
+// A whole warp's wait.  One that runs out, or sees that another has, ends the whole CTA.  The loop is small on purpose, see
+// decayed_values.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, const volatile int *dead) {
+    bool ok = tc::mbar_try_wait(bar, parity);
+    if (!ok) {
+        const uint64_t t0 = tc::globaltimer_ns();
+#pragma unroll 1
+        do ok = tc::mbar_try_wait(bar, parity);
+        while (!ok && !*dead && tc::globaltimer_ns() - t0 < kWaitNs);
     }
+    return __all_sync(0xffffffffu, ok);
 }
 #define WAIT(bar, n_uses) \
-    if (!__all_sync(0xffffffffu, wait_or_dead(&(bar), (uint32_t)(n_uses) & 1u, &sh.dead))) goto done
+    if (!wait_warp(&(bar), (uint32_t)(n_uses) & 1u, &sh.dead)) goto died
 
 // One arrival for the warp, once all its lanes are here.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
@@ -74,9 +73,15 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // What the other warps need of a chunk's decays (in base 2) and norms.
 struct __align__(16) Gates {
-    float b_hi[kC], b_lo[kC];  // sums of log-decays from the chunk's start, in two parts
+    float b[kC];               // sums of log-decays from the chunk's start
     float in[kC];              // 2^b: decay of the incoming state
     float out[kC];             // 2^(b_64 - b): decay to the chunk's end; 0 behind the segment
     float rq[kC], rk[kC];      // 1 / norm of q and k (fused normalisation only)
@@ -89,9 +94,9 @@ struct OutShared {
     float rms[kC];
     uint64_t full[3], empty[3];           // q, k, v of a chunk
     uint64_t gfull[kRing], gempty[kRing];
-    uint64_t fixed;                       // rows behind a segment cleared
+    uint64_t fixed[2];                    // rows behind a segment cleared (turn by turn: V' can be a chunk ahead)
     uint64_t pfull[2], pready[2], ofull[2], ofree[2];
-    uint64_t vready, sready, kv;
+    uint64_t vready, sready, dfree, kv, qs;
     uint64_t zfull[3], zfree[3];          // output tiles (and the gate's values before them)
     uint64_t drain;
     uint32_t tmem;
@@ -101,10 +106,12 @@ constexpr int kStage = 3 * kTile;
 constexpr int kOutP = 3 * kStage, kOutO = kOutP + 2 * 8192, kOutShared = kOutO + 3 * kTile;
 constexpr int kOutSmem = kOutShared + (int)sizeof(OutShared) + 1024;
 static_assert(kOutSmem <= 232448, "shared memory of a CTA");
-constexpr int kOutThreads = 19 * 32;
+constexpr int kOutThreads = 16 * 32;
+// Registers a thread of each warpgroup, see more_registers.
+constexpr int kOutOthers = 104, kOutS = 200, kOutRegs = 128 * (3 * kOutOthers + kOutS);
 
-// Tensor memory: S^T in fp32 and bf16, V'^T in two parts, two buffers each of P (then V^T P^T) and S^T Q^T.
-enum : uint32_t { kTmS = 0, kTmSb = 128, kTmVhi = 192, kTmVlo = 224, kTmP = 256, kTmO = 384 };
+// Tensor memory: V'^T K, S^T in bf16, V'^T in two parts, two buffers each of P (then V^T P^T) and S^T Q^T.
+enum : uint32_t { kTmD = 0, kTmSb = 128, kTmVhi = 192, kTmVlo = 224, kTmP = 256, kTmO = 384 };
 
 constexpr uint64_t kKmajor = tc::smem_desc_base(16, 1024, tc::SW_128B);
 constexpr uint64_t kMNmajor = tc::smem_desc_base(8192, 1024, tc::SW_128B);
@@ -112,45 +119,53 @@ constexpr uint32_t kId64 = tc::idesc_bf16_f32(128, 64, false, false);
 
 __device__ __forceinline__ uint32_t lane_base(int warp) { return (uint32_t)((warp & 3) * 32) << 16; }
 
-// Sums of log2-decays of a chunk's `n` tokens: lane l holds tokens 2l and 2l + 1 (x0, x1; 0 behind the segment).
-// Sums in 64 bits: behind a token that forgets everything, differences of small decays have to survive.
+// Sums of log2-decays of a chunk's tokens, in steps of 2^-44: lane l holds tokens 2l and 2l + 1.  Whole numbers, so that
+// behind a token that forgets everything differences of small decays survive (fp64 would do, at ten times the latency).
+constexpr float kFixed = 17592186044416.f;
 struct Sums {
-    double b0, b1, all;
+    long long b0, b1, all;
+    bool nan0, nan1, nan;  // whether one of the tokens up to here is NaN, or any
 };
+__device__ __forceinline__ float from_fixed(long long x) { return __ll2float_rn(x) * (1.f / kFixed); }
 __device__ __forceinline__ Sums chunk_sums(float x0, float x1) {
     const int lane = threadIdx.x & 31;
-    double s = (double)x0 + (double)x1;
-    const double own = s;
+    const unsigned n0 = __ballot_sync(0xffffffffu, x0 != x0), n1 = __ballot_sync(0xffffffffu, x1 != x1);
+    const long long f0 = __float2ll_rn(x0 * kFixed), f1 = __float2ll_rn(x1 * kFixed);
+    long long s = f0 + f1;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const double up = __shfl_up_sync(0xffffffffu, s, off);
+        const long long up = __shfl_up_sync(0xffffffffu, s, off);
         if (lane >= off) s += up;
     }
     Sums r;
-    r.b0 = s - own + (double)x0;
+    r.b0 = s - f1;
     r.b1 = s;
     r.all = __shfl_sync(0xffffffffu, s, 31);
+    const unsigned upto = 0xffffffffu >> (31 - lane);
+    r.nan0 = (n0 & upto) | (n1 & (upto >> 1));
+    r.nan1 = (n0 | n1) & upto;
+    r.nan = n0 | n1;
     return r;
 }
 
-// 1 / sqrt(sum of squares + eps) of the tile's 64 rows, two rows a lane.
-__device__ __forceinline__ void row_norms(const uint8_t *tile, float eps, float *out) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll 1
-    for (int r = lane; r < kC; r += 32) {
-        float ss = 0.f;
-#pragma unroll 4
-        for (int c = 0; c < 16; ++c) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(tile + (c >> 3) * 8192 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+// 1 / sqrt(sum of squares + eps) of 16 of the tile's rows, half a row a lane.
+__device__ __forceinline__ void row_norms(const uint8_t *tile, int first, float eps, float *out) {
+    const int lane = threadIdx.x & 31, r = first + (lane & 15);
+    const uint8_t *row = tile + (lane >> 4) * 8192 + r * 128;
+    float2 ss = make_float2(0.f, 0.f);
+#pragma unroll 2
+    for (int c = 0; c < 8; ++c) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(row + ((c ^ (r & 7)) << 4));
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                ss = fmaf(bf16_lo(u[i]), bf16_lo(u[i]), ss);
-                ss = fmaf(bf16_hi(u[i]), bf16_hi(u[i]), ss);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const float2 y = make_float2(bf16_lo(u[i]), bf16_hi(u[i]));
+            ss = tc::fma2(y, y, ss);
         }
-        out[r] = rsqrtf(ss + eps);
     }
+    float all = ss.x + ss.y;
+    all += __shfl_xor_sync(0xffffffffu, all, 16);
+    out[r] = rsqrtf(all + eps);
 }
 
 // Clears rows n..63 of a q, k or v tile (tokens of another document, or none): they would meet zeros in the products,
@@ -163,46 +178,109 @@ __device__ __forceinline__ void clear_rows(uint8_t *tile, int n, int thread, int
     }
 }
 
-// This thread's lane of V'^T (value dimension 32 (warp % 4) + lane) for the chunk's tokens, in two bf16 parts.
+// (The code of this file is kept short on purpose, loops not unrolled unless registers ask for it.  A warp of each kind
+// shares an SM sub-partition and its instruction cache: an instruction takes 1.5 clocks of a warp from code of 8 KB, 4
+// from 24 KB and 5 to 7 from 48 KB on, and the first version, 120 KB unrolled, took 4 times as long for want of them.)
+
+// What a lane addresses when its warp moves four 8 x 8 tiles between registers and a chunk's tile of `dim` 16 on: tokens
+// 0 to 15, in the order (first 8 dims, first 8 tokens), (next 8 dims, first 8 tokens), then the next 8 tokens.  Tokens 16 t
+// on are 2048 t bytes further.
+__device__ __forceinline__ uint32_t tile_lane(int dim) {
+    const int lane = threadIdx.x & 31, token = (lane & 7) + (lane >> 4) * 8, chunk = ((dim & 63) >> 3) + ((lane >> 3) & 1);
+    return (uint32_t)((dim >> 6) * 8192 + token * 128 + ((chunk ^ (token & 7)) << 4));
+}
+
+// 32 lanes of V'^T (value dimensions 32 (warp % 4) on) for the chunk's tokens, in two bf16 parts: v's tile is read
+// transposed, so that a register holds two tokens of a value dimension, as the MMA wants A.
 template <bool NORM>
-__device__ __forceinline__ void decayed_values(const uint8_t *v, const Gates &g, int n, int warp, uint32_t hi_col, uint32_t lo_col) {
-    const int dv = (warp & 3) * 32 + (threadIdx.x & 31);
-    const uint8_t *col = v + (dv >> 6) * 8192;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int j = half * 32 + 2 * i;
-            float w0 = g.out[j], w1 = g.out[j + 1];
-            if (NORM) {
-                w0 *= g.rk[j];
-                w1 *= g.rk[j + 1];
-            }
-            const float v0 = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(col + tc::sw128_offset(j, dv & 63)));
-            const float v1 = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(col + tc::sw128_offset(j + 1, dv & 63)));
-            const float x0 = j < n ? w0 * v0 : 0.f, x1 = j + 1 < n ? w1 * v1 : 0.f;
-            hi[i] = pack_bf16(x0, x1);
-            lo[i] = pack_bf16(x0 - bf16_lo(hi[i]), x1 - bf16_hi(hi[i]));
+__device__ __forceinline__ void decayed_values(const uint8_t *v, const Gates &g, int warp, uint32_t hi_col, uint32_t lo_col) {
+    const int c2 = (threadIdx.x & 3) * 2, dim = (warp & 3) * 32;
+    uint32_t from0 = tc::smem_u32(v) + tile_lane(dim), from1 = tc::smem_u32(v) + tile_lane(dim + 16);
+    hi_col += lane_base(warp);
+    lo_col += lane_base(warp);
+#pragma unroll 1
+    for (int j = c2; j < kC; j += 16, from0 += 2048, from1 += 2048, hi_col += 8, lo_col += 8) {
+        uint32_t x[2][4];
+        tc::ldmatrix_t4(from0, x[0]);
+        tc::ldmatrix_t4(from1, x[1]);
+        float2 w[2] = {*reinterpret_cast<const float2 *>(&g.out[j]), *reinterpret_cast<const float2 *>(&g.out[j + 8])};
+        if (NORM) {
+            w[0] = tc::mul2(w[0], *reinterpret_cast<const float2 *>(&g.rk[j]));
+            w[1] = tc::mul2(w[1], *reinterpret_cast<const float2 *>(&g.rk[j + 8]));
         }
-        tc::tmem_st16(hi_col + lane_base(warp) + half * 16, hi);
-        tc::tmem_st16(lo_col + lane_base(warp) + half * 16, lo);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 y = tc::mul2(make_float2(bf16_lo(x[half][e]), bf16_hi(x[half][e])), w[e >> 1]);
+                hi[e] = pack_bf16(y.x, y.y);
+                const float2 r = tc::sub2(y, make_float2(bf16_lo(hi[e]), bf16_hi(hi[e])));
+                lo[e] = pack_bf16(r.x, r.y);
+            }
+            tc::tmem_st_16x8(hi_col + (half << 20), hi);
+            tc::tmem_st_16x8(lo_col + (half << 20), lo);
+        }
     }
     tc::tmem_wait_st();
     tc::tc_fence_before();
 }
 
-// S^T += V'^T K over the chunk's tokens, both parts of V'.
-__device__ __forceinline__ void mma_state(uint32_t s_col, uint32_t hi_col, uint32_t lo_col, const uint8_t *k, bool accumulate, bool elected) {
-    constexpr uint32_t id = tc::idesc_bf16_f32(128, 128, false, true);
+// Four MMAs over consecutive slices of 16 of K: A in tensor memory (8 columns a slice) or in shared memory, B in shared
+// memory, slices `a_step` and `b_step` (in 16 bytes) apart.
+__device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint64_t b, uint32_t b_step, uint32_t id, bool accumulate, bool one) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-        const uint64_t kd = tc::smem_desc(kMNmajor, tc::smem_u32(k + s * 2048));
-        tc::mma_bf16_ts_warp(s_col, hi_col + s * 8, kd, id, accumulate || s > 0, elected);
-        tc::mma_bf16_ts_warp(s_col, lo_col + s * 8, kd, id, true, elected);
+    for (int i = 0; i < 4; ++i) tc::mma_bf16_ts_warp(d, a + 8 * i, b + (uint64_t)b_step * i, id, accumulate || i > 0, one);
+}
+__device__ __forceinline__ void mma_ss4(uint32_t d, uint64_t a, uint32_t a_step, uint64_t b, uint32_t b_step, uint32_t id, bool accumulate, bool one) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tc::mma_bf16_warp(d, a + (uint64_t)a_step * i, b + (uint64_t)b_step * i, id, accumulate || i > 0, one);
+}
+
+// V'^T K over the chunk's tokens, both parts of V'.
+__device__ __forceinline__ void mma_state(uint32_t d_col, uint32_t hi_col, uint32_t lo_col, const uint8_t *k, bool one) {
+    constexpr uint32_t id = tc::idesc_bf16_f32(128, 128, false, true);
+    const uint64_t kd = tc::smem_desc(kMNmajor, tc::smem_u32(k));
+#pragma unroll 1
+    for (int p = 0; p < 2; ++p) mma_ts4(d_col, p ? lo_col : hi_col, kd, 128, id, p, one);
+}
+
+// The registers of a warpgroup's threads, changed by all its warps.  What the groups have afterwards must not be more than
+// the block was launched with, or the group that asks for more waits for ever: the host compares the sums below with the
+// built kernel's registers before it launches it.
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// This thread's column of a state in memory (rows of kDim), as pairs of rows.
+__device__ __forceinline__ void load_column(float2 (&S)[kDim / 2], const float *p) {
+#pragma unroll
+    for (int k = 0; k < kDim / 2; ++k) S[k] = p ? make_float2(p[(size_t)2 * k * kDim], p[(size_t)(2 * k + 1) * kDim]) : make_float2(0.f, 0.f);
+}
+__device__ __forceinline__ void store_column(const float2 (&S)[kDim / 2], float *p) {
+#pragma unroll
+    for (int k = 0; k < kDim / 2; ++k) {
+        p[(size_t)2 * k * kDim] = S[k].x;
+        p[(size_t)(2 * k + 1) * kDim] = S[k].y;
     }
 }
 
+// S <- all S + V'^T K of this thread's lane.
+__device__ __forceinline__ void add_products(float2 (&S)[kDim / 2], float2 all, uint32_t col) {
+#pragma unroll
+    for (int k = 0; k < kDim; k += 32) {
+        float x[32];
+        tc::tmem_ld32(col + k, x);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) S[k / 2 + e] = tc::fma2(S[k / 2 + e], all, make_float2(x[2 * e], x[2 * e + 1]));
+    }
+    tc::tc_fence_before();
+}
 
 template <bool NORM, bool GATE>
 __global__ void __launch_bounds__(kOutThreads, 1)
@@ -220,19 +298,21 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             tc::mbar_init(&sh.zfree[i], 1);
         }
         for (int i = 0; i < kRing; ++i) {
-            tc::mbar_init(&sh.gfull[i], NORM ? 3 : 1);
+            tc::mbar_init(&sh.gfull[i], NORM ? 5 : 1);
             tc::mbar_init(&sh.gempty[i], 14);  // V', S and O warps, the two of P
         }
         for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&sh.fixed[i], 4);
             tc::mbar_init(&sh.pfull[i], 1);
             tc::mbar_init(&sh.pready[i], 2);
             tc::mbar_init(&sh.ofull[i], 1);
             tc::mbar_init(&sh.ofree[i], 4);
         }
-        tc::mbar_init(&sh.fixed, 4);
         tc::mbar_init(&sh.vready, 4);
         tc::mbar_init(&sh.sready, 4);
+        tc::mbar_init(&sh.dfree, 4);
         tc::mbar_init(&sh.kv, 1);
+        tc::mbar_init(&sh.qs, 1);
         tc::mbar_init(&sh.drain, 1);
         sh.dead = 0;
         tc::fence_mbar_init();
@@ -264,8 +344,10 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     }
 
     int n = 0;  // chunks so far: each barrier's phase follows from it
+    if (warp < 8 || warp >= 12) fewer_registers<kOutOthers>();
     if (warp == 2) {
-        // ---- copies
+        // ---- copies and decays; a chunk's decays are read while the one before it is worked on
+        float g0 = 0.f, g1 = 0.f;
         FOR_SEGMENTS
         if (n >= 3) WAIT(sh.empty[st], n / 3 - 1);
         if (lane == 0) {
@@ -281,64 +363,96 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             if (n >= 3) WAIT(sh.zfree[st], n / 3 - 1);
             if (lane == 0) {
                 tc::mbar_arrive_expect_tx(&sh.zfull[st], kTile);
-                tc::tma_load_3d(sm + kOutO + st * kTile, &tm_z, 0, h, t0, &sh.zfull[st]);
+                for (int p = 0; p < 2; ++p) tc::tma_load_3d(sm + kOutO + st * kTile + p * 8192, &tm_z, p * 64, h, t0, &sh.zfull[st]);
             }
         }
+        const auto fetch = [&](int t, int count) {
+            const float *p = a.per_token ? a.g + (size_t)(t + 2 * lane) * a.H + h : a.g + h;
+            g0 = 2 * lane < count ? *p : 0.f;
+            g1 = 2 * lane + 1 < count ? p[a.per_token ? a.H : 0] : 0.f;
+        };
+        if (c0 == 0) fetch(t0, rows);
+        Gates &g = sh.gates[n % kRing];
+        const float x0 = linear::log2_decay(g0), x1 = linear::log2_decay(g1);
+        if (!last_chunk) fetch(t0 + kC, min(kC, sg.len - c0 - kC));
+        const Sums s = chunk_sums(x0, x1);
+        if (n >= kRing) WAIT(sh.gempty[n % kRing], n / kRing - 1);
+        {
+            const float nan = __int_as_float(0x7fffffff);
+            const float2 b = make_float2(s.nan0 ? nan : from_fixed(s.b0), s.nan1 ? nan : from_fixed(s.b1));
+            reinterpret_cast<float2 *>(g.b)[lane] = b;
+            reinterpret_cast<float2 *>(g.in)[lane] = make_float2(ex2(b.x), ex2(b.y));
+            reinterpret_cast<float2 *>(g.out)[lane] = make_float2(ex2(from_fixed(s.all - s.b0)), ex2(from_fixed(s.all - s.b1)));
+            if (lane == 0) g.all = s.nan ? nan : exp2f(from_fixed(s.all));
+        }
+        warp_arrive(&sh.gfull[n % kRing]);
         END_SEGMENTS
     } else if (warp == 3) {
-        // ---- MMAs.  A chunk's Q K^T goes out before the products of the chunk before it, which wait for more.
+        // ---- MMAs, in the order in which they can start: V'^T K and S^T Q^T of a chunk, Q K^T of the next, whose scores are
+        // worked out meanwhile, V^T P^T of the first
         const bool one = tc::elect_one();
-        int fixes = 0, prev = -1;
-        auto rest = [&](int m) -> bool {  // the products of chunk m after its Q K^T
-            const int s = m % 3, b = m & 1;
-            const uint8_t *at = sm + s * kStage;
-            if (!__all_sync(0xffffffffu, wait_or_dead(&sh.vready, m & 1, &sh.dead))) return false;
-            if (!__all_sync(0xffffffffu, wait_or_dead(&sh.sready, m & 1, &sh.dead))) return false;
-            tc::tc_fence_after();
-            mma_state(tm + kTmS, tm + kTmVhi, tm + kTmVlo, at + kTile, true, one);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                tc::mma_bf16_ts_warp(tm + kTmO + b * 64, tm + kTmSb + i * 8,
-                                     tc::smem_desc(kKmajor, tc::smem_u32(at + (i >> 2) * 8192 + (i & 3) * 32)), kId64, i > 0, one);
-            if (one) tc::mma_commit(&sh.kv);
-            if (!__all_sync(0xffffffffu, wait_or_dead(&sh.pready[b], (m >> 1) & 1, &sh.dead))) return false;
-            tc::tc_fence_after();
-            constexpr uint32_t id = tc::idesc_bf16_f32(128, 64, true, false);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                tc::mma_bf16_warp(tm + kTmP + b * 64, tc::smem_desc(kMNmajor, tc::smem_u32(at + 2 * kTile + i * 2048)),
-                                  tc::smem_desc(kKmajor, tc::smem_u32(sm + kOutP + b * 8192 + i * 32)), id, i > 0, one);
-            if (one) {
-                tc::mma_commit(&sh.ofull[b]);
-                tc::mma_commit(&sh.empty[s]);
+        int fixes = 0, left = 0;  // tokens of the segment that are left
+        int u = (int)blockIdx.x - (int)gridDim.x;
+        for (bool more = true; more; ++n) {
+            if (left <= 0) {  // the next segment with tokens
+                for (;;) {
+                    Segment sg;
+                    u += gridDim.x;
+                    more = u < units;
+                    if (!more) break;
+                    if (linear::find_segment(a.cu, a.num_seqs, a.seg, u / a.H, &sg) && sg.len > 0) {
+                        left = sg.len;
+                        break;
+                    }
+                }
             }
-            __syncwarp();
-            return true;
-        };
-        FOR_SEGMENTS
-        WAIT(sh.full[st], n / 3);
-        if (rows < kC) {
-            WAIT(sh.fixed, fixes);
-            ++fixes;
-        }
-        if (n >= 2) WAIT(sh.ofree[n & 1], n / 2 - 1);
-        tc::tc_fence_after();
-        {
-            const uint8_t *at = sm + st * kStage;
-            // (rows 64 to 127 of the result come of what follows the tile's half, and nobody reads them)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t off = (i >> 2) * 8192 + (i & 3) * 32;
-                tc::mma_bf16_warp(tm + kTmP + (n & 1) * 64, tc::smem_desc(kKmajor, tc::smem_u32(at + off)),
-                                  tc::smem_desc(kKmajor, tc::smem_u32(at + kTile + off)), kId64, i > 0, one);
+            if (n > 0) {  // the products of the chunk before
+                const int m = n - 1, s = m % 3, b = m & 1;
+                const uint8_t *at = sm + s * kStage;
+                WAIT(sh.vready, m);
+                WAIT(sh.dfree, m);
+                tc::tc_fence_after();
+                mma_state(tm + kTmD, tm + kTmVhi, tm + kTmVlo, at + kTile, one);
+                if (one) tc::mma_commit(&sh.kv);
+                WAIT(sh.sready, m);
+                tc::tc_fence_after();
+                const uint64_t qd = tc::smem_desc(kKmajor, tc::smem_u32(at));
+#pragma unroll 1
+                for (int p = 0; p < 2; ++p) mma_ts4(tm + kTmO + b * 64, tm + kTmSb + p * 32, qd + p * 512, 2, kId64, p, one);
+                if (one) tc::mma_commit(&sh.qs);
             }
-            if (one) tc::mma_commit(&sh.pfull[n & 1]);
-            __syncwarp();
+            if (more) {
+                const int st = n % 3;
+                WAIT(sh.full[st], n / 3);
+                if (left < kC) {
+                    WAIT(sh.fixed[fixes & 1], fixes >> 1);
+                    ++fixes;
+                }
+                left -= kC;
+                if (n >= 2) WAIT(sh.ofree[n & 1], n / 2 - 1);
+                tc::tc_fence_after();
+                const uint8_t *at = sm + st * kStage;
+                // (rows 64 to 127 of the result come of what follows the tile's half, and nobody reads them)
+                const uint64_t qd = tc::smem_desc(kKmajor, tc::smem_u32(at)), kd = tc::smem_desc(kKmajor, tc::smem_u32(at + kTile));
+#pragma unroll 1
+                for (int p = 0; p < 2; ++p) mma_ss4(tm + kTmP + (n & 1) * 64, qd + p * 512, 2, kd + p * 512, 2, kId64, p, one);
+                if (one) tc::mma_commit(&sh.pfull[n & 1]);
+                __syncwarp();
+            }
+            if (n > 0) {
+                const int m = n - 1, s = m % 3, b = m & 1;
+                const uint8_t *at = sm + s * kStage;
+                WAIT(sh.pready[b], m >> 1);
+                tc::tc_fence_after();
+                mma_ss4(tm + kTmP + b * 64, tc::smem_desc(kMNmajor, tc::smem_u32(at + 2 * kTile)), 128,
+                        tc::smem_desc(kKmajor, tc::smem_u32(sm + kOutP + b * 8192)), 2, tc::idesc_bf16_f32(128, 64, true, false), false, one);
+                if (one) {
+                    tc::mma_commit(&sh.ofull[b]);
+                    tc::mma_commit(&sh.empty[s]);
+                }
+                __syncwarp();
+            }
         }
-        if (prev >= 0 && !rest(prev)) goto done;
-        prev = n;
-        END_SEGMENTS
-        if (prev >= 0 && !rest(prev)) goto done;
     } else if (warp < 2) {
         // ---- P
         const int i = warp * 32 + lane;
@@ -348,29 +462,33 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         tc::tc_fence_after();
         {
             const Gates &g = sh.gates[n % kRing];
-            const float bh = g.b_hi[i], bl = g.b_lo[i];
+            // (the sums' rounding, 2^-24 of up to 64 x 160, costs a score at most a part in 2^11: less than its bf16)
+            const float bi = g.b[i];
+            const uint32_t from = tm + kTmP + (n & 1) * 64 + lane_base(warp);
             uint8_t *row = sm + kOutP + (n & 1) * 8192 + i * 128;
+            const int end = min(i + 1, rows);
+#pragma unroll 1
+            for (int j = 0; j < kC; j += 8) {
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (j < 32 * (warp + 1)) {  // (warp 0 holds the first 32 rows, which end at column 32)
+                    float x[8], b[8];
+                    tc::tmem_ld8(from + j, x);
+                    *reinterpret_cast<float4 *>(b) = *reinterpret_cast<const float4 *>(&g.b[j]);
+                    *reinterpret_cast<float4 *>(b + 4) = *reinterpret_cast<const float4 *>(&g.b[j + 4]);
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-                float x[32];
-                if (part <= warp) tc::tmem_ld32(tm + kTmP + (n & 1) * 64 + lane_base(warp) + part * 32, x);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t u[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float y[2];
-#pragma unroll
-                        for (int f = 0; f < 2; ++f) {
-                            const int at = c * 8 + e * 2 + f, j = part * 32 + at;
-                            float z = x[at] * ex2((bh - g.b_hi[j]) + (bl - g.b_lo[j]));
-                            if (NORM) z *= g.rk[j];
-                            y[f] = part <= warp && j <= i && j < rows ? z : 0.f;
-                        }
-                        u[e] = pack_bf16(y[0], y[1]);
+                    for (int e = 0; e < 8; e += 2) {
+                        const float2 d = tc::sub2(make_float2(bi, bi), make_float2(b[e], b[e + 1]));
+                        float2 y = tc::mul2(make_float2(x[e], x[e + 1]), make_float2(ex2(d.x), ex2(d.y)));
+                        if (NORM) y = tc::mul2(y, *reinterpret_cast<const float2 *>(&g.rk[j + e]));
+                        x[e] = y.x;
+                        x[e + 1] = y.y;
                     }
-                    *reinterpret_cast<uint4 *>(row + (((part * 4 + c) ^ (i & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (j + e >= end) x[e] = 0.f;
+                    u = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
                 }
+                *reinterpret_cast<uint4 *>(row + (((j >> 3) ^ (i & 7)) << 4)) = u;
             }
         }
         tc::fence_async_smem();
@@ -380,6 +498,7 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         END_SEGMENTS
     } else if (warp < 8) {
         // ---- V'
+        int fixes = 0;
         FOR_SEGMENTS
         WAIT(sh.full[st], n / 3);
         if (rows < kC) {
@@ -387,78 +506,72 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             clear_rows(sm + st * kStage + 2 * kTile, rows, threadIdx.x - 128, 128);
             tc::fence_async_smem();
             tc::named_barrier(1, 128);
-            if (lane == 0) tc::mbar_arrive(&sh.fixed);
+            if (lane == 0) tc::mbar_arrive(&sh.fixed[fixes & 1]);
+            ++fixes;
+        }
+        if (NORM) {
+            if (n >= kRing) WAIT(sh.gempty[n % kRing], n / kRing - 1);
+            row_norms(sm + st * kStage, (warp & 3) * 16, a.fu.qk_eps, sh.gates[n % kRing].rq);
+            row_norms(sm + st * kStage + kTile, (warp & 3) * 16, a.fu.qk_eps, sh.gates[n % kRing].rk);
+            warp_arrive(&sh.gfull[n % kRing]);
         }
         WAIT(sh.gfull[n % kRing], n / kRing);
         if (n >= 1) WAIT(sh.kv, n - 1);
         tc::tc_fence_after();
-        decayed_values<NORM>(sm + st * kStage + 2 * kTile, sh.gates[n % kRing], rows, warp, tm + kTmVhi, tm + kTmVlo);
+        decayed_values<NORM>(sm + st * kStage + 2 * kTile, sh.gates[n % kRing], warp, tm + kTmVhi, tm + kTmVlo);
         warp_arrive(&sh.vready);
         if (lane == 0) tc::mbar_arrive(&sh.gempty[n % kRing]);
         END_SEGMENTS
     } else if (warp < 12) {
         // ---- S
+        more_registers<kOutS>();
         const int dv = (warp & 3) * 32 + lane;
+        const uint32_t d_col = tm + kTmD + lane_base(warp), sb_col = tm + kTmSb + lane_base(warp);
         for (int u = blockIdx.x; u < units; u += gridDim.x) {
             Segment sg;
             const int slot = u / a.H, h = u - slot * a.H;
             if (!linear::find_segment(a.cu, a.num_seqs, a.seg, slot, &sg)) continue;
-            const size_t doc_state = ((size_t)sg.doc * a.H + h) * kDim * kDim + dv;
             const float *init = linear::segment_start(a, sg, slot, h, (size_t)kDim * kDim);
-            if (init) init += dv;
-            if (sg.len == 0) {
-                if (a.S_final)
-                    for (int k = 0; k < kDim; ++k) a.S_final[doc_state + (size_t)k * kDim] = init ? init[(size_t)k * kDim] : 0.f;
-                continue;
-            }
+            float2 S[kDim / 2], all = make_float2(1.f, 1.f);
+            load_column(S, init ? init + dv : nullptr);
             for (int c0 = 0; c0 < sg.len; c0 += kC, ++n) {
-                WAIT(sh.gfull[n % kRing], n / kRing);
-                const float all = sh.gates[n % kRing].all;
                 if (c0 > 0) {
                     WAIT(sh.kv, n - 1);
                     tc::tc_fence_after();
+                    add_products(S, all, d_col);
                 }
-#pragma unroll 1
-                for (int part = 0; part < 4; ++part) {
-                    float x[32];
-                    if (c0 == 0) {
+                warp_arrive(&sh.dfree);
+                if (n > 0) WAIT(sh.qs, n - 1);
+                tc::tc_fence_after();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) x[k] = init ? init[(size_t)(part * 32 + k) * kDim] : 0.f;
-                    } else {
-                        tc::tmem_ld32(tm + kTmS + lane_base(warp) + part * 32, x);
-                    }
-                    uint32_t p[16];
+                for (int k = 0; k < kDim; k += 16) {
+                    uint32_t p[8];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        p[k] = pack_bf16(x[2 * k], x[2 * k + 1]);
-                        x[2 * k] *= all;
-                        x[2 * k + 1] *= all;
-                    }
-                    tc::tmem_st16(tm + kTmSb + lane_base(warp) + part * 16, p);
-                    tc::tmem_st32(tm + kTmS + lane_base(warp) + part * 32, x);
+                    for (int e = 0; e < 8; ++e) p[e] = pack_bf16(S[k / 2 + e].x, S[k / 2 + e].y);
+                    tc::tmem_st8(sb_col + k / 2, p);
                 }
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
                 warp_arrive(&sh.sready);
-                if (lane == 0) tc::mbar_arrive(&sh.gempty[n % kRing]);
+                WAIT(sh.gfull[n % kRing], n / kRing);
+                const float x = sh.gates[n % kRing].all;
+                all = make_float2(x, x);
+                warp_arrive(&sh.gempty[n % kRing]);
             }
-            WAIT(sh.kv, n - 1);
-            if (sg.last && a.S_final) {
+            if (sg.len > 0) {
+                WAIT(sh.kv, n - 1);
                 tc::tc_fence_after();
-#pragma unroll 1
-                for (int part = 0; part < 4; ++part) {
-                    float x[32];
-                    tc::tmem_ld32(tm + kTmS + lane_base(warp) + part * 32, x);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) a.S_final[doc_state + (size_t)(part * 32 + k) * kDim] = x[k];
-                }
-                tc::tc_fence_before();
+                add_products(S, all, d_col);
             }
+            if (sg.last && a.S_final) store_column(S, a.S_final + ((size_t)sg.doc * a.H + h) * kDim * kDim + dv);
         }
     } else if (warp < 16) {
         // ---- O
-        const int dv = (warp & 3) * 32 + lane;
-        const float weight = GATE && a.fu.weight ? a.fu.weight[dv] : 1.f;
+        const int dim = (warp & 3) * 32, c2 = (lane & 3) * 2;
+        float2 weight[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)};  // of dimensions dim + 16 h + lane / 4 and 8 on
+        if (GATE && a.fu.weight)
+            for (int h = 0; h < 2; ++h)
+                weight[h] = make_float2(a.fu.weight[dim + 16 * h + (lane >> 2)], a.fu.weight[dim + 16 * h + 8 + (lane >> 2)]);
         FOR_SEGMENTS
         uint8_t *tile = sm + kOutO + st * kTile;
         WAIT(sh.gfull[n % kRing], n / kRing);
@@ -472,60 +585,93 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         {
             const Gates &g = sh.gates[n % kRing];
             const uint32_t t1 = tm + kTmO + (n & 1) * 64 + lane_base(warp), t2 = tm + kTmP + (n & 1) * 64 + lane_base(warp);
-            __nv_bfloat16 *col = reinterpret_cast<__nv_bfloat16 *>(tile) + dv;
-            if constexpr (!GATE) {
+            uint32_t to[2] = {tc::smem_u32(tile) + tile_lane(dim), tc::smem_u32(tile) + tile_lane(dim + 16)};
+            // o of 16 tokens and 32 value dimensions from its two parts, two fragments of 16 x 8 for each 16 dimensions
+            const auto part = [&](int i, float2 (&z)[2][4]) {
+                float x[2][8], y[2][8];
+                tc::tmem_ld_16x16x4(t1 + i, t2 + i, x, y);
 #pragma unroll
-                for (int part = 0; part < 4; ++part) {
-                    float x[16], y[16];
-                    tc::tmem_ld16x2(t1 + part * 16, t2 + part * 16, x, y);
+                for (int f = 0; f < 2; ++f) {
+                    const float2 in = *reinterpret_cast<const float2 *>(&g.in[i + 8 * f + c2]);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const int i = part * 16 + k;
-                        float z = fmaf(g.in[i], x[k], y[k]);
-                        if (NORM) z *= g.rq[i];
-                        col[i * kDim] = __float2bfloat16_rn(z);
+                    for (int e = 0; e < 4; ++e) {
+                        const int h = e >> 1, at = 4 * f + 2 * (e & 1);
+                        z[h][2 * f + (e & 1)] = tc::fma2(in, make_float2(x[h][at], x[h][at + 1]), make_float2(y[h][at], y[h][at + 1]));
                     }
+                    if (NORM) {
+                        const float2 rq = *reinterpret_cast<const float2 *>(&g.rq[i + 8 * f + c2]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) z[e >> 1][2 * f + (e & 1)] = tc::mul2(z[e >> 1][2 * f + (e & 1)], rq);
+                    }
+                }
+            };
+            const auto put = [&](const float2 (&z)[2][4]) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t u[4] = {pack_bf16(z[h][0].x, z[h][0].y), pack_bf16(z[h][1].x, z[h][1].y), pack_bf16(z[h][2].x, z[h][2].y),
+                                           pack_bf16(z[h][3].x, z[h][3].y)};
+                    tc::stmatrix_t4(to[h], u);
+                    to[h] += 2048;
+                }
+            };
+            if (!GATE) {
+#pragma unroll 1
+                for (int i = 0; i < kC; i += 16) {
+                    float2 z[2][4];
+                    part(i, z);
+                    put(z);
                 }
                 tc::tc_fence_before();
                 warp_arrive(&sh.ofree[n & 1]);
             } else {
-                float z[kC], sq[kC];
+                // all of o is taken to registers, so that the next chunk's products can follow
+                float2 z[4][2][4];
 #pragma unroll
-                for (int part = 0; part < 4; ++part) {
-                    float x[16], y[16];
-                    tc::tmem_ld16x2(t1 + part * 16, t2 + part * 16, x, y);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const int i = part * 16 + k;
-                        z[i] = fmaf(g.in[i], x[k], y[k]);
-                        if (NORM) z[i] *= g.rq[i];
-                        sq[i] = z[i] * z[i];
-                    }
-                }
+                for (int t = 0; t < 4; ++t) part(16 * t, z[t]);
                 tc::tc_fence_before();
                 warp_arrive(&sh.ofree[n & 1]);
-                // sums over the warp's 32 value dimensions: each exchange halves the tokens that a lane holds
+                // sums of squares over the value dimension: over a thread's four, its warp's 32 (each exchange leaves a
+                // lane half of the tokens), and the four warps'
 #pragma unroll
-                for (int half = 32; half >= 2; half >>= 1) {
-                    const bool up = lane & (half >> 1);
+                for (int t = 0; t < 4; ++t) {
+                    float2 sq[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int i = 0; i < half; ++i) {
-                        const float give = up ? sq[i] : sq[i + half], keep = up ? sq[i + half] : sq[i];
-                        sq[i] = keep + __shfl_xor_sync(0xffffffffu, give, half >> 1);
-                    }
+                    for (int e = 0; e < 8; ++e) sq[(e & 3) >> 1] = tc::fma2(z[t][e >> 2][e & 3], z[t][e >> 2][e & 3], sq[(e & 3) >> 1]);
+                    const bool up1 = lane & 4, up2 = lane & 8;
+                    float2 x = up1 ? sq[1] : sq[0];
+                    const float2 give = up1 ? sq[0] : sq[1];
+                    x.x += __shfl_xor_sync(0xffffffffu, give.x, 4);
+                    x.y += __shfl_xor_sync(0xffffffffu, give.y, 4);
+                    float y = up2 ? x.y : x.x;
+                    y += __shfl_xor_sync(0xffffffffu, up2 ? x.x : x.y, 8);
+                    y += __shfl_xor_sync(0xffffffffu, y, 16);
+                    if (lane < 16) sh.red[warp & 3][16 * t + (up1 ? 8 : 0) + c2 + (up2 ? 1 : 0)] = y;
                 }
-                // lane's bits 4..0 chose halves of 64, 32, 16, 8, 4 tokens: it holds tokens 2 lane and 2 lane + 1
-                sh.red[warp & 3][2 * lane] = sq[0];
-                sh.red[warp & 3][2 * lane + 1] = sq[1];
                 tc::named_barrier(2, 128);
                 if (threadIdx.x - 384 < kC) {
                     const int i = threadIdx.x - 384;
                     sh.rms[i] = rsqrtf(((sh.red[0][i] + sh.red[1][i]) + (sh.red[2][i] + sh.red[3][i])) * (1.f / kDim) + a.fu.out_eps);
                 }
                 tc::named_barrier(2, 128);
+#pragma unroll 1
+                for (int i = 0; i < kC; i += 16) {
+                    const float2 r[2] = {*reinterpret_cast<const float2 *>(&sh.rms[i + c2]), *reinterpret_cast<const float2 *>(&sh.rms[i + 8 + c2])};
 #pragma unroll
-                for (int i = 0; i < kC; ++i)
-                    col[i * kDim] = __float2bfloat16_rn(z[i] * sh.rms[i] * weight * sigmoidf(__bfloat162float(col[i * kDim])));
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t gate[4];
+                        tc::ldmatrix_t4(to[h], gate);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 x = tc::mul2(make_float2(bf16_lo(gate[e]), bf16_hi(gate[e])), make_float2(-linear::kLog2e, -linear::kLog2e));
+                            const float2 y = tc::add2(make_float2(ex2(x.x), ex2(x.y)), make_float2(1.f, 1.f));
+                            const float w = e & 1 ? weight[h].y : weight[h].x;
+                            z[0][h][e] = tc::mul2(tc::mul2(z[0][h][e], make_float2(rcp(y.x), rcp(y.y))), tc::mul2(r[e >> 1], make_float2(w, w)));
+                        }
+                    }
+                    put(z[0]);
+#pragma unroll
+                    for (int e = 0; e < 24; ++e) z[e / 8][e / 4 % 2][e % 4] = z[e / 8 + 1][e / 4 % 2][e % 4];  // the next 16 tokens'
+                }
             }
         }
         if (lane == 0) tc::mbar_arrive(&sh.gempty[n % kRing]);
@@ -534,56 +680,28 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         if (rows == kC) {
             if (threadIdx.x == 384) {
                 tc::tma_store_3d(&tm_o, 0, h, t0, tile);
+                tc::tma_store_3d(&tm_o, 64, h, t0, tile + 8192);
                 tc::bulk_commit();
                 tc::bulk_wait_read();
                 tc::mbar_arrive(&sh.zfree[st]);
             }
         } else {
-            for (int i = threadIdx.x - 384; i < rows * 16; i += 128)
-                reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + ((size_t)(t0 + (i >> 4)) * a.H + h) * kDim)[i & 15] =
-                    reinterpret_cast<const uint4 *>(tile)[i];
+#pragma unroll 1
+            for (int i = threadIdx.x - 384; i < rows * 16; i += 128) {
+                const int t = i >> 4, c = i & 15;
+                reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + ((size_t)(t0 + t) * a.H + h) * kDim)[c] =
+                    *reinterpret_cast<const uint4 *>(tile + (c >> 3) * 8192 + t * 128 + (((c & 7) ^ (t & 7)) << 4));
+            }
             tc::fence_async_smem();
             tc::named_barrier(2, 128);
             if (threadIdx.x == 384) tc::mbar_arrive(&sh.zfree[st]);
         }
         __syncwarp();
         END_SEGMENTS
-    } else if (warp == 16) {
-        // ---- decays
-        FOR_SEGMENTS
-        Gates &g = sh.gates[n % kRing];
-        const int j = 2 * lane;
-        float x0 = 0.f, x1 = 0.f;
-        if (a.per_token) {
-            if (j < rows) x0 = linear::log2_decay(a.g[(size_t)(t0 + j) * a.H + h]);
-            if (j + 1 < rows) x1 = linear::log2_decay(a.g[(size_t)(t0 + j + 1) * a.H + h]);
-        } else {
-            const float x = linear::log2_decay(a.g[h]);
-            if (j < rows) x0 = x;
-            if (j + 1 < rows) x1 = x;
-        }
-        const Sums s = chunk_sums(x0, x1);
-        if (n >= kRing) WAIT(sh.gempty[n % kRing], n / kRing - 1);
-        {
-            const float2 hi = make_float2((float)s.b0, (float)s.b1);
-            reinterpret_cast<float2 *>(g.b_hi)[lane] = hi;
-            reinterpret_cast<float2 *>(g.b_lo)[lane] = make_float2((float)(s.b0 - (double)hi.x), (float)(s.b1 - (double)hi.y));
-            reinterpret_cast<float2 *>(g.in)[lane] = make_float2(exp2f(hi.x), exp2f(hi.y));
-            reinterpret_cast<float2 *>(g.out)[lane] = make_float2(exp2f((float)(s.all - s.b0)), exp2f((float)(s.all - s.b1)));
-            if (lane == 0) g.all = exp2f((float)s.all);
-        }
-        warp_arrive(&sh.gfull[n % kRing]);
-        END_SEGMENTS
-    } else if (NORM) {
-        // ---- norms of q (warp 17) and k (warp 18)
-        FOR_SEGMENTS
-        WAIT(sh.full[st], n / 3);
-        if (n >= kRing) WAIT(sh.gempty[n % kRing], n / kRing - 1);
-        Gates &g = sh.gates[n % kRing];
-        row_norms(sm + st * kStage + (warp - 17) * kTile, a.fu.qk_eps, warp == 17 ? g.rq : g.rk);
-        warp_arrive(&sh.gfull[n % kRing]);
-        END_SEGMENTS
     }
+    goto done;
+died:
+    sh.dead = 1;
 done:
     __syncwarp();
     if (warp == 3) {  // every MMA done before the tensor memory goes
@@ -608,18 +726,18 @@ done:
 
 // ---------------------------------------------------------------------------
 // What each segment but a document's last adds to the state by its end, S^T = sum_j 2^(b_end - b_j) v_j k_j^T.  The
-// chunks are taken from the last to the first, so that every weight is known when its chunk is reached and the sum in
-// tensor memory is never rescaled; it also leaves the segment's first rows in L2 for the pass that forms the outputs.
+// chunks are taken from the last to the first, so that every weight is known when its chunk is reached and the sum is
+// never rescaled; it also leaves the segment's first rows in L2 for the pass that forms the outputs.
 // Only k and v are read: 512 bytes a token and head.
-//     warp 0  copies   warp 1  MMAs   warp 2  decays   warp 3  norms of k   warps 4-7, 8-11  V' of every other chunk
-//     warps 12-15  the finished sums to memory
+//     warp 0  copies, decays   warp 1  MMAs   warps 4-7, 8-11  V' (and norms of k) of every other chunk
+//     warps 12-15  the sums over the chunks, in registers
 // ---------------------------------------------------------------------------
 constexpr int kSegStages = 6;
 struct SegShared {
     Gates gates[kRing];
     uint64_t full[kSegStages], empty[kSegStages];
     uint64_t gfull[kRing], gempty[kRing];
-    uint64_t vready[2], vfree[2], sfull[2], sfree[2], drain;
+    uint64_t vready[2], vfree[2], dfull[2], dfree[2], drain;
     uint32_t tmem;
     volatile int dead;
 };
@@ -628,6 +746,7 @@ constexpr int kSegShared = kSegStages * kSegStage;
 constexpr int kSegSmem = kSegShared + (int)sizeof(SegShared) + 1024;
 static_assert(kSegSmem <= 232448, "shared memory of a CTA");
 constexpr int kSegThreads = 16 * 32;
+constexpr int kSegOthers = 104, kSegSums = 184, kSegRegs = 128 * (3 * kSegOthers + kSegSums);
 
 template <bool NORM>
 __global__ void __launch_bounds__(kSegThreads, 1)
@@ -642,14 +761,14 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             tc::mbar_init(&sh.empty[i], 1);
         }
         for (int i = 0; i < kRing; ++i) {
-            tc::mbar_init(&sh.gfull[i], NORM ? 2 : 1);
+            tc::mbar_init(&sh.gfull[i], NORM ? 5 : 1);
             tc::mbar_init(&sh.gempty[i], 4);
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&sh.vready[i], 4);
             tc::mbar_init(&sh.vfree[i], 1);
-            tc::mbar_init(&sh.sfull[i], 1);
-            tc::mbar_init(&sh.sfree[i], 4);
+            tc::mbar_init(&sh.dfull[i], 1);
+            tc::mbar_init(&sh.dfree[i], 4);
         }
         tc::mbar_init(&sh.drain, 1);
         sh.dead = 0;
@@ -665,7 +784,7 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const bool valid = linear::valid_table(a.cu, a.num_seqs, a.total);  // also the barrier behind the set-up
     tc::tc_fence_after();
     if (a.first && blockIdx.x == 0 && threadIdx.x == 0) *a.status = valid ? (int32_t)KDA_OK : (int32_t)KDA_ERR_INVALID_ARG;
-    const uint32_t tm = sh.tmem, tm_vhi = tm + 256, tm_vlo = tm + 288;  // sums at 0 and 128, V' at 256 and 320
+    const uint32_t tm = sh.tmem, tm_vhi = tm + 256, tm_vlo = tm + 288;  // V'^T K at 0 and 128, V' at 256 and 320
     const int units = valid ? a.slots * a.H : 0;
     const int share = a.H / a.Hqk;
 
@@ -679,9 +798,14 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         for (int c0 = sg.len - kC; c0 >= 0; c0 -= kC, ++n) {                                                   \
             [[maybe_unused]] const int t0 = sg.t0 + c0, st = n % kSegStages, b = n & 1;
 
-    int n = 0, m = 0;  // chunks and segments so far
+    if (warp < 12) fewer_registers<kSegOthers>();
+    int n = 0;  // chunks so far
     if (warp == 0) {
+        // copies and decays; a chunk's decays are read while the one before it is worked on
+        float g0 = 0.f, g1 = 0.f;
         FOR_FULL_SEGMENTS
+        long long later = 0;  // the log-decays of the chunks behind this one, held short of overflow
+        bool nan = false;
         FOR_CHUNKS
         if (n >= kSegStages) WAIT(sh.empty[st], n / kSegStages - 1);
         if (lane == 0) {
@@ -692,85 +816,79 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 tc::tma_load_3d(to + kTile + p * 8192, &tm_v, p * 64, h, t0, &sh.full[st]);
             }
         }
-        END_SEGMENTS
+        const auto fetch = [&](int t) {
+            const float *p = a.per_token ? a.g + (size_t)(t + 2 * lane) * a.H + h : a.g + h;
+            g0 = *p;
+            g1 = p[a.per_token ? a.H : 0];
+        };
+        if (c0 == sg.len - kC) fetch(t0);
+        Gates &g = sh.gates[n % kRing];
+        const float x0 = linear::log2_decay(g0), x1 = linear::log2_decay(g1);
+        if (c0 > 0) fetch(t0 - kC);
+        const Sums s = chunk_sums(x0, x1);
+        if (n >= kRing) WAIT(sh.gempty[n % kRing], n / kRing - 1);
+        reinterpret_cast<float2 *>(g.out)[lane] =
+            nan ? make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff))
+                : make_float2(ex2(from_fixed(later + (s.all - s.b0))), ex2(from_fixed(later + (s.all - s.b1))));
+        later = min(max(later + s.all, -(1ll << 60)), 1ll << 60);
+        nan = nan || s.nan;
+        warp_arrive(&sh.gfull[n % kRing]);
+        }
+        if (lane == 0) a.seg_decay[(size_t)slot * a.H + h] = nan ? __int_as_float(0x7fffffff) : exp2f(from_fixed(later));
+        }
     } else if (warp == 1) {
         const bool one = tc::elect_one();
         FOR_FULL_SEGMENTS
-        if (m >= 2) WAIT(sh.sfree[m & 1], m / 2 - 1);
         FOR_CHUNKS
         WAIT(sh.full[st], n / kSegStages);
         WAIT(sh.vready[b], n / 2);
+        if (n >= 2) WAIT(sh.dfree[b], n / 2 - 1);
         tc::tc_fence_after();
-        mma_state(tm + (m & 1) * 128, tm_vhi + b * 64, tm_vlo + b * 64, sm + st * kSegStage, c0 + kC < sg.len, one);
+        mma_state(tm + b * 128, tm_vhi + b * 64, tm_vlo + b * 64, sm + st * kSegStage, one);
         if (one) {
             tc::mma_commit(&sh.empty[st]);
             tc::mma_commit(&sh.vfree[b]);
-            if (c0 == 0) tc::mma_commit(&sh.sfull[m & 1]);
+            tc::mma_commit(&sh.dfull[b]);
         }
         __syncwarp();
-        }
-        ++m;
-        }
-    } else if (warp == 2) {
-        FOR_FULL_SEGMENTS
-        double later = 0.0;  // the log-decays of the chunks behind this one
-        FOR_CHUNKS
-        Gates &g = sh.gates[n % kRing];
-        float x0, x1;
-        if (a.per_token) {
-            x0 = linear::log2_decay(a.g[(size_t)(t0 + 2 * lane) * a.H + h]);
-            x1 = linear::log2_decay(a.g[(size_t)(t0 + 2 * lane + 1) * a.H + h]);
-        } else {
-            x0 = x1 = linear::log2_decay(a.g[h]);
-        }
-        const Sums s = chunk_sums(x0, x1);
-        if (n >= kRing) WAIT(sh.gempty[n % kRing], n / kRing - 1);
-        reinterpret_cast<float2 *>(g.out)[lane] = make_float2(exp2f((float)(later + (s.all - s.b0))), exp2f((float)(later + (s.all - s.b1))));
-        later += s.all;
-        warp_arrive(&sh.gfull[n % kRing]);
-        }
-        if (lane == 0) a.seg_decay[(size_t)slot * a.H + h] = exp2f((float)later);
-        }
-    } else if (warp == 3) {
-        if (NORM) {
-            FOR_FULL_SEGMENTS
-            FOR_CHUNKS
-            WAIT(sh.full[st], n / kSegStages);
-            if (n >= kRing) WAIT(sh.gempty[n % kRing], n / kRing - 1);
-            row_norms(sm + st * kSegStage, a.fu.qk_eps, sh.gates[n % kRing].rk);
-            warp_arrive(&sh.gfull[n % kRing]);
-            END_SEGMENTS
-        }
+        END_SEGMENTS
+    } else if (warp < 4) {
     } else if (warp < 12) {
         const int group = (warp >> 2) - 1;
         FOR_FULL_SEGMENTS
         FOR_CHUNKS
         if (b != group) continue;
         WAIT(sh.full[st], n / kSegStages);
+        if (NORM) {
+            if (n >= kRing) WAIT(sh.gempty[n % kRing], n / kRing - 1);
+            row_norms(sm + st * kSegStage, (warp & 3) * 16, a.fu.qk_eps, sh.gates[n % kRing].rk);
+            warp_arrive(&sh.gfull[n % kRing]);
+        }
         WAIT(sh.gfull[n % kRing], n / kRing);
         if (n >= 2) WAIT(sh.vfree[b], n / 2 - 1);
         tc::tc_fence_after();
-        decayed_values<NORM>(sm + st * kSegStage + kTile, sh.gates[n % kRing], kC, warp, tm_vhi + b * 64, tm_vlo + b * 64);
+        decayed_values<NORM>(sm + st * kSegStage + kTile, sh.gates[n % kRing], warp, tm_vhi + b * 64, tm_vlo + b * 64);
         warp_arrive(&sh.vready[b]);
         if (lane == 0) tc::mbar_arrive(&sh.gempty[n % kRing]);
         END_SEGMENTS
-    } else {
+    } else if (warp < 16) {
+        more_registers<kSegSums>();
         FOR_FULL_SEGMENTS
-        WAIT(sh.sfull[m & 1], m / 2);
-        tc::tc_fence_after();
-        float *to = a.seg_state + ((size_t)slot * a.H + h) * kDim * kDim + (warp & 3) * 32 + lane;
-#pragma unroll 1
-        for (int part = 0; part < 4; ++part) {
-            float x[32];
-            tc::tmem_ld32(tm + (m & 1) * 128 + lane_base(warp) + part * 32, x);
+        float2 S[kDim / 2];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) to[(size_t)(part * 32 + k) * kDim] = x[k];
+        for (int k = 0; k < kDim / 2; ++k) S[k] = make_float2(0.f, 0.f);
+        FOR_CHUNKS
+        WAIT(sh.dfull[b], n / 2);
+        tc::tc_fence_after();
+        add_products(S, make_float2(1.f, 1.f), tm + b * 128 + lane_base(warp));
+        warp_arrive(&sh.dfree[b]);
         }
-        tc::tc_fence_before();
-        warp_arrive(&sh.sfree[m & 1]);
-        ++m;
+        store_column(S, a.seg_state + ((size_t)slot * a.H + h) * kDim * kDim + (warp & 3) * 32 + lane);
         }
     }
+    goto done;
+died:
+    sh.dead = 1;
 done:
     __syncwarp();
     if (warp == 1) {
@@ -805,28 +923,39 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// [total, heads, 128] bf16 tensor in boxes of a chunk's tokens of one head: halves of 64 channels with the 128-byte
-// swizzle (operands of MMAs), or whole rows as they are (the output, and the gate).
-bool make_map(CUtensorMap *map, const void *base, int total, int heads, bool operand) {
+// [total, heads, 128] bf16 tensor in boxes of 64 channels of one head of a chunk's tokens, 128-byte swizzle.
+bool make_map(CUtensorMap *map, const void *base, int total, int heads) {
     auto fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[3] = {(cuuint64_t)kDim, (cuuint64_t)heads, (cuuint64_t)total};
     cuuint64_t strides[2] = {(cuuint64_t)kDim * 2, (cuuint64_t)heads * kDim * 2};
-    cuuint32_t box[3] = {operand ? 64u : (cuuint32_t)kDim, 1, (cuuint32_t)kC};
+    cuuint32_t box[3] = {64, 1, (cuuint32_t)kC};
     cuuint32_t estr[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, operand ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Whether a kernel was built with the registers that its warpgroups share out.
+template <auto Kernel>
+cudaError_t enough_registers(int threads, int wanted) {
+    static const int regs = [] {
+        cudaFuncAttributes at;
+        return cudaFuncGetAttributes(&at, Kernel) == cudaSuccess ? (at.numRegs + 7) / 8 * 8 : 0;
+    }();
+    return regs * threads >= wanted ? cudaSuccess : cudaErrorInvalidConfiguration;
 }
 
 template <bool NORM, bool GATE>
 cudaError_t launch_out(const CUtensorMap *m, const Args &a, int grid, cudaStream_t st) {
-    const cudaError_t e = allow_smem<linear_out_tc<NORM, GATE>>(kOutSmem);
+    cudaError_t e = enough_registers<linear_out_tc<NORM, GATE>>(kOutThreads, kOutRegs);
+    if (e == cudaSuccess) e = allow_smem<linear_out_tc<NORM, GATE>>(kOutSmem);
     return e != cudaSuccess ? e : launch_dependent(linear_out_tc<NORM, GATE>, dim3(grid), dim3(kOutThreads), kOutSmem, st, m[0], m[1], m[2], m[3], m[4], a);
 }
 template <bool NORM>
 cudaError_t launch_segment(const CUtensorMap *m, const Args &a, int grid, cudaStream_t st) {
-    const cudaError_t e = allow_smem<linear_segment_tc<NORM>>(kSegSmem);
+    cudaError_t e = enough_registers<linear_segment_tc<NORM>>(kSegThreads, kSegRegs);
+    if (e == cudaSuccess) e = allow_smem<linear_segment_tc<NORM>>(kSegSmem);
     return e != cudaSuccess ? e : launch_dependent(linear_segment_tc<NORM>, dim3(grid), dim3(kSegThreads), kSegSmem, st, m[1], m[2], a);
 }
 
@@ -836,12 +965,9 @@ cudaError_t launch_linear_tc(const linear::Args &args, cudaStream_t st) {
     Args a = args;
     CUtensorMap m[5];
     // (a map of an empty tensor cannot be made; with no tokens nothing is copied and any map will do)
-    const int rows = a.total > 0 ? a.total : 1;
-    if (a.total > 0) {
-        if (!make_map(&m[0], a.q, rows, a.Hqk, true) || !make_map(&m[1], a.k, rows, a.Hqk, true) || !make_map(&m[2], a.v, rows, a.H, true) ||
-            !make_map(&m[3], a.o, rows, a.H, false) || !make_map(&m[4], a.fu.gate ? a.fu.gate : a.o, rows, a.H, false))
-            return cudaErrorInvalidValue;
-    }
+    if (a.total > 0 && (!make_map(&m[0], a.q, a.total, a.Hqk) || !make_map(&m[1], a.k, a.total, a.Hqk) || !make_map(&m[2], a.v, a.total, a.H) ||
+                        !make_map(&m[3], a.o, a.total, a.H) || !make_map(&m[4], a.fu.gate ? a.fu.gate : a.o, a.total, a.H)))
+        return cudaErrorInvalidValue;
     int sms = 0;
     cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;
