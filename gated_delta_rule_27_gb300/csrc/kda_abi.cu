@@ -433,7 +433,7 @@ static kda_status linear_check(int32_t rows, int32_t H, int32_t H_qk, int32_t d_
 static kda_status linear_plan(int32_t total_tokens, int32_t num_seqs, int32_t H, int32_t d, int32_t *seg, int32_t *slots,
                               kda::linear::Layout *lay) {
     if (num_seqs < 0) return KDA_ERR_INVALID_ARG;
-    *seg = kda::linear::plan_segment(total_tokens, H);
+    *seg = kda::linear::plan_segment(total_tokens, num_seqs, H);
     const int64_t n = total_tokens / *seg + (int64_t)num_seqs;
     if (n * H > INT_MAX) return KDA_ERR_UNSUPPORTED;
     *slots = (int32_t)n;

@@ -16,6 +16,7 @@ using linear::Segment;
 
 constexpr int kTok = 16;    // tokens staged at once
 constexpr int kSplit = 4;   // threads of a column
+constexpr float kGentle = 24.f;  // largest log2 of a decay over kTok tokens that the state's units may follow
 
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
@@ -30,7 +31,8 @@ linear_simt_kernel(const Args a) {
     constexpr int NT = D * kSplit, R = D / kSplit, kWarps = NT / 32;
     constexpr int kLoads = kTok * D / NT;  // elements of a staged tensor a thread loads
     __shared__ __align__(16) float s_q[kTok][D], s_k[kTok][D], s_v[kTok][D], s_o[OUT ? kTok : 1][D];
-    __shared__ float s_a[kTok];
+    __shared__ float s_a[kTok], s_in[kTok], s_out[kTok];
+    __shared__ bool s_gentle;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int col = tid / kSplit, part = tid % kSplit;  // rows 4 (i kSplit + part) .. + 3 for i < R / 4
     tc::grid_dep_launch();
@@ -79,10 +81,25 @@ linear_simt_kernel(const Args a) {
             s_k[i / D][i % D] = to_f32(nk[e]);
             s_v[i / D][i % D] = to_f32(nv[e]);
         }
-        if (tid < n) s_a[tid] = exp2f(ng);
-        if (!OUT && tid < 32) {
-            float x = tid < n ? ng : 0.f;
-            total += (double)warp_sum(x);
+        if (tid < 32) {  // the decays' sums from the first staged token on
+            float b = tid < n ? ng : 0.f;
+#pragma unroll
+            for (int off = 1; off < kTok; off <<= 1) {
+                const float up = __shfl_up_sync(0xffffffffu, b, off);
+                if (tid >= off) b += up;
+            }
+            const float all = __shfl_sync(0xffffffffu, b, kTok - 1);
+            total += (double)all;
+            float most = fabsf(b);  // (growth and decay may cancel in the whole)
+#pragma unroll
+            for (int off = 16; off; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+            const bool nan = __any_sync(0xffffffffu, b != b);
+            if (tid < kTok) {
+                s_a[tid] = exp2f(ng);
+                s_in[tid] = exp2f(b);
+                s_out[tid] = exp2f(-b);
+            }
+            if (tid == 0) s_gentle = !nan && most < kGentle;
         }
         __syncthreads();
         if (c0 + kTok < sg.len) fetch(c0 + kTok);
@@ -96,25 +113,56 @@ linear_simt_kernel(const Args a) {
             }
             __syncthreads();
         }
-        for (int t = 0; t < n; ++t) {
-            const float2 av = make_float2(s_a[t], s_a[t]), vv = make_float2(s_v[t][col], s_v[t][col]);
-            float2 acc = make_float2(0.f, 0.f);
+        // The state is kept in units of the decay since the first of these tokens, where that is not so strong that the
+        // units overflow: it saves the product with each token's decay, and the rounding of that decay, which a slow one
+        // would pile up token after token.
+        if (s_gentle) {
+            for (int t = 0; t < n; ++t) {
+                const float vo = s_v[t][col] * s_out[t];
+                const float2 vv = make_float2(vo, vo);
+                float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < R / 4; ++i) {
-                const float4 kk = *reinterpret_cast<const float4 *>(&s_k[t][4 * (i * kSplit + part)]);
-                S[2 * i] = tc::fma2(make_float2(kk.x, kk.y), vv, tc::mul2(av, S[2 * i]));
-                S[2 * i + 1] = tc::fma2(make_float2(kk.z, kk.w), vv, tc::mul2(av, S[2 * i + 1]));
+                for (int i = 0; i < R / 4; ++i) {
+                    const float4 kk = *reinterpret_cast<const float4 *>(&s_k[t][4 * (i * kSplit + part)]);
+                    S[2 * i] = tc::fma2(make_float2(kk.x, kk.y), vv, S[2 * i]);
+                    S[2 * i + 1] = tc::fma2(make_float2(kk.z, kk.w), vv, S[2 * i + 1]);
+                    if (OUT) {
+                        const float4 qq = *reinterpret_cast<const float4 *>(&s_q[t][4 * (i * kSplit + part)]);
+                        acc = tc::fma2(make_float2(qq.x, qq.y), S[2 * i], acc);
+                        acc = tc::fma2(make_float2(qq.z, qq.w), S[2 * i + 1], acc);
+                    }
+                }
                 if (OUT) {
-                    const float4 qq = *reinterpret_cast<const float4 *>(&s_q[t][4 * (i * kSplit + part)]);
-                    acc = tc::fma2(make_float2(qq.x, qq.y), S[2 * i], acc);
-                    acc = tc::fma2(make_float2(qq.z, qq.w), S[2 * i + 1], acc);
+                    float x = acc.x + acc.y;
+                    x += __shfl_xor_sync(0xffffffffu, x, 1);
+                    x += __shfl_xor_sync(0xffffffffu, x, 2);
+                    if (part == 0) s_o[t][col] = x * s_in[t];
                 }
             }
-            if (OUT) {
-                float x = acc.x + acc.y;
-                x += __shfl_xor_sync(0xffffffffu, x, 1);
-                x += __shfl_xor_sync(0xffffffffu, x, 2);
-                if (part == 0) s_o[t][col] = x;
+            const float2 end = make_float2(s_in[n - 1], s_in[n - 1]);
+#pragma unroll
+            for (int i = 0; i < R / 2; ++i) S[i] = tc::mul2(S[i], end);
+        } else {
+            for (int t = 0; t < n; ++t) {
+                const float2 av = make_float2(s_a[t], s_a[t]), vv = make_float2(s_v[t][col], s_v[t][col]);
+                float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < R / 4; ++i) {
+                    const float4 kk = *reinterpret_cast<const float4 *>(&s_k[t][4 * (i * kSplit + part)]);
+                    S[2 * i] = tc::fma2(make_float2(kk.x, kk.y), vv, tc::mul2(av, S[2 * i]));
+                    S[2 * i + 1] = tc::fma2(make_float2(kk.z, kk.w), vv, tc::mul2(av, S[2 * i + 1]));
+                    if (OUT) {
+                        const float4 qq = *reinterpret_cast<const float4 *>(&s_q[t][4 * (i * kSplit + part)]);
+                        acc = tc::fma2(make_float2(qq.x, qq.y), S[2 * i], acc);
+                        acc = tc::fma2(make_float2(qq.z, qq.w), S[2 * i + 1], acc);
+                    }
+                }
+                if (OUT) {
+                    float x = acc.x + acc.y;
+                    x += __shfl_xor_sync(0xffffffffu, x, 1);
+                    x += __shfl_xor_sync(0xffffffffu, x, 2);
+                    if (part == 0) s_o[t][col] = x;
+                }
             }
         }
         __syncthreads();

@@ -728,16 +728,19 @@ done:
 // What each segment but a document's last adds to the state by its end, S^T = sum_j 2^(b_end - b_j) v_j k_j^T.  The
 // chunks are taken from the last to the first, so that every weight is known when its chunk is reached and the sum is
 // never rescaled; it also leaves the segment's first rows in L2 for the pass that forms the outputs.
-// Only k and v are read: 512 bytes a token and head.
-//     warp 0  copies, decays   warp 1  MMAs   warps 4-7, 8-11  V' (and norms of k) of every other chunk
+// Only k and v are read: 512 bytes a token and head; and only as far back as weights above 2^-192: fp32 holds no state that
+// a weight below that leaves anything of.
+//     warp 0  copies   warp 1  MMAs   warp 2  decays   warps 4-7, 8-11  V' (and norms of k) of every other chunk
 //     warps 12-15  the sums over the chunks, in registers
 // ---------------------------------------------------------------------------
-constexpr int kSegStages = 6;
+constexpr int kSegStages = 6, kTold = 8;
 struct SegShared {
     Gates gates[kRing];
     uint64_t full[kSegStages], empty[kSegStages];
     uint64_t gfull[kRing], gempty[kRing];
     uint64_t vready[2], vfree[2], dfull[2], dfree[2], drain;
+    uint64_t told[kTold];  // whether a chunk is its segment's last one that counts
+    int stop[kTold];
     uint32_t tmem;
     volatile int dead;
 };
@@ -747,6 +750,8 @@ constexpr int kSegSmem = kSegShared + (int)sizeof(SegShared) + 1024;
 static_assert(kSegSmem <= 232448, "shared memory of a CTA");
 constexpr int kSegThreads = 16 * 32;
 constexpr int kSegOthers = 104, kSegSums = 184, kSegRegs = 128 * (3 * kSegOthers + kSegSums);
+
+constexpr long long kGone = -(192ll << 44);  // in the sums' fixed point
 
 template <bool NORM>
 __global__ void __launch_bounds__(kSegThreads, 1)
@@ -760,6 +765,7 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             tc::mbar_init(&sh.full[i], 1);
             tc::mbar_init(&sh.empty[i], 1);
         }
+        for (int i = 0; i < kTold; ++i) tc::mbar_init(&sh.told[i], 1);
         for (int i = 0; i < kRing; ++i) {
             tc::mbar_init(&sh.gfull[i], NORM ? 5 : 1);
             tc::mbar_init(&sh.gempty[i], 4);
@@ -801,12 +807,13 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     if (warp < 12) fewer_registers<kSegOthers>();
     int n = 0;  // chunks so far
     if (warp == 0) {
-        // copies and decays; a chunk's decays are read while the one before it is worked on
-        float g0 = 0.f, g1 = 0.f;
         FOR_FULL_SEGMENTS
-        long long later = 0;  // the log-decays of the chunks behind this one, held short of overflow
-        bool nan = false;
         FOR_CHUNKS
+        if (c0 + kC < sg.len) {
+            // (the decays are at most four chunks ahead of what has been copied: `told` goes round in eight)
+            WAIT(sh.told[(n - 1) % kTold], (n - 1) / kTold);
+            if (sh.stop[(n - 1) % kTold]) break;
+        }
         if (n >= kSegStages) WAIT(sh.empty[st], n / kSegStages - 1);
         if (lane == 0) {
             uint8_t *to = sm + st * kSegStage;
@@ -816,6 +823,31 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 tc::tma_load_3d(to + kTile + p * 8192, &tm_v, p * 64, h, t0, &sh.full[st]);
             }
         }
+        END_SEGMENTS
+    } else if (warp == 1) {
+        const bool one = tc::elect_one();
+        FOR_FULL_SEGMENTS
+        FOR_CHUNKS
+        WAIT(sh.full[st], n / kSegStages);
+        WAIT(sh.vready[b], n / 2);
+        if (n >= 2) WAIT(sh.dfree[b], n / 2 - 1);
+        tc::tc_fence_after();
+        mma_state(tm + b * 128, tm_vhi + b * 64, tm_vlo + b * 64, sm + st * kSegStage, one);
+        if (one) {
+            tc::mma_commit(&sh.empty[st]);
+            tc::mma_commit(&sh.vfree[b]);
+            tc::mma_commit(&sh.dfull[b]);
+        }
+        __syncwarp();
+        if (sh.stop[n % kTold]) c0 = 0;
+        END_SEGMENTS
+    } else if (warp == 2) {
+        // decays; a chunk's are read while the one before it is worked on
+        float g0 = 0.f, g1 = 0.f;
+        FOR_FULL_SEGMENTS
+        long long later = 0;  // the log-decays of the chunks behind this one, held short of overflow
+        bool nan = false;
+        FOR_CHUNKS
         const auto fetch = [&](int t) {
             const float *p = a.per_token ? a.g + (size_t)(t + 2 * lane) * a.H + h : a.g + h;
             g0 = *p;
@@ -832,32 +864,24 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 : make_float2(ex2(from_fixed(later + (s.all - s.b0))), ex2(from_fixed(later + (s.all - s.b1))));
         later = min(max(later + s.all, -(1ll << 60)), 1ll << 60);
         nan = nan || s.nan;
+        const bool stop = c0 == 0 || (!nan && later < kGone);
+        if (lane == 0) sh.stop[n % kTold] = stop;
         warp_arrive(&sh.gfull[n % kRing]);
+        if (lane == 0) tc::mbar_arrive(&sh.told[n % kTold]);
+        if (stop) c0 = 0;
         }
         if (lane == 0) a.seg_decay[(size_t)slot * a.H + h] = nan ? __int_as_float(0x7fffffff) : exp2f(from_fixed(later));
         }
-    } else if (warp == 1) {
-        const bool one = tc::elect_one();
-        FOR_FULL_SEGMENTS
-        FOR_CHUNKS
-        WAIT(sh.full[st], n / kSegStages);
-        WAIT(sh.vready[b], n / 2);
-        if (n >= 2) WAIT(sh.dfree[b], n / 2 - 1);
-        tc::tc_fence_after();
-        mma_state(tm + b * 128, tm_vhi + b * 64, tm_vlo + b * 64, sm + st * kSegStage, one);
-        if (one) {
-            tc::mma_commit(&sh.empty[st]);
-            tc::mma_commit(&sh.vfree[b]);
-            tc::mma_commit(&sh.dfull[b]);
-        }
-        __syncwarp();
-        END_SEGMENTS
-    } else if (warp < 4) {
+    } else if (warp == 3) {
     } else if (warp < 12) {
         const int group = (warp >> 2) - 1;
         FOR_FULL_SEGMENTS
         FOR_CHUNKS
-        if (b != group) continue;
+        if (b != group) {
+            WAIT(sh.told[n % kTold], n / kTold);
+            if (sh.stop[n % kTold]) c0 = 0;
+            continue;
+        }
         WAIT(sh.full[st], n / kSegStages);
         if (NORM) {
             if (n >= kRing) WAIT(sh.gempty[n % kRing], n / kRing - 1);
@@ -868,8 +892,10 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         if (n >= 2) WAIT(sh.vfree[b], n / 2 - 1);
         tc::tc_fence_after();
         decayed_values<NORM>(sm + st * kSegStage + kTile, sh.gates[n % kRing], warp, tm_vhi + b * 64, tm_vlo + b * 64);
+        const bool stop = sh.stop[n % kTold];
         warp_arrive(&sh.vready[b]);
         if (lane == 0) tc::mbar_arrive(&sh.gempty[n % kRing]);
+        if (stop) c0 = 0;
         END_SEGMENTS
     } else if (warp < 16) {
         more_registers<kSegSums>();
@@ -881,7 +907,9 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         WAIT(sh.dfull[b], n / 2);
         tc::tc_fence_after();
         add_products(S, make_float2(1.f, 1.f), tm + b * 128 + lane_base(warp));
+        const bool stop = sh.stop[n % kTold];
         warp_arrive(&sh.dfree[b]);
+        if (stop) c0 = 0;
         }
         store_column(S, a.seg_state + ((size_t)slot * a.H + h) * kDim * kDim + (warp & 3) * 32 + lane);
         }
