@@ -15,7 +15,8 @@
 //     warp 3       issues all MMAs
 //     warps 4-7    the norms of q and k (fused normalisation only); V': v times its decay, in two bf16 parts, to tensor memory (the A operand of the state's product)
 //     warps 8-11   S: the state, decayed and added to, and its bf16 copy (the A operand of S^T Q^T)
-//     warps 12-15  O: the two parts of o added, normalised, to shared memory and out by TMA
+//     warps 12-15  O: the two parts of o added, to shared memory and out by TMA; with the gated normalisation, which takes
+//                  twice as long, another four warps take every other chunk
 //
 // Roundings to bf16: P and the copy of S, which only reach o, itself rounded to bf16 (each adds an error of the size
 // of that rounding in its part of o).  V' reaches the state, which is fp32: it is taken in two parts (16 bits of 24).
@@ -90,8 +91,7 @@ struct __align__(16) Gates {
 
 struct OutShared {
     Gates gates[kRing];
-    float red[4][kC];
-    float rms[kC];
+    float red[2][4][kC], rms[2][kC];  // of the two groups of O
     uint64_t full[3], empty[3];           // q, k, v of a chunk
     uint64_t gfull[kRing], gempty[kRing];
     uint64_t fixed[2];                    // rows behind a segment cleared (turn by turn: V' can be a chunk ahead)
@@ -106,9 +106,15 @@ constexpr int kStage = 3 * kTile;
 constexpr int kOutP = 3 * kStage, kOutO = kOutP + 2 * 8192, kOutShared = kOutO + 3 * kTile;
 constexpr int kOutSmem = kOutShared + (int)sizeof(OutShared) + 1024;
 static_assert(kOutSmem <= 232448, "shared memory of a CTA");
-constexpr int kOutThreads = 16 * 32;
+template <bool GATE>
+constexpr int kOutThreads = GATE ? 640 : 512;
 // Registers a thread of each warpgroup, see more_registers.
-constexpr int kOutOthers = 104, kOutS = 200, kOutRegs = 128 * (3 * kOutOthers + kOutS);
+template <bool GATE>
+constexpr int kOutOthers = GATE ? 72 : 104;
+template <bool GATE>
+constexpr int kOutS = GATE ? 184 : 200;
+template <bool GATE>
+constexpr int kOutRegs = 128 * ((GATE ? 4 : 3) * kOutOthers<GATE> + kOutS<GATE>);
 
 // Tensor memory: V'^T K, S^T in bf16, V'^T in two parts, two buffers each of P (then V^T P^T) and S^T Q^T.
 enum : uint32_t { kTmD = 0, kTmSb = 128, kTmVhi = 192, kTmVlo = 224, kTmP = 256, kTmO = 384 };
@@ -283,7 +289,7 @@ __device__ __forceinline__ void add_products(float2 (&S)[kDim / 2], float2 all, 
 }
 
 template <bool NORM, bool GATE>
-__global__ void __launch_bounds__(kOutThreads, 1)
+__global__ void __launch_bounds__(kOutThreads<GATE>, 1)
 linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
               const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_z, const Args a) {
     extern __shared__ uint8_t smem_raw[];
@@ -344,7 +350,7 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     }
 
     int n = 0;  // chunks so far: each barrier's phase follows from it
-    if (warp < 8 || warp >= 12) fewer_registers<kOutOthers>();
+    if (warp < 8 || warp >= 12) fewer_registers<kOutOthers<GATE>>();
     if (warp == 2) {
         // ---- copies and decays; a chunk's decays are read while the one before it is worked on
         float g0 = 0.f, g1 = 0.f;
@@ -357,13 +363,6 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 tc::tma_load_3d(to + p * 8192, &tm_q, p * 64, h / share, t0, &sh.full[st]);
                 tc::tma_load_3d(to + kTile + p * 8192, &tm_k, p * 64, h / share, t0, &sh.full[st]);
                 tc::tma_load_3d(to + 2 * kTile + p * 8192, &tm_v, p * 64, h, t0, &sh.full[st]);
-            }
-        }
-        if (GATE) {
-            if (n >= 3) WAIT(sh.zfree[st], n / 3 - 1);
-            if (lane == 0) {
-                tc::mbar_arrive_expect_tx(&sh.zfull[st], kTile);
-                for (int p = 0; p < 2; ++p) tc::tma_load_3d(sm + kOutO + st * kTile + p * 8192, &tm_z, p * 64, h, t0, &sh.zfull[st]);
             }
         }
         const auto fetch = [&](int t, int count) {
@@ -386,6 +385,13 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             if (lane == 0) g.all = s.nan ? nan : exp2f(from_fixed(s.all));
         }
         warp_arrive(&sh.gfull[n % kRing]);
+        if (GATE) {
+            if (n >= 3) WAIT(sh.zfree[st], n / 3 - 1);
+            if (lane == 0) {
+                tc::mbar_arrive_expect_tx(&sh.zfull[st], kTile);
+                for (int p = 0; p < 2; ++p) tc::tma_load_3d(sm + kOutO + st * kTile + p * 8192, &tm_z, p * 64, h, t0, &sh.zfull[st]);
+            }
+        }
         END_SEGMENTS
     } else if (warp == 3) {
         // ---- MMAs, in the order in which they can start: V'^T K and S^T Q^T of a chunk, Q K^T of the next, whose scores are
@@ -421,36 +427,41 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 for (int p = 0; p < 2; ++p) mma_ts4(tm + kTmO + b * 64, tm + kTmSb + p * 32, qd + p * 512, 2, kId64, p, one);
                 if (one) tc::mma_commit(&sh.qs);
             }
-            if (more) {
-                const int st = n % 3;
-                WAIT(sh.full[st], n / 3);
-                if (left < kC) {
-                    WAIT(sh.fixed[fixes & 1], fixes >> 1);
-                    ++fixes;
-                }
-                left -= kC;
-                if (n >= 2) WAIT(sh.ofree[n & 1], n / 2 - 1);
-                tc::tc_fence_after();
-                const uint8_t *at = sm + st * kStage;
-                // (rows 64 to 127 of the result come of what follows the tile's half, and nobody reads them)
-                const uint64_t qd = tc::smem_desc(kKmajor, tc::smem_u32(at)), kd = tc::smem_desc(kKmajor, tc::smem_u32(at + kTile));
+            // the next Q K^T waits for the output that was in its place: a quick one is gone before P is there, while
+            // a gated one takes longer than P
+#pragma unroll
+            for (int turn = 0; turn < 2; ++turn) {
+                if (turn == (GATE ? 1 : 0) && more) {
+                    const int st = n % 3;
+                    WAIT(sh.full[st], n / 3);
+                    if (left < kC) {
+                        WAIT(sh.fixed[fixes & 1], fixes >> 1);
+                        ++fixes;
+                    }
+                    left -= kC;
+                    if (n >= 2) WAIT(sh.ofree[n & 1], n / 2 - 1);
+                    tc::tc_fence_after();
+                    const uint8_t *at = sm + st * kStage;
+                    // (rows 64 to 127 of the result come of what follows the tile's half, and nobody reads them)
+                    const uint64_t qd = tc::smem_desc(kKmajor, tc::smem_u32(at)), kd = tc::smem_desc(kKmajor, tc::smem_u32(at + kTile));
 #pragma unroll 1
-                for (int p = 0; p < 2; ++p) mma_ss4(tm + kTmP + (n & 1) * 64, qd + p * 512, 2, kd + p * 512, 2, kId64, p, one);
-                if (one) tc::mma_commit(&sh.pfull[n & 1]);
-                __syncwarp();
-            }
-            if (n > 0) {
-                const int m = n - 1, s = m % 3, b = m & 1;
-                const uint8_t *at = sm + s * kStage;
-                WAIT(sh.pready[b], m >> 1);
-                tc::tc_fence_after();
-                mma_ss4(tm + kTmP + b * 64, tc::smem_desc(kMNmajor, tc::smem_u32(at + 2 * kTile)), 128,
-                        tc::smem_desc(kKmajor, tc::smem_u32(sm + kOutP + b * 8192)), 2, tc::idesc_bf16_f32(128, 64, true, false), false, one);
-                if (one) {
-                    tc::mma_commit(&sh.ofull[b]);
-                    tc::mma_commit(&sh.empty[s]);
+                    for (int p = 0; p < 2; ++p) mma_ss4(tm + kTmP + (n & 1) * 64, qd + p * 512, 2, kd + p * 512, 2, kId64, p, one);
+                    if (one) tc::mma_commit(&sh.pfull[n & 1]);
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (turn == (GATE ? 0 : 1) && n > 0) {
+                    const int m = n - 1, s = m % 3, b = m & 1;
+                    const uint8_t *at = sm + s * kStage;
+                    WAIT(sh.pready[b], m >> 1);
+                    tc::tc_fence_after();
+                    mma_ss4(tm + kTmP + b * 64, tc::smem_desc(kMNmajor, tc::smem_u32(at + 2 * kTile)), 128,
+                            tc::smem_desc(kKmajor, tc::smem_u32(sm + kOutP + b * 8192)), 2, tc::idesc_bf16_f32(128, 64, true, false), false, one);
+                    if (one) {
+                        tc::mma_commit(&sh.ofull[b]);
+                        tc::mma_commit(&sh.empty[s]);
+                    }
+                    __syncwarp();
+                }
             }
         }
     } else if (warp < 2) {
@@ -524,7 +535,7 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         END_SEGMENTS
     } else if (warp < 12) {
         // ---- S
-        more_registers<kOutS>();
+        more_registers<kOutS<GATE>>();
         const int dv = (warp & 3) * 32 + lane;
         const uint32_t d_col = tm + kTmD + lane_base(warp), sb_col = tm + kTmSb + lane_base(warp);
         for (int u = blockIdx.x; u < units; u += gridDim.x) {
@@ -565,14 +576,18 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             }
             if (sg.last && a.S_final) store_column(S, a.S_final + ((size_t)sg.doc * a.H + h) * kDim * kDim + dv);
         }
-    } else if (warp < 16) {
-        // ---- O
+    } else {
+        // ---- O; with the gated normalisation two groups of four warps, every other chunk each
+        const int group = GATE ? (warp >> 2) - 3 : 0, first = 384 + group * 128, tid = (int)threadIdx.x - first;
         const int dim = (warp & 3) * 32, c2 = (lane & 3) * 2;
+        float (&red)[4][kC] = sh.red[group], (&rms)[kC] = sh.rms[group];
+        int going = -1;  // the tile whose copy out is not known to have read it
         float2 weight[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)};  // of dimensions dim + 16 h + lane / 4 and 8 on
         if (GATE && a.fu.weight)
             for (int h = 0; h < 2; ++h)
                 weight[h] = make_float2(a.fu.weight[dim + 16 * h + (lane >> 2)], a.fu.weight[dim + 16 * h + 8 + (lane >> 2)]);
         FOR_SEGMENTS
+        if (GATE && (n & 1) != group) continue;
         uint8_t *tile = sm + kOutO + st * kTile;
         WAIT(sh.gfull[n % kRing], n / kRing);
         if (GATE) {
@@ -614,30 +629,16 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     to[h] += 2048;
                 }
             };
-            if (!GATE) {
+            if (GATE) {
+                // sums of squares over the value dimension: over a thread's four, its warp's 32 (each exchange leaves a lane
+                // half of the tokens), and the four warps'
+                const bool up1 = lane & 4, up2 = lane & 8;
 #pragma unroll 1
                 for (int i = 0; i < kC; i += 16) {
-                    float2 z[2][4];
+                    float2 z[2][4], sq[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     part(i, z);
-                    put(z);
-                }
-                tc::tc_fence_before();
-                warp_arrive(&sh.ofree[n & 1]);
-            } else {
-                // all of o is taken to registers, so that the next chunk's products can follow
-                float2 z[4][2][4];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) part(16 * t, z[t]);
-                tc::tc_fence_before();
-                warp_arrive(&sh.ofree[n & 1]);
-                // sums of squares over the value dimension: over a thread's four, its warp's 32 (each exchange leaves a
-                // lane half of the tokens), and the four warps'
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    float2 sq[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) sq[(e & 3) >> 1] = tc::fma2(z[t][e >> 2][e & 3], z[t][e >> 2][e & 3], sq[(e & 3) >> 1]);
-                    const bool up1 = lane & 4, up2 = lane & 8;
+                    for (int e = 0; e < 8; ++e) sq[(e & 3) >> 1] = tc::fma2(z[e >> 2][e & 3], z[e >> 2][e & 3], sq[(e & 3) >> 1]);
                     float2 x = up1 ? sq[1] : sq[0];
                     const float2 give = up1 ? sq[0] : sq[1];
                     x.x += __shfl_xor_sync(0xffffffffu, give.x, 4);
@@ -645,17 +646,21 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     float y = up2 ? x.y : x.x;
                     y += __shfl_xor_sync(0xffffffffu, up2 ? x.x : x.y, 8);
                     y += __shfl_xor_sync(0xffffffffu, y, 16);
-                    if (lane < 16) sh.red[warp & 3][16 * t + (up1 ? 8 : 0) + c2 + (up2 ? 1 : 0)] = y;
+                    if (lane < 16) red[warp & 3][i + (up1 ? 8 : 0) + c2 + (up2 ? 1 : 0)] = y;
                 }
-                tc::named_barrier(2, 128);
-                if (threadIdx.x - 384 < kC) {
-                    const int i = threadIdx.x - 384;
-                    sh.rms[i] = rsqrtf(((sh.red[0][i] + sh.red[1][i]) + (sh.red[2][i] + sh.red[3][i])) * (1.f / kDim) + a.fu.out_eps);
+                tc::named_barrier(2 + group, 128);
+                if (tid < kC) {
+                    const int i = tid;
+                    rms[i] = rsqrtf(((red[0][i] + red[1][i]) + (red[2][i] + red[3][i])) * (1.f / kDim) + a.fu.out_eps);
                 }
-                tc::named_barrier(2, 128);
+                tc::named_barrier(2 + group, 128);
+            }
 #pragma unroll 1
-                for (int i = 0; i < kC; i += 16) {
-                    const float2 r[2] = {*reinterpret_cast<const float2 *>(&sh.rms[i + c2]), *reinterpret_cast<const float2 *>(&sh.rms[i + 8 + c2])};
+            for (int i = 0; i < kC; i += 16) {
+                float2 z[2][4];
+                part(i, z);
+                if (GATE) {
+                    const float2 r[2] = {*reinterpret_cast<const float2 *>(&rms[i + c2]), *reinterpret_cast<const float2 *>(&rms[i + 8 + c2])};
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t gate[4];
@@ -665,36 +670,52 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                             const float2 x = tc::mul2(make_float2(bf16_lo(gate[e]), bf16_hi(gate[e])), make_float2(-linear::kLog2e, -linear::kLog2e));
                             const float2 y = tc::add2(make_float2(ex2(x.x), ex2(x.y)), make_float2(1.f, 1.f));
                             const float w = e & 1 ? weight[h].y : weight[h].x;
-                            z[0][h][e] = tc::mul2(tc::mul2(z[0][h][e], make_float2(rcp(y.x), rcp(y.y))), tc::mul2(r[e >> 1], make_float2(w, w)));
+                            z[h][e] = tc::mul2(tc::mul2(z[h][e], make_float2(rcp(y.x), rcp(y.y))), tc::mul2(r[e >> 1], make_float2(w, w)));
                         }
                     }
-                    put(z[0]);
-#pragma unroll
-                    for (int e = 0; e < 24; ++e) z[e / 8][e / 4 % 2][e % 4] = z[e / 8 + 1][e / 4 % 2][e % 4];  // the next 16 tokens'
                 }
+                put(z);
             }
+            tc::tc_fence_before();
+            warp_arrive(&sh.ofree[n & 1]);
         }
         if (lane == 0) tc::mbar_arrive(&sh.gempty[n % kRing]);
         tc::fence_async_smem();
-        tc::named_barrier(2, 128);
+        tc::named_barrier(2 + group, 128);
+        // a tile is free again once its copy out has read it: seen to when the next one is on its way
         if (rows == kC) {
-            if (threadIdx.x == 384) {
+            if (tid == 0) {
                 tc::tma_store_3d(&tm_o, 0, h, t0, tile);
                 tc::tma_store_3d(&tm_o, 64, h, t0, tile + 8192);
                 tc::bulk_commit();
-                tc::bulk_wait_read();
-                tc::mbar_arrive(&sh.zfree[st]);
+                if (GATE) {  // the gate's values of three chunks on wait for the tile
+                    tc::bulk_wait_read();
+                    tc::mbar_arrive(&sh.zfree[st]);
+                } else {
+                    if (going >= 0) {
+                        tc::bulk_wait_read_all_but_one();
+                        tc::mbar_arrive(&sh.zfree[going]);
+                    }
+                    going = st;
+                }
             }
         } else {
 #pragma unroll 1
-            for (int i = threadIdx.x - 384; i < rows * 16; i += 128) {
+            for (int i = tid; i < rows * 16; i += 128) {
                 const int t = i >> 4, c = i & 15;
                 reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + ((size_t)(t0 + t) * a.H + h) * kDim)[c] =
                     *reinterpret_cast<const uint4 *>(tile + (c >> 3) * 8192 + t * 128 + (((c & 7) ^ (t & 7)) << 4));
             }
             tc::fence_async_smem();
-            tc::named_barrier(2, 128);
-            if (threadIdx.x == 384) tc::mbar_arrive(&sh.zfree[st]);
+            tc::named_barrier(2 + group, 128);
+            if (tid == 0) {
+                if (going >= 0) {
+                    tc::bulk_wait_read();
+                    tc::mbar_arrive(&sh.zfree[going]);
+                    going = -1;
+                }
+                tc::mbar_arrive(&sh.zfree[st]);
+            }
         }
         __syncwarp();
         END_SEGMENTS
@@ -709,7 +730,7 @@ done:
         __syncwarp();
         tc::mbar_wait(&sh.drain, 0);
     }
-    if (threadIdx.x == 384) tc::bulk_wait_all();
+    if (warp >= 12 && threadIdx.x % 128 == 0) tc::bulk_wait_all();
     tc::tc_fence_before();
     __syncthreads();
     if (sh.dead && warp == 2) {  // copies in flight: each stage's last one, which ends a phase of either parity
@@ -976,9 +997,9 @@ cudaError_t enough_registers(int threads, int wanted) {
 
 template <bool NORM, bool GATE>
 cudaError_t launch_out(const CUtensorMap *m, const Args &a, int grid, cudaStream_t st) {
-    cudaError_t e = enough_registers<linear_out_tc<NORM, GATE>>(kOutThreads, kOutRegs);
+    cudaError_t e = enough_registers<linear_out_tc<NORM, GATE>>(kOutThreads<GATE>, kOutRegs<GATE>);
     if (e == cudaSuccess) e = allow_smem<linear_out_tc<NORM, GATE>>(kOutSmem);
-    return e != cudaSuccess ? e : launch_dependent(linear_out_tc<NORM, GATE>, dim3(grid), dim3(kOutThreads), kOutSmem, st, m[0], m[1], m[2], m[3], m[4], a);
+    return e != cudaSuccess ? e : launch_dependent(linear_out_tc<NORM, GATE>, dim3(grid), dim3(kOutThreads<GATE>), kOutSmem, st, m[0], m[1], m[2], m[3], m[4], a);
 }
 template <bool NORM>
 cudaError_t launch_segment(const CUtensorMap *m, const Args &a, int grid, cudaStream_t st) {
