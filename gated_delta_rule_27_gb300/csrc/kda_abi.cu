@@ -430,10 +430,11 @@ static kda_status linear_check(int32_t rows, int32_t H, int32_t H_qk, int32_t d_
 }
 
 // Segments of a prefill call and where its workspace holds them.
-static kda_status linear_plan(int32_t total_tokens, int32_t num_seqs, int32_t H, int32_t d, int32_t *seg, int32_t *slots,
-                              kda::linear::Layout *lay) {
+static bool linear_on_tensor_cores(int32_t d, kda_dtype dt) { return dt == KDA_BF16 && d == 128; }
+static kda_status linear_plan(int32_t total_tokens, int32_t num_seqs, int32_t H, int32_t d, kda_dtype dt, int32_t *seg,
+                              int32_t *slots, kda::linear::Layout *lay) {
     if (num_seqs < 0) return KDA_ERR_INVALID_ARG;
-    *seg = kda::linear::plan_segment(total_tokens, num_seqs, H);
+    *seg = kda::linear::plan_segment(total_tokens, num_seqs, H, linear_on_tensor_cores(d, dt));
     const int64_t n = total_tokens / *seg + (int64_t)num_seqs;
     if (n * H > INT_MAX) return KDA_ERR_UNSUPPORTED;
     *slots = (int32_t)n;
@@ -444,7 +445,7 @@ static kda_status linear_plan(int32_t total_tokens, int32_t num_seqs, int32_t H,
 size_t kda_linear_workspace_size(int32_t total_tokens, int32_t num_seqs, int32_t H, int32_t d_k, int32_t d_v, kda_dtype in_dtype) {
     int32_t seg, slots;
     kda::linear::Layout lay;
-    if (linear_check(total_tokens, H, H, d_k, d_v, in_dtype) || linear_plan(total_tokens, num_seqs, H, d_k, &seg, &slots, &lay)) return 0;
+    if (linear_check(total_tokens, H, H, d_k, d_v, in_dtype) || linear_plan(total_tokens, num_seqs, H, d_k, in_dtype, &seg, &slots, &lay)) return 0;
     return lay.total;
 }
 
@@ -455,7 +456,7 @@ kda_status kda_linear_prefill(const void *q, const void *k, const void *v, const
     if (kda_status st = linear_check(total_tokens, H, H_qk, d_k, d_v, in_dtype)) return st;
     int32_t seg, slots;
     kda::linear::Layout lay;
-    if (kda_status st = linear_plan(total_tokens, num_seqs, H, d_k, &seg, &slots, &lay)) return st;
+    if (kda_status st = linear_plan(total_tokens, num_seqs, H, d_k, in_dtype, &seg, &slots, &lay)) return st;
     kda::Fusion fu;
     if (kda_status st = fusion_from(opts, total_tokens > 0, o, &fu)) return st;
     if (num_seqs == 0) return total_tokens == 0 ? KDA_OK : KDA_ERR_INVALID_ARG;
@@ -476,7 +477,7 @@ kda_status kda_linear_prefill(const void *q, const void *k, const void *v, const
     a.seg_state = reinterpret_cast<float *>(ws + lay.state_off);
     a.status = reinterpret_cast<int32_t *>(ws), a.fu = fu;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = in_dtype == KDA_BF16 && d_k == 128 ? kda::launch_linear_tc(a, s) : kda::launch_linear_simt(a, d_k, in_dtype, s);
+    const cudaError_t e = linear_on_tensor_cores(d_k, in_dtype) ? kda::launch_linear_tc(a, s) : kda::launch_linear_simt(a, d_k, in_dtype, s);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

@@ -77,19 +77,20 @@ __device__ __forceinline__ bool find_segment(const int32_t *__restrict__ cu, int
 struct Args;
 __device__ __forceinline__ const float *segment_start(const Args &a, const Segment &s, int slot, int h, size_t state);
 
-// Tokens of a segment.  One document: as many segments of all heads as there are SMs, or a small multiple of that where
-// they do not fit the SMs well.  Several documents, whose lengths are not known here: four segments an SM, so that the
-// longest leave no SM alone for long.  256 tokens at least, below which a segment's state costs more than it saves.
-inline int plan_segment(int64_t total, int64_t num_seqs, int64_t H) {
+// Tokens of a segment.  Tensor cores: one document is cut into as many segments of all heads as there are SMs, or a
+// small multiple of that where they do not fit the SMs well; several documents, whose lengths are not known here, into four
+// segments an SM, so that the longest leave no SM alone for long; 256 tokens at least, below which a segment's state costs
+// more than it saves.  CUDA cores, which take a token some ten times as long: four segments an SM, of 64 tokens at least.
+inline int plan_segment(int64_t total, int64_t num_seqs, int64_t H, bool tensor_cores) {
     constexpr int64_t kSms = 152;
     int64_t parts = 4 * kSms / H;
-    for (int64_t r = 1; num_seqs == 1 && r <= 3; ++r) {
+    for (int64_t r = 1; tensor_cores && num_seqs == 1 && r <= 3; ++r) {
         parts = r * kSms / H;
         if (10 * parts * H >= 9 * r * kSms) break;
     }
     if (parts < 1) parts = 1;
-    const int64_t seg = ((total + parts - 1) / parts + 63) / 64 * 64;
-    return (int)(seg < 256 ? 256 : seg);
+    const int64_t seg = ((total + parts - 1) / parts + 63) / 64 * 64, least = tensor_cores ? 256 : 64;
+    return (int)(seg < least ? least : seg);
 }
 
 struct Args {

@@ -35,8 +35,8 @@ linear_simt_kernel(const Args a) {
     __shared__ bool s_gentle;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int col = tid / kSplit, part = tid % kSplit;  // rows 4 (i kSplit + part) .. + 3 for i < R / 4
-    tc::grid_dep_launch();
     tc::grid_dep_wait();
+    tc::grid_dep_launch();
     const bool valid = linear::valid_table(a.cu, a.num_seqs, a.total);
     if (a.first && blockIdx.x == 0 && tid == 0) *a.status = valid ? (int32_t)KDA_OK : (int32_t)KDA_ERR_INVALID_ARG;
     if (!valid) return;
@@ -117,6 +117,7 @@ linear_simt_kernel(const Args a) {
         // units overflow: it saves the product with each token's decay, and the rounding of that decay, which a slow one
         // would pile up token after token.
         if (s_gentle) {
+#pragma unroll 4
             for (int t = 0; t < n; ++t) {
                 const float vo = s_v[t][col] * s_out[t];
                 const float2 vv = make_float2(vo, vo);
@@ -205,9 +206,9 @@ linear_simt_kernel(const Args a) {
 // of the segment: block x finds such documents by the first of theirs.
 constexpr int kChainThreads = 256;
 __global__ void __launch_bounds__(kChainThreads) linear_chain_kernel(const Args a, int vecs) {
-    tc::grid_dep_launch();
-    tc::grid_dep_wait();
+    tc::grid_dep_launch();  // (the kernel before this one has waited for all that the next one reads, but the states)
     const bool valid = linear::valid_table(a.cu, a.num_seqs, a.total);
+    tc::grid_dep_wait();
     if (!valid) return;
     const int token = blockIdx.x * a.seg, h = blockIdx.y;
     if (token >= a.total) return;

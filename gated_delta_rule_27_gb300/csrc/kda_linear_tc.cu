@@ -327,8 +327,17 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         tc::tmem_alloc(&sh.tmem, 512);
         tc::tmem_relinquish();
     }
+    // Behind the segments' kernels, which have waited for everything before them, only the states have to be waited for: the
+    // S warps do.  (All of them, whatever they read: this kernel's end then means the end of the ones before it.)
+    if (a.first) tc::grid_dep_wait();
     tc::grid_dep_launch();
-    tc::grid_dep_wait();
+    if (threadIdx.x == 0) {
+        tc::prefetch_map(&tm_q);
+        tc::prefetch_map(&tm_k);
+        tc::prefetch_map(&tm_v);
+        tc::prefetch_map(&tm_o);
+        if (GATE) tc::prefetch_map(&tm_z);
+    }
     tc::tc_fence_before();
     const bool valid = linear::valid_table(a.cu, a.num_seqs, a.total);  // also the barrier behind the set-up
     tc::tc_fence_after();
@@ -536,6 +545,7 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     } else if (warp < 12) {
         // ---- S
         more_registers<kOutS<GATE>>();
+        tc::grid_dep_wait();
         const int dv = (warp & 3) * 32 + lane;
         const uint32_t d_col = tm + kTmD + lane_base(warp), sb_col = tm + kTmSb + lane_base(warp);
         for (int u = blockIdx.x; u < units; u += gridDim.x) {
@@ -805,8 +815,8 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         tc::tmem_alloc(&sh.tmem, 512);
         tc::tmem_relinquish();
     }
-    tc::grid_dep_launch();
     tc::grid_dep_wait();
+    tc::grid_dep_launch();  // (not before the wait: the kernels behind this one read q, k, v and g without one)
     tc::tc_fence_before();
     const bool valid = linear::valid_table(a.cu, a.num_seqs, a.total);  // also the barrier behind the set-up
     tc::tc_fence_after();

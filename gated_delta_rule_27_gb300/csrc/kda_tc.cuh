@@ -239,6 +239,11 @@ __device__ __forceinline__ void tma_prefetch_3d(const void *tmap, int x, int y, 
                  : "memory");
 }
 
+// Prefetches a tensor map (in kernel-parameter space).
+__device__ __forceinline__ void prefetch_map(const void *tmap) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
+}
+
 // Prefetches the line of global memory that holds p into L2.
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
