@@ -475,7 +475,7 @@ kda_status kda_linear_prefill(const void *q, const void *k, const void *v, const
     a.S0 = S0, a.o = o, a.S_final = S_final, a.aliased = S0 && S0 == S_final;
     a.seg_decay = reinterpret_cast<float *>(ws + lay.decay_off);
     a.seg_state = reinterpret_cast<float *>(ws + lay.state_off);
-    a.status = reinterpret_cast<int32_t *>(ws), a.fu = fu;
+    a.status = reinterpret_cast<int32_t *>(ws), a.ticket = a.status + kda::linear::kTicketWord, a.fu = fu;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = linear_on_tensor_cores(d_k, in_dtype) ? kda::launch_linear_tc(a, s) : kda::launch_linear_simt(a, d_k, in_dtype, s);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;

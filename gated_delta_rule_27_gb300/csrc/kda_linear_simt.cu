@@ -3,8 +3,8 @@
 //
 // The recurrence itself, token by token, with the state in registers: a thread owns D / 4 of one column's rows (column
 // = value dimension), so S_t = a S + k v needs the token's k rows, one v and no other thread, and o = S^T q is finished
-// among the column's four threads by two exchanges.  q, k and v of 16 tokens are staged in shared memory as fp32 while
-// the 16 before them are worked on.  Arithmetic bounds it: 3 d^2 operations a token and head, all in fp32.
+// among the column's four threads by two exchanges.  q, k and v of 16 or 32 tokens are staged in shared memory as
+// fp32 while those before them are worked on.  Arithmetic bounds it: 3 d^2 operations a token and head, all in fp32.
 #include "kda_linear.cuh"
 #include "kda_tc.cuh"
 
@@ -14,9 +14,8 @@ namespace {
 using linear::Args;
 using linear::Segment;
 
-constexpr int kTok = 16;    // tokens staged at once
 constexpr int kSplit = 4;   // threads of a column
-constexpr float kGentle = 24.f;  // largest log2 of a decay over kTok tokens that the state's units may follow
+constexpr float kGentle = 24.f;  // largest log2 of a decay over the staged tokens that the state's units may follow
 
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
@@ -29,6 +28,7 @@ template <typename Tin, int D, bool OUT>
 __global__ void __launch_bounds__(D * kSplit)
 linear_simt_kernel(const Args a) {
     constexpr int NT = D * kSplit, R = D / kSplit, kWarps = NT / 32;
+    constexpr int kTok = D == 128 ? 16 : 32;  // tokens staged at once
     constexpr int kLoads = kTok * D / NT;  // elements of a staged tensor a thread loads
     __shared__ __align__(16) float s_q[kTok][D], s_k[kTok][D], s_v[kTok][D], s_o[OUT ? kTok : 1][D];
     __shared__ float s_a[kTok], s_in[kTok], s_out[kTok];
@@ -202,41 +202,59 @@ linear_simt_kernel(const Args a) {
 }
 
 // The state behind each segment but a document's last, in place of what the segment adds: S <- decay S + added, from
-// the document's incoming state on.  Every document of more than one segment holds a token whose index is a multiple
-// of the segment: block x finds such documents by the first of theirs.
-constexpr int kChainThreads = 256;
-__global__ void __launch_bounds__(kChainThreads) linear_chain_kernel(const Args a, int vecs) {
+// the document's incoming state on.  Block x looks after document x, or where documents outnumber segments after the one
+// that holds the first token of the x-th stretch of `seg` tokens, if that is the first such token in it: every document of
+// more than one segment holds one.
+constexpr int kChainThreads = 256, kLinks = 8;
+__global__ void __launch_bounds__(kChainThreads) linear_chain_kernel(const Args a, int vecs, int by_document) {
     tc::grid_dep_launch();  // (the kernel before this one has waited for all that the next one reads, but the states)
-    const bool valid = linear::valid_table(a.cu, a.num_seqs, a.total);
-    tc::grid_dep_wait();
-    if (!valid) return;
-    const int token = blockIdx.x * a.seg, h = blockIdx.y;
-    if (token >= a.total) return;
-    int lo = 0, hi = a.num_seqs;  // the document of the token: cu[lo] <= token < cu[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.cu[mid] <= token) lo = mid;
-        else hi = mid;
+    const int h = blockIdx.y, token = blockIdx.x * a.seg;
+    int doc = blockIdx.x;
+    if (!by_document) {
+        int hi = a.num_seqs;  // cu[doc] <= token < cu[hi]
+        doc = 0;
+        while (hi - doc > 1) {
+            const int mid = (doc + hi) >> 1;
+            if (a.cu[mid] <= token) doc = mid;
+            else hi = mid;
+        }
     }
-    const int begin = a.cu[lo], len = a.cu[lo + 1] - begin;
-    if (len <= a.seg || token - begin >= a.seg) return;
-    const int links = (len + a.seg - 1) / a.seg - 1, slot = begin / a.seg + lo;
+    const int begin = a.cu[doc], len = a.cu[doc + 1] - begin;
+    const bool mine = len > a.seg && (by_document || (token >= begin && token - begin < a.seg));
+    if (!mine || !linear::valid_table(a.cu, a.num_seqs, a.total)) {
+        tc::grid_dep_wait();  // (so that this kernel's end means the end of the one before it)
+        return;
+    }
+    const int links = (len + a.seg - 1) / a.seg - 1, slot = begin / a.seg + doc;
     const int e = blockIdx.z * kChainThreads + threadIdx.x;
+    tc::grid_dep_wait();
     if (e >= vecs) return;
-    float4 s = a.S0 ? reinterpret_cast<const float4 *>(a.S0)[((size_t)lo * a.H + h) * vecs + e] : make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 s = a.S0 ? reinterpret_cast<const float4 *>(a.S0)[((size_t)doc * a.H + h) * vecs + e] : make_float4(0.f, 0.f, 0.f, 0.f);
     float4 *p = reinterpret_cast<float4 *>(a.seg_state) + ((size_t)slot * a.H + h) * vecs + e;
     const float *decay = a.seg_decay + (size_t)slot * a.H + h;
     const size_t step = (size_t)a.H * vecs;
     if (a.aliased) p[links * step] = s;
-#pragma unroll 4
-    for (int i = 0; i < links; ++i, p += step, decay += a.H) {
-        const float4 add = *p;
-        const float d = *decay;
-        s.x = fmaf(d, s.x, add.x);
-        s.y = fmaf(d, s.y, add.y);
-        s.z = fmaf(d, s.z, add.z);
-        s.w = fmaf(d, s.w, add.w);
-        *p = s;
+    // eight links' loads at a time: one after another, each would wait for memory
+    for (int i = 0; i < links; i += kLinks) {
+        float4 add[kLinks];
+        float d[kLinks];
+#pragma unroll
+        for (int l = 0; l < kLinks; ++l)
+            if (i + l < links) {
+                add[l] = __ldcg(p + l * step);
+                d[l] = __ldcg(decay + l * a.H);
+            }
+#pragma unroll
+        for (int l = 0; l < kLinks; ++l)
+            if (i + l < links) {
+                s.x = fmaf(d[l], s.x, add[l].x);
+                s.y = fmaf(d[l], s.y, add[l].y);
+                s.z = fmaf(d[l], s.z, add[l].z);
+                s.w = fmaf(d[l], s.w, add[l].w);
+                p[l * step] = s;
+            }
+        p += kLinks * step;
+        decay += kLinks * a.H;
     }
 }
 
@@ -271,9 +289,10 @@ cudaError_t launch_linear_simt(const linear::Args &a, int d, kda_dtype dt, cudaS
 }
 
 cudaError_t launch_linear_chain(const linear::Args &a, int d, cudaStream_t st) {
-    const int vecs = d * d / 4;
-    const dim3 grid((unsigned)((a.total + a.seg - 1) / a.seg), (unsigned)a.H, (unsigned)((vecs + kChainThreads - 1) / kChainThreads));
-    return launch_dependent(linear_chain_kernel, grid, dim3(kChainThreads), 0, st, a, vecs);
+    const int vecs = d * d / 4, stretches = (a.total + a.seg - 1) / a.seg;
+    const bool by_document = a.num_seqs <= stretches;
+    const dim3 grid((unsigned)(by_document ? a.num_seqs : stretches), (unsigned)a.H, (unsigned)((vecs + kChainThreads - 1) / kChainThreads));
+    return launch_dependent(linear_chain_kernel, grid, dim3(kChainThreads), 0, st, a, vecs, by_document ? 1 : 0);
 }
 
 }  // namespace kda

@@ -39,6 +39,7 @@ constexpr int kDim = 128;
 constexpr int kTile = kC * kDim * 2;
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kRing = 4;  // chunks whose decays are kept
+constexpr int kUnits = 4;  // units known ahead
 
 // A whole warp's wait.  One that runs out, or sees that another has, ends the whole CTA.  The loop is small on purpose, see
 // decayed_values.
@@ -89,6 +90,12 @@ struct __align__(16) Gates {
     float all, pad[3];         // 2^b_64
 };
 
+// What a CTA works on: a segment of a head.
+struct Unit {
+    Segment sg;
+    int slot, h;  // slot -1: no more
+};
+
 struct OutShared {
     Gates gates[kRing];
     float red[2][4][kC], rms[2][kC];  // of the two groups of O
@@ -98,7 +105,9 @@ struct OutShared {
     uint64_t pfull[2], pready[2], ofull[2], ofree[2];
     uint64_t vready, sready, dfree, kv, qs;
     uint64_t zfull[3], zfree[3];          // output tiles (and the gate's values before them)
+    uint64_t ufull[kUnits], uempty[kUnits];
     uint64_t drain;
+    Unit unit[kUnits];
     uint32_t tmem;
     volatile int dead;
 };
@@ -288,6 +297,17 @@ __device__ __forceinline__ void add_products(float2 (&S)[kDim / 2], float2 all, 
     tc::tc_fence_before();
 }
 
+// The unit behind `u` for a warp's CTA.
+__device__ __forceinline__ int next_unit(const Args &a, int u) {
+    if (!a.ticket) return u + (int)gridDim.x;
+    int t = 0;
+    if ((threadIdx.x & 31) == 0) {
+        tc::grid_dep_wait();  // the kernel that sets the ticket to 0
+        t = atomicAdd(a.ticket, 1);
+    }
+    return (int)gridDim.x + __shfl_sync(0xffffffffu, t, 0);
+}
+
 template <bool NORM, bool GATE>
 __global__ void __launch_bounds__(kOutThreads<GATE>, 1)
 linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -313,6 +333,10 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             tc::mbar_init(&sh.pready[i], 2);
             tc::mbar_init(&sh.ofull[i], 1);
             tc::mbar_init(&sh.ofree[i], 4);
+        }
+        for (int i = 0; i < kUnits; ++i) {
+            tc::mbar_init(&sh.ufull[i], 1);
+            tc::mbar_init(&sh.uempty[i], GATE ? 19 : 15);  // all warps but the copies'
         }
         tc::mbar_init(&sh.vready, 4);
         tc::mbar_init(&sh.sready, 4);
@@ -346,24 +370,45 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     const int units = valid ? a.slots * a.H : 0;
     const int share = a.H / a.Hqk;
 
-#define FOR_SEGMENTS                                                                               \
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {                                          \
-        Segment sg;                                                                                \
-        const int slot = u / a.H, h = u - slot * a.H;                                              \
-        if (!linear::find_segment(a.cu, a.num_seqs, a.seg, slot, &sg)) continue;                   \
-        for (int c0 = 0; c0 < sg.len; c0 += kC, ++n) {                                             \
-            [[maybe_unused]] const int t0 = sg.t0 + c0, rows = min(kC, sg.len - c0), st = n % 3;   \
-            [[maybe_unused]] const bool last_chunk = c0 + kC >= sg.len;
+// The units of a CTA, as the copies' warp hands them out, and their chunks.
+#define NEXT_UNIT                                                    \
+    WAIT(sh.ufull[turn % kUnits], turn / kUnits);                    \
+    const Segment sg = sh.unit[turn % kUnits].sg;                    \
+    [[maybe_unused]] const int slot = sh.unit[turn % kUnits].slot, h = sh.unit[turn % kUnits].h; \
+    warp_arrive(&sh.uempty[turn % kUnits]);                          \
+    ++turn;
+#define CHUNKS                                                       \
+    for (int c0 = 0; c0 < sg.len; c0 += kC, ++n) {                   \
+        [[maybe_unused]] const int t0 = sg.t0 + c0, rows = min(kC, sg.len - c0), st = n % 3;
+#define FOR_SEGMENTS                                                 \
+    for (;;) {                                                       \
+        NEXT_UNIT                                                    \
+        if (slot < 0) break;                                         \
+        CHUNKS
 #define END_SEGMENTS \
     }                \
     }
 
+    int turn = 0;  // units so far
     int n = 0;  // chunks so far: each barrier's phase follows from it
     if (warp < 8 || warp >= 12) fewer_registers<kOutOthers<GATE>>();
     if (warp == 2) {
-        // ---- copies and decays; a chunk's decays are read while the one before it is worked on
+        // ---- units, copies and decays; a chunk's decays are read while the one before it is worked on.  Documents are of
+        // any length, so behind its first unit a CTA takes the next that nobody has: dealt out in turn, the CTA with the
+        // most chunks had half as many again as the mean (8 documents, 33000 tokens x 32 heads).
         float g0 = 0.f, g1 = 0.f;
-        FOR_SEGMENTS
+        for (int u = blockIdx.x;; ++turn) {
+            Segment sg;
+            while (u < units && !linear::find_segment(a.cu, a.num_seqs, a.seg, u / a.H, &sg)) u = next_unit(a, u);
+            const int slot = u / a.H, h = u - slot * a.H;
+            if (turn >= kUnits) WAIT(sh.uempty[turn % kUnits], turn / kUnits - 1);
+            if (lane == 0) {
+                sh.unit[turn % kUnits] = Unit{sg, u < units ? slot : -1, h};
+                tc::mbar_arrive(&sh.ufull[turn % kUnits]);
+            }
+            if (u >= units) break;
+            CHUNKS
+            const bool last_chunk = c0 + kC >= sg.len;
         if (n >= 3) WAIT(sh.empty[st], n / 3 - 1);
         if (lane == 0) {
             uint8_t *to = sm + st * kStage;
@@ -401,25 +446,19 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 for (int p = 0; p < 2; ++p) tc::tma_load_3d(sm + kOutO + st * kTile + p * 8192, &tm_z, p * 64, h, t0, &sh.zfull[st]);
             }
         }
-        END_SEGMENTS
+            }
+            u = next_unit(a, u);
+        }
     } else if (warp == 3) {
         // ---- MMAs, in the order in which they can start: V'^T K and S^T Q^T of a chunk, Q K^T of the next, whose scores are
         // worked out meanwhile, V^T P^T of the first
         const bool one = tc::elect_one();
         int fixes = 0, left = 0;  // tokens of the segment that are left
-        int u = (int)blockIdx.x - (int)gridDim.x;
         for (bool more = true; more; ++n) {
-            if (left <= 0) {  // the next segment with tokens
-                for (;;) {
-                    Segment sg;
-                    u += gridDim.x;
-                    more = u < units;
-                    if (!more) break;
-                    if (linear::find_segment(a.cu, a.num_seqs, a.seg, u / a.H, &sg) && sg.len > 0) {
-                        left = sg.len;
-                        break;
-                    }
-                }
+            while (more && left <= 0) {
+                NEXT_UNIT
+                more = slot >= 0;
+                left = more ? sg.len : 0;
             }
             if (n > 0) {  // the products of the chunk before
                 const int m = n - 1, s = m % 3, b = m & 1;
@@ -438,9 +477,10 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             }
             // the next Q K^T waits for the output that was in its place: a quick one is gone before P is there, while
             // a gated one takes longer than P
-#pragma unroll
-            for (int turn = 0; turn < 2; ++turn) {
-                if (turn == (GATE ? 1 : 0) && more) {
+            const int second = GATE && n >= 2;
+#pragma unroll 1
+            for (int go = 0; go < 2; ++go) {
+                if (go == second && more) {
                     const int st = n % 3;
                     WAIT(sh.full[st], n / 3);
                     if (left < kC) {
@@ -458,7 +498,7 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     if (one) tc::mma_commit(&sh.pfull[n & 1]);
                     __syncwarp();
                 }
-                if (turn == (GATE ? 0 : 1) && n > 0) {
+                if (go != second && n > 0) {
                     const int m = n - 1, s = m % 3, b = m & 1;
                     const uint8_t *at = sm + s * kStage;
                     WAIT(sh.pready[b], m >> 1);
@@ -548,10 +588,9 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         tc::grid_dep_wait();
         const int dv = (warp & 3) * 32 + lane;
         const uint32_t d_col = tm + kTmD + lane_base(warp), sb_col = tm + kTmSb + lane_base(warp);
-        for (int u = blockIdx.x; u < units; u += gridDim.x) {
-            Segment sg;
-            const int slot = u / a.H, h = u - slot * a.H;
-            if (!linear::find_segment(a.cu, a.num_seqs, a.seg, slot, &sg)) continue;
+        for (;;) {
+            NEXT_UNIT
+            if (slot < 0) break;
             const float *init = linear::segment_start(a, sg, slot, h, (size_t)kDim * kDim);
             float2 S[kDim / 2], all = make_float2(1.f, 1.f);
             load_column(S, init ? init + dv : nullptr);
@@ -740,7 +779,7 @@ done:
         __syncwarp();
         tc::mbar_wait(&sh.drain, 0);
     }
-    if (warp >= 12 && threadIdx.x % 128 == 0) tc::bulk_wait_all();
+    if (warp >= 12 && threadIdx.x % 128 == 0) tc::bulk_wait_read();
     tc::tc_fence_before();
     __syncthreads();
     if (sh.dead && warp == 2) {  // copies in flight: each stage's last one, which ends a phase of either parity
@@ -759,8 +798,8 @@ done:
 // What each segment but a document's last adds to the state by its end, S^T = sum_j 2^(b_end - b_j) v_j k_j^T.  The
 // chunks are taken from the last to the first, so that every weight is known when its chunk is reached and the sum is
 // never rescaled; it also leaves the segment's first rows in L2 for the pass that forms the outputs.
-// Only k and v are read: 512 bytes a token and head; and only as far back as weights above 2^-192: fp32 holds no state that
-// a weight below that leaves anything of.
+// Only k and v are read: 512 bytes a token and head; and only as far back as weights are above 2^-126, below which they are
+// zero here (exp2 flushes what fp32 holds no normal number for).
 //     warp 0  copies   warp 1  MMAs   warp 2  decays   warps 4-7, 8-11  V' (and norms of k) of every other chunk
 //     warps 12-15  the sums over the chunks, in registers
 // ---------------------------------------------------------------------------
@@ -782,7 +821,7 @@ static_assert(kSegSmem <= 232448, "shared memory of a CTA");
 constexpr int kSegThreads = 16 * 32;
 constexpr int kSegOthers = 104, kSegSums = 184, kSegRegs = 128 * (3 * kSegOthers + kSegSums);
 
-constexpr long long kGone = -(192ll << 44);  // in the sums' fixed point
+constexpr long long kGone = -(127ll << 44);  // in the sums' fixed point
 
 template <bool NORM>
 __global__ void __launch_bounds__(kSegThreads, 1)
@@ -820,7 +859,10 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     tc::tc_fence_before();
     const bool valid = linear::valid_table(a.cu, a.num_seqs, a.total);  // also the barrier behind the set-up
     tc::tc_fence_after();
-    if (a.first && blockIdx.x == 0 && threadIdx.x == 0) *a.status = valid ? (int32_t)KDA_OK : (int32_t)KDA_ERR_INVALID_ARG;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        *a.status = valid ? (int32_t)KDA_OK : (int32_t)KDA_ERR_INVALID_ARG;
+        *a.ticket = 0;
+    }
     const uint32_t tm = sh.tmem, tm_vhi = tm + 256, tm_vlo = tm + 288;  // V'^T K at 0 and 128, V' at 256 and 320
     const int units = valid ? a.slots * a.H : 0;
     const int share = a.H / a.Hqk;
@@ -1038,6 +1080,8 @@ cudaError_t launch_linear_tc(const linear::Args &args, cudaStream_t st) {
         if (e == cudaSuccess) e = launch_linear_chain(a, kDim, st);
         if (e != cudaSuccess) return e;
         a.first = 0;
+    } else {
+        a.ticket = nullptr;
     }
     if (a.fu.qk_norm) return a.fu.gate ? launch_out<true, true>(m, a, grid, st) : launch_out<true, false>(m, a, grid, st);
     return a.fu.gate ? launch_out<false, true>(m, a, grid, st) : launch_out<false, false>(m, a, grid, st);
