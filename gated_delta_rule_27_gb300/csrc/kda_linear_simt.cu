@@ -1,10 +1,14 @@
 // kda_linear_simt.cu -- chunked linear attention on the CUDA cores: fp32 inputs, and d = 16 or 64; and the chaining of
 // the segments' states, which the tensor-core path shares.
 //
-// The recurrence itself, token by token, with the state in registers: a thread owns D / 4 of one column's rows (column
-// = value dimension), so S_t = a S + k v needs the token's k rows, one v and no other thread, and o = S^T q is finished
-// among the column's four threads by two exchanges.  q, k and v of 16 or 32 tokens are staged in shared memory as
-// fp32 while those before them are worked on.  Arithmetic bounds it: 3 d^2 operations a token and head, all in fp32.
+// The recurrence itself, token by token, with the state in registers: a thread owns a tile of the state, so
+// S_t = a S + k v needs the token's k and v of that tile and no other thread.  o = S^T q is added up among the threads of a
+// column (lanes of one warp), two tokens at a time: each exchange leaves a lane half of the sums.  q, k and v of 16 or 32
+// tokens are staged in shared memory as fp32 while those before them are worked on.
+//
+// Arithmetic bounds it at its best, 2 d^2 multiply-adds a token and head in fp32; what it takes in fact is the registers'
+// share of shared memory, 128 bytes a clock whoever else wants the same: with one column a thread (64 bytes of k and q for
+// 8 elements) a token took 300 clocks of an SM at d = 64, with tiles of 8 x 4 it takes a quarter of that.
 #include "kda_linear.cuh"
 #include "kda_tc.cuh"
 
@@ -14,8 +18,23 @@ namespace {
 using linear::Args;
 using linear::Segment;
 
-constexpr int kSplit = 4;   // threads of a column
 constexpr float kGentle = 24.f;  // largest log2 of a decay over the staged tokens that the state's units may follow
+
+// A thread's tile: kRows x kCols of the state; the D / kRows threads of a column are neighbours in a warp, and hold a sum for
+// each of two tokens' kCols columns in the end.
+template <int D>
+struct Tile {
+    static constexpr int kRows = D == 16 ? 4 : 8, kCols = D == 16 ? 2 : D == 64 ? 4 : 8;
+    static constexpr int kLanes = D / kRows, kThreads = kLanes * (D / kCols);
+    static constexpr int kTok = D == 128 ? 16 : 32;              // tokens staged at once
+    static constexpr int kVecs = kTok * D / 4 / kThreads;        // vectors of four elements of a staged tensor a thread loads
+    static_assert(kLanes == 2 * kCols && kLanes <= 32);
+};
+
+template <typename Tin>
+struct alignas(4 * sizeof(Tin)) Four {
+    Tin x[4];
+};
 
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
@@ -25,61 +44,68 @@ __device__ __forceinline__ float warp_sum(float x) {
 
 // OUT: the outputs and final states; else what each segment but a document's last adds to the state.
 template <typename Tin, int D, bool OUT>
-__global__ void __launch_bounds__(D * kSplit)
+__global__ void __launch_bounds__(Tile<D>::kThreads)
 linear_simt_kernel(const Args a) {
-    constexpr int NT = D * kSplit, R = D / kSplit, kWarps = NT / 32;
-    constexpr int kTok = D == 128 ? 16 : 32;  // tokens staged at once
-    constexpr int kLoads = kTok * D / NT;  // elements of a staged tensor a thread loads
+    using T = Tile<D>;
+    constexpr int NT = T::kThreads, R = T::kRows, C = T::kCols, kTok = T::kTok, kWarps = NT / 32;
     __shared__ __align__(16) float s_q[kTok][D], s_k[kTok][D], s_v[kTok][D], s_o[OUT ? kTok : 1][D];
     __shared__ float s_a[kTok], s_in[kTok], s_out[kTok];
     __shared__ bool s_gentle;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int col = tid / kSplit, part = tid % kSplit;  // rows 4 (i kSplit + part) .. + 3 for i < R / 4
-    tc::grid_dep_wait();
+    const int part = tid % T::kLanes, row0 = part * R, col0 = tid / T::kLanes * C;
+    // (behind the segments' kernels, which have waited for everything before them, only the states have to be waited for)
+    if (a.first) tc::grid_dep_wait();
     tc::grid_dep_launch();
     const bool valid = linear::valid_table(a.cu, a.num_seqs, a.total);
     if (a.first && blockIdx.x == 0 && tid == 0) *a.status = valid ? (int32_t)KDA_OK : (int32_t)KDA_ERR_INVALID_ARG;
-    if (!valid) return;
     const int slot = blockIdx.x / a.H, h = blockIdx.x - slot * a.H, hq = h / (a.H / a.Hqk);
     Segment sg;
-    if (!linear::find_segment(a.cu, a.num_seqs, a.seg, slot, &sg) || (!OUT && sg.last)) return;
+    if (!valid || !linear::find_segment(a.cu, a.num_seqs, a.seg, slot, &sg) || (!OUT && sg.last)) {
+        if (!a.first) tc::grid_dep_wait();  // so that this kernel's end means the end of the ones before it
+        return;
+    }
     const Tin *q = static_cast<const Tin *>(a.q), *k = static_cast<const Tin *>(a.k), *v = static_cast<const Tin *>(a.v);
     const size_t doc_state = ((size_t)sg.doc * a.H + h) * D * D, seg_state = ((size_t)slot * a.H + h) * D * D;
     const float *init = OUT ? linear::segment_start(a, sg, slot, h, (size_t)D * D) : nullptr;
-
-    float2 S[R / 2];
-#pragma unroll
-    for (int i = 0; i < R / 4; ++i) {
-        const size_t r = (size_t)4 * (i * kSplit + part) * D + col;
-        S[2 * i] = init ? make_float2(init[r], init[r + D]) : make_float2(0.f, 0.f);
-        S[2 * i + 1] = init ? make_float2(init[r + 2 * D], init[r + 3 * D]) : make_float2(0.f, 0.f);
-    }
     double total = 0.0;  // log2 of the segment's decay
 
-    Tin nq[kLoads], nk[kLoads], nv[kLoads];
+    Four<Tin> nq[T::kVecs], nk[T::kVecs], nv[T::kVecs];
     float ng = 0.f;
     auto fetch = [&](int c0) {
 #pragma unroll
-        for (int e = 0; e < kLoads; ++e) {
-            const int i = e * NT + tid, t = c0 + i / D, c = i % D;
+        for (int e = 0; e < T::kVecs; ++e) {
+            const int i = (e * NT + tid) * 4, t = c0 + i / D, c = i % D;
             if (t < sg.len) {
                 const size_t at = ((size_t)(sg.t0 + t) * a.Hqk + hq) * D + c;
-                if (OUT) nq[e] = q[at];
-                nk[e] = k[at];
-                nv[e] = v[((size_t)(sg.t0 + t) * a.H + h) * D + c];
+                if (OUT) nq[e] = *reinterpret_cast<const Four<Tin> *>(q + at);
+                nk[e] = *reinterpret_cast<const Four<Tin> *>(k + at);
+                nv[e] = *reinterpret_cast<const Four<Tin> *>(v + ((size_t)(sg.t0 + t) * a.H + h) * D + c);
             }
         }
         if (tid < kTok && c0 + tid < sg.len) ng = linear::log2_decay(a.per_token ? a.g[(size_t)(sg.t0 + c0 + tid) * a.H + h] : a.g[h]);
     };
+    // (rows behind the segment are staged as zeros, which add nothing to the state)
+    const auto stage = [](float *to, const Four<Tin> &x, bool there) {
+        *reinterpret_cast<float4 *>(to) = there ? make_float4(to_f32(x.x[0]), to_f32(x.x[1]), to_f32(x.x[2]), to_f32(x.x[3])) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
     fetch(0);
+    if (!a.first) tc::grid_dep_wait();
+    float2 S[R / 2][C];  // pairs of rows
+#pragma unroll
+    for (int r = 0; r < R / 2; ++r)
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const size_t at = (size_t)(row0 + 2 * r) * D + col0 + c;
+            S[r][c] = init ? make_float2(init[at], init[at + D]) : make_float2(0.f, 0.f);
+        }
     for (int c0 = 0; c0 < sg.len; c0 += kTok) {
         const int n = min(kTok, sg.len - c0);
 #pragma unroll
-        for (int e = 0; e < kLoads; ++e) {
-            const int i = e * NT + tid;
-            if (OUT) s_q[i / D][i % D] = to_f32(nq[e]);
-            s_k[i / D][i % D] = to_f32(nk[e]);
-            s_v[i / D][i % D] = to_f32(nv[e]);
+        for (int e = 0; e < T::kVecs; ++e) {
+            const int i = (e * NT + tid) * 4, t = i / D, c = i % D;
+            if (OUT) stage(&s_q[t][c], nq[e], t < n);
+            stage(&s_k[t][c], nk[e], t < n);
+            stage(&s_v[t][c], nv[e], t < n);
         }
         if (tid < 32) {  // the decays' sums from the first staged token on
             float b = tid < n ? ng : 0.f;
@@ -88,14 +114,13 @@ linear_simt_kernel(const Args a) {
                 const float up = __shfl_up_sync(0xffffffffu, b, off);
                 if (tid >= off) b += up;
             }
-            const float all = __shfl_sync(0xffffffffu, b, kTok - 1);
-            total += (double)all;
-            float most = fabsf(b);  // (growth and decay may cancel in the whole)
+            total += (double)__shfl_sync(0xffffffffu, b, kTok - 1);
+            float most = tid < kTok ? fabsf(b) : 0.f;  // (growth and decay may cancel in the whole)
+            const bool nan = __any_sync(0xffffffffu, b != b);
 #pragma unroll
             for (int off = 16; off; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
-            const bool nan = __any_sync(0xffffffffu, b != b);
             if (tid < kTok) {
-                s_a[tid] = exp2f(ng);
+                s_a[tid] = tid < n ? exp2f(ng) : 1.f;
                 s_in[tid] = exp2f(b);
                 s_out[tid] = exp2f(-b);
             }
@@ -116,55 +141,68 @@ linear_simt_kernel(const Args a) {
         // The state is kept in units of the decay since the first of these tokens, where that is not so strong that the
         // units overflow: it saves the product with each token's decay, and the rounding of that decay, which a slow one
         // would pile up token after token.
-        if (s_gentle) {
-#pragma unroll 4
-            for (int t = 0; t < n; ++t) {
-                const float vo = s_v[t][col] * s_out[t];
-                const float2 vv = make_float2(vo, vo);
-                float2 acc = make_float2(0.f, 0.f);
+        const bool gentle = s_gentle;
+#pragma unroll 1
+        for (int t0 = 0; t0 < n; t0 += 2) {
+            float x[2 * C];
 #pragma unroll
-                for (int i = 0; i < R / 4; ++i) {
-                    const float4 kk = *reinterpret_cast<const float4 *>(&s_k[t][4 * (i * kSplit + part)]);
-                    S[2 * i] = tc::fma2(make_float2(kk.x, kk.y), vv, S[2 * i]);
-                    S[2 * i + 1] = tc::fma2(make_float2(kk.z, kk.w), vv, S[2 * i + 1]);
-                    if (OUT) {
-                        const float4 qq = *reinterpret_cast<const float4 *>(&s_q[t][4 * (i * kSplit + part)]);
-                        acc = tc::fma2(make_float2(qq.x, qq.y), S[2 * i], acc);
-                        acc = tc::fma2(make_float2(qq.z, qq.w), S[2 * i + 1], acc);
+            for (int u = 0; u < 2; ++u) {
+                const int t = t0 + u;
+                float vv[C];
+#pragma unroll
+                for (int c = 0; c < C; c += 2) *reinterpret_cast<float2 *>(vv + c) = *reinterpret_cast<const float2 *>(&s_v[t][col0 + c]);
+                if (gentle) {
+                    const float w = s_out[t];
+#pragma unroll
+                    for (int c = 0; c < C; ++c) vv[c] *= w;
+                } else {
+                    const float2 av = make_float2(s_a[t], s_a[t]);
+#pragma unroll
+                    for (int r = 0; r < R / 2; ++r)
+#pragma unroll
+                        for (int c = 0; c < C; ++c) S[r][c] = tc::mul2(av, S[r][c]);
+                }
+                float2 acc[C];
+#pragma unroll
+                for (int c = 0; c < C; ++c) acc[c] = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int r = 0; r < R / 2; r += 2) {
+                    const float4 kk = *reinterpret_cast<const float4 *>(&s_k[t][row0 + 2 * r]);
+                    const float4 qq = OUT ? *reinterpret_cast<const float4 *>(&s_q[t][row0 + 2 * r]) : kk;
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        const float2 vc = make_float2(vv[c], vv[c]);
+                        S[r][c] = tc::fma2(make_float2(kk.x, kk.y), vc, S[r][c]);
+                        S[r + 1][c] = tc::fma2(make_float2(kk.z, kk.w), vc, S[r + 1][c]);
+                        if (OUT) {
+                            acc[c] = tc::fma2(make_float2(qq.x, qq.y), S[r][c], acc[c]);
+                            acc[c] = tc::fma2(make_float2(qq.z, qq.w), S[r + 1][c], acc[c]);
+                        }
                     }
                 }
-                if (OUT) {
-                    float x = acc.x + acc.y;
-                    x += __shfl_xor_sync(0xffffffffu, x, 1);
-                    x += __shfl_xor_sync(0xffffffffu, x, 2);
-                    if (part == 0) s_o[t][col] = x * s_in[t];
-                }
+#pragma unroll
+                for (int c = 0; c < C; ++c) x[u * C + c] = acc[c].x + acc[c].y;
             }
+            if (OUT) {
+#pragma unroll
+                for (int half = C; half; half >>= 1) {
+                    const bool up = part & half;
+#pragma unroll
+                    for (int i = 0; i < half; ++i) {
+                        const float give = up ? x[i] : x[i + half], keep = up ? x[i + half] : x[i];
+                        x[i] = keep + __shfl_xor_sync(0xffffffffu, give, half);
+                    }
+                }
+                const int t = t0 + part / C;  // the lane's sum is token part / C's of column part % C
+                s_o[t][col0 + part % C] = gentle ? x[0] * s_in[t] : x[0];
+            }
+        }
+        if (gentle) {
             const float2 end = make_float2(s_in[n - 1], s_in[n - 1]);
 #pragma unroll
-            for (int i = 0; i < R / 2; ++i) S[i] = tc::mul2(S[i], end);
-        } else {
-            for (int t = 0; t < n; ++t) {
-                const float2 av = make_float2(s_a[t], s_a[t]), vv = make_float2(s_v[t][col], s_v[t][col]);
-                float2 acc = make_float2(0.f, 0.f);
+            for (int r = 0; r < R / 2; ++r)
 #pragma unroll
-                for (int i = 0; i < R / 4; ++i) {
-                    const float4 kk = *reinterpret_cast<const float4 *>(&s_k[t][4 * (i * kSplit + part)]);
-                    S[2 * i] = tc::fma2(make_float2(kk.x, kk.y), vv, tc::mul2(av, S[2 * i]));
-                    S[2 * i + 1] = tc::fma2(make_float2(kk.z, kk.w), vv, tc::mul2(av, S[2 * i + 1]));
-                    if (OUT) {
-                        const float4 qq = *reinterpret_cast<const float4 *>(&s_q[t][4 * (i * kSplit + part)]);
-                        acc = tc::fma2(make_float2(qq.x, qq.y), S[2 * i], acc);
-                        acc = tc::fma2(make_float2(qq.z, qq.w), S[2 * i + 1], acc);
-                    }
-                }
-                if (OUT) {
-                    float x = acc.x + acc.y;
-                    x += __shfl_xor_sync(0xffffffffu, x, 1);
-                    x += __shfl_xor_sync(0xffffffffu, x, 2);
-                    if (part == 0) s_o[t][col] = x;
-                }
-            }
+                for (int c = 0; c < C; ++c) S[r][c] = tc::mul2(S[r][c], end);
         }
         __syncthreads();
         if (OUT) {
@@ -190,13 +228,13 @@ linear_simt_kernel(const Args a) {
     float *to = OUT ? (sg.last && a.S_final ? a.S_final + doc_state : nullptr) : a.seg_state + seg_state;
     if (to) {
 #pragma unroll
-        for (int i = 0; i < R / 4; ++i) {
-            const size_t r = (size_t)4 * (i * kSplit + part) * D + col;
-            to[r] = S[2 * i].x;
-            to[r + D] = S[2 * i].y;
-            to[r + 2 * D] = S[2 * i + 1].x;
-            to[r + 3 * D] = S[2 * i + 1].y;
-        }
+        for (int r = 0; r < R / 2; ++r)
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const size_t at = (size_t)(row0 + 2 * r) * D + col0 + c;
+                to[at] = S[r][c].x;
+                to[at + D] = S[r][c].y;
+            }
     }
     if (!OUT && tid == 0) a.seg_decay[(size_t)slot * a.H + h] = exp2f((float)total);
 }
@@ -264,12 +302,12 @@ cudaError_t launch_d(const Args &args, cudaStream_t st) {
     a.first = 1;
     const dim3 grid((unsigned)(a.slots * a.H));
     if (a.total > a.seg) {
-        cudaError_t e = launch_dependent(linear_simt_kernel<Tin, D, false>, grid, dim3(D * kSplit), 0, st, a);
+        cudaError_t e = launch_dependent(linear_simt_kernel<Tin, D, false>, grid, dim3(Tile<D>::kThreads), 0, st, a);
         if (e == cudaSuccess) e = launch_linear_chain(a, D, st);
         if (e != cudaSuccess) return e;
         a.first = 0;
     }
-    return launch_dependent(linear_simt_kernel<Tin, D, true>, grid, dim3(D * kSplit), 0, st, a);
+    return launch_dependent(linear_simt_kernel<Tin, D, true>, grid, dim3(Tile<D>::kThreads), 0, st, a);
 }
 
 template <typename Tin>
