@@ -142,7 +142,7 @@ linear_simt_kernel(const Args a) {
         // units overflow: it saves the product with each token's decay, and the rounding of that decay, which a slow one
         // would pile up token after token.
         const bool gentle = s_gentle;
-#pragma unroll 1
+#pragma unroll(D == 128 ? 1 : 4)
         for (int t0 = 0; t0 < n; t0 += 2) {
             float x[2 * C];
 #pragma unroll

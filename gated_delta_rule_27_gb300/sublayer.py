@@ -17,6 +17,11 @@ share can be measured:
     (kda_short_conv_*, kda_prefill_chunked_ex / kda_decode_step_ex).
 
 Hidden size: H * d (the pages give none for the model).
+
+The sublayer of linear attention with one decay per head stands beside it
+(linear_prefill_forward, linear_decode_forward), with rotary positions on q
+and k (kda_rope) and the recurrence of kda_linear_prefill /
+kda_linear_decode_step.
 """
 from __future__ import annotations
 
@@ -138,3 +143,59 @@ def decode_forward(x, S, conv_state, w: Weights, H: int, d: int, events=None, qk
     y = bufs.o.view(N, H * d) @ w.W_o
     _mark(events, 4)
     return y
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# The sublayer of linear attention with one decay per head: x -> Q/K/V projections -> rotary positions on Q and K ->
+# decay gate (one log-decay a token and head, read as for KDA's) -> the recurrence, with the Q/K normalisation before
+# it (which no rotation changes) and the gated normalisation behind it fused -> output projection.
+# ---------------------------------------------------------------------------------------------------------------
+@dataclasses.dataclass
+class LinearWeights:
+    W_q: torch.Tensor   # [D, H_qk d] bf16
+    W_k: torch.Tensor   # [D, H_qk d]
+    W_v: torch.Tensor   # [D, H d]
+    W_a: torch.Tensor   # decay gate [D, H]
+    W_z: torch.Tensor   # output gate [D, H d]
+    W_o: torch.Tensor   # [H d, D]
+    out_weight: torch.Tensor  # [d] fp32
+    rope_steps: torch.Tensor  # [rot / 2] int64 (libkda.rope_steps)
+    rope_scale: float
+
+
+def synthetic_linear_weights(D: int, H: int, H_qk: int, d: int, seed: int, device, rot: int = None, scaling=None) -> LinearWeights:
+    gen = torch.Generator(device="cpu").manual_seed(seed)
+    mat = lambda r, c: (torch.randn((r, c), generator=gen) / r ** 0.5).to(torch.bfloat16).to(device)
+    freq, scale = libkda.rope_frequencies(d if rot is None else rot, scaling=scaling)
+    return LinearWeights(mat(D, H_qk * d), mat(D, H_qk * d), mat(D, H * d), mat(D, H), mat(D, H * d), mat(H * d, D),
+                         (1.0 + 0.1 * torch.randn(d, generator=gen)).to(device), libkda.rope_steps(freq).to(device), scale)
+
+
+def _linear_inputs(x, positions, w: LinearWeights, d: int):
+    R = x.shape[0]
+    q, k, v, z = ((x @ m).view(R, -1, d) for m in (w.W_q, w.W_k, w.W_v, w.W_z))
+    libkda.kda_rope(q, k, positions, w.rope_steps, q, k, scale=w.rope_scale)
+    g = -torch.nn.functional.softplus((x @ w.W_a).float())
+    return q, k, v, z, g
+
+
+def linear_prefill_forward(x, cu_seqlens, positions, w: LinearWeights, d: int, S0=None, qk_eps=1e-6, out_eps=1e-6, workspace=None):
+    """x [T, D] bf16 at positions [T] int32 -> (y [T, D] bf16, S [N, H, d, d]) for packed documents, from the states S0
+    (None: zeros)."""
+    T, N = x.shape[0], cu_seqlens.numel() - 1
+    q, k, v, z, g = _linear_inputs(x, positions, w, d)
+    o = torch.empty_like(v)
+    S = torch.empty((N, v.shape[1], d, d), dtype=torch.float32, device=x.device)
+    libkda.kda_linear_prefill(q, k, v, g, cu_seqlens, o, S0=S0, S_final=S, workspace=workspace, qk_l2norm=True, qk_eps=qk_eps, out_gate=z,
+                              out_weight=w.out_weight, out_eps=out_eps)
+    return o.view(T, -1) @ w.W_o, S
+
+
+def linear_decode_forward(x, positions, S_pool, seq_idx, w: LinearWeights, d: int, qk_eps=1e-6, out_eps=1e-6):
+    """One token of each listed slot: x [N, D] bf16 at positions [N]; S_pool [slots, H, d, d] updated in place; returns
+    y [N, D]."""
+    q, k, v, z, g = _linear_inputs(x, positions, w, d)
+    o = torch.empty_like(v)
+    libkda.kda_linear_decode_step(q, k, v, g, S_pool, o, seq_idx=seq_idx, qk_l2norm=True, qk_eps=qk_eps, out_gate=z, out_weight=w.out_weight,
+                                  out_eps=out_eps)
+    return o.view(x.shape[0], -1) @ w.W_o
