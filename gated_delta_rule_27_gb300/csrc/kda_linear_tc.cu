@@ -13,13 +13,13 @@
 //     warps 0-1    P: Q K^T from tensor memory, times the decays, to shared memory in bf16
 //     warp 2       copies of q, k, v (and of the output gate) by TMA, three chunks ahead, and the decays' sums
 //     warp 3       issues all MMAs
-//     warps 4-7    the norms of q and k (fused normalisation only); V': v times its decay, in two bf16 parts, to tensor memory (the A operand of the state's product)
+//     warps 4-7    the norms of q and k (fused normalisation only); V': v times its decay, in three bf16 parts (the A operand of the state's product)
 //     warps 8-11   S: the state, decayed and added to, and its bf16 copy (the A operand of S^T Q^T)
 //     warps 12-15  O: the two parts of o added, to shared memory and out by TMA; with the gated normalisation, which takes
 //                  twice as long, another four warps take every other chunk
 //
 // Roundings to bf16: P and the copy of S, which only reach o, itself rounded to bf16 (each adds an error of the size
-// of that rounding in its part of o).  V' reaches the state, which is fp32: it is taken in two parts (16 bits of 24).
+// of that rounding in its part of o).  V' reaches the state, which is fp32: it is taken in three parts, all its 24 bits.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -37,24 +37,17 @@ using linear::Segment;
 constexpr int kC = 64;    // tokens of a chunk
 constexpr int kDim = 128;
 constexpr int kTile = kC * kDim * 2;
-constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kRing = 4;  // chunks whose decays are kept
 constexpr int kUnits = 4;  // units known ahead
 
-// A whole warp's wait.  One that runs out, or sees that another has, ends the whole CTA.  The loop is small on purpose, see
-// decayed_values.
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, const volatile int *dead) {
-    bool ok = tc::mbar_try_wait(bar, parity);
-    if (!ok) {
-        const uint64_t t0 = tc::globaltimer_ns();
-#pragma unroll 1
-        do ok = tc::mbar_try_wait(bar, parity);
-        while (!ok && !*dead && tc::globaltimer_ns() - t0 < kWaitNs);
-    }
-    return __all_sync(0xffffffffu, ok);
+// A whole warp's wait.  One that runs out, after about a second (each try is suspended for 4 us), ends the warp's work, and
+// so the waits of the others, one second on.  The loop is small on purpose, see tile_lane.
+constexpr int kTries = 1 << 18;
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, tc::mbar_wait_suspended(bar, parity, kTries));
 }
 #define WAIT(bar, n_uses) \
-    if (!wait_warp(&(bar), (uint32_t)(n_uses) & 1u, &sh.dead)) goto died
+    if (!wait_warp(&(bar), (uint32_t)(n_uses) & 1u)) goto died
 
 // One arrival for the warp, once all its lanes are here.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
@@ -103,7 +96,7 @@ struct OutShared {
     uint64_t gfull[kRing], gempty[kRing];
     uint64_t fixed[2];                    // rows behind a segment cleared (turn by turn: V' can be a chunk ahead)
     uint64_t pfull[2], pready[2], ofull[2], ofree[2];
-    uint64_t vready, sready, dfree, kv, qs;
+    uint64_t vready[2], sready, dfree, kv, qs, pused;
     uint64_t zfull[3], zfree[3];          // output tiles (and the gate's values before them)
     uint64_t ufull[kUnits], uempty[kUnits];
     uint64_t drain;
@@ -112,7 +105,7 @@ struct OutShared {
     volatile int dead;
 };
 constexpr int kStage = 3 * kTile;
-constexpr int kOutP = 3 * kStage, kOutO = kOutP + 2 * 8192, kOutShared = kOutO + 3 * kTile;
+constexpr int kOutP = 3 * kStage, kOutO = kOutP + 8192, kOutV3 = kOutO + 3 * kTile, kOutShared = kOutV3 + kTile;
 constexpr int kOutSmem = kOutShared + (int)sizeof(OutShared) + 1024;
 static_assert(kOutSmem <= 232448, "shared memory of a CTA");
 template <bool GATE>
@@ -205,12 +198,16 @@ __device__ __forceinline__ uint32_t tile_lane(int dim) {
     return (uint32_t)((dim >> 6) * 8192 + token * 128 + ((chunk ^ (token & 7)) << 4));
 }
 
-// 32 lanes of V'^T (value dimensions 32 (warp % 4) on) for the chunk's tokens, in two bf16 parts: v's tile is read
-// transposed, so that a register holds two tokens of a value dimension, as the MMA wants A.
+// 32 lanes of V'^T (value dimensions 32 (warp % 4) on) for the chunk's tokens, in three bf16 parts: v's tile is read
+// transposed, so that a register holds two tokens of a value dimension, as the MMA wants A.  The third part goes back to
+// shared memory, a tile like v's: tensor memory has no room for it beside the outputs.  The first 32 tokens are `ready`
+// before the others: their MMAs run meanwhile.
 template <bool NORM>
-__device__ __forceinline__ void decayed_values(const uint8_t *v, const Gates &g, int warp, uint32_t hi_col, uint32_t lo_col) {
+__device__ __forceinline__ void decayed_values(const uint8_t *v, uint8_t *third, const Gates &g, int warp, uint32_t hi_col, uint32_t lo_col,
+                                               uint64_t *ready) {
     const int c2 = (threadIdx.x & 3) * 2, dim = (warp & 3) * 32;
     uint32_t from0 = tc::smem_u32(v) + tile_lane(dim), from1 = tc::smem_u32(v) + tile_lane(dim + 16);
+    const uint32_t to_third = tc::smem_u32(third) - tc::smem_u32(v);
     hi_col += lane_base(warp);
     lo_col += lane_base(warp);
 #pragma unroll 1
@@ -225,39 +222,59 @@ __device__ __forceinline__ void decayed_values(const uint8_t *v, const Gates &g,
         }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            uint32_t hi[4], lo[4];
+            uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float2 y = tc::mul2(make_float2(bf16_lo(x[half][e]), bf16_hi(x[half][e])), w[e >> 1]);
                 hi[e] = pack_bf16(y.x, y.y);
                 const float2 r = tc::sub2(y, make_float2(bf16_lo(hi[e]), bf16_hi(hi[e])));
-                lo[e] = pack_bf16(r.x, r.y);
+                mid[e] = pack_bf16(r.x, r.y);
+                const float2 rr = tc::sub2(r, make_float2(bf16_lo(mid[e]), bf16_hi(mid[e])));
+                lo[e] = pack_bf16(rr.x, rr.y);
             }
             tc::tmem_st_16x8(hi_col + (half << 20), hi);
-            tc::tmem_st_16x8(lo_col + (half << 20), lo);
+            tc::tmem_st_16x8(lo_col + (half << 20), mid);
+            tc::stmatrix_t4((half ? from1 : from0) + to_third, lo);
+        }
+        if (j & 16) {
+            tc::fence_async_smem();
+            tc::tmem_wait_st();
+            tc::tc_fence_before();
+            warp_arrive(ready + (j >> 5));
         }
     }
-    tc::tmem_wait_st();
-    tc::tc_fence_before();
 }
 
-// Four MMAs over consecutive slices of 16 of K: A in tensor memory (8 columns a slice) or in shared memory, B in shared
-// memory, slices `a_step` and `b_step` (in 16 bytes) apart.
-__device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint64_t b, uint32_t b_step, uint32_t id, bool accumulate, bool one) {
+// A value that all lanes of the warp have, in a register of the whole warp: what an MMA takes has to be in those, and from
+// values that the compiler cannot tell to be the same in all lanes it moves every operand of every MMA there (24
+// instructions an MMA, of which the issuing warp did not get enough: 100 to 140 clocks for one that runs for 32 to 64).
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(0xffffffffu, x); }
+
+// The lower half of a shared-memory descriptor; the upper one is the layout's alone.
+__device__ __forceinline__ uint32_t desc_lo(uint64_t base, uint32_t smem_addr) { return (uint32_t)base | ((smem_addr & 0x3FFFF) >> 4); }
+__device__ __forceinline__ uint64_t desc(uint64_t base, uint32_t lo) { return (base & 0xffffffff00000000ull) | lo; }
+
+// MMAs over consecutive slices of 16 of K: A in tensor memory (8 columns a slice) or in shared memory, B in shared memory,
+// slices `a_step` and `b_step` (in 16 bytes) apart.
+template <int STEPS>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b_base, uint32_t b, uint32_t b_step, uint32_t id, bool accumulate, bool one) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) tc::mma_bf16_ts_warp(d, a + 8 * i, b + (uint64_t)b_step * i, id, accumulate || i > 0, one);
+    for (int i = 0; i < STEPS; ++i) tc::mma_bf16_ts_warp(d, a + 8 * i, desc(b_base, b + b_step * i), id, accumulate || i > 0, one);
 }
-__device__ __forceinline__ void mma_ss4(uint32_t d, uint64_t a, uint32_t a_step, uint64_t b, uint32_t b_step, uint32_t id, bool accumulate, bool one) {
+template <int STEPS>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a_base, uint32_t a, uint32_t a_step, uint64_t b_base, uint32_t b, uint32_t b_step,
+                                       uint32_t id, bool accumulate, bool one) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) tc::mma_bf16_warp(d, a + (uint64_t)a_step * i, b + (uint64_t)b_step * i, id, accumulate || i > 0, one);
+    for (int i = 0; i < STEPS; ++i) tc::mma_bf16_warp(d, desc(a_base, a + a_step * i), desc(b_base, b + b_step * i), id, accumulate || i > 0, one);
 }
 
-// V'^T K over the chunk's tokens, both parts of V'.
-__device__ __forceinline__ void mma_state(uint32_t d_col, uint32_t hi_col, uint32_t lo_col, const uint8_t *k, bool one) {
+// V'^T K over the first or last 32 of the chunk's tokens, all parts of V'.
+__device__ __forceinline__ void mma_state(int half, uint32_t d_col, uint32_t hi_col, uint32_t lo_col, uint32_t third, uint32_t k, bool one) {
     constexpr uint32_t id = tc::idesc_bf16_f32(128, 128, false, true);
-    const uint64_t kd = tc::smem_desc(kMNmajor, tc::smem_u32(k));
-#pragma unroll 1
-    for (int p = 0; p < 2; ++p) mma_ts4(d_col, p ? lo_col : hi_col, kd, 128, id, p, one);
+    const uint32_t kd = desc_lo(kMNmajor, k + half * 4096);
+    mma_ts<2>(d_col, hi_col + half * 16, kMNmajor, kd, 128, id, half > 0, one);
+    mma_ts<2>(d_col, lo_col + half * 16, kMNmajor, kd, 128, id, true, one);
+    mma_ss<2>(d_col, kMNmajor, desc_lo(kMNmajor, third + half * 4096), 128, kMNmajor, kd, 128, tc::idesc_bf16_f32(128, 128, true, true), true, one);
 }
 
 // The registers of a warpgroup's threads, changed by all its warps.  What the groups have afterwards must not be more than
@@ -338,11 +355,13 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             tc::mbar_init(&sh.ufull[i], 1);
             tc::mbar_init(&sh.uempty[i], GATE ? 19 : 15);  // all warps but the copies'
         }
-        tc::mbar_init(&sh.vready, 4);
+        tc::mbar_init(&sh.vready[0], 4);
+        tc::mbar_init(&sh.vready[1], 4);
         tc::mbar_init(&sh.sready, 4);
         tc::mbar_init(&sh.dfree, 4);
         tc::mbar_init(&sh.kv, 1);
         tc::mbar_init(&sh.qs, 1);
+        tc::mbar_init(&sh.pused, 1);
         tc::mbar_init(&sh.drain, 1);
         sh.dead = 0;
         tc::fence_mbar_init();
@@ -453,6 +472,7 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         // ---- MMAs, in the order in which they can start: V'^T K and S^T Q^T of a chunk, Q K^T of the next, whose scores are
         // worked out meanwhile, V^T P^T of the first
         const bool one = tc::elect_one();
+        const uint32_t base = uniform(tc::smem_u32(sm)), tu = uniform(tm);
         int fixes = 0, left = 0;  // tokens of the segment that are left
         for (bool more = true; more; ++n) {
             while (more && left <= 0) {
@@ -460,19 +480,21 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 more = slot >= 0;
                 left = more ? sg.len : 0;
             }
+            const uint32_t un = uniform(n), um = un - 1, s = um % 3, b = um & 1, before = base + s * kStage;
             if (n > 0) {  // the products of the chunk before
-                const int m = n - 1, s = m % 3, b = m & 1;
-                const uint8_t *at = sm + s * kStage;
-                WAIT(sh.vready, m);
-                WAIT(sh.dfree, m);
-                tc::tc_fence_after();
-                mma_state(tm + kTmD, tm + kTmVhi, tm + kTmVlo, at + kTile, one);
-                if (one) tc::mma_commit(&sh.kv);
-                WAIT(sh.sready, m);
-                tc::tc_fence_after();
-                const uint64_t qd = tc::smem_desc(kKmajor, tc::smem_u32(at));
+                WAIT(sh.dfree, um);
 #pragma unroll 1
-                for (int p = 0; p < 2; ++p) mma_ts4(tm + kTmO + b * 64, tm + kTmSb + p * 32, qd + p * 512, 2, kId64, p, one);
+                for (uint32_t half = 0; half < 2; ++half) {
+                    WAIT(sh.vready[half], um);
+                    tc::tc_fence_after();
+                    mma_state(half, tu + kTmD, tu + kTmVhi, tu + kTmVlo, base + kOutV3, before + kTile, one);
+                }
+                if (one) tc::mma_commit(&sh.kv);
+                WAIT(sh.sready, um);
+                tc::tc_fence_after();
+                const uint32_t qd = desc_lo(kKmajor, before);
+#pragma unroll(GATE ? 1 : 2)
+                for (uint32_t p = 0; p < 2; ++p) mma_ts<4>(tu + kTmO + b * 64, tu + kTmSb + p * 32, kKmajor, qd + p * 512, 2, kId64, p, one);
                 if (one) tc::mma_commit(&sh.qs);
             }
             // the next Q K^T waits for the output that was in its place: a quick one is gone before P is there, while
@@ -481,32 +503,30 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 #pragma unroll 1
             for (int go = 0; go < 2; ++go) {
                 if (go == second && more) {
-                    const int st = n % 3;
-                    WAIT(sh.full[st], n / 3);
+                    const uint32_t st = un % 3;
+                    WAIT(sh.full[st], un / 3);
                     if (left < kC) {
                         WAIT(sh.fixed[fixes & 1], fixes >> 1);
                         ++fixes;
                     }
                     left -= kC;
-                    if (n >= 2) WAIT(sh.ofree[n & 1], n / 2 - 1);
+                    if (n >= 2) WAIT(sh.ofree[un & 1], un / 2 - 1);
                     tc::tc_fence_after();
-                    const uint8_t *at = sm + st * kStage;
                     // (rows 64 to 127 of the result come of what follows the tile's half, and nobody reads them)
-                    const uint64_t qd = tc::smem_desc(kKmajor, tc::smem_u32(at)), kd = tc::smem_desc(kKmajor, tc::smem_u32(at + kTile));
-#pragma unroll 1
-                    for (int p = 0; p < 2; ++p) mma_ss4(tm + kTmP + (n & 1) * 64, qd + p * 512, 2, kd + p * 512, 2, kId64, p, one);
-                    if (one) tc::mma_commit(&sh.pfull[n & 1]);
+                    const uint32_t qd = desc_lo(kKmajor, base + st * kStage), kd = desc_lo(kKmajor, base + st * kStage + kTile), d = tu + kTmP + (un & 1) * 64;
+#pragma unroll(GATE ? 1 : 2)
+                    for (uint32_t p = 0; p < 2; ++p) mma_ss<4>(d, kKmajor, qd + p * 512, 2, kKmajor, kd + p * 512, 2, kId64, p, one);
+                    if (one) tc::mma_commit(&sh.pfull[un & 1]);
                     __syncwarp();
                 }
                 if (go != second && n > 0) {
-                    const int m = n - 1, s = m % 3, b = m & 1;
-                    const uint8_t *at = sm + s * kStage;
-                    WAIT(sh.pready[b], m >> 1);
+                    WAIT(sh.pready[b], um >> 1);
                     tc::tc_fence_after();
-                    mma_ss4(tm + kTmP + b * 64, tc::smem_desc(kMNmajor, tc::smem_u32(at + 2 * kTile)), 128,
-                            tc::smem_desc(kKmajor, tc::smem_u32(sm + kOutP + b * 8192)), 2, tc::idesc_bf16_f32(128, 64, true, false), false, one);
+                    mma_ss<4>(tu + kTmP + b * 64, kMNmajor, desc_lo(kMNmajor, before + 2 * kTile), 128, kKmajor, desc_lo(kKmajor, base + kOutP), 2,
+                            tc::idesc_bf16_f32(128, 64, true, false), false, one);
                     if (one) {
                         tc::mma_commit(&sh.ofull[b]);
+                        tc::mma_commit(&sh.pused);
                         tc::mma_commit(&sh.empty[s]);
                     }
                     __syncwarp();
@@ -519,13 +539,14 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         FOR_SEGMENTS
         WAIT(sh.gfull[n % kRing], n / kRing);
         WAIT(sh.pfull[n & 1], n / 2);
+        if (n >= 1) WAIT(sh.pused, n - 1);
         tc::tc_fence_after();
         {
             const Gates &g = sh.gates[n % kRing];
             // (the sums' rounding, 2^-24 of up to 64 x 160, costs a score at most a part in 2^11: less than its bf16)
             const float bi = g.b[i];
             const uint32_t from = tm + kTmP + (n & 1) * 64 + lane_base(warp);
-            uint8_t *row = sm + kOutP + (n & 1) * 8192 + i * 128;
+            uint8_t *row = sm + kOutP + i * 128;
             const int end = min(i + 1, rows);
 #pragma unroll 1
             for (int j = 0; j < kC; j += 8) {
@@ -571,15 +592,15 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         if (NORM) {
             if (n >= kRing) WAIT(sh.gempty[n % kRing], n / kRing - 1);
-            row_norms(sm + st * kStage, (warp & 3) * 16, a.fu.qk_eps, sh.gates[n % kRing].rq);
-            row_norms(sm + st * kStage + kTile, (warp & 3) * 16, a.fu.qk_eps, sh.gates[n % kRing].rk);
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k)
+                row_norms(sm + st * kStage + k * kTile, (warp & 3) * 16, a.fu.qk_eps, k ? sh.gates[n % kRing].rk : sh.gates[n % kRing].rq);
             warp_arrive(&sh.gfull[n % kRing]);
         }
         WAIT(sh.gfull[n % kRing], n / kRing);
         if (n >= 1) WAIT(sh.kv, n - 1);
         tc::tc_fence_after();
-        decayed_values<NORM>(sm + st * kStage + 2 * kTile, sh.gates[n % kRing], warp, tm + kTmVhi, tm + kTmVlo);
-        warp_arrive(&sh.vready);
+        decayed_values<NORM>(sm + st * kStage + 2 * kTile, sm + kOutV3, sh.gates[n % kRing], warp, tm + kTmVhi, tm + kTmVlo, sh.vready);
         if (lane == 0) tc::mbar_arrive(&sh.gempty[n % kRing]);
         END_SEGMENTS
     } else if (warp < 12) {
@@ -803,19 +824,19 @@ done:
 //     warp 0  copies   warp 1  MMAs   warp 2  decays   warps 4-7, 8-11  V' (and norms of k) of every other chunk
 //     warps 12-15  the sums over the chunks, in registers
 // ---------------------------------------------------------------------------
-constexpr int kSegStages = 6, kTold = 8;
+constexpr int kSegStages = 5, kTold = 8;
 struct SegShared {
     Gates gates[kRing];
     uint64_t full[kSegStages], empty[kSegStages];
     uint64_t gfull[kRing], gempty[kRing];
-    uint64_t vready[2], vfree[2], dfull[2], dfree[2], drain;
+    uint64_t vready[2][2], vfree[2], dfull[2], dfree[2], drain;
     uint64_t told[kTold];  // whether a chunk is its segment's last one that counts
     int stop[kTold];
     uint32_t tmem;
     volatile int dead;
 };
 constexpr int kSegStage = 2 * kTile;
-constexpr int kSegShared = kSegStages * kSegStage;
+constexpr int kSegV3 = kSegStages * kSegStage, kSegShared = kSegV3 + 2 * kTile;
 constexpr int kSegSmem = kSegShared + (int)sizeof(SegShared) + 1024;
 static_assert(kSegSmem <= 232448, "shared memory of a CTA");
 constexpr int kSegThreads = 16 * 32;
@@ -841,7 +862,8 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             tc::mbar_init(&sh.gempty[i], 4);
         }
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&sh.vready[i], 4);
+            tc::mbar_init(&sh.vready[i][0], 4);
+            tc::mbar_init(&sh.vready[i][1], 4);
             tc::mbar_init(&sh.vfree[i], 1);
             tc::mbar_init(&sh.dfull[i], 1);
             tc::mbar_init(&sh.dfree[i], 4);
@@ -899,13 +921,18 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         END_SEGMENTS
     } else if (warp == 1) {
         const bool one = tc::elect_one();
+        const uint32_t base = uniform(tc::smem_u32(sm)), tu = uniform(tm);
         FOR_FULL_SEGMENTS
         FOR_CHUNKS
         WAIT(sh.full[st], n / kSegStages);
-        WAIT(sh.vready[b], n / 2);
         if (n >= 2) WAIT(sh.dfree[b], n / 2 - 1);
-        tc::tc_fence_after();
-        mma_state(tm + b * 128, tm_vhi + b * 64, tm_vlo + b * 64, sm + st * kSegStage, one);
+        const uint32_t un = uniform(n), ub = un & 1, v = tu + 256 + ub * 64;
+#pragma unroll 1
+        for (uint32_t half = 0; half < 2; ++half) {
+            WAIT(sh.vready[b][half], n / 2);
+            tc::tc_fence_after();
+            mma_state(half, tu + ub * 128, v, v + 32, base + kSegV3 + ub * kTile, base + un % kSegStages * kSegStage, one);
+        }
         if (one) {
             tc::mma_commit(&sh.empty[st]);
             tc::mma_commit(&sh.vfree[b]);
@@ -964,9 +991,9 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         WAIT(sh.gfull[n % kRing], n / kRing);
         if (n >= 2) WAIT(sh.vfree[b], n / 2 - 1);
         tc::tc_fence_after();
-        decayed_values<NORM>(sm + st * kSegStage + kTile, sh.gates[n % kRing], warp, tm_vhi + b * 64, tm_vlo + b * 64);
+        decayed_values<NORM>(sm + st * kSegStage + kTile, sm + kSegV3 + b * kTile, sh.gates[n % kRing], warp, tm_vhi + b * 64, tm_vlo + b * 64, sh.vready[b]);
         const bool stop = sh.stop[n % kTold];
-        warp_arrive(&sh.vready[b]);
+        __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sh.gempty[n % kRing]);
         if (stop) c0 = 0;
         END_SEGMENTS

@@ -90,6 +90,30 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
+// Tries until the phase completes, `tries` times at most: each is suspended until then or for some time (4 us on this
+// device, where a suspension is asked for; mbar_try_wait returns at once).
+__device__ __forceinline__ bool mbar_wait_suspended(uint64_t *bar, uint32_t parity, int tries) {
+    uint32_t ok;
+    asm volatile(
+        "{\n"
+        ".reg .pred p, again;\n"
+        ".reg .s32 left;\n"
+        "mov.s32 left, %3;\n"
+        "TRY_%=:\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %4;\n"
+        "@p bra DONE_%=;\n"
+        "add.s32 left, left, -1;\n"
+        "setp.gt.s32 again, left, 0;\n"
+        "@again bra TRY_%=;\n"
+        "DONE_%=:\n"
+        "selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(tries), "r"(4000u)
+        : "memory");
+    return ok != 0;
+}
+
 __device__ __forceinline__ uint64_t globaltimer_ns() {
     uint64_t t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
