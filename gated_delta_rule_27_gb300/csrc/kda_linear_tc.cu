@@ -96,7 +96,7 @@ struct OutShared {
     uint64_t gfull[kRing], gempty[kRing];
     uint64_t fixed[2];                    // rows behind a segment cleared (turn by turn: V' can be a chunk ahead)
     uint64_t pfull[2], pready[2], ofull[2], ofree[2];
-    uint64_t vready[2], sready, dfree, kv, qs, pused;
+    uint64_t vready[2], kv[2], sready, dfree, qs, pused;
     uint64_t zfull[3], zfree[3];          // output tiles (and the gate's values before them)
     uint64_t ufull[kUnits], uempty[kUnits];
     uint64_t drain;
@@ -108,15 +108,12 @@ constexpr int kStage = 3 * kTile;
 constexpr int kOutP = 3 * kStage, kOutO = kOutP + 8192, kOutV3 = kOutO + 3 * kTile, kOutShared = kOutV3 + kTile;
 constexpr int kOutSmem = kOutShared + (int)sizeof(OutShared) + 1024;
 static_assert(kOutSmem <= 232448, "shared memory of a CTA");
-template <bool GATE>
-constexpr int kOutThreads = GATE ? 640 : 512;
+constexpr int kOutThreads = 640;
 // Registers a thread of each warpgroup, see more_registers.
+constexpr int kOutOthers = 72, kOutS = 184, kOutRegs = 128 * (4 * kOutOthers + kOutS);
+// The warp that issues the outputs' MMAs beside the state's (none with the gate: there warp 3 issues all).
 template <bool GATE>
-constexpr int kOutOthers = GATE ? 72 : 104;
-template <bool GATE>
-constexpr int kOutS = GATE ? 184 : 200;
-template <bool GATE>
-constexpr int kOutRegs = 128 * ((GATE ? 4 : 3) * kOutOthers<GATE> + kOutS<GATE>);
+constexpr int kOutSecond = GATE ? 3 : 16;
 
 // Tensor memory: V'^T K, S^T in bf16, V'^T in two parts, two buffers each of P (then V^T P^T) and S^T Q^T.
 enum : uint32_t { kTmD = 0, kTmSb = 128, kTmVhi = 192, kTmVlo = 224, kTmP = 256, kTmO = 384 };
@@ -203,8 +200,8 @@ __device__ __forceinline__ uint32_t tile_lane(int dim) {
 // shared memory, a tile like v's: tensor memory has no room for it beside the outputs.  The first 32 tokens are `ready`
 // before the others: their MMAs run meanwhile.
 template <bool NORM>
-__device__ __forceinline__ void decayed_values(const uint8_t *v, uint8_t *third, const Gates &g, int warp, uint32_t hi_col, uint32_t lo_col,
-                                               uint64_t *ready) {
+__device__ __forceinline__ bool decayed_values(const uint8_t *v, uint8_t *third, const Gates &g, int warp, uint32_t hi_col, uint32_t lo_col,
+                                               uint64_t *ready, uint64_t *done, int uses) {
     const int c2 = (threadIdx.x & 3) * 2, dim = (warp & 3) * 32;
     uint32_t from0 = tc::smem_u32(v) + tile_lane(dim), from1 = tc::smem_u32(v) + tile_lane(dim + 16);
     const uint32_t to_third = tc::smem_u32(third) - tc::smem_u32(v);
@@ -212,6 +209,10 @@ __device__ __forceinline__ void decayed_values(const uint8_t *v, uint8_t *third,
     lo_col += lane_base(warp);
 #pragma unroll 1
     for (int j = c2; j < kC; j += 16, from0 += 2048, from1 += 2048, hi_col += 8, lo_col += 8) {
+        if (!(j & 16) && uses > 0) {
+            if (!wait_warp(done + (j >> 5), (uint32_t)(uses - 1) & 1u)) return false;
+            tc::tc_fence_after();
+        }
         uint32_t x[2][4];
         tc::ldmatrix_t4(from0, x[0]);
         tc::ldmatrix_t4(from1, x[1]);
@@ -243,6 +244,7 @@ __device__ __forceinline__ void decayed_values(const uint8_t *v, uint8_t *third,
             warp_arrive(ready + (j >> 5));
         }
     }
+    return true;
 }
 
 // A value that all lanes of the warp have, in a register of the whole warp: what an MMA takes has to be in those, and from
@@ -326,7 +328,7 @@ __device__ __forceinline__ int next_unit(const Args &a, int u) {
 }
 
 template <bool NORM, bool GATE>
-__global__ void __launch_bounds__(kOutThreads<GATE>, 1)
+__global__ void __launch_bounds__(kOutThreads, 1)
 linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
               const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_z, const Args a) {
     extern __shared__ uint8_t smem_raw[];
@@ -336,7 +338,7 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 3; ++i) {
             tc::mbar_init(&sh.full[i], 1);
-            tc::mbar_init(&sh.empty[i], 1);
+            tc::mbar_init(&sh.empty[i], GATE ? 1 : 2);
             tc::mbar_init(&sh.zfull[i], 1);
             tc::mbar_init(&sh.zfree[i], 1);
         }
@@ -348,21 +350,22 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             tc::mbar_init(&sh.fixed[i], 4);
             tc::mbar_init(&sh.pfull[i], 1);
             tc::mbar_init(&sh.pready[i], 2);
-            tc::mbar_init(&sh.ofull[i], 1);
+            tc::mbar_init(&sh.ofull[i], GATE ? 1 : 2);
             tc::mbar_init(&sh.ofree[i], 4);
         }
         for (int i = 0; i < kUnits; ++i) {
             tc::mbar_init(&sh.ufull[i], 1);
-            tc::mbar_init(&sh.uempty[i], GATE ? 19 : 15);  // all warps but the copies'
+            tc::mbar_init(&sh.uempty[i], GATE ? 19 : 16);  // all warps at work but the copies'
         }
         tc::mbar_init(&sh.vready[0], 4);
         tc::mbar_init(&sh.vready[1], 4);
         tc::mbar_init(&sh.sready, 4);
         tc::mbar_init(&sh.dfree, 4);
-        tc::mbar_init(&sh.kv, 1);
+        tc::mbar_init(&sh.kv[0], 1);
+        tc::mbar_init(&sh.kv[1], 1);
         tc::mbar_init(&sh.qs, 1);
         tc::mbar_init(&sh.pused, 1);
-        tc::mbar_init(&sh.drain, 1);
+        tc::mbar_init(&sh.drain, GATE ? 1 : 2);
         sh.dead = 0;
         tc::fence_mbar_init();
     }
@@ -410,7 +413,7 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 
     int turn = 0;  // units so far
     int n = 0;  // chunks so far: each barrier's phase follows from it
-    if (warp < 8 || warp >= 12) fewer_registers<kOutOthers<GATE>>();
+    if (warp < 8 || warp >= 12) fewer_registers<kOutOthers>();
     if (warp == 2) {
         // ---- units, copies and decays; a chunk's decays are read while the one before it is worked on.  Documents are of
         // any length, so behind its first unit a CTA takes the next that nobody has: dealt out in turn, the CTA with the
@@ -468,10 +471,10 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             }
             u = next_unit(a, u);
         }
-    } else if (warp == 3) {
+    } else if (warp == 3 || warp == kOutSecond<GATE>) {
         // ---- MMAs, in the order in which they can start: V'^T K and S^T Q^T of a chunk, Q K^T of the next, whose scores are
-        // worked out meanwhile, V^T P^T of the first
-        const bool one = tc::elect_one();
+        // worked out meanwhile, V^T P^T of the first.
+        const bool one = tc::elect_one(), state = warp == 3, out = GATE || !state;
         const uint32_t base = uniform(tc::smem_u32(sm)), tu = uniform(tm);
         int fixes = 0, left = 0;  // tokens of the segment that are left
         for (bool more = true; more; ++n) {
@@ -481,21 +484,34 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 left = more ? sg.len : 0;
             }
             const uint32_t un = uniform(n), um = un - 1, s = um % 3, b = um & 1, before = base + s * kStage;
-            if (n > 0) {  // the products of the chunk before
+            if (state && n > 0) {  // of the chunk before
                 WAIT(sh.dfree, um);
 #pragma unroll 1
                 for (uint32_t half = 0; half < 2; ++half) {
                     WAIT(sh.vready[half], um);
                     tc::tc_fence_after();
                     mma_state(half, tu + kTmD, tu + kTmVhi, tu + kTmVlo, base + kOutV3, before + kTile, one);
+                    if (one) tc::mma_commit(&sh.kv[half]);
+                    __syncwarp();
                 }
-                if (one) tc::mma_commit(&sh.kv);
+                if (!GATE && n >= 3) WAIT(sh.ofree[b], um / 2 - 1);
                 WAIT(sh.sready, um);
                 tc::tc_fence_after();
                 const uint32_t qd = desc_lo(kKmajor, before);
 #pragma unroll(GATE ? 1 : 2)
                 for (uint32_t p = 0; p < 2; ++p) mma_ts<4>(tu + kTmO + b * 64, tu + kTmSb + p * 32, kKmajor, qd + p * 512, 2, kId64, p, one);
-                if (one) tc::mma_commit(&sh.qs);
+                if (one) {
+                    tc::mma_commit(&sh.qs);
+                    if (!GATE) {
+                        tc::mma_commit(&sh.ofull[b]);
+                        tc::mma_commit(&sh.empty[s]);
+                    }
+                }
+                __syncwarp();
+            }
+            if (!out) {
+                left -= kC;
+                continue;
             }
             // the next Q K^T waits for the output that was in its place: a quick one is gone before P is there, while
             // a gated one takes longer than P
@@ -598,14 +614,13 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             warp_arrive(&sh.gfull[n % kRing]);
         }
         WAIT(sh.gfull[n % kRing], n / kRing);
-        if (n >= 1) WAIT(sh.kv, n - 1);
-        tc::tc_fence_after();
-        decayed_values<NORM>(sm + st * kStage + 2 * kTile, sm + kOutV3, sh.gates[n % kRing], warp, tm + kTmVhi, tm + kTmVlo, sh.vready);
+        if (!decayed_values<NORM>(sm + st * kStage + 2 * kTile, sm + kOutV3, sh.gates[n % kRing], warp, tm + kTmVhi, tm + kTmVlo, sh.vready, sh.kv, n))
+            goto died;
         if (lane == 0) tc::mbar_arrive(&sh.gempty[n % kRing]);
         END_SEGMENTS
     } else if (warp < 12) {
         // ---- S
-        more_registers<kOutS<GATE>>();
+        more_registers<kOutS>();
         tc::grid_dep_wait();
         const int dv = (warp & 3) * 32 + lane;
         const uint32_t d_col = tm + kTmD + lane_base(warp), sb_col = tm + kTmSb + lane_base(warp);
@@ -617,7 +632,7 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             load_column(S, init ? init + dv : nullptr);
             for (int c0 = 0; c0 < sg.len; c0 += kC, ++n) {
                 if (c0 > 0) {
-                    WAIT(sh.kv, n - 1);
+                    WAIT(sh.kv[1], n - 1);
                     tc::tc_fence_after();
                     add_products(S, all, d_col);
                 }
@@ -640,13 +655,13 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 warp_arrive(&sh.gempty[n % kRing]);
             }
             if (sg.len > 0) {
-                WAIT(sh.kv, n - 1);
+                WAIT(sh.kv[1], n - 1);
                 tc::tc_fence_after();
                 add_products(S, all, d_col);
             }
             if (sg.last && a.S_final) store_column(S, a.S_final + ((size_t)sg.doc * a.H + h) * kDim * kDim + dv);
         }
-    } else {
+    } else if (GATE || warp < 16) {
         // ---- O; with the gated normalisation two groups of four warps, every other chunk each
         const int group = GATE ? (warp >> 2) - 3 : 0, first = 384 + group * 128, tid = (int)threadIdx.x - first;
         const int dim = (warp & 3) * 32, c2 = (lane & 3) * 2;
@@ -795,7 +810,7 @@ died:
     sh.dead = 1;
 done:
     __syncwarp();
-    if (warp == 3) {  // every MMA done before the tensor memory goes
+    if (warp == 3 || warp == kOutSecond<GATE>) {  // every MMA done before the tensor memory goes
         if (tc::elect_one()) tc::mma_commit(&sh.drain);
         __syncwarp();
         tc::mbar_wait(&sh.drain, 0);
@@ -829,7 +844,7 @@ struct SegShared {
     Gates gates[kRing];
     uint64_t full[kSegStages], empty[kSegStages];
     uint64_t gfull[kRing], gempty[kRing];
-    uint64_t vready[2][2], vfree[2], dfull[2], dfree[2], drain;
+    uint64_t vready[2][2], vfree[2][2], dfull[2], dfree[2], drain;
     uint64_t told[kTold];  // whether a chunk is its segment's last one that counts
     int stop[kTold];
     uint32_t tmem;
@@ -864,11 +879,12 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&sh.vready[i][0], 4);
             tc::mbar_init(&sh.vready[i][1], 4);
-            tc::mbar_init(&sh.vfree[i], 1);
+            tc::mbar_init(&sh.vfree[i][0], 1);
+            tc::mbar_init(&sh.vfree[i][1], 1);
             tc::mbar_init(&sh.dfull[i], 1);
             tc::mbar_init(&sh.dfree[i], 4);
         }
-        tc::mbar_init(&sh.drain, 1);
+        tc::mbar_init(&sh.drain, 2);
         sh.dead = 0;
         tc::fence_mbar_init();
     }
@@ -919,11 +935,16 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             }
         }
         END_SEGMENTS
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == 3) {
         const bool one = tc::elect_one();
         const uint32_t base = uniform(tc::smem_u32(sm)), tu = uniform(tm);
         FOR_FULL_SEGMENTS
         FOR_CHUNKS
+        if (b != warp >> 1) {
+            WAIT(sh.told[n % kTold], n / kTold);
+            if (sh.stop[n % kTold]) c0 = 0;
+            continue;
+        }
         WAIT(sh.full[st], n / kSegStages);
         if (n >= 2) WAIT(sh.dfree[b], n / 2 - 1);
         const uint32_t un = uniform(n), ub = un & 1, v = tu + 256 + ub * 64;
@@ -932,10 +953,11 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             WAIT(sh.vready[b][half], n / 2);
             tc::tc_fence_after();
             mma_state(half, tu + ub * 128, v, v + 32, base + kSegV3 + ub * kTile, base + un % kSegStages * kSegStage, one);
+            if (one) tc::mma_commit(&sh.vfree[b][half]);
+            __syncwarp();
         }
         if (one) {
             tc::mma_commit(&sh.empty[st]);
-            tc::mma_commit(&sh.vfree[b]);
             tc::mma_commit(&sh.dfull[b]);
         }
         __syncwarp();
@@ -972,7 +994,6 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         if (lane == 0) a.seg_decay[(size_t)slot * a.H + h] = nan ? __int_as_float(0x7fffffff) : exp2f(from_fixed(later));
         }
-    } else if (warp == 3) {
     } else if (warp < 12) {
         const int group = (warp >> 2) - 1;
         FOR_FULL_SEGMENTS
@@ -989,9 +1010,9 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             warp_arrive(&sh.gfull[n % kRing]);
         }
         WAIT(sh.gfull[n % kRing], n / kRing);
-        if (n >= 2) WAIT(sh.vfree[b], n / 2 - 1);
-        tc::tc_fence_after();
-        decayed_values<NORM>(sm + st * kSegStage + kTile, sm + kSegV3 + b * kTile, sh.gates[n % kRing], warp, tm_vhi + b * 64, tm_vlo + b * 64, sh.vready[b]);
+        if (!decayed_values<NORM>(sm + st * kSegStage + kTile, sm + kSegV3 + b * kTile, sh.gates[n % kRing], warp, tm_vhi + b * 64, tm_vlo + b * 64, sh.vready[b],
+                                  sh.vfree[b], n / 2))
+            goto died;
         const bool stop = sh.stop[n % kTold];
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sh.gempty[n % kRing]);
@@ -1019,7 +1040,7 @@ died:
     sh.dead = 1;
 done:
     __syncwarp();
-    if (warp == 1) {
+    if (warp == 1 || warp == 3) {
         if (tc::elect_one()) tc::mma_commit(&sh.drain);
         __syncwarp();
         tc::mbar_wait(&sh.drain, 0);
@@ -1076,9 +1097,9 @@ cudaError_t enough_registers(int threads, int wanted) {
 
 template <bool NORM, bool GATE>
 cudaError_t launch_out(const CUtensorMap *m, const Args &a, int grid, cudaStream_t st) {
-    cudaError_t e = enough_registers<linear_out_tc<NORM, GATE>>(kOutThreads<GATE>, kOutRegs<GATE>);
+    cudaError_t e = enough_registers<linear_out_tc<NORM, GATE>>(kOutThreads, kOutRegs);
     if (e == cudaSuccess) e = allow_smem<linear_out_tc<NORM, GATE>>(kOutSmem);
-    return e != cudaSuccess ? e : launch_dependent(linear_out_tc<NORM, GATE>, dim3(grid), dim3(kOutThreads<GATE>), kOutSmem, st, m[0], m[1], m[2], m[3], m[4], a);
+    return e != cudaSuccess ? e : launch_dependent(linear_out_tc<NORM, GATE>, dim3(grid), dim3(kOutThreads), kOutSmem, st, m[0], m[1], m[2], m[3], m[4], a);
 }
 template <bool NORM>
 cudaError_t launch_segment(const CUtensorMap *m, const Args &a, int grid, cudaStream_t st) {
