@@ -405,6 +405,8 @@ def kda_linear_prefill(q, k, v, g, cu_seqlens, o, S0=None, S_final=None, workspa
     [T, H, d], g [T, H] or [H]; the fused normalisations as for fusion_opts."""
     if workspace is None and torch.is_tensor(q) and torch.is_tensor(v) and v.dim() == 3 and torch.is_tensor(cu_seqlens):
         workspace = new_linear_workspace(q, v, cu_seqlens)
+        if stream is not None:  # the allocator may give it out again only behind this stream's work
+            workspace.record_stream(stream)
     rc = (_tree_calls or _tree()).linear_prefill(q, k, v, g, cu_seqlens, o, S0, S_final, workspace, stream, qk_l2norm, qk_eps,
                                                  out_gate, out_weight, out_eps)
     if rc != KDA_OK:

@@ -5,7 +5,8 @@ a type, 2^-24 for fp32 and 2^-8 for bf16):
   fp32 sums         of T terms, each with a few roundings:           (T + 64) 2^-23 of m or A
   tensor cores, o   its own rounding, and one of the scores and one of the state, which share m between them:
                     2^-8 (|o| + m)
-  tensor cores, S   k v^T's v in two parts, the second off by 2^-8 of the first's 2^-8:    2^-16 A
+  tensor cores, S   k v^T's v in three parts, all 24 bits.  A product's sum is cut off, not rounded: each of 3 T products and of the
+                    12 sums a chunk carries loses at most 2^-23 of the largest:      (4 T + 64) 2^-23 A
   rsqrt, exp2, 1/x  of the fused steps and the decays, 2^-21 of the value each
 """
 import numpy as np
@@ -47,7 +48,7 @@ def expected(x, cu, S0, fused, tensor_cores):
     T = max(1, o.shape[0])
     loose_o, loose_S = ((T + 64) * 2.0 ** -23 + 2.0 ** -20) * m, ((T + 64) * 2.0 ** -23 + 2.0 ** -20) * A
     if tensor_cores:
-        loose_o, loose_S = loose_o + 2.0 ** -8 * m, loose_S + 2.0 ** -16 * A
+        loose_o, loose_S = loose_o + 2.0 ** -8 * m, loose_S + 3 * T * 2.0 ** -23 * A
     if fused:
         o, loose_o = linear.gated(o, m, x["z"].double().numpy(), x["weight"].double().numpy(), EPS, loose_o)
     loose_o = loose_o + (HALF[x["v"].dtype] + 2.0 ** -20) * np.abs(o)
@@ -269,6 +270,21 @@ def test_streams_and_graphs(dtype, d):
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0][0], refs[1][0]) and torch.equal(outs[0][1], refs[1][1])
+
+
+def test_a_workspace_of_its_own_on_another_stream():
+    """Memory that the call takes for itself is not given out again before the other stream's work is done."""
+    x, cu, stream = inputs(4000, 4, 4, 128, BF, 47), [0, 4000], torch.cuda.Stream()
+    ref = run_prefill(x, cu)
+    on, table = {n: t.cuda() for n, t in x.items()}, i32(cu)
+    o, S = torch.empty_like(on["v"]), torch.empty((1, 4, 128, 128), device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(20_000_000)
+    libkda.kda_linear_prefill(on["q"], on["k"], on["v"], on["g"], table, o, S_final=S, stream=stream)
+    others = [libkda.new_linear_workspace(on["q"], on["v"], table).fill_(255) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert others and torch.equal(o, ref[0]) and torch.equal(S, ref[1])
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
