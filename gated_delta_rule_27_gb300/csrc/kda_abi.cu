@@ -436,7 +436,7 @@ static kda_status linear_plan(int32_t total_tokens, int32_t num_seqs, int32_t H,
     if (num_seqs < 0) return KDA_ERR_INVALID_ARG;
     *seg = kda::linear::plan_segment(total_tokens, num_seqs, H, linear_on_tensor_cores(d, dt));
     const int64_t n = total_tokens / *seg + (int64_t)num_seqs;
-    if (n * H > INT_MAX) return KDA_ERR_UNSUPPORTED;
+    if (n * H > INT_MAX - 4096) return KDA_ERR_UNSUPPORTED;  // units are counted past their end by a grid or two
     *slots = (int32_t)n;
     *lay = kda::linear::layout(n, H, d, total_tokens > *seg);
     return KDA_OK;
@@ -463,7 +463,7 @@ kda_status kda_linear_prefill(const void *q, const void *k, const void *v, const
     if (!given4(cu_seqlens)) return KDA_ERR_INVALID_ARG;
     if (total_tokens > 0) {
         if (!given16(q) || !given16(k) || !given16(v) || !given4(g) || !given16(o)) return KDA_ERR_INVALID_ARG;
-        if (o == q || o == k || o == v || o == (const void *)g) return KDA_ERR_INVALID_ARG;
+        if (o == q || o == k || o == v || o == (const void *)g || o == (const void *)S0) return KDA_ERR_INVALID_ARG;
     }
     if (!aligned16(S0) || !aligned16(S_final)) return KDA_ERR_INVALID_ARG;
     if (S_final && (S_final == q || S_final == k || S_final == v || S_final == o || S_final == (const void *)g)) return KDA_ERR_INVALID_ARG;

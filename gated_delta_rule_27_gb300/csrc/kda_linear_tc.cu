@@ -7,16 +7,24 @@
 // so each product has 128 rows (the value dimension) or the chunk's 64 tokens.  S^T stays in the registers of one warpgroup
 // for a whole segment: the tensor core cuts its sums off instead of rounding them, which a sum over thousands of tokens
 // would show (8e-6 of S after 4096 tokens), so it forms each chunk's V'^T K by itself and the sum over chunks is rounded.
-// q, k, v are read once, o is written once: 1 KB a token and head against 98 kFLOP, so HBM bounds
-// it and the work per chunk only has to hide behind the copies (a CTA with its SM's share of HBM takes 1.45 us a
-// chunk).  What a CTA does is spread over warps that each do one thing, chunk after chunk, across segments:
+// q, k, v are read once, o is written once: 1 KB a token and head against 98 kFLOP, so HBM is the bound to reach, 1.45 us a
+// chunk for a CTA with its SM's share.  The output kernel takes 1.75 (65536 tokens x 16 heads: 200 us, 5.4 TB/s; 2.6 with both
+// fused normalisations): its warps issue in half of all clocks, some 1600 instructions a chunk and SM sub-partition, and the
+// longest of the roles (V', 2400 clocks, and 200 for each of its waits) paces the others.  What a CTA does is spread over
+// warps that each do one thing, chunk after chunk, across segments:
 //     warps 0-1    P: Q K^T from tensor memory, times the decays, to shared memory in bf16
 //     warp 2       copies of q, k, v (and of the output gate) by TMA, three chunks ahead, and the decays' sums
-//     warp 3       issues all MMAs
-//     warps 4-7    the norms of q and k (fused normalisation only); V': v times its decay, in three bf16 parts (the A operand of the state's product)
+//     warp 3       issues the MMAs of the state (V'^T K, S^T Q^T)
+//     warps 4-7    the norms of q and k (fused normalisation only); V': v times its decay, in three bf16 parts (the A operand
+//                  of the state's product)
 //     warps 8-11   S: the state, decayed and added to, and its bf16 copy (the A operand of S^T Q^T)
-//     warps 12-15  O: the two parts of o added, to shared memory and out by TMA; with the gated normalisation, which takes
-//                  twice as long, another four warps take every other chunk
+//     warps 12-15  O: the two parts of o added, to shared memory and out by TMA
+//     warps 16-19  one warp that issues the outputs' MMAs (Q K^T, V^T P^T): a warp that issues all of them waits for so many
+//                  things in turn that the tensor core stands still (204 us against 200); with the gated normalisation,
+//                  which takes twice as long, O of every other chunk instead, and warp 3 issues all MMAs
+//
+// Measured and not kept: the outputs' MMAs issued by a P warp (230 us); V' by eight warps, one of which issues the state's
+// MMAs (225); more registers for V' and O (201).
 //
 // Roundings to bf16: P and the copy of S, which only reach o, itself rounded to bf16 (each adds an error of the size
 // of that rounding in its part of o).  V' reaches the state, which is fp32: it is taken in three parts, all its 24 bits.
@@ -111,11 +119,11 @@ static_assert(kOutSmem <= 232448, "shared memory of a CTA");
 constexpr int kOutThreads = 640;
 // Registers a thread of each warpgroup, see more_registers.
 constexpr int kOutOthers = 72, kOutS = 184, kOutRegs = 128 * (4 * kOutOthers + kOutS);
-// The warp that issues the outputs' MMAs beside the state's (none with the gate: there warp 3 issues all).
+// The warp that issues the outputs' MMAs.
 template <bool GATE>
 constexpr int kOutSecond = GATE ? 3 : 16;
 
-// Tensor memory: V'^T K, S^T in bf16, V'^T in two parts, two buffers each of P (then V^T P^T) and S^T Q^T.
+// Tensor memory: V'^T K, S^T in bf16, V'^T's first two parts, two buffers each of P (then V^T P^T) and S^T Q^T.
 enum : uint32_t { kTmD = 0, kTmSb = 128, kTmVhi = 192, kTmVlo = 224, kTmP = 256, kTmO = 384 };
 
 constexpr uint64_t kKmajor = tc::smem_desc_base(16, 1024, tc::SW_128B);
@@ -198,7 +206,9 @@ __device__ __forceinline__ uint32_t tile_lane(int dim) {
 // 32 lanes of V'^T (value dimensions 32 (warp % 4) on) for the chunk's tokens, in three bf16 parts: v's tile is read
 // transposed, so that a register holds two tokens of a value dimension, as the MMA wants A.  The third part goes back to
 // shared memory, a tile like v's: tensor memory has no room for it beside the outputs.  The first 32 tokens are `ready`
-// before the others: their MMAs run meanwhile.
+// before the others: their MMAs run meanwhile; and each half waits for the MMAs of the `uses`-th one in its place to be `done`.
+// False if a wait ran out.  (Two parts would do with 8 MMAs instead of 12 and take 5 to 12% less time of long prompts, but
+// their 16 bits put S off by 2.2e-6 of its size; all 24 by 4e-7, like fp32 sums.)
 template <bool NORM>
 __device__ __forceinline__ bool decayed_values(const uint8_t *v, uint8_t *third, const Gates &g, int warp, uint32_t hi_col, uint32_t lo_col,
                                                uint64_t *ready, uint64_t *done, int uses) {
@@ -473,7 +483,7 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
     } else if (warp == 3 || warp == kOutSecond<GATE>) {
         // ---- MMAs, in the order in which they can start: V'^T K and S^T Q^T of a chunk, Q K^T of the next, whose scores are
-        // worked out meanwhile, V^T P^T of the first.
+        // worked out meanwhile, V^T P^T of the first
         const bool one = tc::elect_one(), state = warp == 3, out = GATE || !state;
         const uint32_t base = uniform(tc::smem_u32(sm)), tu = uniform(tm);
         int fixes = 0, left = 0;  // tokens of the segment that are left
@@ -836,8 +846,10 @@ done:
 // never rescaled; it also leaves the segment's first rows in L2 for the pass that forms the outputs.
 // Only k and v are read: 512 bytes a token and head; and only as far back as weights are above 2^-126, below which they are
 // zero here (exp2 flushes what fp32 holds no normal number for).
-//     warp 0  copies   warp 1  MMAs   warp 2  decays   warps 4-7, 8-11  V' (and norms of k) of every other chunk
+//     warp 0  copies   warp 2  decays   warps 1, 3  MMAs, and warps 4-7, 8-11  V' (and norms of k), of every other chunk
 //     warps 12-15  the sums over the chunks, in registers
+// 65536 tokens x 16 heads, none forgotten: 100 us, 1.0 a chunk against the 0.7 of an SM's share of HBM (one warp for all MMAs:
+// 106 us); V' is the longest role here too.
 // ---------------------------------------------------------------------------
 constexpr int kSegStages = 5, kTold = 8;
 struct SegShared {

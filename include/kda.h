@@ -424,11 +424,13 @@ KDA_API kda_status kda_draft_verify(const void *logits, const float *draft_probs
  *
  * Accuracy.  bf16 at d = 128: sums are fp32; the products' operands that are
  * not inputs are bf16 -- the scores and the state where they form o (each adds
- * an error of the size of o's own rounding), and k v^T's decayed v in two parts
- * (16 bits of the 24: S is off by 2 to 4e-6 of its size, 2-norm).  Elsewhere
- * all arithmetic is fp32.  A NaN or infinity in a token's q, k or v can reach
- * the earlier outputs of its document in the same 64 tokens, but no other
- * document.
+ * an error of the size of o's own rounding) -- but for k v^T's decayed v, of
+ * which all 24 bits count (S is off by 4e-7 of its size, 2-norm).  Elsewhere
+ * all arithmetic is fp32.  Decays below 2^-126 over a run of tokens may count
+ * as 0.  A NaN or infinity in a token's q, k or v can reach the earlier outputs
+ * of its document in the same 64 tokens, but no other document.
+ * Calls that may overlap (unordered streams, graphs that run side by side) need
+ * a workspace each; calls in order on one stream may share one.
  *
  * kda_linear_decode_step: one token for each of num_active sequences.
  *   q, k, v, g, o, opts  as above with num_active rows

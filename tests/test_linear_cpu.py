@@ -39,6 +39,8 @@ def test_attention_sizes(name):
         assert call(name, **bad) == INVALID, bad
     for bad in (dict(dk=32, dv=32), dict(dk=64), dict(dk=256, dv=256), {rows: 1 << 30, "H": 4, "Hqk": 2}):
         assert call(name, **bad) == UNSUPPORTED, bad
+    if name == "kda_linear_prefill":
+        assert call(name, N=2 ** 31 - 1, T=0, H=1, Hqk=1) == UNSUPPORTED
 
 
 @pytest.mark.parametrize("name", CALLS)
@@ -61,6 +63,7 @@ def test_aliases():
         assert call("kda_linear_decode_step", o=DECODE[p]) == INVALID
         assert call("kda_linear_decode_step", S=DECODE[p]) == INVALID
     assert call("kda_linear_prefill", S=PREFILL["o"]) == INVALID
+    assert call("kda_linear_prefill", o=PREFILL["S0"]) == INVALID
     assert call("kda_linear_decode_step", S=DECODE["o"]) == INVALID
     for wrong in (dict(q_out=ROPE["k"]), dict(k_out=ROPE["q"]), dict(k_out=ROPE["q_out"]), dict(k=ROPE["q"])):
         assert call("kda_rope", **wrong) == INVALID, wrong
