@@ -161,6 +161,25 @@ __device__ __forceinline__ Sums chunk_sums(float x0, float x1) {
     return r;
 }
 
+// 2^b_64 where it is the same for chunk after chunk (one decay for a head): its rounding would be too, and add up over a
+// thousand chunks (S of 65536 tokens off by up to 1.4e-6 of a head's size instead of 3e-7).  So each factor makes up for what
+// the ones before it have left out.
+struct Decay {
+    float hi = 0.f, lo = 0.f, left = 0.f;  // the factor, in two parts; what the product of those so far lacks, relative to it
+    Decay() = default;
+    __device__ explicit Decay(long long log2) {
+        const double x = exp2((double)log2 * (1. / kFixed));
+        hi = (float)x;
+        if (x < 1e38) lo = (float)(x - hi);
+    }
+    __device__ float next() {
+        if (!(hi < 1e38f)) return hi;
+        const float more = fmaf(hi, left, lo), r = hi + more, lacks = more - (r - hi);
+        left = r > 0.f ? lacks / r : 0.f;
+        return r;
+    }
+};
+
 // 1 / sqrt(sum of squares + eps) of 16 of the tile's rows, half a row a lane.
 __device__ __forceinline__ void row_norms(const uint8_t *tile, int first, float eps, float *out) {
     const int lane = threadIdx.x & 31, r = first + (lane & 15);
@@ -429,6 +448,7 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         // any length, so behind its first unit a CTA takes the next that nobody has: dealt out in turn, the CTA with the
         // most chunks had half as many again as the mean (8 documents, 33000 tokens x 32 heads).
         float g0 = 0.f, g1 = 0.f;
+        Decay all;
         for (int u = blockIdx.x;; ++turn) {
             Segment sg;
             while (u < units && !linear::find_segment(a.cu, a.num_seqs, a.seg, u / a.H, &sg)) u = next_unit(a, u);
@@ -468,7 +488,9 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             reinterpret_cast<float2 *>(g.b)[lane] = b;
             reinterpret_cast<float2 *>(g.in)[lane] = make_float2(ex2(b.x), ex2(b.y));
             reinterpret_cast<float2 *>(g.out)[lane] = make_float2(ex2(from_fixed(s.all - s.b0)), ex2(from_fixed(s.all - s.b1)));
-            if (lane == 0) g.all = s.nan ? nan : exp2f(from_fixed(s.all));
+            if (c0 == 0 && !a.per_token) all = Decay(s.all);
+            const float x = a.per_token || rows < kC ? exp2f(from_fixed(s.all)) : all.next();
+            if (lane == 0) g.all = s.nan ? nan : x;
         }
         warp_arrive(&sh.gfull[n % kRing]);
         if (GATE) {
