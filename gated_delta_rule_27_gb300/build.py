@@ -3,7 +3,7 @@
 Each .cu file under csrc/ is compiled to an object in parallel, then linked
 into ``gated_delta_rule_27_gb300/lib/libkda.so``.  A rebuild happens only when a
 source or header is newer than the library.  The Python marshalling of the
-draft-tree calls (csrc/kda_tree_py.cpp, host code that reads torch tensors) is
+draft-tree, linear-attention and rotary calls (csrc/kda_tree_py.cpp, host code that reads torch tensors) is
 compiled next to it into ``lib/_kda_tree.so``; libkda.so itself knows no torch.
 """
 from __future__ import annotations

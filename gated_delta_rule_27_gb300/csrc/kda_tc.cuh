@@ -581,15 +581,7 @@ __device__ __forceinline__ void stmatrix_t4(uint32_t addr, const uint32_t (&r)[4
                  : "memory");
 }
 
-// Each thread of a warp writes 16 consecutive columns of its TMEM lane; tmem_wait_st() returns once the warp's writes
-// are done.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&u)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
-        "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
-        : "memory");
-}
+// Returns once the warp's writes to tensor memory are done.
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 3-D tiled TMA store of a shared-memory tile (bulk-group completion).
