@@ -406,7 +406,7 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     // S warps do.  (All of them, whatever they read: this kernel's end then means the end of the ones before it.)
     if (a.first) tc::grid_dep_wait();
     tc::grid_dep_launch();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && a.total > 0) {
         tc::prefetch_map(&tm_q);
         tc::prefetch_map(&tm_k);
         tc::prefetch_map(&tm_v);
@@ -488,8 +488,9 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             reinterpret_cast<float2 *>(g.b)[lane] = b;
             reinterpret_cast<float2 *>(g.in)[lane] = make_float2(ex2(b.x), ex2(b.y));
             reinterpret_cast<float2 *>(g.out)[lane] = make_float2(ex2(from_fixed(s.all - s.b0)), ex2(from_fixed(s.all - s.b1)));
-            if (c0 == 0 && !a.per_token) all = Decay(s.all);
-            const float x = a.per_token || rows < kC ? exp2f(from_fixed(s.all)) : all.next();
+            const bool repeats = !a.per_token && sg.len >= 2 * kC;
+            if (repeats && c0 == 0) all = Decay(s.all);
+            const float x = repeats && rows == kC ? all.next() : exp2f(from_fixed(s.all));
             if (lane == 0) g.all = s.nan ? nan : x;
         }
         warp_arrive(&sh.gfull[n % kRing]);
@@ -1146,7 +1147,7 @@ cudaError_t launch_segment(const CUtensorMap *m, const Args &a, int grid, cudaSt
 
 cudaError_t launch_linear_tc(const linear::Args &args, cudaStream_t st) {
     Args a = args;
-    CUtensorMap m[5];
+    CUtensorMap m[5] = {};
     // (a map of an empty tensor cannot be made; with no tokens nothing is copied and any map will do)
     if (a.total > 0 && (!make_map(&m[0], a.q, a.total, a.Hqk) || !make_map(&m[1], a.k, a.total, a.Hqk) || !make_map(&m[2], a.v, a.total, a.H) ||
                         !make_map(&m[3], a.o, a.total, a.H) || !make_map(&m[4], a.fu.gate ? a.fu.gate : a.o, a.total, a.H)))

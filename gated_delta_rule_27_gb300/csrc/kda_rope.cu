@@ -8,17 +8,18 @@
 // Bound by HBM: q and k are read and written once.  A block works out the sines and cosines of a few tokens once, in
 // shared memory, and turns those tokens' heads, 16 bytes a load: of two vectors half the rotated part apart, or of one that
 // holds whole pairs.  (One thread for each pair with its own sine and cosine took 53 us for 4096 tokens of 32 heads, two
-// thirds of it in the functions.)  65536 tokens x 32 heads of 128, bf16: 169 us in halves, 187 interleaved (158 at a plain copy's
-// rate): 57% of the issue slots go into addresses and turns.  4096 tokens: 15 us for 10.  (A thread that keeps its place in
-// the head and goes through the heads issues fewer instructions and took longer, 178 and 222 us.)
+// thirds of it in the functions.)  65536 tokens x 32 heads of 128, bf16: 164 us in halves, 179 interleaved (158 at a plain copy's
+// rate); 4096 tokens 15.6 and 17.2 for 9.9.  (A thread that keeps its place in the head and goes through the heads issues fewer
+// instructions and took longer: 178 us for 169 at the time, 222 for 199.)
 #include "kda_linear.cuh"
 #include "kda_tc.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;       // tokens of a block
+constexpr int kThreads = 128;       // (256 at up to 64 registers: 16.1 and 17.7 us for the 15.6 and 17.2 of 4096 tokens, 169 and 186
+                                    // for the 164 and 179 of 65536; without the bound on registers 21 and 200 interleaved)
+constexpr int kMaxTokens = 4;       // tokens of a block
 constexpr int kTable = 4096;        // sines and cosines that a block may hold
 
 template <typename Tin, int VEC>
@@ -45,7 +46,7 @@ __device__ __forceinline__ void store(Tin *p, const Vec<Tin, VEC> &v) {
 // Block (x, y): tokens x `tokens` on, heads y `heads` on (q's first, then k's).  A head is `turned` items that turn VEC
 // pairs (VEC / 2 if INTERLEAVED) and `copied` items of VEC elements behind them.
 template <typename Tin, int VEC, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, int tokens, int heads, int turned, int copied) {
+__global__ void __launch_bounds__(kThreads, 8) rope_kernel(const RopeArgs a, int tokens, int heads, int turned, int copied) {
     constexpr int W = INTERLEAVED && VEC == 1 ? 2 : VEC, kBatch = INTERLEAVED ? 4 : 2;  // elements of a load; items at once
     extern __shared__ float2 s_turn[];  // [tokens, pairs]: cosine, sine
     tc::grid_dep_launch();
@@ -128,13 +129,14 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, int to
 template <typename Tin, int VEC, bool INTERLEAVED>
 cudaError_t launch_v(const RopeArgs &a, cudaStream_t st) {
     const int pairs = a.rot / 2, all = a.Hq + a.Hk;
-    // Few tokens: a block for each and for part of its heads, so that every SM has one; else up to eight tokens, which share
-    // what a block costs (65536 tokens x 32 heads: 344 us one by one, 205 four, 192 eight).
-    int tokens = a.total / 512;
+    // Few tokens: a block for each and for part of its heads, so that every SM has eight (512 tokens x 32 heads 3.1 us; four
+    // 4.0, sixteen 3.9); else up to four tokens, which share
+    // what a block costs (65536 tokens x 32 heads, blocks of 256 threads: 344 us one by one, 205 four, 192 eight; of 128: 164 four, 165 eight).
+    int tokens = a.total / 1024;
     tokens = tokens < 1 ? 1 : tokens > kMaxTokens ? kMaxTokens : tokens;
     while (tokens > 1 && tokens * pairs > kTable) --tokens;
-    const int blocks = (a.total + tokens - 1) / tokens;
-    int parts = 152 * 2 / blocks;
+    const int blocks = (a.total - 1) / tokens + 1;
+    int parts = 152 * 8 / blocks;
     parts = parts < 1 ? 1 : parts > all ? all : parts;
     const int heads = (all + parts - 1) / parts;
     const bool in_place = (a.Hq == 0 || a.q == a.q_out) && (a.Hk == 0 || a.k == a.k_out);

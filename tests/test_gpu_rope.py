@@ -120,3 +120,16 @@ def test_graph_replay():
     positions.copy_(torch.arange(33))
     graph.replay()
     check(q, out, np.arange(33), freq, 1.0, False)
+
+
+def test_as_many_tokens_as_an_int_counts():
+    T = 2 ** 31 - 1
+    q, positions = torch.zeros((T, 1, 2), dtype=BF, device="cuda"), torch.zeros(T, dtype=torch.int32, device="cuda")
+    q[-1, 0], positions[-1] = torch.tensor([1.0, 2.0]), 5
+    last = q[-1:].cpu()
+    freq, _ = libkda.rope_frequencies(2)
+    libkda.kda_rope(q, None, positions, libkda.rope_steps(freq).cuda(), q, None)
+    check(last, q[-1:], np.array([5]), freq, 1.0, False)
+    assert not q[:-1].any()
+    del q, positions
+    torch.cuda.empty_cache()
