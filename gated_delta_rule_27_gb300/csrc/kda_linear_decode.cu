@@ -4,7 +4,7 @@
 // Bound by HBM: the fp32 state is read and written once (128 KB a sequence and head at d = 128), everything else is
 // small.  One CTA owns one state; a thread holds 16 rows of four adjacent columns, all loaded before any arithmetic.
 // The new state needs no sum over rows, so it is stored at once; o's sums over rows end in shared memory, in a fixed
-// order.  256 sequences x 32 heads, d = 128: 163 us, 6.7 TB/s, 98% of a plain copy's rate; one sequence x 16 heads 4.4 us,
+// order.  256 sequences x 32 heads, d = 128: 161 us, 6.7 TB/s, 99% of a plain copy's rate; one sequence x 16 heads 4.3 us,
 // of which 3.6 are the host's.
 #include "kda_linear.cuh"
 #include "kda_tc.cuh"
