@@ -434,7 +434,7 @@ static bool linear_on_tensor_cores(int32_t d, kda_dtype dt) { return dt == KDA_B
 static kda_status linear_plan(int32_t total_tokens, int32_t num_seqs, int32_t H, int32_t d, kda_dtype dt, int32_t *seg,
                               int32_t *slots, kda::linear::Layout *lay) {
     if (num_seqs < 0) return KDA_ERR_INVALID_ARG;
-    *seg = kda::linear::plan_segment(total_tokens, num_seqs, H, linear_on_tensor_cores(d, dt));
+    *seg = kda::linear::plan_segment(total_tokens, num_seqs, H, d, linear_on_tensor_cores(d, dt));
     const int64_t n = total_tokens / *seg + (int64_t)num_seqs;
     if (n * H > INT_MAX - 4096) return KDA_ERR_UNSUPPORTED;  // units are counted past their end by a grid or two
     *slots = (int32_t)n;

@@ -81,24 +81,35 @@ __device__ __forceinline__ const float *segment_start(const Args &a, const Segme
 // segments of all heads as there are SMs, or a small multiple of that where they do not fit the SMs well, of 256 tokens at
 // least.  Several make segments of their own by ending: the batch is cut into as many as leave an SM four in all, so that
 // the longest document leaves no SM alone for long, of 512 tokens at least (8 documents, 33000 tokens x 32 heads: 394 us in
-// pieces of 8256 tokens, 325 of 2368, 372 of 1216).  CUDA cores, which take a token some ten times as long: four segments an
-// SM, of 64 tokens at least.
-inline int plan_segment(int64_t total, int64_t num_seqs, int64_t H, bool tensor_cores) {
+// pieces of 8256 tokens, 325 of 2368, 372 of 1216).
+//
+// CUDA cores, which take a token some ten times as long: four segments an SM, of 64 tokens at least at d = 128.  Below that a
+// state is a quarter or less, and segments are short where there are few tokens (32 at least: d = 64, fp32, 5 heads, 400 tokens
+// 14.5 us for 20.7; 1501 tokens at d = 128 82 us for 56), and eight an SM where those still have 64 tokens and the four have 128
+// (33000 tokens x 32 heads, d = 64, 1260 us for 1480; 4096 x 16, d = 128, 370 for 319).
+inline int plan_segment(int64_t total, int64_t num_seqs, int64_t H, int d, bool tensor_cores) {
     constexpr int64_t kSms = 152;
-    int64_t parts = 4 * kSms / H, least = 64;
+    const auto cut = [&](int64_t parts, int64_t unit, int64_t least) {
+        const int64_t seg = parts < 1 ? total : ((total + parts - 1) / parts);
+        return seg < least ? least : (seg + unit - 1) / unit * unit;
+    };
+    int64_t seg;
     if (tensor_cores && num_seqs > 1) {
-        parts -= num_seqs;
-        least = 512;
+        seg = cut(4 * kSms / H - num_seqs, 64, 512);
     } else if (tensor_cores) {
+        int64_t parts = 0;
         for (int64_t r = 1; r <= 3; ++r) {
             parts = r * kSms / H;
             if (10 * parts * H >= 9 * r * kSms) break;
         }
-        least = 256;
+        seg = cut(parts, 64, 256);
+    } else if (d == 128) {
+        seg = cut(4 * kSms / H, 64, 64);
+    } else {
+        seg = cut(4 * kSms / H, 32, 32);
+        if (seg >= 128) seg = cut(8 * kSms / H, 32, 64);
     }
-    if (parts < 1) parts = 1;
-    const int64_t seg = ((total + parts - 1) / parts + 63) / 64 * 64;
-    return (int)(seg < least ? least : seg);
+    return (int)(seg < 0x7fffffc0 ? seg : 0x7fffffc0);
 }
 
 struct Args {
@@ -107,7 +118,7 @@ struct Args {
     int per_token;
     const int32_t *cu;
     int num_seqs, total, H, Hqk;  // head h of v reads head h / (H / Hqk) of q and k
-    int seg, slots;       // tokens of a segment (a multiple of 64), slots of segments
+    int seg, slots;       // tokens of a segment (a multiple of 64, or 32 on the CUDA cores), slots of segments
     const float *S0;      // [num_seqs, H, d, d] or null
     void *o;
     float *S_final;       // or null
