@@ -9,8 +9,8 @@
 // Arithmetic bounds it at its best, 2 d^2 multiply-adds a token and head in fp32; what it takes in fact is the registers'
 // share of shared memory, 128 bytes a clock whoever else wants the same: with one column a thread (64 bytes of k and q for
 // 8 elements) a token took 300 clocks of an SM at d = 64, with tiles of 8 x 4 it takes a quarter of that.  1501 tokens x 5 heads,
-// fp32, d = 64: 39 us for the three launches (11, 8 and 18 under a profiler), where HBM would need 0.8: 120 CTAs of four warps,
-// each of which goes through its 64 tokens one after the other.
+// fp32, d = 64: 27 us for the three launches, where HBM would need 0.8: 235 CTAs of four warps, each of which goes through its 32
+// tokens one after the other (39 us with segments of 64 tokens).
 #include "kda_linear.cuh"
 #include "kda_tc.cuh"
 
