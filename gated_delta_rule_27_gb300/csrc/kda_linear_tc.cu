@@ -86,8 +86,8 @@ __device__ __forceinline__ float rcp(float x) {
 struct __align__(16) Gates {
     float b[kC];               // sums of log-decays from the chunk's start
     float in[kC];              // 2^b: decay of the incoming state
-    float out[kC];             // 2^(b_64 - b): decay to the chunk's end; 0 behind the segment
-    float rq[kC], rk[kC];      // 1 / norm of q and k (fused normalisation only)
+    float out[kC];             // 2^(b_64 - b): decay to the chunk's end; 1 behind the segment
+    float rq[kC], rk[kC];      // 1 / norm of q and k, 0 behind the segment (fused normalisation only)
     float all, pad[3];         // 2^b_64
 };
 
@@ -180,8 +180,9 @@ struct Decay {
     }
 };
 
-// 1 / sqrt(sum of squares + eps) of 16 of the tile's rows, half a row a lane.
-__device__ __forceinline__ void row_norms(const uint8_t *tile, int first, float eps, float *out) {
+// 1 / sqrt(sum of squares + eps) of 16 of the tile's rows, half a row a lane; 0 from row n on, whose tokens are not the
+// segment's (of a cleared row without eps it would be infinite, and the product with its zeros NaN).
+__device__ __forceinline__ void row_norms(const uint8_t *tile, int first, int n, float eps, float *out) {
     const int lane = threadIdx.x & 31, r = first + (lane & 15);
     const uint8_t *row = tile + (lane >> 4) * 8192 + r * 128;
     float2 ss = make_float2(0.f, 0.f);
@@ -197,7 +198,7 @@ __device__ __forceinline__ void row_norms(const uint8_t *tile, int first, float 
     }
     float all = ss.x + ss.y;
     all += __shfl_xor_sync(0xffffffffu, all, 16);
-    out[r] = rsqrtf(all + eps);
+    out[r] = r < n ? rsqrtf(all + eps) : 0.f;
 }
 
 // Clears rows n..63 of a q, k or v tile (tokens of another document, or none): they would meet zeros in the products,
@@ -643,7 +644,7 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             if (n >= kRing) WAIT(sh.gempty[n % kRing], n / kRing - 1);
 #pragma unroll 1
             for (int k = 0; k < 2; ++k)
-                row_norms(sm + st * kStage + k * kTile, (warp & 3) * 16, a.fu.qk_eps, k ? sh.gates[n % kRing].rk : sh.gates[n % kRing].rq);
+                row_norms(sm + st * kStage + k * kTile, (warp & 3) * 16, rows, a.fu.qk_eps, k ? sh.gates[n % kRing].rk : sh.gates[n % kRing].rq);
             warp_arrive(&sh.gfull[n % kRing]);
         }
         WAIT(sh.gfull[n % kRing], n / kRing);
@@ -1041,7 +1042,7 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         WAIT(sh.full[st], n / kSegStages);
         if (NORM) {
             if (n >= kRing) WAIT(sh.gempty[n % kRing], n / kRing - 1);
-            row_norms(sm + st * kSegStage, (warp & 3) * 16, a.fu.qk_eps, sh.gates[n % kRing].rk);
+            row_norms(sm + st * kSegStage, (warp & 3) * 16, kC, a.fu.qk_eps, sh.gates[n % kRing].rk);
             warp_arrive(&sh.gfull[n % kRing]);
         }
         WAIT(sh.gfull[n % kRing], n / kRing);
