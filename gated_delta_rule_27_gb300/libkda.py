@@ -155,6 +155,16 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on(stream, allocate, *args):
+    """allocate(*args) as the given stream's memory (None: the current stream's).  The allocator hands out what is free in
+    a stream's own order: a block of another stream may still be in use there when the call starts, and one that is given
+    back right behind the call may be in use by the call when it is handed out again."""
+    if stream is None:
+        return allocate(*args)
+    with torch.cuda.stream(stream):
+        return allocate(*args)
+
+
 def kda_prefill_workspace_size(total_tokens: int, num_seqs: int, H: int, d_k: int, d_v: int, in_dtype: int,
                                chunk_size: int = 64) -> int:
     return int(load().kda_prefill_workspace_size(total_tokens, num_seqs, H, d_k, d_v, in_dtype, chunk_size))
@@ -404,9 +414,7 @@ def kda_linear_prefill(q, k, v, g, cu_seqlens, o, S0=None, S_final=None, workspa
     """Linear attention with one decay per head over packed documents (kda_linear_prefill): q, k [T, H_qk, d], v, o
     [T, H, d], g [T, H] or [H]; the fused normalisations as for fusion_opts."""
     if workspace is None and torch.is_tensor(q) and torch.is_tensor(v) and v.dim() == 3 and torch.is_tensor(cu_seqlens):
-        workspace = new_linear_workspace(q, v, cu_seqlens)
-        if stream is not None:  # the allocator may give it out again only behind this stream's work
-            workspace.record_stream(stream)
+        workspace = _on(stream, new_linear_workspace, q, v, cu_seqlens)
     rc = (_tree_calls or _tree()).linear_prefill(q, k, v, g, cu_seqlens, o, S0, S_final, workspace, stream, qk_l2norm, qk_eps,
                                                  out_gate, out_weight, out_eps)
     if rc != KDA_OK:

@@ -34,3 +34,31 @@ def test_norms_without_an_epsilon(lengths, dtype, d):
     x = inputs(sum(lengths), 4, 2, d, dtype, 73)
     S0 = 0.1 * torch.randn((len(lengths), 4, d, d), generator=torch.Generator().manual_seed(1))
     check(x, lengths, linear.unit(f64(x["q"]), 0.0), linear.unit(f64(x["k"]), 0.0), S0, qk_l2norm=True, qk_eps=0.0)
+
+
+def test_calls_on_two_streams_take_memory_of_their_own(monkeypatch):
+    """Calls without a workspace, on the current stream and on another, one right behind the other: the second must not be
+    given memory that the first one's work, still to come, is to use."""
+    lengths, H, d = [4000, 64], 4, 128
+    cu = torch.tensor(table(lengths), dtype=torch.int32, device="cuda")
+    xs = [inputs(sum(lengths), H, H, d, BF, 79 + i) for i in range(2)]
+    refs = [run_prefill(x, table(lengths)) for x in xs]
+    on = [{n: t.cuda() for n, t in x.items()} for x in xs]
+    outs = [(torch.empty_like(x["v"]), torch.empty((2, H, d, d), device="cuda")) for x in on]
+    streams, taken, allocate = [None, torch.cuda.Stream()], [], libkda.new_linear_workspace
+
+    def noted(*args):
+        workspace = allocate(*args)
+        taken.append(workspace.data_ptr())
+        return workspace
+
+    monkeypatch.setattr(libkda, "new_linear_workspace", noted)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(2_000_000)
+    for _ in range(20):
+        for x, (o, S), stream in zip(on, outs, streams):
+            libkda.kda_linear_prefill(x["q"], x["k"], x["v"], x["g"], cu, o, S_final=S, stream=stream)
+    torch.cuda.synchronize()
+    assert not set(taken[0::2]) & set(taken[1::2])
+    for out, ref in zip(outs, refs):
+        assert torch.equal(out[0], ref[0]) and torch.equal(out[1], ref[1])
