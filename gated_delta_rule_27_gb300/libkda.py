@@ -178,7 +178,7 @@ def kda_prefill_chunked(q, k, v, g, beta, cu_seqlens, o, S0=None, S_final=None, 
     N = cu_seqlens.numel() - 1
     dt = _dtype_code(q)
     if workspace is None:
-        workspace = new_workspace(T, N, H, d_k, d_v, dt, chunk_size, q.device)
+        workspace = _on(stream, new_workspace, T, N, H, d_k, d_v, dt, chunk_size, q.device)
     rc = load().kda_prefill_chunked(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens), N, T, H,
                                     d_k, d_v, dt, chunk_size, _ptr(S0), _ptr(o), _ptr(S_final), _ptr(workspace),
                                     workspace.numel() * workspace.element_size(), _stream(stream))
@@ -200,7 +200,7 @@ def kda_prefill_chunked_profiled(q, k, v, g, beta, cu_seqlens, o, events, S0=Non
     N = cu_seqlens.numel() - 1
     dt = _dtype_code(q)
     if workspace is None:
-        workspace = new_workspace(T, N, H, d_k, d_v, dt, chunk_size, q.device)
+        workspace = _on(stream, new_workspace, T, N, H, d_k, d_v, dt, chunk_size, q.device)
     n_ev = PREFILL_MAX_KERNELS + 1
     ev_arr = (ctypes.c_void_p * n_ev)(*[ctypes.c_void_p(e.cuda_event) for e in events[:n_ev]])
     n_k = ctypes.c_int32(0)
@@ -261,7 +261,7 @@ def kda_prefill_chunked_ex(q, k, v, g, beta, cu_seqlens, o, S0=None, S_final=Non
     N = cu_seqlens.numel() - 1
     dt = _dtype_code(q)
     if workspace is None:
-        workspace = new_workspace(T, N, H, d_k, d_v, dt, chunk_size, q.device)
+        workspace = _on(stream, new_workspace, T, N, H, d_k, d_v, dt, chunk_size, q.device)
     opts = fusion_opts(**fusion)
     rc = load().kda_prefill_chunked_ex(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens), N, T, H,
                                        d_k, d_v, dt, chunk_size, _ptr(S0), _ptr(o), _ptr(S_final), _ptr(workspace),
@@ -492,19 +492,20 @@ def new_workspace(T, N, H, d_k, d_v, in_dtype, chunk_size, device) -> torch.Tens
 
 
 def prefill(q, k, v, g, beta, cu_seqlens, S0=None, chunk_size=64, want_state=True, workspace=None, stream=None):
-    """Allocates o (and S_final) with torch and runs kda_prefill_chunked; returns (o, S_final)."""
+    """Allocates o (and S_final) with torch, as the stream's memory, and runs kda_prefill_chunked; returns (o, S_final)."""
     T, H, d_k = q.shape
     N = cu_seqlens.numel() - 1
-    o = torch.empty((T, H, v.shape[2]), dtype=v.dtype, device=q.device)
-    S_final = torch.empty((N, H, d_k, v.shape[2]), dtype=torch.float32, device=q.device) if want_state else None
+    fresh = lambda shape, dtype: _on(stream, lambda: torch.empty(shape, dtype=dtype, device=q.device))  # noqa: E731
+    o = fresh((T, H, v.shape[2]), v.dtype)
+    S_final = fresh((N, H, d_k, v.shape[2]), torch.float32) if want_state else None
     kda_prefill_chunked(q, k, v, g, beta, cu_seqlens, o, S0=S0, S_final=S_final, workspace=workspace,
                         chunk_size=chunk_size, stream=stream)
     return o, S_final
 
 
 def decode_step(q, k, v, g, beta, S_inout, stream=None):
-    """Allocates o with torch, runs kda_decode_step (S_inout updated in place); returns o."""
-    o = torch.empty_like(v)
+    """Allocates o with torch, as the stream's memory, runs kda_decode_step (S_inout updated in place); returns o."""
+    o = _on(stream, torch.empty_like, v)
     kda_decode_step(q, k, v, g, beta, S_inout, o, stream=stream)
     return o
 

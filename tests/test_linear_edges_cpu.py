@@ -1,4 +1,4 @@
-"""Linear attention's binding and limits where they went wrong once, without a GPU."""
+"""The binding and its limits where they went wrong once, without a GPU."""
 import contextlib
 import types
 
@@ -9,8 +9,16 @@ from gated_delta_rule_27_gb300 import libkda
 from tests.test_linear_cpu import GIVEN
 
 
+Q = torch.zeros(3, 4, 64)
+DELTA = dict(q=Q, k=Q, v=Q, g=Q, beta=torch.zeros(3, 4), cu_seqlens=torch.zeros(2, dtype=torch.int32), o=Q)
+CALLS = {"kda_linear_prefill": ("new_linear_workspace", {**GIVEN["kda_linear_prefill"], "workspace": None}),
+         "kda_prefill_chunked": ("new_workspace", DELTA), "kda_prefill_chunked_ex": ("new_workspace", DELTA),
+         "kda_prefill_chunked_profiled": ("new_workspace", {**DELTA, "events": []})}
+
+
+@pytest.mark.parametrize("name", CALLS)
 @pytest.mark.parametrize("given", [False, True])
-def test_a_workspace_is_the_stream_s_own(monkeypatch, given):
+def test_a_workspace_is_the_stream_s_own(monkeypatch, name, given):
     """Scratch that a call takes for itself is allocated with the call's stream as the current one."""
     current, taken, stream = [], [], types.SimpleNamespace(cuda_stream=1)
 
@@ -25,8 +33,30 @@ def test_a_workspace_is_the_stream_s_own(monkeypatch, given):
         return torch.zeros(256, dtype=torch.uint8)
 
     monkeypatch.setattr(torch.cuda, "stream", on)
-    monkeypatch.setattr(libkda, "new_linear_workspace", allocate)
-    args = {**GIVEN["kda_linear_prefill"], "workspace": None}
-    with pytest.raises(ValueError, match="device tensors"):  # (the binding's answer to tensors on the host)
-        libkda.kda_linear_prefill(**args, stream=stream if given else None)
+    allocator, args = CALLS[name]
+    monkeypatch.setattr(libkda, allocator, allocate)
+    with pytest.raises((ValueError, IndexError)):  # (the binding's answers to tensors on the host, and to no events)
+        getattr(libkda, name)(**args, stream=stream if given else None)
     assert taken == [stream if given else None] and not current
+
+
+@pytest.mark.parametrize("name,outputs", [("prefill", 2), ("decode_step", 1)])
+def test_outputs_are_the_stream_s_own(monkeypatch, name, outputs):
+    current, taken = [], []
+
+    @contextlib.contextmanager
+    def on(s):
+        current.append(s)
+        yield
+        current.pop()
+
+    def noted(allocate):
+        return lambda *args, **kw: (taken.append(current[-1] if current else None), allocate(*args, **kw))[1]
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(libkda, "kda_prefill_chunked", lambda *args, **kw: None)
+    monkeypatch.setattr(libkda, "kda_decode_step", lambda *args, **kw: None)
+    for f in ("empty", "empty_like"):
+        monkeypatch.setattr(torch, f, noted(getattr(torch, f)))
+    getattr(libkda, name)(Q, Q, Q, Q, torch.zeros(3, 4), torch.zeros(2, dtype=torch.int32), stream="one")
+    assert taken == ["one"] * outputs
