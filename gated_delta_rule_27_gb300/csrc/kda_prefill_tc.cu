@@ -567,8 +567,9 @@ __device__ bool prepare_unit(const PrepParams &p, int slot, int h, int t0, int L
         sk2 += __shfl_xor_sync(0xffffffffu, sk2, 2);
         sq2 += __shfl_xor_sync(0xffffffffu, sq2, 2);
         if (qd == 0) {
-            s_invk[r] = rsqrtf(sk2 + p.qk_eps);
-            s_invq[r] = rsqrtf(sq2 + p.qk_eps);
+            // (0 past the chunk's end: without an epsilon a row of zeros there would make it infinite, and their product NaN)
+            s_invk[r] = r < Lc ? rsqrtf(sk2 + p.qk_eps) : 0.f;
+            s_invq[r] = r < Lc ? rsqrtf(sq2 + p.qk_eps) : 0.f;
         }
         grp.sync();
     }
