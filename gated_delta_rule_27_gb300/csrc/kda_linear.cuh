@@ -128,6 +128,7 @@ struct Args {
     int32_t *ticket;      // the output kernel's next unit (null: units are dealt out in turn)
     int aliased;          // S_final is S0: a document of several segments starts from a copy of it
     int first;            // whether the kernel is its call's first, which sets the status word
+    int withheld;         // in tests of waits that run out only (tensor cores): no chunk's decays are published
     Fusion fu;
 };
 

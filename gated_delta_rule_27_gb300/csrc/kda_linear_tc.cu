@@ -49,13 +49,16 @@ constexpr int kRing = 4;  // chunks whose decays are kept
 constexpr int kUnits = 4;  // units known ahead
 
 // A whole warp's wait.  One that runs out, after about a second (each try is suspended for 4 us), ends the warp's work, and
-// so the waits of the others, one second on.  The loop is small on purpose, see tile_lane.
+// so the waits of the others, one second on: until all have left their work, warps meet at such waits only, or as at MEET below.
+// (The outputs' kernel waits for the segments' within that second: their launch takes 25 ms for as many tokens as memory
+// holds.)  The loop is small on purpose, see tile_lane.
 constexpr int kTries = 1 << 18;
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, tc::mbar_wait_suspended(bar, parity, kTries));
 }
 #define WAIT(bar, n_uses) \
-    if (!wait_warp(&(bar), (uint32_t)(n_uses) & 1u)) goto died
+    if (!wait_warp(&(bar), (uint32_t)(n_uses) & 1u)) goto LEAVE
+#define LEAVE died
 
 // One arrival for the warp, once all its lanes are here.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
@@ -110,7 +113,7 @@ struct OutShared {
     uint64_t drain;
     Unit unit[kUnits];
     uint32_t tmem;
-    volatile int dead;
+    volatile int dead, left[2];  // whether a wait has run out: any warp's, one's of a group of O
 };
 constexpr int kStage = 3 * kTile;
 constexpr int kOutP = 3 * kStage, kOutO = kOutP + 8192, kOutV3 = kOutO + 3 * kTile, kOutShared = kOutV3 + kTile;
@@ -382,6 +385,7 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             tc::mbar_init(&sh.pready[i], 2);
             tc::mbar_init(&sh.ofull[i], GATE ? 1 : 2);
             tc::mbar_init(&sh.ofree[i], 4);
+            sh.left[i] = 0;
         }
         for (int i = 0; i < kUnits; ++i) {
             tc::mbar_init(&sh.ufull[i], 1);
@@ -494,7 +498,7 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             const float x = repeats && rows == kC ? all.next() : exp2f(from_fixed(s.all));
             if (lane == 0) g.all = s.nan ? nan : x;
         }
-        warp_arrive(&sh.gfull[n % kRing]);
+        if (!a.withheld) warp_arrive(&sh.gfull[n % kRing]);
         if (GATE) {
             if (n >= 3) WAIT(sh.zfree[st], n / 3 - 1);
             if (lane == 0) {
@@ -636,8 +640,8 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             clear_rows(sm + st * kStage + kTile, rows, threadIdx.x - 128, 128);
             clear_rows(sm + st * kStage + 2 * kTile, rows, threadIdx.x - 128, 128);
             tc::fence_async_smem();
-            tc::named_barrier(1, 128);
-            if (lane == 0) tc::mbar_arrive(&sh.fixed[fixes & 1]);
+            warp_arrive(&sh.fixed[fixes & 1]);
+            WAIT(sh.fixed[fixes & 1], fixes >> 1);
             ++fixes;
         }
         if (NORM) {
@@ -701,6 +705,15 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         const int dim = (warp & 3) * 32, c2 = (lane & 3) * 2;
         float (&red)[4][kC] = sh.red[group], (&rms)[kC] = sh.rms[group];
         int going = -1;  // the tile whose copy out is not known to have read it
+// All four warps of the group here, with what they have written for each other.  The barrier has no limit of its own: a warp
+// whose wait has run out says so and arrives once more, so that the others, each of which gets here or gives up in the end, are
+// all let go, see it, and follow it.  That is looked at where a chunk's waits lie before the barrier; none lies between its others.
+#define MEET tc::named_barrier(2 + group, 128)
+#define MEET_BEHIND_WAITS \
+    MEET;                 \
+    if (sh.left[group]) goto LEAVE
+#undef LEAVE
+#define LEAVE left_behind
         float2 weight[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)};  // of dimensions dim + 16 h + lane / 4 and 8 on
         if (GATE && a.fu.weight)
             for (int h = 0; h < 2; ++h)
@@ -767,12 +780,12 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     y += __shfl_xor_sync(0xffffffffu, y, 16);
                     if (lane < 16) red[warp & 3][i + (up1 ? 8 : 0) + c2 + (up2 ? 1 : 0)] = y;
                 }
-                tc::named_barrier(2 + group, 128);
+                MEET_BEHIND_WAITS;
                 if (tid < kC) {
                     const int i = tid;
                     rms[i] = rsqrtf(((red[0][i] + red[1][i]) + (red[2][i] + red[3][i])) * (1.f / kDim) + a.fu.out_eps);
                 }
-                tc::named_barrier(2 + group, 128);
+                MEET;
             }
 #pragma unroll 1
             for (int i = 0; i < kC; i += 16) {
@@ -800,7 +813,11 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         if (lane == 0) tc::mbar_arrive(&sh.gempty[n % kRing]);
         tc::fence_async_smem();
-        tc::named_barrier(2 + group, 128);
+        if (GATE) {
+            MEET;
+        } else {
+            MEET_BEHIND_WAITS;
+        }
         // a tile is free again once its copy out has read it: seen to when the next one is on its way
         if (rows == kC) {
             if (tid == 0) {
@@ -826,7 +843,7 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     *reinterpret_cast<const uint4 *>(tile + (c >> 3) * 8192 + t * 128 + (((c & 7) ^ (t & 7)) << 4));
             }
             tc::fence_async_smem();
-            tc::named_barrier(2 + group, 128);
+            MEET;
             if (tid == 0) {
                 if (going >= 0) {
                     tc::bulk_wait_read();
@@ -838,6 +855,15 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         __syncwarp();
         END_SEGMENTS
+        goto done;
+    left_behind:
+        sh.left[group] = 1;
+        __threadfence_block();
+        __syncwarp();
+        tc::named_barrier_arrive(2 + group, 128);
+        goto died;
+#undef LEAVE
+#define LEAVE died
     }
     goto done;
 died:
@@ -1024,7 +1050,7 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         nan = nan || s.nan;
         const bool stop = c0 == 0 || (!nan && later < kGone);
         if (lane == 0) sh.stop[n % kTold] = stop;
-        warp_arrive(&sh.gfull[n % kRing]);
+        if (!a.withheld) warp_arrive(&sh.gfull[n % kRing]);
         if (lane == 0) tc::mbar_arrive(&sh.told[n % kTold]);
         if (stop) c0 = 0;
         }
@@ -1159,6 +1185,7 @@ cudaError_t launch_linear_tc(const linear::Args &args, cudaStream_t st) {
     const int64_t units = (int64_t)a.slots * a.H;
     const int grid = (int)(units < sms ? units : sms);
     a.first = 1;
+    a.withheld = testing_fault() == kFaultNoPublish;
     if (a.total > a.seg) {  // some document may have more than one segment
         e = a.fu.qk_norm ? launch_segment<true>(m, a, grid, st) : launch_segment<false>(m, a, grid, st);
         if (e == cudaSuccess) e = launch_linear_chain(a, kDim, st);

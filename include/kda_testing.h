@@ -9,7 +9,7 @@
  * while the context stays usable.
  *
  * Both hooks set process-wide state that every later kda_prefill_chunked (the
- * fault: or kda_draft_verify) call on any thread reads at launch time; a test
+ * fault: or kda_draft_verify, or kda_linear_prefill) call on any thread reads at launch time; a test
  * must restore the defaults (plan -1, fault KDA_TESTING_FAULT_NONE with wait
  * limit 0) when it is done.
  */
@@ -40,7 +40,9 @@ KDA_API kda_status kda_testing_set_plan(int32_t plan);
 #define KDA_TESTING_FAULT_NO_PUBLISH 1  /* chain and pipe plans: the state chains publish none of their state
                                            images, so the output units' bounded waits on them run out;
                                            draft verification: the last CTA of each request that has several
-                                           sends nothing to the others, whose waits for it run out */
+                                           sends nothing to the others, whose waits for it run out;
+                                           linear prefill on the tensor cores: the decays of no chunk are published
+                                           to the CTA's other warps, whose waits run out */
 #define KDA_TESTING_FAULT_CHUNK_TABLE 2 /* bounds-checking build (libkda_debug.so) only: the chunk table claims
                                            1000 chunks more than exist, which the kernels' bounds checks must
                                            catch (KDA_ERR_BOUNDS); the release build ignores this fault */
@@ -48,8 +50,9 @@ KDA_API kda_status kda_testing_set_plan(int32_t plan);
 /*
  * Injects `fault` into later calls and bounds the device-side waits on
  * another CTA's publication flag by `wait_limit_ns` nanoseconds (0 keeps the
- * default of two seconds, in the draft verification one).  KDA_ERR_INVALID_ARG for an unknown fault or a
- * negative limit.
+ * default of two seconds, in the draft verification one; the linear prefill's
+ * waits of one warp on another always take one).  KDA_ERR_INVALID_ARG for an
+ * unknown fault or a negative limit.
  */
 KDA_API kda_status kda_testing_set_fault(int32_t fault, int64_t wait_limit_ns);
 
