@@ -11,6 +11,8 @@
 // 8 elements) a token took 300 clocks of an SM at d = 64, with tiles of 8 x 4 it takes a quarter of that.  1501 tokens x 5 heads,
 // fp32, d = 64: 27 us for the three launches, where HBM would need 0.8: 235 CTAs of four warps, each of which goes through its 32
 // tokens one after the other (39 us with segments of 64 tokens).
+#include <type_traits>
+
 #include "kda_linear.cuh"
 #include "kda_tc.cuh"
 
@@ -20,7 +22,7 @@ namespace {
 using linear::Args;
 using linear::Segment;
 
-constexpr float kGentle = 24.f;  // largest log2 of a decay over the staged tokens that the state's units may follow
+constexpr float kGentle = 24.f;  // largest range of the decays' sums (log2) over the staged tokens that the state's units may follow
 
 // A thread's tile: kRows x kCols of the state; the D / kRows threads of a column are neighbours in a warp, and hold a sum for
 // each of two tokens' kCols columns in the end.
@@ -51,7 +53,7 @@ linear_simt_kernel(const Args a) {
     using T = Tile<D>;
     constexpr int NT = T::kThreads, R = T::kRows, C = T::kCols, kTok = T::kTok, kWarps = NT / 32;
     __shared__ __align__(16) float s_q[kTok][D], s_k[kTok][D], s_v[kTok][D], s_o[OUT ? kTok : 1][D];
-    __shared__ float s_a[kTok], s_in[kTok], s_out[kTok];
+    __shared__ float s_a[kTok], s_in[kTok], s_out[kTok], s_first;
     __shared__ bool s_gentle;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int part = tid % T::kLanes, row0 = part * R, col0 = tid / T::kLanes * C;
@@ -100,6 +102,7 @@ linear_simt_kernel(const Args a) {
             const size_t at = (size_t)(row0 + 2 * r) * D + col0 + c;
             S[r][c] = init ? make_float2(init[at], init[at + D]) : make_float2(0.f, 0.f);
         }
+    float unit = 1.f;  // of the state in S
     for (int c0 = 0; c0 < sg.len; c0 += kTok) {
         const int n = min(kTok, sg.len - c0);
 #pragma unroll
@@ -117,16 +120,20 @@ linear_simt_kernel(const Args a) {
                 if (tid >= off) b += up;
             }
             total += (double)__shfl_sync(0xffffffffu, b, kTok - 1);
-            float most = tid < kTok ? fabsf(b) : 0.f;  // (growth and decay may cancel in the whole)
-            const bool nan = __any_sync(0xffffffffu, b != b);
-#pragma unroll
-            for (int off = 16; off; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+            // the least and the most of 0 and the sums (as integers: bits of floats of one sign are in their absolute values' order)
+            const float mine = tid < kTok ? b : 0.f;
+            const float least = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fminf(mine, 0.f))));
+            const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(mine, 0.f))));
+            const bool gentle = !__any_sync(0xffffffffu, b != b) && most - least < kGentle;
             if (tid < kTok) {
                 s_a[tid] = tid < n ? exp2f(ng) : 1.f;
-                s_in[tid] = exp2f(b);
-                s_out[tid] = exp2f(-b);
+                s_in[tid] = exp2f(b - least);
+                s_out[tid] = exp2f(least - b);
             }
-            if (tid == 0) s_gentle = !nan && most < kGentle;
+            if (tid == 0) {
+                s_gentle = gentle;
+                s_first = exp2f(least);
+            }
         }
         __syncthreads();
         if (c0 + kTok < sg.len) fetch(c0 + kTok);
@@ -140,72 +147,79 @@ linear_simt_kernel(const Args a) {
             }
             __syncthreads();
         }
-        // The state is kept in units of the decay since the first of these tokens, where that is not so strong that the
-        // units overflow: it saves the product with each token's decay, and the rounding of that decay, which a slow one
-        // would pile up token after token.
+        // The state is kept in units of the decay since the first of these tokens, where that is not too strong: it saves the
+        // product with each token's decay, and the rounding of that decay, which a slow one would pile up token after token.
+        // The unit is the smallest of those decays (the last one's, unless something grows), so that nothing is above what the
+        // recurrence itself holds; what falls below fp32's numbers by it is 2^-125 at most.
         const bool gentle = s_gentle;
-#pragma unroll(D == 128 ? 1 : 4)
-        for (int t0 = 0; t0 < n; t0 += 2) {
-            float x[2 * C];
+        const float change = gentle ? unit * s_first : unit;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int t = t0 + u;
-                float vv[C];
+        for (int r = 0; r < R / 2; ++r)
 #pragma unroll
-                for (int c = 0; c < C; c += 2) *reinterpret_cast<float2 *>(vv + c) = *reinterpret_cast<const float2 *>(&s_v[t][col0 + c]);
-                if (gentle) {
-                    const float w = s_out[t];
+            for (int c = 0; c < C; ++c) S[r][c] = tc::mul2(S[r][c], make_float2(change, change));
+        unit = gentle ? s_in[n - 1] : 1.f;
+        // (A loop for each kind, and two pairs of tokens unrolled: 33000 tokens x 32 heads, d = 64, bf16 1190 us, with the choice
+        // inside 1250; 1501 x 16 40 us, without unrolling 50, with four pairs 44.)
+        const auto tokens = [&](auto kind) {
+            constexpr bool gentle = decltype(kind)::value;
+#pragma unroll(D == 128 ? 1 : 2)
+            for (int t0 = 0; t0 < n; t0 += 2) {
+                float x[2 * C];
 #pragma unroll
-                    for (int c = 0; c < C; ++c) vv[c] *= w;
-                } else {
-                    const float2 av = make_float2(s_a[t], s_a[t]);
+                for (int u = 0; u < 2; ++u) {
+                    const int t = t0 + u;
+                    float vv[C];
 #pragma unroll
-                    for (int r = 0; r < R / 2; ++r)
+                    for (int c = 0; c < C; c += 2) *reinterpret_cast<float2 *>(vv + c) = *reinterpret_cast<const float2 *>(&s_v[t][col0 + c]);
+                    if (gentle) {
+                        const float w = s_out[t];
 #pragma unroll
-                        for (int c = 0; c < C; ++c) S[r][c] = tc::mul2(av, S[r][c]);
-                }
-                float2 acc[C];
+                        for (int c = 0; c < C; ++c) vv[c] *= w;
+                    } else {
+                        const float2 av = make_float2(s_a[t], s_a[t]);
 #pragma unroll
-                for (int c = 0; c < C; ++c) acc[c] = make_float2(0.f, 0.f);
+                        for (int r = 0; r < R / 2; ++r)
 #pragma unroll
-                for (int r = 0; r < R / 2; r += 2) {
-                    const float4 kk = *reinterpret_cast<const float4 *>(&s_k[t][row0 + 2 * r]);
-                    const float4 qq = OUT ? *reinterpret_cast<const float4 *>(&s_q[t][row0 + 2 * r]) : kk;
+                            for (int c = 0; c < C; ++c) S[r][c] = tc::mul2(av, S[r][c]);
+                    }
+                    float2 acc[C];
 #pragma unroll
-                    for (int c = 0; c < C; ++c) {
-                        const float2 vc = make_float2(vv[c], vv[c]);
-                        S[r][c] = tc::fma2(make_float2(kk.x, kk.y), vc, S[r][c]);
-                        S[r + 1][c] = tc::fma2(make_float2(kk.z, kk.w), vc, S[r + 1][c]);
-                        if (OUT) {
-                            acc[c] = tc::fma2(make_float2(qq.x, qq.y), S[r][c], acc[c]);
-                            acc[c] = tc::fma2(make_float2(qq.z, qq.w), S[r + 1][c], acc[c]);
+                    for (int c = 0; c < C; ++c) acc[c] = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int r = 0; r < R / 2; r += 2) {
+                        const float4 kk = *reinterpret_cast<const float4 *>(&s_k[t][row0 + 2 * r]);
+                        const float4 qq = OUT ? *reinterpret_cast<const float4 *>(&s_q[t][row0 + 2 * r]) : kk;
+#pragma unroll
+                        for (int c = 0; c < C; ++c) {
+                            const float2 vc = make_float2(vv[c], vv[c]);
+                            S[r][c] = tc::fma2(make_float2(kk.x, kk.y), vc, S[r][c]);
+                            S[r + 1][c] = tc::fma2(make_float2(kk.z, kk.w), vc, S[r + 1][c]);
+                            if (OUT) {
+                                acc[c] = tc::fma2(make_float2(qq.x, qq.y), S[r][c], acc[c]);
+                                acc[c] = tc::fma2(make_float2(qq.z, qq.w), S[r + 1][c], acc[c]);
+                            }
                         }
                     }
+#pragma unroll
+                    for (int c = 0; c < C; ++c) x[u * C + c] = acc[c].x + acc[c].y;
                 }
+                if (OUT) {
 #pragma unroll
-                for (int c = 0; c < C; ++c) x[u * C + c] = acc[c].x + acc[c].y;
-            }
-            if (OUT) {
+                    for (int half = C; half; half >>= 1) {
+                        const bool up = part & half;
 #pragma unroll
-                for (int half = C; half; half >>= 1) {
-                    const bool up = part & half;
-#pragma unroll
-                    for (int i = 0; i < half; ++i) {
-                        const float give = up ? x[i] : x[i + half], keep = up ? x[i + half] : x[i];
-                        x[i] = keep + __shfl_xor_sync(0xffffffffu, give, half);
+                        for (int i = 0; i < half; ++i) {
+                            const float give = up ? x[i] : x[i + half], keep = up ? x[i + half] : x[i];
+                            x[i] = keep + __shfl_xor_sync(0xffffffffu, give, half);
+                        }
                     }
+                    const int t = t0 + part / C;  // the lane's sum is token part / C's of column part % C
+                    s_o[t][col0 + part % C] = gentle ? x[0] * s_in[t] : x[0];
                 }
-                const int t = t0 + part / C;  // the lane's sum is token part / C's of column part % C
-                s_o[t][col0 + part % C] = gentle ? x[0] * s_in[t] : x[0];
             }
-        }
-        if (gentle) {
-            const float2 end = make_float2(s_in[n - 1], s_in[n - 1]);
-#pragma unroll
-            for (int r = 0; r < R / 2; ++r)
-#pragma unroll
-                for (int c = 0; c < C; ++c) S[r][c] = tc::mul2(S[r][c], end);
-        }
+        };
+        if (gentle) tokens(std::true_type());
+        else tokens(std::false_type());
         __syncthreads();
         if (OUT) {
             Tin *o = static_cast<Tin *>(a.o);
@@ -234,8 +248,8 @@ linear_simt_kernel(const Args a) {
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const size_t at = (size_t)(row0 + 2 * r) * D + col0 + c;
-                to[at] = S[r][c].x;
-                to[at + D] = S[r][c].y;
+                to[at] = S[r][c].x * unit;
+                to[at + D] = S[r][c].y * unit;
             }
     }
     if (!OUT && tid == 0) a.seg_decay[(size_t)slot * a.H + h] = exp2f((float)total);

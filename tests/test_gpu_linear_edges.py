@@ -17,7 +17,7 @@ def table(lengths):
 
 
 def check(x, lengths, q, k, S0=None, **more):
-    """A prefill of x against the recurrence over q, k in 64 bits."""
+    """A prefill of x against the recurrence over q, k in 64 bits; returns the largest of the sums over absolute values."""
     cu, dtype, d = table(lengths), x["v"].dtype, x["v"].shape[-1]
     o, S = run_prefill(x, cu, S0, **more)
     ref_o, ref_S, m, A = linear.attention(q, k, f64(x["v"]), f64(x["g"]), cu, None if S0 is None else f64(S0))
@@ -25,6 +25,7 @@ def check(x, lengths, q, k, S0=None, **more):
     sums = (T + 64) * 2.0 ** -23 + 2.0 ** -20
     within(o, ref_o, (sums + (2.0 ** -8 if tensor_cores else 0)) * m + (HALF[dtype] + 2.0 ** -20) * np.abs(ref_o), "o")
     within(S, ref_S, (sums + (3 * T * 2.0 ** -23 if tensor_cores else 0)) * A, "S")
+    return max(m.max(), A.max())
 
 
 @pytest.mark.parametrize("lengths", [[1], [63], [64], [65], [77], [65, 1, 0, 77, 63], [900]], ids=str)
@@ -62,3 +63,16 @@ def test_calls_on_two_streams_take_memory_of_their_own(monkeypatch):
     assert not set(taken[0::2]) & set(taken[1::2])
     for out, ref in zip(outs, refs):
         assert torch.equal(out[0], ref[0]) and torch.equal(out[1], ref[1])
+
+
+@pytest.mark.parametrize("kind", ["decays", "grows", "both"])
+@pytest.mark.parametrize("dtype,d", [(F32, 16), (F32, 64), (F32, 128), (BF, 16), (BF, 128)])
+def test_values_near_the_largest(dtype, d, kind):
+    """Twenty bits of decay over 32 tokens, growth, and growth behind decay, of values whose sums stay below fp32's largest even
+    if all terms had one sign: nothing on the way may overflow."""
+    x = inputs(400, 2, 1, d, dtype, 89)
+    g = {"decays": torch.full((400,), -0.4), "grows": torch.full((400,), 0.1), "both": torch.where(torch.arange(400) % 30 < 15, -0.4, 0.4)}[kind]
+    x["g"] = g[:, None].expand(400, 2).contiguous()
+    x["v"] = (x["v"].float() * 2.0 ** {"decays": 115, "grows": 70, "both": 104}[kind]).to(dtype)
+    most = check(x, [150, 250], f64(x["q"]), f64(x["k"]))
+    assert most < 2.0 ** 127
