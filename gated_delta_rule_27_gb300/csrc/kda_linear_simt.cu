@@ -46,15 +46,17 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
-// OUT: the outputs and final states; else what each segment but a document's last adds to the state.
+// OUT: the outputs and final states; else what each segment but a document's last adds to the state.  (Three blocks an SM have to
+// be asked for where the compiler aims at four, with 128 registers and some spilled: 1501 tokens x 5 heads 27.4 us, else 29.8.)
 template <typename Tin, int D, bool OUT>
-__global__ void __launch_bounds__(Tile<D>::kThreads)
+__global__ void __launch_bounds__(Tile<D>::kThreads, D == 64 && !OUT ? 3 : 0)
 linear_simt_kernel(const Args a) {
     using T = Tile<D>;
     constexpr int NT = T::kThreads, R = T::kRows, C = T::kCols, kTok = T::kTok, kWarps = NT / 32;
     __shared__ __align__(16) float s_q[kTok][D], s_k[kTok][D], s_v[kTok][D], s_o[OUT ? kTok : 1][D];
-    __shared__ float s_a[kTok], s_in[kTok], s_out[kTok], s_first;
+    __shared__ float s_a[kTok], s_in[kTok], s_out[kTok], s_first, s_last;
     __shared__ bool s_gentle;
+    __shared__ linear::Repeated s_repeated;  // of one decay for a head: a stage's
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int part = tid % T::kLanes, row0 = part * R, col0 = tid / T::kLanes * C;
     // (behind the segments' kernels, which have waited for everything before them, only the states have to be waited for)
@@ -103,6 +105,7 @@ linear_simt_kernel(const Args a) {
             S[r][c] = init ? make_float2(init[at], init[at + D]) : make_float2(0.f, 0.f);
         }
     float unit = 1.f;  // of the state in S
+    const bool repeats = !a.per_token && sg.len >= 2 * kTok;
     for (int c0 = 0; c0 < sg.len; c0 += kTok) {
         const int n = min(kTok, sg.len - c0);
 #pragma unroll
@@ -119,7 +122,8 @@ linear_simt_kernel(const Args a) {
                 const float up = __shfl_up_sync(0xffffffffu, b, off);
                 if (tid >= off) b += up;
             }
-            total += (double)__shfl_sync(0xffffffffu, b, kTok - 1);
+            const float end = __shfl_sync(0xffffffffu, b, kTok - 1);
+            total += (double)end;
             // the least and the most of 0 and the sums (as integers: bits of floats of one sign are in their absolute values' order)
             const float mine = tid < kTok ? b : 0.f;
             const float least = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fminf(mine, 0.f))));
@@ -133,6 +137,11 @@ linear_simt_kernel(const Args a) {
             if (tid == 0) {
                 s_gentle = gentle;
                 s_first = exp2f(least);
+                s_last = exp2f(end - least);
+                if (repeats) {  // (the end is the least of the sums, or the start is)
+                    if (c0 == 0) s_repeated = linear::Repeated::of((double)ng * kTok);
+                    if (n == kTok) (ng < 0.f ? s_first : s_last) = s_repeated.next();
+                }
             }
         }
         __syncthreads();
@@ -157,7 +166,7 @@ linear_simt_kernel(const Args a) {
         for (int r = 0; r < R / 2; ++r)
 #pragma unroll
             for (int c = 0; c < C; ++c) S[r][c] = tc::mul2(S[r][c], make_float2(change, change));
-        unit = gentle ? s_in[n - 1] : 1.f;
+        unit = gentle ? s_last : 1.f;
         // (A loop for each kind, and two pairs of tokens unrolled: 33000 tokens x 32 heads, d = 64, bf16 1190 us, with the choice
         // inside 1250; 1501 x 16 40 us, without unrolling 50, with four pairs 44.)
         const auto tokens = [&](auto kind) {
@@ -252,7 +261,10 @@ linear_simt_kernel(const Args a) {
                 to[at + D] = S[r][c].y * unit;
             }
     }
-    if (!OUT && tid == 0) a.seg_decay[(size_t)slot * a.H + h] = exp2f((float)total);
+    // (one decay for a head: a factor that the chain of segments repeats)
+    if (!OUT && tid == 0)
+        a.seg_decay[(size_t)slot * a.H + h] =
+            a.per_token ? exp2f((float)total) : linear::Repeated::of((double)linear::log2_decay(a.g[h]) * sg.len).at(sg.index);
 }
 
 // The state behind each segment but a document's last, in place of what the segment adds: S <- decay S + added, from

@@ -164,25 +164,6 @@ __device__ __forceinline__ Sums chunk_sums(float x0, float x1) {
     return r;
 }
 
-// 2^b_64 where it is the same for chunk after chunk (one decay for a head): its rounding would be too, and add up over a
-// thousand chunks (S of 65536 tokens off by up to 1.4e-6 of a head's size instead of 3e-7).  So each factor makes up for what
-// the ones before it have left out.
-struct Decay {
-    float hi = 0.f, lo = 0.f, left = 0.f;  // the factor, in two parts; what the product of those so far lacks, relative to it
-    Decay() = default;
-    __device__ explicit Decay(long long log2) {
-        const double x = exp2((double)log2 * (1. / kFixed));
-        hi = (float)x;
-        if (x < 1e38) lo = (float)(x - hi);
-    }
-    __device__ float next() {
-        if (!(hi < 1e38f)) return hi;
-        const float more = fmaf(hi, left, lo), r = hi + more, lacks = more - (r - hi);
-        left = r > 0.f ? lacks / r : 0.f;
-        return r;
-    }
-};
-
 // 1 / sqrt(sum of squares + eps) of 16 of the tile's rows, half a row a lane; 0 from row n on, whose tokens are not the
 // segment's (of a cleared row without eps it would be infinite, and the product with its zeros NaN).
 __device__ __forceinline__ void row_norms(const uint8_t *tile, int first, int n, float eps, float *out) {
@@ -453,7 +434,7 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         // any length, so behind its first unit a CTA takes the next that nobody has: dealt out in turn, the CTA with the
         // most chunks had half as many again as the mean (8 documents, 33000 tokens x 32 heads).
         float g0 = 0.f, g1 = 0.f;
-        Decay all;
+        linear::Repeated all{};  // 2^b_64 where it is the same for chunk after chunk
         for (int u = blockIdx.x;; ++turn) {
             Segment sg;
             while (u < units && !linear::find_segment(a.cu, a.num_seqs, a.seg, u / a.H, &sg)) u = next_unit(a, u);
@@ -494,7 +475,7 @@ linear_out_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             reinterpret_cast<float2 *>(g.in)[lane] = make_float2(ex2(b.x), ex2(b.y));
             reinterpret_cast<float2 *>(g.out)[lane] = make_float2(ex2(from_fixed(s.all - s.b0)), ex2(from_fixed(s.all - s.b1)));
             const bool repeats = !a.per_token && sg.len >= 2 * kC;
-            if (repeats && c0 == 0) all = Decay(s.all);
+            if (repeats && c0 == 0) all = linear::Repeated::of((double)s.all * (1. / kFixed));
             const float x = repeats && rows == kC ? all.next() : exp2f(from_fixed(s.all));
             if (lane == 0) g.all = s.nan ? nan : x;
         }
@@ -1054,7 +1035,11 @@ linear_segment_tc(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         if (lane == 0) tc::mbar_arrive(&sh.told[n % kTold]);
         if (stop) c0 = 0;
         }
-        if (lane == 0) a.seg_decay[(size_t)slot * a.H + h] = nan ? __int_as_float(0x7fffffff) : exp2f(from_fixed(later));
+        if (lane == 0) {
+            // (one decay for a head: a factor that the chain of segments repeats)
+            const float x = a.per_token ? exp2f(from_fixed(later)) : linear::Repeated::of((double)later * (1. / kFixed)).at(sg.index);
+            a.seg_decay[(size_t)slot * a.H + h] = nan ? __int_as_float(0x7fffffff) : x;
+        }
         }
     } else if (warp < 12) {
         const int group = (warp >> 2) - 1;

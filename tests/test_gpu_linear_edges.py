@@ -76,3 +76,24 @@ def test_values_near_the_largest(dtype, d, kind):
     x["v"] = (x["v"].float() * 2.0 ** {"decays": 115, "grows": 70, "both": 104}[kind]).to(dtype)
     most = check(x, [150, 250], f64(x["q"]), f64(x["k"]))
     assert most < 2.0 ** 127
+
+
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("T,H,d,dtype,factors,tokens", [
+    (16384, 608, 128, F32, 1024, 16), (32768, 608, 64, F32, 512, 32), (32768, 608, 16, BF, 512, 32),  # stages of one segment or two
+    (65536, 1, 64, F32, 1023, 64), (65536, 2, 128, F32, 255, 256), (38912, 1, 128, BF, 151, 256)])   # links of the chain
+def test_one_decay_for_many_factors(T, H, d, dtype, factors, tokens, sign):
+    """S0 alone, decayed or grown by one factor for each run of `tokens` tokens: its rounding must not add up.  The mean error of
+    S in steps of 2^-24, over its elements: independent roundings, one a factor, 0.3 at most; the product of the factors is
+    right to a step of fp32, 2; the log-decay to base 2 has two roundings, times the exponent reached, 0.5; the last run's
+    and the chain's products, 2.  A factor that is off by a fifth of 2^-24 adds 30 and more."""
+    run = np.float32(sign * 2.0 ** -2 / T) * (1 + np.arange(64, dtype=np.float32) / 64)
+    g = next(x for x in run if abs(float(np.float32(np.exp(tokens * float(x)))) / np.exp(tokens * float(x)) - 1) > 0.2 * 2.0 ** -24)
+    v, qk = torch.zeros((T, H, d), dtype=dtype, device="cuda"), torch.zeros((T, 1, d), dtype=dtype, device="cuda")
+    S0 = torch.randn((1, H, d, d), generator=torch.Generator(device="cuda").manual_seed(97), device="cuda")
+    S, cu = torch.empty_like(S0), torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    libkda.kda_linear_prefill(qk, qk, v, torch.full((H,), float(g), device="cuda"), cu, torch.empty_like(v), S0=S0, S_final=S)
+    some = S0 != 0
+    assert (S[~some] == 0).all()
+    error = (S[some].double() / (S0[some].double() * np.exp(float(g) * T)) - 1).mean().item()
+    assert abs(error) <= 8 * 2.0 ** -24, error * 2 ** 24
