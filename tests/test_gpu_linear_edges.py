@@ -97,3 +97,23 @@ def test_one_decay_for_many_factors(T, H, d, dtype, factors, tokens, sign):
     assert (S[~some] == 0).all()
     error = (S[some].double() / (S0[some].double() * np.exp(float(g) * T)) - 1).mean().item()
     assert abs(error) <= 8 * 2.0 ** -24, error * 2 ** 24
+
+
+STATE = 8e-7  # see test_the_state_keeps_24_bits; test_linear_edges_cpu shows what it tells apart
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("per_token", [False, True])
+@pytest.mark.parametrize("lengths", [[64], [65], [700], [3000, 200], [1, 4097]], ids=str)
+def test_the_state_keeps_24_bits(lengths, per_token, norm):
+    """The state on the tensor cores in the 2-norm, each document and head by itself.  A chunk's product is twelve sums, each cut off
+    below 24 bits, which takes 2^-24 of it on average: 7.2e-7 at most if all were as large as the last; beside that
+    the independent errors of single terms (2^-22 at most: exp2, the norm, their products) count for 2e-7, in quadrature.  The
+    decayed v in two bf16 parts instead of three, or with a third one that belongs elsewhere, is off by 2e-6."""
+    cu = table(lengths)
+    x = inputs(cu[-1], 3, 3, 128, BF, 101, per_token)
+    q, k = f64(x["q"]), f64(x["k"])
+    _, ref, _, _ = linear.attention(linear.unit(q, 1e-6) if norm else q, linear.unit(k, 1e-6) if norm else k, f64(x["v"]), f64(x["g"]), cu)
+    _, S = run_prefill(x, cu, qk_l2norm=norm)
+    off = np.linalg.norm(f64(S) - ref, axis=(2, 3)) / np.linalg.norm(ref, axis=(2, 3))
+    assert (off <= STATE).all(), off

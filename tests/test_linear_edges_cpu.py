@@ -60,3 +60,24 @@ def test_outputs_are_the_stream_s_own(monkeypatch, name, outputs):
         monkeypatch.setattr(torch, f, noted(getattr(torch, f)))
     getattr(libkda, name)(Q, Q, Q, Q, torch.zeros(3, 4), torch.zeros(2, dtype=torch.int32), stream="one")
     assert taken == ["one"] * outputs
+
+
+@pytest.mark.parametrize("T", [64, 700])
+@pytest.mark.parametrize("third", ["there", "missing", "another row's", "another token's"])
+def test_what_the_state_s_tolerance_tells_apart(third, T):
+    """The decayed v in three bf16 parts, as the tensor cores take it, in 64-bit sums: all 24 bits are well within the
+    tolerance of the state's test on the GPU, and a third part that is missing or out of place is well outside."""
+    from tests.test_gpu_linear_edges import STATE, inputs
+
+    x = inputs(T, 1, 1, 128, torch.bfloat16, 103)
+    k, v, g = x["k"][:, 0].double(), x["v"][:, 0].float(), x["g"][:, 0].double()
+    w = torch.exp(g.sum() - g.cumsum(0))
+    y = v * w.float()[:, None]
+    bf16 = lambda t: t.to(torch.bfloat16).float()  # noqa: E731
+    high = bf16(y)
+    middle = bf16(y - high)
+    low = bf16(y - high - middle)
+    low = {"there": low, "missing": 0 * low, "another row's": low.roll(8, 1), "another token's": low.roll(1, 0)}[third]
+    ref = k.T @ (v.double() * w[:, None])
+    off = (k.T @ (high.double() + middle.double() + low.double()) - ref).norm() / ref.norm()
+    assert off < STATE / 4 if third == "there" else off > 2 * STATE, off
