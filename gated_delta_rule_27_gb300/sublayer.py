@@ -172,8 +172,7 @@ def synthetic_linear_weights(D: int, H: int, H_qk: int, d: int, seed: int, devic
 
 
 def _linear_inputs(x, positions, w: LinearWeights, d: int):
-    R = x.shape[0]
-    q, k, v, z = ((x @ m).view(R, -1, d) for m in (w.W_q, w.W_k, w.W_v, w.W_z))
+    q, k, v, z = ((x @ m).view(x.shape[0], m.shape[1] // d, d) for m in (w.W_q, w.W_k, w.W_v, w.W_z))
     libkda.kda_rope(q, k, positions, w.rope_steps, q, k, scale=w.rope_scale)
     g = -torch.nn.functional.softplus((x @ w.W_a).float())
     return q, k, v, z, g
@@ -182,13 +181,13 @@ def _linear_inputs(x, positions, w: LinearWeights, d: int):
 def linear_prefill_forward(x, cu_seqlens, positions, w: LinearWeights, d: int, S0=None, qk_eps=1e-6, out_eps=1e-6, workspace=None):
     """x [T, D] bf16 at positions [T] int32 -> (y [T, D] bf16, S [N, H, d, d]) for packed documents, from the states S0
     (None: zeros)."""
-    T, N = x.shape[0], cu_seqlens.numel() - 1
+    N = cu_seqlens.numel() - 1
     q, k, v, z, g = _linear_inputs(x, positions, w, d)
     o = torch.empty_like(v)
     S = torch.empty((N, v.shape[1], d, d), dtype=torch.float32, device=x.device)
     libkda.kda_linear_prefill(q, k, v, g, cu_seqlens, o, S0=S0, S_final=S, workspace=workspace, qk_l2norm=True, qk_eps=qk_eps, out_gate=z,
                               out_weight=w.out_weight, out_eps=out_eps)
-    return o.view(T, -1) @ w.W_o, S
+    return o.flatten(1) @ w.W_o, S
 
 
 def linear_decode_forward(x, positions, S_pool, seq_idx, w: LinearWeights, d: int, qk_eps=1e-6, out_eps=1e-6):
@@ -198,4 +197,4 @@ def linear_decode_forward(x, positions, S_pool, seq_idx, w: LinearWeights, d: in
     o = torch.empty_like(v)
     libkda.kda_linear_decode_step(q, k, v, g, S_pool, o, seq_idx=seq_idx, qk_l2norm=True, qk_eps=qk_eps, out_gate=z, out_weight=w.out_weight,
                                   out_eps=out_eps)
-    return o.view(x.shape[0], -1) @ w.W_o
+    return o.flatten(1) @ w.W_o
