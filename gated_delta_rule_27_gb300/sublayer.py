@@ -148,7 +148,12 @@ def decode_forward(x, S, conv_state, w: Weights, H: int, d: int, events=None, qk
 # ---------------------------------------------------------------------------------------------------------------
 # The sublayer of linear attention with one decay per head: x -> Q/K/V projections -> rotary positions on Q and K ->
 # decay gate (one log-decay a token and head, read as for KDA's) -> the recurrence, with the Q/K normalisation before
-# it (which no rotation changes) and the gated normalisation behind it fused -> output projection.
+# it and the gated normalisation behind it fused -> output projection.
+#
+# The normalisation is of what the rotation gives.  No rotation changes a norm, but rope_scale does: where a head turns as a
+# whole the normalisation takes the scale out again, and where only its first part turns the scale weighs that part against
+# the rest.  For a scale that acts on the scores (as stretched contexts have it in softmax attention), q and k are
+# normalised first, then rotated, and libkda.kda_linear_prefill is called without its own normalisation.
 # ---------------------------------------------------------------------------------------------------------------
 @dataclasses.dataclass
 class LinearWeights:
@@ -160,7 +165,7 @@ class LinearWeights:
     W_o: torch.Tensor   # [H d, D]
     out_weight: torch.Tensor  # [d] fp32
     rope_steps: torch.Tensor  # [rot / 2] int64 (libkda.rope_steps)
-    rope_scale: float
+    rope_scale: float         # of the turned part, before the normalisation
 
 
 def synthetic_linear_weights(D: int, H: int, H_qk: int, d: int, seed: int, device, rot: int = None, scaling=None) -> LinearWeights:
