@@ -18,7 +18,8 @@ template <typename Tin, int D>
 __global__ void __launch_bounds__((D / 4) * (D / kRows))
 linear_decode_kernel(const LinearDecodeArgs a) {
     constexpr int CG = D / 4, RG = D / kRows, NT = CG * RG;
-    __shared__ float s_q[D], s_k[D], s_part[RG][D], s_o[D], s_scale[3];
+    __shared__ __align__(16) float s_part[RG][D];  // written four at a time
+    __shared__ float s_q[D], s_k[D], s_o[D], s_scale[3];
     const int tid = threadIdx.x, cg = tid % CG, rg = tid / CG;
     const int n = blockIdx.x / a.H, h = blockIdx.x - n * a.H;
     tc::grid_dep_launch();
