@@ -466,7 +466,8 @@ kda_status kda_linear_prefill(const void *q, const void *k, const void *v, const
         if (o == q || o == k || o == v || o == (const void *)g || o == (const void *)S0) return KDA_ERR_INVALID_ARG;
     }
     if (!aligned16(S0) || !aligned16(S_final)) return KDA_ERR_INVALID_ARG;
-    if (S_final && (S_final == q || S_final == k || S_final == v || S_final == o || S_final == (const void *)g)) return KDA_ERR_INVALID_ARG;
+    const void *end = S_final;
+    if (end && (end == q || end == k || end == v || end == o || end == (const void *)g || end == fu.gate)) return KDA_ERR_INVALID_ARG;
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < lay.total) return KDA_ERR_INVALID_ARG;
     char *ws = static_cast<char *>(workspace);
     kda::linear::Args a{};

@@ -1,12 +1,13 @@
 """The binding and its limits where they went wrong once, without a GPU."""
 import contextlib
+import ctypes
 import types
 
 import pytest
 import torch
 
 from gated_delta_rule_27_gb300 import libkda
-from tests.test_linear_cpu import GIVEN
+from tests.test_linear_cpu import GIVEN, PREFILL, call
 
 
 Q = torch.zeros(3, 4, 64)
@@ -81,3 +82,8 @@ def test_what_the_state_s_tolerance_tells_apart(third, T):
     ref = k.T @ (v.double() * w[:, None])
     off = (k.T @ (high.double() + middle.double() + low.double()) - ref).norm() / ref.norm()
     assert off < STATE / 4 if third == "there" else off > 2 * STATE, off
+
+
+def test_the_final_state_in_the_gate_s_place_is_refused():
+    gated = lambda gate: ctypes.byref(libkda.FusionOpts(0, 0.0, gate, None, 1e-6))  # noqa: E731
+    assert call("kda_linear_prefill", opts=gated(PREFILL["S"].value)) == libkda.KDA_ERR_INVALID_ARG
