@@ -435,6 +435,7 @@ static kda_status linear_plan(int32_t total_tokens, int32_t num_seqs, int32_t H,
                               int32_t *slots, kda::linear::Layout *lay) {
     if (num_seqs < 0) return KDA_ERR_INVALID_ARG;
     *seg = kda::linear::plan_segment(total_tokens, num_seqs, H, d, linear_on_tensor_cores(d, dt));
+    if ((int64_t)total_tokens + *seg > INT_MAX) return KDA_ERR_UNSUPPORTED;  // kernels round token counts up to segments
     const int64_t n = total_tokens / *seg + (int64_t)num_seqs;
     if (n * H > INT_MAX - 4096) return KDA_ERR_UNSUPPORTED;  // units are counted past their end by a grid or two
     *slots = (int32_t)n;

@@ -418,9 +418,12 @@ KDA_API kda_status kda_draft_verify(const void *logits, const float *draft_probs
  *   workspace  device scratch of kda_linear_workspace_size(...) bytes, 256-byte
  *              aligned; kda_prefill_check reads how the call ended
  *   opts       the fused normalisations (out_gate [total_tokens, H, d_v]), or NULL
- * d_k == d_v in {16, 64, 128}.  A document's bits do not depend on the other
- * documents' values, but on the batch's number of tokens and on H, which choose
- * how documents are split: results of two packings agree as stated below.
+ * d_k == d_v in {16, 64, 128}.  total_tokens x H, and total_tokens with a
+ * segment's length added, are below 2^31 (KDA_ERR_UNSUPPORTED else).  A document's
+ * bits do not depend on the other documents' values, but on the batch's number
+ * of tokens, on num_seqs (empty documents count) and on H, which choose how
+ * documents are split: results of two packings agree as stated below.  A call
+ * with no sequences does nothing and leaves the workspace's status as it was.
  *
  * Accuracy.  bf16 at d = 128: sums are fp32; the products' operands that are
  * not inputs are bf16 -- the scores and the state where they form o (each adds

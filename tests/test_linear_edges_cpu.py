@@ -87,3 +87,11 @@ def test_what_the_state_s_tolerance_tells_apart(third, T):
 def test_the_final_state_in_the_gate_s_place_is_refused():
     gated = lambda gate: ctypes.byref(libkda.FusionOpts(0, 0.0, gate, None, 1e-6))  # noqa: E731
     assert call("kda_linear_prefill", opts=gated(PREFILL["S"].value)) == libkda.KDA_ERR_INVALID_ARG
+
+
+def test_token_counts_that_leave_an_int_when_rounded_up_are_refused():
+    for d, dtype in ((16, libkda.KDA_BF16), (64, libkda.KDA_F32), (128, libkda.KDA_BF16)):
+        most = 2 ** 31 - 1
+        assert call("kda_linear_prefill", T=most, N=1, H=1, Hqk=1, dk=d, dv=d, dt=dtype) == libkda.KDA_ERR_UNSUPPORTED
+        assert libkda.kda_linear_workspace_size(most, 1, 1, d, d, dtype) == 0
+        assert libkda.kda_linear_workspace_size(most - 2 ** 24, 1, 1, d, d, dtype) > 0
