@@ -107,13 +107,14 @@ __device__ __forceinline__ const float *segment_start(const Args &a, const Segme
 // Tokens of a segment, which are chosen without the documents' lengths.  Tensor cores: one document is cut into as many
 // segments of all heads as there are SMs, or a small multiple of that where they do not fit the SMs well, of 256 tokens at
 // least.  Several make segments of their own by ending: the batch is cut into as many as leave an SM four in all, so that
-// the longest document leaves no SM alone for long, of 512 tokens at least (8 documents, 33000 tokens x 32 heads: 394 us in
-// pieces of 8256 tokens, 325 of 2368, 372 of 1216).
+// the longest document leaves no SM alone for long, of 512 tokens at least (8 documents at random places, 33000 tokens x 32 heads: 278 us
+// in pieces of 3008 tokens, 315 of 8256, 313 of 1216).  From 608 / H documents on that splits none, which suits equal ones (18 x 1833
+// tokens x 32 heads: 207 us, in pieces of 1216 310) and not a long one among short (16 x 1000 and 17000: 540 us and 276).
 //
 // CUDA cores, which take a token some ten times as long: four segments an SM, of 64 tokens at least at d = 128.  Below that a
 // state is a quarter or less, and segments are short where there are few tokens (32 at least: d = 64, fp32, 5 heads, 400 tokens
-// 14.5 us for 20.7; 1501 tokens at d = 128 82 us for 56), and eight an SM where those still have 64 tokens and the four have 128
-// (33000 tokens x 32 heads, d = 64, 1260 us for 1480; 4096 x 16, d = 128, 370 for 319).
+// 13.9 us for 19.7; 1501 tokens 27.4 for 26.5, at d = 128 80.6 for 53.6), and eight an SM where those still have 64 tokens and the four
+// have 128 (33000 tokens x 32 heads, d = 64, bf16, 1200 us for 1450; 4096 x 16, d = 128, fp32, 351 for 293).
 inline int plan_segment(int64_t total, int64_t num_seqs, int64_t H, int d, bool tensor_cores) {
     constexpr int64_t kSms = 152;
     const auto cut = [&](int64_t parts, int64_t unit, int64_t least) {

@@ -10,7 +10,7 @@
 // share of shared memory, 128 bytes a clock whoever else wants the same: with one column a thread (64 bytes of k and q for
 // 8 elements) a token took 300 clocks of an SM at d = 64, with tiles of 8 x 4 it takes a quarter of that.  1501 tokens x 5 heads,
 // fp32, d = 64: 27 us for the three launches, where HBM would need 0.8: 235 CTAs of four warps, each of which goes through its 32
-// tokens one after the other (39 us with segments of 64 tokens).
+// tokens one after the other.
 #include <type_traits>
 
 #include "kda_linear.cuh"

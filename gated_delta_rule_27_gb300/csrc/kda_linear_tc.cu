@@ -8,7 +8,7 @@
 // for a whole segment: the tensor core cuts its sums off instead of rounding them, which a sum over thousands of tokens
 // would show (8e-6 of S after 4096 tokens), so it forms each chunk's V'^T K by itself and the sum over chunks is rounded.
 // q, k, v are read once, o is written once: 1 KB a token and head against 98 kFLOP, so HBM is the bound to reach, 1.45 us a
-// chunk for a CTA with its SM's share.  The output kernel takes 1.75 (65536 tokens x 16 heads: 200 us, 5.4 TB/s; 2.6 with both
+// chunk for a CTA with its SM's share.  The output kernel takes 1.77 (65536 tokens x 16 heads: 203 us, 5.3 TB/s; 2.6 with both
 // fused normalisations): its warps issue in half of all clocks, some 1600 instructions a chunk and SM sub-partition, and the
 // longest of the roles (V', 2400 clocks, and 200 for each of its waits) paces the others.  What a CTA does is spread over
 // warps that each do one thing, chunk after chunk, across segments:
@@ -879,7 +879,7 @@ done:
 // zero here (exp2 flushes what fp32 holds no normal number for).
 //     warp 0  copies   warp 2  decays   warps 1, 3  MMAs, and warps 4-7, 8-11  V' (and norms of k), of every other chunk
 //     warps 12-15  the sums over the chunks, in registers
-// 65536 tokens x 16 heads, none forgotten: 100 us, 1.0 a chunk against the 0.7 of an SM's share of HBM (one warp for all MMAs:
+// 65536 tokens x 16 heads, none forgotten: 103 us, 1.0 a chunk against the 0.7 of an SM's share of HBM (one warp for all MMAs:
 // 106 us); V' is the longest role here too.
 // ---------------------------------------------------------------------------
 constexpr int kSegStages = 5, kTold = 8;

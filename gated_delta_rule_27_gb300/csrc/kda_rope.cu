@@ -8,9 +8,10 @@
 // Bound by HBM: q and k are read and written once.  A block works out the sines and cosines of a few tokens once, in
 // shared memory, and turns those tokens' heads, 16 bytes a load: of two vectors half the rotated part apart, or of one that
 // holds whole pairs.  (One thread for each pair with its own sine and cosine took 53 us for 4096 tokens of 32 heads, two
-// thirds of it in the functions.)  65536 tokens x 32 heads of 128, bf16: 164 us in halves, 179 interleaved (158 at a plain copy's
-// rate); 4096 tokens 15.6 and 17.2 for 9.9.  (A thread that keeps its place in the head and goes through the heads issues fewer
-// instructions and took longer: 178 us for 169 at the time, 222 for 199.)
+// thirds of it in the functions.)  65536 tokens x 32 heads of 128, bf16: 164 us in halves, 180 interleaved (158 at a plain copy's
+// rate); 4096 tokens 15.6 and 17.2 for 9.9, caches cold (14.8 in halves among other calls on other inputs).  (A thread that
+// keeps its place in the head and goes through the heads issues fewer instructions and took longer: 178 us for 169 at the time, 222
+// for 199.)
 #include "kda_linear.cuh"
 #include "kda_tc.cuh"
 
