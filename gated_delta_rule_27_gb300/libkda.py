@@ -165,6 +165,15 @@ def _on(stream, allocate, *args):
         return allocate(*args)
 
 
+def _output_on(stream, allocate, *args):
+    """_on, for a tensor that the caller gets: one that the current stream's work may use too before its memory is given
+    out again."""
+    out = _on(stream, allocate, *args)
+    if stream is not None:
+        out.record_stream(torch.cuda.current_stream(out.device))
+    return out
+
+
 def kda_prefill_workspace_size(total_tokens: int, num_seqs: int, H: int, d_k: int, d_v: int, in_dtype: int,
                                chunk_size: int = 64) -> int:
     return int(load().kda_prefill_workspace_size(total_tokens, num_seqs, H, d_k, d_v, in_dtype, chunk_size))
@@ -495,7 +504,7 @@ def prefill(q, k, v, g, beta, cu_seqlens, S0=None, chunk_size=64, want_state=Tru
     """Allocates o (and S_final) with torch, as the stream's memory, and runs kda_prefill_chunked; returns (o, S_final)."""
     T, H, d_k = q.shape
     N = cu_seqlens.numel() - 1
-    fresh = lambda shape, dtype: _on(stream, lambda: torch.empty(shape, dtype=dtype, device=q.device))  # noqa: E731
+    fresh = lambda shape, dtype: _output_on(stream, lambda: torch.empty(shape, dtype=dtype, device=q.device))  # noqa: E731
     o = fresh((T, H, v.shape[2]), v.dtype)
     S_final = fresh((N, H, d_k, v.shape[2]), torch.float32) if want_state else None
     kda_prefill_chunked(q, k, v, g, beta, cu_seqlens, o, S0=S0, S_final=S_final, workspace=workspace,
@@ -505,7 +514,7 @@ def prefill(q, k, v, g, beta, cu_seqlens, S0=None, chunk_size=64, want_state=Tru
 
 def decode_step(q, k, v, g, beta, S_inout, stream=None):
     """Allocates o with torch, as the stream's memory, runs kda_decode_step (S_inout updated in place); returns o."""
-    o = _on(stream, torch.empty_like, v)
+    o = _output_on(stream, torch.empty_like, v)
     kda_decode_step(q, k, v, g, beta, S_inout, o, stream=stream)
     return o
 

@@ -464,8 +464,8 @@ KDA_API kda_status kda_linear_decode_step(const void *q, const void *k, const vo
  * (x, y) of every head of token t becomes
  *     scale (x cos - y sin, y cos + x sin).
  *   q, q_out   [total_tokens, H_q, d] in_dtype     k, k_out [total_tokens, H_k, d]
- *              each output may be its own input, no other overlap; H_q or H_k may
- *              be 0 (its pointers NULL)
+ *              each output may be its own input, no other overlap, and q and k are
+ *              two tensors; H_q or H_k may be 0 (its pointers NULL)
  *   positions  [total_tokens] int32, device; any sign
  *   steps      [rot / 2] uint64, device: frequency_i as a part of a turn, in steps
  *              of 2^-64 turn (a negative frequency as its two's complement, which

@@ -43,7 +43,8 @@ def test_a_workspace_is_the_stream_s_own(monkeypatch, name, given):
 
 @pytest.mark.parametrize("name,outputs", [("prefill", 2), ("decode_step", 1)])
 def test_outputs_are_the_stream_s_own(monkeypatch, name, outputs):
-    current, taken = [], []
+    """Allocated as the call's stream's, and kept until the work that the current stream then has with them is done."""
+    current, taken, kept = [], [], []
 
     @contextlib.contextmanager
     def on(s):
@@ -57,10 +58,12 @@ def test_outputs_are_the_stream_s_own(monkeypatch, name, outputs):
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(libkda, "kda_prefill_chunked", lambda *args, **kw: None)
     monkeypatch.setattr(libkda, "kda_decode_step", lambda *args, **kw: None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: "current")
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda self, s: kept.append(s))
     for f in ("empty", "empty_like"):
         monkeypatch.setattr(torch, f, noted(getattr(torch, f)))
     getattr(libkda, name)(Q, Q, Q, Q, torch.zeros(3, 4), torch.zeros(2, dtype=torch.int32), stream="one")
-    assert taken == ["one"] * outputs
+    assert taken == ["one"] * outputs and kept == ["current"] * outputs
 
 
 @pytest.mark.parametrize("T", [64, 700])
